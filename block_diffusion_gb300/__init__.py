@@ -6,7 +6,9 @@ fallback: if the library is missing or the device is not sm_103 the calls raise.
 
 Entry points mirror ``include/bdlm.h``:
     bdlm_block_attention, bdlm_lm_head, bdlm_confidence_commit, bdlm_confidence_commit_rule,
-    bdlm_apply_commit, bdlm_status_string, bdlm_device_error, bdlm_release
+    bdlm_apply_commit, bdlm_status_string, bdlm_device_error, bdlm_release; over part of the
+    cache: bdlm_tree_attention, bdlm_compact_kv, bdlm_page_bounds, bdlm_select_pages,
+    bdlm_sparse_attention, bdlm_attention_weights, bdlm_evict_kv
 """
 from __future__ import annotations
 
@@ -35,7 +37,9 @@ BDLM_COMMIT_ENTROPY_BOUNDED = 4
 
 EXPORTS = ("bdlm_block_attention", "bdlm_block_attention_kv", "bdlm_prefill_attention", "bdlm_lm_head", "bdlm_lm_head_device_count",
            "bdlm_lm_head_commit", "bdlm_active_rows", "bdlm_write_block_kv", "bdlm_confidence_commit",
-           "bdlm_confidence_commit_rule", "bdlm_apply_commit", "bdlm_round_loop_create",
+           "bdlm_confidence_commit_rule", "bdlm_apply_commit", "bdlm_tree_attention",
+           "bdlm_compact_kv", "bdlm_page_bounds", "bdlm_select_pages", "bdlm_sparse_attention",
+           "bdlm_attention_weights", "bdlm_evict_kv", "bdlm_round_loop_create",
            "bdlm_round_loop_launch", "bdlm_round_loop_destroy", "bdlm_status_string",
            "bdlm_device_error", "bdlm_selftest_wait_timeout", "bdlm_release")
 
@@ -101,6 +105,21 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.bdlm_prefill_attention.argtypes = [ctypes.POINTER(AttnDesc), I, P, P, P, P, P, P, P, P,
                                            P]
     lib.bdlm_prefill_attention.restype = I
+    D = ctypes.POINTER(AttnDesc)
+    lib.bdlm_tree_attention.argtypes = [D, P, P, P, P, P, P, P, P, P]
+    lib.bdlm_tree_attention.restype = I
+    lib.bdlm_compact_kv.argtypes = [D, P, P, P, P, P, I, I, P, P, P]
+    lib.bdlm_compact_kv.restype = I
+    lib.bdlm_page_bounds.argtypes = [D, P, P, P, P, P, P]
+    lib.bdlm_page_bounds.restype = I
+    lib.bdlm_select_pages.argtypes = [D, P, P, P, P, I, I, I, P, P, P]
+    lib.bdlm_select_pages.restype = I
+    lib.bdlm_sparse_attention.argtypes = [D, P, P, P, I, I, P, P, P, P]
+    lib.bdlm_sparse_attention.restype = I
+    lib.bdlm_attention_weights.argtypes = [D, P, P, P, P, P, F, P, P]
+    lib.bdlm_attention_weights.restype = I
+    lib.bdlm_evict_kv.argtypes = [D, P, P, P, P, P, I, I, P, P, P, P, P]
+    lib.bdlm_evict_kv.restype = I
     lib.bdlm_round_loop_create.argtypes = [ctypes.POINTER(RoundLoopDesc),
                                            ctypes.POINTER(ctypes.c_void_p)]
     lib.bdlm_round_loop_create.restype = I
@@ -138,6 +157,17 @@ def _stream(stream) -> int | None:
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _dense(fn: str, *tensors) -> None:
+    """Refuses tensors that a bare address would misread: not contiguous, or not on the current
+    device (addresses and None pass)."""
+    import torch
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and not isinstance(t, int) and not (t.get_device() == dev
+                                                             and t.is_contiguous()):
+            raise BdlmError(fn, BDLM_ERR_INVALID)
 
 
 def _check(fn: str, rc: int) -> None:
@@ -245,6 +275,81 @@ def bdlm_write_block_kv(desc: AttnDesc, k_new, v_new, k_pages, v_pages, page_tab
                                  _ptr(v_pages), _ptr(page_table), _ptr(prefix_lens),
                                  _stream(stream))
     _check("bdlm_write_block_kv", rc)
+
+
+def bdlm_tree_attention(desc: AttnDesc, q, k_pages, v_pages, page_table, prefix_lens, tree_mask,
+                        out, lse=None, stream=None) -> None:
+    """tree_mask: [B, L] int64/uint64 visibility words, or None (every query sees the block);
+    lse: [B, L, Hq] float32, or None."""
+    lib = load_library()
+    _dense("bdlm_tree_attention", q, k_pages, v_pages, page_table, prefix_lens, tree_mask,
+           out, lse)
+    rc = lib.bdlm_tree_attention(ctypes.byref(desc), _ptr(q), _ptr(k_pages), _ptr(v_pages),
+                                 _ptr(page_table), _ptr(prefix_lens), _ptr(tree_mask), _ptr(out),
+                                 _ptr(lse), _stream(stream))
+    _check("bdlm_tree_attention", rc)
+
+
+def bdlm_compact_kv(desc: AttnDesc, k_pages, v_pages, page_table, base_lens, idx, heads: int,
+                    n_max: int, counts, to_table, stream=None) -> None:
+    """to_table is page_table itself for a move in place."""
+    lib = load_library()
+    _dense("bdlm_compact_kv", k_pages, v_pages, page_table, base_lens, idx, counts, to_table)
+    rc = lib.bdlm_compact_kv(ctypes.byref(desc), _ptr(k_pages), _ptr(v_pages), _ptr(page_table),
+                             _ptr(base_lens), _ptr(idx), int(heads), int(n_max), _ptr(counts),
+                             _ptr(to_table), _stream(stream))
+    _check("bdlm_compact_kv", rc)
+
+
+def bdlm_page_bounds(desc: AttnDesc, k_pages, page_table, from_lens, to_lens, bounds,
+                     stream=None) -> None:
+    lib = load_library()
+    _dense("bdlm_page_bounds", k_pages, page_table, from_lens, to_lens, bounds)
+    rc = lib.bdlm_page_bounds(ctypes.byref(desc), _ptr(k_pages), _ptr(page_table),
+                              _ptr(from_lens), _ptr(to_lens), _ptr(bounds), _stream(stream))
+    _check("bdlm_page_bounds", rc)
+
+
+def bdlm_select_pages(desc: AttnDesc, q, bounds, page_table, prefix_lens, group: int,
+                      n_select: int, sel_cols: int, sel_table, sel_lens, stream=None) -> None:
+    lib = load_library()
+    _dense("bdlm_select_pages", q, bounds, page_table, prefix_lens, sel_table, sel_lens)
+    rc = lib.bdlm_select_pages(ctypes.byref(desc), _ptr(q), _ptr(bounds), _ptr(page_table),
+                               _ptr(prefix_lens), int(group), int(n_select), int(sel_cols),
+                               _ptr(sel_table), _ptr(sel_lens), _stream(stream))
+    _check("bdlm_select_pages", rc)
+
+
+def bdlm_sparse_attention(desc: AttnDesc, q, k_pages, v_pages, group: int, sel_cols: int,
+                          sel_table, sel_lens, out, stream=None) -> None:
+    lib = load_library()
+    _dense("bdlm_sparse_attention", q, k_pages, v_pages, sel_table, sel_lens, out)
+    rc = lib.bdlm_sparse_attention(ctypes.byref(desc), _ptr(q), _ptr(k_pages), _ptr(v_pages),
+                                   int(group), int(sel_cols), _ptr(sel_table), _ptr(sel_lens),
+                                   _ptr(out), _stream(stream))
+    _check("bdlm_sparse_attention", rc)
+
+
+def bdlm_attention_weights(desc: AttnDesc, q, k_pages, page_table, prefix_lens, lse, decay: float,
+                           weights, stream=None) -> None:
+    lib = load_library()
+    _dense("bdlm_attention_weights", q, k_pages, page_table, prefix_lens, lse, weights)
+    rc = lib.bdlm_attention_weights(ctypes.byref(desc), _ptr(q), _ptr(k_pages), _ptr(page_table),
+                                    _ptr(prefix_lens), _ptr(lse), float(decay), _ptr(weights),
+                                    _stream(stream))
+    _check("bdlm_attention_weights", rc)
+
+
+def bdlm_evict_kv(desc: AttnDesc, k_pages, v_pages, page_table, lens, weights, keep: int,
+                  recent: int, to_table, to_weights, kept, new_lens, stream=None) -> None:
+    """to_table is page_table itself, and to_weights weights, for an eviction in place."""
+    lib = load_library()
+    _dense("bdlm_evict_kv", k_pages, v_pages, page_table, lens, weights, to_table, to_weights,
+           kept, new_lens)
+    rc = lib.bdlm_evict_kv(ctypes.byref(desc), _ptr(k_pages), _ptr(v_pages), _ptr(page_table),
+                           _ptr(lens), _ptr(weights), int(keep), int(recent), _ptr(to_table),
+                           _ptr(to_weights), _ptr(kept), _ptr(new_lens), _stream(stream))
+    _check("bdlm_evict_kv", rc)
 
 
 def round_loop_desc(attn: AttnDesc, steps: int, H: int, V: int, rule: int, k: int,

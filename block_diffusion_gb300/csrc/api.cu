@@ -6,8 +6,10 @@
 #include <stdint.h>
 
 #include <mutex>
+#include <vector>
 
 #include "../../include/bdlm.h"
+#include "cache_ops.h"
 #include "kernels.h"
 
 namespace {
@@ -36,6 +38,7 @@ DeviceState g_dev[kMaxDevices];
 // Bumped whenever a workspace is reallocated or freed: CUDA graphs that captured the old
 // buffers are re-captured before their next launch.
 unsigned g_workspace_gen = 0;
+std::vector<void*> g_retired[kMaxDevices];   // smaller workspaces, kept for captured graphs
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
@@ -56,33 +59,59 @@ int current_device(DeviceState** st) {
       return BDLM_ERR_CUDA;
     s.supported = (major == 10 && minor == 3);
     s.num_sms = sms;
-    s.checked = true;
-    if (s.supported) {
-      if (cudaMalloc(&s.err, 256) != cudaSuccess) return BDLM_ERR_NOMEM;
-      if (cudaMemset(s.err, 0, 256) != cudaSuccess) return BDLM_ERR_CUDA;
+    if (s.supported && !s.err) {
+      void* err = nullptr;
+      if (cudaMalloc(&err, 256) != cudaSuccess) return BDLM_ERR_NOMEM;
+      if (cudaMemset(err, 0, 256) != cudaSuccess ||
+          cudaStreamSynchronize(nullptr) != cudaSuccess) {
+        cudaFree(err);
+        return BDLM_ERR_CUDA;
+      }
+      s.err = static_cast<int*>(err);
     }
+    s.checked = true;
   }
   if (!s.supported) return BDLM_ERR_UNSUPPORTED;
   *st = &s;
   return BDLM_OK;
 }
 
-// Grows a zero-initialised buffer; growing waits for the device to be idle first.
-int ensure(void** ptr, size_t* cap, size_t need, bool zero) {
+// Grows a buffer (zero-initialised where `zero`); growing waits for the device to be idle first.
+// The smaller buffer is retired, not freed: a CUDA graph that a caller captured holds its
+// address, and a replay must still find memory there (bdlm_release frees it).  Each growth at
+// least doubles the buffer, so the retired ones add up to less than the live one.  Nothing can
+// be allocated while `stream` is being captured: that growth is refused with BDLM_ERR_NOMEM,
+// which leaves the capture valid.
+int ensure(void** ptr, size_t* cap, size_t need, bool zero, bdlm_stream stream = nullptr) {
   if (need <= *cap) return BDLM_OK;
+  if (stream) {
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    if (cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &cs) != cudaSuccess)
+      return BDLM_ERR_CUDA;
+    if (cs != cudaStreamCaptureStatusNone) return BDLM_ERR_NOMEM;
+  }
   size_t n = need + need / 4 + 4096;
-  ++g_workspace_gen;
+  if (n < 2 * *cap) n = 2 * *cap;
+  if (*ptr && cudaDeviceSynchronize() != cudaSuccess) return BDLM_ERR_CUDA;
+  void* fresh = nullptr;
+  if (cudaMalloc(&fresh, n) != cudaSuccess) return BDLM_ERR_NOMEM;
+  if (zero && (cudaMemset(fresh, 0, n) != cudaSuccess ||
+               cudaStreamSynchronize(nullptr) != cudaSuccess)) {   // `stream` may not wait for it
+    cudaFree(fresh);
+    return BDLM_ERR_CUDA;
+  }
   if (*ptr) {
-    if (cudaDeviceSynchronize() != cudaSuccess) return BDLM_ERR_CUDA;
-    cudaFree(*ptr);
-    *ptr = nullptr;
-    *cap = 0;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    try {
+      g_retired[dev].push_back(*ptr);
+    } catch (...) {   // no host memory for the list
+      cudaFree(fresh);
+      return BDLM_ERR_NOMEM;
+    }
   }
-  if (cudaMalloc(ptr, n) != cudaSuccess) {
-    *ptr = nullptr;
-    return BDLM_ERR_NOMEM;
-  }
-  if (zero && cudaMemset(*ptr, 0, n) != cudaSuccess) return BDLM_ERR_CUDA;
+  ++g_workspace_gen;
+  *ptr = fresh;
   *cap = n;
   return BDLM_OK;
 }
@@ -144,7 +173,8 @@ int attention_impl(DeviceState* st, const bdlm_attn_desc& d, const bdlm_bf16* q,
                    const bdlm_bf16* k_pages, const bdlm_bf16* v_pages, const int32_t* page_table,
                    const int32_t* prefix_lens, bdlm_bf16* out, bdlm_stream stream,
                    int table_div, int mask_block = 0,
-                   const bdlm::BlockKvWrite* kv_write = nullptr);
+                   const bdlm::BlockKvWrite* kv_write = nullptr,
+                   const bdlm::AttnExt* ext = nullptr);
 
 }  // namespace
 
@@ -207,6 +237,10 @@ int bdlm_release(void) {
   cudaFree(st->attn_cnt);
   cudaFree(st->data);
   cudaFree(st->aux);
+  int dev = 0;
+  cudaGetDevice(&dev);
+  for (void* p : g_retired[dev]) cudaFree(p);
+  g_retired[dev].clear();
   st->attn_cnt = nullptr;
   st->data = nullptr;
   st->aux = nullptr;
@@ -372,15 +406,17 @@ namespace {
 int attention_impl(DeviceState* st, const bdlm_attn_desc& d, const bdlm_bf16* q,
                    const bdlm_bf16* k_pages, const bdlm_bf16* v_pages, const int32_t* page_table,
                    const int32_t* prefix_lens, bdlm_bf16* out, bdlm_stream stream,
-                   int table_div, int mask_block, const bdlm::BlockKvWrite* kv_write) {
+                   int table_div, int mask_block, const bdlm::BlockKvWrite* kv_write,
+                   const bdlm::AttnExt* ext) {
   int rc = get_encoder();
   if (rc) return rc;
   const AttnPlan plan = bdlm::plan_attention(d.B, d.L, d.Hq, d.Hkv, d.max_pages_per_seq,
                                              d.page_size, st->num_sms);
   if (plan.n_mma == 0) return BDLM_ERR_UNSUPPORTED;
-  rc = ensure(reinterpret_cast<void**>(&st->attn_cnt), &st->attn_cnt_cap, plan.cnt_bytes, true);
+  rc = ensure(reinterpret_cast<void**>(&st->attn_cnt), &st->attn_cnt_cap, plan.cnt_bytes, true,
+              stream);
   if (rc) return rc;
-  rc = ensure(&st->data, &st->data_cap, plan.part_bytes, false);
+  rc = ensure(&st->data, &st->data_cap, plan.part_bytes, false, stream);
   if (rc) return rc;
   // q viewed as [B*L rows][Hq heads][D]; box = 64 dims x G heads x lsub rows
   CUtensorMap tm_q, tm_k, tm_v;
@@ -401,12 +437,12 @@ int attention_impl(DeviceState* st, const bdlm_attn_desc& d, const bdlm_bf16* q,
     if ((rc = encode(&tm_v, v_pages, 4, dims, strides, box))) return rc;
   }
   const float scale = d.sm_scale > 0.f ? d.sm_scale : 1.0f / sqrtf(128.0f);
-  cudaError_t e = bdlm::launch_attention(tm_q, tm_k, tm_v, page_table, prefix_lens, out, d.B,
-                                         d.L, d.Hq, d.Hkv, d.max_pages_per_seq, d.num_pages,
-                                         scale, plan, static_cast<float*>(st->data),
-                                         st->attn_cnt, st->err, st->num_sms,
-                                         static_cast<cudaStream_t>(stream), table_div,
-                                         mask_block, kv_write);
+  cudaError_t e = bdlm::launch_attention_ext(tm_q, tm_k, tm_v, page_table, prefix_lens, out, d.B,
+                                             d.L, d.Hq, d.Hkv, d.max_pages_per_seq, d.num_pages,
+                                             scale, plan, static_cast<float*>(st->data),
+                                             st->attn_cnt, st->err, st->num_sms,
+                                             static_cast<cudaStream_t>(stream), table_div,
+                                             mask_block, kv_write, ext);
   return e == cudaSuccess ? BDLM_OK : BDLM_ERR_CUDA;
 }
 
@@ -567,6 +603,282 @@ int bdlm_lm_head_commit(const bdlm_bf16* hidden, const bdlm_bf16* w, const uint8
     e = bdlm::launch_lm_commit_finalize(mask, denoising, B, L, part, plan, temperature, rule, k,
                                         threshold, tok_out, conf_out, entropy_out, commit_out, s);
   return e == cudaSuccess ? BDLM_OK : BDLM_ERR_CUDA;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ part of the cache
+namespace {
+
+// The limits of block attention's descriptor that depend on no pointer.
+bool attn_desc_ok(const bdlm_attn_desc& d) {
+  return d.B >= 0 && d.L >= 1 && d.L <= 64 && d.Hq >= 1 && d.Hkv >= 1 && d.Hq % d.Hkv == 0 &&
+         d.Hq / d.Hkv <= 16 && d.D == 128 && d.page_size == 16 && d.max_pages_per_seq >= 1 &&
+         d.num_pages >= 1 && isfinite(d.sm_scale) &&
+         static_cast<long long>(d.B) * d.L * d.Hq <= 0x7FFFFFFFll &&
+         static_cast<long long>(d.B) * d.max_pages_per_seq <= 0x7FFFFFFFll &&
+         static_cast<long long>(d.max_pages_per_seq) * d.page_size <= 0x7FFFFFFFll;
+}
+
+// The same for calls that read no queries (L, Hq and sm_scale unused).
+bool cache_desc_ok(const bdlm_attn_desc& d) {
+  return d.B >= 0 && d.Hkv >= 1 && d.D == 128 && d.page_size == 16 && d.max_pages_per_seq >= 1 &&
+         d.num_pages >= 1 && static_cast<long long>(d.B) * d.Hkv <= 0x7FFFFFFFll &&
+         static_cast<long long>(d.B) * d.max_pages_per_seq <= 0x7FFFFFFFll &&
+         static_cast<long long>(d.max_pages_per_seq) * d.page_size <= 0x7FFFFFFFll;
+}
+
+bdlm::KeyParams key_params(const bdlm_attn_desc& d, const int32_t* page_table,
+                           const int32_t* prefix_lens, int* err) {
+  bdlm::KeyParams p = {};
+  p.page_table = page_table;
+  p.prefix_lens = prefix_lens;
+  p.B = d.B;
+  p.L = d.L;
+  p.Hq = d.Hq;
+  p.Hkv = d.Hkv;
+  p.G = d.Hq / d.Hkv;
+  p.max_pages = d.max_pages_per_seq;
+  p.num_pages = d.num_pages;
+  p.err = err;
+  return p;
+}
+
+int compact_impl(DeviceState* st, const bdlm_attn_desc& d, bdlm_bf16* k_pages, bdlm_bf16* v_pages,
+                 const int32_t* page_table, const int32_t* base_lens, const int32_t* idx,
+                 int heads, int n_max, const int32_t* counts, const int32_t* to_table,
+                 bdlm_stream stream) {
+  const bdlm::CompactParams p{k_pages, v_pages, page_table, to_table, base_lens, idx, counts,
+                              d.B, d.Hkv, heads, d.max_pages_per_seq, d.num_pages, n_max, st->err};
+  return bdlm::launch_compact(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? BDLM_OK
+                                                                                  : BDLM_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+int bdlm_tree_attention(const bdlm_attn_desc* desc, const bdlm_bf16* q, const bdlm_bf16* k_pages,
+                        const bdlm_bf16* v_pages, const int32_t* page_table,
+                        const int32_t* prefix_lens, const uint64_t* tree_mask, bdlm_bf16* out,
+                        float* lse, bdlm_stream stream) {
+  if (!desc || !attn_desc_ok(*desc)) return BDLM_ERR_INVALID;
+  const bdlm_attn_desc d = *desc;
+  if (d.B == 0) return BDLM_OK;
+  if (!q || !k_pages || !v_pages || !page_table || !prefix_lens || !out) return BDLM_ERR_INVALID;
+  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) ||
+      (reinterpret_cast<uintptr_t>(tree_mask) & 7) != 0)
+    return BDLM_ERR_INVALID;
+  std::lock_guard<std::mutex> lk(g_mu);
+  DeviceState* st = nullptr;
+  int rc = current_device(&st);
+  if (rc) return rc;
+  bdlm::AttnExt ext;
+  ext.tree = true;
+  ext.tree_mask = tree_mask;
+  ext.lse = lse;
+  return attention_impl(st, d, q, k_pages, v_pages, page_table, prefix_lens, out, stream, 1, 0,
+                        nullptr, &ext);
+}
+
+int bdlm_page_bounds(const bdlm_attn_desc* desc, const bdlm_bf16* k_pages,
+                     const int32_t* page_table, const int32_t* from_lens, const int32_t* to_lens,
+                     bdlm_bf16* bounds, bdlm_stream stream) {
+  if (!desc || !cache_desc_ok(*desc)) return BDLM_ERR_INVALID;
+  const bdlm_attn_desc d = *desc;
+  if (d.B == 0) return BDLM_OK;
+  if (!k_pages || !page_table || !to_lens || !bounds || !aligned16(k_pages) || !aligned16(bounds))
+    return BDLM_ERR_INVALID;
+  std::lock_guard<std::mutex> lk(g_mu);
+  DeviceState* st = nullptr;
+  int rc = current_device(&st);
+  if (rc) return rc;
+  return bdlm::launch_page_bounds(k_pages, page_table, from_lens, to_lens, d.B, d.Hkv,
+                                  d.max_pages_per_seq, d.num_pages, st->num_sms, bounds, st->err,
+                                  static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? BDLM_OK
+             : BDLM_ERR_CUDA;
+}
+
+int bdlm_select_pages(const bdlm_attn_desc* desc, const bdlm_bf16* q, const bdlm_bf16* bounds,
+                      const int32_t* page_table, const int32_t* prefix_lens, int group,
+                      int n_select, int sel_cols, int32_t* sel_table, int32_t* sel_lens,
+                      bdlm_stream stream) {
+  if (!desc || !attn_desc_ok(*desc)) return BDLM_ERR_INVALID;
+  const bdlm_attn_desc d = *desc;
+  if (group < 1 || d.L % group != 0 || n_select < 0 ||
+      sel_cols < static_cast<long long>(n_select) + (d.L + 30) / 16)
+    return BDLM_ERR_INVALID;
+  const int G = d.Hq / d.Hkv, groups = d.L / group;
+  const long long lists = static_cast<long long>(d.B) * groups * d.Hkv;
+  if (lists > 0x7FFFFFFFll) return BDLM_ERR_INVALID;
+  if (group * G > bdlm::key_rows_max() || d.max_pages_per_seq > bdlm::kSelectMaxPages)
+    return BDLM_ERR_UNSUPPORTED;
+  if (d.B == 0) return BDLM_OK;
+  if (!q || !bounds || !page_table || !prefix_lens || !sel_table || !sel_lens ||
+      !aligned16(q) || !aligned16(bounds))
+    return BDLM_ERR_INVALID;
+  std::lock_guard<std::mutex> lk(g_mu);
+  DeviceState* st = nullptr;
+  int rc = current_device(&st);
+  if (rc) return rc;
+  // a launch scores whole groups of up to 256 query rows per KV head
+  int per = bdlm::key_rows_max() / (group * G) * group;
+  if (per > d.L) per = d.L;
+  const bdlm::KeyPlan plan =
+      bdlm::plan_keys(d.B, d.Hkv, d.max_pages_per_seq, per * G, st->num_sms);
+  if (plan.total_items > 0x7FFFFFFFll) return BDLM_ERR_INVALID;
+  const size_t score_bytes =
+      align256(static_cast<size_t>(lists) * d.max_pages_per_seq * sizeof(float));
+  rc = ensure(&st->data, &st->data_cap, score_bytes + plan.amax_floats * sizeof(float), false,
+              stream);
+  if (rc) return rc;
+  bdlm::KeyParams p = key_params(d, page_table, prefix_lens, st->err);
+  p.tiles_per_item = plan.tiles_per_item;
+  p.items_per_list = plan.items_per_list;
+  p.total_items = static_cast<int>(plan.total_items);
+  p.q = q;
+  p.bounds = bounds;
+  p.scores = static_cast<float*>(st->data);
+  p.amax = reinterpret_cast<float*>(static_cast<uint8_t*>(st->data) + score_bytes);
+  p.group = group;
+  p.groups = groups;
+  p.width = group * G;
+  const CUtensorMap none = {};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  for (p.l0 = 0; p.l0 < d.L; p.l0 += per) {
+    p.rows = (d.L - p.l0 < per ? d.L - p.l0 : per) * G;
+    if (bdlm::launch_keys(true, none, none, p, st->num_sms, s) != cudaSuccess) return BDLM_ERR_CUDA;
+  }
+  const bdlm::SelectParams sp{q, bounds, page_table, prefix_lens, p.scores, p.amax,
+                              d.B, d.L, d.Hq, d.Hkv, G, d.max_pages_per_seq, d.num_pages, group,
+                              groups, p.tiles_per_item, p.items_per_list, n_select, sel_cols,
+                              sel_table, sel_lens, st->err};
+  return bdlm::launch_select_pages(sp, s) == cudaSuccess ? BDLM_OK : BDLM_ERR_CUDA;
+}
+
+int bdlm_sparse_attention(const bdlm_attn_desc* desc, const bdlm_bf16* q, const bdlm_bf16* k_pages,
+                          const bdlm_bf16* v_pages, int group, int sel_cols,
+                          const int32_t* sel_table, const int32_t* sel_lens, bdlm_bf16* out,
+                          bdlm_stream stream) {
+  if (!desc || !attn_desc_ok(*desc)) return BDLM_ERR_INVALID;
+  bdlm_attn_desc d = *desc;
+  if (group < 1 || d.L % group != 0 || sel_cols < 1) return BDLM_ERR_INVALID;
+  if (d.B == 0) return BDLM_OK;
+  if (!q || !k_pages || !v_pages || !sel_table || !sel_lens || !out || !aligned16(q) ||
+      !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out))
+    return BDLM_ERR_INVALID;
+  // every query group is an attention sequence with a page list per KV head
+  d.B *= d.L / group;
+  d.L = group;
+  d.max_pages_per_seq = sel_cols;
+  if (!attn_desc_ok(d)) return BDLM_ERR_INVALID;
+  std::lock_guard<std::mutex> lk(g_mu);
+  DeviceState* st = nullptr;
+  int rc = current_device(&st);
+  if (rc) return rc;
+  bdlm::AttnExt ext;
+  ext.head_tables = true;
+  return attention_impl(st, d, q, k_pages, v_pages, sel_table, sel_lens, out, stream, 1, 0,
+                        nullptr, &ext);
+}
+
+int bdlm_attention_weights(const bdlm_attn_desc* desc, const bdlm_bf16* q,
+                           const bdlm_bf16* k_pages, const int32_t* page_table,
+                           const int32_t* prefix_lens, const float* lse, float decay,
+                           float* weights, bdlm_stream stream) {
+  if (!desc || !attn_desc_ok(*desc) || !isfinite(decay)) return BDLM_ERR_INVALID;
+  const bdlm_attn_desc d = *desc;
+  if (d.B == 0) return BDLM_OK;
+  if (!q || !k_pages || !page_table || !prefix_lens || !lse || !weights || !aligned16(q) ||
+      !aligned16(k_pages))
+    return BDLM_ERR_INVALID;
+  std::lock_guard<std::mutex> lk(g_mu);
+  DeviceState* st = nullptr;
+  int rc = current_device(&st);
+  if (rc) return rc;
+  if ((rc = get_encoder())) return rc;
+  const int G = d.Hq / d.Hkv;
+  int per = bdlm::key_rows_max() / G;   // block positions of one launch
+  if (per > d.L) per = d.L;
+  const bdlm::KeyPlan plan = bdlm::plan_keys(d.B, d.Hkv, d.max_pages_per_seq * d.page_size,
+                                             per * G, st->num_sms);
+  if (plan.total_items > 0x7FFFFFFFll) return BDLM_ERR_INVALID;
+  CUtensorMap tm_q, tm_k;
+  {
+    cuuint64_t dims[4] = {128, static_cast<cuuint64_t>(d.Hkv), 16,
+                          static_cast<cuuint64_t>(d.num_pages)};
+    cuuint64_t strides[3] = {256, static_cast<cuuint64_t>(d.Hkv) * 256,
+                             static_cast<cuuint64_t>(d.Hkv) * 256 * 16};
+    cuuint32_t box[4] = {64, 1, 16, 1};
+    if ((rc = encode(&tm_k, k_pages, 4, dims, strides, box))) return rc;
+  }
+  bdlm::KeyParams p = key_params(d, page_table, prefix_lens, st->err);
+  p.tiles_per_item = plan.tiles_per_item;
+  p.items_per_list = plan.items_per_list;
+  p.total_items = static_cast<int>(plan.total_items);
+  p.lse = lse;
+  p.weights = weights;
+  p.decay = decay;
+  p.scale_log2 = (d.sm_scale > 0.f ? d.sm_scale : 1.0f / sqrtf(128.0f)) * 1.4426950408889634f;
+  // more than 256 query rows per KV head: one launch per 256, each adding to the one before
+  for (p.l0 = 0; p.l0 < d.L; p.l0 += per) {
+    const int nl = d.L - p.l0 < per ? d.L - p.l0 : per;
+    p.rows = nl * G;
+    cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(d.Hq), static_cast<cuuint64_t>(d.B) * d.L};
+    cuuint64_t strides[2] = {256, static_cast<cuuint64_t>(d.Hq) * 256};
+    cuuint32_t box[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(nl)};
+    if ((rc = encode(&tm_q, q, 3, dims, strides, box))) return rc;
+    if (bdlm::launch_keys(false, tm_q, tm_k, p, st->num_sms,
+                          static_cast<cudaStream_t>(stream)) != cudaSuccess)
+      return BDLM_ERR_CUDA;
+    p.decay = 1.f;
+  }
+  return BDLM_OK;
+}
+
+int bdlm_evict_kv(const bdlm_attn_desc* desc, bdlm_bf16* k_pages, bdlm_bf16* v_pages,
+                  const int32_t* page_table, const int32_t* lens, const float* weights, int keep,
+                  int recent, const int32_t* to_table, float* to_weights, int32_t* kept,
+                  int32_t* new_lens, bdlm_stream stream) {
+  if (!desc || !cache_desc_ok(*desc)) return BDLM_ERR_INVALID;
+  const bdlm_attn_desc d = *desc;
+  if (keep < 1 || keep > static_cast<long long>(d.max_pages_per_seq) * d.page_size || recent < 0 ||
+      recent > keep)
+    return BDLM_ERR_INVALID;
+  if (d.B == 0) return BDLM_OK;
+  if (!k_pages || !v_pages || !page_table || !lens || !weights || !to_table || !to_weights ||
+      !kept || !new_lens || lens == new_lens || !aligned16(k_pages) || !aligned16(v_pages))
+    return BDLM_ERR_INVALID;
+  std::lock_guard<std::mutex> lk(g_mu);
+  DeviceState* st = nullptr;
+  int rc = current_device(&st);
+  if (rc) return rc;
+  const bdlm::EvictParams p{lens, weights, to_weights, kept, new_lens, d.B, d.Hkv,
+                            d.max_pages_per_seq, keep, recent, st->err};
+  if (bdlm::launch_evict_select(p, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return BDLM_ERR_CUDA;
+  return compact_impl(st, d, k_pages, v_pages, page_table, nullptr, kept, d.Hkv, keep, new_lens,
+                      to_table, stream);
+}
+
+int bdlm_compact_kv(const bdlm_attn_desc* desc, bdlm_bf16* k_pages, bdlm_bf16* v_pages,
+                    const int32_t* page_table, const int32_t* base_lens, const int32_t* idx,
+                    int heads, int n_max, const int32_t* counts, const int32_t* to_table,
+                    bdlm_stream stream) {
+  if (!desc || !cache_desc_ok(*desc)) return BDLM_ERR_INVALID;
+  const bdlm_attn_desc d = *desc;
+  if ((heads != 1 && heads != d.Hkv) || n_max < 0) return BDLM_ERR_INVALID;
+  if (d.B == 0 || n_max == 0) return BDLM_OK;
+  if (!k_pages || !v_pages || !page_table || !idx || !counts || !to_table || !aligned16(k_pages) ||
+      !aligned16(v_pages))
+    return BDLM_ERR_INVALID;
+  std::lock_guard<std::mutex> lk(g_mu);
+  DeviceState* st = nullptr;
+  int rc = current_device(&st);
+  if (rc) return rc;
+  return compact_impl(st, d, k_pages, v_pages, page_table, base_lens, idx, heads, n_max, counts,
+                      to_table, stream);
 }
 
 }  // extern "C"

@@ -35,19 +35,26 @@
 //    partial, so no split is a short remainder), hand the items out longest splits first,
 //    stage the epilogue's stores through shared memory (whole 128-byte rows per store
 //    instruction), and wait with a suspend-time hint (fewer re-tries taking issue slots).
+//  * A tree of drafted tokens (EXT): each query sees the prefix and the block tokens of its
+//    64-bit visibility word.  Only the one or two tiles that hold block tokens differ from block
+//    attention: there a score outside the word reads as -inf (and its P is 0, never a product
+//    with it).  A query that sees nothing gets zeros; V rows that no query sees are zeroed in
+//    shared memory (they may hold anything, and 0 * NaN would poison O).  EXT also writes
+//    ln sum exp of each query's scores.  Separate instances, so block attention is unchanged.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
 #include <stdint.h>
 
 #include "attention_common.cuh"
+#include "cache_ops.h"
 #include "kernels.h"
 #include "ptx.cuh"
 
 namespace bdlm {
 namespace {
 
-template <int N, int STAGES, int CTAS_PER_SM, bool MASKED, bool ROWS, bool TWO>
+template <int N, int STAGES, int CTAS_PER_SM, bool MASKED, bool ROWS, bool TWO, bool EXT>
 __global__ void __launch_bounds__(attn_threads(ROWS, TWO), CTAS_PER_SM)
 attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
             const __grid_constant__ CUtensorMap tm_v, const AttnParams p) {
@@ -103,6 +110,8 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
   constexpr bool kPTmem = ROWS && !TWO;
   constexpr int kPBufs = 2;
   constexpr uint32_t kQCol = 384;   // first tensor-memory column of Q (kQTmem)
+  __shared__ unsigned long long s_seen[EXT ? kItemRing : 1];   // block tokens some query sees
+  static_assert(!EXT || !MASKED, "tree visibility and block-causal prefill are separate");
   static_assert(!MASKED || ROWS, "the block-causal mask is applied by the row-per-thread softmax");
   static_assert(!ROWS || N == 128, "rows on M: one UMMA of 128 query rows");
   static_assert(!TWO || ROWS, "two sub-groups only with rows on M");
@@ -183,10 +192,11 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     bool ok = true;
     int seq = -1;  // sequence number of the most recently published item
     // Publishes `it` to the item ring (lane 0).
-    auto publish = [&](const Item& it) {
+    auto publish = [&](const Item& it, unsigned long long seen = 0) {
       const int rs = seq % kItemRing;
       if (ok) ok = mbar_wait<ROWS>(&bar_iempty[rs], ((seq / kItemRing) & 1) ^ 1, &abort_flag);
       s_item[rs] = it;
+      if constexpr (EXT) s_seen[rs] = seen;
       mbar_arrive(&bar_ifull[rs]);
     };
     // Takes the next non-empty item from the global counter, publishes it to the item ring
@@ -212,7 +222,9 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       ++seq;
       int* pid = s_pid[seq % 3];
       const int32_t* pt =
-          p.page_table + static_cast<size_t>(it.b / p.table_div) * p.max_pages + it.t_begin / kPage;
+          p.page_table +
+          (static_cast<size_t>(it.b / p.table_div) * p.table_heads +
+           (p.table_heads > 1 ? it.kvh : 0)) * p.max_pages + it.t_begin / kPage;
       const int np = (it.t_end - it.t_begin + kPage - 1) / kPage;
       int bad = 0;
       for (int q = lane; q < np; q += 32) {
@@ -258,7 +270,18 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         fence_proxy_async_global();
         __syncwarp();
       }
-      if (lane == 0) publish(it);
+      unsigned long long seen = ~0ull;
+      if constexpr (EXT) {
+        if (p.tree_mask != nullptr && it.t_end > it.q0) {
+          unsigned long long m = 0;
+          for (int i = lane; i < p.L; i += 32)
+            m |= __ldg(p.tree_mask + static_cast<size_t>(it.b) * p.L + i);
+          seen = static_cast<unsigned long long>(
+                     __reduce_or_sync(0xffffffffu, static_cast<unsigned>(m >> 32))) << 32 |
+                 __reduce_or_sync(0xffffffffu, static_cast<unsigned>(m));
+        }
+      }
+      if (lane == 0) publish(it, seen);
       ok = __shfl_sync(0xffffffffu, ok, 0);
       return true;
     };
@@ -454,6 +477,21 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       int st = 0;
       uint32_t ph = 0;
       int pcount = 0, ocount = 0;
+      // EXT: zeroes the V rows of the block tokens that no query of the sequence sees, in the
+      // tile of `valid` tokens from token tok0 (stage in shared memory)
+      auto zero_unseen = [&](uint8_t* stage, const Item& it, int tok0, int valid,
+                             unsigned long long seen) {
+        bool any = false;
+        for (int t = max(0, it.q0 - tok0); t < valid; ++t) {
+          if ((seen >> (tok0 + t - it.q0)) & 1) continue;
+          any = true;
+          for (int h = 0; h < 2; ++h) {
+            uint4* z = reinterpret_cast<uint4*>(stage + h * kHalfBytes + t * 128);
+            for (int o = 0; o < 8; ++o) z[o] = make_uint4(0, 0, 0, 0);
+          }
+        }
+        if (any) fence_proxy_async_smem();
+      };
       // S of chunk `c` of `it` (global chunk number u): into S buffer u & 1, or with two
       // sub-groups into sub-group x's buffer x (one tile per chunk)
       auto do_s = [&](const Item& it, int c, int u, int seq) {
@@ -514,7 +552,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         if (!kQTmem && c == it.n_chunks - 1) umma_commit(&bar_qempty[qb]);  // Q no longer needed
       };
       // O^T += V^T P^T (O += P V) over the tiles of chunk `c`, for each sub-group
-      auto do_pv = [&](const Item& it, int c, int u) {
+      auto do_pv = [&](const Item& it, int c, int u, unsigned long long seen) {
         const int j0 = c * p.chunk_tiles;
         const int j1 = min(it.n_tiles, j0 + p.chunk_tiles);
         for (int j = j0; j < j1; ++j) {
@@ -533,6 +571,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             }
             fence_proxy_async_smem();
           }
+          if constexpr (EXT) zero_unseen(stage, it, tok0, valid, seen);
           const uint32_t va = kv_addr + st * kStageBytes;
           for (int x = 0; x < kSub; ++x) {
             const int pb = TWO ? x : pcount % kPBufs;
@@ -596,7 +635,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         umma_commit(&bar_sfull[x]);
       };
       auto do_pv_s = [&](const Item& it, int c, int u, const Item& nx, int nc, int nseq,
-                         bool has_next) {
+                         bool has_next, unsigned long long seen) {
         const int stv = st;
         if (!(ok = mbar_wait<ROWS>(&bar_full[stv], ph, &abort_flag))) return;
         if (++st == STAGES) {
@@ -617,6 +656,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
           }
           fence_proxy_async_smem();
         }
+        if constexpr (EXT) zero_unseen(sKV + stv * kStageBytes, it, tok0, valid, seen);
         const int stk = st;
         const uint32_t phk = ph;
         const int qb = nseq % kQBufs;
@@ -664,6 +704,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       Item cur, nxt;
       ok = mbar_wait<ROWS>(&bar_ifull[0], 0, &abort_flag);
       cur = s_item[0];
+      unsigned long long seen = EXT ? s_seen[0] : 0, seen_next = seen;
       if (ok && !cur.end) {
         int c = 0, u = 0;
         do_s(cur, 0, 0, 0);
@@ -679,6 +720,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             const int rs = nseq % kItemRing;
             if (!(ok = mbar_wait<ROWS>(&bar_ifull[rs], (nseq / kItemRing) & 1, &abort_flag))) break;
             nxt = s_item[rs];
+            if constexpr (EXT) seen_next = s_seen[rs];
             has_next = !nxt.end;
           }
           // S(u + 1) ahead of PV(u), so the softmax can start the next tile while PV runs
@@ -687,13 +729,14 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             if (!ok) break;
           }
           if constexpr (TWO)
-            do_pv_s(cur, c, u, nxt, nc, nseq, has_next);
+            do_pv_s(cur, c, u, nxt, nc, nseq, has_next, seen);
           else
-            do_pv(cur, c, u);
+            do_pv(cur, c, u, seen);
           if (!ok) break;
           if (c == cur.n_chunks - 1) mbar_arrive(&bar_iempty[seq % kItemRing]);
           if (!has_next) break;
           cur = nxt;
+          if constexpr (EXT) seen = seen_next;
           c = nc;
           seq = nseq;
           ++u;
@@ -729,6 +772,10 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       const int i_row = it.rg * p.lsub + r_item / p.G;
       int lim = 0x7FFFFFFF;                           // keys past q0 the row may see
       if constexpr (MASKED) lim = (i_row / p.mask_block + 1) * p.mask_block;
+      unsigned long long row_mask = ~0ull;            // block tokens the row sees
+      if constexpr (EXT)
+        if (p.tree_mask != nullptr && i_row < p.L && r_item < p.rows_per_group)
+          row_mask = __ldg(p.tree_mask + static_cast<size_t>(it.b) * p.L + i_row);
       float m_run = -CUDART_INF_F, l_run = 0.f;       // l_run: this half's sum
       for (int c = 0; c < it.n_chunks && ok; ++c, ++u) {
         if (!(ok = mbar_wait_warp<ROWS>(&bar_sfull[x], u & 1, &abort_flag))) break;
@@ -737,7 +784,10 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         int nvalid = min(kTile, it.t_end - key0);
         if constexpr (MASKED) nvalid = min(nvalid, lim - (key0 - it.q0));
         nvalid -= half * 64;   // of this half's columns
-        const bool full = nvalid >= 64;   // every score of this half-row is a key the row sees
+        unsigned long long word = ~0ull;
+        if constexpr (EXT) word = seen_word(row_mask, key0 - it.q0 + half * 64, nvalid);
+        // every score of this half-row is a key the row sees
+        const bool full = EXT ? word == ~0ull : nvalid >= 64;
         // pass 1: the half-row max, 32 scores at a time; then the row max
         float mx = -CUDART_INF_F;
 #pragma unroll
@@ -748,7 +798,12 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
           tmem_wait_ld();
           tmem_regs_ready(*reinterpret_cast<uint32_t(*)[16]>(r));
           tmem_regs_ready(*reinterpret_cast<uint32_t(*)[16]>(r + 16));
-          mx = fmaxf(mx, full ? max32<true>(r, 0, 0) : max32<false>(r, g2 * 32, nvalid));
+          if constexpr (EXT) {
+            if (!full) mask32(r, static_cast<uint32_t>(word >> (g2 * 32)));
+            mx = fmaxf(mx, max32<true>(r, 0, 0));
+          } else {
+            mx = fmaxf(mx, full ? max32<true>(r, 0, 0) : max32<false>(r, g2 * 32, nvalid));
+          }
         }
         s_hmax[pe & 1][x][half][n] = mx;
         mbar_arrive(&bar_pair[pq][pe & 1]);
@@ -778,8 +833,13 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
           tmem_regs_ready(*reinterpret_cast<uint32_t(*)[16]>(r));
           tmem_regs_ready(*reinterpret_cast<uint32_t(*)[16]>(r + 16));
           uint32_t pk[16];
-          sum += full ? exp_pack32<true>(r, 0, 0, cs2, nm2, pk)
-                      : exp_pack32<false>(r, g2 * 32, nvalid, cs2, nm2, pk);
+          if constexpr (EXT) {
+            if (!full) mask32(r, static_cast<uint32_t>(word >> (g2 * 32)));
+            sum += exp_pack32<true>(r, 0, 0, cs2, nm2, pk);
+          } else {
+            sum += full ? exp_pack32<true>(r, 0, 0, cs2, nm2, pk)
+                        : exp_pack32<false>(r, g2 * 32, nvalid, cs2, nm2, pk);
+          }
           tmem_st16(tSx + g2 * 16, pk);   // keys 64h + 32 g2 .. + 31 as 16 columns
         }
         l_run = l_run * alpha + sum;
@@ -821,7 +881,11 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         uint16_t* dst = live ? p.out + ((static_cast<size_t>(it.b) * p.L + i_row) * p.Hq +
                                         static_cast<size_t>(it.kvh) * p.G + r_item % p.G) * 128 + col0
                              : p.out;
-        const float inv = 1.f / l_row;
+        const float inv = EXT && !(l_row > 0.f) ? 0.f : 1.f / l_row;
+        if constexpr (EXT)
+          if (p.lse != nullptr && live && it.n_splits == 1 && half == 0)
+            p.lse[(static_cast<size_t>(it.b) * p.L + i_row) * p.Hq +
+                  static_cast<size_t>(it.kvh) * p.G + r_item % p.G] = row_lse(m_run, l_row, cs);
         uint8_t* stage = s_stage[warp - 2];
         if (it.n_splits == 1) {
           // this half of the row as bf16: 128 bytes per lane
@@ -884,6 +948,10 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       if (it.end) break;
       int i_row[kSub], lim[kSub];   // block position of the row; keys past q0 it may see
       float m_run[kSub], l_run[kSub];   // l_run: this half's sum
+      unsigned long long row_mask = ~0ull;   // EXT (one sub-group): block tokens the row sees
+      if constexpr (EXT)
+        if (p.tree_mask != nullptr && n < p.rows_per_group && it.rg * p.lsub + n / p.G < p.L)
+          row_mask = __ldg(p.tree_mask + static_cast<size_t>(it.b) * p.L + it.rg * p.lsub + n / p.G);
 #pragma unroll
       for (int x = 0; x < kSub; ++x) {
         i_row[x] = it.rg * p.lsub + (x * N + n) / p.G;
@@ -916,7 +984,13 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
           int nvalid = min(kTile, it.t_end - key0);
           if constexpr (MASKED) nvalid = min(nvalid, lim[x] - (key0 - it.q0));
           nvalid -= half * 64;   // of this half's columns
-          if (nvalid < 64) {
+          if constexpr (EXT) {
+            const unsigned long long word = seen_word(row_mask, key0 - it.q0 + half * 64, nvalid);
+            if (word != ~0ull) {
+              mask32(*reinterpret_cast<uint32_t(*)[32]>(r), static_cast<uint32_t>(word));
+              mask32(*reinterpret_cast<uint32_t(*)[32]>(r + 32), static_cast<uint32_t>(word >> 32));
+            }
+          } else if (nvalid < 64) {
 #pragma unroll
             for (int k = 0; k < 64; ++k)
               if (k >= nvalid) r[k] = 0xFF800000u;
@@ -1013,7 +1087,12 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
               live ? p.out + ((static_cast<size_t>(it.b) * p.L + i_row[x]) * p.Hq +
                               static_cast<size_t>(it.kvh) * p.G + r_item % p.G) * 128 + col0
                    : p.out;
-          const float inv = 1.f / l_row;
+          const float inv = EXT && !(l_row > 0.f) ? 0.f : 1.f / l_row;
+          if constexpr (EXT)
+            if (p.lse != nullptr && live && it.n_splits == 1 && half == 0)
+              p.lse[(static_cast<size_t>(it.b) * p.L + i_row[x]) * p.Hq +
+                    static_cast<size_t>(it.kvh) * p.G + r_item % p.G] =
+                  row_lse(m_run[x], l_row, cs);
           uint8_t* stage = s_stage[warp - 2];
           const uint32_t tOr = tO + lane_off + x * N + col0;
           if (it.n_splits == 1) {
@@ -1079,6 +1158,17 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         const uint32_t tS = tmem + lane_off + static_cast<uint32_t>((u & 1) * p.chunk_tiles * N);
         if (!(ok = mbar_wait_warp<ROWS>(&bar_sfull[u & 1], (u >> 1) & 1, &abort_flag))) break;
         tc_fence_after();
+        // EXT: the columns (query rows) that see this thread's key of tile j, as a bit word
+        auto seen_by = [&](int j) -> uint32_t {
+          const int key = it.t_begin + j * kTile + x;
+          if (key >= it.t_end) return 0;
+          if (key < it.q0 || p.tree_mask == nullptr) return ~0u;
+          const unsigned long long* m = p.tree_mask + static_cast<size_t>(it.b) * p.L;
+          uint32_t w = 0;
+          for (int i = 0; i < p.L; ++i)   // at most 32 rows: one row group, row i * G + g
+            if ((__ldg(m + i) >> (key - it.q0)) & 1) w |= ((1u << p.G) - 1) << (i * p.G);
+          return w;
+        };
         // phase A: exact column maxima over the chunk
 #pragma unroll
         for (int cg = 0; cg < N / 16; ++cg) {
@@ -1090,10 +1180,17 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             tmem_ld16(tS + (j - j0) * N + cg * 16, r);
             tmem_wait_ld();
             tmem_regs_ready(r);
-            const bool valid = it.t_begin + j * kTile + x < it.t_end;
+            if constexpr (EXT) {
+              const uint32_t w = seen_by(j) >> (cg * 16);
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
-              if (valid) mx[k] = fmaxf(mx[k], __uint_as_float(r[k]));
+              for (int k = 0; k < 16; ++k)
+                if ((w >> k) & 1) mx[k] = fmaxf(mx[k], __uint_as_float(r[k]));
+            } else {
+              const bool valid = it.t_begin + j * kTile + x < it.t_end;
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                if (valid) mx[k] = fmaxf(mx[k], __uint_as_float(r[k]));
+            }
           }
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
@@ -1125,7 +1222,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
           }
           s_alpha[x] = alpha;
           s_m[x] = mn;
-          s_mc[x] = mn * cs;
+          s_mc[x] = EXT && mn == -CUDART_INF_F ? 0.f : mn * cs;   // (no key seen yet: P = 0)
         }
         named_barrier(1, kSoftmaxThreads);
         const bool need = s_need[u & 1] != 0;
@@ -1171,10 +1268,17 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             for (int cg = 0; cg < N / 16; ++cg)
               tmem_regs_ready(*reinterpret_cast<uint32_t(*)[16]>(r + cg * 16));
             float pv[N];
-            const bool valid = it.t_begin + j * kTile + x < it.t_end;
+            if constexpr (EXT) {
+              const uint32_t w = seen_by(j);
   #pragma unroll
-            for (int n = 0; n < N; ++n)
-              pv[n] = valid ? exp2f(fmaf(__uint_as_float(r[n]), cs, -mcr[n])) : 0.f;
+              for (int n = 0; n < N; ++n)
+                pv[n] = (w >> n) & 1 ? exp2f(fmaf(__uint_as_float(r[n]), cs, -mcr[n])) : 0.f;
+            } else {
+              const bool valid = it.t_begin + j * kTile + x < it.t_end;
+  #pragma unroll
+              for (int n = 0; n < N; ++n)
+                pv[n] = valid ? exp2f(fmaf(__uint_as_float(r[n]), cs, -mcr[n])) : 0.f;
+            }
             if (j + 1 < j1) {
   #pragma unroll
               for (int cg = 0; cg < N / 16; ++cg) {
@@ -1225,6 +1329,10 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
         if (x < N) s_l[x] = (s_red[0][x] + s_red[1][x]) + (s_red[2][x] + s_red[3][x]);
         named_barrier(1, kSoftmaxThreads);
         const size_t head_base = static_cast<size_t>(it.kvh) * p.G;
+        if constexpr (EXT)
+          if (p.lse != nullptr && it.n_splits == 1 && x < rows && x / p.G < p.L)
+            p.lse[(static_cast<size_t>(it.b) * p.L + x / p.G) * p.Hq + head_base + x % p.G] =
+                row_lse(s_m[x], s_l[x], cs);
         if (it.n_splits == 1) {
 #pragma unroll
           for (int cg = 0; cg < N / 16; ++cg) {
@@ -1240,7 +1348,9 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
               if (i >= p.L) continue;
               const size_t o =
                   ((static_cast<size_t>(it.b) * p.L + i) * p.Hq + head_base + n % p.G) * 128 + x;
-              p.out[o] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(r[k]) / s_l[n]));
+              const float ov = __uint_as_float(r[k]);
+              p.out[o] = __bfloat16_as_ushort(
+                  __float2bfloat16_rn(EXT && !(s_l[n] > 0.f) ? 0.f : ov / s_l[n]));
             }
           }
         } else {
@@ -1359,6 +1469,7 @@ attn_order_kernel(const AttnParams p, bool whole, int* __restrict__ order) {
 // flight together and the grid fits the GPU in one wave.
 constexpr int kMergeRows = 2;
 
+template <bool EXT>
 __global__ void __launch_bounds__(256)
 attn_merge_kernel(const AttnParams p, int N) {
   const int lane = threadIdx.x & 31;
@@ -1399,6 +1510,11 @@ attn_merge_kernel(const AttnParams p, int N) {
   const int per = split_len(static_cast<int>(kvl), p);
   const int ns = static_cast<int>((kvl + per - 1) / per);
   if (ns <= 1) return;
+  auto write_lse = [&](bool live, int n, float M, float den) {
+    if (p.lse != nullptr && live && lane == 0)
+      p.lse[(static_cast<size_t>(b) * p.L + rg * p.lsub + n / p.G) * p.Hq +
+            static_cast<size_t>(kvh) * p.G + n % p.G] = row_lse(M, den, p.scale_log2);
+  };
   float4 acc[kMergeRows];
 #pragma unroll
   for (int r = 0; r < kMergeRows; ++r) acc[r] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1414,11 +1530,14 @@ attn_merge_kernel(const AttnParams p, int N) {
       float M = ml[r];
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+      if constexpr (EXT)
+        if (M == -CUDART_INF_F) M = 0.f;   // a row that sees no key in any split: every e is 0
       const float e = lane < ns ? exp2f((ml[r] - M) * p.scale_log2) : 0.f;
       float den = e * ll[r];
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) den += __shfl_xor_sync(0xffffffffu, den, off);
-      wl[r] = valid[r] ? e / den : 0.f;
+      wl[r] = valid[r] && !(EXT && !(den > 0.f)) ? e / den : 0.f;
+      if constexpr (EXT) write_lse(valid[r], n0 + r, M, den);
     }
 #pragma unroll 4
     for (int j = 0; j < ns; ++j) {
@@ -1445,6 +1564,8 @@ attn_merge_kernel(const AttnParams p, int N) {
         if (s0 + lane < ns) M = fmaxf(M, __ldcg(all + (s0 + lane) * unit + N * 128 + n));
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+      if constexpr (EXT)
+        if (M == -CUDART_INF_F) M = 0.f;
       float den = 0.f;
       for (int s0 = 0; s0 < ns; s0 += 32)
         if (s0 + lane < ns) {
@@ -1453,7 +1574,8 @@ attn_merge_kernel(const AttnParams p, int N) {
         }
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) den += __shfl_xor_sync(0xffffffffu, den, off);
-      const float inv = 1.0f / den;
+      const float inv = EXT && !(den > 0.f) ? 0.f : 1.0f / den;
+      if constexpr (EXT) write_lse(true, n, M, den);
       for (int s0 = 0; s0 < ns; s0 += 32) {
         const int cnt = min(32, ns - s0);
         float wl = 0.f;
@@ -1497,22 +1619,22 @@ constexpr size_t smem_bytes() {
   return 1024 + q + static_cast<size_t>(STAGES) * kStageBytes + pbufs * N * 256;
 }
 
-template <int N, int STAGES, int CPS, bool MASKED, bool ROWS, bool TWO>
+template <int N, int STAGES, int CPS, bool MASKED, bool ROWS, bool TWO, bool EXT = false>
 cudaError_t launch_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                      const AttnParams& prm, int num_sms, cudaStream_t stream) {
   constexpr size_t smem = smem_bytes<N, STAGES, ROWS, TWO>();
   static std::atomic<unsigned long long> attr_done{0};
   cudaError_t e = once_per_device(attr_done, [] {
-    cudaError_t r = cudaFuncSetAttribute(attn_kernel<N, STAGES, CPS, MASKED, ROWS, TWO>,
+    cudaError_t r = cudaFuncSetAttribute(attn_kernel<N, STAGES, CPS, MASKED, ROWS, TWO, EXT>,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(smem));
     if (r != cudaSuccess) return r;
-    return cudaFuncSetAttribute(attn_kernel<N, STAGES, CPS, MASKED, ROWS, TWO>,
+    return cudaFuncSetAttribute(attn_kernel<N, STAGES, CPS, MASKED, ROWS, TWO, EXT>,
                                 cudaFuncAttributePreferredSharedMemoryCarveout,
                                 cudaSharedmemCarveoutMaxShared);
   });
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_kernel<N, STAGES, CPS, MASKED, ROWS, TWO>, dim3(num_sms * CPS),
+  return launch_pdl(attn_kernel<N, STAGES, CPS, MASKED, ROWS, TWO, EXT>, dim3(num_sms * CPS),
                     dim3(attn_threads(ROWS, TWO)), smem,
                     stream, tq, tk, tv, prm);
 }
@@ -1609,7 +1731,24 @@ cudaError_t launch_attention(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                              const AttnPlan& plan, float* part, int* cnt, int* err, int num_sms,
                              cudaStream_t stream, int table_div, int mask_block,
                              const BlockKvWrite* kv_write) {
+  return launch_attention_ext(tm_q, tm_k, tm_v, page_table, prefix_lens, out, B, L, Hq, Hkv,
+                              max_pages, num_pages, sm_scale, plan, part, cnt, err, num_sms,
+                              stream, table_div, mask_block, kv_write, nullptr);
+}
+
+cudaError_t launch_attention_ext(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                                 const CUtensorMap& tm_v, const int32_t* page_table,
+                                 const int32_t* prefix_lens, uint16_t* out, int B, int L, int Hq,
+                                 int Hkv, int max_pages, int num_pages, float sm_scale,
+                                 const AttnPlan& plan, float* part, int* cnt, int* err,
+                                 int num_sms, cudaStream_t stream, int table_div, int mask_block,
+                                 const BlockKvWrite* kv_write, const AttnExt* ext) {
   AttnParams prm;
+  const bool tree = ext != nullptr && ext->tree;
+  if (tree && (mask_block > 0 || kv_write)) return cudaErrorInvalidValue;
+  prm.table_heads = ext != nullptr && ext->head_tables ? Hkv : 1;
+  prm.tree_mask = reinterpret_cast<const unsigned long long*>(tree ? ext->tree_mask : nullptr);
+  prm.lse = tree ? ext->lse : nullptr;
   prm.mask_block = mask_block > 0 ? mask_block : 0;
   prm.k_new = kv_write ? kv_write->k_new : nullptr;
   prm.v_new = kv_write ? kv_write->v_new : nullptr;
@@ -1658,7 +1797,23 @@ cudaError_t launch_attention(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
     prm.order = order;
     prm.rank_major = 1;
   }
-  switch (plan.n_mma) {
+  if (tree) {
+    switch (plan.n_mma) {
+      case 16:
+        e = launch_t<16, 3, 2, false, false, false, true>(tm_q, tm_k, tm_v, prm, num_sms, stream);
+        break;
+      case 32:
+        e = launch_t<32, 2, 2, false, false, false, true>(tm_q, tm_k, tm_v, prm, num_sms, stream);
+        break;
+      case 128:
+        e = launch_t<128, 5, 1, false, true, false, true>(tm_q, tm_k, tm_v, prm, num_sms, stream);
+        break;
+      case 256:
+        e = launch_t<128, 4, 1, false, true, true, true>(tm_q, tm_k, tm_v, prm, num_sms, stream);
+        break;
+      default: return cudaErrorInvalidValue;
+    }
+  } else switch (plan.n_mma) {
     case 16:
       if (mask_block > 0) return cudaErrorInvalidValue;   // the mask needs rows on M
       e = launch_t<16, 3, 2, false, false, false>(tm_q, tm_k, tm_v, prm, num_sms, stream);
@@ -1682,7 +1837,7 @@ cudaError_t launch_attention(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
   if (e != cudaSuccess || plan.max_splits <= 1) return e;
   const long long groups = static_cast<long long>(B) * Hkv * plan.row_groups;
   const int row_blocks = (plan.G * plan.lsub + 8 * kMergeRows - 1) / (8 * kMergeRows);
-  e = launch_pdl(attn_merge_kernel, dim3(static_cast<unsigned>(groups), row_blocks), dim3(256), 0,
+  e = launch_pdl(tree ? attn_merge_kernel<true> : attn_merge_kernel<false>, dim3(static_cast<unsigned>(groups), row_blocks), dim3(256), 0,
                  stream, prm, plan.n_mma);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();

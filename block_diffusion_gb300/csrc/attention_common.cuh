@@ -70,6 +70,9 @@ struct AttnParams {
   const int* order;  // whole-sequence mode: sequences by decreasing KV length, else null
   int B, L, Hq, Hkv, G, max_pages, num_pages;
   int table_div;     // sequence b uses page-table row b / table_div (prompt blocks share a row)
+  int table_heads;   // page lists per sequence: 1, or Hkv (every KV head reads pages of its own)
+  const unsigned long long* tree_mask;  // [B, L] block tokens a query sees (EXT; null: all of them)
+  float* lse;                           // [B, L, Hq] ln sum exp of the scores (EXT; null: not wanted)
   int lsub, row_groups, rows_per_group, split_tokens, max_splits, chunk_tiles;
   int even_splits;   // cut each sequence into equal splits of at most split_tokens
   int rank_major;    // items sequence by sequence in `order`, all splits of one together
@@ -151,6 +154,28 @@ __device__ __forceinline__ bool decode_item(int idx, const AttnParams& p, Item& 
   return true;
 }
 
+// Block keys seen by a query with visibility word m, as a word over the 64 keys base .. base + 63
+// past the sequence's first query (base < 0: prefix keys, which every query sees), the first
+// nvalid of which exist.
+__device__ __forceinline__ unsigned long long seen_word(unsigned long long m, int base, int nvalid) {
+  unsigned long long w = ~0ull;
+  if (base >= 64)
+    w = 0;
+  else if (base >= 0)
+    w = m >> base;
+  else if (base > -64)
+    w = (m << -base) | ((1ull << -base) - 1);
+  if (nvalid < 64) w &= nvalid <= 0 ? 0ull : (1ull << nvalid) - 1;
+  return w;
+}
+
+// ln sum exp of a row from its running max (raw score) and sum of exponentials; a row that saw
+// no key has none.
+__device__ __forceinline__ float row_lse(float m, float l, float scale_log2) {
+  constexpr float kLn2 = 0.6931471805599453f;
+  return l > 0.f ? fmaf(m, scale_log2, __log2f(l)) * kLn2 : -CUDART_INF_F;
+}
+
 // Writes 128 bytes per lane to global memory (lane l: w, the 32 words of its row piece; dst,
 // where they go, or null for nothing) through a 1 KB shared-memory staging buffer, 8 rows at a
 // time, so that each global store instruction writes four whole 128-byte row pieces instead of
@@ -178,6 +203,13 @@ __device__ __forceinline__ void store_rows_128b(const uint32_t (&w)[32], void* d
     }
     __syncwarp();
   }
+}
+
+// Scores whose bit of w is clear read as -inf.
+__device__ __forceinline__ void mask32(uint32_t (&r)[32], uint32_t w) {
+#pragma unroll
+  for (int k = 0; k < 32; ++k)
+    if (!((w >> k) & 1)) r[k] = 0xFF800000u;
 }
 
 // Rows on M, two sub-groups: 32 scores of a half-row (keys base .. base + 31 of its 64).

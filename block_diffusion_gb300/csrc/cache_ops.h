@@ -1,0 +1,104 @@
+// Internal interface of the operators that read or keep part of the paged cache: tree and sparse
+// attention (attention.cu), page bounds, page scores and attention weights (key_scores.cu), page
+// selection and eviction (select.cu).
+#pragma once
+
+#include "kernels.h"
+
+namespace bdlm {
+
+// What block attention takes beyond launch_attention's arguments.
+struct AttnExt {
+  bool tree = false;                     // the kernels that take a tree mask and write lse
+  const uint64_t* tree_mask = nullptr;   // [B, L] visibility words, or null: every query sees all L
+  float* lse = nullptr;                  // [B, L, Hq], or null
+  bool head_tables = false;              // page_table holds a row per (sequence, KV head)
+};
+
+cudaError_t launch_attention_ext(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                                 const CUtensorMap& tm_v, const int32_t* page_table,
+                                 const int32_t* prefix_lens, uint16_t* out, int B, int L, int Hq,
+                                 int Hkv, int max_pages, int num_pages, float sm_scale,
+                                 const AttnPlan& plan, float* part, int* cnt, int* err,
+                                 int num_sms, cudaStream_t stream, int table_div, int mask_block,
+                                 const BlockKvWrite* kv_write, const AttnExt* ext);
+
+// ------------------------------------------------------------------ key_scores.cu
+struct KeyPlan {
+  int tiles_per_item = 1, items_per_list = 1;
+  long long total_items = 0;
+  size_t amax_floats = 0;   // page scores: largest |bound| per (run, gathering warp)
+};
+
+struct KeyParams {
+  const int32_t* page_table;
+  const int32_t* prefix_lens;
+  int B, L, Hq, Hkv, G, max_pages, num_pages;
+  int l0, rows;                // query rows l0 * G .. + rows of each (sequence, KV head)
+  int tiles_per_item, items_per_list, total_items;
+  int* err;
+  // attention weights
+  const float* lse;            // [B, L, Hq]
+  float* weights;              // [B, Hkv, max_pages * 16]
+  float decay, scale_log2;
+  // page scores
+  const uint16_t* q;
+  const uint16_t* bounds;      // [num_pages, Hkv, 2, 128]
+  float* scores;               // [B, groups, Hkv, max_pages]
+  float* amax;                 // [B, Hkv, items_per_list, 8]
+  int group, groups, width;    // positions per group, groups per sequence, query rows per group
+};
+
+KeyPlan plan_keys(int B, int Hkv, int max_keys, int rows, int num_sms);
+int key_rows_max();   // query rows of one launch
+// pages: page scores (tm_q, tm_k unused), else attention weights.
+cudaError_t launch_keys(bool pages, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                        const KeyParams& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_page_bounds(const uint16_t* k_pages, const int32_t* page_table,
+                               const int32_t* from, const int32_t* to, int B, int Hkv,
+                               int max_pages, int num_pages, int num_sms, uint16_t* bounds,
+                               int* err, cudaStream_t stream);
+
+// ------------------------------------------------------------------ select.cu
+struct SelectParams {
+  const uint16_t* q;
+  const uint16_t* bounds;
+  const int32_t* page_table;
+  const int32_t* prefix_lens;
+  const float* scores;
+  const float* amax;
+  int B, L, Hq, Hkv, G, max_pages, num_pages, group, groups;
+  int tiles_per_item, items_per_list;
+  int n_select, sel_cols;
+  int32_t* sel_table;
+  int32_t* sel_lens;
+  int* err;
+};
+constexpr int kSelectMaxPages = 262144;   // a list's page bitmap fits shared memory
+cudaError_t launch_select_pages(const SelectParams& p, cudaStream_t stream);
+
+struct EvictParams {
+  const int32_t* lens;
+  const float* weights;
+  float* to_weights;
+  int32_t* kept;       // [B, Hkv, keep]
+  int32_t* new_lens;
+  int B, Hkv, max_pages, keep, recent;
+  int* err;
+};
+cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t stream);
+
+struct CompactParams {
+  uint16_t* k_pages;
+  uint16_t* v_pages;
+  const int32_t* page_table;
+  const int32_t* to_table;    // page_table itself: in place
+  const int32_t* base;        // [B] first position, or null: 0
+  const int32_t* idx;         // [B, heads, n_max]
+  const int32_t* counts;      // [B]
+  int B, Hkv, heads, max_pages, num_pages, n_max;
+  int* err;
+};
+cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream);
+
+}  // namespace bdlm

@@ -1,0 +1,666 @@
+// The choices over a paged cache and the moves that follow them: the best pages of each query
+// group, the tokens that an eviction keeps, and the move of kept tokens to the front.
+//
+// Top k of a row of floats: the row's keys (floats mapped to unsigned integers of the same order)
+// are counted in up to 2048 buckets that evenly divide the range still in question, the bucket
+// holding the k-th largest becomes the next range, and so on; 32-bit keys take three rounds at
+// most.  One CTA per row, everything after the first read in shared memory where it fits.  The
+// buckets divide the range in use (min .. max first), not fixed bits of the key: rows of similar
+// values would otherwise fall into a few buckets, whose counters then serialise.  Ties at the k-th
+// value go to the lowest index, and the output is in index order, so nothing depends on the order
+// in which threads run.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+#include <stdint.h>
+
+#include "cache_ops.h"
+#include "ptx.cuh"
+
+namespace bdlm {
+namespace {
+
+constexpr int kTok = 16;       // tokens per page
+constexpr int kBuckets = 2048;
+
+// Unsigned key with the floats' order; -0 and +0 are equal, NaN comes below every number.
+__device__ __forceinline__ uint32_t order_key(float f) {
+  if (f != f) return 0;
+  const uint32_t u = __float_as_uint(f + 0.0f);   // -0 -> +0
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+struct BlockSum {   // sums and scans over the CTA; s: one word per warp
+  int* s;
+  __device__ __forceinline__ int exclusive(int v, int* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, off);
+      if (lane >= off) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) s[warp] = x;
+    __syncthreads();
+    int before = 0, all = 0;
+    for (int w = 0; w < warps; ++w) {
+      if (w < warp) before += s[w];
+      all += s[w];
+    }
+    *total = all;
+    return before + x - v;
+  }
+};
+
+// Minimum and maximum over the CTA (every thread gets both).
+template <typename T>
+__device__ __forceinline__ void block_range(T& lo, T& hi, T* s) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    const T a = __shfl_xor_sync(0xffffffffu, lo, off), b = __shfl_xor_sync(0xffffffffu, hi, off);
+    lo = a < lo ? a : lo;
+    hi = b > hi ? b : hi;
+  }
+  const int warps = blockDim.x >> 5;
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) {
+    s[threadIdx.x >> 5] = lo;
+    s[32 + (threadIdx.x >> 5)] = hi;
+  }
+  __syncthreads();
+  for (int w = 0; w < warps; ++w) {
+    lo = s[w] < lo ? s[w] : lo;
+    hi = s[32 + w] > hi ? s[32 + w] : hi;
+  }
+  __syncthreads();
+}
+
+// The k-th largest of the keys that `each` yields (each(f): calls f(key) for this thread's share,
+// the same keys every time), 1 <= k <= their number, all within [lo, hi].  Returns it, and in
+// *above how many are larger.  hist: kBuckets counters.  Whole CTA.
+template <typename K, typename Each>
+__device__ __forceinline__ K kth_largest(int k, K lo, K hi, Each&& each, int* hist, int* s_scan,
+                                         K* s_pick, int* above) {
+  int larger = 0;
+  BlockSum sum{s_scan};
+  while (lo < hi) {
+    const K range = hi - lo;
+    int bits = sizeof(K) == 8 ? 64 - __clzll(static_cast<long long>(range))
+                              : 32 - __clz(static_cast<int>(range));
+    const int shift = bits > 11 ? bits - 11 : 0;
+    for (int i = threadIdx.x; i < kBuckets; i += blockDim.x) hist[i] = 0;
+    __syncthreads();
+    each([&](K key) {
+      if (key >= lo && key <= hi) atomicAdd(&hist[static_cast<int>((key - lo) >> shift)], 1);
+    });
+    __syncthreads();
+    // this thread's buckets, counted from the top
+    const int per = kBuckets / static_cast<int>(blockDim.x);
+    int mine = 0;
+    for (int i = 0; i < per; ++i)
+      mine += hist[kBuckets - 1 - (static_cast<int>(threadIdx.x) * per + i)];
+    int total;
+    int before = larger + sum.exclusive(mine, &total);
+    if (before < k && before + mine >= k) {
+      for (int i = 0; i < per; ++i) {
+        const int bucket = kBuckets - 1 - (static_cast<int>(threadIdx.x) * per + i);
+        if (before + hist[bucket] >= k) {
+          s_pick[0] = static_cast<K>(bucket);
+          s_scan[33] = before;
+          break;
+        }
+        before += hist[bucket];
+      }
+    }
+    __syncthreads();
+    const K from = lo + (s_pick[0] << shift), width = (static_cast<K>(1) << shift) - 1;
+    larger = s_scan[33];
+    if (hi - from > width) hi = from + width;
+    lo = from;
+    __syncthreads();
+  }
+  *above = larger;
+  return lo;
+}
+
+// ------------------------------------------------------------------ page selection
+constexpr int kSelThreads = 512;
+constexpr int kSelKeys = 16384;      // keys held in shared memory (64 KB); longer rows are re-read
+constexpr int kSelExact = 1024;      // near ties held in shared memory
+
+// a + b as s + e exactly
+__device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
+  s = __fadd_rn(a, b);
+  const float bb = __fadd_rn(s, -a);
+  e = __fadd_rn(__fadd_rn(a, -__fadd_rn(s, -bb)), __fadd_rn(b, -bb));
+}
+
+// The score of one page for one group, to about 2^-45 of its terms, as an ordered 64-bit key.
+// Whole warp: lane l takes dims 4l .. 4l + 3.  The products of two bf16 are exact in float32; they
+// are added with the rounding errors carried along.
+__device__ __forceinline__ unsigned long long exact_score(const SelectParams& p, int b, int s,
+                                                          int kvh, int id) {
+  const int lane = threadIdx.x & 31;
+  const uint2* row = reinterpret_cast<const uint2*>(p.bounds) +
+                     (static_cast<size_t>(id) * p.Hkv + kvh) * 64 + lane;
+  const uint2 lo = __ldg(row), hi = __ldg(row + 32);
+  unsigned long long best = 0;
+  for (int n = 0; n < p.group * p.G; ++n) {
+    const int i = s * p.group + n / p.G;
+    const uint2 q = __ldg(reinterpret_cast<const uint2*>(p.q) +
+                          ((static_cast<size_t>(b) * p.L + i) * p.Hq + kvh * p.G + n % p.G) * 32 +
+                          lane);
+    const float qv[4] = {bf16_lo(q.x), bf16_hi(q.x), bf16_lo(q.y), bf16_hi(q.y)};
+    const float lv[4] = {bf16_lo(lo.x), bf16_hi(lo.x), bf16_lo(lo.y), bf16_hi(lo.y)};
+    const float hv[4] = {bf16_lo(hi.x), bf16_hi(hi.x), bf16_lo(hi.y), bf16_hi(hi.y)};
+    float a = 0.f, e = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float r;
+      two_sum(a, __fmul_rn(qv[k], qv[k] > 0.f ? hv[k] : lv[k]), a, r);
+      e = __fadd_rn(e, r);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      const float a2 = __shfl_xor_sync(0xffffffffu, a, off);
+      const float e2 = __shfl_xor_sync(0xffffffffu, e, off);
+      float r;
+      two_sum(a, a2, a, r);
+      e = __fadd_rn(__fadd_rn(e, e2), r);
+    }
+    float top, rest;
+    two_sum(a, e, top, rest);   // normalised: top decides, then rest
+    const unsigned long long key =
+        static_cast<unsigned long long>(order_key(top)) << 32 | order_key(rest);
+    best = key > best ? key : best;
+  }
+  return best;
+}
+
+// One CTA per (sequence, query group, KV head).  The scores come from the tensor core in float32;
+// where two of them lie closer than their rounding could explain, float32 does not say which is
+// larger.  So with T the k-th largest and E a bound on a score's error, pages above T + 2E are
+// in, pages below T - 2E are out, and the few between are scored again to about 45 bits.
+//   E = 2^-14 max_n |q_n|_1 max |bound|: a score sums 128 products (and 128 zeros) in 16 MMAs
+//   of 16; each adds at most 17 roundings or truncations of 2^-23 of the largest partial sum, which
+//   is at most |q|_1 max|bound|, so the error is below 16 * 17 * 2^-23 < 2^-14.9 of it.
+// Latency bound: a few thousand keys, three rounds over shared memory; the launch is one CTA per
+// list, so long batches overlap several per SM.
+__global__ void __launch_bounds__(kSelThreads)
+select_pages_kernel(const SelectParams p) {
+  extern __shared__ uint32_t sm[];
+  __shared__ int hist[kBuckets];
+  __shared__ unsigned long long s_exact[kSelExact];
+  __shared__ int s_page[kSelExact];
+  __shared__ int s_scan[34];
+  __shared__ unsigned long long s_wide[64];
+  __shared__ unsigned long long s_pick[1];
+  __shared__ int s_cand;
+  __shared__ float s_f[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kWarps = kSelThreads / 32;
+  const int list = blockIdx.x;
+  const int kvh = list % p.Hkv, bs = list / p.Hkv;
+  const int b = bs / p.groups, s = bs - b * p.groups;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int prefix = p.prefix_lens[b];
+  int32_t* out = p.sel_table + static_cast<size_t>(list) * p.sel_cols;
+  const bool bad = prefix < 0 || static_cast<long long>(prefix) + p.L >
+                                     static_cast<long long>(p.max_pages) * kTok;
+  const int n = bad ? 0 : prefix / kTok;
+  const int k = n < p.n_select ? n : p.n_select;
+  const int tail = bad ? 0 : (prefix % kTok + p.L + kTok - 1) / kTok;
+  if (kvh == 0 && tid == 0) {
+    p.sel_lens[bs] = bad ? -1 : k * kTok + prefix % kTok + p.L - p.group;
+    if (bad && s == 0) atomicOr(p.err, BDLM_DEVERR_LENGTH);
+  }
+  const int32_t* pt = p.page_table + static_cast<size_t>(b) * p.max_pages;
+  // the unfinished page and the block's pages follow the selected ones; unused columns hold -1
+  for (int c = k + tid; c < p.sel_cols; c += kSelThreads) out[c] = c < k + tail ? pt[n + c - k] : -1;
+  if (n <= p.n_select) {
+    for (int c = tid; c < k; c += kSelThreads) out[c] = pt[c];
+    return;
+  }
+  if (k == 0) return;
+
+  // keys, in shared memory when they fit; the page bitmap follows them
+  uint32_t* keys = sm;
+  const bool held = n <= kSelKeys;
+  uint32_t* taken = sm + (held ? n : 0);
+  const int words = (n + 31) / 32;
+  const float* row = p.scores + static_cast<size_t>(list) * p.max_pages;
+  uint32_t lo = 0xFFFFFFFFu, hi = 0;
+  for (int i = tid; i < n; i += kSelThreads) {
+    const uint32_t key = order_key(__ldcg(row + i));
+    if (held) keys[i] = key;
+    lo = min(lo, key);
+    hi = max(hi, key);
+  }
+  for (int i = tid; i < words; i += kSelThreads) taken[i] = 0;
+  if (tid == 0) s_cand = 0;
+  block_range(lo, hi, reinterpret_cast<uint32_t*>(s_wide));
+  auto key_at = [&](int i) { return held ? keys[i] : order_key(__ldcg(row + i)); };
+  int above;
+  const uint32_t T = kth_largest<uint32_t>(
+      k, lo, hi,
+      [&](auto&& f) {
+        for (int i = tid; i < n; i += kSelThreads) f(key_at(i));
+      },
+      hist, s_scan, reinterpret_cast<uint32_t*>(s_pick), &above);
+
+  // the error bound: the group's largest |q|_1 times the list's largest |bound|
+  float q1 = 0.f, am = 0.f;
+  for (int r = warp; r < p.group * p.G; r += kWarps) {
+    const uint2 q = __ldg(reinterpret_cast<const uint2*>(p.q) +
+                          ((static_cast<size_t>(b) * p.L + s * p.group + r / p.G) * p.Hq +
+                           kvh * p.G + r % p.G) * 32 + lane);
+    float v = fabsf(bf16_lo(q.x)) + fabsf(bf16_hi(q.x)) + fabsf(bf16_lo(q.y)) + fabsf(bf16_hi(q.y));
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    q1 = fmaxf(q1, v);
+  }
+  {
+    const int tiles = (n + 127) / 128;
+    const int runs = (tiles + p.tiles_per_item - 1) / p.tiles_per_item;
+    const float* a = p.amax + (static_cast<size_t>(b) * p.Hkv + kvh) * p.items_per_list * 8;
+    for (int i = tid; i < runs * 8; i += kSelThreads) am = fmaxf(am, __ldcg(a + i));
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, off));
+  }
+  if (lane == 0) {
+    s_f[warp] = q1;
+    s_f[16 + warp] = am;
+  }
+  __syncthreads();
+  for (int w = 0; w < kWarps; ++w) {
+    q1 = fmaxf(q1, s_f[w]);
+    am = fmaxf(am, s_f[16 + w]);
+  }
+  const float band = q1 * am * 0x1p-13f;   // 2E
+  const uint32_t tf = T & 0x80000000u ? T & 0x7FFFFFFFu : ~T;
+  const float t = __uint_as_float(tf);
+  // (scores or bounds that are not finite have no error bound: their float32 order stands)
+  const bool refine = T != 0 && band <= 3e38f && fabsf(t) <= 3e38f;
+  const uint32_t k_hi = refine ? order_key(__fadd_ru(t, band)) : T;
+  const uint32_t k_lo = refine ? order_key(__fadd_rd(t, -band)) : T;
+
+  // pages above the band are in; pages in it are candidates for the rest
+  int sure = 0;
+  for (int i = tid; i < words * 32; i += kSelThreads) {
+    const uint32_t key = i < n ? key_at(i) : 0;
+    const bool in = i < n && key > k_hi;
+    const uint32_t bits = __ballot_sync(0xffffffffu, in);
+    if (lane == 0) taken[i >> 5] = bits;
+    sure += in;
+    if (i < n && !in && key >= k_lo) {
+      const int c = atomicAdd(&s_cand, 1);
+      if (c < kSelExact) s_page[c] = i;
+    }
+  }
+  BlockSum sum{s_scan};
+  int n_sure;
+  sum.exclusive(sure, &n_sure);
+  __syncthreads();
+  const int m = s_cand, need = k - n_sure;   // 1 <= need <= m
+  if (m == need) {
+    for (int i = tid; i < n; i += kSelThreads) {
+      const uint32_t key = key_at(i);
+      if (key >= k_lo && key <= k_hi) atomicOr(&taken[i >> 5], 1u << (i & 31));
+    }
+  } else if (!refine) {
+    // equal keys (or not finite): the lowest positions
+    int base = 0;
+    for (int i0 = 0; i0 < n; i0 += kSelThreads) {
+      const int i = i0 + tid;
+      const bool c = i < n && key_at(i) == T;
+      int total;
+      const int before = base + sum.exclusive(c, &total);
+      if (c && before < need) atomicOr(&taken[i >> 5], 1u << (i & 31));
+      base += total;
+    }
+  } else if (m <= kSelExact) {
+    for (int c = warp; c < m; c += kWarps) {
+      const int id = pt[s_page[c]];
+      const unsigned long long e =
+          id >= 0 && id < p.num_pages ? exact_score(p, b, s, kvh, id) : 0ull;
+      if (lane == 0) s_exact[c] = e;
+    }
+    __syncthreads();
+    for (int c = tid; c < m; c += kSelThreads) {
+      const unsigned long long e = s_exact[c];
+      const int page = s_page[c];
+      int rank = 0;   // candidates ahead of this one
+      for (int j = 0; j < m; ++j)
+        rank += s_exact[j] > e || (s_exact[j] == e && s_page[j] < page);
+      if (rank < need) atomicOr(&taken[page >> 5], 1u << (page & 31));
+    }
+  } else {
+    // more near ties than fit (pages that are copies of each other): the same by counting, the
+    // scores computed again in every round
+    auto each_exact = [&](auto&& f) {
+      for (int i = warp; i < n; i += kWarps) {
+        const uint32_t key = key_at(i);
+        if (key < k_lo || key > k_hi) continue;
+        const int id = pt[i];
+        const unsigned long long e =
+            id >= 0 && id < p.num_pages ? exact_score(p, b, s, kvh, id) : 0ull;
+        if (lane == 0) f(i, e);
+      }
+    };
+    unsigned long long elo = ~0ull, ehi = 0;
+    each_exact([&](int, unsigned long long e) {
+      elo = e < elo ? e : elo;
+      ehi = e > ehi ? e : ehi;
+    });
+    block_range(elo, ehi, s_wide);
+    int larger;
+    const unsigned long long TE = kth_largest<unsigned long long>(
+        need, elo, ehi,
+        [&](auto&& f) { each_exact([&](int, unsigned long long e) { f(e); }); }, hist, s_scan,
+        s_pick, &larger);
+    // larger ones are in; of those equal to TE the lowest positions: marked in a second bitmap
+    uint32_t* equal = taken + words;
+    for (int i = tid; i < words; i += kSelThreads) equal[i] = 0;
+    __syncthreads();
+    each_exact([&](int i, unsigned long long e) {
+      if (e > TE) atomicOr(&taken[i >> 5], 1u << (i & 31));
+      if (e == TE) atomicOr(&equal[i >> 5], 1u << (i & 31));
+    });
+    __syncthreads();
+    int base = 0;
+    for (int w0 = 0; w0 < words; w0 += kSelThreads) {
+      const int w = w0 + tid;
+      const uint32_t bits = w < words ? equal[w] : 0;
+      int total;
+      int before = base + sum.exclusive(__popc(bits), &total);
+      uint32_t keep = 0;
+      for (uint32_t x = bits; x && before < need - larger; x &= x - 1, ++before) keep |= x & (0u - x);
+      if (keep) taken[w] |= keep;
+      base += total;
+    }
+  }
+  __syncthreads();
+
+  // the taken pages in position order
+  int base = 0;
+  for (int w0 = 0; w0 < words; w0 += kSelThreads) {
+    const int w = w0 + tid;
+    uint32_t bits = w < words ? taken[w] : 0;
+    int total;
+    int at = base + sum.exclusive(__popc(bits), &total);
+    for (; bits; bits &= bits - 1) out[at++] = pt[w * 32 + __ffs(static_cast<int>(bits)) - 1];
+    base += total;
+  }
+}
+
+// ------------------------------------------------------------------ eviction
+constexpr int kEvictThreads = 1024;
+constexpr int kEvictKeys = 22528;   // 88 KB of keys: two CTAs per SM; longer rows are re-read (L2)
+
+// One CTA per (sequence, KV head): the k = keep - recent largest weights before the last `recent`
+// tokens, then one pass in position order that writes the kept positions and moves their weights
+// to the front.  In place is safe: a round's weights are read before the barrier of its scan and
+// written after it, to positions no later than their own, so no later round reads over them.
+// Bound by latency of the counting rounds over shared memory; weights are read once or twice.
+__global__ void __launch_bounds__(kEvictThreads)
+evict_select_kernel(const EvictParams p) {
+  extern __shared__ uint32_t sm[];
+  __shared__ int hist[kBuckets];
+  __shared__ int s_scan[34];
+  __shared__ uint32_t s_range[64];
+  __shared__ uint32_t s_pick[1];
+  __shared__ int s_cnt[2][32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int b = blockIdx.x / p.Hkv, kvh = blockIdx.x - b * p.Hkv;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int n = p.lens[b];
+  const size_t stride = static_cast<size_t>(p.max_pages) * kTok;
+  int32_t* kept = p.kept + static_cast<size_t>(blockIdx.x) * p.keep;
+  const bool bad = n < 0 || n > static_cast<long long>(stride);
+  if (kvh == 0 && tid == 0) {
+    p.new_lens[b] = bad ? 0 : min(n, p.keep);
+    if (bad) atomicOr(p.err, BDLM_DEVERR_LENGTH);
+  }
+  for (int i = (bad ? 0 : min(n, p.keep)) + tid; i < p.keep; i += kEvictThreads) kept[i] = -1;
+  if (bad) return;
+  const float* w = p.weights + blockIdx.x * stride;
+  float* to = p.to_weights + blockIdx.x * stride;
+  if (n <= p.keep) {
+    for (int i = tid; i < n; i += kEvictThreads) {
+      kept[i] = i;
+      if (to != w) to[i] = w[i];
+    }
+    return;
+  }
+  const int cand = n - p.recent, k = p.keep - p.recent;   // k < cand
+  const bool held = cand <= kEvictKeys;
+  uint32_t T = 0xFFFFFFFFu;
+  int above = 0;
+  auto key_at = [&](int i) { return held ? sm[i] : order_key(__ldcg(w + i)); };
+  if (k > 0) {
+    uint32_t lo = 0xFFFFFFFFu, hi = 0;
+    for (int i = tid; i < cand; i += kEvictThreads) {
+      const uint32_t key = order_key(__ldcg(w + i));
+      if (held) sm[i] = key;
+      lo = min(lo, key);
+      hi = max(hi, key);
+    }
+    block_range(lo, hi, s_range);
+    T = kth_largest<uint32_t>(
+        k, lo, hi,
+        [&](auto&& f) {
+          for (int i = tid; i < cand; i += kEvictThreads) f(key_at(i));
+        },
+        hist, s_scan, s_pick, &above);
+  }
+  const int ties = k - above;   // tokens of weight T that stay
+  int n_gt = 0, n_eq = 0;       // larger and equal ones before this round
+  for (int i0 = 0; i0 < n; i0 += kEvictThreads) {
+    const int i = i0 + tid;
+    const bool late = i >= cand && i < n;
+    const uint32_t key = k > 0 && i < cand ? key_at(i) : 0;
+    const bool gt = late || (k > 0 && i < cand && key > T);
+    const bool eq = k > 0 && i < cand && key == T;
+    const float v = i < n ? __ldcg(w + i) : 0.f;
+    const uint32_t bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
+    if (lane == 0) {
+      s_cnt[0][warp] = __popc(bg);
+      s_cnt[1][warp] = __popc(be);
+    }
+    __syncthreads();
+    int g = n_gt, e = n_eq;
+    for (int x = 0; x < kEvictThreads / 32; ++x) {
+      const int cg = s_cnt[0][x], ce = s_cnt[1][x];
+      if (x < warp) {
+        g += cg;
+        e += ce;
+      }
+      n_gt += cg;
+      n_eq += ce;
+    }
+    const uint32_t below = (1u << lane) - 1u;
+    g += __popc(bg & below);
+    e += __popc(be & below);
+    if (gt || (eq && e < ties)) {
+      const int at = g + min(e, ties);
+      kept[at] = i;
+      to[at] = v;
+    }
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------------ moving tokens
+// Token base + idx[j] of a sequence (and KV head) becomes token base + j.  Rows of K and V are 256
+// bytes per head.  HBM bound: each kept row is read and written once.
+//
+// To other pages the moves are independent: a warp takes 32 tokens of one (sequence, KV head),
+// lanes 0-15 the K row and 16-31 the V row, eight tokens in flight.
+//
+// In place (idx increasing, so every token moves to its own slot or an earlier one) a slot may only
+// be written once the tokens before have been read.  A warp therefore owns a 64-byte column slice
+// of K or V of one (sequence, KV head), which no other warp touches, and walks the tokens in
+// order, 64 at a time: all loads, then all stores.  Tokens that stay are skipped.
+constexpr int kMoveWarps = 8;
+
+__device__ __forceinline__ long long token_row(const CompactParams& p, const int32_t* table, int b,
+                                               long long tok, int kvh) {
+  if (tok < 0 || tok >= static_cast<long long>(p.max_pages) * kTok) {
+    atomicOr(p.err, BDLM_DEVERR_LENGTH);
+    return -1;
+  }
+  const int id = __ldg(table + static_cast<size_t>(b) * p.max_pages + tok / kTok);
+  if (id < 0 || id >= p.num_pages) {
+    atomicOr(p.err, BDLM_DEVERR_PAGE);
+    return -1;
+  }
+  return (static_cast<long long>(id) * kTok + tok % kTok) * p.Hkv + kvh;
+}
+
+__global__ void __launch_bounds__(kMoveWarps * 32)
+move_tokens_kernel(const CompactParams p, int runs) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const long long unit = static_cast<long long>(blockIdx.x) * kMoveWarps + (threadIdx.x >> 5);
+  if (unit >= static_cast<long long>(p.B) * p.Hkv * runs) return;
+  const int run = static_cast<int>(unit % runs);
+  const int bh = static_cast<int>(unit / runs);
+  const int b = bh / p.Hkv, kvh = bh - b * p.Hkv;
+  const int count = min(p.counts[b], p.n_max);
+  const int j = run * 32 + lane;
+  if (run * 32 >= count) return;
+  const int base = p.base ? p.base[b] : 0;
+  long long from = -1, to = -1;   // this lane's token
+  if (j < count && base >= 0) {
+    const int i = __ldg(p.idx + (static_cast<size_t>(b) * p.heads + (p.heads > 1 ? kvh : 0)) * p.n_max + j);
+    if (i < 0) {
+      atomicOr(p.err, BDLM_DEVERR_ROW);
+    } else {
+      from = token_row(p, p.page_table, b, static_cast<long long>(base) + i, kvh);
+      to = token_row(p, p.to_table, b, static_cast<long long>(base) + j, kvh);
+      if (from < 0) to = -1;
+    }
+  } else if (base < 0 && lane == 0) {
+    atomicOr(p.err, BDLM_DEVERR_LENGTH);
+  }
+  uint4* pool = reinterpret_cast<uint4*>(lane < 16 ? p.k_pages : p.v_pages) + (lane & 15);
+  constexpr int kBatch = 8;
+  for (int t0 = 0; t0 < 32; t0 += kBatch) {
+    uint4 v[kBatch];
+    long long dst[kBatch];
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x) {
+      const long long f = __shfl_sync(0xffffffffu, from, t0 + x);
+      dst[x] = __shfl_sync(0xffffffffu, to, t0 + x);
+      if (dst[x] >= 0) v[x] = __ldcs(pool + f * 16);
+    }
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x)
+      if (dst[x] >= 0) pool[dst[x] * 16] = v[x];
+  }
+}
+
+__global__ void __launch_bounds__(kMoveWarps * 32)
+move_in_place_kernel(const CompactParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const long long unit = static_cast<long long>(blockIdx.x) * kMoveWarps + (threadIdx.x >> 5);
+  if (unit >= static_cast<long long>(p.B) * p.Hkv * 8) return;
+  const int slice = static_cast<int>(unit & 3), is_v = static_cast<int>(unit >> 2) & 1;
+  const int bh = static_cast<int>(unit >> 3);
+  const int b = bh / p.Hkv, kvh = bh - b * p.Hkv;
+  const int count = min(p.counts[b], p.n_max);
+  const int base = p.base ? p.base[b] : 0;
+  if (base < 0) {
+    if (lane == 0) atomicOr(p.err, BDLM_DEVERR_LENGTH);
+    return;
+  }
+  const int32_t* idx = p.idx + (static_cast<size_t>(b) * p.heads + (p.heads > 1 ? kvh : 0)) * p.n_max;
+  uint4* pool = reinterpret_cast<uint4*>(is_v ? p.v_pages : p.k_pages) + slice * 4 + (lane & 3);
+  for (int j0 = 0; j0 < count; j0 += 64) {
+    long long from[2], to[2];   // tokens j0 + lane and j0 + 32 + lane
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int j = j0 + h * 32 + lane;
+      from[h] = to[h] = -1;
+      if (j >= count) continue;
+      const int i = __ldg(idx + j);
+      if (i == j) continue;   // stays where it is
+      if (i < 0) {
+        atomicOr(p.err, BDLM_DEVERR_ROW);
+        continue;
+      }
+      from[h] = token_row(p, p.page_table, b, static_cast<long long>(base) + i, kvh);
+      to[h] = token_row(p, p.to_table, b, static_cast<long long>(base) + j, kvh);
+      if (from[h] < 0) to[h] = -1;
+    }
+    if (!__any_sync(0xffffffffu, to[0] >= 0 || to[1] >= 0)) continue;
+    uint4 v[8];
+    long long dst[8];
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {   // four lanes a token, eight tokens an instruction
+      const int t = (x & 3) * 8 + (lane >> 2);
+      const long long f = __shfl_sync(0xffffffffu, from[x >> 2], t);
+      dst[x] = __shfl_sync(0xffffffffu, to[x >> 2], t);
+      if (dst[x] >= 0) v[x] = __ldcg(pool + f * 16);
+    }
+    __syncwarp();   // every row of the batch is read before a slot is written
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+      if (dst[x] >= 0) pool[dst[x] * 16] = v[x];
+    __syncwarp();
+  }
+}
+
+template <typename F>
+cudaError_t allow_smem(std::atomic<unsigned long long>& done, F* kernel, size_t bytes) {
+  return once_per_device(done, [&] {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(bytes));
+  });
+}
+
+}  // namespace
+
+cudaError_t launch_select_pages(const SelectParams& p, cudaStream_t stream) {
+  // keys (where a row fits), then two bitmaps of the row's pages
+  const size_t keys = p.max_pages <= kSelKeys ? p.max_pages : kSelKeys;
+  const size_t words = (static_cast<size_t>(p.max_pages) + 31) / 32;
+  constexpr size_t kMost = (kSelKeys + 2 * (kSelectMaxPages / 32)) * 4;
+  static std::atomic<unsigned long long> attr_done{0};
+  cudaError_t e = allow_smem(attr_done, select_pages_kernel, kMost);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(select_pages_kernel, dim3(static_cast<unsigned>(p.B) * p.groups * p.Hkv),
+                    dim3(kSelThreads), (keys + 2 * words) * 4, stream, p);
+}
+
+cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t stream) {
+  const long long tokens = static_cast<long long>(p.max_pages) * kTok;
+  const size_t keys = tokens <= kEvictKeys ? tokens : kEvictKeys;
+  static std::atomic<unsigned long long> attr_done{0};
+  cudaError_t e = allow_smem(attr_done, evict_select_kernel, kEvictKeys * 4);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(evict_select_kernel, dim3(static_cast<unsigned>(p.B) * p.Hkv),
+                    dim3(kEvictThreads), keys * 4, stream, p);
+}
+
+cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream) {
+  if (p.to_table == p.page_table) {
+    const long long units = static_cast<long long>(p.B) * p.Hkv * 8;
+    return launch_pdl(move_in_place_kernel,
+                      dim3(static_cast<unsigned>((units + kMoveWarps - 1) / kMoveWarps)),
+                      dim3(kMoveWarps * 32), 0, stream, p);
+  }
+  const int runs = (p.n_max + 31) / 32;
+  const long long units = static_cast<long long>(p.B) * p.Hkv * runs;
+  return launch_pdl(move_tokens_kernel,
+                    dim3(static_cast<unsigned>((units + kMoveWarps - 1) / kMoveWarps)),
+                    dim3(kMoveWarps * 32), 0, stream, p, runs);
+}
+
+}  // namespace bdlm

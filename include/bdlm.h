@@ -23,7 +23,10 @@
  *    lives in a per-device workspace that the library allocates on first need and grows
  *    when a larger problem arrives (growing synchronises the device).  Calls that share
  *    a device must not run concurrently on different streams: they share that
- *    workspace.  bdlm_release() frees it.
+ *    workspace.  It cannot grow while `stream` is being captured (BDLM_ERR_NOMEM: run the call
+ *    once before capturing it); a captured graph keeps the memory it was captured with, and
+ *    graphs must not run concurrently either.  bdlm_release() frees the workspace, after which
+ *    graphs captured before it must not run.
  *  - Return value: BDLM_OK (0) or a negative BDLM_ERR_* code; bdlm_status_string() names it.
  */
 #ifndef BDLM_H
@@ -330,6 +333,132 @@ int bdlm_lm_head_commit(const bdlm_bf16* hidden, const bdlm_bf16* w, const uint8
  * masked to unmasked).  mask, commit: [n] uint8.  n == 0 is a no-op.
  */
 int bdlm_apply_commit(uint8_t* mask, const uint8_t* commit, int n, bdlm_stream stream);
+
+/*
+ * Attention of a tree of drafted tokens over the paged KV cache.
+ * The pages have no counterpart (their blocks are bidirectional); for verifying several drafted
+ * continuations of a prefix in one forward, and for block attention with its normalisers.
+ *
+ * As bdlm_block_attention, but query i of sequence b sees the whole prefix and those block tokens
+ * t whose bit t of tree_mask[b*L + i] is set (bits at and past L are ignored; tree_mask NULL: all
+ * L tokens, which is bdlm_block_attention).  Any pattern is allowed; a query that sees nothing (no
+ * prefix and an empty word) gets out = 0.  K of a block token may hold anything for the queries
+ * that do not see it; V of a token that no query of its sequence sees may hold anything, V of one
+ * that some query sees must be finite.
+ *   tree_mask  [B, L]      uint64 (8-byte aligned), or NULL
+ *   lse        [B, L, Hq]  float, or NULL: ln of the sum of exp(sm_scale * q . K[j]) over the keys
+ *                          the query sees; -inf for a query that sees nothing
+ * Other arguments, layouts and limits as bdlm_block_attention.
+ */
+int bdlm_tree_attention(const bdlm_attn_desc* desc, const bdlm_bf16* q, const bdlm_bf16* k_pages,
+                        const bdlm_bf16* v_pages, const int32_t* page_table,
+                        const int32_t* prefix_lens, const uint64_t* tree_mask, bdlm_bf16* out,
+                        float* lse, bdlm_stream stream);
+
+/*
+ * Moves tokens of the paged KV cache to the front: for j < counts[b] (at most n_max), the K and V
+ * of token base_lens[b] + idx[b, h, j] become those of token base_lens[b] + j.  Used to keep the
+ * accepted path of a drafted tree (base = prefix_lens, idx = the path's block positions) and by
+ * bdlm_evict_kv.
+ *   base_lens  [B] int32, or NULL for 0
+ *   idx        [B, heads, n_max] int32; heads = 1 (one list for all KV heads) or Hkv; strictly
+ *              increasing and >= 0 within a list
+ *   counts     [B] int32
+ *   to_table   [B, max_pages_per_seq] int32: the pages written.  Either page_table itself (the
+ *              same pointer): in place; or pages that no page_table row of the call lists.
+ * Slots that no token moves to are left as they were.  An index below 0, a token past the page
+ * table or a bad page id skips that token and sets a device error bit (ROW, LENGTH, PAGE).  desc as
+ * bdlm_write_block_kv (L unused).  k_pages, v_pages 16-byte aligned.  n_max == 0 is a no-op.
+ */
+int bdlm_compact_kv(const bdlm_attn_desc* desc, bdlm_bf16* k_pages, bdlm_bf16* v_pages,
+                    const int32_t* page_table, const int32_t* base_lens, const int32_t* idx,
+                    int heads, int n_max, const int32_t* counts, const int32_t* to_table,
+                    bdlm_stream stream);
+
+/*
+ * Bounds of the keys of each page, from which bdlm_select_pages scores it:
+ *     bounds[page, h, 0, d] = min over the page's 16 tokens of K[token, h, d],  [.., 1, d] = max
+ * (exact) for every full page that holds a token from_lens[b] <= t < to_lens[b] of sequence b, full
+ * meaning that all its 16 tokens are before to_lens[b].  Other pages' bounds are left as they
+ * were.  Called when tokens are final (after a prompt, after a block's last write).
+ *   from_lens [B] int32, or NULL for 0;  to_lens [B] int32, from <= to
+ *   bounds    [num_pages, Hkv, 2, D] bf16 (16-byte aligned), by page like the pools
+ * K of full pages is finite.  desc as bdlm_write_block_kv (L unused).
+ */
+int bdlm_page_bounds(const bdlm_attn_desc* desc, const bdlm_bf16* k_pages,
+                     const int32_t* page_table, const int32_t* from_lens, const int32_t* to_lens,
+                     bdlm_bf16* bounds, bdlm_stream stream);
+
+/*
+ * The pages that each group of queries attends to.  A group is `group` consecutive block
+ * positions (L % group == 0; group = L: one list for the block, group = 1: one per query) and, per
+ * KV head, the query heads that share it.  The score of a full page of the prefix
+ *     max over the group's query rows q of  sum_d (q_d > 0 ? q_d * max_d : q_d * min_d)
+ * bounds q . K from above over the page's keys.  Per (sequence, group, KV head) the
+ * n = min(n_select, full prefix pages) pages of highest score (the lower position first among
+ * equals) are listed in position order, followed by the pages that hold the prefix's last
+ * prefix_len % 16 tokens and the block; columns past them hold -1.  The choice is that of exact
+ * scores: where float32 cannot tell two scores apart they are computed again more precisely.
+ *   bounds     as bdlm_page_bounds; finite for the full pages of the prefixes
+ *   sel_table  [B, L/group, Hkv, sel_cols] int32 page ids; sel_cols >= n_select + (L + 30) / 16
+ *   sel_lens   [B, L/group] int32: tokens listed before the last `group` ones, the prefix length
+ *              bdlm_sparse_attention takes (n*16 + prefix_len%16 + L - group; -1 for a bad length)
+ * group * Hq / Hkv <= 256 and max_pages_per_seq <= 262144, else BDLM_ERR_UNSUPPORTED.  A page with
+ * a bad id is only listed when the others do not suffice.  Scratch (a float per list and page of
+ * the table) comes from the library workspace.  Other arguments as bdlm_block_attention.
+ */
+int bdlm_select_pages(const bdlm_attn_desc* desc, const bdlm_bf16* q, const bdlm_bf16* bounds,
+                      const int32_t* page_table, const int32_t* prefix_lens, int group,
+                      int n_select, int sel_cols, int32_t* sel_table, int32_t* sel_lens,
+                      bdlm_stream stream);
+
+/*
+ * Block attention over listed pages: each (sequence, group, KV head) reads the pages of its row of
+ * sel_table (from bdlm_select_pages, possibly of an earlier step) as its keys, in order; the last
+ * of them are the block's own, so every query sees its whole block and the listed part of the
+ * prefix.  sel_lens[b, s] + group tokens are read.  q, out [B, L, Hq, D] and limits as
+ * bdlm_block_attention; desc->max_pages_per_seq is not used.
+ */
+int bdlm_sparse_attention(const bdlm_attn_desc* desc, const bdlm_bf16* q, const bdlm_bf16* k_pages,
+                          const bdlm_bf16* v_pages, int group, int sel_cols,
+                          const int32_t* sel_table, const int32_t* sel_lens, bdlm_bf16* out,
+                          bdlm_stream stream);
+
+/*
+ * Attention weight gathered by each cached token: for token j < prefix_lens[b] and KV head g,
+ *     weights[b, g, j] = decay * weights[b, g, j]
+ *                        + sum over i, h with h / (Hq/Hkv) = g of exp(sm_scale * q[b,i,h] . K_b[j,g] - lse[b,i,h])
+ * with lse from bdlm_tree_attention on the same queries, so the sum adds up attention
+ * probabilities.  Later positions (the block's, and behind) are left as they were.
+ *   lse      [B, L, Hq] float
+ *   weights  [B, Hkv, max_pages_per_seq * 16] float, updated in place
+ * decay is finite (1: plain accumulation, 0: this step alone; weights must be finite in any case).
+ * Tokens of a page with a bad id are left as they were.  Other arguments as bdlm_block_attention.
+ */
+int bdlm_attention_weights(const bdlm_attn_desc* desc, const bdlm_bf16* q,
+                           const bdlm_bf16* k_pages, const int32_t* page_table,
+                           const int32_t* prefix_lens, const float* lse, float decay,
+                           float* weights, bdlm_stream stream);
+
+/*
+ * Evicts cached tokens by accumulated attention weight.  A sequence of more than `keep` tokens keeps,
+ * for each KV head on its own, its last `recent` tokens and, of the others, the keep - recent of
+ * largest weight (the lower position first among equals; -0 equals 0, a NaN comes last); kept
+ * tokens stay in order.  Their K, V and weights move to positions 0 .. keep - 1.  A sequence of at
+ * most `keep` tokens keeps all.
+ *   lens        [B] int32 tokens in the cache;  new_lens [B] int32 = min(lens, keep), another array
+ *   weights     [B, Hkv, max_pages_per_seq * 16] float;  to_weights the same shape (may be weights)
+ *   kept        [B, Hkv, keep] int32: the kept positions, increasing; -1 past new_lens
+ *   to_table    as bdlm_compact_kv: page_table itself (in place), or other pages
+ * 1 <= keep <= max_pages_per_seq * 16, 0 <= recent <= keep.  Slots and weights at and past
+ * new_lens are left as they were.  A length outside the page table sets a device error bit and
+ * gives new_lens 0.  Pages now hold other tokens: their bounds are to be made again.  desc as
+ * bdlm_write_block_kv (L unused).
+ */
+int bdlm_evict_kv(const bdlm_attn_desc* desc, bdlm_bf16* k_pages, bdlm_bf16* v_pages,
+                  const int32_t* page_table, const int32_t* lens, const float* weights, int keep,
+                  int recent, const int32_t* to_table, float* to_weights, int32_t* kept,
+                  int32_t* new_lens, bdlm_stream stream);
 
 /*
  * A whole block's denoising on the device: rounds repeat inside one CUDA graph, with a
