@@ -725,34 +725,32 @@ int bdlm_select_pages(const bdlm_attn_desc* desc, const bdlm_bf16* q, const bdlm
   // a launch scores whole groups of up to 256 query rows per KV head
   int per = bdlm::key_rows_max() / (group * G) * group;
   if (per > d.L) per = d.L;
-  const bdlm::KeyPlan plan =
-      bdlm::plan_keys(d.B, d.Hkv, d.max_pages_per_seq, per * G, st->num_sms);
-  if (plan.total_items > 0x7FFFFFFFll) return BDLM_ERR_INVALID;
+  const int max_tiles = (d.max_pages_per_seq + bdlm::kKeyTile - 1) / bdlm::kKeyTile;
   const size_t score_bytes =
       align256(static_cast<size_t>(lists) * d.max_pages_per_seq * sizeof(float));
-  rc = ensure(&st->data, &st->data_cap, score_bytes + plan.amax_floats * sizeof(float), false,
-              stream);
+  const size_t amax_bytes =
+      static_cast<size_t>(d.B) * d.Hkv * max_tiles * bdlm::kAmaxPerTile * sizeof(float);
+  // workspace: near ties' exact scores | scores | magnitudes
+  rc = ensure(&st->data, &st->data_cap, 3 * score_bytes + amax_bytes, false, stream);
   if (rc) return rc;
   bdlm::KeyParams p = key_params(d, page_table, prefix_lens, st->err);
-  p.tiles_per_item = plan.tiles_per_item;
-  p.items_per_list = plan.items_per_list;
-  p.total_items = static_cast<int>(plan.total_items);
+  p.max_tiles = max_tiles;
   p.q = q;
   p.bounds = bounds;
-  p.scores = static_cast<float*>(st->data);
-  p.amax = reinterpret_cast<float*>(static_cast<uint8_t*>(st->data) + score_bytes);
+  p.scores = reinterpret_cast<float*>(static_cast<uint8_t*>(st->data) + 2 * score_bytes);
+  p.amax = reinterpret_cast<float*>(static_cast<uint8_t*>(st->data) + 3 * score_bytes);
   p.group = group;
   p.groups = groups;
   p.width = group * G;
-  const CUtensorMap none = {};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   for (p.l0 = 0; p.l0 < d.L; p.l0 += per) {
     p.rows = (d.L - p.l0 < per ? d.L - p.l0 : per) * G;
-    if (bdlm::launch_keys(true, none, none, p, st->num_sms, s) != cudaSuccess) return BDLM_ERR_CUDA;
+    if (bdlm::launch_page_scores(p, st->num_sms, s) != cudaSuccess) return BDLM_ERR_CUDA;
   }
   const bdlm::SelectParams sp{q, bounds, page_table, prefix_lens, p.scores, p.amax,
+                              static_cast<unsigned long long*>(st->data),
                               d.B, d.L, d.Hq, d.Hkv, G, d.max_pages_per_seq, d.num_pages, group,
-                              groups, p.tiles_per_item, p.items_per_list, n_select, sel_cols,
+                              groups, max_tiles, n_select, sel_cols,
                               sel_table, sel_lens, st->err};
   return bdlm::launch_select_pages(sp, s) == cudaSuccess ? BDLM_OK : BDLM_ERR_CUDA;
 }
@@ -801,9 +799,6 @@ int bdlm_attention_weights(const bdlm_attn_desc* desc, const bdlm_bf16* q,
   const int G = d.Hq / d.Hkv;
   int per = bdlm::key_rows_max() / G;   // block positions of one launch
   if (per > d.L) per = d.L;
-  const bdlm::KeyPlan plan = bdlm::plan_keys(d.B, d.Hkv, d.max_pages_per_seq * d.page_size,
-                                             per * G, st->num_sms);
-  if (plan.total_items > 0x7FFFFFFFll) return BDLM_ERR_INVALID;
   CUtensorMap tm_q, tm_k;
   {
     cuuint64_t dims[4] = {128, static_cast<cuuint64_t>(d.Hkv), 16,
@@ -814,9 +809,8 @@ int bdlm_attention_weights(const bdlm_attn_desc* desc, const bdlm_bf16* q,
     if ((rc = encode(&tm_k, k_pages, 4, dims, strides, box))) return rc;
   }
   bdlm::KeyParams p = key_params(d, page_table, prefix_lens, st->err);
-  p.tiles_per_item = plan.tiles_per_item;
-  p.items_per_list = plan.items_per_list;
-  p.total_items = static_cast<int>(plan.total_items);
+  p.max_tiles = static_cast<int>((static_cast<long long>(d.max_pages_per_seq) * d.page_size +
+                                  bdlm::kKeyTile - 1) / bdlm::kKeyTile);
   p.lse = lse;
   p.weights = weights;
   p.decay = decay;
@@ -829,8 +823,8 @@ int bdlm_attention_weights(const bdlm_attn_desc* desc, const bdlm_bf16* q,
     cuuint64_t strides[2] = {256, static_cast<cuuint64_t>(d.Hq) * 256};
     cuuint32_t box[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(nl)};
     if ((rc = encode(&tm_q, q, 3, dims, strides, box))) return rc;
-    if (bdlm::launch_keys(false, tm_q, tm_k, p, st->num_sms,
-                          static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    if (bdlm::launch_attention_weights(tm_q, tm_k, p, st->num_sms,
+                                       static_cast<cudaStream_t>(stream)) != cudaSuccess)
       return BDLM_ERR_CUDA;
     p.decay = 1.f;
   }

@@ -191,6 +191,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     uint32_t ph = 0;
     bool ok = true;
     int seq = -1;  // sequence number of the most recently published item
+    const bool counted = p.total_items > static_cast<int>(gridDim.x);
     // Publishes `it` to the item ring (lane 0).
     auto publish = [&](const Item& it, unsigned long long seen = 0) {
       const int rs = seq % kItemRing;
@@ -202,11 +203,20 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     // Takes the next non-empty item from the global counter, publishes it to the item ring
     // and loads its page ids (whole warp).  When the work is done it publishes the end marker
     // at once (the MMA warp needs it before it can finish the current item) and returns false.
+    bool first = true;
     auto grab = [&](Item& it) -> bool {
       while (true) {
-        int idx = 0;
-        if (lane == 0) idx = atomicAdd(p.work, 1);
-        idx = __shfl_sync(0xffffffffu, idx, 0);
+        // the first item is the CTA's own number; later ones come from the counter, unless no
+        // item is left past the first ones (a small problem pays for no atomics)
+        int idx = blockIdx.x;
+        if (!first) {
+          idx = p.total_items;
+          if (counted) {
+            if (lane == 0) idx = static_cast<int>(gridDim.x) + atomicAdd(p.work, 1);
+            idx = __shfl_sync(0xffffffffu, idx, 0);
+          }
+        }
+        first = false;
         if (idx >= p.total_items) {
           ++seq;
           if (lane == 0) {
@@ -427,10 +437,12 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     if (lane == 0) {
       griddep_launch_dependents();  // this CTA takes no more work
       // the last CTA to finish taking work resets the counter for the next launch
-      __threadfence();
-      if (atomicAdd(p.work + 1, 1) == static_cast<int>(gridDim.x) - 1) {
-        p.work[0] = 0;
-        p.work[1] = 0;
+      if (counted) {
+        __threadfence();
+        if (atomicAdd(p.work + 1, 1) == static_cast<int>(gridDim.x) - 1) {
+          p.work[0] = 0;
+          p.work[1] = 0;
+        }
       }
       if (!ok) {
         for (int s = 0; s < STAGES; ++s) mbar_wait_drain(&bar_full[s], ph ^ (s < st ? 0 : 1));
@@ -1634,7 +1646,9 @@ cudaError_t launch_t(const CUtensorMap& tq, const CUtensorMap& tk, const CUtenso
                                 cudaSharedmemCarveoutMaxShared);
   });
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_kernel<N, STAGES, CPS, MASKED, ROWS, TWO, EXT>, dim3(num_sms * CPS),
+  // no more CTAs than items: a small problem's kernel ends sooner
+  const int grid = prm.total_items < num_sms * CPS ? prm.total_items : num_sms * CPS;
+  return launch_pdl(attn_kernel<N, STAGES, CPS, MASKED, ROWS, TWO, EXT>, dim3(grid),
                     dim3(attn_threads(ROWS, TWO)), smem,
                     stream, tq, tk, tv, prm);
 }

@@ -24,18 +24,15 @@ cudaError_t launch_attention_ext(const CUtensorMap& tm_q, const CUtensorMap& tm_
                                  const BlockKvWrite* kv_write, const AttnExt* ext);
 
 // ------------------------------------------------------------------ key_scores.cu
-struct KeyPlan {
-  int tiles_per_item = 1, items_per_list = 1;
-  long long total_items = 0;
-  size_t amax_floats = 0;   // page scores: largest |bound| per (run, gathering warp)
-};
+constexpr int kKeyTile = 128;    // keys (tokens, or pages) per tile
+constexpr int kAmaxPerTile = 8;  // page scores: largest |bound| of a tile, one value per warp
 
 struct KeyParams {
   const int32_t* page_table;
   const int32_t* prefix_lens;
   int B, L, Hq, Hkv, G, max_pages, num_pages;
   int l0, rows;                // query rows l0 * G .. + rows of each (sequence, KV head)
-  int tiles_per_item, items_per_list, total_items;
+  int max_tiles;               // tiles of the longest list the page table allows
   int* err;
   // attention weights
   const float* lse;            // [B, L, Hq]
@@ -45,15 +42,14 @@ struct KeyParams {
   const uint16_t* q;
   const uint16_t* bounds;      // [num_pages, Hkv, 2, 128]
   float* scores;               // [B, groups, Hkv, max_pages]
-  float* amax;                 // [B, Hkv, items_per_list, 8]
+  float* amax;                 // [B, Hkv, max_tiles, kAmaxPerTile]
   int group, groups, width;    // positions per group, groups per sequence, query rows per group
 };
 
-KeyPlan plan_keys(int B, int Hkv, int max_keys, int rows, int num_sms);
 int key_rows_max();   // query rows of one launch
-// pages: page scores (tm_q, tm_k unused), else attention weights.
-cudaError_t launch_keys(bool pages, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
-                        const KeyParams& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_attention_weights(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                                     const KeyParams& p, int num_sms, cudaStream_t stream);
+cudaError_t launch_page_scores(const KeyParams& p, int num_sms, cudaStream_t stream);
 cudaError_t launch_page_bounds(const uint16_t* k_pages, const int32_t* page_table,
                                const int32_t* from, const int32_t* to, int B, int Hkv,
                                int max_pages, int num_pages, int num_sms, uint16_t* bounds,
@@ -67,8 +63,9 @@ struct SelectParams {
   const int32_t* prefix_lens;
   const float* scores;
   const float* amax;
+  unsigned long long* exact;   // [B, groups, Hkv, max_pages]: near ties' scores, where they are many
   int B, L, Hq, Hkv, G, max_pages, num_pages, group, groups;
-  int tiles_per_item, items_per_list;
+  int max_tiles;
   int n_select, sel_cols;
   int32_t* sel_table;
   int32_t* sel_lens;

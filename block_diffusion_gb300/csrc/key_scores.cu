@@ -14,15 +14,19 @@
 // bytes per key move besides, so HBM does up to about 200 query rows; beyond, the tensor core and
 // the exponentials (one per key and row; an SM does about 32 a clock) are close to it.
 //
-// One persistent CTA per SM walks items (a list = sequence and KV head, and a run of tiles of 128
-// keys) in a fixed stride that every warp derives for itself, so no warp hands out work:
-//   warp 0     one lane issues tcgen05.mma (and allocates tensor memory)
-//   warps 1-2  weights: TMA, Q of an item (a 64-dim x G x L box per half) and one 16-slot page box
-//              per page and half, alternate tiles each (one warp's 16 boxes take about 1 us)
-//   warps 4-11 reduction, two sets of four warps (one per lane quadrant) on alternate tiles
-//   warps 12-19  page scores: a page's bounds are 512 bytes, too small for a box each (128 boxes
-//              of one row per K atom), so eight warps gather them with cp.async, 16 lanes a row,
-//              into the 128-byte swizzle, and build q+ and q- in shared memory
+// (Page scores of up to 32 rows: a kernel of its own, below.)
+//
+// One persistent CTA per SM takes an equal, contiguous share of all tiles of 128 keys, laid end to
+// end list by list (a list = sequence and KV head): equal bytes per SM whatever the lengths, and Q
+// changes only where a list ends.  Every warp walks the share by itself, so no warp hands out work:
+//   warp 0       one lane issues tcgen05.mma (and allocates tensor memory)
+//   warps 1-2    weights: one 16-slot page box per page and half by TMA, alternate tiles each (one
+//                warp's 16 boxes take about 1 us)
+//   warp 3       finds the CTA's share; weights: Q of a list by TMA (a 64-dim x G x L box per half)
+//   warps 4-     reduction, two or four sets of four warps (one per lane quadrant) in turn
+//   page scores  a page's bounds are 512 bytes, too small for a box each (128 boxes of one row per
+//                K atom): warps 12-19 gather them with cp.async, 16 lanes a row, into the 128-byte
+//                swizzle, and warps 1-3 build q+ and q- of a list in shared memory
 // Stages are 32 KB (128 keys x 128 values); a page tile takes two (hi, then lo).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -35,11 +39,11 @@
 namespace bdlm {
 namespace {
 
-constexpr int kKeys = 128;           // keys per tile (UMMA M)
+constexpr int kKeys = kKeyTile;      // keys per tile (UMMA M)
 constexpr int kPageTokens = 16;
 constexpr int kStage = 32768;        // 128 keys x 128 bf16, two 64-wide K atoms
 constexpr int kAtom = 16384;
-constexpr int kLoaders = 8;          // page scores: gathering warps
+constexpr int kLoaders = kAmaxPerTile;         // page scores: gathering warps
 
 // WIDE: up to 256 query rows; else up to 32 (more stages, two Q buffers).
 template <bool PAGES, bool WIDE>
@@ -47,10 +51,17 @@ struct Cfg {
   static constexpr int kRowsMax = WIDE ? 256 : 32;
   static constexpr int kQBytes = kRowsMax * (PAGES ? 512 : 256);
   static constexpr int kQBufs = WIDE ? 1 : 2;
-  static constexpr int kStages = WIDE ? (PAGES ? 3 : 4) : (PAGES ? 5 : 6);
+  static_assert(WIDE || !PAGES, "page scores of few rows take the direct kernel below");
+  static constexpr int kStages = PAGES ? 3 : WIDE ? 4 : 6;
+  static constexpr int kAhead = kStages - 1;                   // page scores: stages in flight
+  // Weights of more than 32 rows: two sets share a tile, half of its columns each.  (The MMA stays
+  // one of N = all rows: in halves of 128 it reads A twice, 128 bytes of shared memory a clock, and
+  // the MMAs alone then took 99 us of what are 78 us of copies.)
+  static constexpr bool kSplit = WIDE && !PAGES;
   static constexpr int kDBufs = WIDE ? 2 : 4;                  // X tiles in tensor memory
+  static constexpr int kSets = kSplit ? 4 : 2;                 // reducing sets of four warps
   static constexpr int kTmemCols = WIDE ? 512 : 128;
-  static constexpr int kThreads = PAGES ? 640 : 384;
+  static constexpr int kThreads = 128 + kSets * 128 + (PAGES ? kLoaders * 32 : 0);
   static constexpr size_t kSmem = 1024 + static_cast<size_t>(kQBufs) * kQBytes + kStages * kStage;
 };
 
@@ -67,30 +78,91 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-struct KeyItem {
-  int b, kvh, split, tile0, tiles, n;   // n: keys of the list
+// A walk over a CTA's share of the tiles.
+template <bool PAGES>
+struct KeyWalk {
+  const KeyParams& p;
+  int b, kvh, tile, left;   // left: tiles to go, this one included
+  int n, tiles;             // keys and tiles of the list
+  bool fresh;               // first tile of the share or of its list
+  __device__ __forceinline__ KeyWalk(const KeyParams& prm, const int (&share)[4])
+      : p(prm), b(share[0]), kvh(share[1]), tile(share[2]), left(share[3]), fresh(true) {
+    if (left > 0) list();
+  }
+  __device__ __forceinline__ void list() {
+    n = list_keys(p, b);
+    tiles = (n + kKeys - 1) / kKeys;
+  }
+  static __device__ __forceinline__ int list_keys(const KeyParams& p, int b) {
+    const int prefix = __ldg(p.prefix_lens + b);
+    if (prefix < 0 || static_cast<long long>(prefix) + p.L >
+                          static_cast<long long>(p.max_pages) * kPageTokens)
+      return 0;
+    return PAGES ? prefix / kPageTokens : prefix;
+  }
+  __device__ __forceinline__ void next() {
+    fresh = false;
+    if (--left == 0 || ++tile < tiles) return;
+    tile = 0;
+    fresh = true;
+    if (++kvh < p.Hkv) return;
+    kvh = 0;
+    do {
+      ++b;
+      list();
+    } while (tiles == 0);   // left > 0: a list with tiles follows
+  }
+  __device__ __forceinline__ size_t row() const { return static_cast<size_t>(b) * p.Hkv + kvh; }
 };
 
-// Item idx of the schedule: runs of one list lie `lists` apart, so a CTA's items are spread over
-// the lists and the short last runs of long lists come last.  False for a run past the list's end.
+// This CTA's share of the tiles (whole warp): every CTA adds up all sequences' tiles and takes an
+// equal part of the total; CTA 0 reports bad lengths.
 template <bool PAGES>
-__device__ __forceinline__ bool key_item(int idx, const KeyParams& p, KeyItem& it) {
-  const int lists = p.B * p.Hkv;
-  it.split = idx / lists;
-  const int list = idx - it.split * lists;
-  it.b = list / p.Hkv;
-  it.kvh = list - it.b * p.Hkv;
-  const int prefix = __ldg(p.prefix_lens + it.b);
-  if (prefix < 0 || static_cast<long long>(prefix) + p.L >
-                        static_cast<long long>(p.max_pages) * kPageTokens) {
-    if (it.split == 0 && it.kvh == 0 && threadIdx.x == 0) atomicOr(p.err, BDLM_DEVERR_LENGTH);
-    return false;
+__device__ __forceinline__ void key_share(const KeyParams& p, int (&share)[4]) {
+  const int lane = threadIdx.x & 31;
+  auto seq_tiles = [&](int b) {
+    return b < p.B ? static_cast<long long>((KeyWalk<PAGES>::list_keys(p, b) + kKeys - 1) / kKeys) *
+                         p.Hkv
+                   : 0ll;
+  };
+  long long total = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const int b = b0 + lane;
+    total += seq_tiles(b);
+    if (blockIdx.x == 0 && b < p.B) {
+      const int prefix = __ldg(p.prefix_lens + b);
+      if (prefix < 0 || static_cast<long long>(prefix) + p.L >
+                            static_cast<long long>(p.max_pages) * kPageTokens)
+        atomicOr(p.err, BDLM_DEVERR_LENGTH);
+    }
   }
-  it.n = PAGES ? prefix / kPageTokens : prefix;
-  it.tile0 = it.split * p.tiles_per_item;
-  const int tiles = (it.n + kKeys - 1) / kKeys - it.tile0;
-  it.tiles = tiles < p.tiles_per_item ? tiles : p.tiles_per_item;
-  return it.tiles > 0;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+  const long long first = total * blockIdx.x / gridDim.x;
+  const long long end = total * (blockIdx.x + 1ll) / gridDim.x;
+  if (lane == 0) share[3] = 0;
+  __syncwarp();
+  if (end == first) return;
+  long long before = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    const long long mine = seq_tiles(b0 + lane);
+    long long x = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, off);
+      if (lane >= off) x += y;
+    }
+    x += before;   // tiles up to and with this sequence
+    if (first >= x - mine && first < x) {
+      const long long at = first - (x - mine), per = mine / p.Hkv;
+      share[0] = b0 + lane;
+      share[1] = static_cast<int>(at / per);
+      share[2] = static_cast<int>(at % per);
+      share[3] = static_cast<int>(end - first);
+    }
+    before = __shfl_sync(0xffffffffu, x, 31);
+    if (first < before) break;
+  }
 }
 
 template <bool PAGES, bool WIDE>
@@ -107,27 +179,32 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   __shared__ uint64_t bar_full[C::kStages], bar_empty[C::kStages];
   __shared__ uint64_t bar_qfull[C::kQBufs], bar_qempty[C::kQBufs];
   __shared__ uint64_t bar_dfull[C::kDBufs], bar_dempty[C::kDBufs], bar_lse[2], bar_done;
+  __shared__ uint64_t bar_part[C::kSplit ? 4 : 1][4];        // second halves' sums: by tile, quadrant
+  __shared__ float s_part[C::kSplit ? 4 : 1][C::kSplit ? 128 : 1];
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
+  __shared__ int s_share[4];
   __shared__ __align__(16) float s_lse[PAGES ? 1 : 2][PAGES ? 4 : C::kRowsMax];   // log2 units
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n16 = (p.rows + 15) & ~15;   // UMMA N
+  const int n16 = (p.rows + 15) & ~15;   // columns of X
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&bar_full[s], PAGES ? kLoaders : 1);
       mbar_init(&bar_empty[s], 1);
     }
     for (int b = 0; b < C::kQBufs; ++b) {
-      mbar_init(&bar_qfull[b], PAGES ? kLoaders : 1);
+      mbar_init(&bar_qfull[b], PAGES ? 3 : 1);
       mbar_init(&bar_qempty[b], 1);
     }
     for (int b = 0; b < C::kDBufs; ++b) {
       mbar_init(&bar_dfull[b], 1);
-      mbar_init(&bar_dempty[b], 4);   // the four warps of a set
+      mbar_init(&bar_dempty[b], C::kSplit ? 8 : 4);   // the warps that read a tile
     }
-    mbar_init(&bar_lse[0], 8);
-    mbar_init(&bar_lse[1], 8);
+    mbar_init(&bar_lse[0], C::kSets * 4);
+    mbar_init(&bar_lse[1], C::kSets * 4);
+    if constexpr (C::kSplit)
+      for (int i = 0; i < 16; ++i) mbar_init(&bar_part[i >> 2][i & 3], 1);
     mbar_init(&bar_done, 1);
     abort_flag = 0;
     fence_mbar_init();
@@ -145,63 +222,45 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     }
     fence_proxy_async_smem();
   }
+  griddep_wait();
+  if (warp == 3) key_share<PAGES>(p, s_share);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  griddep_wait();
   const uint32_t tmem = tmem_base;
 
   if (!PAGES && (warp == 1 || warp == 2)) {
-    // ------------------------------------------------------------ TMA: Q and K pages
+    // ------------------------------------------------------------ TMA: K pages
     const uint64_t policy = l2_policy_evict_first();   // K is read once
     bool ok = true;
-    int u = 0, item = 0;   // tiles and items so far
-    KeyItem it;
-    for (int idx = blockIdx.x; idx < p.total_items && ok; idx += gridDim.x) {
-      if (!key_item<PAGES>(idx, p, it)) continue;
-      if (warp == 1) {
-        const int qb = item % C::kQBufs;
-        if (lane == 0) {
-          ok = mbar_wait(&bar_qempty[qb], ((item / C::kQBufs) & 1) ^ 1, &abort_flag);
-          if (ok) {
-            mbar_arrive_expect_tx(&bar_qfull[qb], static_cast<uint32_t>(p.rows) * 256u);
-            for (int h = 0; h < 2; ++h)
-              tma_load_3d(sQ + qb * C::kQBytes + h * n16 * 128, &tm_q, &bar_qfull[qb], h * 64,
-                          it.kvh * p.G, it.b * p.L + p.l0);
-          }
+    int u = 0;
+    for (KeyWalk<PAGES> w(p, s_share); w.left > 0 && ok; w.next(), ++u) {
+      if ((u & 1) != warp - 1) continue;
+      const int st = u % C::kStages;
+      const int page = w.tile * (kKeys / kPageTokens) + (lane & 7);
+      int id = -1;
+      if (lane < 16 && page * kPageTokens < w.n) {
+        id = __ldg(p.page_table + static_cast<size_t>(w.b) * p.max_pages + page);
+        if (id < 0 || id >= p.num_pages) {
+          id = -1;
+          atomicOr(p.err, BDLM_DEVERR_PAGE);
         }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
       }
-      ++item;
-      const int32_t* pt = p.page_table + static_cast<size_t>(it.b) * p.max_pages;
-      for (int j = 0; j < it.tiles && ok; ++j, ++u) {
-        if ((u & 1) != warp - 1) continue;
-        const int st = u % C::kStages;
-        const int page = (it.tile0 + j) * (kKeys / kPageTokens) + (lane & 7);
-        int id = -1;
-        if (lane < 16 && page * kPageTokens < it.n) {
-          id = __ldg(pt + page);
-          if (id < 0 || id >= p.num_pages) {
-            id = -1;
-            atomicOr(p.err, BDLM_DEVERR_PAGE);
-          }
+      const uint32_t have = __ballot_sync(0xffffffffu, id >= 0);
+      if (lane == 0) {
+        ok = mbar_wait(&bar_empty[st], ((u / C::kStages) & 1) ^ 1, &abort_flag);
+        if (ok) {
+          if (have)
+            mbar_arrive_expect_tx(&bar_full[st], static_cast<uint32_t>(__popc(have)) * 2048u);
+          else
+            mbar_arrive(&bar_full[st]);
         }
-        const uint32_t have = __ballot_sync(0xffffffffu, id >= 0);
-        if (lane == 0) {
-          ok = mbar_wait(&bar_empty[st], ((u / C::kStages) & 1) ^ 1, &abort_flag);
-          if (ok) {
-            if (have)
-              mbar_arrive_expect_tx(&bar_full[st], static_cast<uint32_t>(__popc(have)) * 2048u);
-            else
-              mbar_arrive(&bar_full[st]);
-          }
-        }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        __syncwarp();
-        if (ok && id >= 0)
-          tma_load_4d_hint(sA + st * kStage + (lane >> 3) * kAtom + (lane & 7) * 2048, &tm_k,
-                           &bar_full[st], (lane >> 3) * 64, it.kvh, 0, id, policy);
       }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      __syncwarp();
+      if (ok && id >= 0)
+        tma_load_4d_hint(sA + st * kStage + (lane >> 3) * kAtom + (lane & 7) * 2048, &tm_k,
+                         &bar_full[st], (lane >> 3) * 64, w.kvh, 0, id, policy);
     }
     griddep_launch_dependents();
     if (!ok) {
@@ -214,59 +273,52 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         }
       __syncwarp();
     }
-  } else if (PAGES && warp >= 12) {
-    // ------------------------------------------------------------ gather: q+ / q-, page bounds
-    const int t = threadIdx.x - 384;   // 0 .. 255
-    const int c16 = t & 15;            // 16-byte chunk of a 256-byte half row
-    const uint32_t a_base = smem_u32(sA);
-    const uint32_t a_off = static_cast<uint32_t>((c16 >> 3) * kAtom);
-    bool ok = true;
-    int u = 0, item = 0;               // stages issued, items
-    int done = 0;                      // stages handed to the MMA
-    uint32_t top = 0;                  // largest |bound| seen in the item, as a bf16 pair
-    // Hands over the oldest stage in flight: the thread's own chunks have landed
-    // (cp.async.wait_group), so it looks at their magnitudes and signs the stage off.
-    auto hand_over = [&]() {
-      const int st = done % C::kStages;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = i * 16 + (t >> 4);
-        const uint4 v = *reinterpret_cast<const uint4*>(
-            sA + st * kStage + a_off + r * 128 + (((c16 & 7) ^ (r & 7)) << 4));
-        const uint32_t w[4] = {v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu, v.z & 0x7FFF7FFFu,
-                               v.w & 0x7FFF7FFFu};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const __nv_bfloat162 m =
-              __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&top),
-                          *reinterpret_cast<const __nv_bfloat162*>(&w[k]));
-          top = *reinterpret_cast<const uint32_t*>(&m);
+  } else if (!PAGES && warp == 3) {
+    // ------------------------------------------------------------ TMA: Q
+    if (lane == 0) {
+      bool ok = true;
+      int q = 0;
+      for (KeyWalk<PAGES> w(p, s_share); w.left > 0 && ok; w.next()) {
+        if (!w.fresh) continue;
+        const int qb = q % C::kQBufs;
+        if (!(ok = mbar_wait(&bar_qempty[qb], ((q / C::kQBufs) & 1) ^ 1, &abort_flag))) break;
+        mbar_arrive_expect_tx(&bar_qfull[qb], static_cast<uint32_t>(p.rows) * 256u);
+        for (int h = 0; h < 2; ++h)
+          tma_load_3d(sQ + qb * C::kQBytes + h * n16 * 128, &tm_q, &bar_qfull[qb], h * 64,
+                      w.kvh * p.G, w.b * p.L + p.l0);
+        ++q;
+      }
+      if (!ok) {
+        int dummy = 0;
+        for (int b = 0; b < C::kQBufs; ++b) {
+          mbar_wait(&bar_qfull[b], 0, &dummy, 1000000ull);
+          mbar_wait(&bar_qfull[b], 1, &dummy, 1000000ull);
         }
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar_full[st]);
-      ++done;
-    };
-    KeyItem it;
-    for (int idx = blockIdx.x; idx < p.total_items && ok; idx += gridDim.x) {
-      if (!key_item<PAGES>(idx, p, it)) continue;
-      const int qb = item % C::kQBufs;
-      if (!(ok = mbar_wait_warp(&bar_qempty[qb], ((item / C::kQBufs) & 1) ^ 1, &abort_flag))) break;
-      // row n of the item: query l0 + n / G, head kvh * G + n % G; padding rows repeat row 0, so
-      // they cannot raise a maximum
-      for (int c = t; c < n16 * 16; c += kLoaders * 32) {
+    }
+  } else if (PAGES && warp >= 1 && warp <= 3) {
+    // ------------------------------------------------------------ q+ and q-
+    bool ok = true;
+    int q = 0;
+    for (KeyWalk<PAGES> w(p, s_share); w.left > 0 && ok; w.next()) {
+      if (!w.fresh) continue;
+      const int qb = q % C::kQBufs;
+      if (!(ok = mbar_wait_warp(&bar_qempty[qb], ((q / C::kQBufs) & 1) ^ 1, &abort_flag))) break;
+      // row n: query l0 + n / G, head kvh * G + n % G; padding rows repeat row 0, so they cannot
+      // raise a maximum
+#pragma unroll 4
+      for (int c = threadIdx.x - 32; c < n16 * 16; c += 96) {
         const int r = c >> 4, n = r < p.rows ? r : 0, cc = c & 15;
         const uint4 v = __ldg(reinterpret_cast<const uint4*>(
-                                  p.q + ((static_cast<size_t>(it.b) * p.L + p.l0 + n / p.G) * p.Hq +
-                                         it.kvh * p.G + n % p.G) * 128) + cc);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                                  p.q + ((static_cast<size_t>(w.b) * p.L + p.l0 + n / p.G) * p.Hq +
+                                         w.kvh * p.G + n % p.G) * 128) + cc);
+        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const uint32_t neg = ((w[k] >> 15) & 0x00010001u) * 0xFFFFu;   // 16 ones per negative
-          hi[k] = w[k] & ~neg;
-          lo[k] = w[k] & neg;
+          const uint32_t neg = ((x[k] >> 15) & 0x00010001u) * 0xFFFFu;   // 16 ones per negative
+          hi[k] = x[k] & ~neg;
+          lo[k] = x[k] & neg;
         }
         uint8_t* d = sQ + qb * C::kQBytes + ((cc >> 3) * n16 + r) * 128 + (((cc & 7) ^ (r & 7)) << 4);
         *reinterpret_cast<uint4*>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -275,185 +327,258 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar_qfull[qb]);
-      ++item;
-      top = 0;
-      const int32_t* pt = p.page_table + static_cast<size_t>(it.b) * p.max_pages;
-      constexpr int kAhead = C::kStages - 1;   // stages in flight per thread
-      const int u0 = u;
-      for (int j = 0; j < it.tiles && ok; ++j) {
-        int id[8];
+      ++q;
+    }
+  } else if (PAGES && warp >= 12) {
+    // ------------------------------------------------------------ gather of the page bounds
+    const int t = threadIdx.x - 384;   // 0 .. 255
+    const int c16 = t & 15;            // 16-byte chunk of a 256-byte half row
+    const uint32_t a_base = smem_u32(sA);
+    const uint32_t a_off = static_cast<uint32_t>((c16 >> 3) * kAtom);
+    constexpr int kAhead = C::kAhead;
+    bool ok = true;
+    int s = 0, done = 0;   // stages issued, and handed to the MMA
+    uint32_t top = 0;      // largest |bound| seen in the tile, as a bf16 pair
+    KeyWalk<PAGES> back(p, s_share);   // the tile of stage `done`
+    // Hands over the oldest stage in flight: the thread's own chunks have landed
+    // (cp.async.wait_group), so it looks at their magnitudes and signs the stage off.  The largest
+    // magnitude of a tile, one value per warp, is what bounds its scores' rounding error.
+    auto hand_over = [&]() {
+      const int st = done % C::kStages;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int page = (it.tile0 + j) * kKeys + i * 16 + (t >> 4);
-          id[i] = page < it.n ? __ldg(pt + page) : -1;
-          if (page < it.n && (id[i] < 0 || id[i] >= p.num_pages)) {
-            id[i] = -1;
-            if (c16 == 0) atomicOr(p.err, BDLM_DEVERR_PAGE);
-          }
-        }
-        for (int h = 0; h < 2; ++h, ++u) {   // hi (row 1 of a page's bounds), then lo (row 0)
-          if (u - u0 >= kAhead) {
-            cp_async_wait<kAhead - 1>();
-            hand_over();
-          }
-          const int st = u % C::kStages;
-          if (!(ok = mbar_wait_warp(&bar_empty[st], ((u / C::kStages) & 1) ^ 1, &abort_flag))) break;
+      for (int i = 0; i < 8; ++i) {
+        const int r = i * 16 + (t >> 4);
+        const uint4 v = *reinterpret_cast<const uint4*>(
+            sA + st * kStage + a_off + r * 128 + (((c16 & 7) ^ (r & 7)) << 4));
+        const uint32_t x[4] = {v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu, v.z & 0x7FFF7FFFu,
+                               v.w & 0x7FFF7FFFu};
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int r = i * 16 + (t >> 4);
-            const size_t row =
-                (static_cast<size_t>(id[i] < 0 ? 0 : id[i]) * p.Hkv + it.kvh) * 2 + (1 - h);
-            cp_async16(a_base + st * kStage + a_off + r * 128 + (((c16 & 7) ^ (r & 7)) << 4),
-                       p.bounds + row * 128 + c16 * 8, id[i] >= 0);
-          }
-          cp_async_commit();
+        for (int k = 0; k < 4; ++k) {
+          const __nv_bfloat162 m =
+              __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&top),
+                          *reinterpret_cast<const __nv_bfloat162*>(&x[k]));
+          top = *reinterpret_cast<const uint32_t*>(&m);
         }
       }
-      if (!ok) break;
-      cp_async_wait<0>();
-      while (done < u) hand_over();
-      // the run's largest |bound|, one value per warp: what bounds the scores' rounding error
-      __nv_bfloat162 m2 = *reinterpret_cast<const __nv_bfloat162*>(&top);
-      float m = fmaxf(__low2float(m2), __high2float(m2));
-      if (!(__low2float(m2) <= CUDART_INF_F) || !(__high2float(m2) <= CUDART_INF_F)) m = CUDART_INF_F;
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar_full[st]);
+      if (done++ & 1) {
+        const float a = bf16_lo(top), z = bf16_hi(top);
+        float m = a <= CUDART_INF_F && z <= CUDART_INF_F ? fmaxf(a, z) : CUDART_INF_F;   // NaN: inf
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-      if (lane == 0)
-        p.amax[((static_cast<size_t>(it.b) * p.Hkv + it.kvh) * p.items_per_list + it.split) *
-                   kLoaders + (warp - 12)] = m;
+        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+        if (lane == 0) p.amax[(back.row() * p.max_tiles + back.tile) * kLoaders + (warp - 12)] = m;
+        top = 0;
+        back.next();
+      }
+    };
+    KeyWalk<PAGES> w(p, s_share);
+    // page ids of the walk's tile: this thread's eight rows (-1: none)
+    auto load_ids = [&](int (&id)[8]) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int page = w.tile * kKeys + i * 16 + (t >> 4);
+        id[i] = w.left > 0 && page < w.n
+                    ? __ldg(p.page_table + static_cast<size_t>(w.b) * p.max_pages + page)
+                    : -1;
+      }
+    };
+    int id[8];
+    load_ids(id);
+    while (w.left > 0 && ok) {
+      const int kvh = w.kvh, first = w.tile * kKeys, n = w.n;
+      w.next();
+      int id_next[8];   // the next tile's ids arrive while this one's stages are waited for
+      load_ids(id_next);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (id[i] < 0 || id[i] >= p.num_pages) {
+          if (c16 == 0 && first + i * 16 + (t >> 4) < n) atomicOr(p.err, BDLM_DEVERR_PAGE);
+          id[i] = -1;
+        }
+      for (int h = 0; h < 2; ++h, ++s) {   // hi (row 1 of a page's bounds), then lo (row 0)
+        if (s >= kAhead) {
+          cp_async_wait<kAhead - 1>();
+          hand_over();
+        }
+        const int st = s % C::kStages;
+        if (!(ok = mbar_wait_warp(&bar_empty[st], ((s / C::kStages) & 1) ^ 1, &abort_flag))) break;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = i * 16 + (t >> 4);
+          const size_t row = (static_cast<size_t>(id[i] < 0 ? 0 : id[i]) * p.Hkv + kvh) * 2 + (1 - h);
+          cp_async16(a_base + st * kStage + a_off + r * 128 + (((c16 & 7) ^ (r & 7)) << 4),
+                     p.bounds + row * 128 + c16 * 8, id[i] >= 0);
+        }
+        cp_async_commit();
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) id[i] = id_next[i];
     }
-    cp_async_wait<0>();
     griddep_launch_dependents();
+    cp_async_wait<0>();
+    if (ok)
+      while (done < s) hand_over();
   } else if (warp == 0) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       const uint32_t idesc = idesc_bf16_f32(128, n16, false, false);
       const uint32_t q_addr = smem_u32(sQ), a_addr = smem_u32(sA);
       bool ok = true;
-      int u = 0, s = 0, item = 0;   // tiles, stages, items so far
-      KeyItem it;
-      for (int idx = blockIdx.x; idx < p.total_items && ok; idx += gridDim.x) {
-        if (!key_item<PAGES>(idx, p, it)) continue;
-        const int qb = item % C::kQBufs;
-        if (!(ok = mbar_wait(&bar_qfull[qb], (item / C::kQBufs) & 1, &abort_flag))) break;
-        for (int j = 0; j < it.tiles && ok; ++j, ++u) {
-          const int db = u % C::kDBufs;
-          if (!(ok = mbar_wait(&bar_dempty[db], ((u / C::kDBufs) & 1) ^ 1, &abort_flag))) break;
-          const uint32_t d = tmem + static_cast<uint32_t>(db * C::kRowsMax);
-          for (int h = 0; h < kHalves; ++h, ++s) {
-            const int st = s % C::kStages;
-            if (!(ok = mbar_wait(&bar_full[st], (s / C::kStages) & 1, &abort_flag))) break;
-            tc_fence_after();
-            const uint32_t qa = q_addr + qb * C::kQBytes + h * 2 * n16 * 128;
-            const uint32_t aa = a_addr + st * kStage;
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              umma_bf16(d, smem_desc(aa + (kk >> 2) * kAtom + (kk & 3) * 32, 16, 1024),
-                        smem_desc(qa + (kk >> 2) * n16 * 128 + (kk & 3) * 32, 16, 1024), idesc,
-                        h > 0 || kk > 0 ? 1u : 0u);
-            umma_commit(&bar_empty[st]);
-          }
-          if (ok) umma_commit(&bar_dfull[db]);
+      int u = 0, s = 0, q = -1;   // tiles, stages, lists so far
+      for (KeyWalk<PAGES> w(p, s_share); w.left > 0 && ok; ++u) {
+        if (w.fresh) {
+          ++q;
+          if (!(ok = mbar_wait(&bar_qfull[q % C::kQBufs], (q / C::kQBufs) & 1, &abort_flag))) break;
         }
-        if (ok) umma_commit(&bar_qempty[qb]);
-        ++item;
+        const int qb = q % C::kQBufs, db = u % C::kDBufs;
+        if (!(ok = mbar_wait(&bar_dempty[db], ((u / C::kDBufs) & 1) ^ 1, &abort_flag))) break;
+        const uint32_t d = tmem + static_cast<uint32_t>(db * C::kRowsMax);
+        for (int h = 0; h < kHalves; ++h, ++s) {
+          const int st = s % C::kStages;
+          if (!(ok = mbar_wait(&bar_full[st], (s / C::kStages) & 1, &abort_flag))) break;
+          tc_fence_after();
+          const uint32_t qa = q_addr + qb * C::kQBytes + h * 2 * n16 * 128;
+          const uint32_t aa = a_addr + st * kStage;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma_bf16(d, smem_desc(aa + (kk >> 2) * kAtom + (kk & 3) * 32, 16, 1024),
+                      smem_desc(qa + (kk >> 2) * n16 * 128 + (kk & 3) * 32, 16, 1024), idesc,
+                      h > 0 || kk > 0 ? 1u : 0u);
+          umma_commit(&bar_empty[st]);
+        }
+        if (!ok) break;
+        umma_commit(&bar_dfull[db]);
+        w.next();
+        if (w.left == 0 || w.fresh) umma_commit(&bar_qempty[qb]);
       }
       umma_commit(&bar_done);
     }
-  } else if (warp >= 4 && warp < 12) {
+  } else if (warp >= 4 && warp < 4 + C::kSets * 4) {
     // ------------------------------------------------------------ reduction over the query rows
     const int q4 = warp & 3, set = (warp - 4) >> 2;
     const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
     bool ok = true;
-    int u = 0, item = 0;
-    KeyItem it;
-    for (int idx = blockIdx.x; idx < p.total_items && ok; idx += gridDim.x) {
-      if (!key_item<PAGES>(idx, p, it)) continue;
-      const float* lse = s_lse[0];
+    int u = 0, q = 0;
+    const float* lse = s_lse[0];
+    for (KeyWalk<PAGES> w(p, s_share); w.left > 0 && ok; w.next(), ++u) {
       if constexpr (!PAGES) {
-        // the eight warps fill one of two buffers and wait for each other: a warp that writes
-        // buffer x has seen every warp start the item between, so all are done with the item
-        // that used x before
-        float* w = s_lse[item & 1];
-        for (int n = threadIdx.x - 128; n < n16; n += 256)
-          w[n] = n < p.rows
-                     ? __ldg(p.lse + (static_cast<size_t>(it.b) * p.L + p.l0 + n / p.G) * p.Hq +
-                             it.kvh * p.G + n % p.G) * 1.4426950408889634f
-                     : CUDART_INF_F;   // padding rows: 2^-inf = 0
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_lse[item & 1]);
-        if (!(ok = mbar_wait_warp(&bar_lse[item & 1], (item >> 1) & 1, &abort_flag))) break;
-        lse = w;
+        if (w.fresh) {
+          // the warps fill one of two buffers and wait for each other: a warp that writes
+          // buffer x has seen every warp start the list between, so all are done with the list
+          // that used x before
+          float* x = s_lse[q & 1];   // -lse, so that the exponent is one FMA
+          for (int n = threadIdx.x - 128; n < n16; n += C::kSets * 128)
+            x[n] = n < p.rows
+                       ? __ldg(p.lse + (static_cast<size_t>(w.b) * p.L + p.l0 + n / p.G) * p.Hq +
+                               w.kvh * p.G + n % p.G) * -1.4426950408889634f
+                       : -CUDART_INF_F;   // padding rows: 2^-inf = 0
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar_lse[q & 1]);
+          if (!(ok = mbar_wait_warp(&bar_lse[q & 1], (q >> 1) & 1, &abort_flag))) break;
+          lse = x;
+          ++q;
+        }
       }
-      ++item;
-      for (int j = 0; j < it.tiles && ok; ++j, ++u) {
-        if ((u & 1) != set) continue;
-        const int key = (it.tile0 + j) * kKeys + q4 * 32 + lane;
-        bool live = key < it.n;
-        const size_t list = static_cast<size_t>(it.b) * p.Hkv + it.kvh;
-        float* wp = nullptr;
-        float w_old = 0.f;
-        if (live) {
-          const int page = PAGES ? key : key / kPageTokens;
-          const int id = __ldg(p.page_table + static_cast<size_t>(it.b) * p.max_pages + page);
-          live = id >= 0 && id < p.num_pages;
+      if ((u & 1) != (C::kSplit ? set >> 1 : set)) continue;
+      const int half = C::kSplit ? set & 1 : 0;   // which columns of the tile
+      const int key = w.tile * kKeys + q4 * 32 + lane;
+      bool live = key < w.n;
+      float* wp = nullptr;
+      float w_old = 0.f;
+      if (live) {
+        const int page = PAGES ? key : key / kPageTokens;
+        const int id = __ldg(p.page_table + static_cast<size_t>(w.b) * p.max_pages + page);
+        live = id >= 0 && id < p.num_pages;
+      }
+      if constexpr (!PAGES) {
+        wp = p.weights + w.row() * (static_cast<size_t>(p.max_pages) * kPageTokens) + key;
+        if (live && half == 0) w_old = *wp;
+      }
+      const int db = u % C::kDBufs;
+      const int split = C::kSplit ? ((n16 >> 1) + 15) & ~15 : 0;   // columns of the first half
+      const int cols = !C::kSplit ? n16 : half == 0 ? split : n16 - split;
+      if (!(ok = mbar_wait_warp(&bar_dfull[db], (u / C::kDBufs) & 1, &abort_flag))) break;
+      tc_fence_after();
+      const uint32_t td =
+          tmem + lane_off + static_cast<uint32_t>(db * C::kRowsMax + half * split);
+      // 16 columns at a time, the next 16 on their way from tensor memory meanwhile
+      uint32_t r[2][16];
+      tmem_ld16(td, r[0]);
+      auto columns = [&](auto&& each) {
+        for (int c = 0; c < cols; c += 32) {
+          tmem_wait_ld();
+          tmem_regs_ready(r[0]);
+          if (c + 16 < cols) tmem_ld16(td + c + 16, r[1]);
+          each(c, r[0]);
+          if (c + 16 >= cols) break;
+          tmem_wait_ld();
+          tmem_regs_ready(r[1]);
+          if (c + 32 < cols) tmem_ld16(td + c + 32, r[0]);
+          each(c + 16, r[1]);
         }
-        if constexpr (!PAGES) {
-          wp = p.weights + list * (static_cast<size_t>(p.max_pages) * kPageTokens) + key;
-          if (live) w_old = *wp;
-        }
-        const int db = u % C::kDBufs;
-        if (!(ok = mbar_wait_warp(&bar_dfull[db], (u / C::kDBufs) & 1, &abort_flag))) break;
-        tc_fence_after();
-        const uint32_t td = tmem + lane_off + static_cast<uint32_t>(db * C::kRowsMax);
-        if constexpr (!PAGES) {
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
-          for (int c = 0; c < n16; c += 16) {
-            uint32_t r[16];
-            tmem_ld16(td + c, r);
-            tmem_wait_ld();
-            tmem_regs_ready(r);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_dempty[db]);
+      };
+      if constexpr (!PAGES) {
+        // two columns per packed instruction
+        const float2 cs2 = make_float2(p.scale_log2, p.scale_log2);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const float* nlse = lse + half * split;
+        columns([&](int c, const uint32_t (&x)[16]) {
 #pragma unroll
-            for (int k = 0; k < 16; k += 4) {
-              const float4 l4 = *reinterpret_cast<const float4*>(lse + c + k);
-              sum[0] += ex2(fmaf(__uint_as_float(r[k]), p.scale_log2, -l4.x));
-              sum[1] += ex2(fmaf(__uint_as_float(r[k + 1]), p.scale_log2, -l4.y));
-              sum[2] += ex2(fmaf(__uint_as_float(r[k + 2]), p.scale_log2, -l4.z));
-              sum[3] += ex2(fmaf(__uint_as_float(r[k + 3]), p.scale_log2, -l4.w));
+          for (int k = 0; k < 16; k += 4) {
+            const float4 l4 = *reinterpret_cast<const float4*>(nlse + c + k);
+            const float2 a = __ffma2_rn(
+                make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), cs2,
+                make_float2(l4.x, l4.y));
+            const float2 z = __ffma2_rn(
+                make_float2(__uint_as_float(x[k + 2]), __uint_as_float(x[k + 3])), cs2,
+                make_float2(l4.z, l4.w));
+            sum[0] = __fadd2_rn(sum[0], make_float2(ex2(a.x), ex2(a.y)));
+            sum[1] = __fadd2_rn(sum[1], make_float2(ex2(z.x), ex2(z.y)));
+          }
+        });
+        float total = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        if constexpr (C::kSplit) {
+          // the second half's sum goes to the first half's warp.  Four buffers, by tile: the next
+          // tile to use this one is the second after it of the same sets, and its MMA waited for
+          // both halves' warps to have read the tile between, by when the first half's was done
+          // with this one
+          uint64_t* bar = &bar_part[u & 3][q4];
+          float* part = s_part[u & 3] + q4 * 32 + lane;
+          if (half == 1) {
+            *part = total;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+            live = false;
+          } else {
+            if (!(ok = mbar_wait_warp(bar, (u >> 2) & 1, &abort_flag))) break;
+            total += *part;
+          }
+        }
+        if (live) *wp = fmaf(p.decay, w_old, total);
+      } else {
+        // a group's columns are `width` consecutive query rows
+        float m = -CUDART_INF_F;
+        int to_go = p.width;
+        float* out = p.scores + (static_cast<size_t>(w.b) * p.groups + p.l0 / p.group) * p.Hkv *
+                                    static_cast<size_t>(p.max_pages) +
+                     static_cast<size_t>(w.kvh) * p.max_pages + key;
+        columns([&](int c, const uint32_t (&x)[16]) {
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            m = fmaxf(m, __uint_as_float(x[k]));
+            if (--to_go == 0) {
+              if (key < w.n && c + k < p.rows) *out = live ? m : -CUDART_INF_F;
+              out += static_cast<size_t>(p.Hkv) * p.max_pages;
+              m = -CUDART_INF_F;
+              to_go = p.width;
             }
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar_dempty[db]);
-          if (live) *wp = fmaf(p.decay, w_old, (sum[0] + sum[1]) + (sum[2] + sum[3]));
-        } else {
-          // a group's columns are `width` consecutive query rows
-          float m = -CUDART_INF_F;
-          int left = p.width, g = 0;
-          float* out = p.scores + (static_cast<size_t>(it.b) * p.groups + p.l0 / p.group) *
-                                      p.Hkv * static_cast<size_t>(p.max_pages) +
-                       static_cast<size_t>(it.kvh) * p.max_pages + key;
-          for (int c = 0; c < n16; c += 16) {
-            uint32_t r[16];
-            tmem_ld16(td + c, r);
-            tmem_wait_ld();
-            tmem_regs_ready(r);
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              m = fmaxf(m, __uint_as_float(r[k]));
-              if (--left == 0) {
-                if (key < it.n && c + k < p.rows)
-                  out[static_cast<size_t>(g) * p.Hkv * p.max_pages] = live ? m : -CUDART_INF_F;
-                m = -CUDART_INF_F;
-                left = p.width;
-                ++g;
-              }
-            }
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar_dempty[db]);
-        }
+        });
       }
     }
   }
@@ -469,6 +594,160 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     tmem_dealloc(tmem, C::kTmemCols);
   }
   if (threadIdx.x == 0 && abort_flag) atomicOr(p.err, BDLM_DEVERR_TIMEOUT);
+}
+
+// Page scores of up to 32 query rows.  A page's 512 bytes take 2 * 16 to 32 rows * 256 flops: HBM
+// is the only bound, and staging pages in shared memory for tcgen05 (the kernel above) costs more
+// than it saves (42 us against XX us, 16 x 8 lists of 1875-3750 pages, 16 rows).  So each warp scores 16
+// pages with m16n8k16 straight from global memory: the order of the 256 values along K is free as
+// long as both operands have the same, so a lane's 16-byte chunk of a page row (8 values) serves as
+// its fragments of two MMAs, 16 loads a lane are in flight at once, and nothing is staged but q+ and
+// q-.  A CTA takes 128 pages a round (8 warps), its share of the tiles as above, two CTAs per SM.
+constexpr int kDirectRows = 32;
+constexpr int kDirectPitch = 512 + 64;   // bytes of a q row: 64 more, so that 8 lanes miss no bank
+
+__device__ __forceinline__ uint4 ld_stream16(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+template <int NT>   // query rows in tiles of 8
+__global__ void __launch_bounds__(256, 2)
+page_scores_direct_kernel(const KeyParams p) {
+  __shared__ __align__(16) uint8_t sQ[NT * 8 * kDirectPitch];
+  __shared__ int s_share[4];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  griddep_wait();
+  griddep_launch_dependents();
+  if (warp == 0) key_share<true>(p, s_share);
+  __syncthreads();
+  int gid[NT][2];   // the groups of this lane's columns 8 nt + 2t, + 1 (padding: none)
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int n = nt * 8 + 2 * t + k;
+      gid[nt][k] = n < p.rows ? n / p.width : -1;
+    }
+  const int groups = p.rows / p.width;
+  const size_t group_stride = static_cast<size_t>(p.Hkv) * p.max_pages;
+  KeyWalk<true> w(p, s_share);
+  auto load_ids = [&](int (&id)[2]) {   // pages g and g + 8 of this warp's 16
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int page = w.tile * kKeys + warp * 16 + r * 8 + g;
+      id[r] = w.left > 0 && page < w.n
+                  ? __ldg(p.page_table + static_cast<size_t>(w.b) * p.max_pages + page)
+                  : -1;
+    }
+  };
+  int id[2];
+  load_ids(id);
+  while (w.left > 0) {
+    if (w.fresh) {
+      __syncthreads();   // every warp is done with the list before
+      for (int c = threadIdx.x; c < NT * 8 * 16; c += 256) {
+        const int r = c >> 4, cc = c & 15;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (r < p.rows)
+          v = __ldg(reinterpret_cast<const uint4*>(
+                        p.q + ((static_cast<size_t>(w.b) * p.L + p.l0 + r / p.G) * p.Hq +
+                               w.kvh * p.G + r % p.G) * 128) + cc);
+        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t neg = ((x[k] >> 15) & 0x00010001u) * 0xFFFFu;   // 16 ones per negative
+          hi[k] = x[k] & ~neg;
+          lo[k] = x[k] & neg;
+        }
+        *reinterpret_cast<uint4*>(sQ + r * kDirectPitch + cc * 16) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        *reinterpret_cast<uint4*>(sQ + r * kDirectPitch + 256 + cc * 16) =
+            make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      }
+      __syncthreads();
+    }
+    const int first = w.tile * kKeys + warp * 16, n = w.n;
+    const size_t row = w.row(), out_row = (static_cast<size_t>(w.b) * p.groups + p.l0 / p.group) *
+                                              group_stride +
+                                          static_cast<size_t>(w.kvh) * p.max_pages;
+    float* amax = p.amax + (row * p.max_tiles + w.tile) * kLoaders + warp;
+    const int kvh = w.kvh;
+    // the pages' rows: chunk 4j + t of lo (j < 4), then of hi
+    uint4 a[8][2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const bool ok = id[r] >= 0 && id[r] < p.num_pages;
+      if (!ok && first + r * 8 + g < n && t == 0) atomicOr(p.err, BDLM_DEVERR_PAGE);
+      const uint4* src = reinterpret_cast<const uint4*>(p.bounds) +
+                         (static_cast<size_t>(ok ? id[r] : 0) * p.Hkv + kvh) * 32 + t;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) a[j][r] = ok ? ld_stream16(src + 4 * j) : make_uint4(0, 0, 0, 0);
+      if (!ok) id[r] = -1;
+    }
+    const bool live[2] = {id[0] >= 0, id[1] >= 0};
+    w.next();
+    load_ids(id);   // the next tile's ids arrive with this tile's pages
+    float d[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) d[nt][0] = d[nt][1] = d[nt][2] = d[nt][3] = 0.f;
+    uint32_t top = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint4 x = a[j][0], y = a[j][1];
+      const uint32_t words[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t mag = words[k] & 0x7FFF7FFFu;
+        const __nv_bfloat162 m = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&top),
+                                             *reinterpret_cast<const __nv_bfloat162*>(&mag));
+        top = *reinterpret_cast<const uint32_t*>(&m);
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const uint4 q = *reinterpret_cast<const uint4*>(sQ + (nt * 8 + g) * kDirectPitch + j * 64 + t * 16);
+        mma_16816(d[nt], x.x, y.x, x.y, y.y, q.x, q.y);
+        mma_16816(d[nt], x.z, y.z, x.w, y.w, q.z, q.w);
+      }
+    }
+    // the largest |bound| of the 16 pages (a NaN counts as infinite)
+    const float m0 = bf16_lo(top), m1 = bf16_hi(top);
+    float m = m0 <= CUDART_INF_F && m1 <= CUDART_INF_F ? fmaxf(m0, m1) : CUDART_INF_F;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    if (lane == 0) *amax = m;
+    // each group's maximum over its columns, spread over the four lanes of a page
+    for (int s = 0; s < groups; ++s) {
+      float best[2] = {-CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          if (gid[nt][k] == s) {
+            best[0] = fmaxf(best[0], d[nt][k]);
+            best[1] = fmaxf(best[1], d[nt][2 + k]);
+          }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 1));
+        best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 2));
+        const int page = first + r * 8 + g;
+        if (t == (s & 3) && page < n)
+          p.scores[out_row + s * group_stride + page] = live[r] ? best[r] : -CUDART_INF_F;
+      }
+    }
+  }
 }
 
 // Bounds of the full pages that hold tokens from .. to - 1: lo and hi over the 16 slots, per head
@@ -536,39 +815,38 @@ cudaError_t launch_key_t(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const
                                 static_cast<int>(C::kSmem));
   });
   if (e != cudaSuccess) return e;
-  const int grid = p.total_items < num_sms ? p.total_items : num_sms;
+  const long long most = static_cast<long long>(p.B) * p.Hkv * p.max_tiles;
+  const int grid = static_cast<int>(most < num_sms ? most : num_sms);
   return launch_pdl(key_reduce_kernel<PAGES, WIDE>, dim3(grid), dim3(C::kThreads), C::kSmem, stream,
                     tm_q, tm_k, p);
 }
 
 }  // namespace
 
-KeyPlan plan_keys(int B, int Hkv, int max_keys, int rows, int num_sms) {
-  KeyPlan pl;
-  const long long tiles = (static_cast<long long>(max_keys) + kKeys - 1) / kKeys;
-  const long long lists = static_cast<long long>(B) * Hkv;
-  // Runs of up to 16 tiles (32 for wide rows, whose Q costs an item up to 64 KB), shorter while
-  // the batch has fewer than four runs per SM: a run's Q load is then cheap beside an idle SM.
-  long long per = rows > 32 ? 32 : 16;
-  while (per > 1 && lists * ((tiles + per - 1) / per) < 4ll * num_sms) per >>= 1;
-  pl.tiles_per_item = static_cast<int>(per);
-  pl.items_per_list = static_cast<int>((tiles + per - 1) / per);
-  pl.total_items = lists * pl.items_per_list;
-  pl.amax_floats = static_cast<size_t>(pl.total_items) * kLoaders;
-  return pl;
-}
-
 int key_rows_max() { return 256; }
 
-cudaError_t launch_keys(bool pages, const CUtensorMap& tm_q, const CUtensorMap& tm_k,
-                        const KeyParams& p, int num_sms, cudaStream_t stream) {
-  // Up to 32 query rows: more stages and two Q buffers; more rows need their shared memory for Q.
-  const bool wide = p.rows > 32;
-  if (pages)
-    return wide ? launch_key_t<true, true>(tm_q, tm_k, p, num_sms, stream)
-                : launch_key_t<true, false>(tm_q, tm_k, p, num_sms, stream);
-  return wide ? launch_key_t<false, true>(tm_q, tm_k, p, num_sms, stream)
-              : launch_key_t<false, false>(tm_q, tm_k, p, num_sms, stream);
+cudaError_t launch_attention_weights(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
+                                     const KeyParams& p, int num_sms, cudaStream_t stream) {
+  // up to 32 query rows: more stages and two Q buffers; more rows need their shared memory for Q
+  return p.rows > 32 ? launch_key_t<false, true>(tm_q, tm_k, p, num_sms, stream)
+                     : launch_key_t<false, false>(tm_q, tm_k, p, num_sms, stream);
+}
+
+namespace {
+template <int NT>
+cudaError_t launch_direct_t(const KeyParams& p, int num_sms, cudaStream_t stream) {
+  const long long most = static_cast<long long>(p.B) * p.Hkv * p.max_tiles;
+  const int grid = static_cast<int>(most < 2ll * num_sms ? most : 2ll * num_sms);
+  return launch_pdl(page_scores_direct_kernel<NT>, dim3(grid), dim3(256), 0, stream, p);
+}
+}  // namespace
+
+cudaError_t launch_page_scores(const KeyParams& p, int num_sms, cudaStream_t stream) {
+  if (p.rows <= 8) return launch_direct_t<1>(p, num_sms, stream);
+  if (p.rows <= 16) return launch_direct_t<2>(p, num_sms, stream);
+  if (p.rows <= kDirectRows) return launch_direct_t<4>(p, num_sms, stream);
+  const CUtensorMap none = {};
+  return launch_key_t<true, true>(none, none, p, num_sms, stream);
 }
 
 cudaError_t launch_page_bounds(const uint16_t* k_pages, const int32_t* page_table,

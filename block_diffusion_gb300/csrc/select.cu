@@ -3,8 +3,10 @@
 //
 // Top k of a row of floats: the row's keys (floats mapped to unsigned integers of the same order)
 // are counted in up to 2048 buckets that evenly divide the range still in question, the bucket
-// holding the k-th largest becomes the next range, and so on; 32-bit keys take three rounds at
-// most.  One CTA per row, everything after the first read in shared memory where it fits.  The
+// holding the k-th largest becomes the next range, and so on; once that bucket holds at most
+// kDirect keys they are ranked against each other directly, mostly after one round (three rounds
+// at most for 32-bit keys).  One CTA per row, everything after the first read in shared memory
+// where it fits.  The
 // buckets divide the range in use (min .. max first), not fixed bits of the key: rows of similar
 // values would otherwise fall into a few buckets, whose counters then serialise.  Ties at the k-th
 // value go to the lowest index, and the output is in index order, so nothing depends on the order
@@ -22,6 +24,7 @@ namespace {
 
 constexpr int kTok = 16;       // tokens per page
 constexpr int kBuckets = 2048;
+constexpr int kDirect = 256;   // keys ranked directly (the bucket counters' memory holds them)
 
 // Unsigned key with the floats' order; -0 and +0 are equal, NaN comes below every number.
 __device__ __forceinline__ uint32_t order_key(float f) {
@@ -84,6 +87,7 @@ __device__ __forceinline__ K kth_largest(int k, K lo, K hi, Each&& each, int* hi
                                          K* s_pick, int* above) {
   int larger = 0;
   BlockSum sum{s_scan};
+  K* few = reinterpret_cast<K*>(hist);
   while (lo < hi) {
     const K range = hi - lo;
     int bits = sizeof(K) == 8 ? 64 - __clzll(static_cast<long long>(range))
@@ -108,6 +112,8 @@ __device__ __forceinline__ K kth_largest(int k, K lo, K hi, Each&& each, int* hi
         if (before + hist[bucket] >= k) {
           s_pick[0] = static_cast<K>(bucket);
           s_scan[33] = before;
+          s_scan[34] = hist[bucket];
+          s_scan[35] = 0;
           break;
         }
         before += hist[bucket];
@@ -116,10 +122,34 @@ __device__ __forceinline__ K kth_largest(int k, K lo, K hi, Each&& each, int* hi
     __syncthreads();
     const K from = lo + (s_pick[0] << shift), width = (static_cast<K>(1) << shift) - 1;
     larger = s_scan[33];
+    const int count = s_scan[34];
     if (hi - from > width) hi = from + width;
     lo = from;
+    if (count <= kDirect && lo < hi) {
+      each([&](K key) {
+        if (key >= lo && key <= hi) few[atomicAdd(&s_scan[35], 1)] = key;
+      });
+      __syncthreads();
+      if (static_cast<int>(threadIdx.x) < count) {
+        const K key = few[threadIdx.x];
+        int more = 0, same = 0;
+        for (int i = 0; i < count; ++i) {
+          more += few[i] > key;
+          same += few[i] == key;
+        }
+        if (larger + more < k && larger + more + same >= k) {   // equal keys write the same
+          s_pick[0] = key;
+          s_scan[33] = larger + more;
+        }
+      }
+      __syncthreads();
+      lo = s_pick[0];
+      larger = s_scan[33];
+      break;
+    }
     __syncthreads();
   }
+  __syncthreads();
   *above = larger;
   return lo;
 }
@@ -138,43 +168,97 @@ __device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
 
 // The score of one page for one group, to about 2^-45 of its terms, as an ordered 64-bit key.
 // Whole warp: lane l takes dims 4l .. 4l + 3.  The products of two bf16 are exact in float32; they
-// are added with the rounding errors carried along.
+// are added with the rounding errors carried along.  With more than 16 query rows only those that
+// can hold the maximum are taken that far: a plain float32 score of every row first (a lane a
+// row; off by less than 2^-16 of the terms' sum, within E below), then the rows within 2E (`band`)
+// of the largest.  rough: 256 floats of this warp's own.
 __device__ __forceinline__ unsigned long long exact_score(const SelectParams& p, int b, int s,
-                                                          int kvh, int id) {
+                                                          int kvh, int id, float band,
+                                                          float* rough) {
   const int lane = threadIdx.x & 31;
-  const uint2* row = reinterpret_cast<const uint2*>(p.bounds) +
-                     (static_cast<size_t>(id) * p.Hkv + kvh) * 64 + lane;
-  const uint2 lo = __ldg(row), hi = __ldg(row + 32);
-  unsigned long long best = 0;
-  for (int n = 0; n < p.group * p.G; ++n) {
-    const int i = s * p.group + n / p.G;
-    const uint2 q = __ldg(reinterpret_cast<const uint2*>(p.q) +
-                          ((static_cast<size_t>(b) * p.L + i) * p.Hq + kvh * p.G + n % p.G) * 32 +
-                          lane);
-    const float qv[4] = {bf16_lo(q.x), bf16_hi(q.x), bf16_lo(q.y), bf16_hi(q.y)};
-    const float lv[4] = {bf16_lo(lo.x), bf16_hi(lo.x), bf16_lo(lo.y), bf16_hi(lo.y)};
-    const float hv[4] = {bf16_lo(hi.x), bf16_hi(hi.x), bf16_lo(hi.y), bf16_hi(hi.y)};
-    float a = 0.f, e = 0.f;
+  const uint4* page = reinterpret_cast<const uint4*>(p.bounds) +
+                      (static_cast<size_t>(id) * p.Hkv + kvh) * 32;   // 16 chunks of lo, 16 of hi
+  auto query = [&](int n) {
+    return p.q + ((static_cast<size_t>(b) * p.L + s * p.group + n / p.G) * p.Hq + kvh * p.G +
+                  n % p.G) * 128;
+  };
+  const int rows = p.group * p.G;
+  const bool prune = rows > 16;
+  float least = 0.f;
+  if (prune) {
+    float most = -CUDART_INF_F;
+    for (int n = lane; n - lane < rows; n += 32) {
+      const uint4* q = reinterpret_cast<const uint4*>(query(min(n, rows - 1)));
+      float f = 0.f;
+#pragma unroll 4
+      for (int c = 0; c < 16; ++c) {
+        const uint4 lo = __ldg(page + c), hi = __ldg(page + 16 + c), v = __ldg(q + c);
+        const uint32_t lw[4] = {lo.x, lo.y, lo.z, lo.w}, hw[4] = {hi.x, hi.y, hi.z, hi.w},
+                       qw[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      float r;
-      two_sum(a, __fmul_rn(qv[k], qv[k] > 0.f ? hv[k] : lv[k]), a, r);
-      e = __fadd_rn(e, r);
+        for (int k = 0; k < 4; ++k) {
+          const float q0 = bf16_lo(qw[k]), q1 = bf16_hi(qw[k]);
+          f = fmaf(q0, q0 > 0.f ? bf16_lo(hw[k]) : bf16_lo(lw[k]), f);
+          f = fmaf(q1, q1 > 0.f ? bf16_hi(hw[k]) : bf16_hi(lw[k]), f);
+        }
+      }
+      if (n < rows) rough[n] = f;
+      most = fmaxf(most, f);
     }
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-      const float a2 = __shfl_xor_sync(0xffffffffu, a, off);
-      const float e2 = __shfl_xor_sync(0xffffffffu, e, off);
-      float r;
-      two_sum(a, a2, a, r);
-      e = __fadd_rn(__fadd_rn(e, e2), r);
-    }
-    float top, rest;
-    two_sum(a, e, top, rest);   // normalised: top decides, then rest
-    const unsigned long long key =
-        static_cast<unsigned long long>(order_key(top)) << 32 | order_key(rest);
-    best = key > best ? key : best;
+    for (int off = 16; off > 0; off >>= 1)
+      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+    least = __fadd_rd(most, -band);
+    __syncwarp();
   }
+  const uint2 lo = __ldg(reinterpret_cast<const uint2*>(page) + lane);
+  const uint2 hi = __ldg(reinterpret_cast<const uint2*>(page) + 32 + lane);
+  const float lv[4] = {bf16_lo(lo.x), bf16_hi(lo.x), bf16_lo(lo.y), bf16_hi(lo.y)};
+  const float hv[4] = {bf16_lo(hi.x), bf16_hi(hi.x), bf16_lo(hi.y), bf16_hi(hi.y)};
+  unsigned long long best = 0;
+  constexpr int kRows = 4;   // rows at a time: their loads and shuffles overlap
+  for (int n0 = 0; n0 < rows; n0 += kRows) {
+    if (prune) {
+      bool any = false;
+      for (int n = n0; n < min(n0 + kRows, rows); ++n) any |= rough[n] >= least;
+      if (!any) continue;
+    }
+    float a[kRows], e[kRows];
+    uint2 q[kRows];
+#pragma unroll
+    for (int x = 0; x < kRows; ++x)   // (past the end: the last row again)
+      q[x] = __ldg(reinterpret_cast<const uint2*>(query(min(n0 + x, rows - 1))) + lane);
+#pragma unroll
+    for (int x = 0; x < kRows; ++x) {
+      const float qv[4] = {bf16_lo(q[x].x), bf16_hi(q[x].x), bf16_lo(q[x].y), bf16_hi(q[x].y)};
+      a[x] = e[x] = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float r;
+        two_sum(a[x], __fmul_rn(qv[k], qv[k] > 0.f ? hv[k] : lv[k]), a[x], r);
+        e[x] = __fadd_rn(e[x], r);
+      }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+#pragma unroll
+      for (int x = 0; x < kRows; ++x) {
+        const float a2 = __shfl_xor_sync(0xffffffffu, a[x], off);
+        const float e2 = __shfl_xor_sync(0xffffffffu, e[x], off);
+        float r;
+        two_sum(a[x], a2, a[x], r);
+        e[x] = __fadd_rn(__fadd_rn(e[x], e2), r);
+      }
+#pragma unroll
+    for (int x = 0; x < kRows; ++x) {
+      float top, rest;
+      two_sum(a[x], e[x], top, rest);   // normalised: top decides, then rest
+      const unsigned long long key =
+          static_cast<unsigned long long>(order_key(top)) << 32 | order_key(rest);
+      best = key > best ? key : best;
+    }
+  }
+  __syncwarp();   // rough may be written again
   return best;
 }
 
@@ -182,9 +266,9 @@ __device__ __forceinline__ unsigned long long exact_score(const SelectParams& p,
 // where two of them lie closer than their rounding could explain, float32 does not say which is
 // larger.  So with T the k-th largest and E a bound on a score's error, pages above T + 2E are
 // in, pages below T - 2E are out, and the few between are scored again to about 45 bits.
-//   E = 2^-14 max_n |q_n|_1 max |bound|: a score sums 128 products (and 128 zeros) in 16 MMAs
-//   of 16; each adds at most 17 roundings or truncations of 2^-23 of the largest partial sum, which
-//   is at most |q|_1 max|bound|, so the error is below 16 * 17 * 2^-23 < 2^-14.9 of it.
+//   E = 16 * 17 * 2^-23 max_n |q_n|_1 max |bound|: a score sums 128 products (and 128 zeros) in 16
+//   MMAs of 16, each of which rounds or truncates at most 17 values by 2^-23 of the largest
+//   partial sum, and no partial sum exceeds |q|_1 max|bound|.
 // Latency bound: a few thousand keys, three rounds over shared memory; the launch is one CTA per
 // list, so long batches overlap several per SM.
 __global__ void __launch_bounds__(kSelThreads)
@@ -193,11 +277,12 @@ select_pages_kernel(const SelectParams p) {
   __shared__ int hist[kBuckets];
   __shared__ unsigned long long s_exact[kSelExact];
   __shared__ int s_page[kSelExact];
-  __shared__ int s_scan[34];
+  __shared__ int s_scan[36];
   __shared__ unsigned long long s_wide[64];
   __shared__ unsigned long long s_pick[1];
   __shared__ int s_cand;
   __shared__ float s_f[32];
+  __shared__ float s_rough[kSelThreads / 32][256];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kWarps = kSelThreads / 32;
   const int list = blockIdx.x;
@@ -231,13 +316,45 @@ select_pages_kernel(const SelectParams p) {
   uint32_t* taken = sm + (held ? n : 0);
   const int words = (n + 31) / 32;
   const float* row = p.scores + static_cast<size_t>(list) * p.max_pages;
+  // the first scores, the list's magnitudes and the queries are all asked for before any is used
+  constexpr int kEarly = 8;
+  float early[kEarly];
+#pragma unroll
+  for (int x = 0; x < kEarly; ++x)
+    early[x] = tid + x * kSelThreads < n ? __ldcg(row + tid + x * kSelThreads) : 0.f;
+  // the error bound: the group's largest |q|_1 times the list's largest |bound|
+  float q1 = 0.f, am = 0.f;
+  {
+    const int values = (n + kKeyTile - 1) / kKeyTile * kAmaxPerTile;
+    const float* a = p.amax + (static_cast<size_t>(b) * p.Hkv + kvh) * p.max_tiles * kAmaxPerTile;
+    for (int i = tid; i < values; i += kSelThreads) am = fmaxf(am, __ldcg(a + i));
+  }
+  for (int r = warp; r < p.group * p.G; r += kWarps) {
+    const uint2 q = __ldg(reinterpret_cast<const uint2*>(p.q) +
+                          ((static_cast<size_t>(b) * p.L + s * p.group + r / p.G) * p.Hq +
+                           kvh * p.G + r % p.G) * 32 + lane);
+    float v = fabsf(bf16_lo(q.x)) + fabsf(bf16_hi(q.x)) + fabsf(bf16_lo(q.y)) + fabsf(bf16_hi(q.y));
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    q1 = fmaxf(q1, v);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, off));
+  if (lane == 0) {
+    s_f[warp] = q1;
+    s_f[16 + warp] = am;
+  }
   uint32_t lo = 0xFFFFFFFFu, hi = 0;
-  for (int i = tid; i < n; i += kSelThreads) {
-    const uint32_t key = order_key(__ldcg(row + i));
+  auto take_key = [&](int i, float f) {
+    const uint32_t key = order_key(f);
     if (held) keys[i] = key;
     lo = min(lo, key);
     hi = max(hi, key);
-  }
+  };
+#pragma unroll
+  for (int x = 0; x < kEarly; ++x)
+    if (tid + x * kSelThreads < n) take_key(tid + x * kSelThreads, early[x]);
+  for (int i = tid + kEarly * kSelThreads; i < n; i += kSelThreads) take_key(i, __ldcg(row + i));
   for (int i = tid; i < words; i += kSelThreads) taken[i] = 0;
   if (tid == 0) s_cand = 0;
   block_range(lo, hi, reinterpret_cast<uint32_t*>(s_wide));
@@ -250,35 +367,11 @@ select_pages_kernel(const SelectParams p) {
       },
       hist, s_scan, reinterpret_cast<uint32_t*>(s_pick), &above);
 
-  // the error bound: the group's largest |q|_1 times the list's largest |bound|
-  float q1 = 0.f, am = 0.f;
-  for (int r = warp; r < p.group * p.G; r += kWarps) {
-    const uint2 q = __ldg(reinterpret_cast<const uint2*>(p.q) +
-                          ((static_cast<size_t>(b) * p.L + s * p.group + r / p.G) * p.Hq +
-                           kvh * p.G + r % p.G) * 32 + lane);
-    float v = fabsf(bf16_lo(q.x)) + fabsf(bf16_hi(q.x)) + fabsf(bf16_lo(q.y)) + fabsf(bf16_hi(q.y));
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    q1 = fmaxf(q1, v);
-  }
-  {
-    const int tiles = (n + 127) / 128;
-    const int runs = (tiles + p.tiles_per_item - 1) / p.tiles_per_item;
-    const float* a = p.amax + (static_cast<size_t>(b) * p.Hkv + kvh) * p.items_per_list * 8;
-    for (int i = tid; i < runs * 8; i += kSelThreads) am = fmaxf(am, __ldcg(a + i));
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, off));
-  }
-  if (lane == 0) {
-    s_f[warp] = q1;
-    s_f[16 + warp] = am;
-  }
-  __syncthreads();
   for (int w = 0; w < kWarps; ++w) {
     q1 = fmaxf(q1, s_f[w]);
     am = fmaxf(am, s_f[16 + w]);
   }
-  const float band = q1 * am * 0x1p-13f;   // 2E
+  const float band = q1 * am * (2 * 16 * 17 * 0x1p-23f);   // 2E
   const uint32_t tf = T & 0x80000000u ? T & 0x7FFFFFFFu : ~T;
   const float t = __uint_as_float(tf);
   // (scores or bounds that are not finite have no error bound: their float32 order stands)
@@ -324,7 +417,7 @@ select_pages_kernel(const SelectParams p) {
     for (int c = warp; c < m; c += kWarps) {
       const int id = pt[s_page[c]];
       const unsigned long long e =
-          id >= 0 && id < p.num_pages ? exact_score(p, b, s, kvh, id) : 0ull;
+          id >= 0 && id < p.num_pages ? exact_score(p, b, s, kvh, id, band, s_rough[warp]) : 0ull;
       if (lane == 0) s_exact[c] = e;
     }
     __syncthreads();
@@ -337,23 +430,26 @@ select_pages_kernel(const SelectParams p) {
       if (rank < need) atomicOr(&taken[page >> 5], 1u << (page & 31));
     }
   } else {
-    // more near ties than fit (pages that are copies of each other): the same by counting, the
-    // scores computed again in every round
-    auto each_exact = [&](auto&& f) {
-      for (int i = warp; i < n; i += kWarps) {
-        const uint32_t key = key_at(i);
-        if (key < k_lo || key > k_hi) continue;
-        const int id = pt[i];
-        const unsigned long long e =
-            id >= 0 && id < p.num_pages ? exact_score(p, b, s, kvh, id) : 0ull;
-        if (lane == 0) f(i, e);
-      }
-    };
+    // more near ties than fit (pages that are copies of each other): their scores go to the
+    // workspace, and the need-th largest is found by counting again
+    unsigned long long* exact = p.exact + static_cast<size_t>(list) * p.max_pages;
     unsigned long long elo = ~0ull, ehi = 0;
-    each_exact([&](int, unsigned long long e) {
+    for (int i = warp; i < n; i += kWarps) {
+      const uint32_t key = key_at(i);
+      if (key < k_lo || key > k_hi) continue;
+      const int id = pt[i];
+      const unsigned long long e =
+          id >= 0 && id < p.num_pages ? exact_score(p, b, s, kvh, id, band, s_rough[warp]) : 0ull;
+      if (lane == 0) exact[i] = e;
       elo = e < elo ? e : elo;
       ehi = e > ehi ? e : ehi;
-    });
+    }
+    auto each_exact = [&](auto&& f) {
+      for (int i = tid; i < n; i += kSelThreads) {
+        const uint32_t key = key_at(i);
+        if (key >= k_lo && key <= k_hi) f(i, __ldcg(exact + i));
+      }
+    };
     block_range(elo, ehi, s_wide);
     int larger;
     const unsigned long long TE = kth_largest<unsigned long long>(
@@ -396,22 +492,25 @@ select_pages_kernel(const SelectParams p) {
 }
 
 // ------------------------------------------------------------------ eviction
-constexpr int kEvictThreads = 1024;
+constexpr int kEvictThreads = 512;
+constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kEvictKeys = 22528;   // 88 KB of keys: two CTAs per SM; longer rows are re-read (L2)
 
 // One CTA per (sequence, KV head): the k = keep - recent largest weights before the last `recent`
-// tokens, then one pass in position order that writes the kept positions and moves their weights
-// to the front.  In place is safe: a round's weights are read before the barrier of its scan and
-// written after it, to positions no later than their own, so no later round reads over them.
-// Bound by latency of the counting rounds over shared memory; weights are read once or twice.
-__global__ void __launch_bounds__(kEvictThreads)
+// tokens, then the kept positions in order: each warp counts what its stretch of the row keeps, a
+// sum over the warps says where its stretch begins, and it walks the stretch again, writing, with
+// no barrier in between.  Weights go to another array on the way; in place they move afterwards, a
+// round of positions at a time, all reads before the round's barrier and all writes after it: a
+// token never moves to a later position, so no round reads what an earlier one wrote.
+// Bound by the latency of its passes over a few ten thousand keys in shared memory.
+__global__ void __launch_bounds__(kEvictThreads, 2)
 evict_select_kernel(const EvictParams p) {
   extern __shared__ uint32_t sm[];
   __shared__ int hist[kBuckets];
-  __shared__ int s_scan[34];
+  __shared__ int s_scan[36];
   __shared__ uint32_t s_range[64];
   __shared__ uint32_t s_pick[1];
-  __shared__ int s_cnt[2][32];
+  __shared__ int s_gt[kEvictWarps], s_eq[kEvictWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / p.Hkv, kvh = blockIdx.x - b * p.Hkv;
   griddep_wait();
@@ -428,25 +527,35 @@ evict_select_kernel(const EvictParams p) {
   if (bad) return;
   const float* w = p.weights + blockIdx.x * stride;
   float* to = p.to_weights + blockIdx.x * stride;
+  const bool in_place = to == w;
   if (n <= p.keep) {
     for (int i = tid; i < n; i += kEvictThreads) {
       kept[i] = i;
-      if (to != w) to[i] = w[i];
+      if (!in_place) to[i] = w[i];
     }
     return;
   }
   const int cand = n - p.recent, k = p.keep - p.recent;   // k < cand
   const bool held = cand <= kEvictKeys;
-  uint32_t T = 0xFFFFFFFFu;
+  uint32_t T = 0;
   int above = 0;
   auto key_at = [&](int i) { return held ? sm[i] : order_key(__ldcg(w + i)); };
   if (k > 0) {
     uint32_t lo = 0xFFFFFFFFu, hi = 0;
-    for (int i = tid; i < cand; i += kEvictThreads) {
-      const uint32_t key = order_key(__ldcg(w + i));
-      if (held) sm[i] = key;
-      lo = min(lo, key);
-      hi = max(hi, key);
+    constexpr int kBatch = 8;   // loads in flight per thread
+    for (int i0 = tid; i0 < cand; i0 += kBatch * kEvictThreads) {
+      float f[kBatch];
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x)
+        if (i0 + x * kEvictThreads < cand) f[x] = __ldcg(w + i0 + x * kEvictThreads);
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) {
+        if (i0 + x * kEvictThreads >= cand) break;
+        const uint32_t key = order_key(f[x]);
+        if (held) sm[i0 + x * kEvictThreads] = key;
+        lo = min(lo, key);
+        hi = max(hi, key);
+      }
     }
     block_range(lo, hi, s_range);
     T = kth_largest<uint32_t>(
@@ -457,39 +566,65 @@ evict_select_kernel(const EvictParams p) {
         hist, s_scan, s_pick, &above);
   }
   const int ties = k - above;   // tokens of weight T that stay
-  int n_gt = 0, n_eq = 0;       // larger and equal ones before this round
-  for (int i0 = 0; i0 < n; i0 += kEvictThreads) {
-    const int i = i0 + tid;
-    const bool late = i >= cand && i < n;
-    const uint32_t key = k > 0 && i < cand ? key_at(i) : 0;
-    const bool gt = late || (k > 0 && i < cand && key > T);
-    const bool eq = k > 0 && i < cand && key == T;
-    const float v = i < n ? __ldcg(w + i) : 0.f;
+  // this warp's stretch: what it keeps for sure (g) and what equals T (e)
+  const int stretch = ((n + kEvictWarps - 1) / kEvictWarps + 31) & ~31;
+  const int s0 = warp * stretch, s1 = min(n, s0 + stretch);
+  auto look = [&](int i, bool& gt, bool& eq) {
+    gt = i < n && i >= cand;
+    eq = false;
+    if (k > 0 && i < cand) {
+      const uint32_t key = key_at(i);
+      gt = key > T;
+      eq = key == T;
+    }
+  };
+  int g = 0, e = 0;
+  for (int i = s0 + lane; i - lane < s1; i += 32) {
+    bool gt, eq;
+    look(i, gt, eq);
+    g += __popc(__ballot_sync(0xffffffffu, gt));
+    e += __popc(__ballot_sync(0xffffffffu, eq));
+  }
+  if (lane == 0) {
+    s_gt[warp] = g;
+    s_eq[warp] = e;
+  }
+  __syncthreads();
+  g = e = 0;
+  for (int x = 0; x < warp; ++x) {
+    g += s_gt[x];
+    e += s_eq[x];
+  }
+  const uint32_t below = (1u << lane) - 1u;
+  for (int i = s0 + lane; i - lane < s1; i += 32) {
+    bool gt, eq;
+    look(i, gt, eq);
     const uint32_t bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
-    if (lane == 0) {
-      s_cnt[0][warp] = __popc(bg);
-      s_cnt[1][warp] = __popc(be);
-    }
-    __syncthreads();
-    int g = n_gt, e = n_eq;
-    for (int x = 0; x < kEvictThreads / 32; ++x) {
-      const int cg = s_cnt[0][x], ce = s_cnt[1][x];
-      if (x < warp) {
-        g += cg;
-        e += ce;
-      }
-      n_gt += cg;
-      n_eq += ce;
-    }
-    const uint32_t below = (1u << lane) - 1u;
-    g += __popc(bg & below);
-    e += __popc(be & below);
-    if (gt || (eq && e < ties)) {
-      const int at = g + min(e, ties);
+    const int eq_before = e + __popc(be & below);
+    if (gt || (eq && eq_before < ties)) {
+      const int at = g + __popc(bg & below) + min(eq_before, ties);
       kept[at] = i;
-      to[at] = v;
+      if (!in_place) to[at] = __ldcg(w + i);
+    }
+    g += __popc(bg);
+    e += __popc(be);
+  }
+  if (!in_place) return;
+  __syncthreads();
+  constexpr int kRound = 4;
+  for (int j0 = 0; j0 < p.keep; j0 += kRound * kEvictThreads) {
+    float v[kRound];
+#pragma unroll
+    for (int x = 0; x < kRound; ++x) {
+      const int j = j0 + x * kEvictThreads + tid;
+      if (j < p.keep) v[x] = __ldcg(w + __ldcg(kept + j));
     }
     __syncthreads();
+#pragma unroll
+    for (int x = 0; x < kRound; ++x) {
+      const int j = j0 + x * kEvictThreads + tid;
+      if (j < p.keep) to[j] = v[x];
+    }
   }
 }
 
