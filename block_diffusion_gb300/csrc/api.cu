@@ -410,9 +410,11 @@ int attention_impl(DeviceState* st, const bdlm_attn_desc& d, const bdlm_bf16* q,
                    const bdlm::AttnExt* ext) {
   int rc = get_encoder();
   if (rc) return rc;
-  const AttnPlan plan = bdlm::plan_attention(d.B, d.L, d.Hq, d.Hkv, d.max_pages_per_seq,
-                                             d.page_size, st->num_sms);
+  AttnPlan plan = bdlm::plan_attention(d.B, d.L, d.Hq, d.Hkv, d.max_pages_per_seq, d.page_size,
+                                       st->num_sms);
   if (plan.n_mma == 0) return BDLM_ERR_UNSUPPORTED;
+  if (ext && ext->head_tables)
+    bdlm::plan_even_lists(plan, d.B, d.Hkv, d.max_pages_per_seq, st->num_sms);
   rc = ensure(reinterpret_cast<void**>(&st->attn_cnt), &st->attn_cnt_cap, plan.cnt_bytes, true,
               stream);
   if (rc) return rc;

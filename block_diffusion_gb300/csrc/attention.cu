@@ -111,6 +111,8 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
   constexpr int kPBufs = 2;
   constexpr uint32_t kQCol = 384;   // first tensor-memory column of Q (kQTmem)
   __shared__ unsigned long long s_seen[EXT ? kItemRing : 1];   // block tokens some query sees
+  // EXT, rows on N: the visibility words of the item's queries (at most 32 rows)
+  __shared__ unsigned long long s_words[EXT && !ROWS ? kItemRing : 1][EXT && !ROWS ? 32 : 1];
   static_assert(!EXT || !MASKED, "tree visibility and block-causal prefill are separate");
   static_assert(!MASKED || ROWS, "the block-causal mask is applied by the row-per-thread softmax");
   static_assert(!ROWS || N == 128, "rows on M: one UMMA of 128 query rows");
@@ -195,16 +197,32 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
     // Publishes `it` to the item ring (lane 0).
     auto publish = [&](const Item& it, unsigned long long seen = 0) {
       const int rs = seq % kItemRing;
-      if (ok) ok = mbar_wait<ROWS>(&bar_iempty[rs], ((seq / kItemRing) & 1) ^ 1, &abort_flag);
+      // (with the queries' words to write, the whole warp has waited already)
+      if constexpr (!EXT || ROWS)
+        if (ok) ok = mbar_wait<ROWS>(&bar_iempty[rs], ((seq / kItemRing) & 1) ^ 1, &abort_flag);
       s_item[rs] = it;
       if constexpr (EXT) s_seen[rs] = seen;
       mbar_arrive(&bar_ifull[rs]);
+    };
+    // EXT, rows on N: waits for the item's ring slot with the whole warp and writes this lane's
+    // word of it (rows on N: at most 32 queries)
+    auto words = [&](unsigned long long m) {
+      if constexpr (EXT && !ROWS) {
+        const int rs = seq % kItemRing;
+        if (ok)
+          ok = mbar_wait_warp<ROWS>(&bar_iempty[rs], ((seq / kItemRing) & 1) ^ 1, &abort_flag);
+        s_words[rs][lane] = m;
+        __syncwarp();
+      }
     };
     // Takes the next non-empty item from the global counter, publishes it to the item ring
     // and loads its page ids (whole warp).  When the work is done it publishes the end marker
     // at once (the MMA warp needs it before it can finish the current item) and returns false.
     bool first = true;
     auto grab = [&](Item& it) -> bool {
+      bool spec = false;
+      int early = -1;
+      unsigned long long word = 0;
       while (true) {
         // the first item is the CTA's own number; later ones come from the counter, unless no
         // item is left past the first ones (a small problem pays for no atomics)
@@ -216,9 +234,11 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             idx = __shfl_sync(0xffffffffu, idx, 0);
           }
         }
+        spec = first && p.order == nullptr;
         first = false;
         if (idx >= p.total_items) {
           ++seq;
+          words(0);
           if (lane == 0) {
             Item e{};
             e.end = 1;
@@ -226,6 +246,24 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
           }
           ok = __shfl_sync(0xffffffffu, ok, 0);
           return false;
+        }
+        if constexpr (!ROWS) {
+          // rows on N cut sequences at fixed places, so the first item's page ids (and its queries'
+          // words) can be asked for before its sequence's length is known; later items are taken
+          // ahead of their use
+          if (spec) {
+            const int kvh = idx / p.row_groups % p.Hkv, bs = idx / p.row_groups / p.Hkv;
+            const int b = bs % p.B, at = bs / p.B * (p.split_tokens / kPage) + lane;
+            early = at < p.max_pages
+                        ? __ldg(p.page_table +
+                                (static_cast<size_t>(b / p.table_div) * p.table_heads +
+                                 (p.table_heads > 1 ? kvh : 0)) * p.max_pages + at)
+                        : -1;
+            if constexpr (EXT)
+              word = p.tree_mask != nullptr && lane < p.L
+                         ? __ldg(p.tree_mask + static_cast<size_t>(b) * p.L + lane)
+                         : 0;
+          }
         }
         if (decode_item(idx, p, it)) break;
       }
@@ -238,7 +276,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       const int np = (it.t_end - it.t_begin + kPage - 1) / kPage;
       int bad = 0;
       for (int q = lane; q < np; q += 32) {
-        int id = pt[q];
+        int id = !ROWS && q == lane && spec ? early : pt[q];
         if (id < 0 || id >= p.num_pages) {
           bad = 1;
           id = -1;
@@ -282,14 +320,20 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
       }
       unsigned long long seen = ~0ull;
       if constexpr (EXT) {
+        unsigned long long m = ~0ull;
         if (p.tree_mask != nullptr && it.t_end > it.q0) {
-          unsigned long long m = 0;
-          for (int i = lane; i < p.L; i += 32)
-            m |= __ldg(p.tree_mask + static_cast<size_t>(it.b) * p.L + i);
+          m = 0;
+          if (!ROWS && spec) {
+            m = word;
+          } else {
+            for (int i = lane; i < p.L; i += 32)
+              m |= __ldg(p.tree_mask + static_cast<size_t>(it.b) * p.L + i);
+          }
           seen = static_cast<unsigned long long>(
                      __reduce_or_sync(0xffffffffu, static_cast<unsigned>(m >> 32))) << 32 |
                  __reduce_or_sync(0xffffffffu, static_cast<unsigned>(m));
         }
+        words(m);
       }
       if (lane == 0) publish(it, seen);
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -1175,10 +1219,10 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
           const int key = it.t_begin + j * kTile + x;
           if (key >= it.t_end) return 0;
           if (key < it.q0 || p.tree_mask == nullptr) return ~0u;
-          const unsigned long long* m = p.tree_mask + static_cast<size_t>(it.b) * p.L;
           uint32_t w = 0;
           for (int i = 0; i < p.L; ++i)   // at most 32 rows: one row group, row i * G + g
-            if ((__ldg(m + i) >> (key - it.q0)) & 1) w |= ((1u << p.G) - 1) << (i * p.G);
+            if ((s_words[EXT && !ROWS ? rs : 0][EXT && !ROWS ? i : 0] >> (key - it.q0)) & 1)
+              w |= ((1u << p.G) - 1) << (i * p.G);
           return w;
         };
         // phase A: exact column maxima over the chunk
@@ -1338,14 +1382,27 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
           for (int n = 0; n < N; ++n) s_red[q4][n] = l[n];
         }
         named_barrier(1, kSoftmaxThreads);
-        if (x < N) s_l[x] = (s_red[0][x] + s_red[1][x]) + (s_red[2][x] + s_red[3][x]);
-        named_barrier(1, kSoftmaxThreads);
         const size_t head_base = static_cast<size_t>(it.kvh) * p.G;
-        if constexpr (EXT)
-          if (p.lse != nullptr && it.n_splits == 1 && x < rows && x / p.G < p.L)
-            p.lse[(static_cast<size_t>(it.b) * p.L + x / p.G) * p.Hq + head_base + x % p.G] =
-                row_lse(s_m[x], s_l[x], cs);
+        if (x < N) {
+          const float sum = (s_red[0][x] + s_red[1][x]) + (s_red[2][x] + s_red[3][x]);
+          s_l[x] = sum;
+          if constexpr (EXT) {
+            if (it.n_splits == 1) {
+              if (p.lse != nullptr && x < rows && x / p.G < p.L)
+                p.lse[(static_cast<size_t>(it.b) * p.L + x / p.G) * p.Hq + head_base + x % p.G] =
+                    row_lse(s_m[x], sum, cs);
+              // the factor of the row; a row that saw nothing has O = 0, and gets 0
+              s_l[x] = sum > 0.f ? 1.f / sum : 0.f;
+            }
+          }
+        }
+        named_barrier(1, kSoftmaxThreads);
         if (it.n_splits == 1) {
+          // row n is query i, head g of the KV head: counted along, a division a row costs more
+          // than its store
+          int i = it.rg * p.lsub, g = 0;
+          uint16_t* o = p.out + ((static_cast<size_t>(it.b) * p.L + i) * p.Hq + head_base) * 128 + x;
+          const size_t next = static_cast<size_t>(p.Hq - p.G) * 128;   // past the other KV heads
 #pragma unroll
           for (int cg = 0; cg < N / 16; ++cg) {
             uint32_t r[16];
@@ -1355,14 +1412,16 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
               const int n = cg * 16 + k;
-              if (n >= rows) continue;
-              const int i = it.rg * p.lsub + n / p.G;
-              if (i >= p.L) continue;
-              const size_t o =
-                  ((static_cast<size_t>(it.b) * p.L + i) * p.Hq + head_base + n % p.G) * 128 + x;
-              const float ov = __uint_as_float(r[k]);
-              p.out[o] = __bfloat16_as_ushort(
-                  __float2bfloat16_rn(EXT && !(s_l[n] > 0.f) ? 0.f : ov / s_l[n]));
+              if (n < rows && i < p.L) {
+                const float ov = __uint_as_float(r[k]);
+                *o = __bfloat16_as_ushort(__float2bfloat16_rn(EXT ? ov * s_l[n] : ov / s_l[n]));
+              }
+              o += 128;
+              if (++g == p.G) {
+                g = 0;
+                ++i;
+                o += next;
+              }
             }
           }
         } else {
@@ -1736,6 +1795,24 @@ AttnPlan plan_attention(int B, int L, int Hq, int Hkv, int max_pages, int page_s
   }
   pl.cnt_bytes = 2 * sizeof(int);  // the scheduler's next-item and finished-CTA counters
   return pl;
+}
+
+// Shorter splits where the lists (page selections, as long as their tables) are fewer than half the
+// CTAs: the shortest that give every CTA at most one item.  32 lists of 34 pages: 13.4 us in splits
+// of 128, 14.4 us unsplit.  With more lists the usual splits stay: 512 lists of 258 pages took 157 us
+// in splits of 896 and 167 us in splits of 640.
+void plan_even_lists(AttnPlan& pl, int B, int Hkv, int max_pages, int num_sms) {
+  if (pl.whole || pl.n_mma > 32) return;
+  const long long tokens = static_cast<long long>(max_pages) * kPage;
+  const long long groups = static_cast<long long>(B) * Hkv * pl.row_groups;
+  const long long ctas = 2ll * num_sms;
+  if (2 * groups * pl.max_splits > ctas) return;
+  while (pl.split_tokens > kTile &&
+         groups * ((tokens + pl.split_tokens - kTile - 1) / (pl.split_tokens - kTile)) <= ctas)
+    pl.split_tokens -= kTile;
+  pl.max_splits = static_cast<int>((tokens + pl.split_tokens - 1) / pl.split_tokens);
+  pl.part_bytes =
+      static_cast<size_t>(groups) * pl.max_splits * static_cast<size_t>(pl.n_mma) * 130 * sizeof(float);
 }
 
 cudaError_t launch_attention(const CUtensorMap& tm_q, const CUtensorMap& tm_k,

@@ -15,6 +15,8 @@ struct AttnExt {
   bool head_tables = false;              // page_table holds a row per (sequence, KV head)
 };
 
+// Adapts a plan to lists that fill their tables (page selections).
+void plan_even_lists(AttnPlan& pl, int B, int Hkv, int max_pages, int num_sms);
 cudaError_t launch_attention_ext(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                                  const CUtensorMap& tm_v, const int32_t* page_table,
                                  const int32_t* prefix_lens, uint16_t* out, int B, int L, int Hq,

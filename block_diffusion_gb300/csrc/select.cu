@@ -46,11 +46,9 @@ struct BlockSum {   // sums and scans over the CTA; s: one word per warp
     __syncthreads();
     if (lane == 31) s[warp] = x;
     __syncthreads();
-    int before = 0, all = 0;
-    for (int w = 0; w < warps; ++w) {
-      if (w < warp) before += s[w];
-      all += s[w];
-    }
+    const int w = lane < warps ? s[lane] : 0;
+    const int before = __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
+    const int all = __reduce_add_sync(0xffffffffu, w);
     *total = all;
     return before + x - v;
   }
@@ -77,6 +75,32 @@ __device__ __forceinline__ void block_range(T& lo, T& hi, T* s) {
     hi = s[32 + w] > hi ? s[32 + w] : hi;
   }
   __syncthreads();
+}
+
+// The same by ranking `count` <= kDirect keys, listed in `few`, against each other (after a
+// barrier).  Whole CTA.
+template <typename K>
+__device__ __forceinline__ K kth_of_few(int k, const K* few, int count, int* s_scan, K* s_pick,
+                                        int* above) {
+  if (static_cast<int>(threadIdx.x) < count) {
+    const K key = few[threadIdx.x];
+    int more = 0, same = 0;
+#pragma unroll 4
+    for (int i = 0; i < count; ++i) {
+      const K other = few[i];
+      more += other > key;
+      same += other == key;
+    }
+    if (more < k && more + same >= k) {   // equal keys write the same
+      s_pick[0] = key;
+      s_scan[33] = more;
+    }
+  }
+  __syncthreads();
+  const K kth = s_pick[0];
+  *above = s_scan[33];
+  __syncthreads();
+  return kth;
 }
 
 // The k-th largest of the keys that `each` yields (each(f): calls f(key) for this thread's share,
@@ -130,21 +154,9 @@ __device__ __forceinline__ K kth_largest(int k, K lo, K hi, Each&& each, int* hi
         if (key >= lo && key <= hi) few[atomicAdd(&s_scan[35], 1)] = key;
       });
       __syncthreads();
-      if (static_cast<int>(threadIdx.x) < count) {
-        const K key = few[threadIdx.x];
-        int more = 0, same = 0;
-        for (int i = 0; i < count; ++i) {
-          more += few[i] > key;
-          same += few[i] == key;
-        }
-        if (larger + more < k && larger + more + same >= k) {   // equal keys write the same
-          s_pick[0] = key;
-          s_scan[33] = larger + more;
-        }
-      }
-      __syncthreads();
-      lo = s_pick[0];
-      larger = s_scan[33];
+      int more;
+      lo = kth_of_few(k - larger, few, count, s_scan, s_pick, &more);
+      larger += more;
       break;
     }
     __syncthreads();
@@ -166,15 +178,16 @@ __device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
   e = __fadd_rn(__fadd_rn(a, -__fadd_rn(s, -bb)), __fadd_rn(b, -bb));
 }
 
-// The score of one page for one group, to about 2^-45 of its terms, as an ordered 64-bit key.
+// The largest score of one page over query rows row0 .. rows - 1 of one group, to about 2^-45 of its
+// terms, as an ordered 64-bit key (never 0 or 1).
 // Whole warp: lane l takes dims 4l .. 4l + 3.  The products of two bf16 are exact in float32; they
 // are added with the rounding errors carried along.  With more than 16 query rows only those that
 // can hold the maximum are taken that far: a plain float32 score of every row first (a lane a
 // row; off by less than 2^-16 of the terms' sum, within E below), then the rows within 2E (`band`)
 // of the largest.  rough: 256 floats of this warp's own.
 __device__ __forceinline__ unsigned long long exact_score(const SelectParams& p, int b, int s,
-                                                          int kvh, int id, float band,
-                                                          float* rough) {
+                                                          int kvh, int id, int row0, int rows,
+                                                          float band, float* rough) {
   const int lane = threadIdx.x & 31;
   const uint4* page = reinterpret_cast<const uint4*>(p.bounds) +
                       (static_cast<size_t>(id) * p.Hkv + kvh) * 32;   // 16 chunks of lo, 16 of hi
@@ -182,8 +195,7 @@ __device__ __forceinline__ unsigned long long exact_score(const SelectParams& p,
     return p.q + ((static_cast<size_t>(b) * p.L + s * p.group + n / p.G) * p.Hq + kvh * p.G +
                   n % p.G) * 128;
   };
-  const int rows = p.group * p.G;
-  const bool prune = rows > 16;
+  const bool prune = rows - row0 > 16;   // row0 = 0 then
   float least = 0.f;
   if (prune) {
     float most = -CUDART_INF_F;
@@ -217,7 +229,7 @@ __device__ __forceinline__ unsigned long long exact_score(const SelectParams& p,
   const float hv[4] = {bf16_lo(hi.x), bf16_hi(hi.x), bf16_lo(hi.y), bf16_hi(hi.y)};
   unsigned long long best = 0;
   constexpr int kRows = 4;   // rows at a time: their loads and shuffles overlap
-  for (int n0 = 0; n0 < rows; n0 += kRows) {
+  for (int n0 = row0; n0 < rows; n0 += kRows) {
     if (prune) {
       bool any = false;
       for (int n = n0; n < min(n0 + kRows, rows); ++n) any |= rough[n] >= least;
@@ -269,8 +281,9 @@ __device__ __forceinline__ unsigned long long exact_score(const SelectParams& p,
 //   E = 16 * 17 * 2^-23 max_n |q_n|_1 max |bound|: a score sums 128 products (and 128 zeros) in 16
 //   MMAs of 16, each of which rounds or truncates at most 17 values by 2^-23 of the largest
 //   partial sum, and no partial sum exceeds |q|_1 max|bound|.
-// Latency bound: a few thousand keys, three rounds over shared memory; the launch is one CTA per
-// list, so long batches overlap several per SM.
+// Bound by latency: a dozen barriers and half a dozen loads that depend on each other.  So what can
+// be asked for early is, a thread keeps its first eight keys in registers, and the exact scores
+// of one page are spread over warps.
 __global__ void __launch_bounds__(kSelThreads)
 select_pages_kernel(const SelectParams p) {
   extern __shared__ uint32_t sm[];
@@ -310,20 +323,14 @@ select_pages_kernel(const SelectParams p) {
   }
   if (k == 0) return;
 
-  // keys, in shared memory when they fit; the page bitmap follows them
-  uint32_t* keys = sm;
-  const bool held = n <= kSelKeys;
-  uint32_t* taken = sm + (held ? n : 0);
-  const int words = (n + 31) / 32;
+  // ---- keys, magnitudes and queries: all asked for before any is used
   const float* row = p.scores + static_cast<size_t>(list) * p.max_pages;
-  // the first scores, the list's magnitudes and the queries are all asked for before any is used
-  constexpr int kEarly = 8;
-  float early[kEarly];
+  constexpr int kOwn = 8;   // keys of a thread in registers: kOwn * kSelThreads of the row
+  float early[kOwn];
 #pragma unroll
-  for (int x = 0; x < kEarly; ++x)
+  for (int x = 0; x < kOwn; ++x)
     early[x] = tid + x * kSelThreads < n ? __ldcg(row + tid + x * kSelThreads) : 0.f;
-  // the error bound: the group's largest |q|_1 times the list's largest |bound|
-  float q1 = 0.f, am = 0.f;
+  float q1 = 0.f, am = 0.f;   // the group's largest |q|_1, the list's largest |bound|
   {
     const int values = (n + kKeyTile - 1) / kKeyTile * kAmaxPerTile;
     const float* a = p.amax + (static_cast<size_t>(b) * p.Hkv + kvh) * p.max_tiles * kAmaxPerTile;
@@ -344,81 +351,98 @@ select_pages_kernel(const SelectParams p) {
     s_f[warp] = q1;
     s_f[16 + warp] = am;
   }
+  // keys past the registers' share: in shared memory when they fit, else read again each time; the
+  // page bitmap and a second one follow them
+  uint32_t own[kOwn];
+  const bool held = n <= kSelKeys;
+  uint32_t* taken = sm + (held && n > kOwn * kSelThreads ? n : 0);
+  const int words = (n + 31) / 32;
+  uint32_t* second = taken + words;
   uint32_t lo = 0xFFFFFFFFu, hi = 0;
-  auto take_key = [&](int i, float f) {
-    const uint32_t key = order_key(f);
-    if (held) keys[i] = key;
+#pragma unroll
+  for (int x = 0; x < kOwn; ++x) {
+    own[x] = order_key(early[x]);
+    if (tid + x * kSelThreads >= n) continue;
+    lo = min(lo, own[x]);
+    hi = max(hi, own[x]);
+  }
+  for (int i = tid + kOwn * kSelThreads; i < n; i += kSelThreads) {
+    const uint32_t key = order_key(__ldcg(row + i));
+    if (held) sm[i] = key;
     lo = min(lo, key);
     hi = max(hi, key);
-  };
-#pragma unroll
-  for (int x = 0; x < kEarly; ++x)
-    if (tid + x * kSelThreads < n) take_key(tid + x * kSelThreads, early[x]);
-  for (int i = tid + kEarly * kSelThreads; i < n; i += kSelThreads) take_key(i, __ldcg(row + i));
+  }
   for (int i = tid; i < words; i += kSelThreads) taken[i] = 0;
   if (tid == 0) s_cand = 0;
-  block_range(lo, hi, reinterpret_cast<uint32_t*>(s_wide));
-  auto key_at = [&](int i) { return held ? keys[i] : order_key(__ldcg(row + i)); };
-  int above;
-  const uint32_t T = kth_largest<uint32_t>(
-      k, lo, hi,
-      [&](auto&& f) {
-        for (int i = tid; i < n; i += kSelThreads) f(key_at(i));
-      },
-      hist, s_scan, reinterpret_cast<uint32_t*>(s_pick), &above);
+  // f(i, key) for this thread's keys
+  auto each_key = [&](auto&& f) {
+#pragma unroll
+    for (int x = 0; x < kOwn; ++x)
+      if (tid + x * kSelThreads < n) f(tid + x * kSelThreads, own[x]);
+    for (int i = tid + kOwn * kSelThreads; i < n; i += kSelThreads)
+      f(i, held ? sm[i] : order_key(__ldcg(row + i)));
+  };
 
+  // ---- T, the k-th largest
+  int above;
+  uint32_t T;
+  uint32_t* pick = reinterpret_cast<uint32_t*>(s_pick);
+  if (n <= kDirect) {
+    uint32_t* few = reinterpret_cast<uint32_t*>(hist);
+    each_key([&](int i, uint32_t key) { few[i] = key; });
+    __syncthreads();
+    T = kth_of_few<uint32_t>(k, few, n, s_scan, pick, &above);
+  } else {
+    block_range(lo, hi, reinterpret_cast<uint32_t*>(s_wide));
+    T = kth_largest<uint32_t>(
+        k, lo, hi, [&](auto&& f) { each_key([&](int, uint32_t key) { f(key); }); }, hist, s_scan,
+        pick, &above);
+  }
+
+  // ---- the band around T
+  q1 = am = 0.f;
   for (int w = 0; w < kWarps; ++w) {
     q1 = fmaxf(q1, s_f[w]);
     am = fmaxf(am, s_f[16 + w]);
   }
   const float band = q1 * am * (2 * 16 * 17 * 0x1p-23f);   // 2E
-  const uint32_t tf = T & 0x80000000u ? T & 0x7FFFFFFFu : ~T;
-  const float t = __uint_as_float(tf);
+  const float t = __uint_as_float(T & 0x80000000u ? T & 0x7FFFFFFFu : ~T);
   // (scores or bounds that are not finite have no error bound: their float32 order stands)
   const bool refine = T != 0 && band <= 3e38f && fabsf(t) <= 3e38f;
   const uint32_t k_hi = refine ? order_key(__fadd_ru(t, band)) : T;
   const uint32_t k_lo = refine ? order_key(__fadd_rd(t, -band)) : T;
-
-  // pages above the band are in; pages in it are candidates for the rest
+  auto take = [&](int i) { atomicOr(&taken[i >> 5], 1u << (i & 31)); };
   int sure = 0;
-  for (int i = tid; i < words * 32; i += kSelThreads) {
-    const uint32_t key = i < n ? key_at(i) : 0;
-    const bool in = i < n && key > k_hi;
-    const uint32_t bits = __ballot_sync(0xffffffffu, in);
-    if (lane == 0) taken[i >> 5] = bits;
-    sure += in;
-    if (i < n && !in && key >= k_lo) {
+  each_key([&](int i, uint32_t key) {
+    if (key > k_hi) {
+      take(i);
+      ++sure;
+    } else if (key >= k_lo) {
       const int c = atomicAdd(&s_cand, 1);
-      if (c < kSelExact) s_page[c] = i;
+      if (c < kSelExact) {
+        s_page[c] = i;
+        s_exact[c] = 0;
+      }
     }
-  }
+  });
   BlockSum sum{s_scan};
   int n_sure;
   sum.exclusive(sure, &n_sure);
-  __syncthreads();
-  const int m = s_cand, need = k - n_sure;   // 1 <= need <= m
+  const int m = s_cand, need = k - n_sure;   // candidates, and how many of them are in (>= 1)
   if (m == need) {
-    for (int i = tid; i < n; i += kSelThreads) {
-      const uint32_t key = key_at(i);
-      if (key >= k_lo && key <= k_hi) atomicOr(&taken[i >> 5], 1u << (i & 31));
-    }
-  } else if (!refine) {
-    // equal keys (or not finite): the lowest positions
-    int base = 0;
-    for (int i0 = 0; i0 < n; i0 += kSelThreads) {
-      const int i = i0 + tid;
-      const bool c = i < n && key_at(i) == T;
-      int total;
-      const int before = base + sum.exclusive(c, &total);
-      if (c && before < need) atomicOr(&taken[i >> 5], 1u << (i & 31));
-      base += total;
-    }
-  } else if (m <= kSelExact) {
-    for (int c = warp; c < m; c += kWarps) {
-      const int id = pt[s_page[c]];
-      const unsigned long long e =
-          id >= 0 && id < p.num_pages ? exact_score(p, b, s, kvh, id, band, s_rough[warp]) : 0ull;
-      if (lane == 0) s_exact[c] = e;
+    each_key([&](int i, uint32_t key) {
+      if (key >= k_lo && key <= k_hi) take(i);
+    });
+  } else if (refine && m <= kSelExact) {
+    // rows of a candidate in batches, a warp each (all rows where they are pruned together); the
+    // maximum over the batches does not depend on their order
+    const int rows = p.group * p.G, per = rows > 16 ? rows : 4, parts = (rows + per - 1) / per;
+    for (int x = warp; x < m * parts; x += kWarps) {
+      const int c = x / parts, id = pt[s_page[c]];
+      if (id < 0 || id >= p.num_pages) continue;
+      const unsigned long long e = exact_score(p, b, s, kvh, id, x % parts * per,
+                                               min(rows, x % parts * per + per), band, s_rough[warp]);
+      if (lane == 0) atomicMax(&s_exact[c], e);
     }
     __syncthreads();
     for (int c = tid; c < m; c += kSelThreads) {
@@ -427,67 +451,82 @@ select_pages_kernel(const SelectParams p) {
       int rank = 0;   // candidates ahead of this one
       for (int j = 0; j < m; ++j)
         rank += s_exact[j] > e || (s_exact[j] == e && s_page[j] < page);
-      if (rank < need) atomicOr(&taken[page >> 5], 1u << (page & 31));
+      if (rank < need) take(page);
     }
   } else {
-    // more near ties than fit (pages that are copies of each other): their scores go to the
-    // workspace, and the need-th largest is found by counting again
-    unsigned long long* exact = p.exact + static_cast<size_t>(list) * p.max_pages;
-    unsigned long long elo = ~0ull, ehi = 0;
-    for (int i = warp; i < n; i += kWarps) {
-      const uint32_t key = key_at(i);
-      if (key < k_lo || key > k_hi) continue;
-      const int id = pt[i];
-      const unsigned long long e =
-          id >= 0 && id < p.num_pages ? exact_score(p, b, s, kvh, id, band, s_rough[warp]) : 0ull;
-      if (lane == 0) exact[i] = e;
-      elo = e < elo ? e : elo;
-      ehi = e > ehi ? e : ehi;
-    }
-    auto each_exact = [&](auto&& f) {
-      for (int i = tid; i < n; i += kSelThreads) {
-        const uint32_t key = key_at(i);
-        if (key >= k_lo && key <= k_hi) f(i, __ldcg(exact + i));
+    // many near ties (pages that are copies of each other): their exact scores go to the
+    // workspace, and the need-th largest is found by counting again.  Of those equal to it (or
+    // of the keys equal to T, where there is no refining) the lowest positions are in.
+    int equal = need;
+    for (int i = tid; i < words; i += kSelThreads) second[i] = 0;
+    if (refine) {
+      unsigned long long* exact = p.exact + static_cast<size_t>(list) * p.max_pages;
+      each_key([&](int i, uint32_t key) { exact[i] = key >= k_lo && key <= k_hi ? 1 : 0; });
+      __syncthreads();
+      unsigned long long elo = ~0ull, ehi = 0;
+      for (int i = warp; i < n; i += kWarps) {
+        if (__ldcg(exact + i) == 0) continue;
+        const int id = pt[i];
+        unsigned long long e = 1;   // a bad page: below every score
+        if (id >= 0 && id < p.num_pages)
+          e = exact_score(p, b, s, kvh, id, 0, p.group * p.G, band, s_rough[warp]);
+        __syncwarp();
+        if (lane == 0) exact[i] = e;
+        elo = e < elo ? e : elo;
+        ehi = e > ehi ? e : ehi;
       }
-    };
-    block_range(elo, ehi, s_wide);
-    int larger;
-    const unsigned long long TE = kth_largest<unsigned long long>(
-        need, elo, ehi,
-        [&](auto&& f) { each_exact([&](int, unsigned long long e) { f(e); }); }, hist, s_scan,
-        s_pick, &larger);
-    // larger ones are in; of those equal to TE the lowest positions: marked in a second bitmap
-    uint32_t* equal = taken + words;
-    for (int i = tid; i < words; i += kSelThreads) equal[i] = 0;
-    __syncthreads();
-    each_exact([&](int i, unsigned long long e) {
-      if (e > TE) atomicOr(&taken[i >> 5], 1u << (i & 31));
-      if (e == TE) atomicOr(&equal[i >> 5], 1u << (i & 31));
-    });
+      block_range(elo, ehi, s_wide);
+      int larger;
+      const unsigned long long TE = kth_largest<unsigned long long>(
+          need, elo, ehi,
+          [&](auto&& f) {
+            for (int i = tid; i < n; i += kSelThreads) {
+              const unsigned long long e = __ldcg(exact + i);
+              if (e != 0) f(e);
+            }
+          },
+          hist, s_scan, s_pick, &larger);
+      equal = need - larger;
+      for (int i = tid; i < n; i += kSelThreads) {
+        const unsigned long long e = __ldcg(exact + i);
+        if (e > TE) take(i);
+        if (e == TE) atomicOr(&second[i >> 5], 1u << (i & 31));
+      }
+    } else {
+      __syncthreads();
+      each_key([&](int i, uint32_t key) {
+        if (key == T) atomicOr(&second[i >> 5], 1u << (i & 31));
+      });
+    }
     __syncthreads();
     int base = 0;
     for (int w0 = 0; w0 < words; w0 += kSelThreads) {
       const int w = w0 + tid;
-      const uint32_t bits = w < words ? equal[w] : 0;
+      const uint32_t bits = w < words ? second[w] : 0;
       int total;
       int before = base + sum.exclusive(__popc(bits), &total);
       uint32_t keep = 0;
-      for (uint32_t x = bits; x && before < need - larger; x &= x - 1, ++before) keep |= x & (0u - x);
+      for (uint32_t x = bits; x && before < equal; x &= x - 1, ++before) keep |= x & (0u - x);
       if (keep) taken[w] |= keep;
       base += total;
     }
   }
   __syncthreads();
 
-  // the taken pages in position order
+  // ---- the taken pages in position order: where each bitmap word's pages begin, then a thread a page
   int base = 0;
   for (int w0 = 0; w0 < words; w0 += kSelThreads) {
     const int w = w0 + tid;
-    uint32_t bits = w < words ? taken[w] : 0;
     int total;
-    int at = base + sum.exclusive(__popc(bits), &total);
-    for (; bits; bits &= bits - 1) out[at++] = pt[w * 32 + __ffs(static_cast<int>(bits)) - 1];
+    const int at = base + sum.exclusive(w < words ? __popc(taken[w]) : 0, &total);
+    if (w < words) second[w] = static_cast<uint32_t>(at);
     base += total;
+  }
+  __syncthreads();
+#pragma unroll 4
+  for (int i = tid; i < n; i += kSelThreads) {
+    const uint32_t bits = taken[i >> 5], bit = 1u << (i & 31);
+    if (bits & bit) out[second[i >> 5] + __popc(bits & (bit - 1))] = pt[i];
   }
 }
 
@@ -596,18 +635,29 @@ evict_select_kernel(const EvictParams p) {
     e += s_eq[x];
   }
   const uint32_t below = (1u << lane) - 1u;
-  for (int i = s0 + lane; i - lane < s1; i += 32) {
-    bool gt, eq;
-    look(i, gt, eq);
-    const uint32_t bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
-    const int eq_before = e + __popc(be & below);
-    if (gt || (eq && eq_before < ties)) {
-      const int at = g + __popc(bg & below) + min(eq_before, ties);
-      kept[at] = i;
-      if (!in_place) to[at] = __ldcg(w + i);
+  constexpr int kWalk = 8;   // rounds whose weights are loaded together
+  for (int i0 = s0 + lane; i0 - lane < s1; i0 += 32 * kWalk) {
+    float v[kWalk];
+    if (!in_place) {
+#pragma unroll
+      for (int x = 0; x < kWalk; ++x) v[x] = i0 + 32 * x < s1 ? __ldcg(w + i0 + 32 * x) : 0.f;
     }
-    g += __popc(bg);
-    e += __popc(be);
+#pragma unroll
+    for (int x = 0; x < kWalk; ++x) {
+      const int i = i0 + 32 * x;
+      if (i - lane >= s1) break;
+      bool gt, eq;
+      look(i, gt, eq);
+      const uint32_t bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
+      const int eq_before = e + __popc(be & below);
+      if (gt || (eq && eq_before < ties)) {
+        const int at = g + __popc(bg & below) + min(eq_before, ties);
+        kept[at] = i;
+        if (!in_place) to[at] = v[x];
+      }
+      g += __popc(bg);
+      e += __popc(be);
+    }
   }
   if (!in_place) return;
   __syncthreads();
@@ -764,7 +814,7 @@ cudaError_t allow_smem(std::atomic<unsigned long long>& done, F* kernel, size_t 
 
 cudaError_t launch_select_pages(const SelectParams& p, cudaStream_t stream) {
   // keys (where a row fits), then two bitmaps of the row's pages
-  const size_t keys = p.max_pages <= kSelKeys ? p.max_pages : kSelKeys;
+  const size_t keys = p.max_pages <= kSelKeys ? p.max_pages : kSelKeys;   // (more than registers hold)
   const size_t words = (static_cast<size_t>(p.max_pages) + 31) / 32;
   constexpr size_t kMost = (kSelKeys + 2 * (kSelectMaxPages / 32)) * 4;
   static std::atomic<unsigned long long> attr_done{0};
