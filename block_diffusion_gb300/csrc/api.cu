@@ -754,7 +754,7 @@ int bdlm_select_pages(const bdlm_attn_desc* desc, const bdlm_bf16* q, const bdlm
                               d.B, d.L, d.Hq, d.Hkv, G, d.max_pages_per_seq, d.num_pages, group,
                               groups, max_tiles, n_select, sel_cols,
                               sel_table, sel_lens, st->err};
-  return bdlm::launch_select_pages(sp, s) == cudaSuccess ? BDLM_OK : BDLM_ERR_CUDA;
+  return bdlm::launch_select_pages(sp, st->num_sms, s) == cudaSuccess ? BDLM_OK : BDLM_ERR_CUDA;
 }
 
 int bdlm_sparse_attention(const bdlm_attn_desc* desc, const bdlm_bf16* q, const bdlm_bf16* k_pages,

@@ -74,7 +74,7 @@ struct SelectParams {
   int* err;
 };
 constexpr int kSelectMaxPages = 262144;   // a list's page bitmap fits shared memory
-cudaError_t launch_select_pages(const SelectParams& p, cudaStream_t stream);
+cudaError_t launch_select_pages(const SelectParams& p, int num_sms, cudaStream_t stream);
 
 struct EvictParams {
   const int32_t* lens;

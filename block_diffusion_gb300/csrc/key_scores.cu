@@ -25,8 +25,9 @@
 //   warp 3       finds the CTA's share; weights: Q of a list by TMA (a 64-dim x G x L box per half)
 //   warps 4-     reduction, two or four sets of four warps (one per lane quadrant) in turn
 //   page scores  a page's bounds are 512 bytes, too small for a box each (128 boxes of one row per
-//                K atom): warps 12-19 gather them with cp.async, 16 lanes a row, into the 128-byte
-//                swizzle, and warps 1-3 build q+ and q- of a list in shared memory
+//                K atom): the last eight warps gather them, 16 lanes a row, into the 128-byte
+//                swizzle, and build q+ and q- of a list in shared memory as it begins; warps 1-2 run
+//                up to three tiles ahead, reading page ids and asking L2 for the pages' rows
 // Stages are 32 KB (128 keys x 128 values); a page tile takes two (hi, then lo).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -43,6 +44,7 @@ constexpr int kKeys = kKeyTile;      // keys per tile (UMMA M)
 constexpr int kPageTokens = 16;
 constexpr int kStage = 32768;        // 128 keys x 128 bf16, two 64-wide K atoms
 constexpr int kAtom = 16384;
+constexpr int kIdRing = 3;           // page scores: tiles whose page ids are fetched ahead
 constexpr int kLoaders = kAmaxPerTile;         // page scores: gathering warps
 
 // WIDE: up to 256 query rows; else up to 32 (more stages, two Q buffers).
@@ -53,7 +55,6 @@ struct Cfg {
   static constexpr int kQBufs = WIDE ? 1 : 2;
   static_assert(WIDE || !PAGES, "page scores of few rows take the direct kernel below");
   static constexpr int kStages = PAGES ? 3 : WIDE ? 4 : 6;
-  static constexpr int kAhead = kStages - 1;                   // page scores: stages in flight
   // Weights of more than 32 rows: two sets share a tile, half of its columns each.  (The MMA stays
   // one of N = all rows: in halves of 128 it reads A twice, 128 bytes of shared memory a clock, and
   // the MMAs alone then took 99 us of what are 78 us of copies.)
@@ -64,19 +65,6 @@ struct Cfg {
   static constexpr int kThreads = 128 + kSets * 128 + (PAGES ? kLoaders * 32 : 0);
   static constexpr size_t kSmem = 1024 + static_cast<size_t>(kQBufs) * kQBytes + kStages * kStage;
 };
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
-  const int n = valid ? 16 : 0;   // invalid: 16 bytes of zeros
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 // A walk over a CTA's share of the tiles.
 template <bool PAGES>
@@ -183,6 +171,9 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   __shared__ float s_part[C::kSplit ? 4 : 1][C::kSplit ? 128 : 1];
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
+  // page scores: page ids of the tiles ahead (-1: none), from warps 1-2 to the gathering warps
+  __shared__ uint64_t bar_ids[PAGES ? kIdRing : 1], bar_ids_free[PAGES ? kIdRing : 1];
+  __shared__ int s_ids[PAGES ? kIdRing : 1][PAGES ? kKeys : 1];
   __shared__ int s_share[4];
   __shared__ __align__(16) float s_lse[PAGES ? 1 : 2][PAGES ? 4 : C::kRowsMax];   // log2 units
 
@@ -194,7 +185,7 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       mbar_init(&bar_empty[s], 1);
     }
     for (int b = 0; b < C::kQBufs; ++b) {
-      mbar_init(&bar_qfull[b], PAGES ? 3 : 1);
+      mbar_init(&bar_qfull[b], PAGES ? kLoaders : 1);
       mbar_init(&bar_qempty[b], 1);
     }
     for (int b = 0; b < C::kDBufs; ++b) {
@@ -205,6 +196,11 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     mbar_init(&bar_lse[1], C::kSets * 4);
     if constexpr (C::kSplit)
       for (int i = 0; i < 16; ++i) mbar_init(&bar_part[i >> 2][i & 3], 1);
+    if constexpr (PAGES)
+      for (int i = 0; i < kIdRing; ++i) {
+        mbar_init(&bar_ids[i], 2);
+        mbar_init(&bar_ids_free[i], kLoaders);
+      }
     mbar_init(&bar_done, 1);
     abort_flag = 0;
     fence_mbar_init();
@@ -296,62 +292,81 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         }
       }
     }
-  } else if (PAGES && warp >= 1 && warp <= 3) {
-    // ------------------------------------------------------------ q+ and q-
+  } else if (PAGES && (warp == 1 || warp == 2)) {
+    // ------------------------------------------------------------ page ids and L2, tiles ahead
+    const int t = threadIdx.x - 32;   // 0 .. 63: pages t and t + 64 of a tile
     bool ok = true;
-    int q = 0;
-    for (KeyWalk<PAGES> w(p, s_share); w.left > 0 && ok; w.next()) {
-      if (!w.fresh) continue;
-      const int qb = q % C::kQBufs;
-      if (!(ok = mbar_wait_warp(&bar_qempty[qb], ((q / C::kQBufs) & 1) ^ 1, &abort_flag))) break;
-      // row n: query l0 + n / G, head kvh * G + n % G; padding rows repeat row 0, so they cannot
-      // raise a maximum
-#pragma unroll 4
-      for (int c = threadIdx.x - 32; c < n16 * 16; c += 96) {
-        const int r = c >> 4, n = r < p.rows ? r : 0, cc = c & 15;
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(
-                                  p.q + ((static_cast<size_t>(w.b) * p.L + p.l0 + n / p.G) * p.Hq +
-                                         w.kvh * p.G + n % p.G) * 128) + cc);
-        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-        uint32_t hi[4], lo[4];
+    int u = 0;
+    for (KeyWalk<PAGES> w(p, s_share); w.left > 0 && ok; w.next(), ++u) {
+      int id[2];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t neg = ((x[k] >> 15) & 0x00010001u) * 0xFFFFu;   // 16 ones per negative
-          hi[k] = x[k] & ~neg;
-          lo[k] = x[k] & neg;
-        }
-        uint8_t* d = sQ + qb * C::kQBytes + ((cc >> 3) * n16 + r) * 128 + (((cc & 7) ^ (r & 7)) << 4);
-        *reinterpret_cast<uint4*>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(d + 2 * n16 * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      for (int r = 0; r < 2; ++r) {
+        const int page = w.tile * kKeys + t + 64 * r;
+        id[r] = -1;
+        if (page < w.n)
+          id[r] = __ldg(p.page_table + static_cast<size_t>(w.b) * p.max_pages + page);
       }
-      fence_proxy_async_smem();
+      const int ring = u % kIdRing;
+      if (!(ok = mbar_wait_warp(&bar_ids_free[ring], ((u / kIdRing) & 1) ^ 1, &abort_flag))) break;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        if (id[r] < 0 || id[r] >= p.num_pages) {
+          if (w.tile * kKeys + t + 64 * r < w.n) atomicOr(p.err, BDLM_DEVERR_PAGE);
+          id[r] = -1;
+        } else {
+          const uint16_t* row = p.bounds + (static_cast<size_t>(id[r]) * p.Hkv + w.kvh) * 256;
+#pragma unroll
+          for (int l = 0; l < 4; ++l) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + l * 64));
+        }
+        s_ids[ring][t + 64 * r] = id[r];
+      }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar_qfull[qb]);
-      ++q;
+      if (lane == 0) mbar_arrive(&bar_ids[ring]);
     }
-  } else if (PAGES && warp >= 12) {
+  } else if (PAGES && warp >= C::kThreads / 32 - kLoaders) {
     // ------------------------------------------------------------ gather of the page bounds
-    const int t = threadIdx.x - 384;   // 0 .. 255
+    // Through registers: cp.async moves 16 bytes a clock and SM (31 GB/s).  A thread loads one stage
+    // while it stores the one before.
+    const int t = threadIdx.x - (C::kThreads - kLoaders * 32);   // 0 .. 255
     const int c16 = t & 15;            // 16-byte chunk of a 256-byte half row
-    const uint32_t a_base = smem_u32(sA);
-    const uint32_t a_off = static_cast<uint32_t>((c16 >> 3) * kAtom);
-    constexpr int kAhead = C::kAhead;
+    uint8_t* const dst = sA + (c16 >> 3) * kAtom;
     bool ok = true;
-    int s = 0, done = 0;   // stages issued, and handed to the MMA
+    int s = 0, u = 0;      // stages handed to the MMA, tiles whose ids are read
     uint32_t top = 0;      // largest |bound| seen in the tile, as a bf16 pair
-    KeyWalk<PAGES> back(p, s_share);   // the tile of stage `done`
-    // Hands over the oldest stage in flight: the thread's own chunks have landed
-    // (cp.async.wait_group), so it looks at their magnitudes and signs the stage off.  The largest
-    // magnitude of a tile, one value per warp, is what bounds its scores' rounding error.
-    auto hand_over = [&]() {
-      const int st = done % C::kStages;
+    KeyWalk<PAGES> w(p, s_share);
+    // page ids of the walk's tile: this thread's eight rows
+    auto load_ids = [&](int (&id)[8]) {
+      if (w.left <= 0 || !ok) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) id[i] = -1;
+        return;
+      }
+      const int ring = u % kIdRing;
+      ok = mbar_wait_warp(&bar_ids[ring], (u / kIdRing) & 1, &abort_flag);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) id[i] = ok ? s_ids[ring][i * 16 + (t >> 4)] : -1;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar_ids_free[ring]);
+      ++u;
+    };
+    // half 0: hi (row 1 of a page's bounds), half 1: lo (row 0)
+    auto load_half = [&](uint4 (&v)[8], const int (&id)[8], int kvh, int h) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        v[i] = id[i] >= 0 ? __ldg(reinterpret_cast<const uint4*>(p.bounds) +
+                                  ((static_cast<size_t>(id[i]) * p.Hkv + kvh) * 2 + (1 - h)) * 16 + c16)
+                          : make_uint4(0, 0, 0, 0);
+    };
+    auto store_half = [&](const uint4 (&v)[8]) {
+      const int st = s % C::kStages;
+      if (!(ok = ok && mbar_wait_warp(&bar_empty[st], ((s / C::kStages) & 1) ^ 1, &abort_flag)))
+        return;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int r = i * 16 + (t >> 4);
-        const uint4 v = *reinterpret_cast<const uint4*>(
-            sA + st * kStage + a_off + r * 128 + (((c16 & 7) ^ (r & 7)) << 4));
-        const uint32_t x[4] = {v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu, v.z & 0x7FFF7FFFu,
-                               v.w & 0x7FFF7FFFu};
+        *reinterpret_cast<uint4*>(dst + st * kStage + r * 128 + (((c16 & 7) ^ (r & 7)) << 4)) = v[i];
+        const uint32_t x[4] = {v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu, v[i].z & 0x7FFF7FFFu,
+                               v[i].w & 0x7FFF7FFFu};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const __nv_bfloat162 m =
@@ -363,63 +378,63 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar_full[st]);
-      if (done++ & 1) {
-        const float a = bf16_lo(top), z = bf16_hi(top);
-        float m = a <= CUDART_INF_F && z <= CUDART_INF_F ? fmaxf(a, z) : CUDART_INF_F;   // NaN: inf
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-        if (lane == 0) p.amax[(back.row() * p.max_tiles + back.tile) * kLoaders + (warp - 12)] = m;
-        top = 0;
-        back.next();
-      }
+      ++s;
     };
-    KeyWalk<PAGES> w(p, s_share);
-    // page ids of the walk's tile: this thread's eight rows (-1: none)
-    auto load_ids = [&](int (&id)[8]) {
+    // q+ and q- of the walk's list; row n is query l0 + n / G, head kvh * G + n % G (the division as
+    // a product: n < 256, G <= 16).  Padding rows repeat row 0, so they cannot raise a maximum.
+    const int recip = (65536 + p.G - 1) / p.G;
+    int q = 0;   // lists so far
+    auto build_q = [&](int b, int kvh) {
+      const int qb = q % C::kQBufs;
+      if (!(ok = ok && mbar_wait_warp(&bar_qempty[qb], ((q / C::kQBufs) & 1) ^ 1, &abort_flag)))
+        return;
+      const uint16_t* base = p.q + (static_cast<size_t>(b) * p.L + p.l0) * p.Hq * 128 + kvh * p.G * 128;
+#pragma unroll 4
+      for (int r = t >> 4; r < n16; r += 16) {
+        const int n = r < p.rows ? r : 0, i = (n * recip) >> 16;
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(
+                                  base + (static_cast<size_t>(i) * p.Hq + n - i * p.G) * 128) + c16);
+        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+        uint32_t hi[4], lo[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int page = w.tile * kKeys + i * 16 + (t >> 4);
-        id[i] = w.left > 0 && page < w.n
-                    ? __ldg(p.page_table + static_cast<size_t>(w.b) * p.max_pages + page)
-                    : -1;
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t neg = ((x[k] >> 15) & 0x00010001u) * 0xFFFFu;   // 16 ones per negative
+          hi[k] = x[k] & ~neg;
+          lo[k] = x[k] & neg;
+        }
+        uint8_t* d = sQ + qb * C::kQBytes + ((c16 >> 3) * n16 + r) * 128 + (((c16 & 7) ^ (r & 7)) << 4);
+        *reinterpret_cast<uint4*>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4*>(d + 2 * n16 * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar_qfull[qb]);
+      ++q;
     };
     int id[8];
+    uint4 hi[8], lo[8];
     load_ids(id);
+    load_half(hi, id, w.kvh, 0);
     while (w.left > 0 && ok) {
-      const int kvh = w.kvh, first = w.tile * kKeys, n = w.n;
+      const int kvh = w.kvh;
+      float* amax = p.amax + (w.row() * p.max_tiles + w.tile) * kLoaders + (warp - (C::kThreads / 32 - kLoaders));
+      load_half(lo, id, kvh, 1);
+      if (w.fresh) build_q(w.b, kvh);
       w.next();
-      int id_next[8];   // the next tile's ids arrive while this one's stages are waited for
-      load_ids(id_next);
+      store_half(hi);
+      load_ids(id);
+      load_half(hi, id, w.kvh, 0);
+      store_half(lo);
+      // the largest magnitude of the tile, one value per warp, is what bounds its scores' rounding
+      // error (a NaN counts as infinite)
+      const float a = bf16_lo(top), z = bf16_hi(top);
+      float m = a <= CUDART_INF_F && z <= CUDART_INF_F ? fmaxf(a, z) : CUDART_INF_F;
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (id[i] < 0 || id[i] >= p.num_pages) {
-          if (c16 == 0 && first + i * 16 + (t >> 4) < n) atomicOr(p.err, BDLM_DEVERR_PAGE);
-          id[i] = -1;
-        }
-      for (int h = 0; h < 2; ++h, ++s) {   // hi (row 1 of a page's bounds), then lo (row 0)
-        if (s >= kAhead) {
-          cp_async_wait<kAhead - 1>();
-          hand_over();
-        }
-        const int st = s % C::kStages;
-        if (!(ok = mbar_wait_warp(&bar_empty[st], ((s / C::kStages) & 1) ^ 1, &abort_flag))) break;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = i * 16 + (t >> 4);
-          const size_t row = (static_cast<size_t>(id[i] < 0 ? 0 : id[i]) * p.Hkv + kvh) * 2 + (1 - h);
-          cp_async16(a_base + st * kStage + a_off + r * 128 + (((c16 & 7) ^ (r & 7)) << 4),
-                     p.bounds + row * 128 + c16 * 8, id[i] >= 0);
-        }
-        cp_async_commit();
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) id[i] = id_next[i];
+      for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+      if (lane == 0) *amax = m;
+      top = 0;
     }
     griddep_launch_dependents();
-    cp_async_wait<0>();
-    if (ok)
-      while (done < s) hand_over();
   } else if (warp == 0) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
@@ -503,20 +518,17 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       tc_fence_after();
       const uint32_t td =
           tmem + lane_off + static_cast<uint32_t>(db * C::kRowsMax + half * split);
-      // 16 columns at a time, the next 16 on their way from tensor memory meanwhile
-      uint32_t r[2][16];
-      tmem_ld16(td, r[0]);
+      // 16 columns at a time.  The other warps of the scheduler cover the load's latency: fetching
+      // the next 16 meanwhile, or 32 at a time, was slower (109 and 127 us against 99, 16 x 64 x 4
+      // rows over 8192-16384 tokens).
       auto columns = [&](auto&& each) {
-        for (int c = 0; c < cols; c += 32) {
+#pragma unroll 2
+        for (int c = 0; c < cols; c += 16) {
+          uint32_t r[16];
+          tmem_ld16(td + c, r);
           tmem_wait_ld();
-          tmem_regs_ready(r[0]);
-          if (c + 16 < cols) tmem_ld16(td + c + 16, r[1]);
-          each(c, r[0]);
-          if (c + 16 >= cols) break;
-          tmem_wait_ld();
-          tmem_regs_ready(r[1]);
-          if (c + 32 < cols) tmem_ld16(td + c + 32, r[0]);
-          each(c + 16, r[1]);
+          tmem_regs_ready(r);
+          each(c, r);
         }
         tc_fence_before();
         __syncwarp();
@@ -561,21 +573,34 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         }
         if (live) *wp = fmaf(p.decay, w_old, total);
       } else {
-        // a group's columns are `width` consecutive query rows
+        // a group's columns are `width` consecutive query rows: 16 columns at a time where they are
+        // all of one group
         float m = -CUDART_INF_F;
         int to_go = p.width;
         float* out = p.scores + (static_cast<size_t>(w.b) * p.groups + p.l0 / p.group) * p.Hkv *
                                     static_cast<size_t>(p.max_pages) +
                      static_cast<size_t>(w.kvh) * p.max_pages + key;
+        auto flush = [&](int c) {
+          if (key < w.n && c < p.rows) *out = live ? m : -CUDART_INF_F;
+          out += static_cast<size_t>(p.Hkv) * p.max_pages;
+          m = -CUDART_INF_F;
+          to_go = p.width;
+        };
         columns([&](int c, const uint32_t (&x)[16]) {
+          if (to_go >= 16) {
+            float v[5];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            m = fmaxf(m, __uint_as_float(x[k]));
-            if (--to_go == 0) {
-              if (key < w.n && c + k < p.rows) *out = live ? m : -CUDART_INF_F;
-              out += static_cast<size_t>(p.Hkv) * p.max_pages;
-              m = -CUDART_INF_F;
-              to_go = p.width;
+            for (int k = 0; k < 5; ++k)
+              v[k] = fmax3(__uint_as_float(x[3 * k]), __uint_as_float(x[3 * k + 1]),
+                           __uint_as_float(x[3 * k + 2]));
+            m = fmax3(m, __uint_as_float(x[15]), fmaxf(fmax3(v[0], v[1], v[2]), fmaxf(v[3], v[4])));
+            to_go -= 16;
+            if (to_go == 0) flush(c + 15);
+          } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              m = fmaxf(m, __uint_as_float(x[k]));
+              if (--to_go == 0) flush(c + k);
             }
           }
         });

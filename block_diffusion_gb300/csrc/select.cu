@@ -23,8 +23,9 @@ namespace bdlm {
 namespace {
 
 constexpr int kTok = 16;       // tokens per page
+constexpr int kRowThreads = 512;   // threads of a CTA that works on a row
 constexpr int kBuckets = 2048;
-constexpr int kDirect = 256;   // keys ranked directly (the bucket counters' memory holds them)
+constexpr int kDirect = 128;   // keys ranked directly, four lanes a key (in the counters' memory)
 
 // Unsigned key with the floats' order; -0 and +0 are equal, NaN comes below every number.
 __device__ __forceinline__ uint32_t order_key(float f) {
@@ -54,27 +55,28 @@ struct BlockSum {   // sums and scans over the CTA; s: one word per warp
   }
 };
 
-// Minimum and maximum over the CTA (every thread gets both).
+// Minimum and maximum over the CTA (every thread gets both); s: 64 values.
 template <typename T>
 __device__ __forceinline__ void block_range(T& lo, T& hi, T* s) {
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  auto warp_range = [&]() {
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) {
-    const T a = __shfl_xor_sync(0xffffffffu, lo, off), b = __shfl_xor_sync(0xffffffffu, hi, off);
-    lo = a < lo ? a : lo;
-    hi = b > hi ? b : hi;
-  }
-  const int warps = blockDim.x >> 5;
+    for (int off = 16; off > 0; off >>= 1) {
+      const T a = __shfl_xor_sync(0xffffffffu, lo, off), b = __shfl_xor_sync(0xffffffffu, hi, off);
+      lo = a < lo ? a : lo;
+      hi = b > hi ? b : hi;
+    }
+  };
+  warp_range();
   __syncthreads();
-  if ((threadIdx.x & 31) == 0) {
+  if (lane == 0) {
     s[threadIdx.x >> 5] = lo;
     s[32 + (threadIdx.x >> 5)] = hi;
   }
   __syncthreads();
-  for (int w = 0; w < warps; ++w) {
-    lo = s[w] < lo ? s[w] : lo;
-    hi = s[32 + w] > hi ? s[32 + w] : hi;
-  }
-  __syncthreads();
+  lo = s[lane < warps ? lane : 0];
+  hi = s[32 + (lane < warps ? lane : 0)];
+  warp_range();
 }
 
 // The same by ranking `count` <= kDirect keys, listed in `few`, against each other (after a
@@ -82,16 +84,22 @@ __device__ __forceinline__ void block_range(T& lo, T& hi, T* s) {
 template <typename K>
 __device__ __forceinline__ K kth_of_few(int k, const K* few, int count, int* s_scan, K* s_pick,
                                         int* above) {
-  if (static_cast<int>(threadIdx.x) < count) {
-    const K key = few[threadIdx.x];
+  const int c = static_cast<int>(threadIdx.x) >> 2;
+  if ((c & ~7) < count) {   // whole warps
+    const K key = few[c < count ? c : 0];
     int more = 0, same = 0;
-#pragma unroll 4
-    for (int i = 0; i < count; ++i) {
+#pragma unroll 8
+    for (int i = threadIdx.x & 3; i < count; i += 4) {
       const K other = few[i];
       more += other > key;
       same += other == key;
     }
-    if (more < k && more + same >= k) {   // equal keys write the same
+#pragma unroll
+    for (int off = 1; off < 4; off <<= 1) {
+      more += __shfl_xor_sync(0xffffffffu, more, off);
+      same += __shfl_xor_sync(0xffffffffu, same, off);
+    }
+    if (c < count && more < k && more + same >= k) {   // equal keys write the same
       s_pick[0] = key;
       s_scan[33] = more;
     }
@@ -117,31 +125,27 @@ __device__ __forceinline__ K kth_largest(int k, K lo, K hi, Each&& each, int* hi
     int bits = sizeof(K) == 8 ? 64 - __clzll(static_cast<long long>(range))
                               : 32 - __clz(static_cast<int>(range));
     const int shift = bits > 11 ? bits - 11 : 0;
-    for (int i = threadIdx.x; i < kBuckets; i += blockDim.x) hist[i] = 0;
+    reinterpret_cast<int4*>(hist)[threadIdx.x] = make_int4(0, 0, 0, 0);
     __syncthreads();
     each([&](K key) {
       if (key >= lo && key <= hi) atomicAdd(&hist[static_cast<int>((key - lo) >> shift)], 1);
     });
     __syncthreads();
-    // this thread's buckets, counted from the top
-    const int per = kBuckets / static_cast<int>(blockDim.x);
-    int mine = 0;
-    for (int i = 0; i < per; ++i)
-      mine += hist[kBuckets - 1 - (static_cast<int>(threadIdx.x) * per + i)];
+    // this thread's four buckets, counted from the top
+    static_assert(kBuckets == 4 * kRowThreads, "four buckets a thread");
+    const int4 h4 = reinterpret_cast<const int4*>(hist)[kRowThreads - 1 - threadIdx.x];
+    const int mine[4] = {h4.w, h4.z, h4.y, h4.x};
     int total;
-    int before = larger + sum.exclusive(mine, &total);
-    if (before < k && before + mine >= k) {
-      for (int i = 0; i < per; ++i) {
-        const int bucket = kBuckets - 1 - (static_cast<int>(threadIdx.x) * per + i);
-        if (before + hist[bucket] >= k) {
-          s_pick[0] = static_cast<K>(bucket);
-          s_scan[33] = before;
-          s_scan[34] = hist[bucket];
-          s_scan[35] = 0;
-          break;
-        }
-        before += hist[bucket];
+    int before = larger + sum.exclusive(mine[0] + mine[1] + mine[2] + mine[3], &total);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (before < k && before + mine[i] >= k) {
+        s_pick[0] = static_cast<K>(kBuckets - 1 - (static_cast<int>(threadIdx.x) * 4 + i));
+        s_scan[33] = before;
+        s_scan[34] = mine[i];
+        s_scan[35] = 0;
       }
+      before += mine[i];
     }
     __syncthreads();
     const K from = lo + (s_pick[0] << shift), width = (static_cast<K>(1) << shift) - 1;
@@ -167,9 +171,19 @@ __device__ __forceinline__ K kth_largest(int k, K lo, K hi, Each&& each, int* hi
 }
 
 // ------------------------------------------------------------------ page selection
-constexpr int kSelThreads = 512;
-constexpr int kSelKeys = 16384;      // keys held in shared memory (64 KB); longer rows are re-read
+constexpr int kSelThreads = kRowThreads;
+constexpr int kSelKeys = 12288;      // rows held in shared memory (96 KB); longer ones are re-read
 constexpr int kSelExact = 1024;      // near ties held in shared memory
+
+// Query n of a group (n < 256: its position n / G, head n % G; G <= 16, so the division is a product)
+// as 32 lanes' four values each.
+__device__ __forceinline__ const uint2* group_query(const SelectParams& p, int b, int s, int kvh,
+                                                    int n) {
+  const int i = (n * ((65536 + p.G - 1) / p.G)) >> 16;
+  return reinterpret_cast<const uint2*>(p.q) +
+         ((static_cast<size_t>(b) * p.L + s * p.group + i) * p.Hq + kvh * p.G + (n - i * p.G)) * 32 +
+         (threadIdx.x & 31);
+}
 
 // a + b as s + e exactly
 __device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
@@ -178,99 +192,76 @@ __device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
   e = __fadd_rn(__fadd_rn(a, -__fadd_rn(s, -bb)), __fadd_rn(b, -bb));
 }
 
-// The largest score of one page over query rows row0 .. rows - 1 of one group, to about 2^-45 of its
-// terms, as an ordered 64-bit key (never 0 or 1).
-// Whole warp: lane l takes dims 4l .. 4l + 3.  The products of two bf16 are exact in float32; they
-// are added with the rounding errors carried along.  With more than 16 query rows only those that
-// can hold the maximum are taken that far: a plain float32 score of every row first (a lane a
-// row; off by less than 2^-16 of the terms' sum, within E below), then the rows within 2E (`band`)
-// of the largest.  rough: 256 floats of this warp's own.
+// The largest score of one page over query rows row0 .. rows - 1 (at most 16) of one group, to about
+// 2^-45 of its terms, as an ordered 64-bit key (never 0 or 1).  Whole warp: lane l takes dims 4l ..
+// 4l + 3.  First every row's plain float32 score, all rows' queries loaded at once (off by less
+// than 2^-16 of the terms' sum, within E below); then the rows within 2E (`band`) of the largest,
+// the only ones that can hold the maximum: the products of two bf16 are exact in float32, and are
+// added with the rounding errors carried along.
+constexpr int kExactRows = 16;
 __device__ __forceinline__ unsigned long long exact_score(const SelectParams& p, int b, int s,
                                                           int kvh, int id, int row0, int rows,
-                                                          float band, float* rough) {
+                                                          float band) {
   const int lane = threadIdx.x & 31;
-  const uint4* page = reinterpret_cast<const uint4*>(p.bounds) +
-                      (static_cast<size_t>(id) * p.Hkv + kvh) * 32;   // 16 chunks of lo, 16 of hi
-  auto query = [&](int n) {
-    return p.q + ((static_cast<size_t>(b) * p.L + s * p.group + n / p.G) * p.Hq + kvh * p.G +
-                  n % p.G) * 128;
-  };
-  const bool prune = rows - row0 > 16;   // row0 = 0 then
-  float least = 0.f;
-  if (prune) {
-    float most = -CUDART_INF_F;
-    for (int n = lane; n - lane < rows; n += 32) {
-      const uint4* q = reinterpret_cast<const uint4*>(query(min(n, rows - 1)));
-      float f = 0.f;
-#pragma unroll 4
-      for (int c = 0; c < 16; ++c) {
-        const uint4 lo = __ldg(page + c), hi = __ldg(page + 16 + c), v = __ldg(q + c);
-        const uint32_t lw[4] = {lo.x, lo.y, lo.z, lo.w}, hw[4] = {hi.x, hi.y, hi.z, hi.w},
-                       qw[4] = {v.x, v.y, v.z, v.w};
+  const uint2* page = reinterpret_cast<const uint2*>(p.bounds) +
+                      (static_cast<size_t>(id) * p.Hkv + kvh) * 64 + lane;
+  auto query = [&](int n) { return __ldg(group_query(p, b, s, kvh, n)); };
+  const uint2 lo = __ldg(page), hi = __ldg(page + 32);
+  uint2 q[kExactRows];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float q0 = bf16_lo(qw[k]), q1 = bf16_hi(qw[k]);
-          f = fmaf(q0, q0 > 0.f ? bf16_lo(hw[k]) : bf16_lo(lw[k]), f);
-          f = fmaf(q1, q1 > 0.f ? bf16_hi(hw[k]) : bf16_hi(lw[k]), f);
-        }
-      }
-      if (n < rows) rough[n] = f;
-      most = fmaxf(most, f);
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
-    least = __fadd_rd(most, -band);
-    __syncwarp();
-  }
-  const uint2 lo = __ldg(reinterpret_cast<const uint2*>(page) + lane);
-  const uint2 hi = __ldg(reinterpret_cast<const uint2*>(page) + 32 + lane);
+  for (int x = 0; x < kExactRows; ++x) q[x] = query(min(row0 + x, rows - 1));
   const float lv[4] = {bf16_lo(lo.x), bf16_hi(lo.x), bf16_lo(lo.y), bf16_hi(lo.y)};
   const float hv[4] = {bf16_lo(hi.x), bf16_hi(hi.x), bf16_lo(hi.y), bf16_hi(hi.y)};
-  unsigned long long best = 0;
-  constexpr int kRows = 4;   // rows at a time: their loads and shuffles overlap
-  for (int n0 = row0; n0 < rows; n0 += kRows) {
-    if (prune) {
-      bool any = false;
-      for (int n = n0; n < min(n0 + kRows, rows); ++n) any |= rough[n] >= least;
-      if (!any) continue;
-    }
-    float a[kRows], e[kRows];
-    uint2 q[kRows];
+  float f[kExactRows];
 #pragma unroll
-    for (int x = 0; x < kRows; ++x)   // (past the end: the last row again)
-      q[x] = __ldg(reinterpret_cast<const uint2*>(query(min(n0 + x, rows - 1))) + lane);
+  for (int x = 0; x < kExactRows; ++x) {
+    const float qv[4] = {bf16_lo(q[x].x), bf16_hi(q[x].x), bf16_lo(q[x].y), bf16_hi(q[x].y)};
+    f[x] = 0.f;
 #pragma unroll
-    for (int x = 0; x < kRows; ++x) {
-      const float qv[4] = {bf16_lo(q[x].x), bf16_hi(q[x].x), bf16_lo(q[x].y), bf16_hi(q[x].y)};
-      a[x] = e[x] = 0.f;
+    for (int k = 0; k < 4; ++k) f[x] = fmaf(qv[k], qv[k] > 0.f ? hv[k] : lv[k], f[x]);
+  }
+  // sums over the lanes, the rows halved in every step: lane l ends with row l / 2
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float r;
-        two_sum(a[x], __fmul_rn(qv[k], qv[k] > 0.f ? hv[k] : lv[k]), a[x], r);
-        e[x] = __fadd_rn(e[x], r);
-      }
-    }
+  for (int h = kExactRows / 2; h > 0; h >>= 1) {
+    const bool up = lane & (2 * h);
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-#pragma unroll
-      for (int x = 0; x < kRows; ++x) {
-        const float a2 = __shfl_xor_sync(0xffffffffu, a[x], off);
-        const float e2 = __shfl_xor_sync(0xffffffffu, e[x], off);
-        float r;
-        two_sum(a[x], a2, a[x], r);
-        e[x] = __fadd_rn(__fadd_rn(e[x], e2), r);
-      }
-#pragma unroll
-    for (int x = 0; x < kRows; ++x) {
-      float top, rest;
-      two_sum(a[x], e[x], top, rest);   // normalised: top decides, then rest
-      const unsigned long long key =
-          static_cast<unsigned long long>(order_key(top)) << 32 | order_key(rest);
-      best = key > best ? key : best;
+    for (int x = 0; x < h; ++x) {
+      const float keep = up ? f[x + h] : f[x], send = up ? f[x] : f[x + h];
+      f[x] = keep + __shfl_xor_sync(0xffffffffu, send, 2 * h);
     }
   }
-  __syncwarp();   // rough may be written again
+  const float mine = f[0] + __shfl_xor_sync(0xffffffffu, f[0], 1);
+  float most = mine;
+#pragma unroll
+  for (int off = 16; off > 1; off >>= 1)
+    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+  uint32_t near = __ballot_sync(0xffffffffu, mine >= __fadd_rd(most, -band)) & 0x55555555u;
+  if (near == 0) near = 1;   // (scores that are not numbers)
+  unsigned long long best = 0;
+  for (; near; near &= near - 1) {
+    const uint2 v = query(min(row0 + (__ffs(static_cast<int>(near)) - 1) / 2, rows - 1));
+    const float qv[4] = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y)};
+    float a = 0.f, e = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float r;
+      two_sum(a, __fmul_rn(qv[k], qv[k] > 0.f ? hv[k] : lv[k]), a, r);
+      e = __fadd_rn(e, r);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      const float a2 = __shfl_xor_sync(0xffffffffu, a, off);
+      const float e2 = __shfl_xor_sync(0xffffffffu, e, off);
+      float r;
+      two_sum(a, a2, a, r);
+      e = __fadd_rn(__fadd_rn(e, e2), r);
+    }
+    float top, rest;
+    two_sum(a, e, top, rest);   // normalised: top decides, then rest
+    const unsigned long long key =
+        static_cast<unsigned long long>(order_key(top)) << 32 | order_key(rest);
+    best = key > best ? key : best;
+  }
   return best;
 }
 
@@ -284,10 +275,13 @@ __device__ __forceinline__ unsigned long long exact_score(const SelectParams& p,
 // Bound by latency: a dozen barriers and half a dozen loads that depend on each other.  So what can
 // be asked for early is, a thread keeps its first eight keys in registers, and the exact scores
 // of one page are spread over warps.
-__global__ void __launch_bounds__(kSelThreads)
+// CTAS: 1 with all the registers it wants, for no more lists than SMs (128 lists: a call of 58 us
+// against 63 with two CTAs per SM); 2 for more lists (1024: 71 us against 85).
+template <int CTAS>
+__global__ void __launch_bounds__(kSelThreads, CTAS)
 select_pages_kernel(const SelectParams p) {
   extern __shared__ uint32_t sm[];
-  __shared__ int hist[kBuckets];
+  __shared__ __align__(16) int hist[kBuckets];
   __shared__ unsigned long long s_exact[kSelExact];
   __shared__ int s_page[kSelExact];
   __shared__ int s_scan[36];
@@ -295,7 +289,6 @@ select_pages_kernel(const SelectParams p) {
   __shared__ unsigned long long s_pick[1];
   __shared__ int s_cand;
   __shared__ float s_f[32];
-  __shared__ float s_rough[kSelThreads / 32][256];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kWarps = kSelThreads / 32;
   const int list = blockIdx.x;
@@ -316,12 +309,17 @@ select_pages_kernel(const SelectParams p) {
   }
   const int32_t* pt = p.page_table + static_cast<size_t>(b) * p.max_pages;
   // the unfinished page and the block's pages follow the selected ones; unused columns hold -1
-  for (int c = k + tid; c < p.sel_cols; c += kSelThreads) out[c] = c < k + tail ? pt[n + c - k] : -1;
-  if (n <= p.n_select) {
+  const int c0 = k + tid;
+  const int32_t last = c0 < k + tail ? pt[n + tid] : -1;
+  auto finish = [&]() {
+    if (c0 < p.sel_cols) out[c0] = last;
+    for (int c = c0 + kSelThreads; c < p.sel_cols; c += kSelThreads) out[c] = -1;   // (tail <= 5)
+  };
+  if (n <= p.n_select || k == 0) {
     for (int c = tid; c < k; c += kSelThreads) out[c] = pt[c];
+    finish();
     return;
   }
-  if (k == 0) return;
 
   // ---- keys, magnitudes and queries: all asked for before any is used
   const float* row = p.scores + static_cast<size_t>(list) * p.max_pages;
@@ -330,16 +328,19 @@ select_pages_kernel(const SelectParams p) {
 #pragma unroll
   for (int x = 0; x < kOwn; ++x)
     early[x] = tid + x * kSelThreads < n ? __ldcg(row + tid + x * kSelThreads) : 0.f;
+  if (n <= kSelKeys)   // the page ids go to shared memory meanwhile
+    for (int i = tid; i < n; i += kSelThreads)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(sm + i)), "l"(pt + i)
+                   : "memory");
   float q1 = 0.f, am = 0.f;   // the group's largest |q|_1, the list's largest |bound|
   {
     const int values = (n + kKeyTile - 1) / kKeyTile * kAmaxPerTile;
     const float* a = p.amax + (static_cast<size_t>(b) * p.Hkv + kvh) * p.max_tiles * kAmaxPerTile;
     for (int i = tid; i < values; i += kSelThreads) am = fmaxf(am, __ldcg(a + i));
   }
+#pragma unroll 4
   for (int r = warp; r < p.group * p.G; r += kWarps) {
-    const uint2 q = __ldg(reinterpret_cast<const uint2*>(p.q) +
-                          ((static_cast<size_t>(b) * p.L + s * p.group + r / p.G) * p.Hq +
-                           kvh * p.G + r % p.G) * 32 + lane);
+    const uint2 q = __ldg(group_query(p, b, s, kvh, r));
     float v = fabsf(bf16_lo(q.x)) + fabsf(bf16_hi(q.x)) + fabsf(bf16_lo(q.y)) + fabsf(bf16_hi(q.y));
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
@@ -351,11 +352,13 @@ select_pages_kernel(const SelectParams p) {
     s_f[warp] = q1;
     s_f[16 + warp] = am;
   }
-  // keys past the registers' share: in shared memory when they fit, else read again each time; the
-  // page bitmap and a second one follow them
+  // shared memory: page ids, then keys past the registers' share (rows of up to kSelKeys; longer
+  // ones are read again each time), then the page bitmap and a second one
   uint32_t own[kOwn];
   const bool held = n <= kSelKeys;
-  uint32_t* taken = sm + (held && n > kOwn * kSelThreads ? n : 0);
+  int32_t* ids = reinterpret_cast<int32_t*>(sm);
+  uint32_t* keys = sm + n;
+  uint32_t* taken = sm + (held ? (n > kOwn * kSelThreads ? 2 * n : n) : 0);
   const int words = (n + 31) / 32;
   uint32_t* second = taken + words;
   uint32_t lo = 0xFFFFFFFFu, hi = 0;
@@ -368,19 +371,21 @@ select_pages_kernel(const SelectParams p) {
   }
   for (int i = tid + kOwn * kSelThreads; i < n; i += kSelThreads) {
     const uint32_t key = order_key(__ldcg(row + i));
-    if (held) sm[i] = key;
+    if (held) keys[i] = key;
     lo = min(lo, key);
     hi = max(hi, key);
   }
   for (int i = tid; i < words; i += kSelThreads) taken[i] = 0;
   if (tid == 0) s_cand = 0;
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  auto page_id = [&](int i) { return held ? ids[i] : __ldg(pt + i); };
   // f(i, key) for this thread's keys
   auto each_key = [&](auto&& f) {
 #pragma unroll
     for (int x = 0; x < kOwn; ++x)
       if (tid + x * kSelThreads < n) f(tid + x * kSelThreads, own[x]);
     for (int i = tid + kOwn * kSelThreads; i < n; i += kSelThreads)
-      f(i, held ? sm[i] : order_key(__ldcg(row + i)));
+      f(i, held ? keys[i] : order_key(__ldcg(row + i)));
   };
 
   // ---- T, the k-th largest
@@ -400,10 +405,12 @@ select_pages_kernel(const SelectParams p) {
   }
 
   // ---- the band around T
-  q1 = am = 0.f;
-  for (int w = 0; w < kWarps; ++w) {
-    q1 = fmaxf(q1, s_f[w]);
-    am = fmaxf(am, s_f[16 + w]);
+  q1 = s_f[lane & 15];
+  am = s_f[16 + (lane & 15)];
+#pragma unroll
+  for (int off = 8; off > 0; off >>= 1) {
+    q1 = fmaxf(q1, __shfl_xor_sync(0xffffffffu, q1, off));
+    am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, off));
   }
   const float band = q1 * am * (2 * 16 * 17 * 0x1p-23f);   // 2E
   const float t = __uint_as_float(T & 0x80000000u ? T & 0x7FFFFFFFu : ~T);
@@ -433,48 +440,62 @@ select_pages_kernel(const SelectParams p) {
     each_key([&](int i, uint32_t key) {
       if (key >= k_lo && key <= k_hi) take(i);
     });
-  } else if (refine && m <= kSelExact) {
-    // rows of a candidate in batches, a warp each (all rows where they are pruned together); the
-    // maximum over the batches does not depend on their order
-    const int rows = p.group * p.G, per = rows > 16 ? rows : 4, parts = (rows + per - 1) / per;
-    for (int x = warp; x < m * parts; x += kWarps) {
-      const int c = x / parts, id = pt[s_page[c]];
-      if (id < 0 || id >= p.num_pages) continue;
-      const unsigned long long e = exact_score(p, b, s, kvh, id, x % parts * per,
-                                               min(rows, x % parts * per + per), band, s_rough[warp]);
-      if (lane == 0) atomicMax(&s_exact[c], e);
-    }
-    __syncthreads();
-    for (int c = tid; c < m; c += kSelThreads) {
-      const unsigned long long e = s_exact[c];
-      const int page = s_page[c];
-      int rank = 0;   // candidates ahead of this one
-      for (int j = 0; j < m; ++j)
-        rank += s_exact[j] > e || (s_exact[j] == e && s_page[j] < page);
-      if (rank < need) take(page);
-    }
   } else {
-    // many near ties (pages that are copies of each other): their exact scores go to the
-    // workspace, and the need-th largest is found by counting again.  Of those equal to it (or
-    // of the keys equal to T, where there is no refining) the lowest positions are in.
-    int equal = need;
-    for (int i = tid; i < words; i += kSelThreads) second[i] = 0;
-    if (refine) {
-      unsigned long long* exact = p.exact + static_cast<size_t>(list) * p.max_pages;
+    // Up to kSelExact candidates are listed in shared memory, and their rows go to the warps in
+    // batches (all rows together where they are pruned): the maximum over the batches does not
+    // depend on their order.  More of them (pages that are copies of each other) keep their scores
+    // in the workspace.
+    const bool listed = m <= kSelExact;
+    unsigned long long* exact = p.exact + static_cast<size_t>(list) * p.max_pages;
+    unsigned long long elo = ~0ull, ehi = 0;
+    if (!listed && refine) {
       each_key([&](int i, uint32_t key) { exact[i] = key >= k_lo && key <= k_hi ? 1 : 0; });
       __syncthreads();
-      unsigned long long elo = ~0ull, ehi = 0;
-      for (int i = warp; i < n; i += kWarps) {
-        if (__ldcg(exact + i) == 0) continue;
-        const int id = pt[i];
-        unsigned long long e = 1;   // a bad page: below every score
-        if (id >= 0 && id < p.num_pages)
-          e = exact_score(p, b, s, kvh, id, 0, p.group * p.G, band, s_rough[warp]);
-        __syncwarp();
-        if (lane == 0) exact[i] = e;
-        elo = e < elo ? e : elo;
-        ehi = e > ehi ? e : ehi;
+    }
+    const int rows = p.group * p.G, per = kExactRows, parts = listed ? (rows + per - 1) / per : 1;
+    const int work = !refine ? 0 : listed ? m * parts : n;
+    for (int x = warp; x < work; x += kWarps) {
+      // a listed candidate's batch, or every batch of one of many
+      const int c = x / parts, i = listed ? s_page[c] : x;
+      const int first = listed ? x % parts * per : 0, end = listed ? min(rows, first + per) : rows;
+      if (!listed && __ldcg(exact + i) == 0) continue;
+      const int id = page_id(i);
+      unsigned long long e = 1;   // a bad page: below every score
+      if (id >= 0 && id < p.num_pages)
+        for (int row0 = first; row0 < end; row0 += per) {
+          const unsigned long long part =
+              exact_score(p, b, s, kvh, id, row0, min(end, row0 + per), band);
+          e = part > e ? part : e;
+        }
+      __syncwarp();
+      if (lane == 0) {
+        if (listed)
+          atomicMax(&s_exact[c], e);
+        else
+          exact[i] = e;
       }
+      elo = e < elo ? e : elo;
+      ehi = e > ehi ? e : ehi;
+    }
+    __syncthreads();
+    int equal = need;   // how many of `second`, the candidates equal to the last one in, are in
+    for (int i = tid; i < words; i += kSelThreads) second[i] = 0;
+    if (!refine) {
+      __syncthreads();
+      each_key([&](int i, uint32_t key) {
+        if (key == T) atomicOr(&second[i >> 5], 1u << (i & 31));
+      });
+    } else if (listed) {
+      equal = 0;
+      for (int c = tid; c < m; c += kSelThreads) {
+        const unsigned long long e = s_exact[c];
+        const int page = s_page[c];
+        int rank = 0;   // candidates ahead of this one
+        for (int j = 0; j < m; ++j)
+          rank += s_exact[j] > e || (s_exact[j] == e && s_page[j] < page);
+        if (rank < need) take(page);
+      }
+    } else {
       block_range(elo, ehi, s_wide);
       int larger;
       const unsigned long long TE = kth_largest<unsigned long long>(
@@ -492,15 +513,10 @@ select_pages_kernel(const SelectParams p) {
         if (e > TE) take(i);
         if (e == TE) atomicOr(&second[i >> 5], 1u << (i & 31));
       }
-    } else {
-      __syncthreads();
-      each_key([&](int i, uint32_t key) {
-        if (key == T) atomicOr(&second[i >> 5], 1u << (i & 31));
-      });
     }
     __syncthreads();
-    int base = 0;
-    for (int w0 = 0; w0 < words; w0 += kSelThreads) {
+    int base = 0;   // of equal ones the lowest positions
+    for (int w0 = 0; w0 < words && equal > 0; w0 += kSelThreads) {
       const int w = w0 + tid;
       const uint32_t bits = w < words ? second[w] : 0;
       int total;
@@ -526,12 +542,13 @@ select_pages_kernel(const SelectParams p) {
 #pragma unroll 4
   for (int i = tid; i < n; i += kSelThreads) {
     const uint32_t bits = taken[i >> 5], bit = 1u << (i & 31);
-    if (bits & bit) out[second[i >> 5] + __popc(bits & (bit - 1))] = pt[i];
+    if (bits & bit) out[second[i >> 5] + __popc(bits & (bit - 1))] = page_id(i);
   }
+  finish();
 }
 
 // ------------------------------------------------------------------ eviction
-constexpr int kEvictThreads = 512;
+constexpr int kEvictThreads = kRowThreads;
 constexpr int kEvictWarps = kEvictThreads / 32;
 constexpr int kEvictKeys = 22528;   // 88 KB of keys: two CTAs per SM; longer rows are re-read (L2)
 
@@ -545,7 +562,7 @@ constexpr int kEvictKeys = 22528;   // 88 KB of keys: two CTAs per SM; longer ro
 __global__ void __launch_bounds__(kEvictThreads, 2)
 evict_select_kernel(const EvictParams p) {
   extern __shared__ uint32_t sm[];
-  __shared__ int hist[kBuckets];
+  __shared__ __align__(16) int hist[kBuckets];
   __shared__ int s_scan[36];
   __shared__ uint32_t s_range[64];
   __shared__ uint32_t s_pick[1];
@@ -812,15 +829,18 @@ cudaError_t allow_smem(std::atomic<unsigned long long>& done, F* kernel, size_t 
 
 }  // namespace
 
-cudaError_t launch_select_pages(const SelectParams& p, cudaStream_t stream) {
-  // keys (where a row fits), then two bitmaps of the row's pages
-  const size_t keys = p.max_pages <= kSelKeys ? p.max_pages : kSelKeys;   // (more than registers hold)
+cudaError_t launch_select_pages(const SelectParams& p, int num_sms, cudaStream_t stream) {
+  // page ids and keys (of rows that fit), then two bitmaps of the row's pages
+  const size_t keys = 2 * static_cast<size_t>(p.max_pages <= kSelKeys ? p.max_pages : kSelKeys);
   const size_t words = (static_cast<size_t>(p.max_pages) + 31) / 32;
-  constexpr size_t kMost = (kSelKeys + 2 * (kSelectMaxPages / 32)) * 4;
-  static std::atomic<unsigned long long> attr_done{0};
-  cudaError_t e = allow_smem(attr_done, select_pages_kernel, kMost);
+  constexpr size_t kMost = (2 * kSelKeys + 2 * (kSelectMaxPages / 32)) * 4;
+  const unsigned lists = static_cast<unsigned>(p.B) * p.groups * p.Hkv;
+  static std::atomic<unsigned long long> one_done{0}, two_done{0};
+  const bool one = lists <= static_cast<unsigned>(num_sms);
+  cudaError_t e = one ? allow_smem(one_done, select_pages_kernel<1>, kMost)
+                      : allow_smem(two_done, select_pages_kernel<2>, kMost);
   if (e != cudaSuccess) return e;
-  return launch_pdl(select_pages_kernel, dim3(static_cast<unsigned>(p.B) * p.groups * p.Hkv),
+  return launch_pdl(one ? select_pages_kernel<1> : select_pages_kernel<2>, dim3(lists),
                     dim3(kSelThreads), (keys + 2 * words) * 4, stream, p);
 }
 
