@@ -16,8 +16,8 @@
 //
 // (Page scores of up to 32 rows: a kernel of its own, below.)
 //
-// One persistent CTA per SM takes an equal, contiguous share of all tiles of 128 keys, laid end to
-// end list by list (a list = sequence and KV head): equal bytes per SM whatever the lengths, and Q
+// Persistent CTAs, one or two per SM, each take an equal, contiguous share of all tiles of 128 keys, laid end to
+// end list by list (a list = sequence and KV head): equal bytes per CTA whatever the lengths, and Q
 // changes only where a list ends.  Every warp walks the share by itself, so no warp hands out work:
 //   warp 0       one lane issues tcgen05.mma (and allocates tensor memory)
 //   warps 1-2    weights: one 16-slot page box per page and half by TMA, alternate tiles each (one
@@ -47,14 +47,15 @@ constexpr int kAtom = 16384;
 constexpr int kIdRing = 3;           // page scores: tiles whose page ids are fetched ahead
 constexpr int kLoaders = kAmaxPerTile;         // page scores: gathering warps
 
-// WIDE: up to 256 query rows; else up to 32 (more stages, two Q buffers).
+// WIDE: up to 256 query rows; else up to 32, two CTAs per SM (113 us a call against 117 with one CTA
+// of twice the stages, 128 x 8 lists of 512-4096 tokens).
 template <bool PAGES, bool WIDE>
 struct Cfg {
   static constexpr int kRowsMax = WIDE ? 256 : 32;
   static constexpr int kQBytes = kRowsMax * (PAGES ? 512 : 256);
-  static constexpr int kQBufs = WIDE ? 1 : 2;
+  static constexpr int kCtas = WIDE ? 1 : 2;   // per SM
   static_assert(WIDE || !PAGES, "page scores of few rows take the direct kernel below");
-  static constexpr int kStages = PAGES ? 3 : WIDE ? 4 : 6;
+  static constexpr int kStages = PAGES || !WIDE ? 3 : 4;
   // Weights of more than 32 rows: two sets share a tile, half of its columns each.  (The MMA stays
   // one of N = all rows: in halves of 128 it reads A twice, 128 bytes of shared memory a clock, and
   // the MMAs alone then took 99 us of what are 78 us of copies.)
@@ -63,8 +64,17 @@ struct Cfg {
   static constexpr int kSets = kSplit ? 4 : 2;                 // reducing sets of four warps
   static constexpr int kTmemCols = WIDE ? 512 : 128;
   static constexpr int kThreads = 128 + kSets * 128 + (PAGES ? kLoaders * 32 : 0);
-  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kQBufs) * kQBytes + kStages * kStage;
+  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kQBytes) + kStages * kStage;
 };
+
+// 16 bytes that are read once
+__device__ __forceinline__ uint4 ld_stream16(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
 
 // A walk over a CTA's share of the tiles.
 template <bool PAGES>
@@ -154,7 +164,7 @@ __device__ __forceinline__ void key_share(const KeyParams& p, int (&share)[4]) {
 }
 
 template <bool PAGES, bool WIDE>
-__global__ void __launch_bounds__(Cfg<PAGES, WIDE>::kThreads, 1)
+__global__ void __launch_bounds__(Cfg<PAGES, WIDE>::kThreads, Cfg<PAGES, WIDE>::kCtas)
 key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const KeyParams p) {
   using C = Cfg<PAGES, WIDE>;
@@ -163,9 +173,9 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sQ = base;
-  uint8_t* sA = base + C::kQBufs * C::kQBytes;
+  uint8_t* sA = base + C::kQBytes;
   __shared__ uint64_t bar_full[C::kStages], bar_empty[C::kStages];
-  __shared__ uint64_t bar_qfull[C::kQBufs], bar_qempty[C::kQBufs];
+  __shared__ uint64_t bar_qfull, bar_qempty;
   __shared__ uint64_t bar_dfull[C::kDBufs], bar_dempty[C::kDBufs], bar_lse[2], bar_done;
   __shared__ uint64_t bar_part[C::kSplit ? 4 : 1][4];        // second halves' sums: by tile, quadrant
   __shared__ float s_part[C::kSplit ? 4 : 1][C::kSplit ? 128 : 1];
@@ -184,10 +194,8 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       mbar_init(&bar_full[s], PAGES ? kLoaders : 1);
       mbar_init(&bar_empty[s], 1);
     }
-    for (int b = 0; b < C::kQBufs; ++b) {
-      mbar_init(&bar_qfull[b], PAGES ? kLoaders : 1);
-      mbar_init(&bar_qempty[b], 1);
-    }
+    mbar_init(&bar_qfull, PAGES ? kLoaders : 1);
+    mbar_init(&bar_qempty, 1);
     for (int b = 0; b < C::kDBufs; ++b) {
       mbar_init(&bar_dfull[b], 1);
       mbar_init(&bar_dempty[b], C::kSplit ? 8 : 4);   // the warps that read a tile
@@ -211,8 +219,8 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   }
   if (!PAGES) {
     // zero the padding rows of Q once: TMA writes rows 0 .. rows - 1 only
-    for (int a = 0; a < C::kQBufs * 2; ++a) {
-      uint8_t* z = sQ + (a >> 1) * C::kQBytes + ((a & 1) * n16 + p.rows) * 128;
+    for (int a = 0; a < 2; ++a) {
+      uint8_t* z = sQ + (a * n16 + p.rows) * 128;
       for (int o = threadIdx.x * 16; o < (n16 - p.rows) * 128; o += C::kThreads * 16)
         *reinterpret_cast<uint4*>(z + o) = make_uint4(0, 0, 0, 0);
     }
@@ -276,20 +284,16 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       int q = 0;
       for (KeyWalk<PAGES> w(p, s_share); w.left > 0 && ok; w.next()) {
         if (!w.fresh) continue;
-        const int qb = q % C::kQBufs;
-        if (!(ok = mbar_wait(&bar_qempty[qb], ((q / C::kQBufs) & 1) ^ 1, &abort_flag))) break;
-        mbar_arrive_expect_tx(&bar_qfull[qb], static_cast<uint32_t>(p.rows) * 256u);
+        if (!(ok = mbar_wait(&bar_qempty, (q & 1) ^ 1, &abort_flag))) break;
+        mbar_arrive_expect_tx(&bar_qfull, static_cast<uint32_t>(p.rows) * 256u);
         for (int h = 0; h < 2; ++h)
-          tma_load_3d(sQ + qb * C::kQBytes + h * n16 * 128, &tm_q, &bar_qfull[qb], h * 64,
-                      w.kvh * p.G, w.b * p.L + p.l0);
+          tma_load_3d(sQ + h * n16 * 128, &tm_q, &bar_qfull, h * 64, w.kvh * p.G, w.b * p.L + p.l0);
         ++q;
       }
       if (!ok) {
         int dummy = 0;
-        for (int b = 0; b < C::kQBufs; ++b) {
-          mbar_wait(&bar_qfull[b], 0, &dummy, 1000000ull);
-          mbar_wait(&bar_qfull[b], 1, &dummy, 1000000ull);
-        }
+        mbar_wait(&bar_qfull, 0, &dummy, 1000000ull);
+        mbar_wait(&bar_qfull, 1, &dummy, 1000000ull);
       }
     }
   } else if (PAGES && (warp == 1 || warp == 2)) {
@@ -385,9 +389,7 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     const int recip = (65536 + p.G - 1) / p.G;
     int q = 0;   // lists so far
     auto build_q = [&](int b, int kvh) {
-      const int qb = q % C::kQBufs;
-      if (!(ok = ok && mbar_wait_warp(&bar_qempty[qb], ((q / C::kQBufs) & 1) ^ 1, &abort_flag)))
-        return;
+      if (!(ok = ok && mbar_wait_warp(&bar_qempty, (q & 1) ^ 1, &abort_flag))) return;
       const uint16_t* base = p.q + (static_cast<size_t>(b) * p.L + p.l0) * p.Hq * 128 + kvh * p.G * 128;
 #pragma unroll 4
       for (int r = t >> 4; r < n16; r += 16) {
@@ -402,13 +404,13 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           hi[k] = x[k] & ~neg;
           lo[k] = x[k] & neg;
         }
-        uint8_t* d = sQ + qb * C::kQBytes + ((c16 >> 3) * n16 + r) * 128 + (((c16 & 7) ^ (r & 7)) << 4);
+        uint8_t* d = sQ + ((c16 >> 3) * n16 + r) * 128 + (((c16 & 7) ^ (r & 7)) << 4);
         *reinterpret_cast<uint4*>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4*>(d + 2 * n16 * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar_qfull[qb]);
+      if (lane == 0) mbar_arrive(&bar_qfull);
       ++q;
     };
     int id[8];
@@ -445,16 +447,16 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       for (KeyWalk<PAGES> w(p, s_share); w.left > 0 && ok; ++u) {
         if (w.fresh) {
           ++q;
-          if (!(ok = mbar_wait(&bar_qfull[q % C::kQBufs], (q / C::kQBufs) & 1, &abort_flag))) break;
+          if (!(ok = mbar_wait(&bar_qfull, q & 1, &abort_flag))) break;
         }
-        const int qb = q % C::kQBufs, db = u % C::kDBufs;
+        const int db = u % C::kDBufs;
         if (!(ok = mbar_wait(&bar_dempty[db], ((u / C::kDBufs) & 1) ^ 1, &abort_flag))) break;
         const uint32_t d = tmem + static_cast<uint32_t>(db * C::kRowsMax);
         for (int h = 0; h < kHalves; ++h, ++s) {
           const int st = s % C::kStages;
           if (!(ok = mbar_wait(&bar_full[st], (s / C::kStages) & 1, &abort_flag))) break;
           tc_fence_after();
-          const uint32_t qa = q_addr + qb * C::kQBytes + h * 2 * n16 * 128;
+          const uint32_t qa = q_addr + h * 2 * n16 * 128;
           const uint32_t aa = a_addr + st * kStage;
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
@@ -466,7 +468,7 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         if (!ok) break;
         umma_commit(&bar_dfull[db]);
         w.next();
-        if (w.left == 0 || w.fresh) umma_commit(&bar_qempty[qb]);
+        if (w.left == 0 || w.fresh) umma_commit(&bar_qempty);
       }
       umma_commit(&bar_done);
     }
@@ -623,7 +625,7 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 
 // Page scores of up to 32 query rows.  A page's 512 bytes take 2 * 16 to 32 rows * 256 flops: HBM
 // is the only bound, and staging pages in shared memory for tcgen05 (the kernel above) costs more
-// than it saves (42 us against XX us, 16 x 8 lists of 1875-3750 pages, 16 rows).  So each warp scores 16
+// than it saves (42 us against 35 us, 16 x 8 lists of 1875-3750 pages, 16 rows).  So each warp scores 16
 // pages with m16n8k16 straight from global memory: the order of the 256 values along K is free as
 // long as both operands have the same, so a lane's 16-byte chunk of a page row (8 values) serves as
 // its fragments of two MMAs, 16 loads a lane are in flight at once, and nothing is staged but q+ and
@@ -631,13 +633,6 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 constexpr int kDirectRows = 32;
 constexpr int kDirectPitch = 512 + 64;   // bytes of a q row: 64 more, so that 8 lanes miss no bank
 
-__device__ __forceinline__ uint4 ld_stream16(const uint4* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                           uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -778,6 +773,8 @@ page_scores_direct_kernel(const KeyParams p) {
 // Bounds of the full pages that hold tokens from .. to - 1: lo and hi over the 16 slots, per head
 // dim.  A thread takes 8 dims of one page and head: 16 independent 16-byte loads, then packed
 // bf16 minima and maxima (exact).  HBM bound: 4 KB read and 512 bytes written per page and head.
+// 32 prompts of 4096 tokens, 8 heads: 56 us a call with eight CTAs per SM and loads that pass L1 by;
+// 58 with sixteen CTAs per SM, 72 with four, 64 with sixteen and cached loads.
 __global__ void __launch_bounds__(128)
 page_bounds_kernel(const uint16_t* __restrict__ k_pages, const int32_t* __restrict__ page_table,
                    const int32_t* __restrict__ from, const int32_t* __restrict__ to, int Hkv,
@@ -805,7 +802,7 @@ page_bounds_kernel(const uint16_t* __restrict__ k_pages, const int32_t* __restri
     const uint4* src = reinterpret_cast<const uint4*>(k_pages) + static_cast<size_t>(id) * kPageTokens * per + c;
     uint4 v[kPageTokens];
 #pragma unroll
-    for (int s = 0; s < kPageTokens; ++s) v[s] = __ldg(src + static_cast<size_t>(s) * per);
+    for (int s = 0; s < kPageTokens; ++s) v[s] = ld_stream16(src + static_cast<size_t>(s) * per);
     uint32_t lo[4], hi[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -841,7 +838,8 @@ cudaError_t launch_key_t(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const
   });
   if (e != cudaSuccess) return e;
   const long long most = static_cast<long long>(p.B) * p.Hkv * p.max_tiles;
-  const int grid = static_cast<int>(most < num_sms ? most : num_sms);
+  const long long ctas = static_cast<long long>(num_sms) * C::kCtas;
+  const int grid = static_cast<int>(most < ctas ? most : ctas);
   return launch_pdl(key_reduce_kernel<PAGES, WIDE>, dim3(grid), dim3(C::kThreads), C::kSmem, stream,
                     tm_q, tm_k, p);
 }
@@ -878,8 +876,8 @@ cudaError_t launch_page_bounds(const uint16_t* k_pages, const int32_t* page_tabl
                                const int32_t* from, const int32_t* to, int B, int Hkv,
                                int max_pages, int num_pages, int num_sms, uint16_t* bounds,
                                int* err, cudaStream_t stream) {
-  // about 16 CTAs of 128 threads per SM in all, and no more per sequence than its pages can use
-  long long ctas = (16ll * num_sms + B - 1) / B;
+  // about 8 CTAs of 128 threads per SM in all, and no more per sequence than its pages can use
+  long long ctas = (8ll * num_sms + B - 1) / B;
   const long long most = (static_cast<long long>(max_pages) * Hkv * 16 + 127) / 128;
   if (ctas > most) ctas = most;
   return launch_pdl(page_bounds_kernel, dim3(static_cast<unsigned>(ctas * B)), dim3(128), 0, stream,

@@ -617,6 +617,7 @@ evict_select_kernel(const EvictParams p) {
     T = kth_largest<uint32_t>(
         k, lo, hi,
         [&](auto&& f) {
+#pragma unroll 4
           for (int i = tid; i < cand; i += kEvictThreads) f(key_at(i));
         },
         hist, s_scan, s_pick, &above);
@@ -626,15 +627,13 @@ evict_select_kernel(const EvictParams p) {
   const int stretch = ((n + kEvictWarps - 1) / kEvictWarps + 31) & ~31;
   const int s0 = warp * stretch, s1 = min(n, s0 + stretch);
   auto look = [&](int i, bool& gt, bool& eq) {
-    gt = i < n && i >= cand;
-    eq = false;
-    if (k > 0 && i < cand) {
-      const uint32_t key = key_at(i);
-      gt = key > T;
-      eq = key == T;
-    }
+    const uint32_t key = k > 0 ? key_at(min(i, cand - 1)) : 0;
+    const bool old = i < cand;
+    gt = old ? k > 0 && key > T : i < n;
+    eq = old && k > 0 && key == T;
   };
   int g = 0, e = 0;
+#pragma unroll 4
   for (int i = s0 + lane; i - lane < s1; i += 32) {
     bool gt, eq;
     look(i, gt, eq);
