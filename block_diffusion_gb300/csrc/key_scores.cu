@@ -55,7 +55,7 @@ struct Cfg {
   static constexpr int kQBytes = kRowsMax * (PAGES ? 512 : 256);
   static constexpr int kCtas = WIDE ? 1 : 2;   // per SM
   static_assert(WIDE || !PAGES, "page scores of few rows take the direct kernel below");
-  static constexpr int kStages = PAGES || !WIDE ? 3 : 4;
+  static constexpr int kStages = 3;
   // Weights of more than 32 rows: two sets share a tile, half of its columns each.  (The MMA stays
   // one of N = all rows: in halves of 128 it reads A twice, 128 bytes of shared memory a clock, and
   // the MMAs alone then took 99 us of what are 78 us of copies.)
@@ -64,7 +64,13 @@ struct Cfg {
   static constexpr int kSets = kSplit ? 4 : 2;                 // reducing sets of four warps
   static constexpr int kTmemCols = WIDE ? 512 : 128;
   static constexpr int kThreads = 128 + kSets * 128 + (PAGES ? kLoaders * 32 : 0);
-  static constexpr size_t kSmem = 1024 + static_cast<size_t>(kQBytes) + kStages * kStage;
+  // Weights of more than 32 rows: -lse / scale enters X through the MMA, as three bf16 numbers a row
+  // (24 bits) against keys of 1, so that the reduction reads no table from shared memory beside
+  // the MMAs (95 us a pass against 100, 16 x 64 x 4 rows over 8192-16384 tokens): 128-byte rows of which a K
+  // step of 16 is used, one of 1s for the keys.
+  static constexpr int kLseBytes = kSplit ? kRowsMax * 128 : 0, kOneBytes = kSplit ? kKeys * 128 : 0;
+  static constexpr size_t kSmem =
+      1024 + static_cast<size_t>(kQBytes) + kLseBytes + kOneBytes + kStages * kStage;
 };
 
 // 16 bytes that are read once
@@ -173,7 +179,9 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   uint8_t* sQ = base;
-  uint8_t* sA = base + C::kQBytes;
+  uint8_t* sL = base + C::kQBytes;
+  uint8_t* sOne = sL + C::kLseBytes;
+  uint8_t* sA = sOne + C::kOneBytes;
   __shared__ uint64_t bar_full[C::kStages], bar_empty[C::kStages];
   __shared__ uint64_t bar_qfull, bar_qempty;
   __shared__ uint64_t bar_dfull[C::kDBufs], bar_dempty[C::kDBufs], bar_lse[2], bar_done;
@@ -185,7 +193,8 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   __shared__ uint64_t bar_ids[PAGES ? kIdRing : 1], bar_ids_free[PAGES ? kIdRing : 1];
   __shared__ int s_ids[PAGES ? kIdRing : 1][PAGES ? kKeys : 1];
   __shared__ int s_share[4];
-  __shared__ __align__(16) float s_lse[PAGES ? 1 : 2][PAGES ? 4 : C::kRowsMax];   // log2 units
+  constexpr bool kTable = !PAGES && !C::kSplit;   // -lse in shared memory (log2 units)
+  __shared__ __align__(16) float s_lse[kTable ? 2 : 1][kTable ? C::kRowsMax : 4];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n16 = (p.rows + 15) & ~15;   // columns of X
@@ -194,7 +203,7 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       mbar_init(&bar_full[s], PAGES ? kLoaders : 1);
       mbar_init(&bar_empty[s], 1);
     }
-    mbar_init(&bar_qfull, PAGES ? kLoaders : 1);
+    mbar_init(&bar_qfull, PAGES ? kLoaders : C::kSplit ? 2 : 1);
     mbar_init(&bar_qempty, 1);
     for (int b = 0; b < C::kDBufs; ++b) {
       mbar_init(&bar_dfull[b], 1);
@@ -223,6 +232,15 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       uint8_t* z = sQ + (a * n16 + p.rows) * 128;
       for (int o = threadIdx.x * 16; o < (n16 - p.rows) * 128; o += C::kThreads * 16)
         *reinterpret_cast<uint4*>(z + o) = make_uint4(0, 0, 0, 0);
+    }
+    if constexpr (C::kSplit) {
+      // the K step of -lse: each key's row is 1, 1, 1, 0 ...; what the queries' rows do not use is 0
+      for (int c = threadIdx.x; c < (C::kRowsMax + kKeys) * 2; c += C::kThreads) {
+        const int r = c >> 1;
+        const bool ones = r >= C::kRowsMax && (c & 1) == 0;
+        *reinterpret_cast<uint4*>(sL + r * 128 + (((c & 1) ^ (r & 7)) << 4)) =
+            ones ? make_uint4(0x3F803F80u, 0x3F80u, 0, 0) : make_uint4(0, 0, 0, 0);
+      }
     }
     fence_proxy_async_smem();
   }
@@ -278,24 +296,45 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       __syncwarp();
     }
   } else if (!PAGES && warp == 3) {
-    // ------------------------------------------------------------ TMA: Q
-    if (lane == 0) {
-      bool ok = true;
-      int q = 0;
-      for (KeyWalk<PAGES> w(p, s_share); w.left > 0 && ok; w.next()) {
-        if (!w.fresh) continue;
-        if (!(ok = mbar_wait(&bar_qempty, (q & 1) ^ 1, &abort_flag))) break;
+    // ------------------------------------------------------------ TMA: Q; and -lse / scale
+    bool ok = true;
+    int q = 0;
+    const float unscale = -1.4426950408889634f / p.scale_log2;
+    for (KeyWalk<PAGES> w(p, s_share); w.left > 0 && ok; w.next()) {
+      if (!w.fresh) continue;
+      if (!(ok = mbar_wait_warp(&bar_qempty, (q & 1) ^ 1, &abort_flag))) break;
+      if (lane == 0) {
         mbar_arrive_expect_tx(&bar_qfull, static_cast<uint32_t>(p.rows) * 256u);
         for (int h = 0; h < 2; ++h)
           tma_load_3d(sQ + h * n16 * 128, &tm_q, &bar_qfull, h * 64, w.kvh * p.G, w.b * p.L + p.l0);
-        ++q;
       }
-      if (!ok) {
-        int dummy = 0;
-        mbar_wait(&bar_qfull, 0, &dummy, 1000000ull);
-        mbar_wait(&bar_qfull, 1, &dummy, 1000000ull);
+      if constexpr (C::kSplit) {
+#pragma unroll 4
+        for (int n = lane; n < n16; n += 32) {
+          float c = -1e30f;   // padding rows: 2^(a very negative number) = 0
+          if (n < p.rows)
+            c = __ldg(p.lse + (static_cast<size_t>(w.b) * p.L + p.l0 + n / p.G) * p.Hq +
+                      w.kvh * p.G + n % p.G) * unscale;
+          const __nv_bfloat16 hi = __float2bfloat16_rn(c);
+          const float c1 = c - __bfloat162float(hi);
+          const __nv_bfloat16 mid = __float2bfloat16_rn(c1);
+          const __nv_bfloat16 lo = __float2bfloat16_rn(c1 - __bfloat162float(mid));
+          *reinterpret_cast<uint2*>(sL + n * 128 + ((n & 7) << 4)) =
+              make_uint2(__bfloat16_as_ushort(hi) | static_cast<uint32_t>(__bfloat16_as_ushort(mid)) << 16,
+                         __bfloat16_as_ushort(lo));
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_qfull);
       }
+      ++q;
     }
+    if (!ok && lane == 0) {
+      int dummy = 0;
+      mbar_wait(&bar_qfull, 0, &dummy, 1000000ull);
+      mbar_wait(&bar_qfull, 1, &dummy, 1000000ull);
+    }
+    __syncwarp();
   } else if (PAGES && (warp == 1 || warp == 2)) {
     // ------------------------------------------------------------ page ids and L2, tiles ahead
     const int t = threadIdx.x - 32;   // 0 .. 63: pages t and t + 64 of a tile
@@ -466,6 +505,8 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           umma_commit(&bar_empty[st]);
         }
         if (!ok) break;
+        if constexpr (C::kSplit)   // - lse / scale last: the sum is small then, and rounded once
+          umma_bf16(d, smem_desc(smem_u32(sOne), 16, 1024), smem_desc(smem_u32(sL), 16, 1024), idesc, 1u);
         umma_commit(&bar_dfull[db]);
         w.next();
         if (w.left == 0 || w.fresh) umma_commit(&bar_qempty);
@@ -480,7 +521,7 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     int u = 0, q = 0;
     const float* lse = s_lse[0];
     for (KeyWalk<PAGES> w(p, s_share); w.left > 0 && ok; w.next(), ++u) {
-      if constexpr (!PAGES) {
+      if constexpr (kTable) {
         if (w.fresh) {
           // the warps fill one of two buffers and wait for each other: a warp that writes
           // buffer x has seen every warp start the list between, so all are done with the list
@@ -540,11 +581,11 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         // two columns per packed instruction
         const float2 cs2 = make_float2(p.scale_log2, p.scale_log2);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        const float* nlse = lse + half * split;
         columns([&](int c, const uint32_t (&x)[16]) {
 #pragma unroll
           for (int k = 0; k < 16; k += 4) {
-            const float4 l4 = *reinterpret_cast<const float4*>(nlse + c + k);
+            float4 l4 = make_float4(0.f, 0.f, 0.f, 0.f);   // (X holds -lse already)
+            if constexpr (kTable) l4 = *reinterpret_cast<const float4*>(lse + c + k);
             const float2 a = __ffma2_rn(
                 make_float2(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), cs2,
                 make_float2(l4.x, l4.y));
