@@ -94,7 +94,10 @@ int ensure(void** ptr, size_t* cap, size_t need, bool zero, bdlm_stream stream =
   if (n < 2 * *cap) n = 2 * *cap;
   if (*ptr && cudaDeviceSynchronize() != cudaSuccess) return BDLM_ERR_CUDA;
   void* fresh = nullptr;
-  if (cudaMalloc(&fresh, n) != cudaSuccess) return BDLM_ERR_NOMEM;
+  if (cudaMalloc(&fresh, n) != cudaSuccess) {
+    n = need;   // no room to spare: just what the call needs
+    if (cudaMalloc(&fresh, n) != cudaSuccess) return BDLM_ERR_NOMEM;
+  }
   if (zero && (cudaMemset(fresh, 0, n) != cudaSuccess ||
                cudaStreamSynchronize(nullptr) != cudaSuccess)) {   // `stream` may not wait for it
     cudaFree(fresh);

@@ -1249,11 +1249,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             }
           }
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1)
-              mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], off));
-          }
+          for (int k = 0; k < 16; ++k) mx[k] = warp_max(mx[k]);
           if (lane == 0) {
 #pragma unroll
             for (int k = 0; k < 16; ++k) s_red[q4][cg * 16 + k] = mx[k];

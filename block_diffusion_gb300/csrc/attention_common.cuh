@@ -176,6 +176,14 @@ __device__ __forceinline__ float row_lse(float m, float l, float scale_log2) {
   return l > 0.f ? fmaf(m, scale_log2, __log2f(l)) * kLn2 : -CUDART_INF_F;
 }
 
+// Maximum over the warp in one instruction (redux.sync of float32, sm_100 family); a NaN counts as
+// no value, as in fmaxf.
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Writes 128 bytes per lane to global memory (lane l: w, the 32 words of its row piece; dst,
 // where they go, or null for nothing) through a 1 KB shared-memory staging buffer, 8 rows at a
 // time, so that each global store instruction writes four whole 128-byte row pieces instead of

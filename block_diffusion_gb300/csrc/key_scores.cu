@@ -16,9 +16,10 @@
 //
 // (Page scores of up to 32 rows: a kernel of its own, below.)
 //
-// Persistent CTAs, one or two per SM, each take an equal, contiguous share of all tiles of 128 keys, laid end to
-// end list by list (a list = sequence and KV head): equal bytes per CTA whatever the lengths, and Q
-// changes only where a list ends.  Every warp walks the share by itself, so no warp hands out work:
+// Persistent CTAs, one or two per SM, each take an equal, contiguous share of all tiles of 128 keys,
+// laid end to end list by list (a list = sequence and KV head): equal bytes per CTA whatever the
+// lengths, and Q changes only where a list ends.  Every warp walks the share by itself, so no warp
+// hands out work:
 //   warp 0       one lane issues tcgen05.mma (and allocates tensor memory)
 //   warps 1-2    weights: one 16-slot page box per page and half by TMA, alternate tiles each (one
 //                warp's 16 boxes take about 1 us)
@@ -66,8 +67,8 @@ struct Cfg {
   static constexpr int kThreads = 128 + kSets * 128 + (PAGES ? kLoaders * 32 : 0);
   // Weights of more than 32 rows: -lse / scale enters X through the MMA, as three bf16 numbers a row
   // (24 bits) against keys of 1, so that the reduction reads no table from shared memory beside
-  // the MMAs (95 us a pass against 100, 16 x 64 x 4 rows over 8192-16384 tokens): 128-byte rows of which a K
-  // step of 16 is used, one of 1s for the keys.
+  // the MMAs (95 us a pass against 100, 16 x 64 x 4 rows over 8192-16384 tokens): 128-byte rows of
+  // which a K step of 16 is used, one of 1s for the keys.
   static constexpr int kLseBytes = kSplit ? kRowsMax * 128 : 0, kOneBytes = kSplit ? kKeys * 128 : 0;
   static constexpr size_t kSmem =
       1024 + static_cast<size_t>(kQBytes) + kLseBytes + kOneBytes + kStages * kStage;
@@ -552,7 +553,7 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       }
       if constexpr (!PAGES) {
         wp = p.weights + w.row() * (static_cast<size_t>(p.max_pages) * kPageTokens) + key;
-        if (live && half == 0) w_old = *wp;
+        if (live && half == 0) w_old = __ldcg(wp);
       }
       const int db = u % C::kDBufs;
       const int split = C::kSplit ? ((n16 >> 1) + 15) & ~15 : 0;   // columns of the first half
