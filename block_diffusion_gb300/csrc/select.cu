@@ -128,7 +128,8 @@ __device__ __forceinline__ K kth_largest(int k, K lo, K hi, Each&& each, int* hi
     reinterpret_cast<int4*>(hist)[threadIdx.x] = make_int4(0, 0, 0, 0);
     __syncthreads();
     each([&](K key) {
-      if (key >= lo && key <= hi) atomicAdd(&hist[static_cast<int>((key - lo) >> shift)], 1);
+      const K off = key - lo;   // (below lo: wraps past the range)
+      if (off <= range) atomicAdd(&hist[static_cast<int>(off >> shift)], 1);
     });
     __syncthreads();
     // this thread's four buckets, counted from the top
@@ -154,8 +155,9 @@ __device__ __forceinline__ K kth_largest(int k, K lo, K hi, Each&& each, int* hi
     if (hi - from > width) hi = from + width;
     lo = from;
     if (count <= kDirect && lo < hi) {
+      const K span = hi - lo;
       each([&](K key) {
-        if (key >= lo && key <= hi) few[atomicAdd(&s_scan[35], 1)] = key;
+        if (key - lo <= span) few[atomicAdd(&s_scan[35], 1)] = key;
       });
       __syncthreads();
       int more;
@@ -623,56 +625,70 @@ evict_select_kernel(const EvictParams p) {
         hist, s_scan, s_pick, &above);
   }
   const int ties = k - above;   // tokens of weight T that stay
-  // this warp's stretch: what it keeps for sure (g) and what equals T (e)
-  const int stretch = ((n + kEvictWarps - 1) / kEvictWarps + 31) & ~31;
-  const int s0 = warp * stretch, s1 = min(n, s0 + stretch);
-  auto look = [&](int i, bool& gt, bool& eq) {
-    const uint32_t key = k > 0 ? key_at(min(i, cand - 1)) : 0;
-    const bool old = i < cand;
-    gt = old ? k > 0 && key > T : i < n;
-    eq = old && k > 0 && key == T;
-  };
-  int g = 0, e = 0;
+  // the last `recent` tokens stay, in the last places
+  for (int j = k + tid; j < p.keep; j += kEvictThreads) {
+    const int i = n - p.keep + j;
+    kept[j] = i;
+    if (!in_place) to[j] = __ldcg(w + i);
+  }
+  if (k > 0) {
+    // this warp's stretch: what it keeps for sure (g) and what equals T (e)
+    const int stretch = ((cand + kEvictWarps - 1) / kEvictWarps + 31) & ~31;
+    const int s0 = warp * stretch, s1 = min(cand, s0 + stretch);
+    int g = 0, e = 0;
 #pragma unroll 4
-  for (int i = s0 + lane; i - lane < s1; i += 32) {
-    bool gt, eq;
-    look(i, gt, eq);
-    g += __popc(__ballot_sync(0xffffffffu, gt));
-    e += __popc(__ballot_sync(0xffffffffu, eq));
-  }
-  if (lane == 0) {
-    s_gt[warp] = g;
-    s_eq[warp] = e;
-  }
-  __syncthreads();
-  g = e = 0;
-  for (int x = 0; x < warp; ++x) {
-    g += s_gt[x];
-    e += s_eq[x];
-  }
-  const uint32_t below = (1u << lane) - 1u;
-  constexpr int kWalk = 8;   // rounds whose weights are loaded together
-  for (int i0 = s0 + lane; i0 - lane < s1; i0 += 32 * kWalk) {
-    float v[kWalk];
-    if (!in_place) {
-#pragma unroll
-      for (int x = 0; x < kWalk; ++x) v[x] = i0 + 32 * x < s1 ? __ldcg(w + i0 + 32 * x) : 0.f;
+    for (int i = s0 + lane; i < s1; i += 32) {
+      const uint32_t key = key_at(i);
+      g += key > T;
+      e += key == T;
     }
-#pragma unroll
-    for (int x = 0; x < kWalk; ++x) {
-      const int i = i0 + 32 * x;
-      if (i - lane >= s1) break;
-      bool gt, eq;
-      look(i, gt, eq);
-      const uint32_t bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
-      const int eq_before = e + __popc(be & below);
-      if (gt || (eq && eq_before < ties)) {
-        const int at = g + __popc(bg & below) + min(eq_before, ties);
-        kept[at] = i;
-        if (!in_place) to[at] = v[x];
+    g = __reduce_add_sync(0xffffffffu, g);
+    e = __reduce_add_sync(0xffffffffu, e);
+    if (lane == 0) {
+      s_gt[warp] = g;
+      s_eq[warp] = e;
+    }
+    __syncthreads();
+    g = e = 0;
+    int all = 0;
+    for (int x = 0; x < kEvictWarps; ++x) {
+      if (x < warp) {
+        g += s_gt[x];
+        e += s_eq[x];
       }
-      g += __popc(bg);
-      e += __popc(be);
+      all += s_eq[x];
+    }
+    // mostly all tokens of weight T stay (there is one): then one comparison decides a token
+    const bool whole = all == ties;
+    int at = g + (whole ? e : min(e, ties));
+    const uint32_t below = (1u << lane) - 1u;
+    constexpr int kWalk = 8;   // rounds whose weights are loaded together
+    for (int i0 = s0 + lane; i0 - lane < s1; i0 += 32 * kWalk) {
+      float v[kWalk];
+      if (!in_place) {
+#pragma unroll
+        for (int x = 0; x < kWalk; ++x) v[x] = i0 + 32 * x < s1 ? __ldcg(w + i0 + 32 * x) : 0.f;
+      }
+#pragma unroll
+      for (int x = 0; x < kWalk; ++x) {
+        const int i = i0 + 32 * x;
+        if (i - lane >= s1) break;
+        const uint32_t key = i < s1 ? key_at(i) : 0;
+        bool in = i < s1 && key >= T;
+        if (!whole) {
+          const bool eq = in && key == T;
+          const uint32_t be = __ballot_sync(0xffffffffu, eq);
+          if (eq) in = e + __popc(be & below) < ties;
+          e += __popc(be);
+        }
+        const uint32_t bits = __ballot_sync(0xffffffffu, in);
+        if (in) {
+          const int j = at + __popc(bits & below);
+          kept[j] = i;
+          if (!in_place) to[j] = v[x];
+        }
+        at += __popc(bits);
+      }
     }
   }
   if (!in_place) return;
