@@ -312,12 +312,13 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       if constexpr (C::kSplit) {
 #pragma unroll 4
         for (int n = lane; n < n16; n += 32) {
-          float c = -1e30f;   // padding rows: 2^(a very negative number) = 0
+          float c = -CUDART_INF_F;   // padding rows: 2^-inf = 0
           if (n < p.rows)
             c = __ldg(p.lse + (static_cast<size_t>(w.b) * p.L + p.l0 + n / p.G) * p.Hq +
                       w.kvh * p.G + n % p.G) * unscale;
           const __nv_bfloat16 hi = __float2bfloat16_rn(c);
-          const float c1 = c - __bfloat162float(hi);
+          // (past bf16's range, a query that is left out: infinite, with nothing to add to it)
+          const float c1 = fabsf(__bfloat162float(hi)) < CUDART_INF_F ? c - __bfloat162float(hi) : 0.f;
           const __nv_bfloat16 mid = __float2bfloat16_rn(c1);
           const __nv_bfloat16 lo = __float2bfloat16_rn(c1 - __bfloat162float(mid));
           *reinterpret_cast<uint2*>(sL + n * 128 + ((n & 7) << 4)) =

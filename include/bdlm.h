@@ -430,7 +430,7 @@ int bdlm_sparse_attention(const bdlm_attn_desc* desc, const bdlm_bf16* q, const 
  *                        + sum over i, h with h / (Hq/Hkv) = g of exp(sm_scale * q[b,i,h] . K_b[j,g] - lse[b,i,h])
  * with lse from bdlm_tree_attention on the same queries, so the sum adds up attention
  * probabilities.  Later positions (the block's, and behind) are left as they were.
- *   lse      [B, L, Hq] float
+ *   lse      [B, L, Hq] float; +inf leaves a query out
  *   weights  [B, Hkv, max_pages_per_seq * 16] float, updated in place
  * decay is finite (1: plain accumulation, 0: this step alone; weights must be finite in any case).
  * Tokens of a page with a bad id are left as they were.  Other arguments as bdlm_block_attention.

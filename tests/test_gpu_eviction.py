@@ -47,6 +47,30 @@ def test_attention_weights(lib, L, Hq, Hkv, lens, decay):
         assert np.array_equal(host(w)[b, :, lens[b]:], w0[b, :, lens[b]:])
 
 
+@pytest.mark.parametrize("L,Hq,Hkv", [(4, 16, 8), (5, 24, 2), (64, 32, 8)])
+def test_weights_of_queries_left_out(lib, L, Hq, Hkv):
+    """A query whose lse is +inf adds nothing, for few query rows and for many alike."""
+    import torch
+    rng = np.random.default_rng(L)
+    a = W.make_attention(rng, 2, L, Hq, Hkv, 128, prefix_lens=np.array([300, 40]), qkv_std=1.0)
+    P = a.page_table_ref.shape[1]
+    d = lib.attn_desc(2, L, Hq, Hkv, 128, P, a.k_ref.shape[0])
+    lse = (5 + rng.random((2, L, Hq))).astype(np.float32)
+    lse[:, 0] = np.inf
+    lse[1, :, 1] = np.inf
+    lse[1, -1, -1] = 3.4e38   # as good as
+    w0 = np.zeros((2, Hkv, P * 16), np.float32)
+    w = dev(w0)
+    lib.bdlm_attention_weights(d, bf16_tensor(a.q), bf16_tensor(a.k_ref), dev(a.page_table_ref),
+                               dev(a.prefix_lens), dev(lse), 1.0, w)
+    torch.cuda.synchronize()
+    assert lib.bdlm_device_error() == 0
+    want, add, s1 = R.attention_weights(a.q, a.k_ref, a.page_table_ref, a.prefix_lens, lse, 1.0, w0, Hkv)
+    # as test_attention_weights
+    tol = add * (2 * R.score_error(s1) + 2.0 ** -15 + 3 * 2.0 ** -17) + 4 * 2.0 ** -24 * np.abs(want)
+    assert np.all(np.abs(host(w).astype(np.float64) - want) <= tol + 1e-30)
+
+
 def test_weights_flag_bad_pages_and_lengths(lib):
     import torch
     rng = np.random.default_rng(2)
