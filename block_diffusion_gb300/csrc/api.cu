@@ -792,6 +792,7 @@ int bdlm_attention_weights(const bdlm_attn_desc* desc, const bdlm_bf16* q,
                            float* weights, bdlm_stream stream) {
   if (!desc || !attn_desc_ok(*desc) || !isfinite(decay)) return BDLM_ERR_INVALID;
   const bdlm_attn_desc d = *desc;
+  if (d.sm_scale > 0.f && d.sm_scale < 0x1p-64f) return BDLM_ERR_UNSUPPORTED;   // lse / sm_scale
   if (d.B == 0) return BDLM_OK;
   if (!q || !k_pages || !page_table || !prefix_lens || !lse || !weights || !aligned16(q) ||
       !aligned16(k_pages))

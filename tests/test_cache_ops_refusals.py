@@ -94,6 +94,12 @@ def test_sizes(so):
         assert compact(so, **bad) == -1, bad
 
 
+def test_weights_refuse_a_vanishing_scale(so):
+    for scale in (1e-38, 2.0 ** -65):
+        assert weights(so, desc(B=0, sm_scale=scale)) == -3, scale
+    assert weights(so, desc(B=0, sm_scale=2.0 ** -64)) == 0
+
+
 def test_empty_calls_succeed_without_a_device(so):
     for call in (tree, bounds, select, sparse, weights, evict, compact):
         assert call(so, desc(B=0)) == 0
