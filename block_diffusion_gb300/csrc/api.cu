@@ -633,6 +633,10 @@ bool cache_desc_ok(const bdlm_attn_desc& d) {
          static_cast<long long>(d.max_pages_per_seq) * d.page_size <= 0x7FFFFFFFll;
 }
 
+// The kernels that walk a sequence's tokens count them, and a few thousand past its end, in 32 bits.
+constexpr int kMaxTokens = 1 << 30;
+bool too_many_tokens(const bdlm_attn_desc& d) { return d.max_pages_per_seq > kMaxTokens / 16; }
+
 bdlm::KeyParams key_params(const bdlm_attn_desc& d, const int32_t* page_table,
                            const int32_t* prefix_lens, int* err) {
   bdlm::KeyParams p = {};
@@ -691,6 +695,7 @@ int bdlm_page_bounds(const bdlm_attn_desc* desc, const bdlm_bf16* k_pages,
                      bdlm_bf16* bounds, bdlm_stream stream) {
   if (!desc || !cache_desc_ok(*desc)) return BDLM_ERR_INVALID;
   const bdlm_attn_desc d = *desc;
+  if (too_many_tokens(d)) return BDLM_ERR_UNSUPPORTED;
   if (d.B == 0) return BDLM_OK;
   if (!k_pages || !page_table || !to_lens || !bounds || !aligned16(k_pages) || !aligned16(bounds))
     return BDLM_ERR_INVALID;
@@ -792,6 +797,7 @@ int bdlm_attention_weights(const bdlm_attn_desc* desc, const bdlm_bf16* q,
                            float* weights, bdlm_stream stream) {
   if (!desc || !attn_desc_ok(*desc) || !isfinite(decay)) return BDLM_ERR_INVALID;
   const bdlm_attn_desc d = *desc;
+  if (too_many_tokens(d)) return BDLM_ERR_UNSUPPORTED;
   if (d.sm_scale > 0.f && d.sm_scale < 0x1p-64f) return BDLM_ERR_UNSUPPORTED;   // lse / sm_scale
   if (d.B == 0) return BDLM_OK;
   if (!q || !k_pages || !page_table || !prefix_lens || !lse || !weights || !aligned16(q) ||
@@ -846,6 +852,7 @@ int bdlm_evict_kv(const bdlm_attn_desc* desc, bdlm_bf16* k_pages, bdlm_bf16* v_p
   if (keep < 1 || keep > static_cast<long long>(d.max_pages_per_seq) * d.page_size || recent < 0 ||
       recent > keep)
     return BDLM_ERR_INVALID;
+  if (too_many_tokens(d)) return BDLM_ERR_UNSUPPORTED;
   if (d.B == 0) return BDLM_OK;
   if (!k_pages || !v_pages || !page_table || !lens || !weights || !to_table || !to_weights ||
       !kept || !new_lens || lens == new_lens || !aligned16(k_pages) || !aligned16(v_pages))
@@ -869,6 +876,7 @@ int bdlm_compact_kv(const bdlm_attn_desc* desc, bdlm_bf16* k_pages, bdlm_bf16* v
   if (!desc || !cache_desc_ok(*desc)) return BDLM_ERR_INVALID;
   const bdlm_attn_desc d = *desc;
   if ((heads != 1 && heads != d.Hkv) || n_max < 0) return BDLM_ERR_INVALID;
+  if (too_many_tokens(d) || n_max > kMaxTokens) return BDLM_ERR_UNSUPPORTED;
   if (d.B == 0 || n_max == 0) return BDLM_OK;
   if (!k_pages || !v_pages || !page_table || !idx || !counts || !to_table || !aligned16(k_pages) ||
       !aligned16(v_pages))

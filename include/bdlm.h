@@ -365,10 +365,14 @@ int bdlm_tree_attention(const bdlm_attn_desc* desc, const bdlm_bf16* q, const bd
  *              increasing and >= 0 within a list
  *   counts     [B] int32
  *   to_table   [B, max_pages_per_seq] int32: the pages written.  Either page_table itself (the
- *              same pointer): in place; or pages that no page_table row of the call lists.
+ *              same pointer): in place; or pages that no page_table row of the call lists.  A page
+ *              that is written belongs to one sequence: pages of a shared prefix stay as they are
+ *              only while no token moves into them.
  * Slots that no token moves to are left as they were.  An index below 0, a token past the page
  * table or a bad page id skips that token and sets a device error bit (ROW, LENGTH, PAGE).  desc as
  * bdlm_write_block_kv (L unused).  k_pages, v_pages 16-byte aligned.  n_max == 0 is a no-op.
+ * max_pages_per_seq > 2^26 (2^30 tokens; also for bdlm_page_bounds, bdlm_attention_weights and
+ * bdlm_evict_kv) or n_max > 2^30 returns BDLM_ERR_UNSUPPORTED.
  */
 int bdlm_compact_kv(const bdlm_attn_desc* desc, bdlm_bf16* k_pages, bdlm_bf16* v_pages,
                     const int32_t* page_table, const int32_t* base_lens, const int32_t* idx,

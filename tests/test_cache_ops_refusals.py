@@ -94,6 +94,17 @@ def test_sizes(so):
         assert compact(so, **bad) == -1, bad
 
 
+@pytest.mark.parametrize("call", [bounds, weights, evict, compact])
+def test_a_table_beyond_the_token_counters(so, call):
+    assert call(so, desc(B=0, cols=2 ** 26 + 1)) == -3
+    assert call(so, desc(B=0, cols=2 ** 26)) == 0
+
+
+def test_counts_beyond_the_token_counters(so):
+    assert compact(so, desc(B=0), n_max=2 ** 30 + 1) == -3
+    assert compact(so, desc(B=0), n_max=2 ** 30) == 0
+
+
 def test_weights_refuse_a_vanishing_scale(so):
     for scale in (1e-38, 2.0 ** -65):
         assert weights(so, desc(B=0, sm_scale=scale)) == -3, scale
