@@ -554,7 +554,7 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       }
       if constexpr (!PAGES) {
         wp = p.weights + w.row() * (static_cast<size_t>(p.max_pages) * kPageTokens) + key;
-        if (live && half == 0) w_old = __ldcg(wp);
+        if (live && half == 0 && p.decay != 0.f) w_old = __ldcg(wp);
       }
       const int db = u % C::kDBufs;
       const int split = C::kSplit ? ((n16 >> 1) + 15) & ~15 : 0;   // columns of the first half

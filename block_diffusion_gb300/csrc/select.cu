@@ -277,8 +277,8 @@ __device__ __forceinline__ unsigned long long exact_score(const SelectParams& p,
 // Bound by latency: a dozen barriers and half a dozen loads that depend on each other.  So what can
 // be asked for early is, a thread keeps its first eight keys in registers, and the exact scores
 // of one page are spread over warps.
-// CTAS: 1 with all the registers it wants, for no more lists than SMs (128 lists: a call of 58 us
-// against 63 with two CTAs per SM); 2 for more lists (1024: 71 us against 85).
+// CTAS: 1 with all the registers it wants, for no more lists than SMs (128 lists of 1875-3750 pages:
+// a call of 52 us against 56 with two CTAs per SM); 2 for more lists (1024 of 125-375: 70 against 83).
 template <int CTAS>
 __global__ void __launch_bounds__(kSelThreads, CTAS)
 select_pages_kernel(const SelectParams p) {

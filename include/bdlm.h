@@ -436,7 +436,7 @@ int bdlm_sparse_attention(const bdlm_attn_desc* desc, const bdlm_bf16* q, const 
  * probabilities.  Later positions (the block's, and behind) are left as they were.
  *   lse      [B, L, Hq] float; +inf leaves a query out
  *   weights  [B, Hkv, max_pages_per_seq * 16] float, updated in place
- * decay is finite (1: plain accumulation, 0: this step alone; weights must be finite in any case).
+ * decay is finite (1: plain accumulation, 0: this step alone, whatever weights held).
  * Tokens of a page with a bad id are left as they were.  Other arguments as bdlm_block_attention; a
  * positive sm_scale below 2^-64 returns BDLM_ERR_UNSUPPORTED.
  */

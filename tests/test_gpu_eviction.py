@@ -71,6 +71,25 @@ def test_weights_of_queries_left_out(lib, L, Hq, Hkv):
     assert np.all(np.abs(host(w).astype(np.float64) - want) <= tol + 1e-30)
 
 
+@pytest.mark.parametrize("L,Hq,Hkv", [(4, 16, 8), (16, 32, 8), (64, 16, 2)])
+def test_weights_of_this_step_alone(lib, L, Hq, Hkv):
+    """decay 0 reads nothing of what the weights held (rows up to 32, up to 256, two launches)."""
+    import torch
+    rng = np.random.default_rng(Hq)
+    a = W.make_attention(rng, 2, L, Hq, Hkv, 128, prefix_lens=np.array([300, 40]), qkv_std=1.0)
+    P = a.page_table_ref.shape[1]
+    d = lib.attn_desc(2, L, Hq, Hkv, 128, P, a.k_ref.shape[0])
+    lse = dev((5 + rng.random((2, L, Hq))).astype(np.float32))
+    got = []
+    for fill in (0.0, float("nan")):
+        w = torch.full((2, Hkv, P * 16), fill, device="cuda")
+        lib.bdlm_attention_weights(d, bf16_tensor(a.q), bf16_tensor(a.k_ref), dev(a.page_table_ref),
+                                   dev(a.prefix_lens), lse, 0.0, w)
+        torch.cuda.synchronize()
+        got.append([host(w)[b, :, :n] for b, n in enumerate((300, 40))])
+    assert all(np.array_equal(x, y) and np.all(x > 0) for x, y in zip(*got))
+
+
 def test_weights_flag_bad_pages_and_lengths(lib):
     import torch
     rng = np.random.default_rng(2)
