@@ -2,7 +2,7 @@
 // group, the tokens that an eviction keeps, and the move of kept tokens to the front.
 //
 // Top k of a row of floats: the row's keys (floats mapped to unsigned integers of the same order)
-// are counted in up to 2048 buckets that evenly divide the range still in question, the bucket
+// are counted in four buckets a thread that evenly divide the range still in question, the bucket
 // holding the k-th largest becomes the next range, and so on; once that bucket holds at most
 // kDirect keys they are ranked against each other directly, mostly after one round (three rounds
 // at most for 32-bit keys).  One CTA per row, everything after the first read in shared memory
@@ -23,8 +23,7 @@ namespace bdlm {
 namespace {
 
 constexpr int kTok = 16;       // tokens per page
-constexpr int kRowThreads = 512;   // threads of a CTA that works on a row
-constexpr int kBuckets = 2048;
+constexpr int kRowThreads = 512;   // threads of a CTA that works on a long row
 constexpr int kDirect = 128;   // keys ranked directly, four lanes a key (in the counters' memory)
 
 // Unsigned key with the floats' order; -0 and +0 are equal, NaN comes below every number.
@@ -84,8 +83,8 @@ __device__ __forceinline__ void block_range(T& lo, T& hi, T* s) {
 template <typename K>
 __device__ __forceinline__ K kth_of_few(int k, const K* few, int count, int* s_scan, K* s_pick,
                                         int* above) {
-  const int c = static_cast<int>(threadIdx.x) >> 2;
-  if ((c & ~7) < count) {   // whole warps
+  for (int c = static_cast<int>(threadIdx.x) >> 2; (c & ~7) < count;   // whole warps
+       c += static_cast<int>(blockDim.x) >> 2) {
     const K key = few[c < count ? c : 0];
     int more = 0, same = 0;
 #pragma unroll 8
@@ -113,10 +112,12 @@ __device__ __forceinline__ K kth_of_few(int k, const K* few, int count, int* s_s
 
 // The k-th largest of the keys that `each` yields (each(f): calls f(key) for this thread's share,
 // the same keys every time), 1 <= k <= their number, all within [lo, hi].  Returns it, and in
-// *above how many are larger.  hist: kBuckets counters.  Whole CTA.
-template <typename K, typename Each>
+// *above how many are larger.  hist: four counters a thread.  Whole CTA of THREADS.
+template <int THREADS, typename K, typename Each>
 __device__ __forceinline__ K kth_largest(int k, K lo, K hi, Each&& each, int* hist, int* s_scan,
                                          K* s_pick, int* above) {
+  constexpr int kBuckets = 4 * THREADS, kLog = THREADS == 512 ? 11 : THREADS == 256 ? 10 : 9;
+  static_assert(kBuckets == 1 << kLog, "");
   int larger = 0;
   BlockSum sum{s_scan};
   K* few = reinterpret_cast<K*>(hist);
@@ -124,7 +125,7 @@ __device__ __forceinline__ K kth_largest(int k, K lo, K hi, Each&& each, int* hi
     const K range = hi - lo;
     int bits = sizeof(K) == 8 ? 64 - __clzll(static_cast<long long>(range))
                               : 32 - __clz(static_cast<int>(range));
-    const int shift = bits > 11 ? bits - 11 : 0;
+    const int shift = bits > kLog ? bits - kLog : 0;
     reinterpret_cast<int4*>(hist)[threadIdx.x] = make_int4(0, 0, 0, 0);
     __syncthreads();
     each([&](K key) {
@@ -133,8 +134,7 @@ __device__ __forceinline__ K kth_largest(int k, K lo, K hi, Each&& each, int* hi
     });
     __syncthreads();
     // this thread's four buckets, counted from the top
-    static_assert(kBuckets == 4 * kRowThreads, "four buckets a thread");
-    const int4 h4 = reinterpret_cast<const int4*>(hist)[kRowThreads - 1 - threadIdx.x];
+    const int4 h4 = reinterpret_cast<const int4*>(hist)[THREADS - 1 - threadIdx.x];
     const int mine[4] = {h4.w, h4.z, h4.y, h4.x};
     int total;
     int before = larger + sum.exclusive(mine[0] + mine[1] + mine[2] + mine[3], &total);
@@ -173,7 +173,8 @@ __device__ __forceinline__ K kth_largest(int k, K lo, K hi, Each&& each, int* hi
 }
 
 // ------------------------------------------------------------------ page selection
-constexpr int kSelThreads = kRowThreads;
+constexpr int kSelThreads = kRowThreads, kSelFewThreads = 128;
+constexpr int kOwn = 8;              // keys of a thread in registers
 constexpr int kSelKeys = 12288;      // rows held in shared memory (96 KB); longer ones are re-read
 constexpr int kSelExact = 1024;      // near ties held in shared memory
 
@@ -277,13 +278,17 @@ __device__ __forceinline__ unsigned long long exact_score(const SelectParams& p,
 // Bound by latency: a dozen barriers and half a dozen loads that depend on each other.  So what can
 // be asked for early is, a thread keeps its first eight keys in registers, and the exact scores
 // of one page are spread over warps.
-// CTAS: 1 with all the registers it wants, for no more lists than SMs (128 lists of 1875-3750 pages:
-// a call of 52 us against 56 with two CTAs per SM); 2 for more lists (1024 of 125-375: 70 against 83).
-template <int CTAS>
-__global__ void __launch_bounds__(kSelThreads, CTAS)
+// 512 threads and CTAS 1, with all the registers it wants, for no more lists than SMs (128 lists of
+// 1875-3750 pages: a call of 52 us against 56 with two CTAs per SM); CTAS 2 for more lists (1024 of
+// 125-375 pages: 70 against 83).  128 threads, six CTAs per SM, for more lists than that has places
+// for, of pages that fit the registers (the same 1024 lists 54 against 70, 2048 lists 54 against 87,
+// 512 lists 38 against 44; with 128 lists of 500-1000 pages it loses, 33 against 29) and of up to 64
+// query rows, which the exact scores need warps for (512 lists of 256 rows: 171 against 158).
+template <int THREADS, int CTAS>
+__global__ void __launch_bounds__(THREADS, CTAS)
 select_pages_kernel(const SelectParams p) {
   extern __shared__ uint32_t sm[];
-  __shared__ __align__(16) int hist[kBuckets];
+  __shared__ __align__(16) int hist[4 * THREADS];
   __shared__ unsigned long long s_exact[kSelExact];
   __shared__ int s_page[kSelExact];
   __shared__ int s_scan[36];
@@ -292,7 +297,7 @@ select_pages_kernel(const SelectParams p) {
   __shared__ int s_cand;
   __shared__ float s_f[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int kWarps = kSelThreads / 32;
+  constexpr int kWarps = THREADS / 32;
   const int list = blockIdx.x;
   const int kvh = list % p.Hkv, bs = list / p.Hkv;
   const int b = bs / p.groups, s = bs - b * p.groups;
@@ -315,30 +320,29 @@ select_pages_kernel(const SelectParams p) {
   const int32_t last = c0 < k + tail ? pt[n + tid] : -1;
   auto finish = [&]() {
     if (c0 < p.sel_cols) out[c0] = last;
-    for (int c = c0 + kSelThreads; c < p.sel_cols; c += kSelThreads) out[c] = -1;   // (tail <= 5)
+    for (int c = c0 + THREADS; c < p.sel_cols; c += THREADS) out[c] = -1;   // (tail <= 5)
   };
   if (n <= p.n_select || k == 0) {
-    for (int c = tid; c < k; c += kSelThreads) out[c] = pt[c];
+    for (int c = tid; c < k; c += THREADS) out[c] = pt[c];
     finish();
     return;
   }
 
   // ---- keys, magnitudes and queries: all asked for before any is used
   const float* row = p.scores + static_cast<size_t>(list) * p.max_pages;
-  constexpr int kOwn = 8;   // keys of a thread in registers: kOwn * kSelThreads of the row
   float early[kOwn];
 #pragma unroll
   for (int x = 0; x < kOwn; ++x)
-    early[x] = tid + x * kSelThreads < n ? __ldcg(row + tid + x * kSelThreads) : 0.f;
+    early[x] = tid + x * THREADS < n ? __ldcg(row + tid + x * THREADS) : 0.f;
   if (n <= kSelKeys)   // the page ids go to shared memory meanwhile
-    for (int i = tid; i < n; i += kSelThreads)
+    for (int i = tid; i < n; i += THREADS)
       asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(sm + i)), "l"(pt + i)
                    : "memory");
   float q1 = 0.f, am = 0.f;   // the group's largest |q|_1, the list's largest |bound|
   {
     const int values = (n + kKeyTile - 1) / kKeyTile * kAmaxPerTile;
     const float* a = p.amax + (static_cast<size_t>(b) * p.Hkv + kvh) * p.max_tiles * kAmaxPerTile;
-    for (int i = tid; i < values; i += kSelThreads) am = fmaxf(am, __ldcg(a + i));
+    for (int i = tid; i < values; i += THREADS) am = fmaxf(am, __ldcg(a + i));
   }
 #pragma unroll 4
   for (int r = warp; r < p.group * p.G; r += kWarps) {
@@ -360,24 +364,24 @@ select_pages_kernel(const SelectParams p) {
   const bool held = n <= kSelKeys;
   int32_t* ids = reinterpret_cast<int32_t*>(sm);
   uint32_t* keys = sm + n;
-  uint32_t* taken = sm + (held ? (n > kOwn * kSelThreads ? 2 * n : n) : 0);
+  uint32_t* taken = sm + (held ? (n > kOwn * THREADS ? 2 * n : n) : 0);
   const int words = (n + 31) / 32;
   uint32_t* second = taken + words;
   uint32_t lo = 0xFFFFFFFFu, hi = 0;
 #pragma unroll
   for (int x = 0; x < kOwn; ++x) {
     own[x] = order_key(early[x]);
-    if (tid + x * kSelThreads >= n) continue;
+    if (tid + x * THREADS >= n) continue;
     lo = min(lo, own[x]);
     hi = max(hi, own[x]);
   }
-  for (int i = tid + kOwn * kSelThreads; i < n; i += kSelThreads) {
+  for (int i = tid + kOwn * THREADS; i < n; i += THREADS) {
     const uint32_t key = order_key(__ldcg(row + i));
     if (held) keys[i] = key;
     lo = min(lo, key);
     hi = max(hi, key);
   }
-  for (int i = tid; i < words; i += kSelThreads) taken[i] = 0;
+  for (int i = tid; i < words; i += THREADS) taken[i] = 0;
   if (tid == 0) s_cand = 0;
   asm volatile("cp.async.wait_all;" ::: "memory");
   auto page_id = [&](int i) { return held ? ids[i] : __ldg(pt + i); };
@@ -385,8 +389,8 @@ select_pages_kernel(const SelectParams p) {
   auto each_key = [&](auto&& f) {
 #pragma unroll
     for (int x = 0; x < kOwn; ++x)
-      if (tid + x * kSelThreads < n) f(tid + x * kSelThreads, own[x]);
-    for (int i = tid + kOwn * kSelThreads; i < n; i += kSelThreads)
+      if (tid + x * THREADS < n) f(tid + x * THREADS, own[x]);
+    for (int i = tid + kOwn * THREADS; i < n; i += THREADS)
       f(i, held ? keys[i] : order_key(__ldcg(row + i)));
   };
 
@@ -401,16 +405,16 @@ select_pages_kernel(const SelectParams p) {
     T = kth_of_few<uint32_t>(k, few, n, s_scan, pick, &above);
   } else {
     block_range(lo, hi, reinterpret_cast<uint32_t*>(s_wide));
-    T = kth_largest<uint32_t>(
+    T = kth_largest<THREADS, uint32_t>(
         k, lo, hi, [&](auto&& f) { each_key([&](int, uint32_t key) { f(key); }); }, hist, s_scan,
         pick, &above);
   }
 
   // ---- the band around T
-  q1 = s_f[lane & 15];
-  am = s_f[16 + (lane & 15)];
+  q1 = s_f[lane & (kWarps - 1)];
+  am = s_f[16 + (lane & (kWarps - 1))];
 #pragma unroll
-  for (int off = 8; off > 0; off >>= 1) {
+  for (int off = kWarps / 2; off > 0; off >>= 1) {
     q1 = fmaxf(q1, __shfl_xor_sync(0xffffffffu, q1, off));
     am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, off));
   }
@@ -481,7 +485,7 @@ select_pages_kernel(const SelectParams p) {
     }
     __syncthreads();
     int equal = need;   // how many of `second`, the candidates equal to the last one in, are in
-    for (int i = tid; i < words; i += kSelThreads) second[i] = 0;
+    for (int i = tid; i < words; i += THREADS) second[i] = 0;
     if (!refine) {
       __syncthreads();
       each_key([&](int i, uint32_t key) {
@@ -489,7 +493,7 @@ select_pages_kernel(const SelectParams p) {
       });
     } else if (listed) {
       equal = 0;
-      for (int c = tid; c < m; c += kSelThreads) {
+      for (int c = tid; c < m; c += THREADS) {
         const unsigned long long e = s_exact[c];
         const int page = s_page[c];
         int rank = 0;   // candidates ahead of this one
@@ -500,17 +504,17 @@ select_pages_kernel(const SelectParams p) {
     } else {
       block_range(elo, ehi, s_wide);
       int larger;
-      const unsigned long long TE = kth_largest<unsigned long long>(
+      const unsigned long long TE = kth_largest<THREADS, unsigned long long>(
           need, elo, ehi,
           [&](auto&& f) {
-            for (int i = tid; i < n; i += kSelThreads) {
+            for (int i = tid; i < n; i += THREADS) {
               const unsigned long long e = __ldcg(exact + i);
               if (e != 0) f(e);
             }
           },
           hist, s_scan, s_pick, &larger);
       equal = need - larger;
-      for (int i = tid; i < n; i += kSelThreads) {
+      for (int i = tid; i < n; i += THREADS) {
         const unsigned long long e = __ldcg(exact + i);
         if (e > TE) take(i);
         if (e == TE) atomicOr(&second[i >> 5], 1u << (i & 31));
@@ -518,7 +522,7 @@ select_pages_kernel(const SelectParams p) {
     }
     __syncthreads();
     int base = 0;   // of equal ones the lowest positions
-    for (int w0 = 0; w0 < words && equal > 0; w0 += kSelThreads) {
+    for (int w0 = 0; w0 < words && equal > 0; w0 += THREADS) {
       const int w = w0 + tid;
       const uint32_t bits = w < words ? second[w] : 0;
       int total;
@@ -533,7 +537,7 @@ select_pages_kernel(const SelectParams p) {
 
   // ---- the taken pages in position order: where each bitmap word's pages begin, then a thread a page
   int base = 0;
-  for (int w0 = 0; w0 < words; w0 += kSelThreads) {
+  for (int w0 = 0; w0 < words; w0 += THREADS) {
     const int w = w0 + tid;
     int total;
     const int at = base + sum.exclusive(w < words ? __popc(taken[w]) : 0, &total);
@@ -542,7 +546,7 @@ select_pages_kernel(const SelectParams p) {
   }
   __syncthreads();
 #pragma unroll 4
-  for (int i = tid; i < n; i += kSelThreads) {
+  for (int i = tid; i < n; i += THREADS) {
     const uint32_t bits = taken[i >> 5], bit = 1u << (i & 31);
     if (bits & bit) out[second[i >> 5] + __popc(bits & (bit - 1))] = page_id(i);
   }
@@ -564,7 +568,7 @@ constexpr int kEvictKeys = 22528;   // 88 KB of keys: two CTAs per SM; longer ro
 __global__ void __launch_bounds__(kEvictThreads, 2)
 evict_select_kernel(const EvictParams p) {
   extern __shared__ uint32_t sm[];
-  __shared__ __align__(16) int hist[kBuckets];
+  __shared__ __align__(16) int hist[4 * kEvictThreads];
   __shared__ int s_scan[36];
   __shared__ uint32_t s_range[64];
   __shared__ uint32_t s_pick[1];
@@ -616,7 +620,7 @@ evict_select_kernel(const EvictParams p) {
       }
     }
     block_range(lo, hi, s_range);
-    T = kth_largest<uint32_t>(
+    T = kth_largest<kEvictThreads, uint32_t>(
         k, lo, hi,
         [&](auto&& f) {
 #pragma unroll 4
@@ -845,18 +849,21 @@ cudaError_t allow_smem(std::atomic<unsigned long long>& done, F* kernel, size_t 
 }  // namespace
 
 cudaError_t launch_select_pages(const SelectParams& p, int num_sms, cudaStream_t stream) {
+  const size_t words = (static_cast<size_t>(p.max_pages) + 31) / 32;
+  const unsigned lists = static_cast<unsigned>(p.B) * p.groups * p.Hkv;
+  if (p.max_pages <= kOwn * kSelFewThreads && lists > 2u * static_cast<unsigned>(num_sms) &&
+      p.group * p.G <= 64)
+    return launch_pdl(select_pages_kernel<kSelFewThreads, 6>, dim3(lists), dim3(kSelFewThreads),
+                      (p.max_pages + 2 * words) * 4, stream, p);
   // page ids and keys (of rows that fit), then two bitmaps of the row's pages
   const size_t keys = 2 * static_cast<size_t>(p.max_pages <= kSelKeys ? p.max_pages : kSelKeys);
-  const size_t words = (static_cast<size_t>(p.max_pages) + 31) / 32;
   constexpr size_t kMost = (2 * kSelKeys + 2 * (kSelectMaxPages / 32)) * 4;
-  const unsigned lists = static_cast<unsigned>(p.B) * p.groups * p.Hkv;
   static std::atomic<unsigned long long> one_done{0}, two_done{0};
   const bool one = lists <= static_cast<unsigned>(num_sms);
-  cudaError_t e = one ? allow_smem(one_done, select_pages_kernel<1>, kMost)
-                      : allow_smem(two_done, select_pages_kernel<2>, kMost);
+  auto* kernel = one ? select_pages_kernel<kSelThreads, 1> : select_pages_kernel<kSelThreads, 2>;
+  cudaError_t e = allow_smem(one ? one_done : two_done, kernel, kMost);
   if (e != cudaSuccess) return e;
-  return launch_pdl(one ? select_pages_kernel<1> : select_pages_kernel<2>, dim3(lists),
-                    dim3(kSelThreads), (keys + 2 * words) * 4, stream, p);
+  return launch_pdl(kernel, dim3(lists), dim3(kSelThreads), (keys + 2 * words) * 4, stream, p);
 }
 
 cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t stream) {
