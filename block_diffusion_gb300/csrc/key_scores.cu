@@ -14,7 +14,7 @@
 // bytes per key move besides, so HBM does up to about 200 query rows; beyond, the tensor core and
 // the exponentials (one per key and row; an SM does about 32 a clock) are close to it.
 //
-// (Page scores of up to 32 rows: a kernel of its own, below.)
+// (Page scores of up to 64 rows: a kernel of its own, below.)
 //
 // Persistent CTAs, one or two per SM, each take an equal, contiguous share of all tiles of 128 keys,
 // laid end to end list by list (a list = sequence and KV head): equal bytes per CTA whatever the
@@ -666,14 +666,15 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   if (threadIdx.x == 0 && abort_flag) atomicOr(p.err, BDLM_DEVERR_TIMEOUT);
 }
 
-// Page scores of up to 32 query rows.  A page's 512 bytes take 2 * 16 to 32 rows * 256 flops: HBM
+// Page scores of up to 64 query rows.  A page's 512 bytes take 2 * 16 to 64 rows * 256 flops: HBM
 // is the only bound, and staging pages in shared memory for tcgen05 (the kernel above) costs more
-// than it saves (42 us against 35 us, 16 x 8 lists of 1875-3750 pages, 16 rows).  So each warp scores 16
+// than it saves (16 x 8 lists of 1875-3750 pages, 16 rows: 42 us against 35; lists of 1250-2500 pages,
+// 64 rows: a whole selection of 72 us against 62).  So each warp scores 16
 // pages with m16n8k16 straight from global memory: the order of the 256 values along K is free as
 // long as both operands have the same, so a lane's 16-byte chunk of a page row (8 values) serves as
 // its fragments of two MMAs, 16 loads a lane are in flight at once, and nothing is staged but q+ and
 // q-.  A CTA takes 128 pages a round (8 warps), its share of the tiles as above, two CTAs per SM.
-constexpr int kDirectRows = 32;
+constexpr int kDirectRows = 64;
 constexpr int kDirectPitch = 512 + 64;   // bytes of a q row: 64 more, so that 8 lanes miss no bank
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -910,7 +911,8 @@ cudaError_t launch_direct_t(const KeyParams& p, int num_sms, cudaStream_t stream
 cudaError_t launch_page_scores(const KeyParams& p, int num_sms, cudaStream_t stream) {
   if (p.rows <= 8) return launch_direct_t<1>(p, num_sms, stream);
   if (p.rows <= 16) return launch_direct_t<2>(p, num_sms, stream);
-  if (p.rows <= kDirectRows) return launch_direct_t<4>(p, num_sms, stream);
+  if (p.rows <= 32) return launch_direct_t<4>(p, num_sms, stream);
+  if (p.rows <= kDirectRows) return launch_direct_t<8>(p, num_sms, stream);
   const CUtensorMap none = {};
   return launch_key_t<true, true>(none, none, p, num_sms, stream);
 }
