@@ -653,6 +653,14 @@ bdlm::KeyParams key_params(const bdlm_attn_desc& d, const int32_t* page_table,
   return p;
 }
 
+// Queries of nl block positions and of the query heads that share a KV head, 64 dims a box.
+int encode_key_q(CUtensorMap* tm, const bdlm_bf16* q, const bdlm_attn_desc& d, int nl) {
+  const cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(d.Hq), static_cast<cuuint64_t>(d.B) * d.L};
+  const cuuint64_t strides[2] = {256, static_cast<cuuint64_t>(d.Hq) * 256};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(d.Hq / d.Hkv), static_cast<cuuint32_t>(nl)};
+  return encode(tm, q, 3, dims, strides, box);
+}
+
 int compact_impl(DeviceState* st, const bdlm_attn_desc& d, bdlm_bf16* k_pages, bdlm_bf16* v_pages,
                  const int32_t* page_table, const int32_t* base_lens, const int32_t* idx,
                  int heads, int n_max, const int32_t* counts, const int32_t* to_table,
@@ -722,7 +730,8 @@ int bdlm_select_pages(const bdlm_attn_desc* desc, const bdlm_bf16* q, const bdlm
   const int G = d.Hq / d.Hkv, groups = d.L / group;
   const long long lists = static_cast<long long>(d.B) * groups * d.Hkv;
   if (lists > 0x7FFFFFFFll) return BDLM_ERR_INVALID;
-  if (group * G > bdlm::key_rows_max() || d.max_pages_per_seq > bdlm::kSelectMaxPages)
+  if (group * G > bdlm::key_rows_max() || d.max_pages_per_seq > bdlm::kSelectMaxPages ||
+      static_cast<long long>(d.num_pages) * d.Hkv > 0x3FFFFFFFll)   // (rows of bounds: 32 bits)
     return BDLM_ERR_UNSUPPORTED;
   if (d.B == 0) return BDLM_OK;
   if (!q || !bounds || !page_table || !prefix_lens || !sel_table || !sel_lens ||
@@ -753,9 +762,19 @@ int bdlm_select_pages(const bdlm_attn_desc* desc, const bdlm_bf16* q, const bdlm
   p.groups = groups;
   p.width = group * G;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  CUtensorMap tm_q = {}, tm_bounds = {};
+  if (per * G > bdlm::kDirectRows) {
+    if ((rc = get_encoder())) return rc;
+    const cuuint64_t dims[2] = {128, static_cast<cuuint64_t>(d.num_pages) * d.Hkv * 2};
+    const cuuint64_t strides[1] = {256};
+    const cuuint32_t box[2] = {64, 1};
+    if ((rc = encode(&tm_bounds, bounds, 2, dims, strides, box))) return rc;
+  }
   for (p.l0 = 0; p.l0 < d.L; p.l0 += per) {
-    p.rows = (d.L - p.l0 < per ? d.L - p.l0 : per) * G;
-    if (bdlm::launch_page_scores(p, st->num_sms, s) != cudaSuccess) return BDLM_ERR_CUDA;
+    const int nl = d.L - p.l0 < per ? d.L - p.l0 : per;
+    p.rows = nl * G;
+    if (p.rows > bdlm::kDirectRows && (rc = encode_key_q(&tm_q, q, d, nl))) return rc;
+    if (bdlm::launch_page_scores(tm_q, tm_bounds, p, st->num_sms, s) != cudaSuccess) return BDLM_ERR_CUDA;
   }
   const bdlm::SelectParams sp{q, bounds, page_table, prefix_lens, p.scores, p.amax,
                               static_cast<unsigned long long*>(st->data),
@@ -831,10 +850,7 @@ int bdlm_attention_weights(const bdlm_attn_desc* desc, const bdlm_bf16* q,
   for (p.l0 = 0; p.l0 < d.L; p.l0 += per) {
     const int nl = d.L - p.l0 < per ? d.L - p.l0 : per;
     p.rows = nl * G;
-    cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(d.Hq), static_cast<cuuint64_t>(d.B) * d.L};
-    cuuint64_t strides[2] = {256, static_cast<cuuint64_t>(d.Hq) * 256};
-    cuuint32_t box[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(nl)};
-    if ((rc = encode(&tm_q, q, 3, dims, strides, box))) return rc;
+    if ((rc = encode_key_q(&tm_q, q, d, nl))) return rc;
     if (bdlm::launch_attention_weights(tm_q, tm_k, p, st->num_sms,
                                        static_cast<cudaStream_t>(stream)) != cudaSuccess)
       return BDLM_ERR_CUDA;

@@ -51,7 +51,11 @@ struct KeyParams {
 int key_rows_max();   // query rows of one launch
 cudaError_t launch_attention_weights(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                                      const KeyParams& p, int num_sms, cudaStream_t stream);
-cudaError_t launch_page_scores(const KeyParams& p, int num_sms, cudaStream_t stream);
+// The maps are used for more than kDirectRows rows: tm_q as for attention weights, tm_bounds rows of
+// 128 values, boxes of one row of 64.
+constexpr int kDirectRows = 64;
+cudaError_t launch_page_scores(const CUtensorMap& tm_q, const CUtensorMap& tm_bounds,
+                               const KeyParams& p, int num_sms, cudaStream_t stream);
 cudaError_t launch_page_bounds(const uint16_t* k_pages, const int32_t* page_table,
                                const int32_t* from, const int32_t* to, int B, int Hkv,
                                int max_pages, int num_pages, int num_sms, uint16_t* bounds,

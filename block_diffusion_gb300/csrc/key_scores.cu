@@ -25,10 +25,13 @@
 //                warp's 16 boxes take about 1 us)
 //   warp 3       finds the CTA's share; weights: Q of a list by TMA (a 64-dim x G x L box per half)
 //   warps 4-     reduction, two or four sets of four warps (one per lane quadrant) in turn
-//   page scores  a page's bounds are 512 bytes, too small for a box each (128 boxes of one row per
-//                K atom): the last eight warps gather them, 16 lanes a row, into the 128-byte
-//                swizzle, and build q+ and q- of a list in shared memory as it begins; warps 1-2 run
-//                up to three tiles ahead, reading page ids and asking L2 for the pages' rows
+//   page scores  warps 1-2: a page's bounds are two rows of 256 bytes, so TMA gathers them, four
+//                rows of 128 bytes an instruction (warp 1 the tiles' hi, warp 2 lo); Q by TMA as for
+//                weights, which the last eight warps split into q+ and q- as a list begins (two
+//                buffers up to 128 query rows); they also take the largest magnitude of each stage.
+//                (Loads to registers are slow beside 227 KB of shared memory, which leave L1 few
+//                lines for what is in flight: pages and Q took 58 us that way, 128 lists of 1250-2500
+//                pages, 256 rows.)
 // Stages are 32 KB (128 keys x 128 values); a page tile takes two (hi, then lo).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -45,8 +48,7 @@ constexpr int kKeys = kKeyTile;      // keys per tile (UMMA M)
 constexpr int kPageTokens = 16;
 constexpr int kStage = 32768;        // 128 keys x 128 bf16, two 64-wide K atoms
 constexpr int kAtom = 16384;
-constexpr int kIdRing = 3;           // page scores: tiles whose page ids are fetched ahead
-constexpr int kLoaders = kAmaxPerTile;         // page scores: gathering warps
+constexpr int kHelpers = kAmaxPerTile;   // page scores: warps that split Q into q+ and q-
 
 // WIDE: up to 256 query rows; else up to 32, two CTAs per SM (113 us a call against 117 with one CTA
 // of twice the stages, 128 x 8 lists of 512-4096 tokens).
@@ -64,7 +66,7 @@ struct Cfg {
   static constexpr int kDBufs = WIDE ? 2 : 4;                  // X tiles in tensor memory
   static constexpr int kSets = kSplit ? 4 : 2;                 // reducing sets of four warps
   static constexpr int kTmemCols = WIDE ? 512 : 128;
-  static constexpr int kThreads = 128 + kSets * 128 + (PAGES ? kLoaders * 32 : 0);
+  static constexpr int kThreads = 128 + kSets * 128 + (PAGES ? kHelpers * 32 : 0);
   // Weights of more than 32 rows: -lse / scale enters X through the MMA, as three bf16 numbers a row
   // (24 bits) against keys of 1, so that the reduction reads no table from shared memory beside
   // the MMAs (95 us a pass against 100, 16 x 64 x 4 rows over 8192-16384 tokens): 128-byte rows of
@@ -73,6 +75,31 @@ struct Cfg {
   static constexpr size_t kSmem =
       1024 + static_cast<size_t>(kQBytes) + kLseBytes + kOneBytes + kStages * kStage;
 };
+
+// Four rows r[] of 64 bf16 from column x of a two-dimensional map, to 512 consecutive bytes.
+__device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, uint64_t* bar, int x,
+                                            const int (&r)[4]) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+      "r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void sts16(uint32_t addr, const uint32_t (&v)[4]) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3])
+               : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
 
 // 16 bytes that are read once
 __device__ __forceinline__ uint4 ld_stream16(const uint4* p) {
@@ -184,28 +211,30 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   uint8_t* sOne = sL + C::kLseBytes;
   uint8_t* sA = sOne + C::kOneBytes;
   __shared__ uint64_t bar_full[C::kStages], bar_empty[C::kStages];
-  __shared__ uint64_t bar_qfull, bar_qempty;
+  __shared__ uint64_t bar_qfull[2], bar_qempty[2], bar_qraw[2];   // (qraw: page scores, Q as loaded)
   __shared__ uint64_t bar_dfull[C::kDBufs], bar_dempty[C::kDBufs], bar_lse[2], bar_done;
   __shared__ uint64_t bar_part[C::kSplit ? 4 : 1][4];        // second halves' sums: by tile, quadrant
   __shared__ float s_part[C::kSplit ? 4 : 1][C::kSplit ? 128 : 1];
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
-  // page scores: page ids of the tiles ahead (-1: none), from warps 1-2 to the gathering warps
-  __shared__ uint64_t bar_ids[PAGES ? kIdRing : 1], bar_ids_free[PAGES ? kIdRing : 1];
-  __shared__ int s_ids[PAGES ? kIdRing : 1][PAGES ? kKeys : 1];
+  __shared__ bool s_have[C::kStages];   // page scores: the stage holds pages
   __shared__ int s_share[4];
   constexpr bool kTable = !PAGES && !C::kSplit;   // -lse in shared memory (log2 units)
   __shared__ __align__(16) float s_lse[kTable ? 2 : 1][kTable ? C::kRowsMax : 4];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n16 = (p.rows + 15) & ~15;   // columns of X
+  const int nq = PAGES && n16 <= C::kRowsMax / 2 ? 2 : 1;   // buffers of Q
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&bar_full[s], PAGES ? kLoaders : 1);
-      mbar_init(&bar_empty[s], 1);
+      mbar_init(&bar_full[s], 1);
+      mbar_init(&bar_empty[s], PAGES ? 1 + kHelpers : 1);
     }
-    mbar_init(&bar_qfull, PAGES ? kLoaders : C::kSplit ? 2 : 1);
-    mbar_init(&bar_qempty, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&bar_qfull[b], PAGES ? kHelpers : C::kSplit ? 2 : 1);
+      mbar_init(&bar_qempty[b], 1);
+      mbar_init(&bar_qraw[b], 1);
+    }
     for (int b = 0; b < C::kDBufs; ++b) {
       mbar_init(&bar_dfull[b], 1);
       mbar_init(&bar_dempty[b], C::kSplit ? 8 : 4);   // the warps that read a tile
@@ -214,11 +243,6 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
     mbar_init(&bar_lse[1], C::kSets * 4);
     if constexpr (C::kSplit)
       for (int i = 0; i < 16; ++i) mbar_init(&bar_part[i >> 2][i & 3], 1);
-    if constexpr (PAGES)
-      for (int i = 0; i < kIdRing; ++i) {
-        mbar_init(&bar_ids[i], 2);
-        mbar_init(&bar_ids_free[i], kLoaders);
-      }
     mbar_init(&bar_done, 1);
     abort_flag = 0;
     fence_mbar_init();
@@ -296,18 +320,20 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         }
       __syncwarp();
     }
-  } else if (!PAGES && warp == 3) {
+  } else if (warp == 3) {
     // ------------------------------------------------------------ TMA: Q; and -lse / scale
     bool ok = true;
     int q = 0;
     const float unscale = -1.4426950408889634f / p.scale_log2;
     for (KeyWalk<PAGES> w(p, s_share); w.left > 0 && ok; w.next()) {
       if (!w.fresh) continue;
-      if (!(ok = mbar_wait_warp(&bar_qempty, (q & 1) ^ 1, &abort_flag))) break;
+      if (!(ok = mbar_wait_warp(&bar_qempty[q % nq], ((q / nq) & 1) ^ 1, &abort_flag))) break;
       if (lane == 0) {
-        mbar_arrive_expect_tx(&bar_qfull, static_cast<uint32_t>(p.rows) * 256u);
+        uint64_t* const bar = PAGES ? &bar_qraw[q % nq] : &bar_qfull[0];
+        mbar_arrive_expect_tx(bar, static_cast<uint32_t>(p.rows) * 256u);
         for (int h = 0; h < 2; ++h)
-          tma_load_3d(sQ + h * n16 * 128, &tm_q, &bar_qfull, h * 64, w.kvh * p.G, w.b * p.L + p.l0);
+          tma_load_3d(sQ + (q % nq) * n16 * 512 + h * n16 * 128, &tm_q, bar, h * 64, w.kvh * p.G,
+                      w.b * p.L + p.l0);
       }
       if constexpr (C::kSplit) {
 #pragma unroll 4
@@ -327,155 +353,135 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bar_qfull);
+        if (lane == 0) mbar_arrive(&bar_qfull[0]);
       }
       ++q;
     }
     if (!ok && lane == 0) {
       int dummy = 0;
-      mbar_wait(&bar_qfull, 0, &dummy, 1000000ull);
-      mbar_wait(&bar_qfull, 1, &dummy, 1000000ull);
+      for (int b = 0; b < nq; ++b) {
+        uint64_t* const bar = PAGES ? &bar_qraw[b] : &bar_qfull[0];
+        mbar_wait(bar, 0, &dummy, 1000000ull);
+        mbar_wait(bar, 1, &dummy, 1000000ull);
+      }
     }
     __syncwarp();
   } else if (PAGES && (warp == 1 || warp == 2)) {
-    // ------------------------------------------------------------ page ids and L2, tiles ahead
-    const int t = threadIdx.x - 32;   // 0 .. 63: pages t and t + 64 of a tile
+    // ------------------------------------------------------------ TMA: page bounds
+    const int h = warp - 1;   // half 0: hi (row 1 of a page's bounds), half 1: lo (row 0)
     bool ok = true;
-    int u = 0;
-    for (KeyWalk<PAGES> w(p, s_share); w.left > 0 && ok; w.next(), ++u) {
-      int id[2];
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int page = w.tile * kKeys + t + 64 * r;
-        id[r] = -1;
-        if (page < w.n)
-          id[r] = __ldg(p.page_table + static_cast<size_t>(w.b) * p.max_pages + page);
-      }
-      const int ring = u % kIdRing;
-      if (!(ok = mbar_wait_warp(&bar_ids_free[ring], ((u / kIdRing) & 1) ^ 1, &abort_flag))) break;
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        if (id[r] < 0 || id[r] >= p.num_pages) {
-          if (w.tile * kKeys + t + 64 * r < w.n) atomicOr(p.err, BDLM_DEVERR_PAGE);
-          id[r] = -1;
-        } else {
-          const uint16_t* row = p.bounds + (static_cast<size_t>(id[r]) * p.Hkv + w.kvh) * 256;
-#pragma unroll
-          for (int l = 0; l < 4; ++l) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + l * 64));
-        }
-        s_ids[ring][t + 64 * r] = id[r];
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar_ids[ring]);
-    }
-  } else if (PAGES && warp >= C::kThreads / 32 - kLoaders) {
-    // ------------------------------------------------------------ gather of the page bounds
-    // Through registers: cp.async moves 16 bytes a clock and SM (31 GB/s).  A thread loads one stage
-    // while it stores the one before.
-    const int t = threadIdx.x - (C::kThreads - kLoaders * 32);   // 0 .. 255
-    const int c16 = t & 15;            // 16-byte chunk of a 256-byte half row
-    uint8_t* const dst = sA + (c16 >> 3) * kAtom;
-    bool ok = true;
-    int s = 0, u = 0;      // stages handed to the MMA, tiles whose ids are read
-    uint32_t top = 0;      // largest |bound| seen in the tile, as a bf16 pair
     KeyWalk<PAGES> w(p, s_share);
-    // page ids of the walk's tile: this thread's eight rows
-    auto load_ids = [&](int (&id)[8]) {
-      if (w.left <= 0 || !ok) {
+    int id[4], n_left;   // pages 4 * lane .. + 3 of the walk's tile
+    auto load_ids = [&]() {
+      const int page = w.tile * kKeys + lane * 4;
+      n_left = w.left > 0 ? w.n - page : 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) id[i] = -1;
-        return;
+      for (int i = 0; i < 4; ++i)
+        id[i] = i < n_left ? __ldg(p.page_table + static_cast<size_t>(w.b) * p.max_pages + page + i) : -1;
+    };
+    load_ids();
+    for (int u = 0; w.left > 0 && ok; ++u) {
+      const int s = 2 * u + h, st = s % C::kStages;
+      // rows of pages that are not there repeat one that is, so that every value counts
+      int row[4], any = -1;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool good = id[i] >= 0 && id[i] < p.num_pages;
+        if (!good && i < n_left) atomicOr(p.err, BDLM_DEVERR_PAGE);
+        row[i] = good ? (id[i] * p.Hkv + w.kvh) * 2 + 1 - h : -1;
+        any = max(any, row[i]);
       }
-      const int ring = u % kIdRing;
-      ok = mbar_wait_warp(&bar_ids[ring], (u / kIdRing) & 1, &abort_flag);
+      const uint32_t have = __ballot_sync(0xffffffffu, any >= 0);
+      const int fill = __shfl_sync(0xffffffffu, any, have ? __ffs(static_cast<int>(have)) - 1 : 0);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) id[i] = ok ? s_ids[ring][i * 16 + (t >> 4)] : -1;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar_ids_free[ring]);
-      ++u;
-    };
-    // half 0: hi (row 1 of a page's bounds), half 1: lo (row 0)
-    auto load_half = [&](uint4 (&v)[8], const int (&id)[8], int kvh, int h) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        v[i] = id[i] >= 0 ? __ldg(reinterpret_cast<const uint4*>(p.bounds) +
-                                  ((static_cast<size_t>(id[i]) * p.Hkv + kvh) * 2 + (1 - h)) * 16 + c16)
-                          : make_uint4(0, 0, 0, 0);
-    };
-    auto store_half = [&](const uint4 (&v)[8]) {
-      const int st = s % C::kStages;
-      if (!(ok = ok && mbar_wait_warp(&bar_empty[st], ((s / C::kStages) & 1) ^ 1, &abort_flag)))
-        return;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = i * 16 + (t >> 4);
-        *reinterpret_cast<uint4*>(dst + st * kStage + r * 128 + (((c16 & 7) ^ (r & 7)) << 4)) = v[i];
-        const uint32_t x[4] = {v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu, v[i].z & 0x7FFF7FFFu,
-                               v[i].w & 0x7FFF7FFFu};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const __nv_bfloat162 m =
-              __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&top),
-                          *reinterpret_cast<const __nv_bfloat162*>(&x[k]));
-          top = *reinterpret_cast<const uint32_t*>(&m);
+      for (int i = 0; i < 4; ++i) row[i] = row[i] >= 0 ? row[i] : fill;
+      w.next();
+      load_ids();   // they arrive while the stage is waited for
+      if (lane == 0) {
+        ok = mbar_wait(&bar_empty[st], ((s / C::kStages) & 1) ^ 1, &abort_flag);
+        if (ok) {
+          s_have[st] = have != 0;
+          if (have)
+            mbar_arrive_expect_tx(&bar_full[st], kStage);
+          else
+            mbar_arrive(&bar_full[st]);
         }
       }
-      fence_proxy_async_smem();
+      ok = __shfl_sync(0xffffffffu, ok, 0);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar_full[st]);
-      ++s;
-    };
-    // q+ and q- of the walk's list; row n is query l0 + n / G, head kvh * G + n % G (the division as
-    // a product: n < 256, G <= 16).  Padding rows repeat row 0, so they cannot raise a maximum.
-    const int recip = (65536 + p.G - 1) / p.G;
-    int q = 0;   // lists so far
-    auto build_q = [&](int b, int kvh) {
-      if (!(ok = ok && mbar_wait_warp(&bar_qempty, (q & 1) ^ 1, &abort_flag))) return;
-      const uint16_t* base = p.q + (static_cast<size_t>(b) * p.L + p.l0) * p.Hq * 128 + kvh * p.G * 128;
+      if (ok && have)
+        for (int a = 0; a < 2; ++a)
+          tma_gather4(sA + st * kStage + a * kAtom + lane * 512, &tm_k, &bar_full[st], a * 64, row);
+    }
+    if (!ok) {
+      // as above: the copies in flight land before the CTA's memory goes away
+      int dummy = 0;
+      if (lane == 0)
+        for (int s = 0; s < C::kStages; ++s) {
+          mbar_wait(&bar_full[s], 0, &dummy, 1000000ull);
+          mbar_wait(&bar_full[s], 1, &dummy, 1000000ull);
+        }
+      __syncwarp();
+    }
+  } else if (PAGES && warp >= C::kThreads / 32 - kHelpers) {
+    // ------------------------------------------------------------ q+ and q-; largest magnitudes
+    const int t = threadIdx.x - (C::kThreads - kHelpers * 32);   // 0 .. 255
+    bool ok = true;
+    int s = 0, q = 0;   // stages and lists so far
+    auto split_q = [&]() {   // in place: q+ where Q is, q- behind it
+      if (!(ok = mbar_wait_warp(&bar_qraw[q % nq], (q / nq) & 1, &abort_flag))) return;
+      const uint32_t at = smem_u32(sQ) + (q % nq) * n16 * 512;
 #pragma unroll 4
-      for (int r = t >> 4; r < n16; r += 16) {
-        const int n = r < p.rows ? r : 0, i = (n * recip) >> 16;
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(
-                                  base + (static_cast<size_t>(i) * p.Hq + n - i * p.G) * 128) + c16);
-        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+      for (int c = t * 16; c < n16 * 256; c += kHelpers * 512) {
+        const uint4 v = lds16(at + c);
+        const uint32_t y[4] = {v.x, v.y, v.z, v.w};
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const uint32_t neg = ((x[k] >> 15) & 0x00010001u) * 0xFFFFu;   // 16 ones per negative
-          hi[k] = x[k] & ~neg;
-          lo[k] = x[k] & neg;
+          const uint32_t neg = ((y[k] >> 15) & 0x00010001u) * 0xFFFFu;   // 16 ones per negative
+          hi[k] = y[k] & ~neg;
+          lo[k] = y[k] & neg;
         }
-        uint8_t* d = sQ + ((c16 >> 3) * n16 + r) * 128 + (((c16 & 7) ^ (r & 7)) << 4);
-        *reinterpret_cast<uint4*>(d) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *reinterpret_cast<uint4*>(d + 2 * n16 * 128) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        sts16(at + c, hi);
+        sts16(at + n16 * 256 + c, lo);
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar_qfull);
+      if (lane == 0) mbar_arrive(&bar_qfull[q % nq]);
       ++q;
     };
-    int id[8];
-    uint4 hi[8], lo[8];
-    load_ids(id);
-    load_half(hi, id, w.kvh, 0);
-    while (w.left > 0 && ok) {
-      const int kvh = w.kvh;
-      float* amax = p.amax + (w.row() * p.max_tiles + w.tile) * kLoaders + (warp - (C::kThreads / 32 - kLoaders));
-      load_half(lo, id, kvh, 1);
-      if (w.fresh) build_q(w.b, kvh);
-      w.next();
-      store_half(hi);
-      load_ids(id);
-      load_half(hi, id, w.kvh, 0);
-      store_half(lo);
+    for (KeyWalk<PAGES> w(p, s_share); w.left > 0 && ok; w.next()) {
+      if (w.fresh) split_q();
+      uint32_t top = 0;   // largest |bound| seen in the tile, as a bf16 pair
+      for (int h = 0; h < kHalves && ok; ++h, ++s) {
+        const int st = s % C::kStages;
+        if (!(ok = mbar_wait_warp(&bar_full[st], (s / C::kStages) & 1, &abort_flag))) break;
+        if (s_have[st]) {
+          const uint32_t a = smem_u32(sA) + st * kStage + t * 16;
+#pragma unroll
+          for (int i = 0; i < kStage / 16 / (kHelpers * 32); ++i) {
+            const uint4 v = lds16(a + i * kHelpers * 512);
+            const uint32_t y[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t mag = y[k] & 0x7FFF7FFFu;
+              const __nv_bfloat162 m = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&top),
+                                                   *reinterpret_cast<const __nv_bfloat162*>(&mag));
+              top = *reinterpret_cast<const uint32_t*>(&m);
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_empty[st]);
+      }
       // the largest magnitude of the tile, one value per warp, is what bounds its scores' rounding
       // error (a NaN counts as infinite)
       const float a = bf16_lo(top), z = bf16_hi(top);
       float m = a <= CUDART_INF_F && z <= CUDART_INF_F ? fmaxf(a, z) : CUDART_INF_F;
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-      if (lane == 0) *amax = m;
-      top = 0;
+      if (lane == 0)
+        p.amax[(w.row() * p.max_tiles + w.tile) * kHelpers + (warp - (C::kThreads / 32 - kHelpers))] = m;
     }
     griddep_launch_dependents();
   } else if (warp == 0) {
@@ -488,7 +494,7 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       for (KeyWalk<PAGES> w(p, s_share); w.left > 0 && ok; ++u) {
         if (w.fresh) {
           ++q;
-          if (!(ok = mbar_wait(&bar_qfull, q & 1, &abort_flag))) break;
+          if (!(ok = mbar_wait(&bar_qfull[q % nq], (q / nq) & 1, &abort_flag))) break;
         }
         const int db = u % C::kDBufs;
         if (!(ok = mbar_wait(&bar_dempty[db], ((u / C::kDBufs) & 1) ^ 1, &abort_flag))) break;
@@ -497,7 +503,7 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           const int st = s % C::kStages;
           if (!(ok = mbar_wait(&bar_full[st], (s / C::kStages) & 1, &abort_flag))) break;
           tc_fence_after();
-          const uint32_t qa = q_addr + h * 2 * n16 * 128;
+          const uint32_t qa = q_addr + ((q % nq) * 2 + h) * 2 * n16 * 128;
           const uint32_t aa = a_addr + st * kStage;
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
@@ -511,7 +517,7 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           umma_bf16(d, smem_desc(smem_u32(sOne), 16, 1024), smem_desc(smem_u32(sL), 16, 1024), idesc, 1u);
         umma_commit(&bar_dfull[db]);
         w.next();
-        if (w.left == 0 || w.fresh) umma_commit(&bar_qempty);
+        if (w.left == 0 || w.fresh) umma_commit(&bar_qempty[q % nq]);
       }
       umma_commit(&bar_done);
     }
@@ -674,7 +680,6 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 // long as both operands have the same, so a lane's 16-byte chunk of a page row (8 values) serves as
 // its fragments of two MMAs, 16 loads a lane are in flight at once, and nothing is staged but q+ and
 // q-.  A CTA takes 128 pages a round (8 warps), its share of the tiles as above, two CTAs per SM.
-constexpr int kDirectRows = 64;
 constexpr int kDirectPitch = 512 + 64;   // bytes of a q row: 64 more, so that 8 lanes miss no bank
 
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -746,7 +751,7 @@ page_scores_direct_kernel(const KeyParams p) {
     const size_t row = w.row(), out_row = (static_cast<size_t>(w.b) * p.groups + p.l0 / p.group) *
                                               group_stride +
                                           static_cast<size_t>(w.kvh) * p.max_pages;
-    float* amax = p.amax + (row * p.max_tiles + w.tile) * kLoaders + warp;
+    float* amax = p.amax + (row * p.max_tiles + w.tile) * kHelpers + warp;
     const int kvh = w.kvh;
     // the pages' rows: chunk 4j + t of lo (j < 4), then of hi
     uint4 a[8][2];
@@ -908,13 +913,13 @@ cudaError_t launch_direct_t(const KeyParams& p, int num_sms, cudaStream_t stream
 }
 }  // namespace
 
-cudaError_t launch_page_scores(const KeyParams& p, int num_sms, cudaStream_t stream) {
+cudaError_t launch_page_scores(const CUtensorMap& tm_q, const CUtensorMap& tm_bounds,
+                               const KeyParams& p, int num_sms, cudaStream_t stream) {
   if (p.rows <= 8) return launch_direct_t<1>(p, num_sms, stream);
   if (p.rows <= 16) return launch_direct_t<2>(p, num_sms, stream);
   if (p.rows <= 32) return launch_direct_t<4>(p, num_sms, stream);
   if (p.rows <= kDirectRows) return launch_direct_t<8>(p, num_sms, stream);
-  const CUtensorMap none = {};
-  return launch_key_t<true, true>(none, none, p, num_sms, stream);
+  return launch_key_t<true, true>(tm_q, tm_bounds, p, num_sms, stream);
 }
 
 cudaError_t launch_page_bounds(const uint16_t* k_pages, const int32_t* page_table,

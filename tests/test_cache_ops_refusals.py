@@ -84,6 +84,7 @@ def test_sizes(so):
         assert select(so, **bad) == -1, bad
     assert select(so, desc(L=64, Hq=16, Hkv=1), group=64, cols=20) == -3      # 1024 rows in a group
     assert select(so, desc(cols=262145)) == -3
+    assert select(so, desc(B=0, num=2 ** 27)) == -3 and select(so, desc(B=0, num=2 ** 27 - 1)) == 0
     for bad in (dict(group=0), dict(group=3), dict(cols=0), dict(cols=2 ** 28)):
         assert sparse(so, **bad) == -1, bad
     for bad in (dict(decay=float("nan")), dict(decay=float("inf"))):
