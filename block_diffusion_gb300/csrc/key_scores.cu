@@ -25,14 +25,15 @@
 //                warp's 16 boxes take about 1 us)
 //   warp 3       finds the CTA's share; weights: Q of a list by TMA (a 64-dim x G x L box per half)
 //   warps 4-     reduction, two or four sets of four warps (one per lane quadrant) in turn
-//   page scores  warps 1-2: a page's bounds are two rows of 256 bytes, so TMA gathers them, four
-//                rows of 128 bytes an instruction (warp 1 the tiles' hi, warp 2 lo); Q by TMA as for
-//                weights, which the last eight warps split into q+ and q- as a list begins (two
-//                buffers up to 128 query rows); they also take the largest magnitude of each stage.
-//                (Loads to registers are slow beside 227 KB of shared memory, which leave L1 few
-//                lines for what is in flight: pages and Q took 58 us that way, 128 lists of 1250-2500
-//                pages, 256 rows.)
-// Stages are 32 KB (128 keys x 128 values); a page tile takes two (hi, then lo).
+//   page scores  warps 1-2 and two more: a page's bounds are two rows of 256 bytes, so TMA gathers
+//                them, four rows of 128 bytes an instruction (about 50 ns each to issue, so four
+//                warps); Q by TMA as for weights, which the last eight warps split into q+ and q- as
+//                a list begins (two buffers up to 128 query rows); they also take the largest
+//                magnitude of each stage.  (Loads to registers are slow beside 227 KB of shared
+//                memory, which leave L1 few lines for what is in flight: 58 us a launch, 128 lists
+//                of 1250-2500 pages and 256 rows, against 40.)
+// Stages are 32 KB (128 keys x 128 values); a page tile takes two (hi, then lo).  (Halves of them, a
+// ring of six, were no faster: 97 us against 93, 512 lists of 125-375 pages.)
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -66,7 +67,7 @@ struct Cfg {
   static constexpr int kDBufs = WIDE ? 2 : 4;                  // X tiles in tensor memory
   static constexpr int kSets = kSplit ? 4 : 2;                 // reducing sets of four warps
   static constexpr int kTmemCols = WIDE ? 512 : 128;
-  static constexpr int kThreads = 128 + kSets * 128 + (PAGES ? kHelpers * 32 : 0);
+  static constexpr int kThreads = 128 + kSets * 128 + (PAGES ? (kHelpers + 2) * 32 : 0);
   // Weights of more than 32 rows: -lse / scale enters X through the MMA, as three bf16 numbers a row
   // (24 bits) against keys of 1, so that the reduction reads no table from shared memory beside
   // the MMAs (95 us a pass against 100, 16 x 64 x 4 rows over 8192-16384 tokens): 128-byte rows of
@@ -203,6 +204,7 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
                   const KeyParams p) {
   using C = Cfg<PAGES, WIDE>;
   constexpr int kHalves = PAGES ? 2 : 1;   // stages per tile
+  constexpr int kGather2 = 4 + C::kSets * 4;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -366,9 +368,10 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       }
     }
     __syncwarp();
-  } else if (PAGES && (warp == 1 || warp == 2)) {
+  } else if (PAGES && (warp == 1 || warp == 2 || warp == kGather2 || warp == kGather2 + 1)) {
     // ------------------------------------------------------------ TMA: page bounds
-    const int h = warp - 1;   // half 0: hi (row 1 of a page's bounds), half 1: lo (row 0)
+    // half 0: hi (row 1 of a page's bounds), half 1: lo (row 0); which 64 of the 128 values
+    const int h = warp < kGather2 ? warp - 1 : warp - kGather2, atom = warp < kGather2 ? 0 : 1;
     bool ok = true;
     KeyWalk<PAGES> w(p, s_share);
     int id[4], n_left;   // pages 4 * lane .. + 3 of the walk's tile
@@ -399,7 +402,7 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       load_ids();   // they arrive while the stage is waited for
       if (lane == 0) {
         ok = mbar_wait(&bar_empty[st], ((s / C::kStages) & 1) ^ 1, &abort_flag);
-        if (ok) {
+        if (ok && atom == 0) {
           s_have[st] = have != 0;
           if (have)
             mbar_arrive_expect_tx(&bar_full[st], kStage);
@@ -410,8 +413,7 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       ok = __shfl_sync(0xffffffffu, ok, 0);
       __syncwarp();
       if (ok && have)
-        for (int a = 0; a < 2; ++a)
-          tma_gather4(sA + st * kStage + a * kAtom + lane * 512, &tm_k, &bar_full[st], a * 64, row);
+        tma_gather4(sA + st * kStage + atom * kAtom + lane * 512, &tm_k, &bar_full[st], atom * 64, row);
     }
     if (!ok) {
       // as above: the copies in flight land before the CTA's memory goes away
