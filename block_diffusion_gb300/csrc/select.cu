@@ -173,19 +173,62 @@ __device__ __forceinline__ K kth_largest(int k, K lo, K hi, Each&& each, int* hi
 }
 
 // ------------------------------------------------------------------ page selection
-constexpr int kSelThreads = kRowThreads, kSelFewThreads = 128;
+constexpr int kSelThreads = kRowThreads;
+constexpr int kSelFewThreads = 128, kSelFewRows = 64;   // the variant for many short lists
 constexpr int kOwn = 8;              // keys of a thread in registers
 constexpr int kSelKeys = 12288;      // rows held in shared memory (96 KB); longer ones are re-read
 constexpr int kSelExact = 1024;      // near ties held in shared memory
 
-// Query n of a group (n < 256: its position n / G, head n % G; G <= 16, so the division is a product)
-// as 32 lanes' four values each.
-__device__ __forceinline__ const uint2* group_query(const SelectParams& p, int b, int s, int kvh,
+// The 16 chunks of query n of a group (n < 256: its position n / G, head n % G; G <= 16, so the
+// division is a product).
+__device__ __forceinline__ const uint4* group_query(const SelectParams& p, int b, int s, int kvh,
                                                     int n) {
   const int i = (n * ((65536 + p.G - 1) / p.G)) >> 16;
-  return reinterpret_cast<const uint2*>(p.q) +
-         ((static_cast<size_t>(b) * p.L + s * p.group + i) * p.Hq + kvh * p.G + (n - i * p.G)) * 32 +
-         (threadIdx.x & 31);
+  return reinterpret_cast<const uint4*>(p.q) +
+         ((static_cast<size_t>(b) * p.L + s * p.group + i) * p.Hq + kvh * p.G + (n - i * p.G)) * 16;
+}
+
+__device__ __forceinline__ float key_value(uint32_t key) {   // of order_key (not NaN)
+  return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
+}
+
+constexpr int kExactRows = 16;   // query rows of a warp's turn
+
+// Scores of one page for query rows row0 .. rows - 1 (at most 16) of one group, in float32 with 11
+// roundings of partial sums.  Whole warp, 16 lanes a row, two rows at a time: lane l has that of row
+// near_row(l), lanes l % 16 >= 8 have -inf.  (All 16 rows' queries in registers at once, their sums
+// crossed over the lanes together, takes fewer instructions but more code, which is read anew by
+// every launch: 58 us a call against 53, 16 x 8 lists of 1875-3750 pages.)
+__device__ __forceinline__ int near_row(int l) { return 2 * (l & 15) + (l >> 4); }
+__device__ __forceinline__ float float_scores(const SelectParams& p, int b, int s, int kvh, int id,
+                                              int row0, int rows) {
+  const int c16 = threadIdx.x & 15, half = (threadIdx.x >> 4) & 1;
+  const uint4* page = reinterpret_cast<const uint4*>(p.bounds) +
+                      (static_cast<size_t>(id) * p.Hkv + kvh) * 32 + c16;
+  const uint4 lo = __ldg(page), hi = __ldg(page + 16);
+  const uint32_t l[4] = {lo.x, lo.y, lo.z, lo.w}, h[4] = {hi.x, hi.y, hi.z, hi.w};
+  float mine = -CUDART_INF_F;
+#pragma unroll 4
+  for (int x = 0; x < kExactRows / 2; ++x) {
+    const uint4 v = __ldg(group_query(p, b, s, kvh, min(row0 + 2 * x + half, rows - 1)) + c16);
+    const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+    float f = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float q0 = bf16_lo(q[k]), q1 = bf16_hi(q[k]);
+      f = fmaf(q0, q0 > 0.f ? bf16_lo(h[k]) : bf16_lo(l[k]), f);
+      f = fmaf(q1, q1 > 0.f ? bf16_hi(h[k]) : bf16_hi(l[k]), f);
+    }
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1) f += __shfl_xor_sync(0xffffffffu, f, off);
+    mine = c16 == x ? f : mine;
+  }
+  return mine;
+}
+__device__ __forceinline__ float warp_most(float v) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+  return v;
 }
 
 // a + b as s + e exactly
@@ -195,54 +238,24 @@ __device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
   e = __fadd_rn(__fadd_rn(a, -__fadd_rn(s, -bb)), __fadd_rn(b, -bb));
 }
 
-// The largest score of one page over query rows row0 .. rows - 1 (at most 16) of one group, to about
-// 2^-45 of its terms, as an ordered 64-bit key (never 0 or 1).  Whole warp: lane l takes dims 4l ..
-// 4l + 3.  First every row's plain float32 score, all rows' queries loaded at once (off by less
-// than 2^-16 of the terms' sum, within E below); then the rows within 2E (`band`) of the largest,
-// the only ones that can hold the maximum: the products of two bf16 are exact in float32, and are
-// added with the rounding errors carried along.
-constexpr int kExactRows = 16;
+// The largest score of one page over the rows of one group whose float32 score (`mine`, of rows row0 ..)
+// is at least `from`, to about 2^-45 of its terms, as an ordered 64-bit key (never 0 or 1; 0: no such
+// row): the products of two bf16 are exact in float32, and are added with the rounding errors
+// carried along.  Whole warp.
 __device__ __forceinline__ unsigned long long exact_score(const SelectParams& p, int b, int s,
                                                           int kvh, int id, int row0, int rows,
-                                                          float band) {
+                                                          float mine, float from) {
   const int lane = threadIdx.x & 31;
   const uint2* page = reinterpret_cast<const uint2*>(p.bounds) +
                       (static_cast<size_t>(id) * p.Hkv + kvh) * 64 + lane;
-  auto query = [&](int n) { return __ldg(group_query(p, b, s, kvh, n)); };
-  const uint2 lo = __ldg(page), hi = __ldg(page + 32);
-  uint2 q[kExactRows];
-#pragma unroll
-  for (int x = 0; x < kExactRows; ++x) q[x] = query(min(row0 + x, rows - 1));
-  const float lv[4] = {bf16_lo(lo.x), bf16_hi(lo.x), bf16_lo(lo.y), bf16_hi(lo.y)};
-  const float hv[4] = {bf16_lo(hi.x), bf16_hi(hi.x), bf16_lo(hi.y), bf16_hi(hi.y)};
-  float f[kExactRows];
-#pragma unroll
-  for (int x = 0; x < kExactRows; ++x) {
-    const float qv[4] = {bf16_lo(q[x].x), bf16_hi(q[x].x), bf16_lo(q[x].y), bf16_hi(q[x].y)};
-    f[x] = 0.f;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) f[x] = fmaf(qv[k], qv[k] > 0.f ? hv[k] : lv[k], f[x]);
-  }
-  // sums over the lanes, the rows halved in every step: lane l ends with row l / 2
-#pragma unroll
-  for (int h = kExactRows / 2; h > 0; h >>= 1) {
-    const bool up = lane & (2 * h);
-#pragma unroll
-    for (int x = 0; x < h; ++x) {
-      const float keep = up ? f[x + h] : f[x], send = up ? f[x] : f[x + h];
-      f[x] = keep + __shfl_xor_sync(0xffffffffu, send, 2 * h);
-    }
-  }
-  const float mine = f[0] + __shfl_xor_sync(0xffffffffu, f[0], 1);
-  float most = mine;
-#pragma unroll
-  for (int off = 16; off > 1; off >>= 1)
-    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
-  uint32_t near = __ballot_sync(0xffffffffu, mine >= __fadd_rd(most, -band)) & 0x55555555u;
-  if (near == 0) near = 1;   // (scores that are not numbers)
   unsigned long long best = 0;
-  for (; near; near &= near - 1) {
-    const uint2 v = query(min(row0 + (__ffs(static_cast<int>(near)) - 1) / 2, rows - 1));
+  for (uint32_t near = __ballot_sync(0xffffffffu, mine >= from && (lane & 15) < kExactRows / 2); near;
+       near &= near - 1) {
+    const int n = min(row0 + near_row(__ffs(static_cast<int>(near)) - 1), rows - 1);
+    const uint2 v = __ldg(reinterpret_cast<const uint2*>(group_query(p, b, s, kvh, n)) + lane);
+    const uint2 lo = __ldg(page), hi = __ldg(page + 32);
+    const float lv[4] = {bf16_lo(lo.x), bf16_hi(lo.x), bf16_lo(lo.y), bf16_hi(lo.y)};
+    const float hv[4] = {bf16_lo(hi.x), bf16_hi(hi.x), bf16_lo(hi.y), bf16_hi(hi.y)};
     const float qv[4] = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y)};
     float a = 0.f, e = 0.f;
 #pragma unroll
@@ -251,7 +264,7 @@ __device__ __forceinline__ unsigned long long exact_score(const SelectParams& p,
       two_sum(a, __fmul_rn(qv[k], qv[k] > 0.f ? hv[k] : lv[k]), a, r);
       e = __fadd_rn(e, r);
     }
-#pragma unroll
+#pragma unroll 1
     for (int off = 16; off > 0; off >>= 1) {
       const float a2 = __shfl_xor_sync(0xffffffffu, a, off);
       const float e2 = __shfl_xor_sync(0xffffffffu, e, off);
@@ -271,7 +284,8 @@ __device__ __forceinline__ unsigned long long exact_score(const SelectParams& p,
 // One CTA per (sequence, query group, KV head).  The scores come from the tensor core in float32;
 // where two of them lie closer than their rounding could explain, float32 does not say which is
 // larger.  So with T the k-th largest and E a bound on a score's error, pages above T + 2E are
-// in, pages below T - 2E are out, and the few between are scored again to about 45 bits.
+// in, pages below T - 2E are out, and the few between are scored again: in float32 with few
+// roundings, whose bound is 1/45 of E and settles nearly all; where it does not, to about 45 bits.
 //   E = 16 * 17 * 2^-23 max_n |q_n|_1 max |bound|: a score sums 128 products (and 128 zeros) in 16
 //   MMAs of 16, each of which rounds or truncates at most 17 values by 2^-23 of the largest
 //   partial sum, and no partial sum exceeds |q|_1 max|bound|.
@@ -290,6 +304,7 @@ select_pages_kernel(const SelectParams p) {
   extern __shared__ uint32_t sm[];
   __shared__ __align__(16) int hist[4 * THREADS];
   __shared__ unsigned long long s_exact[kSelExact];
+  __shared__ uint32_t s_fast[kSelExact];
   __shared__ int s_page[kSelExact];
   __shared__ int s_scan[36];
   __shared__ unsigned long long s_wide[64];
@@ -344,14 +359,21 @@ select_pages_kernel(const SelectParams p) {
     const float* a = p.amax + (static_cast<size_t>(b) * p.Hkv + kvh) * p.max_tiles * kAmaxPerTile;
     for (int i = tid; i < values; i += THREADS) am = fmaxf(am, __ldcg(a + i));
   }
-#pragma unroll 4
-  for (int r = warp; r < p.group * p.G; r += kWarps) {
-    const uint2 q = __ldg(group_query(p, b, s, kvh, r));
-    float v = fabsf(bf16_lo(q.x)) + fabsf(bf16_hi(q.x)) + fabsf(bf16_lo(q.y)) + fabsf(bf16_hi(q.y));
+  for (int r = tid >> 1; r < p.group * p.G; r += THREADS / 2) {   // a row for two threads
+    const uint4* src = group_query(p, b, s, kvh, r) + (tid & 1) * 8;
+    uint4 q[8];
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    for (int x = 0; x < 8; ++x) q[x] = __ldg(src + x);
+    float v = 0.f;
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+      v += (fabsf(bf16_lo(q[x].x)) + fabsf(bf16_hi(q[x].x))) + (fabsf(bf16_lo(q[x].y)) + fabsf(bf16_hi(q[x].y))) +
+           ((fabsf(bf16_lo(q[x].z)) + fabsf(bf16_hi(q[x].z))) + (fabsf(bf16_lo(q[x].w)) + fabsf(bf16_hi(q[x].w))));
     q1 = fmaxf(q1, v);
   }
+  q1 += __shfl_xor_sync(0xffffffffu, q1, 1);   // (each half row's largest: not less than the row's)
+#pragma unroll
+  for (int off = 16; off > 1; off >>= 1) q1 = fmaxf(q1, __shfl_xor_sync(0xffffffffu, q1, off));
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, off));
   if (lane == 0) {
@@ -419,9 +441,10 @@ select_pages_kernel(const SelectParams p) {
     am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, off));
   }
   const float band = q1 * am * (2 * 16 * 17 * 0x1p-23f);   // 2E
-  const float t = __uint_as_float(T & 0x80000000u ? T & 0x7FFFFFFFu : ~T);
-  // (scores or bounds that are not finite have no error bound: their float32 order stands)
-  const bool refine = T != 0 && band <= 3e38f && fabsf(t) <= 3e38f;
+  const float t = key_value(T);
+  // (scores or bounds that are not finite, or whose sums may not be, have no error bound: their
+  // float32 order stands)
+  const bool refine = T != 0 && q1 * am <= 1e38f && fabsf(t) <= 3e38f;
   const uint32_t k_hi = refine ? order_key(__fadd_ru(t, band)) : T;
   const uint32_t k_lo = refine ? order_key(__fadd_rd(t, -band)) : T;
   auto take = [&](int i) { atomicOr(&taken[i >> 5], 1u << (i & 31)); };
@@ -434,6 +457,7 @@ select_pages_kernel(const SelectParams p) {
       const int c = atomicAdd(&s_cand, 1);
       if (c < kSelExact) {
         s_page[c] = i;
+        s_fast[c] = 0;
         s_exact[c] = 0;
       }
     }
@@ -441,96 +465,145 @@ select_pages_kernel(const SelectParams p) {
   BlockSum sum{s_scan};
   int n_sure;
   sum.exclusive(sure, &n_sure);
-  const int m = s_cand, need = k - n_sure;   // candidates, and how many of them are in (>= 1)
+  const int m = s_cand;
+  int need = k - n_sure;   // how many of the m candidates are in (>= 1)
   if (m == need) {
     each_key([&](int i, uint32_t key) {
       if (key >= k_lo && key <= k_hi) take(i);
     });
   } else {
-    // Up to kSelExact candidates are listed in shared memory, and their rows go to the warps in
-    // batches (all rows together where they are pruned): the maximum over the batches does not
-    // depend on their order.  More of them (pages that are copies of each other) keep their scores
-    // in the workspace.
+    // Up to kSelExact candidates are listed in shared memory, and a warp takes 16 of their rows.  First
+    // their float32 scores; candidates that these leave open then get the exact ones of the rows
+    // that can hold their maximum.  More candidates (pages that are copies of each other) keep exact
+    // scores in the workspace.
     const bool listed = m <= kSelExact;
-    unsigned long long* exact = p.exact + static_cast<size_t>(list) * p.max_pages;
-    unsigned long long elo = ~0ull, ehi = 0;
-    if (!listed && refine) {
-      each_key([&](int i, uint32_t key) { exact[i] = key >= k_lo && key <= k_hi ? 1 : 0; });
-      __syncthreads();
-    }
-    const int rows = p.group * p.G, per = kExactRows, parts = listed ? (rows + per - 1) / per : 1;
-    const int work = !refine ? 0 : listed ? m * parts : n;
-    for (int x = warp; x < work; x += kWarps) {
-      // a listed candidate's batch, or every batch of one of many
-      const int c = x / parts, i = listed ? s_page[c] : x;
-      const int first = listed ? x % parts * per : 0, end = listed ? min(rows, first + per) : rows;
-      if (!listed && __ldcg(exact + i) == 0) continue;
-      const int id = page_id(i);
-      unsigned long long e = 1;   // a bad page: below every score
-      if (id >= 0 && id < p.num_pages)
-        for (int row0 = first; row0 < end; row0 += per) {
-          const unsigned long long part =
-              exact_score(p, b, s, kvh, id, row0, min(end, row0 + per), band);
-          e = part > e ? part : e;
+    const int rows = p.group * p.G, parts = (rows + kExactRows - 1) / kExactRows;
+    // 2 * 12 * 2^-24 max |q|_1 max |bound| as a part of `band`, and some for roundings here
+    const float near = band * 0.0235f;
+    if (refine && listed) {
+      // (a turn for each warp at most: at once the exact ones)
+      for (int pass = m * parts <= kWarps ? 1 : 0;; ++pass) {
+        for (int x = warp; x < m * parts; x += kWarps) {
+          const int c = x / parts, first = (x - c * parts) * kExactRows, i = s_page[c];
+          const int id = i >= 0 ? page_id(i) : -1;
+          if (id < 0 || id >= p.num_pages) continue;   // (a bad page: below every score)
+          const float mine = float_scores(p, b, s, kvh, id, first, rows);
+          const float most = warp_most(mine);
+          if (pass == 0) {
+            if (lane == 0) atomicMax(&s_fast[c], order_key(most));
+          } else {
+            // the candidate's largest, where the first pass found it (else 0, whose value is NaN)
+            const float f = fmaxf(most, key_value(s_fast[c]));
+            const unsigned long long e =
+                exact_score(p, b, s, kvh, id, first, rows, mine, __fadd_rd(f, -near));
+            if (lane == 0 && e != 0) atomicMax(&s_exact[c], e);
+          }
         }
-      __syncwarp();
-      if (lane == 0) {
-        if (listed)
-          atomicMax(&s_exact[c], e);
-        else
-          exact[i] = e;
+        __syncthreads();
+        if (pass > 0) break;
+        int in = 0, open = 0;   // candidates
+        for (int c = tid; c < m; c += THREADS) {
+          const float f = key_value(s_fast[c]);
+          int ahead = 0, maybe = -1;   // (-1: itself)
+          for (int j = 0; j < m; ++j) {
+            const float d = key_value(s_fast[j]) - f;
+            ahead += d > near;
+            maybe += d >= -near;
+          }
+          const bool out = s_fast[c] == 0 || ahead >= need, sure = !out && maybe < need;
+          if (sure) take(s_page[c]);
+          if (sure || out) s_page[c] = -1;   // decided
+          in += sure;
+          open += !sure && !out;
+        }
+        int n_in, n_open;
+        sum.exclusive(in + (open << 16), &n_in);   // (at most 1024 of each)
+        n_open = n_in >> 16;
+        n_in &= 0xFFFF;
+        need = n_open > 0 ? need - n_in : 0;
+        if (n_open == 0) break;
       }
-      elo = e < elo ? e : elo;
-      ehi = e > ehi ? e : ehi;
     }
-    __syncthreads();
-    int equal = need;   // how many of `second`, the candidates equal to the last one in, are in
-    for (int i = tid; i < words; i += THREADS) second[i] = 0;
-    if (!refine) {
-      __syncthreads();
-      each_key([&](int i, uint32_t key) {
-        if (key == T) atomicOr(&second[i >> 5], 1u << (i & 31));
-      });
-    } else if (listed) {
-      equal = 0;
-      for (int c = tid; c < m; c += THREADS) {
-        const unsigned long long e = s_exact[c];
-        const int page = s_page[c];
-        int rank = 0;   // candidates ahead of this one
-        for (int j = 0; j < m; ++j)
-          rank += s_exact[j] > e || (s_exact[j] == e && s_page[j] < page);
-        if (rank < need) take(page);
-      }
-    } else {
-      block_range(elo, ehi, s_wide);
-      int larger;
-      const unsigned long long TE = kth_largest<THREADS, unsigned long long>(
-          need, elo, ehi,
-          [&](auto&& f) {
-            for (int i = tid; i < n; i += THREADS) {
-              const unsigned long long e = __ldcg(exact + i);
-              if (e != 0) f(e);
+    if (need > 0) {
+      unsigned long long* exact = p.exact + static_cast<size_t>(list) * p.max_pages;
+      unsigned long long elo = ~0ull, ehi = 0;
+      if (!listed && refine) {
+        each_key([&](int i, uint32_t key) { exact[i] = key >= k_lo && key <= k_hi ? 1 : 0; });
+        __syncthreads();
+        for (int i = warp; i < n; i += kWarps) {
+          if (__ldcg(exact + i) == 0) continue;
+          const int id = page_id(i);
+          unsigned long long e = 1;   // a bad page: below every score
+          if (id >= 0 && id < p.num_pages) {
+            float most = -CUDART_INF_F;
+            for (int x = 0; x < 2 * parts; ++x) {   // every row's float32 score, then again
+              const int first = (x < parts ? x : x - parts) * kExactRows;
+              const float mine = float_scores(p, b, s, kvh, id, first, rows);
+              if (x < parts) {
+                most = fmaxf(most, warp_most(mine));
+                continue;
+              }
+              const unsigned long long part =
+                  exact_score(p, b, s, kvh, id, first, rows, mine, __fadd_rd(most, -near));
+              e = part > e ? part : e;
             }
-          },
-          hist, s_scan, s_pick, &larger);
-      equal = need - larger;
-      for (int i = tid; i < n; i += THREADS) {
-        const unsigned long long e = __ldcg(exact + i);
-        if (e > TE) take(i);
-        if (e == TE) atomicOr(&second[i >> 5], 1u << (i & 31));
+          }
+          __syncwarp();
+          if (lane == 0) exact[i] = e;
+          elo = e < elo ? e : elo;
+          ehi = e > ehi ? e : ehi;
+        }
       }
-    }
-    __syncthreads();
-    int base = 0;   // of equal ones the lowest positions
-    for (int w0 = 0; w0 < words && equal > 0; w0 += THREADS) {
-      const int w = w0 + tid;
-      const uint32_t bits = w < words ? second[w] : 0;
-      int total;
-      int before = base + sum.exclusive(__popc(bits), &total);
-      uint32_t keep = 0;
-      for (uint32_t x = bits; x && before < equal; x &= x - 1, ++before) keep |= x & (0u - x);
-      if (keep) taken[w] |= keep;
-      base += total;
+      __syncthreads();
+      int equal = need;   // how many of `second`, the candidates equal to the last one in, are in
+      for (int i = tid; i < words; i += THREADS) second[i] = 0;
+      if (!refine) {
+        __syncthreads();
+        each_key([&](int i, uint32_t key) {
+          if (key == T) atomicOr(&second[i >> 5], 1u << (i & 31));
+        });
+      } else if (listed) {
+        equal = 0;
+        for (int c = tid; c < m; c += THREADS) {
+          const unsigned long long e = s_exact[c];
+          const int page = s_page[c];
+          if (page < 0) continue;
+          int rank = 0;   // candidates ahead of this one
+          for (int j = 0; j < m; ++j)
+            rank += s_exact[j] > e || (s_exact[j] == e && s_page[j] < page);
+          if (rank < need) take(page);
+        }
+      } else {
+        block_range(elo, ehi, s_wide);
+        int larger;
+        const unsigned long long TE = kth_largest<THREADS, unsigned long long>(
+            need, elo, ehi,
+            [&](auto&& f) {
+              for (int i = tid; i < n; i += THREADS) {
+                const unsigned long long e = __ldcg(exact + i);
+                if (e != 0) f(e);
+              }
+            },
+            hist, s_scan, s_pick, &larger);
+        equal = need - larger;
+        for (int i = tid; i < n; i += THREADS) {
+          const unsigned long long e = __ldcg(exact + i);
+          if (e > TE) take(i);
+          if (e == TE) atomicOr(&second[i >> 5], 1u << (i & 31));
+        }
+      }
+      __syncthreads();
+      int base = 0;   // of equal ones the lowest positions
+      for (int w0 = 0; w0 < words && equal > 0; w0 += THREADS) {
+        const int w = w0 + tid;
+        const uint32_t bits = w < words ? second[w] : 0;
+        int total;
+        int before = base + sum.exclusive(__popc(bits), &total);
+        uint32_t keep = 0;
+        for (uint32_t x = bits; x && before < equal; x &= x - 1, ++before) keep |= x & (0u - x);
+        if (keep) taken[w] |= keep;
+        base += total;
+      }
     }
   }
   __syncthreads();
@@ -852,7 +925,7 @@ cudaError_t launch_select_pages(const SelectParams& p, int num_sms, cudaStream_t
   const size_t words = (static_cast<size_t>(p.max_pages) + 31) / 32;
   const unsigned lists = static_cast<unsigned>(p.B) * p.groups * p.Hkv;
   if (p.max_pages <= kOwn * kSelFewThreads && lists > 2u * static_cast<unsigned>(num_sms) &&
-      p.group * p.G <= 64)
+      p.group * p.G <= kSelFewRows)
     return launch_pdl(select_pages_kernel<kSelFewThreads, 6>, dim3(lists), dim3(kSelFewThreads),
                       (p.max_pages + 2 * words) * 4, stream, p);
   // page ids and keys (of rows that fit), then two bitmaps of the row's pages

@@ -126,6 +126,31 @@ def test_selection_of_equal_pages_takes_the_first(lib):
         p.check(lib, 1, n)
 
 
+@pytest.mark.parametrize("L,group,G", [(4, 4, 4), (4, 1, 4), (16, 16, 4), (3, 3, 16), (10, 5, 8), (32, 32, 4)])
+@pytest.mark.parametrize("ties", [False, True])
+def test_selection_of_many_short_lists(lib, L, group, G, ties):
+    """More lists than are worked on at once, of up to 64 query rows and of more."""
+    rng = np.random.default_rng(L + G)
+    p = Pages(rng, rng.integers(0, 1500, size=90), L, 8 * G, 8)
+    if ties:   # few kinds of pages, one bf16 step apart in one dim
+        p.bounds[:] = p.bounds[0]
+        p.bounds[:, :, 1, 7] += rng.integers(0, 6, size=(p.num, 1)).astype(np.uint16)
+    for n in (1, 30):
+        p.check(lib, group, n)
+
+
+@pytest.mark.parametrize("L,group,Hq,Hkv", [(64, 64, 32, 8), (32, 16, 64, 8), (5, 5, 16, 1), (48, 48, 4, 1)])
+def test_selection_of_near_ties_over_many_rows(lib, L, group, Hq, Hkv):
+    """Pages whose scores differ by a bf16 step of one or two bounds, for some rows only."""
+    rng = np.random.default_rng(L + Hq)
+    p = Pages(rng, [2500, 19000], L, Hq, Hkv)
+    p.bounds[:] = p.bounds[0]
+    for dim in (3, 90):
+        p.bounds[:, :, :, dim] += rng.integers(0, 3, size=(p.num, 1, 2)).astype(np.uint16)
+    for n in (1, 40, 155):
+        p.check(lib, group, n)
+
+
 def test_selection_tells_close_scores_apart(lib):
     """Scores that differ by less than float32 resolves at their size: one dim moves by a step of
     bf16 where the query is small."""
