@@ -297,7 +297,7 @@ __device__ __forceinline__ unsigned long long exact_score(const SelectParams& p,
 // 125-375 pages: 70 against 83).  128 threads, six CTAs per SM, for more lists than that has places
 // for, of pages that fit the registers (the same 1024 lists 54 against 70, 2048 lists 54 against 87,
 // 512 lists 38 against 44; with 128 lists of 500-1000 pages it loses, 33 against 29) and of up to 64
-// query rows, which the exact scores need warps for (512 lists of 256 rows: 171 against 158).
+// query rows, which near ties need warps for (512 lists of 256 rows: 105 against 85).
 template <int THREADS, int CTAS>
 __global__ void __launch_bounds__(THREADS, CTAS)
 select_pages_kernel(const SelectParams p) {
