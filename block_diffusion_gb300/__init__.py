@@ -150,11 +150,24 @@ def _ptr(x) -> int | None:
     return x.data_ptr()
 
 
+_device = _raw_stream = None   # of torch, once CUDA is initialised
+
+
+def _current_device() -> int:
+    global _device, _raw_stream
+    if _device is None:
+        import torch
+        torch.cuda.current_device()
+        # without the check for initialisation (0.1 us against 0.2), and the current stream's handle
+        # without a Stream object around it (0.1 us against 2.9)
+        _raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    return _device()
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
-        # the current stream's handle without a Stream object around it (0.1 us against 2.9)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        dev = _current_device()
+        return _raw_stream(dev)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -163,8 +176,7 @@ def _stream(stream) -> int | None:
 def _dense(fn: str, stream, *tensors) -> list:
     """Device addresses of the tensors (addresses and None pass), and the stream's.  Refuses a
     tensor that a bare address would misread: not contiguous, or not on the current device."""
-    import torch
-    dev = torch.cuda.current_device()
+    dev = _current_device()
     out = []
     for t in tensors:
         if t is not None and not isinstance(t, int):
@@ -172,7 +184,7 @@ def _dense(fn: str, stream, *tensors) -> list:
                 raise BdlmError(fn, BDLM_ERR_INVALID)
             t = t.data_ptr()
         out.append(t)
-    out.append(_stream(stream))
+    out.append(_raw_stream(dev) if stream is None else _stream(stream))
     return out
 
 
