@@ -741,46 +741,52 @@ int bdlm_select_pages(const bdlm_attn_desc* desc, const bdlm_bf16* q, const bdlm
   DeviceState* st = nullptr;
   int rc = current_device(&st);
   if (rc) return rc;
-  // a launch scores whole groups of up to 256 query rows per KV head
-  int per = bdlm::key_rows_max() / (group * G) * group;
-  if (per > d.L) per = d.L;
-  const int max_tiles = (d.max_pages_per_seq + bdlm::kKeyTile - 1) / bdlm::kKeyTile;
-  const size_t score_bytes =
-      align256(static_cast<size_t>(lists) * d.max_pages_per_seq * sizeof(float));
-  const size_t amax_bytes =
-      static_cast<size_t>(d.B) * d.Hkv * max_tiles * bdlm::kAmaxPerTile * sizeof(float);
-  // workspace: near ties' exact scores | scores | magnitudes
-  rc = ensure(&st->data, &st->data_cap, 3 * score_bytes + amax_bytes, false, stream);
-  if (rc) return rc;
-  bdlm::KeyParams p = key_params(d, page_table, prefix_lens, st->err);
-  p.max_tiles = max_tiles;
-  p.q = q;
-  p.bounds = bounds;
-  p.scores = reinterpret_cast<float*>(static_cast<uint8_t*>(st->data) + 2 * score_bytes);
-  p.amax = reinterpret_cast<float*>(static_cast<uint8_t*>(st->data) + 3 * score_bytes);
-  p.group = group;
-  p.groups = groups;
-  p.width = group * G;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  CUtensorMap tm_q = {}, tm_bounds = {};
-  if (per * G > bdlm::kDirectRows) {
-    if ((rc = get_encoder())) return rc;
-    const cuuint64_t dims[2] = {128, static_cast<cuuint64_t>(d.num_pages) * d.Hkv * 2};
-    const cuuint64_t strides[1] = {256};
-    const cuuint32_t box[2] = {64, 1};
-    if ((rc = encode(&tm_bounds, bounds, 2, dims, strides, box))) return rc;
+  const int max_tiles = (d.max_pages_per_seq + bdlm::kKeyTile - 1) / bdlm::kKeyTile;
+  bdlm::SelectParams sp{q, bounds, page_table, prefix_lens, nullptr, nullptr, nullptr,
+                        d.B, d.L, d.Hq, d.Hkv, G, d.max_pages_per_seq, d.num_pages, group,
+                        groups, max_tiles, n_select, sel_cols,
+                        sel_table, sel_lens, st->err};
+  if (!bdlm::select_scores_itself(static_cast<int>(lists), d.max_pages_per_seq, group * G,
+                                  st->num_sms)) {
+    // workspace: near ties' exact scores | scores | magnitudes
+    const size_t score_bytes =
+        align256(static_cast<size_t>(lists) * d.max_pages_per_seq * sizeof(float));
+    const size_t amax_bytes =
+        static_cast<size_t>(d.B) * d.Hkv * max_tiles * bdlm::kAmaxPerTile * sizeof(float);
+    rc = ensure(&st->data, &st->data_cap, 3 * score_bytes + amax_bytes, false, stream);
+    if (rc) return rc;
+    bdlm::KeyParams p = key_params(d, page_table, prefix_lens, st->err);
+    p.max_tiles = max_tiles;
+    p.q = q;
+    p.bounds = bounds;
+    p.scores = reinterpret_cast<float*>(static_cast<uint8_t*>(st->data) + 2 * score_bytes);
+    p.amax = reinterpret_cast<float*>(static_cast<uint8_t*>(st->data) + 3 * score_bytes);
+    p.group = group;
+    p.groups = groups;
+    p.width = group * G;
+    // a launch scores whole groups of up to 256 query rows per KV head
+    int per = bdlm::key_rows_max() / (group * G) * group;
+    if (per > d.L) per = d.L;
+    CUtensorMap tm_q = {}, tm_bounds = {};
+    if (per * G > bdlm::kDirectRows) {
+      if ((rc = get_encoder())) return rc;
+      const cuuint64_t dims[2] = {128, static_cast<cuuint64_t>(d.num_pages) * d.Hkv * 2};
+      const cuuint64_t strides[1] = {256};
+      const cuuint32_t box[2] = {64, 1};
+      if ((rc = encode(&tm_bounds, bounds, 2, dims, strides, box))) return rc;
+    }
+    for (p.l0 = 0; p.l0 < d.L; p.l0 += per) {
+      const int nl = d.L - p.l0 < per ? d.L - p.l0 : per;
+      p.rows = nl * G;
+      if (p.rows > bdlm::kDirectRows && (rc = encode_key_q(&tm_q, q, d, nl))) return rc;
+      if (bdlm::launch_page_scores(tm_q, tm_bounds, p, st->num_sms, s) != cudaSuccess)
+        return BDLM_ERR_CUDA;
+    }
+    sp.scores = p.scores;
+    sp.amax = p.amax;
+    sp.exact = static_cast<unsigned long long*>(st->data);
   }
-  for (p.l0 = 0; p.l0 < d.L; p.l0 += per) {
-    const int nl = d.L - p.l0 < per ? d.L - p.l0 : per;
-    p.rows = nl * G;
-    if (p.rows > bdlm::kDirectRows && (rc = encode_key_q(&tm_q, q, d, nl))) return rc;
-    if (bdlm::launch_page_scores(tm_q, tm_bounds, p, st->num_sms, s) != cudaSuccess) return BDLM_ERR_CUDA;
-  }
-  const bdlm::SelectParams sp{q, bounds, page_table, prefix_lens, p.scores, p.amax,
-                              static_cast<unsigned long long*>(st->data),
-                              d.B, d.L, d.Hq, d.Hkv, G, d.max_pages_per_seq, d.num_pages, group,
-                              groups, max_tiles, n_select, sel_cols,
-                              sel_table, sel_lens, st->err};
   return bdlm::launch_select_pages(sp, st->num_sms, s) == cudaSuccess ? BDLM_OK : BDLM_ERR_CUDA;
 }
 

@@ -78,6 +78,9 @@ struct SelectParams {
   int* err;
 };
 constexpr int kSelectMaxPages = 262144;   // a list's page bitmap fits shared memory
+// Whether launch_select_pages needs no scores (short lists that fill the GPU once at most): scores, amax
+// and exact are not used then.
+bool select_scores_itself(int lists, int max_pages, int rows, int num_sms);
 cudaError_t launch_select_pages(const SelectParams& p, int num_sms, cudaStream_t stream);
 
 struct EvictParams {

@@ -40,6 +40,7 @@
 #include <stdint.h>
 
 #include "cache_ops.h"
+#include "page_mma.cuh"
 #include "ptx.cuh"
 
 namespace bdlm {
@@ -99,15 +100,6 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                : "r"(addr)
                : "memory");
-  return v;
-}
-
-// 16 bytes that are read once
-__device__ __forceinline__ uint4 ld_stream16(const uint4* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
   return v;
 }
 
@@ -436,14 +428,8 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 #pragma unroll 4
       for (int c = t * 16; c < n16 * 256; c += kHelpers * 512) {
         const uint4 v = lds16(at + c);
-        const uint32_t y[4] = {v.x, v.y, v.z, v.w};
         uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t neg = ((y[k] >> 15) & 0x00010001u) * 0xFFFFu;   // 16 ones per negative
-          hi[k] = y[k] & ~neg;
-          lo[k] = y[k] & neg;
-        }
+        split_signs(v, hi, lo);
         sts16(at + c, hi);
         sts16(at + n16 * 256 + c, lo);
       }
@@ -461,27 +447,15 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         if (s_have[st]) {
           const uint32_t a = smem_u32(sA) + st * kStage + t * 16;
 #pragma unroll
-          for (int i = 0; i < kStage / 16 / (kHelpers * 32); ++i) {
-            const uint4 v = lds16(a + i * kHelpers * 512);
-            const uint32_t y[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t mag = y[k] & 0x7FFF7FFFu;
-              const __nv_bfloat162 m = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&top),
-                                                   *reinterpret_cast<const __nv_bfloat162*>(&mag));
-              top = *reinterpret_cast<const uint32_t*>(&m);
-            }
-          }
+          for (int i = 0; i < kStage / 16 / (kHelpers * 32); ++i)
+            most_magnitude(top, lds16(a + i * kHelpers * 512));
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar_empty[st]);
       }
       // the largest magnitude of the tile, one value per warp, is what bounds its scores' rounding
-      // error (a NaN counts as infinite)
-      const float a = bf16_lo(top), z = bf16_hi(top);
-      float m = a <= CUDART_INF_F && z <= CUDART_INF_F ? fmaxf(a, z) : CUDART_INF_F;
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+      // error
+      const float m = warp_magnitude(top);
       if (lane == 0)
         p.amax[(w.row() * p.max_tiles + w.tile) * kHelpers + (warp - (C::kThreads / 32 - kHelpers))] = m;
     }
@@ -677,22 +651,9 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
 // Page scores of up to 64 query rows.  A page's 512 bytes take 2 * 16 to 64 rows * 256 flops: HBM
 // is the only bound, and staging pages in shared memory for tcgen05 (the kernel above) costs more
 // than it saves (16 x 8 lists of 1875-3750 pages, 16 rows: 42 us against 35; lists of 1250-2500 pages,
-// 64 rows: a whole selection of 72 us against 62).  So each warp scores 16
-// pages with m16n8k16 straight from global memory: the order of the 256 values along K is free as
-// long as both operands have the same, so a lane's 16-byte chunk of a page row (8 values) serves as
-// its fragments of two MMAs, 16 loads a lane are in flight at once, and nothing is staged but q+ and
-// q-.  A CTA takes 128 pages a round (8 warps), its share of the tiles as above, two CTAs per SM.
-constexpr int kDirectPitch = 512 + 64;   // bytes of a q row: 64 more, so that 8 lanes miss no bank
-
-__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
+// 64 rows: a whole selection of 72 us against 62).  So each warp scores 16 pages straight from global
+// memory (page_mma.cuh).  A CTA takes 128 pages a round (8 warps), its share of the tiles as above,
+// two CTAs per SM.
 template <int NT>   // query rows in tiles of 8
 __global__ void __launch_bounds__(256, 2)
 page_scores_direct_kernel(const KeyParams p) {
@@ -735,17 +696,7 @@ page_scores_direct_kernel(const KeyParams p) {
           v = __ldg(reinterpret_cast<const uint4*>(
                         p.q + ((static_cast<size_t>(w.b) * p.L + p.l0 + r / p.G) * p.Hq +
                                w.kvh * p.G + r % p.G) * 128) + cc);
-        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t neg = ((x[k] >> 15) & 0x00010001u) * 0xFFFFu;   // 16 ones per negative
-          hi[k] = x[k] & ~neg;
-          lo[k] = x[k] & neg;
-        }
-        *reinterpret_cast<uint4*>(sQ + r * kDirectPitch + cc * 16) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-        *reinterpret_cast<uint4*>(sQ + r * kDirectPitch + 256 + cc * 16) =
-            make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        stage_query(sQ, r, cc, v);
       }
       __syncthreads();
     }
@@ -755,48 +706,20 @@ page_scores_direct_kernel(const KeyParams p) {
                                           static_cast<size_t>(w.kvh) * p.max_pages;
     float* amax = p.amax + (row * p.max_tiles + w.tile) * kHelpers + warp;
     const int kvh = w.kvh;
-    // the pages' rows: chunk 4j + t of lo (j < 4), then of hi
     uint4 a[8][2];
+    bool live[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const bool ok = id[r] >= 0 && id[r] < p.num_pages;
-      if (!ok && first + r * 8 + g < n && t == 0) atomicOr(p.err, BDLM_DEVERR_PAGE);
-      const uint4* src = reinterpret_cast<const uint4*>(p.bounds) +
-                         (static_cast<size_t>(ok ? id[r] : 0) * p.Hkv + kvh) * 32 + t;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) a[j][r] = ok ? ld_stream16(src + 4 * j) : make_uint4(0, 0, 0, 0);
-      if (!ok) id[r] = -1;
+      live[r] = id[r] >= 0 && id[r] < p.num_pages;
+      if (!live[r] && first + r * 8 + g < n && t == 0) atomicOr(p.err, BDLM_DEVERR_PAGE);
+      load_page(p.bounds, id[r], live[r], p.Hkv, kvh, t, r, a);
     }
-    const bool live[2] = {id[0] >= 0, id[1] >= 0};
     w.next();
     load_ids(id);   // the next tile's ids arrive with this tile's pages
     float d[NT][4];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) d[nt][0] = d[nt][1] = d[nt][2] = d[nt][3] = 0.f;
     uint32_t top = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const uint4 x = a[j][0], y = a[j][1];
-      const uint32_t words[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t mag = words[k] & 0x7FFF7FFFu;
-        const __nv_bfloat162 m = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&top),
-                                             *reinterpret_cast<const __nv_bfloat162*>(&mag));
-        top = *reinterpret_cast<const uint32_t*>(&m);
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const uint4 q = *reinterpret_cast<const uint4*>(sQ + (nt * 8 + g) * kDirectPitch + j * 64 + t * 16);
-        mma_16816(d[nt], x.x, y.x, x.y, y.y, q.x, q.y);
-        mma_16816(d[nt], x.z, y.z, x.w, y.w, q.z, q.w);
-      }
-    }
-    // the largest |bound| of the 16 pages (a NaN counts as infinite)
-    const float m0 = bf16_lo(top), m1 = bf16_hi(top);
-    float m = m0 <= CUDART_INF_F && m1 <= CUDART_INF_F ? fmaxf(m0, m1) : CUDART_INF_F;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    page_products<NT>(a, sQ, g, t, d, top);
+    const float m = warp_magnitude(top);   // of the 16 pages
     if (lane == 0) *amax = m;
     // each group's maximum over its columns, spread over the four lanes of a page
     for (int s = 0; s < groups; ++s) {

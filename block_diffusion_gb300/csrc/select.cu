@@ -17,6 +17,7 @@
 #include <stdint.h>
 
 #include "cache_ops.h"
+#include "page_mma.cuh"
 #include "ptx.cuh"
 
 namespace bdlm {
@@ -174,6 +175,7 @@ __device__ __forceinline__ K kth_largest(int k, K lo, K hi, Each&& each, int* hi
 
 // ------------------------------------------------------------------ page selection
 constexpr int kSelThreads = kRowThreads;
+constexpr int kSelOwnPages = 512;    // pages of lists that the kernel scores itself
 constexpr int kSelFewThreads = 128, kSelFewRows = 64;   // the variant for many short lists
 constexpr int kOwn = 8;              // keys of a thread in registers
 constexpr int kSelKeys = 12288;      // rows held in shared memory (96 KB); longer ones are re-read
@@ -298,7 +300,12 @@ __device__ __forceinline__ unsigned long long exact_score(const SelectParams& p,
 // for, of pages that fit the registers (the same 1024 lists 54 against 70, 2048 lists 54 against 87,
 // 512 lists 38 against 44; with 128 lists of 500-1000 pages it loses, 33 against 29) and of up to 64
 // query rows, which near ties need warps for (512 lists of 256 rows: 105 against 85).
-template <int THREADS, int CTAS>
+//
+// NT > 0: the kernel scores its list's pages itself, for up to 8 NT query rows and kSelOwnPages pages,
+// which saves the scores' launch and their way through memory (8 lists of 125 pages and 8 rows: 8.7 us
+// a call against 11.2; 128 lists of 62-187 pages and 32 rows: 17 against 23; at 500 pages a list it
+// is even).
+template <int THREADS, int CTAS, int NT = 0>
 __global__ void __launch_bounds__(THREADS, CTAS)
 select_pages_kernel(const SelectParams p) {
   extern __shared__ uint32_t sm[];
@@ -311,6 +318,8 @@ select_pages_kernel(const SelectParams p) {
   __shared__ unsigned long long s_pick[1];
   __shared__ int s_cand;
   __shared__ float s_f[32];
+  __shared__ __align__(16) uint8_t sQ[NT > 0 ? NT * 8 * kDirectPitch : 16];
+  __shared__ float s_score[NT > 0 ? kSelOwnPages : 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kWarps = THREADS / 32;
   const int list = blockIdx.x;
@@ -338,26 +347,85 @@ select_pages_kernel(const SelectParams p) {
     for (int c = c0 + THREADS; c < p.sel_cols; c += THREADS) out[c] = -1;   // (tail <= 5)
   };
   if (n <= p.n_select || k == 0) {
-    for (int c = tid; c < k; c += THREADS) out[c] = pt[c];
+    for (int c = tid; c < (NT > 0 ? n : k); c += THREADS) {
+      const int id = pt[c];
+      if (c < k) out[c] = id;
+      if (NT > 0 && (id < 0 || id >= p.num_pages)) atomicOr(p.err, BDLM_DEVERR_PAGE);
+    }
     finish();
     return;
   }
 
   // ---- keys, magnitudes and queries: all asked for before any is used
-  const float* row = p.scores + static_cast<size_t>(list) * p.max_pages;
+  const float* row = NT > 0 ? s_score : p.scores + static_cast<size_t>(list) * p.max_pages;
   float early[kOwn];
+  if constexpr (NT == 0) {
 #pragma unroll
-  for (int x = 0; x < kOwn; ++x)
-    early[x] = tid + x * THREADS < n ? __ldcg(row + tid + x * THREADS) : 0.f;
+    for (int x = 0; x < kOwn; ++x)
+      early[x] = tid + x * THREADS < n ? __ldcg(row + tid + x * THREADS) : 0.f;
+  }
   if (n <= kSelKeys)   // the page ids go to shared memory meanwhile
     for (int i = tid; i < n; i += THREADS)
       asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(sm + i)), "l"(pt + i)
                    : "memory");
   float q1 = 0.f, am = 0.f;   // the group's largest |q|_1, the list's largest |bound|
-  {
+  if constexpr (NT == 0) {
     const int values = (n + kKeyTile - 1) / kKeyTile * kAmaxPerTile;
     const float* a = p.amax + (static_cast<size_t>(b) * p.Hkv + kvh) * p.max_tiles * kAmaxPerTile;
     for (int i = tid; i < values; i += THREADS) am = fmaxf(am, __ldcg(a + i));
+  } else {
+    // each warp scores 16 pages at a time; its first pages' bounds and the queries are asked for
+    // together
+    const int g = lane >> 2, t = lane & 3, rows = p.group * p.G;
+    bool live[2];
+    uint4 a[8][2];
+    auto load = [&](int first) {   // pages g and g + 8
+      int id[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int page = first + r * 8 + g;
+        id[r] = page < n ? __ldg(pt + page) : -1;
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        live[r] = id[r] >= 0 && id[r] < p.num_pages;
+        if (!live[r] && first + r * 8 + g < n && t == 0) atomicOr(p.err, BDLM_DEVERR_PAGE);
+        load_page(p.bounds, id[r], live[r], p.Hkv, kvh, t, r, a);
+      }
+    };
+    load(warp * 16);
+    for (int c = tid; c < NT * 8 * 16; c += THREADS) {
+      const int r = c >> 4, cc = c & 15;
+      stage_query(sQ, r, cc, r < rows ? __ldg(group_query(p, b, s, kvh, r) + cc) : make_uint4(0, 0, 0, 0));
+    }
+    __syncthreads();
+    uint32_t top = 0;
+    for (int first = warp * 16; first < n;) {
+      float d[NT][4], best[2] = {-CUDART_INF_F, -CUDART_INF_F};
+      page_products<NT>(a, sQ, g, t, d, top);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+          if (nt * 8 + 2 * t + x < rows) {
+            best[0] = fmaxf(best[0], d[nt][x]);
+            best[1] = fmaxf(best[1], d[nt][2 + x]);
+          }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 1));
+        best[r] = fmaxf(best[r], __shfl_xor_sync(0xffffffffu, best[r], 2));
+        const int page = first + r * 8 + g;
+        if (t == 0 && page < n) s_score[page] = live[r] ? best[r] : -CUDART_INF_F;
+      }
+      first += kWarps * 16;
+      if (first < n) load(first);
+    }
+    am = warp_magnitude(top);
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < kOwn; ++x)
+      early[x] = tid + x * THREADS < n ? s_score[tid + x * THREADS] : 0.f;
   }
   for (int r = tid >> 1; r < p.group * p.G; r += THREADS / 2) {   // a row for two threads
     const uint4* src = group_query(p, b, s, kvh, r) + (tid & 1) * 8;
@@ -921,6 +989,10 @@ cudaError_t allow_smem(std::atomic<unsigned long long>& done, F* kernel, size_t 
 
 }  // namespace
 
+bool select_scores_itself(int lists, int max_pages, int rows, int num_sms) {
+  return lists <= num_sms && max_pages <= kSelOwnPages && rows <= 32;
+}
+
 cudaError_t launch_select_pages(const SelectParams& p, int num_sms, cudaStream_t stream) {
   const size_t words = (static_cast<size_t>(p.max_pages) + 31) / 32;
   const unsigned lists = static_cast<unsigned>(p.B) * p.groups * p.Hkv;
@@ -928,6 +1000,12 @@ cudaError_t launch_select_pages(const SelectParams& p, int num_sms, cudaStream_t
       p.group * p.G <= kSelFewRows)
     return launch_pdl(select_pages_kernel<kSelFewThreads, 6>, dim3(lists), dim3(kSelFewThreads),
                       (p.max_pages + 2 * words) * 4, stream, p);
+  const int rows = p.group * p.G;
+  if (select_scores_itself(static_cast<int>(lists), p.max_pages, rows, num_sms))
+    return launch_pdl(rows <= 8    ? select_pages_kernel<kSelThreads, 1, 1>
+                      : rows <= 16 ? select_pages_kernel<kSelThreads, 1, 2>
+                                   : select_pages_kernel<kSelThreads, 1, 4>,
+                      dim3(lists), dim3(kSelThreads), (p.max_pages + 2 * words) * 4, stream, p);
   // page ids and keys (of rows that fit), then two bitmaps of the row's pages
   const size_t keys = 2 * static_cast<size_t>(p.max_pages <= kSelKeys ? p.max_pages : kSelKeys);
   constexpr size_t kMost = (2 * kSelKeys + 2 * (kSelectMaxPages / 32)) * 4;

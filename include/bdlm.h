@@ -408,8 +408,9 @@ int bdlm_page_bounds(const bdlm_attn_desc* desc, const bdlm_bf16* k_pages,
  *   sel_lens   [B, L/group] int32: tokens listed before the last `group` ones, the prefix length
  *              bdlm_sparse_attention takes (n*16 + prefix_len%16 + L - group; -1 for a bad length)
  * group * Hq / Hkv <= 256, max_pages_per_seq <= 262144 and num_pages * Hkv < 2^30, else
- * BDLM_ERR_UNSUPPORTED.  A page with a bad id is only listed when the others do not suffice.  Scratch (12 bytes per list and page of
- * the table) comes from the library workspace.  Other arguments as bdlm_block_attention.
+ * BDLM_ERR_UNSUPPORTED.  A page with a bad id is only listed when the others do not suffice.
+ * Scratch (at most 12 bytes per list and page of the table) comes from the library workspace.
+ * Other arguments as bdlm_block_attention.
  */
 int bdlm_select_pages(const bdlm_attn_desc* desc, const bdlm_bf16* q, const bdlm_bf16* bounds,
                       const int32_t* page_table, const int32_t* prefix_lens, int group,

@@ -238,7 +238,7 @@ def test_an_explicit_stream_and_the_current_one_agree(lib):
 
 def test_a_capture_that_would_need_memory_is_refused_and_stays_valid(lib):
     import torch
-    x = Step(lib, 6, **SHAPES[0])
+    x = Step(lib, 6, **SHAPES[1])
     x()
     want = x.results()
     x.clear()

@@ -178,6 +178,20 @@ def test_selection_flags_bad_pages_and_lengths(lib):
     p.check(lib, 4, 30)
 
 
+@pytest.mark.parametrize("lens", [[200, 640], [200, 9000]])
+@pytest.mark.parametrize("n", [0, 40, 600])
+def test_a_bad_page_is_flagged_whether_or_not_it_is_scored(lib, lens, n):
+    """Short lists, which are scored and chosen from in one kernel, and longer ones."""
+    rng = np.random.default_rng(11)
+    p = Pages(rng, lens, 4, 8, 2)
+    t = p.table.copy()
+    t[0, 5] = p.num
+    sel, _ = p.run(lib, 4, n, table=t)
+    assert lib.bdlm_device_error() == lib.BDLM_DEVERR_PAGE
+    assert np.array_equal(sel[0, 0, :, :min(n, 12)], np.tile(t[0, :min(n, 12)], (2, 1)))
+    p.check(lib, 4, n)
+
+
 @pytest.mark.parametrize("L,group,Hq,Hkv,n", [(1, 1, 16, 8, 8), (4, 4, 32, 8, 16), (4, 1, 32, 8, 16),
                                              (6, 3, 24, 8, 5), (64, 64, 32, 8, 12), (32, 8, 32, 8, 64),
                                              (16, 16, 16, 1, 30), (2, 1, 4, 4, 300)])
