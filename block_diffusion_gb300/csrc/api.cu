@@ -661,16 +661,6 @@ int encode_key_q(CUtensorMap* tm, const bdlm_bf16* q, const bdlm_attn_desc& d, i
   return encode(tm, q, 3, dims, strides, box);
 }
 
-int compact_impl(DeviceState* st, const bdlm_attn_desc& d, bdlm_bf16* k_pages, bdlm_bf16* v_pages,
-                 const int32_t* page_table, const int32_t* base_lens, const int32_t* idx,
-                 int heads, int n_max, const int32_t* counts, const int32_t* to_table,
-                 bdlm_stream stream) {
-  const bdlm::CompactParams p{k_pages, v_pages, page_table, to_table, base_lens, idx, counts,
-                              d.B, d.Hkv, heads, d.max_pages_per_seq, d.num_pages, n_max, st->err};
-  return bdlm::launch_compact(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? BDLM_OK
-                                                                                  : BDLM_ERR_CUDA;
-}
-
 }  // namespace
 
 extern "C" {
@@ -885,10 +875,11 @@ int bdlm_evict_kv(const bdlm_attn_desc* desc, bdlm_bf16* k_pages, bdlm_bf16* v_p
   if (rc) return rc;
   const bdlm::EvictParams p{lens, weights, to_weights, kept, new_lens, d.B, d.Hkv,
                             d.max_pages_per_seq, keep, recent, st->err};
-  if (bdlm::launch_evict_select(p, static_cast<cudaStream_t>(stream)) != cudaSuccess)
-    return BDLM_ERR_CUDA;
-  return compact_impl(st, d, k_pages, v_pages, page_table, nullptr, kept, d.Hkv, keep, new_lens,
-                      to_table, stream);
+  const bdlm::CompactParams m{k_pages, v_pages, page_table, to_table, nullptr, kept, new_lens,
+                              d.B, d.Hkv, d.Hkv, d.max_pages_per_seq, d.num_pages, keep, st->err};
+  return bdlm::launch_evict(p, m, st->num_sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? BDLM_OK
+             : BDLM_ERR_CUDA;
 }
 
 int bdlm_compact_kv(const bdlm_attn_desc* desc, bdlm_bf16* k_pages, bdlm_bf16* v_pages,
@@ -907,8 +898,10 @@ int bdlm_compact_kv(const bdlm_attn_desc* desc, bdlm_bf16* k_pages, bdlm_bf16* v
   DeviceState* st = nullptr;
   int rc = current_device(&st);
   if (rc) return rc;
-  return compact_impl(st, d, k_pages, v_pages, page_table, base_lens, idx, heads, n_max, counts,
-                      to_table, stream);
+  const bdlm::CompactParams p{k_pages, v_pages, page_table, to_table, base_lens, idx, counts,
+                              d.B, d.Hkv, heads, d.max_pages_per_seq, d.num_pages, n_max, st->err};
+  return bdlm::launch_compact(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? BDLM_OK
+                                                                                  : BDLM_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -92,8 +92,6 @@ struct EvictParams {
   int B, Hkv, max_pages, keep, recent;
   int* err;
 };
-cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t stream);
-
 struct CompactParams {
   uint16_t* k_pages;
   uint16_t* v_pages;
@@ -106,5 +104,8 @@ struct CompactParams {
   int* err;
 };
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream);
+// The choice and the move of what it keeps (m: base null, idx kept, counts new_lens, n_max keep).
+cudaError_t launch_evict(const EvictParams& p, const CompactParams& m, int num_sms,
+                         cudaStream_t stream);
 
 }  // namespace bdlm

@@ -697,6 +697,7 @@ select_pages_kernel(const SelectParams p) {
 // ------------------------------------------------------------------ eviction
 constexpr int kEvictThreads = kRowThreads;
 constexpr int kEvictWarps = kEvictThreads / 32;
+constexpr int kEvictMoveKeep = 512;   // tokens that a list's own CTA moves to other pages
 constexpr int kEvictKeys = 22528;   // 88 KB of keys: two CTAs per SM; longer rows are re-read (L2)
 
 // One CTA per (sequence, KV head): the k = keep - recent largest weights before the last `recent`
@@ -706,9 +707,8 @@ constexpr int kEvictKeys = 22528;   // 88 KB of keys: two CTAs per SM; longer ro
 // round of positions at a time, all reads before the round's barrier and all writes after it: a
 // token never moves to a later position, so no round reads what an earlier one wrote.
 // Bound by the latency of its passes over a few ten thousand keys in shared memory.
-__global__ void __launch_bounds__(kEvictThreads, 2)
-evict_select_kernel(const EvictParams p) {
-  extern __shared__ uint32_t sm[];
+// Returns how many tokens the list keeps.
+__device__ __forceinline__ int choose_tokens(const EvictParams& p, uint32_t* sm) {
   __shared__ __align__(16) int hist[4 * kEvictThreads];
   __shared__ int s_scan[36];
   __shared__ uint32_t s_range[64];
@@ -716,8 +716,6 @@ evict_select_kernel(const EvictParams p) {
   __shared__ int s_gt[kEvictWarps], s_eq[kEvictWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / p.Hkv, kvh = blockIdx.x - b * p.Hkv;
-  griddep_wait();
-  griddep_launch_dependents();
   const int n = p.lens[b];
   const size_t stride = static_cast<size_t>(p.max_pages) * kTok;
   int32_t* kept = p.kept + static_cast<size_t>(blockIdx.x) * p.keep;
@@ -727,7 +725,7 @@ evict_select_kernel(const EvictParams p) {
     if (bad) atomicOr(p.err, BDLM_DEVERR_LENGTH);
   }
   for (int i = (bad ? 0 : min(n, p.keep)) + tid; i < p.keep; i += kEvictThreads) kept[i] = -1;
-  if (bad) return;
+  if (bad) return 0;
   const float* w = p.weights + blockIdx.x * stride;
   float* to = p.to_weights + blockIdx.x * stride;
   const bool in_place = to == w;
@@ -736,7 +734,7 @@ evict_select_kernel(const EvictParams p) {
       kept[i] = i;
       if (!in_place) to[i] = w[i];
     }
-    return;
+    return n;
   }
   const int cand = n - p.recent, k = p.keep - p.recent;   // k < cand
   const bool held = cand <= kEvictKeys;
@@ -836,7 +834,7 @@ evict_select_kernel(const EvictParams p) {
       }
     }
   }
-  if (!in_place) return;
+  if (!in_place) return p.keep;
   __syncthreads();
   constexpr int kRound = 4;
   for (int j0 = 0; j0 < p.keep; j0 += kRound * kEvictThreads) {
@@ -853,6 +851,7 @@ evict_select_kernel(const EvictParams p) {
       if (j < p.keep) to[j] = v[x];
     }
   }
+  return p.keep;
 }
 
 // ------------------------------------------------------------------ moving tokens
@@ -882,23 +881,15 @@ __device__ __forceinline__ long long token_row(const CompactParams& p, const int
   return (static_cast<long long>(id) * kTok + tok % kTok) * p.Hkv + kvh;
 }
 
-__global__ void __launch_bounds__(kMoveWarps * 32)
-move_tokens_kernel(const CompactParams p, int runs) {
-  griddep_wait();
-  griddep_launch_dependents();
+// Tokens t0 .. t1 - 1 of the 32 tokens `run` of the first `count` (a warp).
+__device__ __forceinline__ void move_run(const CompactParams& p, int b, int kvh, int run, int count,
+                                         int t0, int t1) {
   const int lane = threadIdx.x & 31;
-  const long long unit = static_cast<long long>(blockIdx.x) * kMoveWarps + (threadIdx.x >> 5);
-  if (unit >= static_cast<long long>(p.B) * p.Hkv * runs) return;
-  const int run = static_cast<int>(unit % runs);
-  const int bh = static_cast<int>(unit / runs);
-  const int b = bh / p.Hkv, kvh = bh - b * p.Hkv;
-  const int count = min(p.counts[b], p.n_max);
   const int j = run * 32 + lane;
-  if (run * 32 >= count) return;
   const int base = p.base ? p.base[b] : 0;
   long long from = -1, to = -1;   // this lane's token
   if (j < count && base >= 0) {
-    const int i = __ldg(p.idx + (static_cast<size_t>(b) * p.heads + (p.heads > 1 ? kvh : 0)) * p.n_max + j);
+    const int i = __ldcg(p.idx + (static_cast<size_t>(b) * p.heads + (p.heads > 1 ? kvh : 0)) * p.n_max + j);
     if (i < 0) {
       atomicOr(p.err, BDLM_DEVERR_ROW);
     } else {
@@ -911,7 +902,7 @@ move_tokens_kernel(const CompactParams p, int runs) {
   }
   uint4* pool = reinterpret_cast<uint4*>(lane < 16 ? p.k_pages : p.v_pages) + (lane & 15);
   constexpr int kBatch = 8;
-  for (int t0 = 0; t0 < 32; t0 += kBatch) {
+  for (; t0 < t1; t0 += kBatch) {
     uint4 v[kBatch];
     long long dst[kBatch];
 #pragma unroll
@@ -927,16 +918,21 @@ move_tokens_kernel(const CompactParams p, int runs) {
 }
 
 __global__ void __launch_bounds__(kMoveWarps * 32)
-move_in_place_kernel(const CompactParams p) {
+move_tokens_kernel(const CompactParams p, int runs) {
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31;
   const long long unit = static_cast<long long>(blockIdx.x) * kMoveWarps + (threadIdx.x >> 5);
-  if (unit >= static_cast<long long>(p.B) * p.Hkv * 8) return;
-  const int slice = static_cast<int>(unit & 3), is_v = static_cast<int>(unit >> 2) & 1;
-  const int bh = static_cast<int>(unit >> 3);
-  const int b = bh / p.Hkv, kvh = bh - b * p.Hkv;
-  const int count = min(p.counts[b], p.n_max);
+  if (unit >= static_cast<long long>(p.B) * p.Hkv * runs) return;
+  const int run = static_cast<int>(unit % runs);
+  const int bh = static_cast<int>(unit / runs);
+  const int b = bh / p.Hkv, count = min(p.counts[b], p.n_max);
+  if (run * 32 < count) move_run(p, b, bh - b * p.Hkv, run, count, 0, 32);
+}
+
+// Slice 0 .. 7 (four of K, four of V) of the first `count` tokens (a warp).
+__device__ __forceinline__ void move_slice(const CompactParams& p, int b, int kvh, int unit, int count) {
+  const int lane = threadIdx.x & 31;
+  const int slice = unit & 3, is_v = unit >> 2;
   const int base = p.base ? p.base[b] : 0;
   if (base < 0) {
     if (lane == 0) atomicOr(p.err, BDLM_DEVERR_LENGTH);
@@ -951,7 +947,7 @@ move_in_place_kernel(const CompactParams p) {
       const int j = j0 + h * 32 + lane;
       from[h] = to[h] = -1;
       if (j >= count) continue;
-      const int i = __ldg(idx + j);
+      const int i = __ldcg(idx + j);
       if (i == j) continue;   // stays where it is
       if (i < 0) {
         atomicOr(p.err, BDLM_DEVERR_ROW);
@@ -976,6 +972,39 @@ move_in_place_kernel(const CompactParams p) {
     for (int x = 0; x < 8; ++x)
       if (dst[x] >= 0) pool[dst[x] * 16] = v[x];
     __syncwarp();
+  }
+}
+
+__global__ void __launch_bounds__(kMoveWarps * 32)
+move_in_place_kernel(const CompactParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const long long unit = static_cast<long long>(blockIdx.x) * kMoveWarps + (threadIdx.x >> 5);
+  if (unit >= static_cast<long long>(p.B) * p.Hkv * 8) return;
+  const int bh = static_cast<int>(unit >> 3), b = bh / p.Hkv;
+  move_slice(p, b, bh - b * p.Hkv, static_cast<int>(unit & 7), min(p.counts[b], p.n_max));
+}
+
+// The choice; with MOVE, the list's tokens move in the same kernel (for few short lists, whose own
+// SMs are enough).
+template <bool MOVE>
+__global__ void __launch_bounds__(kEvictThreads, MOVE ? 1 : 2)
+evict_kernel(const EvictParams p, const CompactParams m) {
+  extern __shared__ uint32_t sm[];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int count = choose_tokens(p, sm);
+  if constexpr (MOVE) {
+    __syncthreads();   // the kept positions are written
+    const int warp = threadIdx.x >> 5, b = blockIdx.x / p.Hkv, kvh = blockIdx.x - b * p.Hkv;
+    if (m.to_table != m.page_table) {
+      for (int u = warp; u * 16 < count; u += kEvictWarps) {   // half a run
+        const int t0 = (u & 1) * 16;
+        move_run(m, b, kvh, u >> 1, count, t0, t0 + 16);
+      }
+    } else if (warp < 8) {
+      move_slice(m, b, kvh, warp, count);
+    }
   }
 }
 
@@ -1017,16 +1046,6 @@ cudaError_t launch_select_pages(const SelectParams& p, int num_sms, cudaStream_t
   return launch_pdl(kernel, dim3(lists), dim3(kSelThreads), (keys + 2 * words) * 4, stream, p);
 }
 
-cudaError_t launch_evict_select(const EvictParams& p, cudaStream_t stream) {
-  const long long tokens = static_cast<long long>(p.max_pages) * kTok;
-  const size_t keys = tokens <= kEvictKeys ? tokens : kEvictKeys;
-  static std::atomic<unsigned long long> attr_done{0};
-  cudaError_t e = allow_smem(attr_done, evict_select_kernel, kEvictKeys * 4);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(evict_select_kernel, dim3(static_cast<unsigned>(p.B) * p.Hkv),
-                    dim3(kEvictThreads), keys * 4, stream, p);
-}
-
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream) {
   if (p.to_table == p.page_table) {
     const long long units = static_cast<long long>(p.B) * p.Hkv * 8;
@@ -1039,6 +1058,21 @@ cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream) {
   return launch_pdl(move_tokens_kernel,
                     dim3(static_cast<unsigned>((units + kMoveWarps - 1) / kMoveWarps)),
                     dim3(kMoveWarps * 32), 0, stream, p, runs);
+}
+
+cudaError_t launch_evict(const EvictParams& p, const CompactParams& m, int num_sms,
+                         cudaStream_t stream) {
+  const long long tokens = static_cast<long long>(p.max_pages) * kTok;
+  const size_t keys = tokens <= kEvictKeys ? tokens : kEvictKeys;
+  const long long lists = static_cast<long long>(p.B) * p.Hkv;
+  const bool in_place = m.to_table == m.page_table;
+  const bool move = lists <= num_sms && (in_place || p.keep <= kEvictMoveKeep);
+  static std::atomic<unsigned long long> one_done{0}, two_done{0};
+  auto* kernel = move ? evict_kernel<true> : evict_kernel<false>;
+  cudaError_t e = allow_smem(move ? one_done : two_done, kernel, kEvictKeys * 4);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(kernel, dim3(static_cast<unsigned>(lists)), dim3(kEvictThreads), keys * 4, stream, p, m);
+  return e != cudaSuccess || move ? e : launch_compact(m, stream);
 }
 
 }  // namespace bdlm
