@@ -60,20 +60,20 @@ struct Cfg {
   static constexpr int kQBytes = kRowsMax * (PAGES ? 512 : 256);
   static constexpr int kCtas = WIDE ? 1 : 2;   // per SM
   static_assert(WIDE || !PAGES, "page scores of few rows take the direct kernel below");
-  static constexpr int kStages = 3;
   // Weights of more than 32 rows: two sets share a tile, half of its columns each.  (The MMA stays
   // one of N = all rows: in halves of 128 it reads A twice, 128 bytes of shared memory a clock, and
   // the MMAs alone then took 99 us of what are 78 us of copies.)
   static constexpr bool kSplit = WIDE && !PAGES;
+  static constexpr int kStages = 3;            // (weights of more than 32 rows: four were no faster)
   static constexpr int kDBufs = WIDE ? 2 : 4;                  // X tiles in tensor memory
   static constexpr int kSets = kSplit ? 4 : 2;                 // reducing sets of four warps
   static constexpr int kTmemCols = WIDE ? 512 : 128;
   static constexpr int kThreads = 128 + kSets * 128 + (PAGES ? (kHelpers + 2) * 32 : 0);
   // Weights of more than 32 rows: -lse / scale enters X through the MMA, as three bf16 numbers a row
   // (24 bits) against keys of 1, so that the reduction reads no table from shared memory beside
-  // the MMAs (95 us a pass against 100, 16 x 64 x 4 rows over 8192-16384 tokens): 128-byte rows of
-  // which a K step of 16 is used, one of 1s for the keys.
-  static constexpr int kLseBytes = kSplit ? kRowsMax * 128 : 0, kOneBytes = kSplit ? kKeys * 128 : 0;
+  // the MMAs (95 us a pass against 100, 16 x 64 x 4 rows over 8192-16384 tokens): one K step of 32
+  // bytes a row, without swizzle, and one of 1s for the keys.
+  static constexpr int kLseBytes = kSplit ? kRowsMax * 32 : 0, kOneBytes = kSplit ? kKeys * 32 : 0;
   static constexpr size_t kSmem =
       1024 + static_cast<size_t>(kQBytes) + kLseBytes + kOneBytes + kStages * kStage;
 };
@@ -87,6 +87,13 @@ __device__ __forceinline__ void tma_gather4(void* dst, const CUtensorMap* map, u
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
       "r"(smem_u32(bar))
       : "memory");
+}
+
+// One K step (16 bf16 a row) without swizzle: core matrices of 8 rows x 16 bytes, two along K, then the
+// next 8 rows.
+__device__ __forceinline__ uint32_t step_chunk(int r, int c) { return (r >> 3) * 256 + c * 128 + (r & 7) * 16; }
+__device__ __forceinline__ uint64_t step_desc(uint32_t saddr) {
+  return smem_desc(saddr, 128, 256) & ~(static_cast<uint64_t>(7) << 61);
 }
 
 __device__ __forceinline__ void sts16(uint32_t addr, const uint32_t (&v)[4]) {
@@ -257,7 +264,7 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       for (int c = threadIdx.x; c < (C::kRowsMax + kKeys) * 2; c += C::kThreads) {
         const int r = c >> 1;
         const bool ones = r >= C::kRowsMax && (c & 1) == 0;
-        *reinterpret_cast<uint4*>(sL + r * 128 + (((c & 1) ^ (r & 7)) << 4)) =
+        *reinterpret_cast<uint4*>(sL + step_chunk(r, c & 1)) =
             ones ? make_uint4(0x3F803F80u, 0x3F80u, 0, 0) : make_uint4(0, 0, 0, 0);
       }
     }
@@ -341,7 +348,7 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
           const float c1 = fabsf(__bfloat162float(hi)) < CUDART_INF_F ? c - __bfloat162float(hi) : 0.f;
           const __nv_bfloat16 mid = __float2bfloat16_rn(c1);
           const __nv_bfloat16 lo = __float2bfloat16_rn(c1 - __bfloat162float(mid));
-          *reinterpret_cast<uint2*>(sL + n * 128 + ((n & 7) << 4)) =
+          *reinterpret_cast<uint2*>(sL + step_chunk(n, 0)) =
               make_uint2(__bfloat16_as_ushort(hi) | static_cast<uint32_t>(__bfloat16_as_ushort(mid)) << 16,
                          __bfloat16_as_ushort(lo));
         }
@@ -490,7 +497,7 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
         }
         if (!ok) break;
         if constexpr (C::kSplit)   // - lse / scale last: the sum is small then, and rounded once
-          umma_bf16(d, smem_desc(smem_u32(sOne), 16, 1024), smem_desc(smem_u32(sL), 16, 1024), idesc, 1u);
+          umma_bf16(d, step_desc(smem_u32(sOne)), step_desc(smem_u32(sL)), idesc, 1u);
         umma_commit(&bar_dfull[db]);
         w.next();
         if (w.left == 0 || w.fresh) umma_commit(&bar_qempty[q % nq]);
