@@ -34,6 +34,10 @@ __device__ __forceinline__ uint32_t order_key(float f) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+__device__ __forceinline__ float key_value(uint32_t key) {   // of order_key (not NaN)
+  return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
+}
+
 struct BlockSum {   // sums and scans over the CTA; s: one word per warp
   int* s;
   __device__ __forceinline__ int exclusive(int v, int* total) {
@@ -190,10 +194,6 @@ __device__ __forceinline__ const uint4* group_query(const SelectParams& p, int b
          ((static_cast<size_t>(b) * p.L + s * p.group + i) * p.Hq + kvh * p.G + (n - i * p.G)) * 16;
 }
 
-__device__ __forceinline__ float key_value(uint32_t key) {   // of order_key (not NaN)
-  return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
-}
-
 constexpr int kExactRows = 16;   // query rows of a warp's turn
 
 // Scores of one page for query rows row0 .. rows - 1 (at most 16) of one group, in float32 with 11
@@ -308,7 +308,7 @@ __device__ __forceinline__ unsigned long long exact_score(const SelectParams& p,
 template <int THREADS, int CTAS, int NT = 0>
 __global__ void __launch_bounds__(THREADS, CTAS)
 select_pages_kernel(const SelectParams p) {
-  extern __shared__ uint32_t sm[];
+  extern __shared__ __align__(16) uint32_t sm[];
   __shared__ __align__(16) int hist[4 * THREADS];
   __shared__ unsigned long long s_exact[kSelExact];
   __shared__ uint32_t s_fast[kSelExact];
@@ -740,30 +740,61 @@ __device__ __forceinline__ int choose_tokens(const EvictParams& p, uint32_t* sm)
   const bool held = cand <= kEvictKeys;
   uint32_t T = 0;
   int above = 0;
-  auto key_at = [&](int i) { return held ? sm[i] : order_key(__ldcg(w + i)); };
+  // Four weights, i a multiple of 4: rows are multiples of 16 tokens, so past `cand` they are the row's.
+  const bool wide = (reinterpret_cast<uintptr_t>(w) & 15) == 0;
+  auto load4 = [&](int i) {
+    return wide ? __ldcg(reinterpret_cast<const float4*>(w + i))
+                : make_float4(__ldcg(w + i), __ldcg(w + i + 1), __ldcg(w + i + 2), __ldcg(w + i + 3));
+  };
+  // f(keys of i .. i + 3, how many of them are before `end`)
+  auto four = [&](int i, int end, auto&& f) {
+    uint32_t key[4];
+    if (held) {
+      const uint4 v = *reinterpret_cast<const uint4*>(sm + i);
+      key[0] = v.x, key[1] = v.y, key[2] = v.z, key[3] = v.w;
+    } else {
+      const float4 v = load4(i);
+      key[0] = order_key(v.x), key[1] = order_key(v.y), key[2] = order_key(v.z), key[3] = order_key(v.w);
+    }
+    f(key, end - i);
+  };
   if (k > 0) {
     uint32_t lo = 0xFFFFFFFFu, hi = 0;
-    constexpr int kBatch = 8;   // loads in flight per thread
-    for (int i0 = tid; i0 < cand; i0 += kBatch * kEvictThreads) {
-      float f[kBatch];
-#pragma unroll
-      for (int x = 0; x < kBatch; ++x)
-        if (i0 + x * kEvictThreads < cand) f[x] = __ldcg(w + i0 + x * kEvictThreads);
+    constexpr int kBatch = 4;   // loads in flight per thread, of 16 bytes where the row is aligned
+    for (int i0 = tid * 4; i0 < cand; i0 += kBatch * 4 * kEvictThreads) {
+      float4 f[kBatch];
 #pragma unroll
       for (int x = 0; x < kBatch; ++x) {
-        if (i0 + x * kEvictThreads >= cand) break;
-        const uint32_t key = order_key(f[x]);
-        if (held) sm[i0 + x * kEvictThreads] = key;
-        lo = min(lo, key);
-        hi = max(hi, key);
+        const int i = i0 + x * 4 * kEvictThreads;
+        if (i >= cand) break;
+        f[x] = load4(i);
+      }
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) {
+        const int i = i0 + x * 4 * kEvictThreads;
+        if (i >= cand) break;
+        const uint32_t key[4] = {order_key(f[x].x), order_key(f[x].y), order_key(f[x].z),
+                                 order_key(f[x].w)};
+        if (held) *reinterpret_cast<uint4*>(sm + i) = make_uint4(key[0], key[1], key[2], key[3]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (i + c < cand) {
+            lo = min(lo, key[c]);
+            hi = max(hi, key[c]);
+          }
       }
     }
     block_range(lo, hi, s_range);
     T = kth_largest<kEvictThreads, uint32_t>(
         k, lo, hi,
         [&](auto&& f) {
-#pragma unroll 4
-          for (int i = tid; i < cand; i += kEvictThreads) f(key_at(i));
+#pragma unroll 2
+          for (int i = tid * 4; i < cand; i += 4 * kEvictThreads)
+            four(i, cand, [&](const uint32_t (&key)[4], int left) {
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                if (c < left) f(key[c]);
+            });
         },
         hist, s_scan, s_pick, &above);
   }
@@ -776,15 +807,18 @@ __device__ __forceinline__ int choose_tokens(const EvictParams& p, uint32_t* sm)
   }
   if (k > 0) {
     // this warp's stretch: what it keeps for sure (g) and what equals T (e)
-    const int stretch = ((cand + kEvictWarps - 1) / kEvictWarps + 31) & ~31;
+    const int stretch = ((cand + kEvictWarps - 1) / kEvictWarps + 127) & ~127;
     const int s0 = warp * stretch, s1 = min(cand, s0 + stretch);
     int g = 0, e = 0;
-#pragma unroll 4
-    for (int i = s0 + lane; i < s1; i += 32) {
-      const uint32_t key = key_at(i);
-      g += key > T;
-      e += key == T;
-    }
+#pragma unroll 2
+    for (int i = s0 + lane * 4; i < s1; i += 128)
+      four(i, s1, [&](const uint32_t (&key)[4], int left) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          g += c < left && key[c] > T;
+          e += c < left && key[c] == T;
+        }
+      });
     g = __reduce_add_sync(0xffffffffu, g);
     e = __reduce_add_sync(0xffffffffu, e);
     if (lane == 0) {
@@ -805,32 +839,45 @@ __device__ __forceinline__ int choose_tokens(const EvictParams& p, uint32_t* sm)
     const bool whole = all == ties;
     int at = g + (whole ? e : min(e, ties));
     const uint32_t below = (1u << lane) - 1u;
-    constexpr int kWalk = 8;   // rounds whose weights are loaded together
-    for (int i0 = s0 + lane; i0 - lane < s1; i0 += 32 * kWalk) {
-      float v[kWalk];
-      if (!in_place) {
+#pragma unroll 2
+    for (int i0 = s0; i0 < s1; i0 += 128) {
+      const int i = i0 + lane * 4;
+      uint32_t key[4] = {0, 0, 0, 0}, in = 0;   // `in`: a bit per key
+      if (i < s1)
+        four(i, s1, [&](const uint32_t (&v)[4], int left) {
 #pragma unroll
-        for (int x = 0; x < kWalk; ++x) v[x] = i0 + 32 * x < s1 ? __ldcg(w + i0 + 32 * x) : 0.f;
-      }
+          for (int c = 0; c < 4; ++c) {
+            key[c] = v[c];
+            in |= (c < left && v[c] >= T) << c;
+          }
+        });
+      if (!whole) {   // of those equal to T the first `ties` of the row
+        int rank = e;
 #pragma unroll
-      for (int x = 0; x < kWalk; ++x) {
-        const int i = i0 + 32 * x;
-        if (i - lane >= s1) break;
-        const uint32_t key = i < s1 ? key_at(i) : 0;
-        bool in = i < s1 && key >= T;
-        if (!whole) {
-          const bool eq = in && key == T;
-          const uint32_t be = __ballot_sync(0xffffffffu, eq);
-          if (eq) in = e + __popc(be & below) < ties;
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t be = __ballot_sync(0xffffffffu, (in >> c & 1) && key[c] == T);
+          rank += __popc(be & below);
           e += __popc(be);
         }
-        const uint32_t bits = __ballot_sync(0xffffffffu, in);
-        if (in) {
-          const int j = at + __popc(bits & below);
-          kept[j] = i;
-          if (!in_place) to[j] = v[x];
-        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if ((in >> c & 1) && key[c] == T && rank++ >= ties) in &= ~(1u << c);
+      }
+      int j = at;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t bits = __ballot_sync(0xffffffffu, in >> c & 1);
+        j += __popc(bits & below);
         at += __popc(bits);
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (!(in >> c & 1)) continue;
+        kept[j] = i + c;
+        // (a zero's sign and a NaN's bits are not in the key)
+        if (!in_place)
+          to[j] = key[c] == 0 || key[c] == 0x80000000u ? __ldcg(w + i + c) : key_value(key[c]);
+        ++j;
       }
     }
   }
@@ -990,7 +1037,7 @@ move_in_place_kernel(const CompactParams p) {
 template <bool MOVE>
 __global__ void __launch_bounds__(kEvictThreads, MOVE ? 1 : 2)
 evict_kernel(const EvictParams p, const CompactParams m) {
-  extern __shared__ uint32_t sm[];
+  extern __shared__ __align__(16) uint32_t sm[];
   griddep_wait();
   griddep_launch_dependents();
   const int count = choose_tokens(p, sm);

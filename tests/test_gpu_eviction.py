@@ -186,6 +186,36 @@ def test_eviction(lib, lens, keep, recent, kind, in_place):
     assert np.array_equal(gk, k2) and np.array_equal(gv, v2)
 
 
+@pytest.mark.parametrize("lens,keep", [([700, 90], 64), ([26000], 900)])
+def test_eviction_of_weights_at_odd_addresses(lib, lens, keep):
+    """Weights that start 4 bytes past 16, with zeros of both signs and NaN, keep their bits."""
+    import torch
+    rng = np.random.default_rng(keep)
+    k, v, table, _ = cache(rng, lens, 2, max(lens), 0)
+    B, stride = len(lens), table.shape[1] * 16
+    w = rng.random((B, 2, stride)).astype(np.float32) * (rng.random((B, 2, stride)) < 0.05)
+    w[:, :, ::7] *= -0.0
+    w[:, 0, 3:9] = np.nan
+    w[:, 0, 5:60].view(np.uint32)[...] |= np.uint32(1)
+    flat = torch.zeros(w.size + 1, device="cuda")
+    flat[1:] = dev(w).view(-1)
+    wd = flat[1:].view(B, 2, stride)
+    assert wd.data_ptr() % 16 == 4
+    d = lib.attn_desc(B, 1, 2, 2, 128, table.shape[1], k.shape[0])
+    kept = torch.empty((B, 2, keep), dtype=torch.int32, device="cuda")
+    new = torch.empty((B,), dtype=torch.int32, device="cuda")
+    tw, td = torch.full_like(wd, -3.0), dev(table)
+    lib.bdlm_evict_kv(d, bf16_tensor(k), bf16_tensor(v), td, dev(np.array(lens, np.int32)), wd, keep, 5, td,
+                      tw, kept, new)
+    torch.cuda.synchronize()
+    assert lib.bdlm_device_error() == 0
+    for b, n in enumerate(lens):
+        for h in range(2):
+            want = R.evict(w[b, h], n, keep, 5)
+            assert np.array_equal(host(kept)[b, h, :len(want)], want)
+            assert np.array_equal(host(tw)[b, h, :len(want)].view(np.uint32), w[b, h][want].view(np.uint32))
+
+
 def test_eviction_flags_bad_lengths_and_pages(lib):
     rng = np.random.default_rng(4)
     lens = np.array([300, -2, 10 ** 6], np.int32)
