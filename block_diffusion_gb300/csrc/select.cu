@@ -4,13 +4,12 @@
 // Top k of a row of floats: the row's keys (floats mapped to unsigned integers of the same order)
 // are counted in four buckets a thread that evenly divide the range still in question, the bucket
 // holding the k-th largest becomes the next range, and so on; once that bucket holds at most
-// kDirect keys they are ranked against each other directly, mostly after one round (three rounds
+// kDirect keys they are ranked against each other directly, mostly after one round (four rounds
 // at most for 32-bit keys).  One CTA per row, everything after the first read in shared memory
-// where it fits.  The
-// buckets divide the range in use (min .. max first), not fixed bits of the key: rows of similar
-// values would otherwise fall into a few buckets, whose counters then serialise.  Ties at the k-th
-// value go to the lowest index, and the output is in index order, so nothing depends on the order
-// in which threads run.
+// where it fits.  The buckets divide the range in use (min .. max first), not fixed bits of the
+// key: rows of similar values would otherwise fall into a few buckets, whose counters then
+// serialise.  Ties at the k-th value go to the lowest index, and the output is in index order, so
+// nothing depends on the order in which threads run.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
