@@ -908,10 +908,12 @@ __device__ __forceinline__ int choose_tokens(const EvictParams& p, uint32_t* sm)
 // lanes 0-15 the K row and 16-31 the V row, eight tokens in flight.
 //
 // In place (idx increasing, so every token moves to its own slot or an earlier one) a slot may only
-// be written once the tokens before have been read.  A warp therefore owns a 64-byte column slice
-// of K or V of one (sequence, KV head), which no other warp touches, and walks the tokens in
-// order, 64 at a time: all loads, then all stores.  Tokens that stay are skipped.
-constexpr int kMoveWarps = 8;
+// be written once the tokens before have been read.  A CTA therefore owns a (sequence, KV head) and
+// moves some tokens a round: all loads, a barrier, all stores.  The next round's loads may overtake
+// them: it reads only slots behind this round's.  Tokens that stay are skipped.  (A warp to a
+// 64-byte column slice, walking all tokens without barriers: 299 us against 219, 32 x 8 lists of
+// 8192-16384 tokens to 4096; eight warps of eight tokens instead of sixteen of four: 227.)
+constexpr int kMoveWarps = 8, kInPlaceWarps = 16;
 
 __device__ __forceinline__ long long token_row(const CompactParams& p, const int32_t* table, int b,
                                                long long tok, int kvh) {
@@ -975,60 +977,56 @@ move_tokens_kernel(const CompactParams p, int runs) {
   if (run * 32 < count) move_run(p, b, bh - b * p.Hkv, run, count, 0, 32);
 }
 
-// Slice 0 .. 7 (four of K, four of V) of the first `count` tokens (a warp).
-__device__ __forceinline__ void move_slice(const CompactParams& p, int b, int kvh, int unit, int count) {
-  const int lane = threadIdx.x & 31;
-  const int slice = unit & 3, is_v = unit >> 2;
+// The first `count` tokens of one (sequence, KV head) in place (a CTA of WARPS).
+template <int WARPS, int BATCH>
+__device__ __forceinline__ void move_in_place(const CompactParams& p, int b, int kvh, int count) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int base = p.base ? p.base[b] : 0;
   if (base < 0) {
-    if (lane == 0) atomicOr(p.err, BDLM_DEVERR_LENGTH);
+    if (threadIdx.x == 0) atomicOr(p.err, BDLM_DEVERR_LENGTH);
     return;
   }
   const int32_t* idx = p.idx + (static_cast<size_t>(b) * p.heads + (p.heads > 1 ? kvh : 0)) * p.n_max;
-  uint4* pool = reinterpret_cast<uint4*>(is_v ? p.v_pages : p.k_pages) + slice * 4 + (lane & 3);
-  for (int j0 = 0; j0 < count; j0 += 64) {
-    long long from[2], to[2];   // tokens j0 + lane and j0 + 32 + lane
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int j = j0 + h * 32 + lane;
-      from[h] = to[h] = -1;
-      if (j >= count) continue;
-      const int i = __ldcg(idx + j);
-      if (i == j) continue;   // stays where it is
-      if (i < 0) {
-        atomicOr(p.err, BDLM_DEVERR_ROW);
-        continue;
-      }
-      from[h] = token_row(p, p.page_table, b, static_cast<long long>(base) + i, kvh);
-      to[h] = token_row(p, p.to_table, b, static_cast<long long>(base) + j, kvh);
-      if (from[h] < 0) to[h] = -1;
+  uint4* pool = reinterpret_cast<uint4*>(lane < 16 ? p.k_pages : p.v_pages) + (lane & 15);
+  long long from, to;   // lanes below BATCH: the warp's tokens of a round
+  auto look_up = [&](int j0) {
+    const int j = j0 + warp * BATCH + lane;
+    from = to = -1;
+    if (lane >= BATCH || j >= count) return;
+    const int i = __ldcg(idx + j);
+    if (i == j) return;   // stays where it is
+    if (i < 0) {
+      atomicOr(p.err, BDLM_DEVERR_ROW);
+      return;
     }
-    if (!__any_sync(0xffffffffu, to[0] >= 0 || to[1] >= 0)) continue;
-    uint4 v[8];
-    long long dst[8];
+    from = token_row(p, p.page_table, b, static_cast<long long>(base) + i, kvh);
+    to = token_row(p, p.to_table, b, static_cast<long long>(base) + j, kvh);
+    if (from < 0) to = -1;
+  };
+  look_up(0);
+  for (int j0 = 0; j0 < count; j0 += WARPS * BATCH) {
+    uint4 v[BATCH];
+    long long dst[BATCH];
 #pragma unroll
-    for (int x = 0; x < 8; ++x) {   // four lanes a token, eight tokens an instruction
-      const int t = (x & 3) * 8 + (lane >> 2);
-      const long long f = __shfl_sync(0xffffffffu, from[x >> 2], t);
-      dst[x] = __shfl_sync(0xffffffffu, to[x >> 2], t);
+    for (int x = 0; x < BATCH; ++x) {
+      const long long f = __shfl_sync(0xffffffffu, from, x);
+      dst[x] = __shfl_sync(0xffffffffu, to, x);
       if (dst[x] >= 0) v[x] = __ldcg(pool + f * 16);
     }
-    __syncwarp();   // every row of the batch is read before a slot is written
+    look_up(j0 + WARPS * BATCH);   // the next round's rows meanwhile
+    __syncthreads();   // every row of the round is read before a slot is written
 #pragma unroll
-    for (int x = 0; x < 8; ++x)
+    for (int x = 0; x < BATCH; ++x)
       if (dst[x] >= 0) pool[dst[x] * 16] = v[x];
-    __syncwarp();
   }
 }
 
-__global__ void __launch_bounds__(kMoveWarps * 32)
+__global__ void __launch_bounds__(kInPlaceWarps * 32, 2)
 move_in_place_kernel(const CompactParams p) {
   griddep_wait();
   griddep_launch_dependents();
-  const long long unit = static_cast<long long>(blockIdx.x) * kMoveWarps + (threadIdx.x >> 5);
-  if (unit >= static_cast<long long>(p.B) * p.Hkv * 8) return;
-  const int bh = static_cast<int>(unit >> 3), b = bh / p.Hkv;
-  move_slice(p, b, bh - b * p.Hkv, static_cast<int>(unit & 7), min(p.counts[b], p.n_max));
+  const int b = blockIdx.x / p.Hkv;
+  move_in_place<kInPlaceWarps, 4>(p, b, blockIdx.x - b * p.Hkv, min(p.counts[b], p.n_max));
 }
 
 // The choice; with MOVE, the list's tokens move in the same kernel (for few short lists, whose own
@@ -1048,8 +1046,8 @@ evict_kernel(const EvictParams p, const CompactParams m) {
         const int t0 = (u & 1) * 16;
         move_run(m, b, kvh, u >> 1, count, t0, t0 + 16);
       }
-    } else if (warp < 8) {
-      move_slice(m, b, kvh, warp, count);
+    } else {
+      move_in_place<kEvictWarps, 8>(m, b, kvh, count);
     }
   }
 }
@@ -1093,12 +1091,9 @@ cudaError_t launch_select_pages(const SelectParams& p, int num_sms, cudaStream_t
 }
 
 cudaError_t launch_compact(const CompactParams& p, cudaStream_t stream) {
-  if (p.to_table == p.page_table) {
-    const long long units = static_cast<long long>(p.B) * p.Hkv * 8;
-    return launch_pdl(move_in_place_kernel,
-                      dim3(static_cast<unsigned>((units + kMoveWarps - 1) / kMoveWarps)),
-                      dim3(kMoveWarps * 32), 0, stream, p);
-  }
+  if (p.to_table == p.page_table)
+    return launch_pdl(move_in_place_kernel, dim3(static_cast<unsigned>(p.B) * p.Hkv),
+                      dim3(kInPlaceWarps * 32), 0, stream, p);
   const int runs = (p.n_max + 31) / 32;
   const long long units = static_cast<long long>(p.B) * p.Hkv * runs;
   return launch_pdl(move_tokens_kernel,

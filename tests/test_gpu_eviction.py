@@ -150,7 +150,9 @@ def run_evict(lib, k, v, table, lens, w, keep, recent, to, in_place, stream=None
     ([600, 300], 100, 0, "random"), ([600, 300], 100, 100, "random"), ([50, 33], 1, 0, "random"),
     ([50, 33], 1, 1, "random"), ([700, 300, 40], 64, 5, "equal"), ([700, 300], 64, 5, "few"),
     ([3000, 2100], 1500, 64, "tail"), ([2000], 2000, 10, "random"), ([500], 499, 3, "random"),
-    ([26000], 5000, 100, "random"), ([1100, 90], 80, 8, "odd")])
+    ([26000], 5000, 100, "random"), ([1100, 90], 80, 8, "odd"),
+    # more lists than SMs, which move in a kernel of their own
+    ([5 + 37 * i % 400 for i in range(70)], 150, 9, "random"), ([300] * 60, 200, 0, "tail")])
 def test_eviction(lib, lens, keep, recent, kind, in_place):
     rng = np.random.default_rng(sum(lens) + keep)
     Hkv = 2 if max(lens) > 5000 else 3
@@ -252,6 +254,25 @@ def test_compact(lib, heads, in_place):
     assert lib.bdlm_device_error() == 0
     k2, v2 = plain_move(k, v, table, to, base, idx, counts, Hkv)
     assert np.array_equal(bits(kd), k2) and np.array_equal(bits(vd), v2)
+
+
+@pytest.mark.parametrize("n_max", [1, 64, 513])
+def test_compact_in_place_again_and_again(lib, n_max):
+    """Every second, then every third token of long lists: each round's reads lie behind its writes."""
+    import torch
+    rng = np.random.default_rng(n_max)
+    B, Hkv = 3, 4
+    k, v, table, _ = cache(rng, [2000] * B, Hkv, 2000, 0)
+    kd, vd, td = bf16_tensor(k), bf16_tensor(v), dev(table)
+    d = lib.attn_desc(B, 1, Hkv, Hkv, 128, table.shape[1], k.shape[0])
+    counts = np.array([n_max, n_max // 2, n_max], np.int32)
+    for step in (2, 3):
+        idx = np.tile((np.arange(n_max) * step + 1).astype(np.int32), (B, 1, 1))
+        lib.bdlm_compact_kv(d, kd, vd, td, None, dev(idx), 1, n_max, dev(counts), td)
+        k, v = plain_move(k, v, table, table, np.zeros(B, int), idx, counts, Hkv)
+    torch.cuda.synchronize()
+    assert lib.bdlm_device_error() == 0
+    assert np.array_equal(bits(kd), k) and np.array_equal(bits(vd), v)
 
 
 def test_compact_flags_bad_rows(lib):
