@@ -909,8 +909,8 @@ __device__ __forceinline__ int choose_tokens(const EvictParams& p, uint32_t* sm)
 //
 // In place (idx increasing, so every token moves to its own slot or an earlier one) a slot may only
 // be written once the tokens before have been read.  A CTA therefore owns a (sequence, KV head) and
-// moves some tokens a round: all loads, a barrier, all stores.  The next round's loads may overtake
-// them: it reads only slots behind this round's.  Tokens that stay are skipped.  (A warp to a
+// moves some tokens at a time: all loads, a barrier, all stores.  The next loads may overtake the
+// stores: they read only slots behind those.  Tokens that stay are skipped.  (A warp to a
 // 64-byte column slice, walking all tokens without barriers: 299 us against 219, 32 x 8 lists of
 // 8192-16384 tokens to 4096; eight warps of eight tokens instead of sixteen of four: 227.)
 constexpr int kMoveWarps = 8, kInPlaceWarps = 16;
