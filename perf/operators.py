@@ -315,7 +315,8 @@ def _own(s):
         bd.bdlm_sparse_attention(d, s["q"], s["k"], s["v"], s["group"], s["sel_cols"], s["sel"], s["sel_lens"], s["out"])
         return s["out"]
     if op == "weights":
-        bd.bdlm_attention_weights(d, s["q"], s["k"], s["table"], s["lens"], s["lse"], s["decay"], s["weights"])
+        # (the library takes lse densely laid out; one that is passes as it is)
+        bd.bdlm_attention_weights(d, s["q"], s["k"], s["table"], s["lens"], s["lse"].contiguous(), s["decay"], s["weights"])
         return s["weights"]
     bd.bdlm_evict_kv(d, s["k"], s["v"], s["table"], s["lens"], s["weights"], s["keep"], s["recent"], s["to_table"],
                      s["to_weights"], s["kept"], s["new_lens"])
