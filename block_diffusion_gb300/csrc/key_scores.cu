@@ -228,7 +228,9 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
   const int nq = PAGES && n16 <= C::kRowsMax / 2 ? 2 : 1;   // buffers of Q
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&bar_full[s], 1);
+      // (page scores: both warps that fill the stage arrive, so that it is not consumed, where none of
+      // its pages is there to be loaded, before both have seen it empty)
+      mbar_init(&bar_full[s], PAGES ? 2 : 1);
       mbar_init(&bar_empty[s], PAGES ? 1 + kHelpers : 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -401,13 +403,11 @@ key_reduce_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constan
       load_ids();   // they arrive while the stage is waited for
       if (lane == 0) {
         ok = mbar_wait(&bar_empty[st], ((s / C::kStages) & 1) ^ 1, &abort_flag);
-        if (ok && atom == 0) {
-          s_have[st] = have != 0;
-          if (have)
-            mbar_arrive_expect_tx(&bar_full[st], kStage);
-          else
-            mbar_arrive(&bar_full[st]);
-        }
+        if (ok && atom == 0) s_have[st] = have != 0;
+        if (ok && have)
+          mbar_arrive_expect_tx(&bar_full[st], kAtom);   // this warp's half of the stage
+        else if (ok)
+          mbar_arrive(&bar_full[st]);
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
       __syncwarp();

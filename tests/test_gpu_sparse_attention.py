@@ -192,6 +192,34 @@ def test_a_bad_page_is_flagged_whether_or_not_it_is_scored(lib, lens, n):
     p.check(lib, 4, n)
 
 
+@pytest.mark.parametrize("L,Hq,Hkv", [(64, 32, 8), (48, 8, 2), (5, 64, 4)])
+def test_whole_tiles_of_bad_pages_hold_up_nothing(lib, L, Hq, Hkv):
+    """Runs of 128 and more bad ids between good pages, scored for more than 64 rows a list: the choice
+    among the good pages is theirs alone, and no wait runs out."""
+    rng = np.random.default_rng(L)
+    p = Pages(rng, [16 * 1100 + 3, 16 * 900, 40, 16 * 1300], L, Hq, Hkv)
+    t = p.table.copy()
+    for b, runs in ((0, [(128, 256), (512, 900)]), (1, [(0, 128), (256, 384), (512, 640), (768, 896)]),
+                    (3, [(0, 1290)])):
+        for lo, hi in runs:
+            t[b, lo:hi] = np.where(np.arange(hi - lo) % 2, -1, p.num + 7)
+    for n in (1, 100):
+        sel, lens = p.run(lib, L, n, table=t)
+        assert lib.bdlm_device_error() == lib.BDLM_DEVERR_PAGE
+        for b in range(4):
+            full = int(p.lens[b]) // 16
+            good = np.flatnonzero((t[b, :full] >= 0) & (t[b, :full] < p.num))
+            k = min(n, full)
+            for h in range(Hkv):
+                got = sel[b, 0, h, :k]
+                if len(good) < k:   # every good page, and bad ones that make up the number
+                    assert set(t[b, good]) <= set(got)
+                    continue
+                score = R.page_scores(p.q[b], p.bounds, t[b, good], h, Hq // Hkv)
+                best = np.sort(good[np.argsort(-score, kind="stable")[:k]])
+                assert np.array_equal(got, t[b, best])
+
+
 @pytest.mark.parametrize("L,group,Hq,Hkv,n", [(1, 1, 16, 8, 8), (4, 4, 32, 8, 16), (4, 1, 32, 8, 16),
                                              (6, 3, 24, 8, 5), (64, 64, 32, 8, 12), (32, 8, 32, 8, 64),
                                              (16, 16, 16, 1, 30), (2, 1, 4, 4, 300)])
