@@ -46,6 +46,15 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeTiledFn g_encode = nullptr;
 
+// cudaMalloc whose failure is told by the return value alone: the runtime's last error is cleared, or
+// the next call that asks for it after a launch would report this one's failure as its own.
+bool device_alloc(void** ptr, size_t bytes) {
+  if (cudaMalloc(ptr, bytes) == cudaSuccess) return true;
+  cudaGetLastError();
+  *ptr = nullptr;
+  return false;
+}
+
 int current_device(DeviceState** st) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return BDLM_ERR_CUDA;
@@ -61,7 +70,7 @@ int current_device(DeviceState** st) {
     s.num_sms = sms;
     if (s.supported && !s.err) {
       void* err = nullptr;
-      if (cudaMalloc(&err, 256) != cudaSuccess) return BDLM_ERR_NOMEM;
+      if (!device_alloc(&err, 256)) return BDLM_ERR_NOMEM;
       if (cudaMemset(err, 0, 256) != cudaSuccess ||
           cudaStreamSynchronize(nullptr) != cudaSuccess) {
         cudaFree(err);
@@ -94,9 +103,9 @@ int ensure(void** ptr, size_t* cap, size_t need, bool zero, bdlm_stream stream =
   if (n < 2 * *cap) n = 2 * *cap;
   if (*ptr && cudaDeviceSynchronize() != cudaSuccess) return BDLM_ERR_CUDA;
   void* fresh = nullptr;
-  if (cudaMalloc(&fresh, n) != cudaSuccess) {
+  if (!device_alloc(&fresh, n)) {
     n = need;   // no room to spare: just what the call needs
-    if (cudaMalloc(&fresh, n) != cudaSuccess) return BDLM_ERR_NOMEM;
+    if (!device_alloc(&fresh, n)) return BDLM_ERR_NOMEM;
   }
   if (zero && (cudaMemset(fresh, 0, n) != cudaSuccess ||
                cudaStreamSynchronize(nullptr) != cudaSuccess)) {   // `stream` may not wait for it
@@ -1063,7 +1072,7 @@ int bdlm_round_loop_create(const bdlm_round_loop_desc* desc, bdlm_round_loop** o
   const size_t h_b = align256(R * d.H * 2);
   const size_t r4 = align256(R * 4), r1 = align256(R);
   const size_t total = 2 * q_b + 2 * kv_b + h_b + 2 * r4 + r1 + 256;
-  if (cudaMalloc(&lp->scratch, total) != cudaSuccess) {
+  if (!device_alloc(&lp->scratch, total)) {
     delete lp;
     return BDLM_ERR_NOMEM;
   }

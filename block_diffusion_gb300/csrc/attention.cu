@@ -1924,10 +1924,9 @@ cudaError_t launch_attention_ext(const CUtensorMap& tm_q, const CUtensorMap& tm_
   if (e != cudaSuccess || plan.max_splits <= 1) return e;
   const long long groups = static_cast<long long>(B) * Hkv * plan.row_groups;
   const int row_blocks = (plan.G * plan.lsub + 8 * kMergeRows - 1) / (8 * kMergeRows);
-  e = launch_pdl(tree ? attn_merge_kernel<true> : attn_merge_kernel<false>, dim3(static_cast<unsigned>(groups), row_blocks), dim3(256), 0,
-                 stream, prm, plan.n_mma);
-  if (e != cudaSuccess) return e;
-  return cudaGetLastError();
+  return launch_pdl(tree ? attn_merge_kernel<true> : attn_merge_kernel<false>,
+                    dim3(static_cast<unsigned>(groups), row_blocks), dim3(256), 0, stream, prm,
+                    plan.n_mma);
 }
 
 }  // namespace bdlm
