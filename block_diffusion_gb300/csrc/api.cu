@@ -55,7 +55,21 @@ bool device_alloc(void** ptr, size_t bytes) {
   return false;
 }
 
-int current_device(DeviceState** st) {
+// Whether `stream` is being captured (the legacy default stream cannot be): nothing may be allocated
+// then, nor the device waited for, which would end the capture.
+int is_capturing(bdlm_stream stream, bool* yes) {
+  *yes = false;
+  if (!stream) return BDLM_OK;
+  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &cs) != cudaSuccess)
+    return BDLM_ERR_CUDA;
+  *yes = cs != cudaStreamCaptureStatusNone;
+  return BDLM_OK;
+}
+
+// The current device's state.  The first call sets up its error word, and is refused with
+// BDLM_ERR_NOMEM while `stream` is being captured.
+int current_device(DeviceState** st, bdlm_stream stream) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return BDLM_ERR_CUDA;
   if (dev < 0 || dev >= kMaxDevices) return BDLM_ERR_UNSUPPORTED;
@@ -69,6 +83,10 @@ int current_device(DeviceState** st) {
     s.supported = (major == 10 && minor == 3);
     s.num_sms = sms;
     if (s.supported && !s.err) {
+      bool captured;
+      const int rc = is_capturing(stream, &captured);
+      if (rc) return rc;
+      if (captured) return BDLM_ERR_NOMEM;
       void* err = nullptr;
       if (!device_alloc(&err, 256)) return BDLM_ERR_NOMEM;
       if (cudaMemset(err, 0, 256) != cudaSuccess ||
@@ -91,14 +109,12 @@ int current_device(DeviceState** st) {
 // least doubles the buffer, so the retired ones add up to less than the live one.  Nothing can
 // be allocated while `stream` is being captured: that growth is refused with BDLM_ERR_NOMEM,
 // which leaves the capture valid.
-int ensure(void** ptr, size_t* cap, size_t need, bool zero, bdlm_stream stream = nullptr) {
+int ensure(void** ptr, size_t* cap, size_t need, bool zero, bdlm_stream stream) {
   if (need <= *cap) return BDLM_OK;
-  if (stream) {
-    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-    if (cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &cs) != cudaSuccess)
-      return BDLM_ERR_CUDA;
-    if (cs != cudaStreamCaptureStatusNone) return BDLM_ERR_NOMEM;
-  }
+  bool captured;
+  const int rc = is_capturing(stream, &captured);
+  if (rc) return rc;
+  if (captured) return BDLM_ERR_NOMEM;
   size_t n = need + need / 4 + 4096;
   if (n < 2 * *cap) n = 2 * *cap;
   if (*ptr && cudaDeviceSynchronize() != cudaSuccess) return BDLM_ERR_CUDA;
@@ -181,6 +197,8 @@ LmCommitLayout lm_commit_layout(const bdlm::LmConfPlan& plan, int rows) {
   return l;
 }
 
+int reserve_attention(DeviceState* st, const bdlm_attn_desc& d, bool head_tables, AttnPlan* plan,
+                      bdlm_stream stream);
 int attention_impl(DeviceState* st, const bdlm_attn_desc& d, const bdlm_bf16* q,
                    const bdlm_bf16* k_pages, const bdlm_bf16* v_pages, const int32_t* page_table,
                    const int32_t* prefix_lens, bdlm_bf16* out, bdlm_stream stream,
@@ -231,7 +249,7 @@ int bdlm_selftest_wait_timeout(int limit_us, bdlm_stream stream) {
   if (limit_us < 1 || limit_us > 2000000) return BDLM_ERR_INVALID;
   std::lock_guard<std::mutex> lk(g_mu);
   DeviceState* st = nullptr;
-  const int rc = current_device(&st);
+  const int rc = current_device(&st, stream);
   if (rc) return rc;
   const cudaError_t e = bdlm::launch_wait_timeout(
       st->err, static_cast<unsigned long long>(limit_us) * 1000ull,
@@ -242,7 +260,7 @@ int bdlm_selftest_wait_timeout(int limit_us, bdlm_stream stream) {
 int bdlm_release(void) {
   std::lock_guard<std::mutex> lk(g_mu);
   DeviceState* st = nullptr;
-  int rc = current_device(&st);
+  int rc = current_device(&st, nullptr);
   if (rc) return rc;
   if (cudaDeviceSynchronize() != cudaSuccess) return BDLM_ERR_CUDA;
   ++g_workspace_gen;
@@ -279,11 +297,11 @@ int bdlm_confidence_commit_rule(const bdlm_bf16* logits, const uint8_t* mask, in
   if (static_cast<long long>(B) * L > 0x7FFFFFFFll) return BDLM_ERR_INVALID;
   std::lock_guard<std::mutex> lk(g_mu);
   DeviceState* st = nullptr;
-  int rc = current_device(&st);
+  int rc = current_device(&st, stream);
   if (rc) return rc;
   const CommitPlan plan = bdlm::plan_commit(B, L, V, st->num_sms);
   if (plan.total_items > 0x7FFFFFFFll) return BDLM_ERR_INVALID;
-  rc = ensure(&st->data, &st->data_cap, plan.part_bytes, false);
+  rc = ensure(&st->data, &st->data_cap, plan.part_bytes, false, stream);
   if (rc) return rc;
   cudaError_t e = bdlm::launch_commit(logits, mask, B, L, V, threshold, temperature, tok_out,
                                       conf_out, entropy_out, commit_out, plan,
@@ -320,7 +338,7 @@ int bdlm_block_attention(const bdlm_attn_desc* desc, const bdlm_bf16* q,
     return BDLM_ERR_INVALID;
   std::lock_guard<std::mutex> lk(g_mu);
   DeviceState* st = nullptr;
-  int rc = current_device(&st);
+  int rc = current_device(&st, stream);
   if (rc) return rc;
   return attention_impl(st, d, q, k_pages, v_pages, page_table, prefix_lens, out, stream, 1);
 }
@@ -348,7 +366,7 @@ int bdlm_block_attention_kv(const bdlm_attn_desc* desc, const bdlm_bf16* q,
     return BDLM_ERR_INVALID;
   std::lock_guard<std::mutex> lk(g_mu);
   DeviceState* st = nullptr;
-  int rc = current_device(&st);
+  int rc = current_device(&st, stream);
   if (rc) return rc;
   const bdlm::BlockKvWrite kw{k_new, v_new, k_pages, v_pages};
   return attention_impl(st, d, q, k_pages, v_pages, page_table, prefix_lens, out, stream, 1, 0,
@@ -389,10 +407,16 @@ int bdlm_prefill_attention(const bdlm_attn_desc* desc, int prompt_len, const bdl
     return BDLM_ERR_INVALID;
   std::lock_guard<std::mutex> lk(g_mu);
   DeviceState* st = nullptr;
-  int rc = current_device(&st);
+  int rc = current_device(&st, stream);
   if (rc) return rc;
-  rc = ensure(&st->aux, &st->aux_cap, static_cast<size_t>(d.B) * nb * sizeof(int32_t), false);
+  rc = ensure(&st->aux, &st->aux_cap, static_cast<size_t>(d.B) * nb * sizeof(int32_t), false,
+              stream);
   if (rc) return rc;
+  bdlm_attn_desc dv = d;
+  dv.B = d.B * nb;
+  dv.L = Lq;
+  AttnPlan plan;   // before anything is launched: a refused call writes nothing
+  if ((rc = reserve_attention(st, dv, false, &plan, stream))) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // the prompt's K/V into the cache, then one attention sequence per chunk of Lq queries
   if (bdlm::launch_write_block_kv(k_new, v_new, k_pages, v_pages, page_table, prefix_lens, d.B,
@@ -402,15 +426,24 @@ int bdlm_prefill_attention(const bdlm_attn_desc* desc, int prompt_len, const bdl
   int32_t* pre = static_cast<int32_t*>(st->aux);
   if (bdlm::launch_prompt_prefix(prefix_lens, d.B, nb, Lq, pre, s) != cudaSuccess)
     return BDLM_ERR_CUDA;
-  bdlm_attn_desc dv = d;
-  dv.B = d.B * nb;
-  dv.L = Lq;
   return attention_impl(st, dv, q, k_pages, v_pages, page_table, pre, out, stream, nb,
                         Lq > d.L ? d.L : 0);
 }
 }  // extern "C"
 
 namespace {
+
+// Plans the attention and sizes its workspaces.
+int reserve_attention(DeviceState* st, const bdlm_attn_desc& d, bool head_tables, AttnPlan* plan,
+                      bdlm_stream stream) {
+  *plan = bdlm::plan_attention(d.B, d.L, d.Hq, d.Hkv, d.max_pages_per_seq, d.page_size,
+                               st->num_sms);
+  if (plan->n_mma == 0) return BDLM_ERR_UNSUPPORTED;
+  if (head_tables) bdlm::plan_even_lists(*plan, d.B, d.Hkv, d.max_pages_per_seq, st->num_sms);
+  const int rc = ensure(reinterpret_cast<void**>(&st->attn_cnt), &st->attn_cnt_cap,
+                        plan->cnt_bytes, true, stream);
+  return rc ? rc : ensure(&st->data, &st->data_cap, plan->part_bytes, false, stream);
+}
 
 // Block attention of d.B sequences (the caller holds g_mu and has validated d); sequence b
 // uses page-table row b / table_div; mask_block > 0 makes each sequence's queries
@@ -422,16 +455,8 @@ int attention_impl(DeviceState* st, const bdlm_attn_desc& d, const bdlm_bf16* q,
                    const bdlm::AttnExt* ext) {
   int rc = get_encoder();
   if (rc) return rc;
-  AttnPlan plan = bdlm::plan_attention(d.B, d.L, d.Hq, d.Hkv, d.max_pages_per_seq, d.page_size,
-                                       st->num_sms);
-  if (plan.n_mma == 0) return BDLM_ERR_UNSUPPORTED;
-  if (ext && ext->head_tables)
-    bdlm::plan_even_lists(plan, d.B, d.Hkv, d.max_pages_per_seq, st->num_sms);
-  rc = ensure(reinterpret_cast<void**>(&st->attn_cnt), &st->attn_cnt_cap, plan.cnt_bytes, true,
-              stream);
-  if (rc) return rc;
-  rc = ensure(&st->data, &st->data_cap, plan.part_bytes, false, stream);
-  if (rc) return rc;
+  AttnPlan plan;
+  if ((rc = reserve_attention(st, d, ext && ext->head_tables, &plan, stream))) return rc;
   // q viewed as [B*L rows][Hq heads][D]; box = 64 dims x G heads x lsub rows
   CUtensorMap tm_q, tm_k, tm_v;
   {
@@ -474,11 +499,11 @@ int lm_head_impl(const bdlm_bf16* hidden, const bdlm_bf16* w, const int32_t* act
   if (static_cast<long long>(n_rows) * V > (1ll << 40)) return BDLM_ERR_INVALID;
   std::lock_guard<std::mutex> lk(g_mu);
   DeviceState* st = nullptr;
-  int rc = current_device(&st);
+  int rc = current_device(&st, stream);
   if (rc) return rc;
   if ((rc = get_encoder())) return rc;
   const LmHeadPlan plan = bdlm::plan_lm_head(n_active, H, V, st->num_sms);
-  rc = ensure(&st->data, &st->data_cap, plan.gather_bytes, false);
+  rc = ensure(&st->data, &st->data_cap, plan.gather_bytes, false, stream);
   if (rc) return rc;
   uint16_t* gathered = static_cast<uint16_t*>(st->data);
   CUtensorMap tm_w, tm_h;
@@ -528,7 +553,7 @@ int bdlm_active_rows(const uint8_t* mask, const uint8_t* denoising, int B, int L
   if (!mask || !active_idx || !n_active_dev) return BDLM_ERR_INVALID;
   std::lock_guard<std::mutex> lk(g_mu);
   DeviceState* st = nullptr;
-  int rc = current_device(&st);
+  int rc = current_device(&st, stream);
   if (rc) return rc;
   cudaError_t e = bdlm::launch_active_rows(mask, denoising, B, L, active_idx, n_active_dev,
                                            static_cast<cudaStream_t>(stream));
@@ -553,7 +578,7 @@ int bdlm_write_block_kv(const bdlm_attn_desc* desc, const bdlm_bf16* k_new,
     return BDLM_ERR_INVALID;
   std::lock_guard<std::mutex> lk(g_mu);
   DeviceState* st = nullptr;
-  int rc = current_device(&st);
+  int rc = current_device(&st, stream);
   if (rc) return rc;
   cudaError_t e = bdlm::launch_write_block_kv(k_new, v_new, k_pages, v_pages, page_table,
                                               prefix_lens, d.B, d.L, d.Hkv, d.max_pages_per_seq,
@@ -579,14 +604,14 @@ int bdlm_lm_head_commit(const bdlm_bf16* hidden, const bdlm_bf16* w, const uint8
   if (R > 0x7FFFFFFFll || R * V > (1ll << 40)) return BDLM_ERR_INVALID;
   std::lock_guard<std::mutex> lk(g_mu);
   DeviceState* st = nullptr;
-  int rc = current_device(&st);
+  int rc = current_device(&st, stream);
   if (rc) return rc;
   if ((rc = get_encoder())) return rc;
   const int rows = static_cast<int>(R);
   const bdlm::LmConfPlan plan = bdlm::plan_lm_conf(rows, H, V, st->num_sms);
   if (plan.max_row_tiles > plan.units) return BDLM_ERR_UNSUPPORTED;
   const LmCommitLayout lay = lm_commit_layout(plan, rows);
-  rc = ensure(&st->data, &st->data_cap, lay.total, false);
+  rc = ensure(&st->data, &st->data_cap, lay.total, false, stream);
   if (rc) return rc;
   uint8_t* base = static_cast<uint8_t*>(st->data);
   uint16_t* gathered = reinterpret_cast<uint16_t*>(base);
@@ -687,7 +712,7 @@ int bdlm_tree_attention(const bdlm_attn_desc* desc, const bdlm_bf16* q, const bd
     return BDLM_ERR_INVALID;
   std::lock_guard<std::mutex> lk(g_mu);
   DeviceState* st = nullptr;
-  int rc = current_device(&st);
+  int rc = current_device(&st, stream);
   if (rc) return rc;
   bdlm::AttnExt ext;
   ext.tree = true;
@@ -708,7 +733,7 @@ int bdlm_page_bounds(const bdlm_attn_desc* desc, const bdlm_bf16* k_pages,
     return BDLM_ERR_INVALID;
   std::lock_guard<std::mutex> lk(g_mu);
   DeviceState* st = nullptr;
-  int rc = current_device(&st);
+  int rc = current_device(&st, stream);
   if (rc) return rc;
   return bdlm::launch_page_bounds(k_pages, page_table, from_lens, to_lens, d.B, d.Hkv,
                                   d.max_pages_per_seq, d.num_pages, st->num_sms, bounds, st->err,
@@ -738,7 +763,7 @@ int bdlm_select_pages(const bdlm_attn_desc* desc, const bdlm_bf16* q, const bdlm
     return BDLM_ERR_INVALID;
   std::lock_guard<std::mutex> lk(g_mu);
   DeviceState* st = nullptr;
-  int rc = current_device(&st);
+  int rc = current_device(&st, stream);
   if (rc) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int max_tiles = (d.max_pages_per_seq + bdlm::kKeyTile - 1) / bdlm::kKeyTile;
@@ -807,7 +832,7 @@ int bdlm_sparse_attention(const bdlm_attn_desc* desc, const bdlm_bf16* q, const 
   if (!attn_desc_ok(d)) return BDLM_ERR_INVALID;
   std::lock_guard<std::mutex> lk(g_mu);
   DeviceState* st = nullptr;
-  int rc = current_device(&st);
+  int rc = current_device(&st, stream);
   if (rc) return rc;
   bdlm::AttnExt ext;
   ext.head_tables = true;
@@ -829,7 +854,7 @@ int bdlm_attention_weights(const bdlm_attn_desc* desc, const bdlm_bf16* q,
     return BDLM_ERR_INVALID;
   std::lock_guard<std::mutex> lk(g_mu);
   DeviceState* st = nullptr;
-  int rc = current_device(&st);
+  int rc = current_device(&st, stream);
   if (rc) return rc;
   if ((rc = get_encoder())) return rc;
   const int G = d.Hq / d.Hkv;
@@ -880,7 +905,7 @@ int bdlm_evict_kv(const bdlm_attn_desc* desc, bdlm_bf16* k_pages, bdlm_bf16* v_p
     return BDLM_ERR_INVALID;
   std::lock_guard<std::mutex> lk(g_mu);
   DeviceState* st = nullptr;
-  int rc = current_device(&st);
+  int rc = current_device(&st, stream);
   if (rc) return rc;
   const bdlm::EvictParams p{lens, weights, to_weights, kept, new_lens, d.B, d.Hkv,
                             d.max_pages_per_seq, keep, recent, st->err};
@@ -905,7 +930,7 @@ int bdlm_compact_kv(const bdlm_attn_desc* desc, bdlm_bf16* k_pages, bdlm_bf16* v
     return BDLM_ERR_INVALID;
   std::lock_guard<std::mutex> lk(g_mu);
   DeviceState* st = nullptr;
-  int rc = current_device(&st);
+  int rc = current_device(&st, stream);
   if (rc) return rc;
   const bdlm::CompactParams p{k_pages, v_pages, page_table, to_table, base_lens, idx, counts,
                               d.B, d.Hkv, heads, d.max_pages_per_seq, d.num_pages, n_max, st->err};
@@ -935,11 +960,11 @@ struct bdlm_round_loop {
 namespace {
 
 // Sizes the library workspaces for one round of the loop (nothing may be allocated while the
-// round is being captured).
-int reserve_round(const bdlm_round_loop_desc& d) {
+// round is being captured, nor while `stream` is).
+int reserve_round(const bdlm_round_loop_desc& d, bdlm_stream stream) {
   std::lock_guard<std::mutex> lk(g_mu);
   DeviceState* st = nullptr;
-  int rc = current_device(&st);
+  int rc = current_device(&st, stream);
   if (rc) return rc;
   const bdlm_attn_desc& a = d.attn;
   const AttnPlan ap = bdlm::plan_attention(a.B, a.L, a.Hq, a.Hkv, a.max_pages_per_seq,
@@ -952,9 +977,9 @@ int reserve_round(const bdlm_round_loop_desc& d) {
   const size_t fused = lm_commit_layout(cp, R).total;
   if (fused > data) data = fused;
   if ((rc = ensure(reinterpret_cast<void**>(&st->attn_cnt), &st->attn_cnt_cap, ap.cnt_bytes,
-                   true)))
+                   true, stream)))
     return rc;
-  if ((rc = ensure(&st->data, &st->data_cap, data, false))) return rc;
+  if ((rc = ensure(&st->data, &st->data_cap, data, false, stream))) return rc;
   return get_encoder();
 }
 
@@ -965,12 +990,13 @@ void drop_graph(bdlm_round_loop* lp) {
   lp->graph = nullptr;
 }
 
-// Builds the graph: step counter := 0, then WHILE(condition) { one round }.
-int capture_round_loop(bdlm_round_loop* lp) {
+// Builds the graph: step counter := 0, then WHILE(condition) { one round }.  It will be launched on
+// `stream`.
+int capture_round_loop(bdlm_round_loop* lp, bdlm_stream stream) {
   const bdlm_round_loop_desc& d = lp->d;
   const bdlm_attn_desc& a = d.attn;
   const int R = a.B * a.L;
-  int rc = reserve_round(d);
+  int rc = reserve_round(d, stream);
   if (rc) return rc;
   {
     std::lock_guard<std::mutex> lk(g_mu);
@@ -1091,7 +1117,7 @@ int bdlm_round_loop_create(const bdlm_round_loop_desc* desc, bdlm_round_loop** o
     delete lp;
     return BDLM_ERR_CUDA;
   }
-  const int rc = capture_round_loop(lp);
+  const int rc = capture_round_loop(lp, nullptr);
   if (rc) {
     bdlm_round_loop_destroy(lp);
     return rc;
@@ -1108,7 +1134,7 @@ int bdlm_round_loop_launch(bdlm_round_loop* loop, bdlm_stream stream) {
     gen = g_workspace_gen;
   }
   if (gen != loop->gen || !loop->exec) {
-    const int rc = capture_round_loop(loop);  // a workspace moved since the capture
+    const int rc = capture_round_loop(loop, stream);  // a workspace moved since the capture
     if (rc) return rc;
   }
   return cudaGraphLaunch(loop->exec, static_cast<cudaStream_t>(stream)) == cudaSuccess

@@ -23,10 +23,11 @@
  *    lives in a per-device workspace that the library allocates on first need and grows
  *    when a larger problem arrives (growing synchronises the device).  Calls that share
  *    a device must not run concurrently on different streams: they share that
- *    workspace.  It cannot grow while `stream` is being captured (BDLM_ERR_NOMEM: run the call
- *    once before capturing it); a captured graph keeps the memory it was captured with, and
- *    graphs must not run concurrently either.  bdlm_release() frees the workspace, after which
- *    graphs captured before it must not run.
+ *    workspace.  It cannot grow while `stream` is being captured: the call returns
+ *    BDLM_ERR_NOMEM and the capture goes on (run the call once before capturing it; a device's
+ *    first call is refused in the same way).  A captured graph keeps the memory it was captured
+ *    with, and graphs must not run concurrently either.  bdlm_release() frees the workspace,
+ *    after which graphs captured before it must not run.
  *  - Return value: BDLM_OK (0) or a negative BDLM_ERR_* code; bdlm_status_string() names it.
  */
 #ifndef BDLM_H

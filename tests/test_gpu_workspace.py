@@ -1,5 +1,9 @@
 """The library workspace: growth inside a capture, allocations that fail, what a captured graph keeps
 and what is given back."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 
@@ -17,7 +21,7 @@ class Calls:
     def __init__(self, lib):
         import torch
         rng = np.random.default_rng(21)
-        a = W.make_attention(rng, 2, 4, 32, 8, 128, prefix_lens=np.array([5000, 64]), poison=False)
+        a = W.make_attention(rng, 2, 4, 32, 8, 128, prefix_lens=np.array([9000, 64]), poison=False)
         self.lib, self.a = lib, a
         self.q, self.k, self.v = bf16_tensor(a.q), bf16_tensor(a.k_ref), bf16_tensor(a.v_ref)
         self.t, self.n = dev(a.page_table_ref), dev(a.prefix_lens)
@@ -103,3 +107,126 @@ def test_an_allocation_that_failed_leaves_no_error_behind(lib):
     torch.cuda.synchronize()
     assert np.array_equal(host(c.out.float()), want)
     assert lib.bdlm_device_error() == 0
+CAPTURED = ["block_attention", "block_attention_kv", "prefill", "tree_attention", "select_pages", "commit",
+            "commit_rule", "lm_head", "lm_head_device_count", "lm_head_commit"]
+
+
+@pytest.mark.parametrize("name", CAPTURED)
+def test_growth_in_a_capture_is_refused_and_the_capture_stays_valid(lib, name):
+    """Every entry point that takes scratch: with the workspace released the captured call is refused,
+    and what is captured beside it replays; after a call outside it is captured and replays."""
+    import torch
+    c = Calls(lib)
+    call = getattr(c, name)
+    x = torch.zeros((), device="cuda")
+    torch.cuda.synchronize()
+    lib.bdlm_release()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        with pytest.raises(lib.BdlmError) as e:
+            call()
+        x.add_(1.0)
+    assert e.value.status == lib.BDLM_ERR_NOMEM
+    graph.replay()
+    torch.cuda.synchronize()
+    assert float(x) == 1.0
+    call()
+    outs = (c.out, c.tok, c.conf, c.com, c.logits, c.sel, c.sl)
+    want = [o.clone() for o in outs]
+    for o in outs:
+        o.zero_()
+    with torch.cuda.graph(second := torch.cuda.CUDAGraph(), stream=torch.cuda.Stream()):
+        call()
+    second.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    assert lib.bdlm_device_error() == 0
+
+
+def test_a_refused_prefill_has_written_nothing(lib):
+    """Room for its prompts' table but not for its attention: the K/V write is not captured either."""
+    import torch
+    c = Calls(lib)
+    torch.cuda.synchronize()
+    lib.bdlm_release()
+    c.prefill()
+    wide = torch.zeros((2, 16384), dtype=torch.int32, device="cuda")
+    wide[:, :c.t.shape[1]] = c.t
+    d = lib.attn_desc(2, 4, 32, 8, 128, 16384, c.k.shape[0])
+    c.k.fill_(3.0)
+    with torch.cuda.graph(graph := torch.cuda.CUDAGraph(), stream=torch.cuda.Stream()):
+        with pytest.raises(lib.BdlmError) as e:
+            lib.bdlm_prefill_attention(d, 4, c.q, c.kn, c.kn, c.k, c.v, wide, c.zero, c.out)
+        c.out.zero_()
+    assert e.value.status == lib.BDLM_ERR_NOMEM
+    graph.replay()
+    torch.cuda.synchronize()
+    assert float(c.k.float().min()) == 3.0
+    assert lib.bdlm_device_error() == 0
+
+
+def test_a_loop_relaunched_in_a_capture_is_refused_where_it_would_need_memory(lib):
+    import torch
+    from test_gpu_round_loop import Case
+    c = Case(5, B=4)
+    mask, den = dev(c.mask0), dev(c.den)
+    tok = torch.zeros((c.S, c.B, c.L), dtype=torch.int32, device="cuda")
+    conf = torch.zeros((c.S, c.B, c.L), device="cuda")
+    com = torch.zeros((c.S, c.B, c.L), dtype=torch.uint8, device="cuda")
+    done = torch.zeros((1,), dtype=torch.int32, device="cuda")
+    loop = lib.bdlm_round_loop_create(lib.round_loop_desc(
+        c.desc(lib), c.S, c.H, c.V, lib.BDLM_COMMIT_TOPK, 1, 0.5, 1.0, q_steps=c.q, k_new_steps=c.kn,
+        v_new_steps=c.vn, hidden_steps=c.hid, k_pages=c.k0, v_pages=c.v0, page_table=c.pt,
+        prefix_lens=c.pl, w=c.w, mask=mask, denoising=den, tok_steps=tok, conf_steps=conf,
+        commit_steps=com, steps_done=done))
+    try:
+        torch.cuda.synchronize()
+        lib.bdlm_release()
+        x = torch.zeros((), device="cuda")
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+            with pytest.raises(lib.BdlmError) as e:
+                lib.bdlm_round_loop_launch(loop)
+            x.add_(1.0)
+        assert e.value.status == lib.BDLM_ERR_NOMEM
+        graph.replay()
+        lib.bdlm_round_loop_launch(loop)
+        torch.cuda.synchronize()
+        assert float(x) == 1.0 and 1 <= int(done) <= c.S
+    finally:
+        lib.bdlm_round_loop_destroy(loop)
+
+
+FIRST = """
+import sys
+sys.path[:0] = [{root!r}, {tests!r}]
+import torch
+import block_diffusion_gb300 as bd
+from test_gpu_workspace import Calls
+c = Calls(bd)
+x = torch.zeros((), device="cuda")
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g, stream=torch.cuda.Stream()):
+    try:
+        c.lm_head()
+        raise SystemExit("not refused")
+    except bd.BdlmError as e:
+        assert e.status == bd.BDLM_ERR_NOMEM, e
+    x.add_(1.0)
+g.replay()
+c.lm_head()
+torch.cuda.synchronize()
+assert float(x) == 1.0 and float(c.logits.float().min()) == 64.0
+assert bd.bdlm_device_error() == 0
+print("fine")
+"""
+
+
+def test_a_process_whose_first_call_is_captured(lib):
+    """The library's first call on a device sets up its error word, which is memory too."""
+    tests = os.path.dirname(os.path.abspath(__file__))
+    code = FIRST.format(root=os.path.dirname(tests), tests=tests)
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "fine", r.stdout + r.stderr
