@@ -11,12 +11,14 @@
 #include "../../include/bdlm.h"
 #include "cache_ops.h"
 #include "kernels.h"
+#include "workspace.h"
 
 namespace {
 
 using bdlm::AttnPlan;
 using bdlm::CommitPlan;
 using bdlm::LmHeadPlan;
+using bdlm::Workspace;
 
 constexpr int kMaxDevices = 64;
 
@@ -25,12 +27,10 @@ struct DeviceState {
   bool supported = false;
   int num_sms = 0;
   int* err = nullptr;            // device error word
-  int* attn_cnt = nullptr;       // attention scheduler counters (zero between calls)
-  size_t attn_cnt_cap = 0;
-  void* data = nullptr;          // split / commit partials, gathered rows, sequence order
-  size_t data_cap = 0;
-  void* aux = nullptr;           // prompt-block prefix lengths of a prefill
-  size_t aux_cap = 0;
+  Workspace attn_cnt;            // attention scheduler counters (zero between calls)
+  Workspace data;                // split / commit partials, gathered rows, sequence order
+  Workspace aux;                 // prompt-block prefix lengths of a prefill
+  std::vector<void*> retired;    // smaller workspaces that callers' graphs may hold
 };
 
 std::mutex g_mu;
@@ -38,7 +38,8 @@ DeviceState g_dev[kMaxDevices];
 // Bumped whenever a workspace is reallocated or freed: CUDA graphs that captured the old
 // buffers are re-captured before their next launch.
 unsigned g_workspace_gen = 0;
-std::vector<void*> g_retired[kMaxDevices];   // smaller workspaces, kept for captured graphs
+// This thread is capturing the round loop's own graph, which such a bump has captured again.
+thread_local bool t_own_capture = false;
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
@@ -103,45 +104,39 @@ int current_device(DeviceState** st, bdlm_stream stream) {
   return BDLM_OK;
 }
 
-// Grows a buffer (zero-initialised where `zero`); growing waits for the device to be idle first.
-// The smaller buffer is retired, not freed: a CUDA graph that a caller captured holds its
-// address, and a replay must still find memory there (bdlm_release frees it).  Each growth at
-// least doubles the buffer, so the retired ones add up to less than the live one.  Nothing can
-// be allocated while `stream` is being captured: that growth is refused with BDLM_ERR_NOMEM,
+// A device's memory, as bdlm::grow takes it.
+struct DeviceMemory {
+  DeviceState* st;
+  bool wait() { return cudaDeviceSynchronize() == cudaSuccess; }
+  bool alloc(void** ptr, size_t bytes) { return device_alloc(ptr, bytes); }
+  void free(void* ptr) { cudaFree(ptr); }
+  bool zero(void* ptr, size_t bytes) {   // waits: the caller's stream may not wait for it
+    return cudaMemset(ptr, 0, bytes) == cudaSuccess && cudaStreamSynchronize(nullptr) == cudaSuccess;
+  }
+  bool retire(void* ptr) {
+    try {
+      st->retired.push_back(ptr);
+      return true;
+    } catch (...) {   // no host memory for the list
+      return false;
+    }
+  }
+};
+
+// Makes a workspace (zero-initialised where `zero`) hold `need` bytes, for work on `stream`.  Nothing
+// can be allocated while `stream` is being captured: growth is refused with BDLM_ERR_NOMEM then,
 // which leaves the capture valid.
-int ensure(void** ptr, size_t* cap, size_t need, bool zero, bdlm_stream stream) {
-  if (need <= *cap) return BDLM_OK;
+int ensure(DeviceState* st, Workspace& w, size_t need, bool zero, bdlm_stream stream) {
   bool captured;
   const int rc = is_capturing(stream, &captured);
   if (rc) return rc;
+  if (need <= w.cap) {
+    if (captured && !t_own_capture) w.in_graph = true;
+    return BDLM_OK;
+  }
   if (captured) return BDLM_ERR_NOMEM;
-  size_t n = need + need / 4 + 4096;
-  if (n < 2 * *cap) n = 2 * *cap;
-  if (*ptr && cudaDeviceSynchronize() != cudaSuccess) return BDLM_ERR_CUDA;
-  void* fresh = nullptr;
-  if (!device_alloc(&fresh, n)) {
-    n = need;   // no room to spare: just what the call needs
-    if (!device_alloc(&fresh, n)) return BDLM_ERR_NOMEM;
-  }
-  if (zero && (cudaMemset(fresh, 0, n) != cudaSuccess ||
-               cudaStreamSynchronize(nullptr) != cudaSuccess)) {   // `stream` may not wait for it
-    cudaFree(fresh);
-    return BDLM_ERR_CUDA;
-  }
-  if (*ptr) {
-    int dev = 0;
-    cudaGetDevice(&dev);
-    try {
-      g_retired[dev].push_back(*ptr);
-    } catch (...) {   // no host memory for the list
-      cudaFree(fresh);
-      return BDLM_ERR_NOMEM;
-    }
-  }
   ++g_workspace_gen;
-  *ptr = fresh;
-  *cap = n;
-  return BDLM_OK;
+  return bdlm::grow(w, need, zero, DeviceMemory{st});
 }
 
 int get_encoder() {
@@ -264,17 +259,12 @@ int bdlm_release(void) {
   if (rc) return rc;
   if (cudaDeviceSynchronize() != cudaSuccess) return BDLM_ERR_CUDA;
   ++g_workspace_gen;
-  cudaFree(st->attn_cnt);
-  cudaFree(st->data);
-  cudaFree(st->aux);
-  int dev = 0;
-  cudaGetDevice(&dev);
-  for (void* p : g_retired[dev]) cudaFree(p);
-  g_retired[dev].clear();
-  st->attn_cnt = nullptr;
-  st->data = nullptr;
-  st->aux = nullptr;
-  st->attn_cnt_cap = st->data_cap = st->aux_cap = 0;
+  for (Workspace* w : {&st->attn_cnt, &st->data, &st->aux}) {
+    cudaFree(w->ptr);
+    *w = Workspace{};
+  }
+  for (void* p : st->retired) cudaFree(p);
+  st->retired.clear();
   return BDLM_OK;
 }
 
@@ -301,11 +291,11 @@ int bdlm_confidence_commit_rule(const bdlm_bf16* logits, const uint8_t* mask, in
   if (rc) return rc;
   const CommitPlan plan = bdlm::plan_commit(B, L, V, st->num_sms);
   if (plan.total_items > 0x7FFFFFFFll) return BDLM_ERR_INVALID;
-  rc = ensure(&st->data, &st->data_cap, plan.part_bytes, false, stream);
+  rc = ensure(st, st->data, plan.part_bytes, false, stream);
   if (rc) return rc;
   cudaError_t e = bdlm::launch_commit(logits, mask, B, L, V, threshold, temperature, tok_out,
                                       conf_out, entropy_out, commit_out, plan,
-                                      static_cast<bdlm::CommitPartial*>(st->data), st->err,
+                                      static_cast<bdlm::CommitPartial*>(st->data.ptr), st->err,
                                       static_cast<cudaStream_t>(stream), rule, k);
   return e == cudaSuccess ? BDLM_OK : BDLM_ERR_CUDA;
 }
@@ -409,8 +399,7 @@ int bdlm_prefill_attention(const bdlm_attn_desc* desc, int prompt_len, const bdl
   DeviceState* st = nullptr;
   int rc = current_device(&st, stream);
   if (rc) return rc;
-  rc = ensure(&st->aux, &st->aux_cap, static_cast<size_t>(d.B) * nb * sizeof(int32_t), false,
-              stream);
+  rc = ensure(st, st->aux, static_cast<size_t>(d.B) * nb * sizeof(int32_t), false, stream);
   if (rc) return rc;
   bdlm_attn_desc dv = d;
   dv.B = d.B * nb;
@@ -423,7 +412,7 @@ int bdlm_prefill_attention(const bdlm_attn_desc* desc, int prompt_len, const bdl
                                   prompt_len, d.Hkv, d.max_pages_per_seq, d.num_pages, st->err,
                                   s) != cudaSuccess)
     return BDLM_ERR_CUDA;
-  int32_t* pre = static_cast<int32_t*>(st->aux);
+  int32_t* pre = static_cast<int32_t*>(st->aux.ptr);
   if (bdlm::launch_prompt_prefix(prefix_lens, d.B, nb, Lq, pre, s) != cudaSuccess)
     return BDLM_ERR_CUDA;
   return attention_impl(st, dv, q, k_pages, v_pages, page_table, pre, out, stream, nb,
@@ -440,9 +429,8 @@ int reserve_attention(DeviceState* st, const bdlm_attn_desc& d, bool head_tables
                                st->num_sms);
   if (plan->n_mma == 0) return BDLM_ERR_UNSUPPORTED;
   if (head_tables) bdlm::plan_even_lists(*plan, d.B, d.Hkv, d.max_pages_per_seq, st->num_sms);
-  const int rc = ensure(reinterpret_cast<void**>(&st->attn_cnt), &st->attn_cnt_cap,
-                        plan->cnt_bytes, true, stream);
-  return rc ? rc : ensure(&st->data, &st->data_cap, plan->part_bytes, false, stream);
+  const int rc = ensure(st, st->attn_cnt, plan->cnt_bytes, true, stream);
+  return rc ? rc : ensure(st, st->data, plan->part_bytes, false, stream);
 }
 
 // Block attention of d.B sequences (the caller holds g_mu and has validated d); sequence b
@@ -478,8 +466,8 @@ int attention_impl(DeviceState* st, const bdlm_attn_desc& d, const bdlm_bf16* q,
   const float scale = d.sm_scale > 0.f ? d.sm_scale : 1.0f / sqrtf(128.0f);
   cudaError_t e = bdlm::launch_attention_ext(tm_q, tm_k, tm_v, page_table, prefix_lens, out, d.B,
                                              d.L, d.Hq, d.Hkv, d.max_pages_per_seq, d.num_pages,
-                                             scale, plan, static_cast<float*>(st->data),
-                                             st->attn_cnt, st->err, st->num_sms,
+                                             scale, plan, static_cast<float*>(st->data.ptr),
+                                             static_cast<int*>(st->attn_cnt.ptr), st->err, st->num_sms,
                                              static_cast<cudaStream_t>(stream), table_div,
                                              mask_block, kv_write, ext);
   return e == cudaSuccess ? BDLM_OK : BDLM_ERR_CUDA;
@@ -503,9 +491,9 @@ int lm_head_impl(const bdlm_bf16* hidden, const bdlm_bf16* w, const int32_t* act
   if (rc) return rc;
   if ((rc = get_encoder())) return rc;
   const LmHeadPlan plan = bdlm::plan_lm_head(n_active, H, V, st->num_sms);
-  rc = ensure(&st->data, &st->data_cap, plan.gather_bytes, false, stream);
+  rc = ensure(st, st->data, plan.gather_bytes, false, stream);
   if (rc) return rc;
-  uint16_t* gathered = static_cast<uint16_t*>(st->data);
+  uint16_t* gathered = static_cast<uint16_t*>(st->data.ptr);
   CUtensorMap tm_w, tm_h;
   {
     cuuint64_t dims[2] = {static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(V)};
@@ -611,9 +599,9 @@ int bdlm_lm_head_commit(const bdlm_bf16* hidden, const bdlm_bf16* w, const uint8
   const bdlm::LmConfPlan plan = bdlm::plan_lm_conf(rows, H, V, st->num_sms);
   if (plan.max_row_tiles > plan.units) return BDLM_ERR_UNSUPPORTED;
   const LmCommitLayout lay = lm_commit_layout(plan, rows);
-  rc = ensure(&st->data, &st->data_cap, lay.total, false, stream);
+  rc = ensure(st, st->data, lay.total, false, stream);
   if (rc) return rc;
-  uint8_t* base = static_cast<uint8_t*>(st->data);
+  uint8_t* base = static_cast<uint8_t*>(st->data.ptr);
   uint16_t* gathered = reinterpret_cast<uint16_t*>(base);
   bdlm::CommitPartial* part = reinterpret_cast<bdlm::CommitPartial*>(base + lay.off_part);
   int32_t* act = reinterpret_cast<int32_t*>(base + lay.off_act);
@@ -778,14 +766,14 @@ int bdlm_select_pages(const bdlm_attn_desc* desc, const bdlm_bf16* q, const bdlm
         align256(static_cast<size_t>(lists) * d.max_pages_per_seq * sizeof(float));
     const size_t amax_bytes =
         static_cast<size_t>(d.B) * d.Hkv * max_tiles * bdlm::kAmaxPerTile * sizeof(float);
-    rc = ensure(&st->data, &st->data_cap, 3 * score_bytes + amax_bytes, false, stream);
+    rc = ensure(st, st->data, 3 * score_bytes + amax_bytes, false, stream);
     if (rc) return rc;
     bdlm::KeyParams p = key_params(d, page_table, prefix_lens, st->err);
     p.max_tiles = max_tiles;
     p.q = q;
     p.bounds = bounds;
-    p.scores = reinterpret_cast<float*>(static_cast<uint8_t*>(st->data) + 2 * score_bytes);
-    p.amax = reinterpret_cast<float*>(static_cast<uint8_t*>(st->data) + 3 * score_bytes);
+    p.scores = reinterpret_cast<float*>(static_cast<uint8_t*>(st->data.ptr) + 2 * score_bytes);
+    p.amax = reinterpret_cast<float*>(static_cast<uint8_t*>(st->data.ptr) + 3 * score_bytes);
     p.group = group;
     p.groups = groups;
     p.width = group * G;
@@ -809,7 +797,7 @@ int bdlm_select_pages(const bdlm_attn_desc* desc, const bdlm_bf16* q, const bdlm
     }
     sp.scores = p.scores;
     sp.amax = p.amax;
-    sp.exact = static_cast<unsigned long long*>(st->data);
+    sp.exact = static_cast<unsigned long long*>(st->data.ptr);
   }
   return bdlm::launch_select_pages(sp, st->num_sms, s) == cudaSuccess ? BDLM_OK : BDLM_ERR_CUDA;
 }
@@ -976,10 +964,8 @@ int reserve_round(const bdlm_round_loop_desc& d, bdlm_stream stream) {
   size_t data = ap.part_bytes;
   const size_t fused = lm_commit_layout(cp, R).total;
   if (fused > data) data = fused;
-  if ((rc = ensure(reinterpret_cast<void**>(&st->attn_cnt), &st->attn_cnt_cap, ap.cnt_bytes,
-                   true, stream)))
-    return rc;
-  if ((rc = ensure(&st->data, &st->data_cap, data, false, stream))) return rc;
+  if ((rc = ensure(st, st->attn_cnt, ap.cnt_bytes, true, stream))) return rc;
+  if ((rc = ensure(st, st->data, data, false, stream))) return rc;
   return get_encoder();
 }
 
@@ -1042,6 +1028,7 @@ int capture_round_loop(bdlm_round_loop* lp, bdlm_stream stream) {
   c.dst[3] = reinterpret_cast<uint4*>(lp->h_w);
   c.n_vec[3] = static_cast<long long>(R) * d.H * 2 / 16;
   int r2 = BDLM_OK;
+  t_own_capture = true;
   if (bdlm::launch_select_step(c, lp->step, d.steps, lp->cap) != cudaSuccess) r2 = BDLM_ERR_CUDA;
   if (!r2) r2 = bdlm_block_attention_kv(&a, lp->q_w, lp->k_w, lp->v_w, d.k_pages, d.v_pages,
                                         d.page_table, d.prefix_lens, a.L, lp->attn_out, s);
@@ -1059,6 +1046,7 @@ int capture_round_loop(bdlm_round_loop* lp, bdlm_stream stream) {
   if (!r2 && bdlm::launch_loop_condition(handle, d.mask, R, lp->step, d.steps, d.steps_done,
                                          lp->cap) != cudaSuccess)
     r2 = BDLM_ERR_CUDA;
+  t_own_capture = false;
   cudaGraph_t captured = nullptr;
   const cudaError_t ec = cudaStreamEndCapture(lp->cap, &captured);
   if (r2) return r2;
@@ -1136,6 +1124,13 @@ int bdlm_round_loop_launch(bdlm_round_loop* loop, bdlm_stream stream) {
   if (gen != loop->gen || !loop->exec) {
     const int rc = capture_round_loop(loop, stream);  // a workspace moved since the capture
     if (rc) return rc;
+  }
+  bool captured;
+  const int rc = is_capturing(stream, &captured);
+  if (rc) return rc;
+  if (captured) {   // the caller's graph will hold what the loop's does
+    std::lock_guard<std::mutex> lk(g_mu);
+    g_dev[loop->device].attn_cnt.in_graph = g_dev[loop->device].data.in_graph = true;
   }
   return cudaGraphLaunch(loop->exec, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? BDLM_OK

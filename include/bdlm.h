@@ -26,8 +26,8 @@
  *    workspace.  It cannot grow while `stream` is being captured: the call returns
  *    BDLM_ERR_NOMEM and the capture goes on (run the call once before capturing it; a device's
  *    first call is refused in the same way).  A captured graph keeps the memory it was captured
- *    with, and graphs must not run concurrently either.  bdlm_release() frees the workspace,
- *    after which graphs captured before it must not run.
+ *    with, which is then kept beside a larger workspace, and graphs must not run concurrently
+ *    either.  bdlm_release() frees all of it, after which graphs captured before must not run.
  *  - Return value: BDLM_OK (0) or a negative BDLM_ERR_* code; bdlm_status_string() names it.
  */
 #ifndef BDLM_H

@@ -230,3 +230,57 @@ def test_a_process_whose_first_call_is_captured(lib):
     code = FIRST.format(root=os.path.dirname(tests), tests=tests)
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "fine", r.stdout + r.stderr
+
+
+def test_a_workspace_that_no_capture_used_is_given_back_when_it_grows(lib):
+    """Growing from 0.8 to 1.6 GB leaves about a quarter more than the need held, not both buffers."""
+    import torch
+    table = torch.zeros((1, 262144), dtype=torch.int32, device="cuda")
+    lens = dev(np.array([0], np.int32))
+
+    def select(L, Hkv):   # scratch: 12 bytes per list and page of the table, L * Hkv lists
+        q = torch.zeros((1, L, Hkv, 128), dtype=torch.bfloat16, device="cuda")
+        bounds = torch.zeros((1, Hkv, 2, 128), dtype=torch.bfloat16, device="cuda")
+        sel = torch.zeros((1, L, Hkv, 8), dtype=torch.int32, device="cuda")
+        sl = torch.zeros((1, L), dtype=torch.int32, device="cuda")
+        d = lib.attn_desc(1, L, Hkv, Hkv, 128, 262144, 1)
+        lib.bdlm_select_pages(d, q, bounds, table, lens, 1, 2, 8, sel, sl)
+        torch.cuda.synchronize()
+
+    torch.cuda.synchronize()
+    lib.bdlm_release()
+    select(1, 8)
+    lib.bdlm_release()
+    torch.cuda.empty_cache()
+    free = torch.cuda.mem_get_info()[0]
+    for L in (32, 64, 64):
+        select(L, 8)
+    torch.cuda.empty_cache()
+    held = free - torch.cuda.mem_get_info()[0]
+    need = 64 * 8 * 262144 * 12
+    assert need <= held <= 1.25 * need + 2 ** 28, held / need
+    lib.bdlm_release()
+
+
+def test_a_workspace_that_a_graph_uses_outlives_growth(lib):
+    """The graph replays in the memory it was captured with; later growth, which no graph has seen,
+    gives its buffers back."""
+    import torch
+    c = Calls(lib)
+    torch.cuda.synchronize()
+    lib.bdlm_release()
+    c.block_attention()
+    want = host(c.out.float())
+    with torch.cuda.graph(graph := torch.cuda.CUDAGraph(), stream=torch.cuda.Stream()):
+        c.block_attention()
+    for rows in (512, 4096, 32768):
+        hidden = torch.zeros((rows, 1024), dtype=torch.bfloat16, device="cuda")
+        lib.bdlm_lm_head(hidden, hidden[:512], torch.arange(rows, dtype=torch.int32, device="cuda"), rows,
+                         rows, 1024, 512, torch.empty((rows, 512), dtype=torch.bfloat16, device="cuda"))
+        junk = torch.full((2 ** 24,), 7.0, device="cuda")   # whatever was freed gets written
+        c.out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(host(c.out.float()), want)
+        del junk
+    assert lib.bdlm_device_error() == 0
