@@ -112,6 +112,7 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
   constexpr uint32_t kQCol = 384;   // first tensor-memory column of Q (kQTmem)
   __shared__ unsigned long long s_seen[EXT ? kItemRing : 1];   // block tokens some query sees
   // EXT, rows on N: the visibility words of the item's queries (at most 32 rows)
+  __shared__ int s_row[EXT && !ROWS ? 32 : 1];   // EXT, rows on N: where a row's output goes
   __shared__ unsigned long long s_words[EXT && !ROWS ? kItemRing : 1][EXT && !ROWS ? 32 : 1];
   static_assert(!EXT || !MASKED, "tree visibility and block-causal prefill are separate");
   static_assert(!MASKED || ROWS, "the block-causal mask is applied by the row-per-thread softmax");
@@ -1384,11 +1385,13 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
           s_l[x] = sum;
           if constexpr (EXT) {
             if (it.n_splits == 1) {
-              if (p.lse != nullptr && x < rows && x / p.G < p.L)
-                p.lse[(static_cast<size_t>(it.b) * p.L + x / p.G) * p.Hq + head_base + x % p.G] =
-                    row_lse(s_m[x], sum, cs);
-              // the factor of the row; a row that saw nothing has O = 0, and gets 0
-              s_l[x] = sum > 0.f ? 1.f / sum : 0.f;
+              const int q = x / p.G;
+              const size_t at = (static_cast<size_t>(it.b) * p.L + q) * p.Hq + head_base + (x - q * p.G);
+              if (p.lse != nullptr && x < rows && q < p.L) p.lse[at] = row_lse(s_m[x], sum, cs);
+              const float l_row = sum > 0.f ? sum : 1.f;   // a row that saw nothing: O = 0 stays 0
+              s_l[x] = l_row;
+              s_alpha[x] = 1.f / l_row;   // (the factors of the chunks are done with)
+              s_row[x] = static_cast<int>(at);   // (B * L * Hq fits an int)
             }
           }
         }
@@ -1405,18 +1408,48 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
             tmem_ld16(tO + lane_off + cg * 16, r);
             tmem_wait_ld();
             tmem_regs_ready(r);
+            // EXT rounds as block attention does, but its products with 1 / l are divided out only
+            // where that can matter: sixteen divisions are code that every launch fetches anew (8
+            // queries over 60 tokens 9.9 us a call against 8.4)
+            uint32_t nearest = ~0u;
+            if constexpr (EXT) {
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                const float res = __uint_as_float(r[k]) * s_alpha[cg * 16 + k];
+                nearest = min(nearest, bf16_border(res));
+                r[k] = __float_as_uint(res);
+              }
+            }
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
               const int n = cg * 16 + k;
               if (n < rows && i < p.L) {
                 const float ov = __uint_as_float(r[k]);
-                *o = __bfloat16_as_ushort(__float2bfloat16_rn(EXT ? ov * s_l[n] : ov / s_l[n]));
+                *o = __bfloat16_as_ushort(__float2bfloat16_rn(EXT ? ov : ov / s_l[n]));
               }
               o += 128;
               if (++g == p.G) {
                 g = 0;
                 ++i;
                 o += next;
+              }
+            }
+            if constexpr (EXT) {
+              if (__any_sync(0xffffffffu, nearest <= kBf16Border)) {
+                uint32_t divide = 0;
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                  divide |= (bf16_border(__uint_as_float(r[k])) <= kBf16Border) << k;
+                divide = __reduce_or_sync(0xffffffffu, divide);
+                const int live = min(rows, p.L * p.G) - cg * 16;
+                if (live < 16) divide &= (1u << max(live, 0)) - 1;
+#pragma unroll 1
+                for (; divide != 0; divide &= divide - 1) {
+                  const int n = cg * 16 + __ffs(static_cast<int>(divide)) - 1;
+                  const float ov = tmem_ld1(tO + lane_off + n);
+                  p.out[static_cast<size_t>(s_row[n]) * 128 + x] =
+                      __bfloat16_as_ushort(__float2bfloat16_rn(ov / s_l[n]));
+                }
               }
             }
           }

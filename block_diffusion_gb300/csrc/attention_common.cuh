@@ -176,6 +176,24 @@ __device__ __forceinline__ float row_lse(float m, float l, float scale_log2) {
   return l > 0.f ? fmaf(m, scale_log2, __log2f(l)) * kLn2 : -CUDART_INF_F;
 }
 
+// x = a * (1 / b), each rounded, may round to another bf16 than a / b does where bf16_border(x) is at
+// most kBf16Border.  x has two roundings of half a step at most, 2^-24 each, and a / b one: they lie
+// within 3 steps of float32 of each other, so a border between two bf16, low half 0x8000, can only lie
+// between them if it is as near to x.
+constexpr uint32_t kBf16Border = 8u << 16;
+__device__ __forceinline__ uint32_t bf16_border(float x) {   // (its low half + 0x8004) << 16
+  return __float_as_uint(x) * 0x10000u + 0x80040000u;
+}
+
+// One column of this warp's lanes of tensor memory (whole warp).
+__device__ __forceinline__ float tmem_ld1(uint32_t taddr) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
+  tmem_wait_ld();
+  asm volatile("" : "+r"(r));
+  return __uint_as_float(r);
+}
+
 // Maximum over the warp in one instruction (redux.sync of float32, sm_100 family); a NaN counts as
 // no value, as in fmaxf.
 __device__ __forceinline__ float warp_max(float x) {

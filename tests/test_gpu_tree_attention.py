@@ -137,3 +137,24 @@ def test_bad_pages_and_lengths_are_flagged(lib):
     torch.cuda.synchronize()
     assert lib.bdlm_device_error() == lib.BDLM_DEVERR_PAGE | lib.BDLM_DEVERR_LENGTH
     check(lib, a, masks(rng, 3, 8, "tree"))
+
+
+@pytest.mark.parametrize("B,L,lo,hi", [(640, 4, 20, 200), (640, 8, 20, 200), (400, 16, 20, 200), (200, 40, 20, 200),
+                                       (24, 8, 2000, 9000), (24, 40, 2000, 9000)])
+def test_no_mask_is_block_attention_over_many_results(lib, B, L, lo, hi):
+    """Bit for bit over millions of results, among which any other rounding of the quotient shows."""
+    import torch
+    torch.manual_seed(L)
+    cols = (hi + L + 15) // 16
+    lens = torch.randint(lo, hi, (B,), dtype=torch.int32, device="cuda")
+    t = torch.randperm(B * cols, device="cuda").int().view(B, cols)
+    k = torch.randn((B * cols, 16, 8, 128), device="cuda").bfloat16()
+    v = torch.randn((B * cols, 16, 8, 128), device="cuda").bfloat16()
+    q = torch.randn((B, L, 32, 128), device="cuda").bfloat16()
+    block, tree = torch.empty_like(q), torch.empty_like(q)
+    d = lib.attn_desc(B, L, 32, 8, 128, cols, B * cols)
+    lib.bdlm_block_attention(d, q, k, v, t, lens, L, block)
+    lib.bdlm_tree_attention(d, q, k, v, t, lens, None, tree)
+    torch.cuda.synchronize()
+    assert torch.equal(block, tree)
+    assert lib.bdlm_device_error() == 0
