@@ -173,14 +173,24 @@ def _stream(stream) -> int | None:
     return stream.cuda_stream
 
 
-def _dense(fn: str, stream, *tensors) -> list:
+_kinds = None   # the element types an argument may have
+
+
+def _dense(fn: str, kinds: str, stream, *tensors) -> list:
     """Device addresses of the tensors (addresses and None pass), and the stream's.  Refuses a
-    tensor that a bare address would misread: not contiguous, or not on the current device."""
+    tensor that a bare address would misread: of another element type than its letter in `kinds`
+    (b: bf16 or its 16 bits, i: int32, f: float32, w: 64-bit words), not contiguous, or not on
+    the current device.  Shapes are the caller's, as in C."""
+    global _kinds
     dev = _current_device()
+    if _kinds is None:
+        import torch
+        _kinds = {"b": (torch.bfloat16, torch.int16, torch.uint16), "i": (torch.int32, torch.uint32),
+                  "f": (torch.float32,), "w": (torch.int64, torch.uint64)}
     out = []
-    for t in tensors:
+    for kind, t in zip(kinds, tensors):
         if t is not None and not isinstance(t, int):
-            if t.get_device() != dev or not t.is_contiguous():
+            if t.dtype not in _kinds[kind] or t.get_device() != dev or not t.is_contiguous():
                 raise BdlmError(fn, BDLM_ERR_INVALID)
             t = t.data_ptr()
         out.append(t)
@@ -299,8 +309,8 @@ def bdlm_tree_attention(desc: AttnDesc, q, k_pages, v_pages, page_table, prefix_
                         out, lse=None, stream=None) -> None:
     """tree_mask: [B, L] int64/uint64 visibility words, or None (every query sees the block);
     lse: [B, L, Hq] float32, or None."""
-    *ptrs, s = _dense("bdlm_tree_attention", stream, q, k_pages, v_pages, page_table, prefix_lens,
-                      tree_mask, out, lse)
+    *ptrs, s = _dense("bdlm_tree_attention", "bbbiiwbf", stream, q, k_pages, v_pages, page_table,
+                      prefix_lens, tree_mask, out, lse)
     rc = load_library().bdlm_tree_attention(ctypes.byref(desc), *ptrs, s)
     _check("bdlm_tree_attention", rc)
 
@@ -308,8 +318,8 @@ def bdlm_tree_attention(desc: AttnDesc, q, k_pages, v_pages, page_table, prefix_
 def bdlm_compact_kv(desc: AttnDesc, k_pages, v_pages, page_table, base_lens, idx, heads: int,
                     n_max: int, counts, to_table, stream=None) -> None:
     """to_table is page_table itself for a move in place."""
-    k, v, table, base, ix, c, to, s = _dense("bdlm_compact_kv", stream, k_pages, v_pages,
-                                             page_table, base_lens, idx, counts, to_table)
+    k, v, table, base, ix, c, to, s = _dense("bdlm_compact_kv", "bbiiiii", stream, k_pages,
+                                             v_pages, page_table, base_lens, idx, counts, to_table)
     rc = load_library().bdlm_compact_kv(ctypes.byref(desc), k, v, table, base, ix, int(heads),
                                         int(n_max), c, to, s)
     _check("bdlm_compact_kv", rc)
@@ -317,15 +327,15 @@ def bdlm_compact_kv(desc: AttnDesc, k_pages, v_pages, page_table, base_lens, idx
 
 def bdlm_page_bounds(desc: AttnDesc, k_pages, page_table, from_lens, to_lens, bounds,
                      stream=None) -> None:
-    ptrs = _dense("bdlm_page_bounds", stream, k_pages, page_table, from_lens, to_lens, bounds)
+    ptrs = _dense("bdlm_page_bounds", "biiib", stream, k_pages, page_table, from_lens, to_lens, bounds)
     rc = load_library().bdlm_page_bounds(ctypes.byref(desc), *ptrs)
     _check("bdlm_page_bounds", rc)
 
 
 def bdlm_select_pages(desc: AttnDesc, q, bounds, page_table, prefix_lens, group: int,
                       n_select: int, sel_cols: int, sel_table, sel_lens, stream=None) -> None:
-    *ptrs, sel, lens, s = _dense("bdlm_select_pages", stream, q, bounds, page_table, prefix_lens,
-                                 sel_table, sel_lens)
+    *ptrs, sel, lens, s = _dense("bdlm_select_pages", "bbiiii", stream, q, bounds, page_table,
+                                 prefix_lens, sel_table, sel_lens)
     rc = load_library().bdlm_select_pages(ctypes.byref(desc), *ptrs, int(group), int(n_select),
                                           int(sel_cols), sel, lens, s)
     _check("bdlm_select_pages", rc)
@@ -333,8 +343,8 @@ def bdlm_select_pages(desc: AttnDesc, q, bounds, page_table, prefix_lens, group:
 
 def bdlm_sparse_attention(desc: AttnDesc, q, k_pages, v_pages, group: int, sel_cols: int,
                           sel_table, sel_lens, out, stream=None) -> None:
-    qp, k, v, sel, lens, o, s = _dense("bdlm_sparse_attention", stream, q, k_pages, v_pages,
-                                       sel_table, sel_lens, out)
+    qp, k, v, sel, lens, o, s = _dense("bdlm_sparse_attention", "bbbiib", stream, q, k_pages,
+                                       v_pages, sel_table, sel_lens, out)
     rc = load_library().bdlm_sparse_attention(ctypes.byref(desc), qp, k, v, int(group),
                                               int(sel_cols), sel, lens, o, s)
     _check("bdlm_sparse_attention", rc)
@@ -342,8 +352,8 @@ def bdlm_sparse_attention(desc: AttnDesc, q, k_pages, v_pages, group: int, sel_c
 
 def bdlm_attention_weights(desc: AttnDesc, q, k_pages, page_table, prefix_lens, lse, decay: float,
                            weights, stream=None) -> None:
-    *ptrs, w, s = _dense("bdlm_attention_weights", stream, q, k_pages, page_table, prefix_lens, lse,
-                         weights)
+    *ptrs, w, s = _dense("bdlm_attention_weights", "bbiiff", stream, q, k_pages, page_table,
+                         prefix_lens, lse, weights)
     rc = load_library().bdlm_attention_weights(ctypes.byref(desc), *ptrs, float(decay), w, s)
     _check("bdlm_attention_weights", rc)
 
@@ -351,8 +361,9 @@ def bdlm_attention_weights(desc: AttnDesc, q, k_pages, page_table, prefix_lens, 
 def bdlm_evict_kv(desc: AttnDesc, k_pages, v_pages, page_table, lens, weights, keep: int,
                   recent: int, to_table, to_weights, kept, new_lens, stream=None) -> None:
     """to_table is page_table itself, and to_weights weights, for an eviction in place."""
-    *ptrs, to, tw, kp, nl, s = _dense("bdlm_evict_kv", stream, k_pages, v_pages, page_table, lens,
-                                      weights, to_table, to_weights, kept, new_lens)
+    *ptrs, to, tw, kp, nl, s = _dense("bdlm_evict_kv", "bbiififii", stream, k_pages, v_pages,
+                                      page_table, lens, weights, to_table, to_weights, kept,
+                                      new_lens)
     rc = load_library().bdlm_evict_kv(ctypes.byref(desc), *ptrs, int(keep), int(recent), to, tw,
                                       kp, nl, s)
     _check("bdlm_evict_kv", rc)

@@ -118,6 +118,54 @@ def test_empty_calls_succeed_without_a_device(so):
     assert compact(so, n_max=0) == 0
 
 
+def binding_calls(bd):
+    """Each operator's call of B = 0 sequences (nothing is launched), and its tensors' types by name."""
+    d = bd.attn_desc(0, 4, 8, 8, 128, 2, 8)
+    b, i, f, w = "bfloat16", "int32", "float32", "int64"
+    return [
+        (dict(q=b, k_pages=b, v_pages=b, page_table=i, prefix_lens=i, tree_mask=w, out=b, lse=f),
+         lambda t: bd.bdlm_tree_attention(d, **t, stream=0)),
+        (dict(k_pages=b, v_pages=b, page_table=i, base_lens=i, idx=i, counts=i, to_table=i),
+         lambda t: bd.bdlm_compact_kv(d, **t, heads=1, n_max=4, stream=0)),
+        (dict(k_pages=b, page_table=i, from_lens=i, to_lens=i, bounds=b),
+         lambda t: bd.bdlm_page_bounds(d, **t, stream=0)),
+        (dict(q=b, bounds=b, page_table=i, prefix_lens=i, sel_table=i, sel_lens=i),
+         lambda t: bd.bdlm_select_pages(d, **t, group=4, n_select=2, sel_cols=4, stream=0)),
+        (dict(q=b, k_pages=b, v_pages=b, sel_table=i, sel_lens=i, out=b),
+         lambda t: bd.bdlm_sparse_attention(d, **t, group=4, sel_cols=4, stream=0)),
+        (dict(q=b, k_pages=b, page_table=i, prefix_lens=i, lse=f, weights=f),
+         lambda t: bd.bdlm_attention_weights(d, **t, decay=1.0, stream=0)),
+        (dict(k_pages=b, v_pages=b, page_table=i, lens=i, weights=f, to_table=i, to_weights=f, kept=i,
+              new_lens=i),
+         lambda t: bd.bdlm_evict_kv(d, **t, keep=4, recent=1, stream=0)),
+    ]
+
+
+def test_binding_refuses_other_element_types(so, monkeypatch):
+    """An address says nothing of the type behind it: int64 indices (of sort or nonzero), float64 weights
+    or float16 queries would be read as something else."""
+    import torch
+
+    import block_diffusion_gb300 as bd
+    monkeypatch.setattr(bd, "_device", lambda: -1)         # the CPU's tensors stand for the device's
+    monkeypatch.setattr(bd, "_raw_stream", lambda dev: 0)
+    every = [torch.bfloat16, torch.float16, torch.float32, torch.float64, torch.uint8, torch.int32,
+             torch.int64]
+    for types, call in binding_calls(bd):
+        good = {n: torch.zeros(64, dtype=getattr(torch, t)) for n, t in types.items()}
+        call(good)
+        for name, t in types.items():
+            for other in every:
+                if other == getattr(torch, t):
+                    continue
+                with pytest.raises(bd.BdlmError) as e:
+                    call(dict(good, **{name: torch.zeros(64, dtype=other)}))
+                assert e.value.status == bd.BDLM_ERR_INVALID, (name, other)
+        for name, t in types.items():                       # the same bits under another name pass
+            if t == "bfloat16":
+                call(dict(good, **{name: good[name].view(torch.int16)}))
+
+
 @pytest.mark.gpu
 def test_binding_refuses_tensors_an_address_would_misread():
     import torch
