@@ -659,6 +659,12 @@ bool cache_desc_ok(const bdlm_attn_desc& d) {
 constexpr int kMaxTokens = 1 << 30;
 bool too_many_tokens(const bdlm_attn_desc& d) { return d.max_pages_per_seq > kMaxTokens / 16; }
 
+// Moves of n tokens a list to other pages are one launch, a CTA for eight runs of 32.
+bool too_many_moves(const bdlm_attn_desc& d, int n) {
+  const long long runs = (static_cast<long long>(n) + 31) / 32;
+  return static_cast<long long>(d.B) * d.Hkv * runs > 8 * 0x7FFFFFFFll;
+}
+
 bdlm::KeyParams key_params(const bdlm_attn_desc& d, const int32_t* page_table,
                            const int32_t* prefix_lens, int* err) {
   bdlm::KeyParams p = {};
@@ -886,7 +892,8 @@ int bdlm_evict_kv(const bdlm_attn_desc* desc, bdlm_bf16* k_pages, bdlm_bf16* v_p
   if (keep < 1 || keep > static_cast<long long>(d.max_pages_per_seq) * d.page_size || recent < 0 ||
       recent > keep)
     return BDLM_ERR_INVALID;
-  if (too_many_tokens(d)) return BDLM_ERR_UNSUPPORTED;
+  if (too_many_tokens(d) || (to_table != page_table && too_many_moves(d, keep)))
+    return BDLM_ERR_UNSUPPORTED;
   if (d.B == 0) return BDLM_OK;
   if (!k_pages || !v_pages || !page_table || !lens || !weights || !to_table || !to_weights ||
       !kept || !new_lens || lens == new_lens || !aligned16(k_pages) || !aligned16(v_pages))
@@ -911,7 +918,9 @@ int bdlm_compact_kv(const bdlm_attn_desc* desc, bdlm_bf16* k_pages, bdlm_bf16* v
   if (!desc || !cache_desc_ok(*desc)) return BDLM_ERR_INVALID;
   const bdlm_attn_desc d = *desc;
   if ((heads != 1 && heads != d.Hkv) || n_max < 0) return BDLM_ERR_INVALID;
-  if (too_many_tokens(d) || n_max > kMaxTokens) return BDLM_ERR_UNSUPPORTED;
+  if (too_many_tokens(d) || n_max > kMaxTokens ||
+      (to_table != page_table && too_many_moves(d, n_max)))
+    return BDLM_ERR_UNSUPPORTED;
   if (d.B == 0 || n_max == 0) return BDLM_OK;
   if (!k_pages || !v_pages || !page_table || !idx || !counts || !to_table || !aligned16(k_pages) ||
       !aligned16(v_pages))

@@ -373,7 +373,8 @@ int bdlm_tree_attention(const bdlm_attn_desc* desc, const bdlm_bf16* q, const bd
  * table or a bad page id skips that token and sets a device error bit (ROW, LENGTH, PAGE).  desc as
  * bdlm_write_block_kv (L unused).  k_pages, v_pages 16-byte aligned.  n_max == 0 is a no-op.
  * max_pages_per_seq > 2^26 (2^30 tokens; also for bdlm_page_bounds, bdlm_attention_weights and
- * bdlm_evict_kv) or n_max > 2^30 returns BDLM_ERR_UNSUPPORTED.
+ * bdlm_evict_kv) or n_max > 2^30 returns BDLM_ERR_UNSUPPORTED, and so does a move to other pages
+ * of more than 2^34 - 8 runs of 32 tokens (B * Hkv * ceil(n_max / 32); keep for bdlm_evict_kv).
  */
 int bdlm_compact_kv(const bdlm_attn_desc* desc, bdlm_bf16* k_pages, bdlm_bf16* v_pages,
                     const int32_t* page_table, const int32_t* base_lens, const int32_t* idx,

@@ -106,6 +106,15 @@ def test_counts_beyond_the_token_counters(so):
     assert compact(so, desc(B=0), n_max=2 ** 30) == 0
 
 
+def test_moves_beyond_a_grid(so):
+    """More moves to other pages than one launch has CTAs for (256 tokens of a list and head each)."""
+    many = desc(B=2 ** 15, Hq=2 ** 15, Hkv=2 ** 15, cols=2 ** 15, num=1)
+    assert compact(so, many, n_max=2 ** 19 - 31, to=P + 64) == -3      # 2^30 lists of 2^14 runs
+    assert compact(so, many, n_max=2 ** 30, to=P + 64) == -3
+    wide = desc(B=2 ** 5, Hq=2 ** 10, Hkv=2 ** 10, cols=2 ** 26, num=1)
+    assert evict(so, wide, keep=2 ** 30, to=P + 64) == -3
+
+
 def test_weights_refuse_a_vanishing_scale(so):
     for scale in (1e-38, 2.0 ** -65):
         assert weights(so, desc(B=0, sm_scale=scale)) == -3, scale
