@@ -111,7 +111,7 @@ def test_moves_beyond_a_grid(so):
     many = desc(B=2 ** 15, Hq=2 ** 15, Hkv=2 ** 15, cols=2 ** 15, num=1)
     assert compact(so, many, n_max=2 ** 19 - 31, to=P + 64) == -3      # 2^30 lists of 2^14 runs
     assert compact(so, many, n_max=2 ** 30, to=P + 64) == -3
-    wide = desc(B=2 ** 5, Hq=2 ** 10, Hkv=2 ** 10, cols=2 ** 26, num=1)
+    wide = desc(B=2 ** 4, Hq=2 ** 11, Hkv=2 ** 11, cols=2 ** 26, num=1)
     assert evict(so, wide, keep=2 ** 30, to=P + 64) == -3
 
 
