@@ -173,7 +173,15 @@ def _stream(stream) -> int | None:
     return stream.cuda_stream
 
 
-_kinds = None   # the element types an argument may have
+_types = {}   # by the `kinds` of a call: what element types each of its tensors may have
+
+
+def _element_types(kinds: str) -> tuple:
+    import torch
+    each = {"b": (torch.bfloat16, torch.int16, torch.uint16), "i": (torch.int32, torch.uint32),
+            "f": (torch.float32,), "w": (torch.int64, torch.uint64)}
+    _types[kinds] = tuple(each[k] for k in kinds)
+    return _types[kinds]
 
 
 def _dense(fn: str, kinds: str, stream, *tensors) -> list:
@@ -181,16 +189,11 @@ def _dense(fn: str, kinds: str, stream, *tensors) -> list:
     tensor that a bare address would misread: of another element type than its letter in `kinds`
     (b: bf16 or its 16 bits, i: int32, f: float32, w: 64-bit words), not contiguous, or not on
     the current device.  Shapes are the caller's, as in C."""
-    global _kinds
     dev = _current_device()
-    if _kinds is None:
-        import torch
-        _kinds = {"b": (torch.bfloat16, torch.int16, torch.uint16), "i": (torch.int32, torch.uint32),
-                  "f": (torch.float32,), "w": (torch.int64, torch.uint64)}
     out = []
-    for kind, t in zip(kinds, tensors):
-        if t is not None and not isinstance(t, int):
-            if t.dtype not in _kinds[kind] or t.get_device() != dev or not t.is_contiguous():
+    for types, t in zip(_types.get(kinds) or _element_types(kinds), tensors):
+        if t is not None and t.__class__ is not int:
+            if t.dtype not in types or t.get_device() != dev or not t.is_contiguous():
                 raise BdlmError(fn, BDLM_ERR_INVALID)
             t = t.data_ptr()
         out.append(t)
