@@ -22,6 +22,9 @@
 //    ring carries K of chunk u+1 ahead of V of chunk u and S^T is double-buffered, so the
 //    softmax of one chunk overlaps the K stream of the next and the pipeline never drains
 //    between items.
+//  * P is rounded to bf16, half a step of 2^-8 of each value: an MMA has operands of one type and
+//    V is bf16, so a P of more bits would be two MMAs.  The sums l, m and O are float32, and l
+//    adds the values before that rounding.
 //  * Either whole sequences, longest first (when there are enough items), or splits of a
 //    long sequence that write (O, m, l) partials merged by a small second kernel; no CTA
 //    ever waits on another one, and every wait inside a CTA is bounded.
@@ -111,8 +114,8 @@ attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CU
   constexpr int kPBufs = 2;
   constexpr uint32_t kQCol = 384;   // first tensor-memory column of Q (kQTmem)
   __shared__ unsigned long long s_seen[EXT ? kItemRing : 1];   // block tokens some query sees
-  // EXT, rows on N: the visibility words of the item's queries (at most 32 rows)
   __shared__ int s_row[EXT && !ROWS ? 32 : 1];   // EXT, rows on N: where a row's output goes
+  // EXT, rows on N: the visibility words of the item's queries (at most 32 rows)
   __shared__ unsigned long long s_words[EXT && !ROWS ? kItemRing : 1][EXT && !ROWS ? 32 : 1];
   static_assert(!EXT || !MASKED, "tree visibility and block-causal prefill are separate");
   static_assert(!MASKED || ROWS, "the block-causal mask is applied by the row-per-thread softmax");

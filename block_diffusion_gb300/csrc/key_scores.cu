@@ -754,8 +754,9 @@ page_scores_direct_kernel(const KeyParams p) {
 // Bounds of the full pages that hold tokens from .. to - 1: lo and hi over the 16 slots, per head
 // dim.  A thread takes 8 dims of one page and head: 16 independent 16-byte loads, then packed
 // bf16 minima and maxima (exact).  HBM bound: 4 KB read and 512 bytes written per page and head.
-// 32 prompts of 4096 tokens, 8 heads: 56 us a call with eight CTAs per SM and loads that pass L1 by;
-// 58 with sixteen CTAs per SM, 72 with four, 64 with sixteen and cached loads.
+// 32 prompts of 4096 tokens, 8 heads: 50 us a call, 6.0 TB/s.  Over and over on one prompt 44 us with
+// eight CTAs per SM and loads that pass L1 by; 47 with sixteen CTAs per SM, 59 with four, 51 with
+// sixteen and cached loads.
 __global__ void __launch_bounds__(128)
 page_bounds_kernel(const uint16_t* __restrict__ k_pages, const int32_t* __restrict__ page_table,
                    const int32_t* __restrict__ from, const int32_t* __restrict__ to, int Hkv,
@@ -831,7 +832,8 @@ int key_rows_max() { return 256; }
 
 cudaError_t launch_attention_weights(const CUtensorMap& tm_q, const CUtensorMap& tm_k,
                                      const KeyParams& p, int num_sms, cudaStream_t stream) {
-  // up to 32 query rows: more stages and two Q buffers; more rows need their shared memory for Q
+  // up to 32 query rows: two CTAs per SM, 32-column tiles in four tensor-memory buffers, -lse from a table
+  // in shared memory; more rows: one CTA per SM, a tile's columns split between sets, -lse by MMA
   return p.rows > 32 ? launch_key_t<false, true>(tm_q, tm_k, p, num_sms, stream)
                      : launch_key_t<false, false>(tm_q, tm_k, p, num_sms, stream);
 }
