@@ -60,7 +60,7 @@ bool device_alloc(void** ptr, size_t bytes) {
 // then, nor the device waited for, which would end the capture.
 int is_capturing(bdlm_stream stream, bool* yes) {
   *yes = false;
-  if (!stream) return BDLM_OK;
+  if (!stream || stream == static_cast<bdlm_stream>(cudaStreamLegacy)) return BDLM_OK;
   cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
   if (cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &cs) != cudaSuccess)
     return BDLM_ERR_CUDA;
