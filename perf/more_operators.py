@@ -316,7 +316,8 @@ def _own(s):
         bd.bdlm_attention_kv8(d, s["q"], s["k8"], s["v8"], s["scales"], s["table"], s["lens"], s["out"])
         return s["out"]
     if op == "write":
-        bd.bdlm_write_kv8(d, s["L"], s["first"], s["k_new"], s["v_new"], s["k8"], s["v8"], s["scales"], s["table"], s["lens"])
+        bd.bdlm_write_kv8(d, s["L"], s["first"], s["k_new"].shape[0], s["k_new"], s["v_new"], s["k8"], s["v8"],
+                          s["scales"], s["table"], s["lens"])
         return s["k8"], s["v8"], s["scales"]
     if op == "rotary":
         bd.bdlm_rotary(d, s["rotary"], s["L"], s["q"], s["stride"], s["k"], s["stride"], s["lens"], s["positions"], False,
