@@ -8,7 +8,8 @@ Entry points mirror ``include/bdlm.h``:
     bdlm_block_attention, bdlm_lm_head, bdlm_confidence_commit, bdlm_confidence_commit_rule,
     bdlm_apply_commit, bdlm_status_string, bdlm_device_error, bdlm_release; over part of the
     cache: bdlm_tree_attention, bdlm_compact_kv, bdlm_page_bounds, bdlm_select_pages,
-    bdlm_sparse_attention, bdlm_attention_weights, bdlm_evict_kv
+    bdlm_sparse_attention, bdlm_attention_weights, bdlm_evict_kv; on the cache's side of a step:
+    bdlm_build_tables, bdlm_rotary_init, bdlm_rotary, bdlm_write_kv8, bdlm_attention_kv8
 """
 from __future__ import annotations
 
@@ -35,11 +36,18 @@ BDLM_COMMIT_SEQUENTIAL = 2
 BDLM_COMMIT_ANTI_SEQUENTIAL = 3
 BDLM_COMMIT_ENTROPY_BOUNDED = 4
 
+BDLM_ROTARY_NONE = 0
+BDLM_ROTARY_LINEAR = 1
+BDLM_ROTARY_BASE = 2
+BDLM_ROTARY_BANDS = 3
+BDLM_ROTARY_YARN = 4
+
 EXPORTS = ("bdlm_block_attention", "bdlm_block_attention_kv", "bdlm_prefill_attention", "bdlm_lm_head", "bdlm_lm_head_device_count",
            "bdlm_lm_head_commit", "bdlm_active_rows", "bdlm_write_block_kv", "bdlm_confidence_commit",
            "bdlm_confidence_commit_rule", "bdlm_apply_commit", "bdlm_tree_attention",
            "bdlm_compact_kv", "bdlm_page_bounds", "bdlm_select_pages", "bdlm_sparse_attention",
-           "bdlm_attention_weights", "bdlm_evict_kv", "bdlm_round_loop_create",
+           "bdlm_attention_weights", "bdlm_evict_kv", "bdlm_build_tables", "bdlm_rotary_init",
+           "bdlm_rotary", "bdlm_write_kv8", "bdlm_attention_kv8", "bdlm_round_loop_create",
            "bdlm_round_loop_launch", "bdlm_round_loop_destroy", "bdlm_status_string",
            "bdlm_device_error", "bdlm_selftest_wait_timeout", "bdlm_release")
 
@@ -50,6 +58,12 @@ class AttnDesc(ctypes.Structure):
                 ("Hkv", ctypes.c_int), ("D", ctypes.c_int), ("page_size", ctypes.c_int),
                 ("max_pages_per_seq", ctypes.c_int), ("num_pages", ctypes.c_int),
                 ("sm_scale", ctypes.c_float)]
+
+
+class RotaryDesc(ctypes.Structure):
+    """bdlm_rotary_desc."""
+    _fields_ = [("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int),
+                ("amplitude", ctypes.c_float), ("turns", ctypes.c_uint64 * 64)]
 
 
 class RoundLoopDesc(ctypes.Structure):
@@ -120,6 +134,18 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.bdlm_attention_weights.restype = I
     lib.bdlm_evict_kv.argtypes = [D, P, P, P, P, P, I, I, P, P, P, P, P]
     lib.bdlm_evict_kv.restype = I
+    lib.bdlm_build_tables.argtypes = [D, P, P, P, I, P, P, P, P, I, P, P, P, P]
+    lib.bdlm_build_tables.restype = I
+    G = ctypes.c_double
+    lib.bdlm_rotary_init.argtypes = [ctypes.POINTER(RotaryDesc), I, I, G, I, G, G, G, G, G]
+    lib.bdlm_rotary_init.restype = I
+    LL = ctypes.c_longlong
+    lib.bdlm_rotary.argtypes = [D, ctypes.POINTER(RotaryDesc), I, P, LL, P, LL, P, P, I, P, P, P]
+    lib.bdlm_rotary.restype = I
+    lib.bdlm_write_kv8.argtypes = [D, I, P, I, P, P, P, P, P, P, P, P]
+    lib.bdlm_write_kv8.restype = I
+    lib.bdlm_attention_kv8.argtypes = [D, P, P, P, P, P, P, P, P]
+    lib.bdlm_attention_kv8.restype = I
     lib.bdlm_round_loop_create.argtypes = [ctypes.POINTER(RoundLoopDesc),
                                            ctypes.POINTER(ctypes.c_void_p)]
     lib.bdlm_round_loop_create.restype = I
@@ -179,16 +205,29 @@ _types = {}   # by the `kinds` of a call: what element types each of its tensors
 def _element_types(kinds: str) -> tuple:
     import torch
     each = {"b": (torch.bfloat16, torch.int16, torch.uint16), "i": (torch.int32, torch.uint32),
-            "f": (torch.float32,), "w": (torch.int64, torch.uint64)}
+            "f": (torch.float32,), "w": (torch.int64, torch.uint64),
+            "e": (torch.float8_e4m3fn, torch.uint8)}
     _types[kinds] = tuple(each[k] for k in kinds)
     return _types[kinds]
+
+
+def _rows(fn: str, t):
+    """Device address of a bf16 tensor that may be a slice of a wider one: contiguous in its last two
+    dimensions (an address and None pass)."""
+    if t is None or t.__class__ is int:
+        return t
+    types = _types.get("b") or _element_types("b")
+    if t.dtype not in types[0] or t.get_device() != _current_device() or t.dim() < 2 or not (
+            t.stride(-1) == 1 and (t.stride(-2) == t.shape[-1] or t.shape[-2] == 1)):
+        raise BdlmError(fn, BDLM_ERR_INVALID)
+    return t.data_ptr()
 
 
 def _dense(fn: str, kinds: str, stream, *tensors) -> list:
     """Device addresses of the tensors (addresses and None pass), and the stream's.  Refuses a
     tensor that a bare address would misread: of another element type than its letter in `kinds`
-    (b: bf16 or its 16 bits, i: int32, f: float32, w: 64-bit words), not contiguous, or not on
-    the current device.  Shapes are the caller's, as in C."""
+    (b: bf16 or its 16 bits, i: int32, f: float32, w: 64-bit words, e: e4m3 or its 8 bits), not contiguous,
+    or not on the current device.  Shapes are the caller's, as in C."""
     dev = _current_device()
     out = []
     for types, t in zip(_types.get(kinds) or _element_types(kinds), tensors):
@@ -370,6 +409,57 @@ def bdlm_evict_kv(desc: AttnDesc, k_pages, v_pages, page_table, lens, weights, k
     rc = load_library().bdlm_evict_kv(ctypes.byref(desc), *ptrs, int(keep), int(recent), to, tw,
                                       kp, nl, s)
     _check("bdlm_evict_kv", rc)
+
+
+def bdlm_build_tables(desc: AttnDesc, old_lens, new_lens, free_pages, n_free: int, free_from,
+                      page_table, lens_out, first, max_tokens: int, positions, slots, free_next,
+                      stream=None) -> None:
+    """free_from, positions, slots and free_next may be None."""
+    old, new, free, ff, t, lo, fi, pos, sl, fn, s = _dense(
+        "bdlm_build_tables", "iiiiiiiiii", stream, old_lens, new_lens, free_pages, free_from,
+        page_table, lens_out, first, positions, slots, free_next)
+    rc = load_library().bdlm_build_tables(ctypes.byref(desc), old, new, free, int(n_free), ff, t, lo,
+                                          fi, int(max_tokens), pos, sl, fn, s)
+    _check("bdlm_build_tables", rc)
+
+
+def bdlm_rotary_init(rot_dim: int, interleaved: bool, base: float, scaling: int = BDLM_ROTARY_NONE,
+                     factor: float = 1.0, original_len: float = 0.0, few: float = 0.0,
+                     many: float = 0.0, amplitude: float = 0.0) -> RotaryDesc:
+    r = RotaryDesc()
+    rc = load_library().bdlm_rotary_init(ctypes.byref(r), int(rot_dim), int(bool(interleaved)), float(base),
+                                         int(scaling), float(factor), float(original_len), float(few),
+                                         float(many), float(amplitude))
+    _check("bdlm_rotary_init", rc)
+    return r
+
+
+def bdlm_rotary(desc: AttnDesc, rotary: RotaryDesc, n_tokens: int, q, q_stride: int, k, k_stride: int,
+                start, positions, inverse: bool, q_out, k_out, stream=None) -> None:
+    """q and k may be slices of a wider tensor, their tokens q_stride / k_stride elements apart (0: dense);
+    start or positions may be None, and q with q_out or k with k_out."""
+    qp, kp = _rows("bdlm_rotary", q), _rows("bdlm_rotary", k)
+    st, pos, qo, ko, s = _dense("bdlm_rotary", "iibb", stream, start, positions, q_out, k_out)
+    rc = load_library().bdlm_rotary(ctypes.byref(desc), ctypes.byref(rotary), int(n_tokens), qp,
+                                    int(q_stride), kp, int(k_stride), st, pos, int(bool(inverse)), qo, ko, s)
+    _check("bdlm_rotary", rc)
+
+
+def bdlm_write_kv8(desc: AttnDesc, n_tokens: int, first, n_rows: int, k_new, v_new, k_pages, v_pages,
+                   scales, page_table, prefix_lens, stream=None) -> None:
+    """first may be None (n_rows is not used then)."""
+    f, *ptrs, s = _dense("bdlm_write_kv8", "ibbeefii", stream, first, k_new, v_new, k_pages, v_pages,
+                         scales, page_table, prefix_lens)
+    rc = load_library().bdlm_write_kv8(ctypes.byref(desc), int(n_tokens), f, int(n_rows), *ptrs, s)
+    _check("bdlm_write_kv8", rc)
+
+
+def bdlm_attention_kv8(desc: AttnDesc, q, k_pages, v_pages, scales, page_table, prefix_lens, out,
+                       stream=None) -> None:
+    ptrs = _dense("bdlm_attention_kv8", "beefiib", stream, q, k_pages, v_pages, scales, page_table,
+                  prefix_lens, out)
+    rc = load_library().bdlm_attention_kv8(ctypes.byref(desc), *ptrs)
+    _check("bdlm_attention_kv8", rc)
 
 
 def round_loop_desc(attn: AttnDesc, steps: int, H: int, V: int, rule: int, k: int,

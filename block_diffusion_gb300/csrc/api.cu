@@ -11,6 +11,7 @@
 #include "../../include/bdlm.h"
 #include "cache_ops.h"
 #include "kernels.h"
+#include "step_ops.h"
 #include "workspace.h"
 
 namespace {
@@ -933,6 +934,187 @@ int bdlm_compact_kv(const bdlm_attn_desc* desc, bdlm_bf16* k_pages, bdlm_bf16* v
                               d.B, d.Hkv, heads, d.max_pages_per_seq, d.num_pages, n_max, st->err};
   return bdlm::launch_compact(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? BDLM_OK
                                                                                   : BDLM_ERR_CUDA;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------ the cache's side of a step
+extern "C" {
+
+int bdlm_build_tables(const bdlm_attn_desc* desc, const int32_t* old_lens, const int32_t* new_lens,
+                      const int32_t* free_pages, int n_free, const int32_t* free_from,
+                      int32_t* page_table, int32_t* lens_out, int32_t* first, int max_tokens,
+                      int32_t* positions, int32_t* slots, int32_t* free_next, bdlm_stream stream) {
+  if (!desc) return BDLM_ERR_INVALID;
+  const bdlm_attn_desc d = *desc;
+  if (d.B < 0 || d.page_size != 16 || d.max_pages_per_seq < 1 || d.num_pages < 1 || n_free < 0 ||
+      max_tokens < 0 || static_cast<long long>(d.B) * d.max_pages_per_seq > 0x7FFFFFFFll)
+    return BDLM_ERR_INVALID;
+  if (too_many_tokens(d) || d.num_pages > (1 << 27)) return BDLM_ERR_UNSUPPORTED;
+  if (d.B == 0) return BDLM_OK;
+  if (!old_lens || !new_lens || (!free_pages && n_free > 0) || !page_table || !lens_out || !first)
+    return BDLM_ERR_INVALID;
+  std::lock_guard<std::mutex> lk(g_mu);
+  DeviceState* st = nullptr;
+  int rc = current_device(&st, stream);
+  if (rc) return rc;
+  if ((rc = ensure(st, st->aux, static_cast<size_t>(d.B) * sizeof(int2), false, stream))) return rc;
+  bdlm::TableParams p;
+  p.old_lens = old_lens;
+  p.new_lens = new_lens;
+  p.free_pages = free_pages;
+  p.free_from = free_from;
+  p.page_table = page_table;
+  p.lens_out = lens_out;
+  p.first = first;
+  p.positions = positions;
+  p.slots = slots;
+  p.free_next = free_next;
+  p.plan = static_cast<int2*>(st->aux.ptr);
+  p.B = d.B;
+  p.max_pages = d.max_pages_per_seq;
+  p.num_pages = d.num_pages;
+  p.n_free = n_free;
+  p.max_tokens = max_tokens;
+  p.err = st->err;
+  return bdlm::launch_build_tables(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? BDLM_OK
+                                                                                        : BDLM_ERR_CUDA;
+}
+
+int bdlm_rotary_init(bdlm_rotary_desc* rotary, int rot_dim, int interleaved, double base,
+                     int scaling, double factor, double original_len, double few, double many,
+                     double amplitude) {
+  if (!rotary || rot_dim < 16 || rot_dim > 128 || rot_dim % 16 != 0 || !(base > 1.0) || !isfinite(base) ||
+      scaling < BDLM_ROTARY_NONE || scaling > BDLM_ROTARY_YARN || !(amplitude >= 0.0) ||
+      !isfinite(amplitude))
+    return BDLM_ERR_INVALID;
+  if (scaling != BDLM_ROTARY_NONE && (!(factor >= 1.0) || !isfinite(factor))) return BDLM_ERR_INVALID;
+  const bool by_turns = scaling == BDLM_ROTARY_BANDS || scaling == BDLM_ROTARY_YARN;
+  if (by_turns && (!(original_len > 0.0) || !isfinite(original_len) || !(few > 0.0) || !(many > few) ||
+                   !isfinite(many)))
+    return BDLM_ERR_INVALID;
+  const double pi = 3.14159265358979323846;
+  if (scaling == BDLM_ROTARY_BASE) base *= pow(factor, rot_dim / (rot_dim - 2.0));
+  // YARN: the pairs where a turn count would be `many` and `few`, rounded outwards
+  const auto pair_of = [&](double turns) {
+    return rot_dim * log(original_len / (turns * 2.0 * pi)) / (2.0 * log(base));
+  };
+  double low = 0.0, high = 0.0;
+  if (scaling == BDLM_ROTARY_YARN) {
+    low = fmax(floor(pair_of(many)), 0.0);
+    high = fmin(ceil(pair_of(few)), rot_dim / 2 - 1.0);
+  }
+  *rotary = bdlm_rotary_desc{};
+  rotary->rot_dim = rot_dim;
+  rotary->interleaved = interleaved != 0;
+  rotary->amplitude = static_cast<float>(
+      amplitude > 0.0 ? amplitude : scaling == BDLM_ROTARY_YARN ? 0.1 * log(factor) + 1.0 : 1.0);
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    double f = pow(base, -2.0 * i / rot_dim);
+    if (scaling == BDLM_ROTARY_LINEAR) f /= factor;
+    if (by_turns) {
+      double keep = scaling == BDLM_ROTARY_BANDS
+                        ? (original_len * f / (2.0 * pi) - few) / (many - few)
+                        : 1.0 - (i - low) / fmax(high - low, 0.001);
+      keep = fmin(fmax(keep, 0.0), 1.0);
+      f = f * keep + f / factor * (1.0 - keep);
+    }
+    rotary->turns[i] = static_cast<uint64_t>(ldexp(f / (2.0 * pi), 64));   // f <= 1
+  }
+  return BDLM_OK;
+}
+
+int bdlm_rotary(const bdlm_attn_desc* desc, const bdlm_rotary_desc* rotary, int n_tokens,
+                const bdlm_bf16* q, long long q_stride, const bdlm_bf16* k, long long k_stride,
+                const int32_t* start, const int32_t* positions, int inverse, bdlm_bf16* q_out,
+                bdlm_bf16* k_out, bdlm_stream stream) {
+  if (!desc || !rotary) return BDLM_ERR_INVALID;
+  const bdlm_attn_desc d = *desc;
+  const long long q_row = static_cast<long long>(d.Hq) * 128, k_row = static_cast<long long>(d.Hkv) * 128;
+  if (d.B < 0 || n_tokens < 1 || d.Hq < 1 || d.Hkv < 1 || d.D != 128 || rotary->rot_dim < 16 ||
+      rotary->rot_dim > 128 || rotary->rot_dim % 16 != 0)
+    return BDLM_ERR_INVALID;
+  if (q_stride == 0) q_stride = q_row;
+  if (k_stride == 0) k_stride = k_row;
+  if (q_stride < q_row || k_stride < k_row || q_stride % 8 != 0 || k_stride % 8 != 0 ||
+      q_stride > (1ll << 40) || k_stride > (1ll << 40) || d.Hq > (1 << 24) || d.Hkv > (1 << 24) ||
+      static_cast<long long>(d.B) * n_tokens > 0x7FFFFFFFll)
+    return BDLM_ERR_INVALID;
+  if (!q != !q_out || !k != !k_out) return BDLM_ERR_INVALID;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out)) return BDLM_ERR_INVALID;
+  if ((q && q == q_out && q_stride != q_row) || (k && k == k_out && k_stride != k_row))
+    return BDLM_ERR_INVALID;
+  if (d.B == 0 || (!q && !k)) return BDLM_OK;
+  if (!start && !positions) return BDLM_ERR_INVALID;
+  std::lock_guard<std::mutex> lk(g_mu);
+  DeviceState* st = nullptr;
+  const int rc = current_device(&st, stream);
+  if (rc) return rc;
+  bdlm::RotaryParams p;
+  p.q = q;
+  p.k = k;
+  p.q_out = q_out;
+  p.k_out = k_out;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.start = start;
+  p.positions = positions;
+  p.n = n_tokens;
+  p.Hq = q ? d.Hq : 0;
+  p.Hkv = k ? d.Hkv : 0;
+  p.rows = static_cast<long long>(d.B) * n_tokens;
+  p.inverse = inverse != 0;
+  return bdlm::launch_rotary(p, *rotary, st->num_sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? BDLM_OK
+             : BDLM_ERR_CUDA;
+}
+
+int bdlm_write_kv8(const bdlm_attn_desc* desc, int n_tokens, const int32_t* first, int n_rows,
+                   const bdlm_bf16* k_new, const bdlm_bf16* v_new, bdlm_e4m3* k_pages,
+                   bdlm_e4m3* v_pages, float* scales, const int32_t* page_table,
+                   const int32_t* prefix_lens, bdlm_stream stream) {
+  if (!desc || !cache_desc_ok(*desc) || n_tokens < 1 || (first && n_rows < 0)) return BDLM_ERR_INVALID;
+  const bdlm_attn_desc d = *desc;
+  // a CTA for each page that a sequence's tokens may lie in and four heads
+  if (static_cast<long long>(d.B) * ((n_tokens + 30ll) / 16) > 0x7FFFFFFFll || d.Hkv > 4 * 65535)
+    return BDLM_ERR_INVALID;
+  if (d.B == 0) return BDLM_OK;
+  if (!k_new || !v_new || !k_pages || !v_pages || !scales || !page_table || !prefix_lens)
+    return BDLM_ERR_INVALID;
+  if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_pages) || !aligned16(v_pages) ||
+      (reinterpret_cast<uintptr_t>(scales) & 7) != 0)
+    return BDLM_ERR_INVALID;
+  std::lock_guard<std::mutex> lk(g_mu);
+  DeviceState* st = nullptr;
+  const int rc = current_device(&st, stream);
+  if (rc) return rc;
+  const bdlm::WriteKv8Params p{{k_new, v_new}, {k_pages, v_pages}, scales, first, page_table,
+                               prefix_lens, d.B, n_tokens, n_rows, d.Hkv, d.max_pages_per_seq,
+                               d.num_pages, st->err};
+  return bdlm::launch_write_kv8(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? BDLM_OK
+                                                                                     : BDLM_ERR_CUDA;
+}
+
+int bdlm_attention_kv8(const bdlm_attn_desc* desc, const bdlm_bf16* q, const bdlm_e4m3* k_pages,
+                       const bdlm_e4m3* v_pages, const float* scales, const int32_t* page_table,
+                       const int32_t* prefix_lens, bdlm_bf16* out, bdlm_stream stream) {
+  if (!desc || !attn_desc_ok(*desc)) return BDLM_ERR_INVALID;
+  const bdlm_attn_desc d = *desc;
+  if (d.B == 0) return BDLM_OK;
+  if (!q || !k_pages || !v_pages || !scales || !page_table || !prefix_lens || !out) return BDLM_ERR_INVALID;
+  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) ||
+      (reinterpret_cast<uintptr_t>(scales) & 7) != 0)
+    return BDLM_ERR_INVALID;
+  std::lock_guard<std::mutex> lk(g_mu);
+  DeviceState* st = nullptr;
+  const int rc = current_device(&st, stream);
+  if (rc) return rc;
+  const float sm_scale = d.sm_scale > 0.f ? d.sm_scale : 0.08838834764831845f;   // 1 / sqrt(128)
+  const bdlm::Kv8AttnParams p{q, k_pages, v_pages, scales, page_table, prefix_lens, out, d.B, d.L, d.Hq,
+                              d.Hkv, d.max_pages_per_seq, d.num_pages, sm_scale * 1.4426950408889634f,
+                              st->err};
+  return bdlm::launch_attention_kv8(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? BDLM_OK
+                                                                                         : BDLM_ERR_CUDA;
 }
 
 }  // extern "C"

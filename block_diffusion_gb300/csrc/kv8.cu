@@ -1,0 +1,194 @@
+// The 8-bit K/V cache, for sm_103a: writing tokens into it and block attention over it.
+//
+// K and V are held in pages of 16 tokens, [num_pages, Hkv, 16, 128] e4m3, so the block of 16 tokens of a
+// head that shares a scale is 2 KB in one piece.  scales [num_pages, Hkv, 2] holds K's and V's: a value is
+// its code times its scale.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+#include <stdint.h>
+
+#include "kernels.h"
+#include "ptx.cuh"
+#include "step_ops.h"
+
+namespace bdlm {
+namespace {
+
+constexpr int kPage = 16;
+
+// ------------------------------------------------------------------ write
+//
+// A warp writes one page of one head, of K or of V.  The scale is the least power of two 2^e, -40 <= e <= 40,
+// that takes the largest magnitude of the page's tokens to 448 (the largest e4m3) or less: dividing by it
+// is exact, so a value is rounded once, to e4m3's four bits, whatever the scale, and tokens that the page
+// held before move to another scale without rounding anew (but for those that fall below its smallest
+// step).  A finer scale would gain up to one bit of range below, not of precision.
+constexpr int kWriteWarps = 8;
+constexpr int kScaleExp = 40;
+
+// The scale's exponent for a largest magnitude (0 and up, not NaN).
+__device__ __forceinline__ int scale_exponent(float most) {
+  const uint32_t bits = __float_as_uint(most);
+  const int e = static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);   // 448 = 1.75 * 2^8
+  return min(max(e, -kScaleExp), kScaleExp);
+}
+
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t w) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w), __NV_E4M3);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+__global__ void __launch_bounds__(kWriteWarps * 32)
+write_kv8_kernel(const WriteKv8Params p, int max_touched) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int hw = blockIdx.y * kWriteWarps + (threadIdx.x >> 5);   // head and which of K, V
+  const int b = blockIdx.x / max_touched, j = blockIdx.x - b * max_touched;
+  if (hw >= 2 * p.Hkv) return;
+  const int h = hw >> 1, which = hw & 1;
+  const int prefix = p.prefix_lens[b];
+  int n = p.n;
+  long long row0 = static_cast<long long>(b) * p.n;
+  if (p.first != nullptr) {
+    row0 = p.first[b];
+    const long long end = p.first[b + 1];
+    if (row0 < 0 || end < row0 || end > p.n_rows || end - row0 > p.n) {
+      if (lane == 0 && hw == 0 && j == 0) atomicOr(p.err, BDLM_DEVERR_ROW);
+      return;
+    }
+    n = static_cast<int>(end - row0);
+  }
+  if (n == 0) return;
+  if (prefix < 0 || static_cast<long long>(prefix) + n > static_cast<long long>(p.max_pages) * kPage) {
+    if (lane == 0 && hw == 0 && j == 0) atomicOr(p.err, BDLM_DEVERR_LENGTH);
+    return;
+  }
+  const int col = prefix / kPage + j;
+  if (col > (prefix + n - 1) / kPage) return;
+  const int page = p.page_table[static_cast<size_t>(b) * p.max_pages + col];
+  if (page < 0 || page >= p.num_pages) {
+    if (lane == 0 && hw == 0) atomicOr(p.err, BDLM_DEVERR_PAGE);
+    return;
+  }
+  const size_t unit = static_cast<size_t>(page) * p.Hkv + h;
+  uint8_t* codes = p.pages[which] + unit * (kPage * 128);
+  float* scale = p.scales + unit * 2 + which;
+  const int t0 = col * kPage;                         // the page's first token
+  const int held = max(0, prefix - t0);               // tokens before the new ones: slots 0 .. held - 1
+  const int live = min(kPage, prefix + n - t0);       // slots at and past live are left as they are
+  const float was = held > 0 ? *scale : 0.f;
+  const uint16_t* x = p.x[which] + ((row0 + (t0 - prefix)) * p.Hkv + h) * 128;   // of slot 0, a new one or not
+  // lane l: 8 dims of slots 2i + l / 16
+  const int dim = (lane & 15) * 8, odd = lane >> 4;
+  float v[8][8];
+  float most = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int slot = 2 * i + odd;
+    uint4 w = make_uint4(0, 0, 0, 0);
+    if (slot >= held && slot < live)
+      w = *reinterpret_cast<const uint4*>(x + static_cast<size_t>(slot) * p.Hkv * 128 + dim);
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[i][2 * k] = bf16_lo(u[k]);
+      v[i][2 * k + 1] = bf16_hi(u[k]);
+    }
+    if (slot < held) {
+      const uint2 c = *reinterpret_cast<const uint2*>(codes + slot * 128 + dim);
+      const uint32_t cc[4] = {c.x & 0xFFFFu, c.x >> 16, c.y & 0xFFFFu, c.y >> 16};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = from_e4m3x2(cc[k]);
+        v[i][2 * k] = f.x * was;
+        v[i][2 * k + 1] = f.y * was;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) most = fmaxf(most, fabsf(v[i][k]));   // (a NaN counts as nothing)
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+  const int e = scale_exponent(most);
+  const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int slot = 2 * i + odd;
+    if (slot >= live) continue;
+    uint32_t c[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) c[k] = e4m3x2(v[i][2 * k] * inv, v[i][2 * k + 1] * inv);
+    *reinterpret_cast<uint2*>(codes + slot * 128 + dim) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+  }
+  if (lane == 0) *scale = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+}
+
+// ------------------------------------------------------------------ attention
+// A warp per query row, a lane to four dims.
+__global__ void __launch_bounds__(128)
+attention_kv8_kernel(const Kv8AttnParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);   // (b, i, h)
+  if (row >= static_cast<long long>(p.B) * p.L * p.Hq) return;
+  const int h = static_cast<int>(row % p.Hq), b = static_cast<int>(row / p.Hq / p.L), g = h / (p.Hq / p.Hkv);
+  const uint2 w = reinterpret_cast<const uint2*>(p.q + row * 128)[lane];
+  const float q0 = bf16_lo(w.x), q1 = bf16_hi(w.x), q2 = bf16_lo(w.y), q3 = bf16_hi(w.y);
+  const int prefix = p.prefix_lens[b];
+  const long long max_tok = static_cast<long long>(p.max_pages) * kPage;
+  long long n = static_cast<long long>(prefix < 0 ? 0 : prefix) + p.L;
+  if (prefix < 0 || n > max_tok) {
+    if (lane == 0) atomicOr(p.err, BDLM_DEVERR_LENGTH);
+    if (n > max_tok) n = max_tok;
+  }
+  float m = -CUDART_INF_F, l = 0.f, o0 = 0.f, o1 = 0.f, o2 = 0.f, o3 = 0.f;
+  for (long long t0 = 0; t0 < n; t0 += kPage) {
+    const int id = p.page_table[static_cast<size_t>(b) * p.max_pages + t0 / kPage];
+    const bool ok = id >= 0 && id < p.num_pages;
+    if (!ok && lane == 0) atomicOr(p.err, BDLM_DEVERR_PAGE);
+    const size_t unit = static_cast<size_t>(ok ? id : 0) * p.Hkv + g;
+    const float sk = ok ? p.scales[unit * 2] * p.scale_log2 : 0.f, sv = ok ? p.scales[unit * 2 + 1] : 0.f;
+    for (int t = 0; t < kPage && t0 + t < n; ++t) {
+      const uint32_t kc = ok ? reinterpret_cast<const uint32_t*>(p.k_pages + (unit * kPage + t) * 128)[lane] : 0u;
+      const uint32_t vc = ok ? reinterpret_cast<const uint32_t*>(p.v_pages + (unit * kPage + t) * 128)[lane] : 0u;
+      const float2 k01 = from_e4m3x2(kc & 0xFFFFu), k23 = from_e4m3x2(kc >> 16);
+      float s = q0 * k01.x + q1 * k01.y + q2 * k23.x + q3 * k23.y;
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+      s *= sk;
+      const float mn = fmaxf(m, s), a = exp2f(m - mn), e = exp2f(s - mn), ev = e * sv;
+      const float2 v01 = from_e4m3x2(vc & 0xFFFFu), v23 = from_e4m3x2(vc >> 16);
+      l = l * a + e;
+      o0 = o0 * a + ev * v01.x;
+      o1 = o1 * a + ev * v01.y;
+      o2 = o2 * a + ev * v23.x;
+      o3 = o3 * a + ev * v23.y;
+      m = mn;
+    }
+  }
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(o0 / l, o1 / l), hi = __floats2bfloat162_rn(o2 / l, o3 / l);
+  reinterpret_cast<uint2*>(p.out + row * 128)[lane] =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+}
+
+}  // namespace
+
+cudaError_t launch_write_kv8(const WriteKv8Params& p, cudaStream_t stream) {
+  const int touched = (p.n + 2 * kPage - 2) / kPage;   // pages that n tokens lie in at most
+  const dim3 grid(static_cast<unsigned>(p.B) * touched, (2 * p.Hkv + kWriteWarps - 1) / kWriteWarps);
+  return launch_pdl(write_kv8_kernel, grid, dim3(kWriteWarps * 32), 0, stream, p, touched);
+}
+
+cudaError_t launch_attention_kv8(const Kv8AttnParams& p, cudaStream_t stream) {
+  const long long rows = static_cast<long long>(p.B) * p.L * p.Hq;
+  return launch_pdl(attention_kv8_kernel, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0, stream, p);
+}
+
+}  // namespace bdlm

@@ -469,6 +469,131 @@ int bdlm_evict_kv(const bdlm_attn_desc* desc, bdlm_bf16* k_pages, bdlm_bf16* v_p
                   int32_t* new_lens, bdlm_stream stream);
 
 /*
+ * Page tables and slot maps of a step, on the device, from the requests' lengths.
+ * The pages have no counterpart; for growing sequences between steps without the host, and for the
+ * packed tokens of a batch whose sequences grow by different amounts.
+ *
+ * Sequence b holds old_lens[b] tokens in the cache and is to hold new_lens[b]: it needs
+ * ceil(new / 16) - ceil(old / 16) more pages (none where new <= old).  Pages are taken from
+ * free_pages, from entry *free_from on, in sequence order.  A sequence that needs pages is served where
+ * they suffice for it and all sequences before it; one that needs none always is; and where the packed
+ * tokens up to and with a sequence's new ones are more than max_tokens, it and all later sequences
+ * with new tokens are not.  For a sequence that is served, table columns ceil(old/16) .. ceil(new/16)-1
+ * get the new pages, lens_out[b] = new_lens[b], and its new tokens old .. new - 1 are rows
+ * first[b] .. first[b+1]-1 of the packed tokens.  One that is not keeps its pages, has no rows and
+ * lens_out[b] = old_lens[b].  Entries of the table that no new page goes to are left as they were.
+ *   old_lens, new_lens, lens_out [B] int32 (lens_out may be either of the others)
+ *   free_pages [n_free] int32 page ids, each once;  free_from one int32, or NULL for 0
+ *   free_next  one int32, or NULL: the entry after the last page taken (may be free_from)
+ *   first      [B + 1] int32
+ *   positions, slots [max_tokens] int32, or NULL: of packed row r the token's position in its
+ *              sequence and its slot, page * 16 + position % 16; -1 in rows past the last token.
+ * A token whose page id is outside [0, num_pages) has slot -1 and sets a device error bit (PAGE; the
+ * table gets the id as it is).  A length below 0 or past the page table sets LENGTH and its sequence
+ * is not served; a *free_from outside [0, n_free] sets ROW and no page is taken.  desc: B,
+ * page_size, max_pages_per_seq, num_pages; num_pages > 2^27 or max_pages_per_seq > 2^26 returns
+ * BDLM_ERR_UNSUPPORTED.  B == 0 is a no-op.
+ */
+int bdlm_build_tables(const bdlm_attn_desc* desc, const int32_t* old_lens, const int32_t* new_lens,
+                      const int32_t* free_pages, int n_free, const int32_t* free_from,
+                      int32_t* page_table, int32_t* lens_out, int32_t* first, int max_tokens,
+                      int32_t* positions, int32_t* slots, int32_t* free_next, bdlm_stream stream);
+
+/* How bdlm_rotary_init scales the frequencies for contexts longer than original_len. */
+enum {
+  BDLM_ROTARY_NONE = 0,
+  BDLM_ROTARY_LINEAR = 1,  /* f_i / factor */
+  BDLM_ROTARY_BASE = 2,    /* base * factor^(rot_dim / (rot_dim - 2)): the first pair as it was, the
+                              last one's frequency divided by factor */
+  BDLM_ROTARY_BANDS = 3,   /* by the turns t_i = original_len * f_i / 2 pi of a pair: f_i for t_i >=
+                              many, f_i / factor for t_i <= few, between them linear in t_i */
+  BDLM_ROTARY_YARN = 4     /* the same, but linear in i between the pairs, rounded outwards, where t_i
+                              would be many and few; amplitude 0.1 ln(factor) + 1 */
+};
+
+/* Frequencies of rotary positions, in host memory (filled by bdlm_rotary_init). */
+typedef struct {
+  int rot_dim, interleaved;
+  float amplitude;       /* cos and sin are multiplied by it */
+  uint64_t turns[64];    /* of pair i: f_i / (2 pi), in units of 2^-64 turns a position */
+} bdlm_rotary_desc;
+
+/*
+ * Fills *rotary (host memory; no GPU is touched) with f_i = base^(-2 i / rot_dim), i < rot_dim / 2,
+ * scaled as `scaling` says.  rot_dim: a multiple of 16, 16 .. 128; base > 1; factor >= 1 and
+ * original_len > 0 where `scaling` uses them; 0 < few < many for BANDS and YARN.  amplitude: a finite
+ * number > 0, or 0 for the one that belongs to the scaling (1, or YARN's).
+ */
+int bdlm_rotary_init(bdlm_rotary_desc* rotary, int rot_dim, int interleaved, double base,
+                     int scaling, double factor, double original_len, double few, double many,
+                     double amplitude);
+
+/*
+ * Rotary positions applied to queries and keys before they go to the cache and the attention.
+ * The pages have no counterpart (the attention takes q and K with their positions applied).
+ *
+ * Token i of sequence b is at position p = positions[b, i], or start[b] + i where positions is NULL.
+ * In each head, pair j < rot_dim / 2 is elements (j, j + rot_dim/2), or (2j, 2j + 1) with `interleaved`:
+ *     (x, y) -> amplitude * (x cos a - y sin a, x sin a + y cos a),   a = p * f_j;
+ * elements rot_dim .. 127 are copied.  `inverse` turns by -a instead, which is the gradient's way back
+ * through the call (and, with an amplitude of 1, undoes it).  Angles are exact to 2^-32 of a turn at any
+ * position, products are float32, results are rounded once to bf16.
+ *   q, k           [B, n_tokens, Hq / Hkv, D] bf16, 16-byte aligned; a token's heads side by side, the next
+ *                  token q_stride / k_stride elements on (multiples of 8; 0: Hq * D / Hkv * D)
+ *   positions      [B, n_tokens] int32, or NULL;  start [B] int32, read where positions is NULL
+ *   q_out, k_out   [B, n_tokens, Hq / Hkv, D] bf16, 16-byte aligned; q (k) itself where its stride is
+ *                  that of q_out (k_out), else apart from it
+ * q and q_out, or k and k_out, may both be NULL.  Rows of a position below 0 (padding; all of a sequence
+ * whose start is below 0) are left as they were.  desc: B, Hq, Hkv, D.
+ */
+int bdlm_rotary(const bdlm_attn_desc* desc, const bdlm_rotary_desc* rotary, int n_tokens,
+                const bdlm_bf16* q, long long q_stride, const bdlm_bf16* k, long long k_stride,
+                const int32_t* start, const int32_t* positions, int inverse, bdlm_bf16* q_out,
+                bdlm_bf16* k_out, bdlm_stream stream);
+
+/*
+ * The 8-bit cache.  K and V in pages of 16 tokens, head by head,
+ *     k_pages, v_pages [num_pages, Hkv, 16, D] e4m3 codes (16-byte aligned),
+ *     scales           [num_pages, Hkv, 2] float: of the page's K, of its V,
+ * a value being its code times its page's scale.  (A page and head are 2 KB in one piece, unlike in the
+ * bf16 pools: they are written and scaled as one, and read as one.)  Page tables as elsewhere.
+ */
+typedef uint8_t bdlm_e4m3;   /* raw e4m3 bits (no infinities; 0x7F and 0xFF are NaN) */
+
+/*
+ * Writes tokens into the 8-bit cache: a block, or prompts of equal or different lengths.
+ * Counterpart of bdlm_write_block_kv for the 8-bit cache.
+ *
+ * n new tokens of sequence b go to positions prefix_lens[b] .. prefix_lens[b] + n - 1.  first NULL:
+ * n = n_tokens, from rows b * n_tokens on of k_new and v_new; else n = first[b+1] - first[b] <=
+ * n_tokens, from row first[b] on.  Of every page that gets new tokens, K's and V's scale become each the
+ * least power of two 2^e, -40 <= e <= 40, with max |x| <= 448 * 2^e over the page's tokens, old and new
+ * (NaN aside; 2^-40 where all are zero); the codes are the values over it rounded to nearest even,
+ * at most +-448.  Tokens before prefix_lens[b] in the first such page are held anew in its new scale
+ * (exactly, where the old one was a power of two and no value falls below the smallest step); slots behind
+ * the last new token are left as they were.  A page that gets new tokens belongs to one sequence.
+ *   k_new, v_new  [B * n_tokens, or n_rows, Hkv, D] bf16 (16-byte aligned)
+ *   first         [B + 1] int32, or NULL (n_rows is not used then)
+ * A bad page id or a length that does not fit the page table skips what it concerns and sets a device
+ * error bit; entries of `first` that decrease, differ by more than n_tokens or lie outside
+ * [0, n_rows] skip the sequence and set ROW.  desc: B, Hkv, D, page_size, max_pages_per_seq, num_pages.
+ */
+int bdlm_write_kv8(const bdlm_attn_desc* desc, int n_tokens, const int32_t* first, int n_rows,
+                   const bdlm_bf16* k_new, const bdlm_bf16* v_new, bdlm_e4m3* k_pages,
+                   bdlm_e4m3* v_pages, float* scales, const int32_t* page_table,
+                   const int32_t* prefix_lens, bdlm_stream stream);
+
+/*
+ * Block attention over the 8-bit cache: bdlm_block_attention with K and V as bdlm_write_kv8 holds
+ * them.  L = 1 is single-token decoding.  Scales outside [2^-40, 2^40] count as the nearest of the two, NaN
+ * as 2^-40; any others are taken as they are, powers of two or not.  A page with a bad id reads as zeros.  q, out
+ * [B, L, Hq, D] bf16 (16-byte aligned) and all else as bdlm_block_attention.
+ */
+int bdlm_attention_kv8(const bdlm_attn_desc* desc, const bdlm_bf16* q, const bdlm_e4m3* k_pages,
+                       const bdlm_e4m3* v_pages, const float* scales, const int32_t* page_table,
+                       const int32_t* prefix_lens, bdlm_bf16* out, bdlm_stream stream);
+
+/*
  * A whole block's denoising on the device: rounds repeat inside one CUDA graph, with a
  * conditional WHILE node, until no position of any block is masked or `steps` rounds have
  * run; the host only launches the graph.
