@@ -152,14 +152,14 @@ int get_encoder() {
   return BDLM_OK;
 }
 
-// bf16 tensor map, 128-byte swizzle; dims/strides innermost first, strides in bytes.
+// bf16 (or other) tensor map, 128-byte swizzle; dims/strides innermost first, strides in bytes.
 int encode(CUtensorMap* tm, const void* base, int rank, const cuuint64_t* dims,
-           const cuuint64_t* strides, const cuuint32_t* box) {
+           const cuuint64_t* strides, const cuuint32_t* box,
+           CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16) {
   cuuint32_t es[5] = {1, 1, 1, 1, 1};
-  CUresult r = g_encode(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base),
-                        dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  CUresult r = g_encode(tm, type, rank, const_cast<void*>(base), dims, strides, box, es,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? BDLM_OK : BDLM_ERR_INVALID;
 }
 
@@ -1100,6 +1100,7 @@ int bdlm_attention_kv8(const bdlm_attn_desc* desc, const bdlm_bf16* q, const bdl
                        const int32_t* prefix_lens, bdlm_bf16* out, bdlm_stream stream) {
   if (!desc || !attn_desc_ok(*desc)) return BDLM_ERR_INVALID;
   const bdlm_attn_desc d = *desc;
+  if (too_many_tokens(d) || static_cast<long long>(d.num_pages) * d.Hkv >= (1 << 30)) return BDLM_ERR_UNSUPPORTED;
   if (d.B == 0) return BDLM_OK;
   if (!q || !k_pages || !v_pages || !scales || !page_table || !prefix_lens || !out) return BDLM_ERR_INVALID;
   if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) ||
@@ -1107,14 +1108,27 @@ int bdlm_attention_kv8(const bdlm_attn_desc* desc, const bdlm_bf16* q, const bdl
     return BDLM_ERR_INVALID;
   std::lock_guard<std::mutex> lk(g_mu);
   DeviceState* st = nullptr;
-  const int rc = current_device(&st, stream);
+  int rc = current_device(&st, stream);
   if (rc) return rc;
-  const float sm_scale = d.sm_scale > 0.f ? d.sm_scale : 0.08838834764831845f;   // 1 / sqrt(128)
-  const bdlm::Kv8AttnParams p{q, k_pages, v_pages, scales, page_table, prefix_lens, out, d.B, d.L, d.Hq,
-                              d.Hkv, d.max_pages_per_seq, d.num_pages, sm_scale * 1.4426950408889634f,
-                              st->err};
-  return bdlm::launch_attention_kv8(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? BDLM_OK
-                                                                                         : BDLM_ERR_CUDA;
+  if ((rc = get_encoder())) return rc;
+  const bdlm::Kv8AttnPlan plan =
+      bdlm::plan_attention_kv8(d.B, d.L, d.Hq, d.Hkv, d.max_pages_per_seq, st->num_sms);
+  if ((rc = ensure(st, st->attn_cnt, 2 * sizeof(int), true, stream))) return rc;
+  if ((rc = ensure(st, st->data, plan.bytes, false, stream))) return rc;
+  // a page and head are 16 rows of 128 bytes
+  CUtensorMap tm_k, tm_v;
+  const cuuint64_t dims[3] = {128, 16, static_cast<cuuint64_t>(d.num_pages) * d.Hkv};
+  const cuuint64_t strides[2] = {128, 2048};
+  const cuuint32_t box[3] = {128, 16, 1};
+  if ((rc = encode(&tm_k, k_pages, 3, dims, strides, box, CU_TENSOR_MAP_DATA_TYPE_UINT8))) return rc;
+  if ((rc = encode(&tm_v, v_pages, 3, dims, strides, box, CU_TENSOR_MAP_DATA_TYPE_UINT8))) return rc;
+  const float sm_scale = d.sm_scale > 0.f ? d.sm_scale : 1.0f / sqrtf(128.0f);
+  const bdlm::Kv8AttnParams p{q, scales, page_table, prefix_lens, out, d.B, d.L, d.Hq, d.Hkv,
+                              d.max_pages_per_seq, d.num_pages, sm_scale * 1.4426950408889634f, st->err};
+  return bdlm::launch_attention_kv8(p, plan, tm_k, tm_v, st->data.ptr, static_cast<int*>(st->attn_cnt.ptr),
+                                    static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? BDLM_OK
+             : BDLM_ERR_CUDA;
 }
 
 }  // extern "C"

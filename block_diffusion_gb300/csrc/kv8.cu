@@ -1,4 +1,4 @@
-// The 8-bit K/V cache, for sm_103a: writing tokens into it and block attention over it.
+// The 8-bit K/V cache, for sm_103a: writing tokens into it.
 //
 // K and V are held in pages of 16 tokens, [num_pages, Hkv, 16, 128] e4m3, so the block of 16 tokens of a
 // head that shares a scale is 2 KB in one piece.  scales [num_pages, Hkv, 2] holds K's and V's: a value is
@@ -129,66 +129,12 @@ write_kv8_kernel(const WriteKv8Params p, int max_touched) {
   if (lane == 0) *scale = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 }
 
-// ------------------------------------------------------------------ attention
-// A warp per query row, a lane to four dims.
-__global__ void __launch_bounds__(128)
-attention_kv8_kernel(const Kv8AttnParams p) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);   // (b, i, h)
-  if (row >= static_cast<long long>(p.B) * p.L * p.Hq) return;
-  const int h = static_cast<int>(row % p.Hq), b = static_cast<int>(row / p.Hq / p.L), g = h / (p.Hq / p.Hkv);
-  const uint2 w = reinterpret_cast<const uint2*>(p.q + row * 128)[lane];
-  const float q0 = bf16_lo(w.x), q1 = bf16_hi(w.x), q2 = bf16_lo(w.y), q3 = bf16_hi(w.y);
-  const int prefix = p.prefix_lens[b];
-  const long long max_tok = static_cast<long long>(p.max_pages) * kPage;
-  long long n = static_cast<long long>(prefix < 0 ? 0 : prefix) + p.L;
-  if (prefix < 0 || n > max_tok) {
-    if (lane == 0) atomicOr(p.err, BDLM_DEVERR_LENGTH);
-    if (n > max_tok) n = max_tok;
-  }
-  float m = -CUDART_INF_F, l = 0.f, o0 = 0.f, o1 = 0.f, o2 = 0.f, o3 = 0.f;
-  for (long long t0 = 0; t0 < n; t0 += kPage) {
-    const int id = p.page_table[static_cast<size_t>(b) * p.max_pages + t0 / kPage];
-    const bool ok = id >= 0 && id < p.num_pages;
-    if (!ok && lane == 0) atomicOr(p.err, BDLM_DEVERR_PAGE);
-    const size_t unit = static_cast<size_t>(ok ? id : 0) * p.Hkv + g;
-    const float sk = ok ? p.scales[unit * 2] * p.scale_log2 : 0.f, sv = ok ? p.scales[unit * 2 + 1] : 0.f;
-    for (int t = 0; t < kPage && t0 + t < n; ++t) {
-      const uint32_t kc = ok ? reinterpret_cast<const uint32_t*>(p.k_pages + (unit * kPage + t) * 128)[lane] : 0u;
-      const uint32_t vc = ok ? reinterpret_cast<const uint32_t*>(p.v_pages + (unit * kPage + t) * 128)[lane] : 0u;
-      const float2 k01 = from_e4m3x2(kc & 0xFFFFu), k23 = from_e4m3x2(kc >> 16);
-      float s = q0 * k01.x + q1 * k01.y + q2 * k23.x + q3 * k23.y;
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-      s *= sk;
-      const float mn = fmaxf(m, s), a = exp2f(m - mn), e = exp2f(s - mn), ev = e * sv;
-      const float2 v01 = from_e4m3x2(vc & 0xFFFFu), v23 = from_e4m3x2(vc >> 16);
-      l = l * a + e;
-      o0 = o0 * a + ev * v01.x;
-      o1 = o1 * a + ev * v01.y;
-      o2 = o2 * a + ev * v23.x;
-      o3 = o3 * a + ev * v23.y;
-      m = mn;
-    }
-  }
-  const __nv_bfloat162 lo = __floats2bfloat162_rn(o0 / l, o1 / l), hi = __floats2bfloat162_rn(o2 / l, o3 / l);
-  reinterpret_cast<uint2*>(p.out + row * 128)[lane] =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-}
-
 }  // namespace
 
 cudaError_t launch_write_kv8(const WriteKv8Params& p, cudaStream_t stream) {
   const int touched = (p.n + 2 * kPage - 2) / kPage;   // pages that n tokens lie in at most
   const dim3 grid(static_cast<unsigned>(p.B) * touched, (2 * p.Hkv + kWriteWarps - 1) / kWriteWarps);
   return launch_pdl(write_kv8_kernel, grid, dim3(kWriteWarps * 32), 0, stream, p, touched);
-}
-
-cudaError_t launch_attention_kv8(const Kv8AttnParams& p, cudaStream_t stream) {
-  const long long rows = static_cast<long long>(p.B) * p.L * p.Hq;
-  return launch_pdl(attention_kv8_kernel, dim3(static_cast<unsigned>((rows + 3) / 4)), dim3(128), 0, stream, p);
 }
 
 }  // namespace bdlm

@@ -1,5 +1,5 @@
 // Internal interface of the operators on the cache's side of a step: page tables and slot maps, rotary
-// positions (positions.cu), the 8-bit cache's writes and the attention over it (kv8.cu).
+// positions (positions.cu), the 8-bit cache's writes (kv8.cu) and the attention over it (kv8_attention.cu).
 #pragma once
 
 #include "kernels.h"
@@ -51,10 +51,9 @@ struct WriteKv8Params {
 };
 cudaError_t launch_write_kv8(const WriteKv8Params& p, cudaStream_t stream);
 
+// ------------------------------------------------------------------ kv8_attention.cu
 struct Kv8AttnParams {
   const uint16_t* q;
-  const uint8_t* k_pages;
-  const uint8_t* v_pages;
   const float* scales;
   const int32_t* page_table;
   const int32_t* prefix_lens;
@@ -63,6 +62,16 @@ struct Kv8AttnParams {
   float scale_log2;
   int* err;
 };
-cudaError_t launch_attention_kv8(const Kv8AttnParams& p, cudaStream_t stream);
+struct Kv8AttnPlan {
+  int lsub, row_groups, rows;   // block positions and query rows of a row group
+  int n_rows;                   // rows padded
+  int grid;
+  long long parts;
+  size_t part_bytes, cum_offset, bytes;   // of the workspace
+};
+Kv8AttnPlan plan_attention_kv8(int B, int L, int Hq, int Hkv, int max_pages, int num_sms);
+// The maps: units of 16 x 128 bytes, boxes of one.  data: plan.bytes; work: two ints, zero between calls.
+cudaError_t launch_attention_kv8(const Kv8AttnParams& p, const Kv8AttnPlan& plan, const CUtensorMap& tm_k,
+                                 const CUtensorMap& tm_v, void* data, int* work, cudaStream_t stream);
 
 }  // namespace bdlm

@@ -587,7 +587,8 @@ int bdlm_write_kv8(const bdlm_attn_desc* desc, int n_tokens, const int32_t* firs
  * Block attention over the 8-bit cache: bdlm_block_attention with K and V as bdlm_write_kv8 holds
  * them.  L = 1 is single-token decoding.  Scales outside [2^-40, 2^40] count as the nearest of the two, NaN
  * as 2^-40; any others are taken as they are, powers of two or not.  A page with a bad id reads as zeros.  q, out
- * [B, L, Hq, D] bf16 (16-byte aligned) and all else as bdlm_block_attention.
+ * [B, L, Hq, D] bf16 (16-byte aligned), q finite, and all else as bdlm_block_attention.  num_pages * Hkv >=
+ * 2^30 or max_pages_per_seq > 2^26 returns BDLM_ERR_UNSUPPORTED.
  */
 int bdlm_attention_kv8(const bdlm_attn_desc* desc, const bdlm_bf16* q, const bdlm_e4m3* k_pages,
                        const bdlm_e4m3* v_pages, const float* scales, const int32_t* page_table,
