@@ -1116,16 +1116,24 @@ int bdlm_attention_kv8(const bdlm_attn_desc* desc, const bdlm_bf16* q, const bdl
   if ((rc = ensure(st, st->attn_cnt, 2 * sizeof(int), true, stream))) return rc;
   if ((rc = ensure(st, st->data, plan.bytes, false, stream))) return rc;
   // a page and head are 16 rows of 128 bytes
-  CUtensorMap tm_k, tm_v;
+  CUtensorMap tm_q = {}, tm_k, tm_v;
   const cuuint64_t dims[3] = {128, 16, static_cast<cuuint64_t>(d.num_pages) * d.Hkv};
   const cuuint64_t strides[2] = {128, 2048};
   const cuuint32_t box[3] = {128, 16, 1};
   if ((rc = encode(&tm_k, k_pages, 3, dims, strides, box, CU_TENSOR_MAP_DATA_TYPE_UINT8))) return rc;
   if ((rc = encode(&tm_v, v_pages, 3, dims, strides, box, CU_TENSOR_MAP_DATA_TYPE_UINT8))) return rc;
+  if (plan.n_rows >= 128) {
+    const cuuint64_t qdims[3] = {256, static_cast<cuuint64_t>(d.Hq), static_cast<cuuint64_t>(d.B) * d.L};
+    const cuuint64_t qstrides[2] = {256, static_cast<cuuint64_t>(d.Hq) * 256};
+    const cuuint32_t qbox[3] = {128, static_cast<cuuint32_t>(d.Hq / d.Hkv), static_cast<cuuint32_t>(plan.lsub)};
+    if ((rc = encode(&tm_q, static_cast<char*>(st->data.ptr) + plan.q_offset, 3, qdims, qstrides, qbox,
+                     CU_TENSOR_MAP_DATA_TYPE_UINT8)))
+      return rc;
+  }
   const float sm_scale = d.sm_scale > 0.f ? d.sm_scale : 1.0f / sqrtf(128.0f);
   const bdlm::Kv8AttnParams p{q, scales, page_table, prefix_lens, out, d.B, d.L, d.Hq, d.Hkv,
                               d.max_pages_per_seq, d.num_pages, sm_scale * 1.4426950408889634f, st->err};
-  return bdlm::launch_attention_kv8(p, plan, tm_k, tm_v, st->data.ptr, static_cast<int*>(st->attn_cnt.ptr),
+  return bdlm::launch_attention_kv8(p, plan, tm_q, tm_k, tm_v, st->data.ptr, static_cast<int*>(st->attn_cnt.ptr),
                                     static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? BDLM_OK
              : BDLM_ERR_CUDA;

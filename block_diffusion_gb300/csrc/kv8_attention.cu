@@ -25,6 +25,7 @@
 #include <math_constants.h>
 #include <stdint.h>
 
+#include "attention_common.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
 #include "step_ops.h"
@@ -32,14 +33,12 @@
 namespace bdlm {
 namespace {
 
-constexpr int kPage = 16;
-constexpr int kTile = 128;             // tokens of a tile (UMMA M)
 constexpr int kTilePages = kTile / kPage;
 constexpr int kStage = kTile * 128;    // bytes of a tile's K or V
 constexpr int kRing = 4;               // chunk descriptors in flight
 constexpr float kWeightExp = 7.0f;     // a query's largest weight is 2^7 ...
 constexpr float kLazy = 1.5f;          // ... to 2^8.5: a running maximum moves only when it rises by more (e4m3 ends at 448)
-constexpr float kScaleLog = 40.0f;     // scales count as 2^-40 .. 2^40
+constexpr float kLazyMany = 8.0f;      // the same where weights are float16: 1 to 2^8
 
 struct Params {
   const uint16_t* q;
@@ -51,7 +50,9 @@ struct Params {
   int* err;
   int* work;         // [0] next unit, [1] CTAs finished
   const int* cum;    // [B + 1] tiles of the sequences before each (null: up to 32 sequences)
+  const float* q_scale;   // many rows: 2^e of each row group's queries
   int B, L, Hq, Hkv, G, max_pages, num_pages, lsub, row_groups, rows;
+  int rounds;        // of units, where a CTA's share is long
   float scale_log2;
 };
 
@@ -66,11 +67,6 @@ struct Chunk {
   float q_scale;     // q = (hi + lo) * q_scale, times c
 };
 
-__device__ __forceinline__ void mbar_wait_drain(uint64_t* bar, uint32_t parity) {
-  int dummy = 0;
-  mbar_wait(bar, parity, &dummy);
-}
-
 __device__ __forceinline__ int kv_tokens(const Params& p, int b, bool* ok) {
   const int prefix = __ldg(p.prefix_lens + b);
   const long long max_tok = static_cast<long long>(p.max_pages) * kPage;
@@ -83,10 +79,10 @@ __device__ __forceinline__ int kv_tokens(const Params& p, int b, bool* ok) {
 // enough that CTAs' different speeds count for more than a unit's start and end.
 constexpr int kRounds = 4;
 constexpr int kRoundTiles = 32;   // tiles of a share from which on there are kRounds rounds
-__host__ __device__ __forceinline__ long long unit_tiles(long long total, int ctas) {
+__device__ __forceinline__ long long unit_tiles(long long total, int ctas, int rounds) {
   const long long share = (total + ctas - 1) / ctas;
   if (share < kRoundTiles) return share < 1 ? 1 : share;
-  return (total + static_cast<long long>(kRounds) * ctas - 1) / (static_cast<long long>(kRounds) * ctas);
+  return (total + static_cast<long long>(rounds) * ctas - 1) / (static_cast<long long>(rounds) * ctas);
 }
 
 __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
@@ -120,11 +116,10 @@ __device__ __forceinline__ int q_exponent(float most) {
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
-// Maximum over the warp in one instruction (redux.sync of float32, sm_100 family).
-__device__ __forceinline__ float warp_max(float x) {
-  float y;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
-  return y;
+// A page's sK and log2 sV, as the softmax takes them (NaN counts as the smallest).
+__device__ __forceinline__ float2 page_scale(float2 s) {
+  constexpr float kLeast = 9.094947017729282e-13f, kMost = 1099511627776.f;   // 2^-40, 2^40
+  return make_float2(fminf(fmaxf(s.x, kLeast), kMost), __log2f(fminf(fmaxf(s.y, kLeast), kMost)));
 }
 
 // The walk over a CTA's units, list by list, in chunks of up to CHUNK tiles (whole warp, uniform).
@@ -156,7 +151,7 @@ struct Walk {
       sum = __ldg(p.cum + p.B);
     }
     total = sum * lists;
-    per = unit_tiles(total, gridDim.x);
+    per = unit_tiles(total, gridDim.x, p.rounds);
     units = static_cast<int>((total + per - 1) / per);
     counted = units > static_cast<int>(gridDim.x);
     unit = -1;
@@ -251,7 +246,6 @@ constexpr int kPartRow = 130;   // floats of a row's part: O, m, l
 // MMAs; warps 2-5, a token (of S^T) or head dim (of O^T) a thread, do the softmax.  A chunk of tiles whose
 // S^T fit tensor memory is taken at once: the maxima over all of it, then its weights tile by tile.  S^T
 // is double-buffered and K of chunk u + 1 streams ahead of V of chunk u.
-constexpr int kSoftmaxThreads = 128;
 
 template <int N, int STAGES>
 struct Few {
@@ -382,9 +376,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 #pragma unroll
         for (int i = 0; i < (F::kChunkPages + 31) / 32; ++i) {
           const int q = i * 32 + lane;
-          // (NaN counts as the smallest)
-          const float lim = exp2f(kScaleLog), k = fminf(fmaxf(sc[i].x, 1.f / lim), lim);
-          if (q < F::kChunkPages) s_scale[rs][q] = make_float2(k, fminf(fmaxf(__log2f(fmaxf(sc[i].y, 1.f / lim)), -kScaleLog), kScaleLog));
+          if (q < F::kChunkPages) s_scale[rs][q] = page_scale(sc[i]);
         }
       }
       __syncwarp();
@@ -765,6 +757,628 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
   if (threadIdx.x == 0 && abort_flag) atomicOr(p.err, BDLM_DEVERR_TIMEOUT);
 }
 
+// ------------------------------------------------------------------ more query rows per KV head
+//
+// S = Q K^T and O += W V with 128 query rows on M, a row a tensor-memory lane, up to two groups of 128
+// that share every tile.  Here two parts of w would cost the softmax more than all else it does (three
+// instructions a weight), so V is widened instead, once for all rows: converter warps turn a tile's codes
+// into float16 (exactly) in shared memory, w is one float16 (written over S, the A operand in tensor
+// memory) and the second product is kind::f16.  The first takes K's codes as they are and Q's two parts,
+// which a small kernel makes beforehand.  Softmax: two threads a row, 64 tokens each; a page's scales are
+// the same for 16 of them, so the maximum is taken of raw scores page by page.
+template <int SUB>
+struct Many {
+  static constexpr int kRowsItem = 128 * SUB;
+  static constexpr int kStages = SUB == 2 ? 2 : 3;      // of K, and of V
+  static constexpr int kSoftmaxWarps = 8 * SUB;
+  static constexpr int kConvWarps = SUB == 2 ? 2 : 4;
+  static constexpr int kThreads = 64 + 32 * (kSoftmaxWarps + kConvWarps);
+  static constexpr int kChunk = 8;                      // tiles of a descriptor
+  static constexpr int kWide = 2 * kStage;              // a tile's V in float16
+  static constexpr size_t kSmem = 1024 + kRowsItem * 256 + 2 * kStages * kStage + 2 * kWide;
+};
+
+__device__ __forceinline__ uint32_t half2_bits(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t widen2(uint32_t two_codes) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two_codes), __NV_E4M3);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Largest of 16 scores (those at and past nvalid aside).
+__device__ __forceinline__ float max16(const uint32_t* r, int nvalid) {
+  float v[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) v[k] = k < nvalid ? __uint_as_float(r[k]) : -CUDART_INF_F;
+  const float a = fmax3(v[0], v[1], v[2]), b = fmax3(v[3], v[4], v[5]), c = fmax3(v[6], v[7], v[8]);
+  const float d = fmax3(v[9], v[10], v[11]), e = fmax3(v[12], v[13], v[14]);
+  return fmax3(fmax3(a, b, c), fmax3(d, e, v[15]), -CUDART_INF_F);
+}
+
+template <int SUB>
+__global__ void __launch_bounds__(Many<SUB>::kThreads, 1)
+many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                 const __grid_constant__ CUtensorMap tm_v, const Params p) {
+  using F = Many<SUB>;
+  constexpr int STAGES = F::kStages, kRowsItem = F::kRowsItem, kChunk = F::kChunk;
+  constexpr int kChunkPages = kChunk * kTilePages;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint8_t* sQ = base;                       // two parts x kRowsItem rows x 128 bytes
+  uint8_t* sK = sQ + kRowsItem * 256;
+  uint8_t* sV = sK + STAGES * kStage;
+  uint8_t* sW = sV + STAGES * kStage;       // two buffers of V in float16: two halves of 64 dims x 128 tokens
+  __shared__ uint64_t bar_qfull, bar_qempty, bar_kfull[STAGES], bar_kempty[STAGES], bar_vfull[STAGES], bar_vempty[STAGES];
+  __shared__ uint64_t bar_wfull[2], bar_wempty[2], bar_sfull[2], bar_pfull[2], bar_ofull[2], bar_done;
+  __shared__ uint64_t bar_cfull[kRing], bar_cempty[kRing], bar_pair[4 * SUB][2], bar_pair_end[4 * SUB];
+  __shared__ Chunk s_chunk[kRing];
+  __shared__ float2 s_scale[kRing][kChunkPages];
+  __shared__ int s_page[3][kChunkPages];
+  __shared__ uint32_t tmem_base;
+  __shared__ int abort_flag;
+  __shared__ __align__(16) uint8_t s_stage[F::kSoftmaxWarps][1024];
+  __shared__ float s_hmax[2][SUB][2][128], s_hsum[2][SUB][2][128];
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    mbar_init(&bar_qfull, 1);
+    mbar_init(&bar_qempty, 1);
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&bar_kfull[s], 1);
+      mbar_init(&bar_kempty[s], 1);
+      mbar_init(&bar_vfull[s], 1);
+      mbar_init(&bar_vempty[s], F::kConvWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar_wfull[i], F::kConvWarps);
+      mbar_init(&bar_wempty[i], 1);
+      mbar_init(&bar_sfull[i], 1);
+      mbar_init(&bar_pfull[i], 256);
+      mbar_init(&bar_ofull[i], 1);
+    }
+    mbar_init(&bar_done, 1);
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&bar_cfull[i], 1);
+      mbar_init(&bar_cempty[i], 1 + F::kConvWarps + F::kSoftmaxWarps);
+    }
+    for (int i = 0; i < 4 * SUB; ++i) {
+      mbar_init(&bar_pair[i][0], 64);
+      mbar_init(&bar_pair[i][1], 64);
+      mbar_init(&bar_pair_end[i], 64);
+    }
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&tmem_base, 512);
+    tmem_relinquish();
+  }
+  // rows that no query fills read as zeros
+  for (int o = threadIdx.x * 16; o < (kRowsItem - p.rows) * 128; o += F::kThreads * 16) {
+    *reinterpret_cast<uint4*>(sQ + p.rows * 128 + o) = make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4*>(sQ + kRowsItem * 128 + p.rows * 128 + o) = make_uint4(0, 0, 0, 0);
+  }
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  griddep_wait();
+  const uint32_t tmem = tmem_base;
+  const uint32_t tO = tmem + 256;   // S: two buffers, or one of each group
+
+  if (warp == 0) {
+    // =================================================================== producer
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_q);
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+    }
+    const uint64_t policy = l2_policy_evict_first();
+    const int absent = p.num_pages * p.Hkv;
+    int my_cum = 0, kst = 0, vst = 0, q_loads = 0, seq = -1;
+    uint32_t kph = 0, vph = 0;
+    bool ok = true;
+    Walk<kChunk> walk;
+    walk.init(p, lane, my_cum);
+    auto prepare = [&](Chunk& c) -> bool {
+      const bool have = walk.next(p, lane, my_cum, c);
+      ++seq;
+      const int rs = seq % kRing;
+      float2 sc[kChunkPages / 32];
+      if (have) {
+        int* page = s_page[seq % 3];
+        const int at = c.t0 / kPage, n = min(c.n_tiles * kTilePages, (c.t_end - c.t0 + kPage - 1) / kPage);
+        int bad = 0;
+#pragma unroll
+        for (int i = 0; i < kChunkPages / 32; ++i) {
+          const int q = i * 32 + lane;
+          int id = q < n ? __ldg(p.page_table + static_cast<size_t>(c.b) * p.max_pages + at + q) : -1;
+          if (id < 0 || id >= p.num_pages) {
+            bad |= q < n;
+            id = -1;
+          }
+          const int unit = id * p.Hkv + c.kvh;
+          sc[i] = id >= 0 ? __ldg(p.scales + unit) : make_float2(0.f, 0.f);
+          page[q] = id >= 0 ? unit : absent;
+        }
+        c.q_scale = __ldg(p.q_scale + (static_cast<size_t>(c.b) * p.Hkv + c.kvh) * p.row_groups + c.rg) * p.scale_log2;
+        if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.err, BDLM_DEVERR_PAGE);
+      }
+      if (ok) ok = mbar_wait_warp<true>(&bar_cempty[rs], ((seq / kRing) & 1) ^ 1, &abort_flag);
+      if (have) {
+#pragma unroll
+        for (int i = 0; i < kChunkPages / 32; ++i) s_scale[rs][i * 32 + lane] = page_scale(sc[i]);
+      }
+      __syncwarp();
+      if (lane == 0) {
+        if (have) {
+          s_chunk[rs] = c;
+        } else {
+          s_chunk[rs].end = 1;
+        }
+        mbar_arrive(&bar_cfull[rs]);
+      }
+      return have;
+    };
+    auto load_q = [&](const Chunk& c) {
+      if (lane == 0) {
+        if (ok) ok = mbar_wait<true>(&bar_qempty, (q_loads & 1) ^ 1, &abort_flag);
+        if (ok) {
+          mbar_arrive_expect_tx(&bar_qfull, 256u * static_cast<uint32_t>(p.rows));
+          for (int h = 0; h < 2; ++h)
+            tma_load_3d(sQ + h * kRowsItem * 128, &tm_q, &bar_qfull, h * 128, c.kvh * p.G, c.b * p.L + c.rg * p.lsub);
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      ++q_loads;
+    };
+    auto copy = [&](const CUtensorMap* tm, uint8_t* ring, uint64_t* full, uint64_t* empty, int& st, uint32_t& ph, int page) {
+      if (lane == 0) {
+        ok = mbar_wait<true>(&empty[st], ph ^ 1, &abort_flag);
+        if (ok) mbar_arrive_expect_tx(&full[st], kStage);
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) return;
+      if (lane < kTilePages) tma_load_3d_hint(ring + st * kStage + lane * 2048, tm, &full[st], 0, 0, page, policy);
+      if (++st == STAGES) {
+        st = 0;
+        ph ^= 1;
+      }
+    };
+    Chunk cur, nxt;
+    bool have = prepare(cur), have_next = false;
+    int cs = 0;
+    if (have) {
+      load_q(cur);
+      copy(&tm_k, sK, bar_kfull, bar_kempty, kst, kph, s_page[0][lane & 7]);
+      have_next = prepare(nxt);
+    }
+    while (have && ok) {
+      for (int j = 0; j < cur.n_tiles && ok; ++j) {
+        // K of the next tile, then V of this one
+        if (j + 1 < cur.n_tiles) {
+          copy(&tm_k, sK, bar_kfull, bar_kempty, kst, kph, s_page[cs % 3][(j + 1) * kTilePages + (lane & 7)]);
+        } else if (have_next) {
+          if (nxt.first) load_q(nxt);
+          if (ok) copy(&tm_k, sK, bar_kfull, bar_kempty, kst, kph, s_page[(cs + 1) % 3][lane & 7]);
+        }
+        if (ok) copy(&tm_v, sV, bar_vfull, bar_vempty, vst, vph, s_page[cs % 3][j * kTilePages + (lane & 7)]);
+      }
+      cur = nxt;
+      have = have_next;
+      ++cs;
+      if (have && ok) have_next = prepare(nxt);
+    }
+    if (lane == 0) {
+      griddep_launch_dependents();
+      if (walk.counted) {
+        __threadfence();
+        if (atomicAdd(p.work + 1, 1) == static_cast<int>(gridDim.x) - 1) {
+          p.work[0] = 0;
+          p.work[1] = 0;
+        }
+      }
+      if (!ok) {
+        for (int s = 0; s < STAGES; ++s) {
+          mbar_wait_drain(&bar_kfull[s], kph ^ (s < kst ? 0 : 1));
+          mbar_wait_drain(&bar_vfull[s], vph ^ (s < vst ? 0 : 1));
+        }
+        if (q_loads > 0) mbar_wait_drain(&bar_qfull, (q_loads - 1) & 1);
+      }
+    }
+  } else if (warp == 1) {
+    // =================================================================== MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t kIdescS = idesc_e4m3_f32(128, 128, false, false);
+      constexpr uint32_t kIdescO = idesc_f16_f32(128, 128, false, true);
+      const uint32_t q_addr = smem_u32(sQ), k_addr = smem_u32(sK), w_addr = smem_u32(sW);
+      bool ok = true;
+      int kst = 0, q_used = 0;
+      uint32_t kph = 0;
+      // S of tile number u, of group x
+      auto issue_s = [&](int u, int x) {
+        const uint32_t tS = tmem + static_cast<uint32_t>((SUB == 2 ? x : u & 1) * 128);
+        const uint32_t ka = k_addr + kst * kStage, qa = q_addr + x * 128 * 128;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          umma_e4m3(tS, smem_desc(qa + (kk >> 2) * (kRowsItem * 128) + (kk & 3) * 32, 16, 1024),
+                    smem_desc(ka + (kk & 3) * 32, 16, 1024), kIdescS, kk > 0 ? 1u : 0u);
+        umma_commit(&bar_sfull[SUB == 2 ? x : u & 1]);
+      };
+      auto wait_k = [&](bool first) {
+        if (first) {
+          if (!(ok = mbar_wait<true>(&bar_qfull, q_used & 1, &abort_flag))) return;
+          ++q_used;
+        }
+        if (!(ok = mbar_wait<true>(&bar_kfull[kst], kph, &abort_flag))) return;
+        tc_fence_after();
+      };
+      auto free_k = [&](bool last) {
+        umma_commit(&bar_kempty[kst]);
+        if (last) umma_commit(&bar_qempty);
+        if (++kst == STAGES) {
+          kst = 0;
+          kph ^= 1;
+        }
+      };
+      auto issue_pv = [&](int u, int x, bool first, int valid) {
+        const uint32_t wa = w_addr + (u & 1) * F::kWide;
+        const uint32_t tP = tmem + static_cast<uint32_t>((SUB == 2 ? x : u & 1) * 128);
+        const int steps = (valid + 15) / 16;
+        for (int q = 0; q < steps; ++q)   // keys 64h .. 64h + 63 of w as columns 64h .. 64h + 31
+          umma_bf16_ts(tO + static_cast<uint32_t>(x * 128), tP + static_cast<uint32_t>((q >> 2) * 64 + (q & 3) * 8),
+                       smem_desc(wa + q * 2048, kStage, 1024), kIdescO, first && q == 0 ? 0u : 1u);
+      };
+      auto wait_p = [&](int u, int x) {
+        ok = SUB == 2 ? mbar_wait<true>(&bar_pfull[x], u & 1, &abort_flag)
+                      : mbar_wait<true>(&bar_pfull[u & 1], (u >> 1) & 1, &abort_flag);
+        tc_fence_after();
+      };
+      Chunk cur, nxt;
+      ok = mbar_wait<true>(&bar_cfull[0], 0, &abort_flag);
+      cur = s_chunk[0];
+      if (ok && !cur.end) {
+        wait_k(true);
+        if (ok) {
+          for (int x = 0; x < SUB; ++x) issue_s(0, x);
+          free_k(cur.last && cur.n_tiles == 1);
+        }
+        int cs = 0;
+        for (int u = 0, j = 0; ok; ++u) {
+          bool has_next = true, next_first = false, next_last;
+          const bool whole = j + 1 == cur.n_tiles;   // of its descriptor
+          if (!whole) {
+            next_last = cur.last && j + 2 == cur.n_tiles;
+          } else {
+            const int rs = (cs + 1) % kRing;
+            if (!(ok = mbar_wait<true>(&bar_cfull[rs], ((cs + 1) / kRing) & 1, &abort_flag))) break;
+            nxt = s_chunk[rs];
+            has_next = !nxt.end;
+            next_first = nxt.first;
+            next_last = nxt.last && nxt.n_tiles == 1;
+          }
+          const bool first = cur.first && j == 0;
+          const int valid = min(kTile, cur.t_end - (cur.t0 + j * kTile));
+          if (SUB == 1) {
+            if (has_next) {   // S(u + 1) ahead of PV(u): the softmax goes on meanwhile
+              wait_k(next_first);
+              if (!ok) break;
+              issue_s(u + 1, 0);
+              free_k(next_last);
+            }
+            if (!(ok = mbar_wait<true>(&bar_wfull[u & 1], (u >> 1) & 1, &abort_flag))) break;
+            wait_p(u, 0);
+            if (!ok) break;
+            issue_pv(u, 0, first, valid);
+            umma_commit(&bar_wempty[u & 1]);
+            umma_commit(&bar_ofull[u & 1]);
+          } else {
+            // PV_0(u), S_0(u + 1), PV_1(u), S_1(u + 1): S_x(u + 1) overwrites the weights that PV_x(u) reads, and
+            // the tensor pipe executes one thread's MMAs in order.  Where the next tile has other queries
+            // both PVs come first.
+            if (!(ok = mbar_wait<true>(&bar_wfull[u & 1], (u >> 1) & 1, &abort_flag))) break;
+            const bool inter = has_next && !next_first;
+            for (int x = 0; x < 2 && ok; ++x) {
+              wait_p(u, x);
+              if (!ok) break;
+              issue_pv(u, x, first, valid);
+              if (x == 1) {
+                umma_commit(&bar_wempty[u & 1]);
+                umma_commit(&bar_ofull[u & 1]);
+              }
+              if (!inter) continue;
+              if (x == 0) wait_k(false);
+              if (ok) issue_s(u + 1, x);
+            }
+            if (!ok) break;
+            if (has_next && !inter) {
+              wait_k(true);
+              if (!ok) break;
+              issue_s(u + 1, 0);
+              issue_s(u + 1, 1);
+            }
+            if (has_next) free_k(next_last);
+          }
+          if (whole) {
+            mbar_arrive(&bar_cempty[cs % kRing]);
+            if (!has_next) break;
+            cur = nxt;
+            j = 0;
+            ++cs;
+          } else {
+            ++j;
+          }
+        }
+      }
+      umma_commit(&bar_done);
+    }
+  } else if (warp >= 2 + F::kSoftmaxWarps) {
+    // =================================================================== converters
+    // Lane l takes 16 dims (chunk l % 8) of tokens l / 8 + 4k: 16 bytes in, twice 16 out.  Lanes of the two
+    // halves write their two pieces in opposite order, so eight lanes' stores meet no bank twice.
+    const int w = warp - 2 - F::kSoftmaxWarps, c8 = lane & 7;
+    bool ok = true;
+    int vst = 0, u = 0;
+    uint32_t vph = 0;
+    for (int cs = 0; ok; ++cs) {
+      const int rs = cs % kRing;
+      if (!(ok = mbar_wait_warp<true>(&bar_cfull[rs], (cs / kRing) & 1, &abort_flag))) break;
+      const Chunk c = s_chunk[rs];
+      if (c.end) break;
+      for (int j = 0; j < c.n_tiles; ++j, ++u) {
+        const int valid = min(kTile, c.t_end - (c.t0 + j * kTile));
+        if (!(ok = mbar_wait_warp<true>(&bar_wempty[u & 1], ((u >> 1) & 1) ^ 1, &abort_flag))) break;
+        if (!(ok = mbar_wait_warp<true>(&bar_vfull[vst], vph, &abort_flag))) break;
+        const uint8_t* src = sV + vst * kStage;
+        uint8_t* dst = sW + (u & 1) * F::kWide + (c8 >> 2) * kStage;
+        constexpr int kEach = kTile / 4 / F::kConvWarps;   // tokens of a lane
+#pragma unroll
+        for (int k0 = 0; k0 < kEach; k0 += 4) {
+          uint4 v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int t = w * (kTile / F::kConvWarps) + (k0 + k) * 4 + (lane >> 3);
+            v[k] = *reinterpret_cast<const uint4*>(src + t * 128 + ((c8 ^ (t & 7)) << 4));
+            if (t >= valid) v[k] = make_uint4(0, 0, 0, 0);   // slots behind the last token may hold anything
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int t = w * (kTile / F::kConvWarps) + (k0 + k) * 4 + (lane >> 3);
+            const uint4 a = make_uint4(widen2(v[k].x & 0xFFFFu), widen2(v[k].x >> 16), widen2(v[k].y & 0xFFFFu), widen2(v[k].y >> 16));
+            const uint4 b = make_uint4(widen2(v[k].z & 0xFFFFu), widen2(v[k].z >> 16), widen2(v[k].w & 0xFFFFu), widen2(v[k].w >> 16));
+            const int first = c8 >> 2, at = (c8 & 3) * 2;
+            *reinterpret_cast<uint4*>(dst + t * 128 + (((at + first) ^ (t & 7)) << 4)) = first ? b : a;
+            *reinterpret_cast<uint4*>(dst + t * 128 + (((at + 1 - first) ^ (t & 7)) << 4)) = first ? a : b;
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bar_vempty[vst]);
+          mbar_arrive(&bar_wfull[u & 1]);
+        }
+        if (++vst == STAGES) {
+          vst = 0;
+          vph ^= 1;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar_cempty[rs]);
+    }
+  } else {
+    // =================================================================== softmax, epilogue
+    const int x = (warp - 2) >> 3;
+    const int half = ((warp - 2) >> 2) & 1;
+    const int q4 = warp & 3;
+    const int n = (q4 << 5) | lane;
+    const int pq = x * 4 + q4;   // the two halves' exchange barriers
+    const int r_item = x * 128 + n;
+    const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
+    const uint32_t col0 = static_cast<uint32_t>(half * 64);
+    const uint32_t tOx = tO + lane_off + static_cast<uint32_t>(x * 128) + col0;
+    bool ok = true;
+    int u = 0, pair_ends = 0;
+    float m_run = -CUDART_INF_F, l_run = 0.f;   // l_run: this half's sum
+    for (int cs = 0; ok; ++cs) {
+      const int rs = cs % kRing;
+      if (!(ok = mbar_wait_warp<true>(&bar_cfull[rs], (cs / kRing) & 1, &abort_flag))) break;
+      const Chunk c = s_chunk[rs];
+      if (c.end) break;
+      if (c.first) {
+        m_run = -CUDART_INF_F;
+        l_run = 0.f;
+      }
+      for (int j = 0; j < c.n_tiles; ++j, ++u) {
+        const uint32_t tSx = tmem + lane_off + static_cast<uint32_t>((SUB == 2 ? x : u & 1) * 128) + col0;
+        ok = SUB == 2 ? mbar_wait_warp<true>(&bar_sfull[x], u & 1, &abort_flag)
+                      : mbar_wait_warp<true>(&bar_sfull[u & 1], (u >> 1) & 1, &abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        const int nvalid = min(kTile, c.t_end - (c.t0 + j * kTile)) - half * 64;   // of this half's columns
+        const bool full = nvalid >= 64;
+        const float2* scales = &s_scale[rs][j * kTilePages + half * 4];
+        float mx = -CUDART_INF_F;
+#pragma unroll
+        for (int g2 = 0; g2 < 2; ++g2) {
+          uint32_t r[32];
+          tmem_ld16(tSx + g2 * 32, *reinterpret_cast<uint32_t(*)[16]>(r));
+          tmem_ld16(tSx + g2 * 32 + 16, *reinterpret_cast<uint32_t(*)[16]>(r + 16));
+          const float2 s0 = scales[2 * g2], s1 = scales[2 * g2 + 1];
+          tmem_wait_ld();
+          tmem_regs_ready(*reinterpret_cast<uint32_t(*)[16]>(r));
+          tmem_regs_ready(*reinterpret_cast<uint32_t(*)[16]>(r + 16));
+          const float t0 = full ? max16(r, 16) : max16(r, nvalid - g2 * 32);
+          const float t1 = full ? max16(r + 16, 16) : max16(r + 16, nvalid - g2 * 32 - 16);
+          mx = fmax3(mx, fmaf(t0, s0.x * c.q_scale, s0.y), fmaf(t1, s1.x * c.q_scale, s1.y));
+        }
+        s_hmax[u & 1][x][half][n] = mx;
+        mbar_arrive(&bar_pair[pq][u & 1]);
+        if (!(ok = mbar_wait_warp<true>(&bar_pair[pq][u & 1], (u >> 1) & 1, &abort_flag))) break;
+        mx = fmaxf(s_hmax[u & 1][x][0][n], s_hmax[u & 1][x][1][n]);
+        float alpha = 1.f;
+        bool resc = false;
+        if (m_run == -CUDART_INF_F) {
+          m_run = mx;
+        } else if (mx - m_run > kLazyMany) {
+          alpha = ex2(m_run - mx);
+          m_run = mx;
+          resc = true;
+        }
+        float sum = 0.f;
+#pragma unroll
+        for (int g2 = 0; g2 < 2; ++g2) {
+          uint32_t r[32];
+          tmem_ld16(tSx + g2 * 32, *reinterpret_cast<uint32_t(*)[16]>(r));
+          tmem_ld16(tSx + g2 * 32 + 16, *reinterpret_cast<uint32_t(*)[16]>(r + 16));
+          tmem_wait_ld();
+          tmem_regs_ready(*reinterpret_cast<uint32_t(*)[16]>(r));
+          tmem_regs_ready(*reinterpret_cast<uint32_t(*)[16]>(r + 16));
+          uint32_t pk[16];
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            const float2 s = scales[2 * g2 + g];
+            const float a = s.x * c.q_scale, b = s.y - m_run;
+            const float2 a2 = make_float2(a, a), b2 = make_float2(b, b);
+            float2 e[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int at = g * 16 + 2 * k;
+              float2 y = __ffma2_rn(make_float2(__uint_as_float(r[at]), __uint_as_float(r[at + 1])), a2, b2);
+              if (!full) {
+                if (g2 * 32 + at >= nvalid) y.x = -CUDART_INF_F;
+                if (g2 * 32 + at + 1 >= nvalid) y.y = -CUDART_INF_F;
+              }
+              e[k] = make_float2(ex2(y.x), ex2(y.y));
+              pk[g * 8 + k] = half2_bits(e[k].x, e[k].y);
+            }
+#pragma unroll
+            for (int w = 4; w > 0; w >>= 1)
+#pragma unroll
+              for (int k = 0; k < w; ++k) e[k] = __fadd2_rn(e[k], e[k + w]);
+            sum = fmaf(e[0].x + e[0].y, ex2(-s.y), sum);
+          }
+          tmem_st16(tSx + g2 * 16, pk);   // tokens 64h + 32 g2 .. + 31 as 16 columns
+        }
+        l_run = fmaf(l_run, alpha, sum);
+        if (__any_sync(0xffffffffu, resc)) {
+          // this warp's half of its rows of O to the new maxima once the last tile's PV is done
+          if (!(ok = mbar_wait_warp<true>(&bar_ofull[(u - 1) & 1], ((u - 1) >> 1) & 1, &abort_flag))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            uint32_t o[16];
+            tmem_ld16(tOx + g * 16, o);
+            tmem_wait_ld();
+            tmem_regs_ready(o);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+            tmem_st16(tOx + g * 16, o);
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(&bar_pfull[SUB == 2 ? x : u & 1]);
+        if (!c.last || j != c.n_tiles - 1) continue;
+        // ---- this half of the row of O, divided by the row's sum or as a part
+        if (!(ok = mbar_wait_warp<true>(&bar_ofull[u & 1], (u >> 1) & 1, &abort_flag))) break;
+        tc_fence_after();
+        s_hsum[pair_ends & 1][x][half][n] = l_run;
+        mbar_arrive(&bar_pair_end[pq]);
+        if (!(ok = mbar_wait_warp<true>(&bar_pair_end[pq], pair_ends & 1, &abort_flag))) break;
+        const float l_row = s_hsum[pair_ends & 1][x][0][n] + s_hsum[pair_ends & 1][x][1][n];
+        ++pair_ends;
+        const int i_row = c.rg * p.lsub + r_item / p.G;
+        const bool live = r_item < p.rows && i_row < p.L;
+        uint8_t* stage = s_stage[warp - 2];
+        if (c.slot < 0) {
+          const float inv = 1.f / l_row;
+          uint32_t w[32];
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            uint32_t o[16];
+            tmem_ld16(tOx + g * 16, o);
+            tmem_wait_ld();
+            tmem_regs_ready(o);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const __nv_bfloat162 h2 = __floats2bfloat162_rn(__uint_as_float(o[2 * k]) * inv, __uint_as_float(o[2 * k + 1]) * inv);
+              w[8 * g + k] = *reinterpret_cast<const uint32_t*>(&h2);
+            }
+          }
+          uint16_t* dst = p.out + ((static_cast<size_t>(c.b) * p.L + i_row) * p.Hq + static_cast<size_t>(c.kvh) * p.G + r_item % p.G) * 128 + col0;
+          store_rows_128b(w, live ? dst : nullptr, stage, lane);
+        } else {
+          float* mine = p.part + static_cast<size_t>(c.slot) * kRowsItem * kPartRow;
+#pragma unroll
+          for (int g2 = 0; g2 < 2; ++g2) {
+            uint32_t o[32];
+            tmem_ld16(tOx + g2 * 32, *reinterpret_cast<uint32_t(*)[16]>(o));
+            tmem_ld16(tOx + g2 * 32 + 16, *reinterpret_cast<uint32_t(*)[16]>(o + 16));
+            tmem_wait_ld();
+            tmem_regs_ready(*reinterpret_cast<uint32_t(*)[16]>(o));
+            tmem_regs_ready(*reinterpret_cast<uint32_t(*)[16]>(o + 16));
+            store_rows_128b(o, live ? mine + r_item * 128 + col0 + g2 * 32 : nullptr, stage, lane);
+          }
+          if (live && half == 0) {
+            mine[kRowsItem * 128 + r_item] = m_run;
+            mine[kRowsItem * 129 + r_item] = l_row;
+          }
+        }
+        tc_fence_before();   // O is read: the next list's first PV (after its weights) may overwrite it
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar_cempty[rs]);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    if (lane == 0) mbar_wait_drain(&bar_done, 0);
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (threadIdx.x == 0 && abort_flag) atomicOr(p.err, BDLM_DEVERR_TIMEOUT);
+}
+
+// The queries of each (sequence, KV head, row group) as two e4m3 parts of 128 bytes side by side, with the power of
+// two that they share.  A CTA a group.
+__global__ void __launch_bounds__(256) split_q_kernel(const Params p, uint8_t* __restrict__ q8, float* __restrict__ q_scale) {
+  __shared__ float s_most[8];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int t = threadIdx.x, lane = t & 31;
+  const int lists = p.Hkv * p.row_groups;
+  const int b = blockIdx.x / lists, list = blockIdx.x - b * lists;
+  const int rg = list % p.row_groups, kvh = list / p.row_groups;
+  const int l0 = rg * p.lsub, rows = min(p.lsub, p.L - l0) * p.G;
+  auto at = [&](int n) {   // of row n, in rows of 128 values
+    return (static_cast<size_t>(b) * p.L + l0 + n / p.G) * p.Hq + static_cast<size_t>(kvh) * p.G + n % p.G;
+  };
+  float most = 0.f;
+  for (int o = t; o < rows * 16; o += 256) most = fmaxf(most, magnitude(__ldg(reinterpret_cast<const uint4*>(p.q + at(o >> 4) * 128) + (o & 15))));
+  most = warp_max(most);
+  if (lane == 0) s_most[t >> 5] = most;
+  __syncthreads();
+  for (int w = 0; w < 8; ++w) most = fmaxf(most, s_most[w]);
+  const int e = q_exponent(most);
+  const float inv = pow2(-e);
+  if (t == 0) q_scale[blockIdx.x] = pow2(e);
+  for (int o = t; o < rows * 16; o += 256) {
+    const size_t row = at(o >> 4);
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p.q + row * 128) + (o & 15));
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) split_e4m3x2(bf16_lo(u[k]) * inv, bf16_hi(u[k]) * inv, hi[k], lo[k]);
+    *reinterpret_cast<uint2*>(q8 + row * 256 + (o & 15) * 8) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+    *reinterpret_cast<uint2*>(q8 + row * 256 + 128 + (o & 15) * 8) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+  }
+}
+
 // Tiles of the sequences before each, for more than 32 sequences.  One CTA.
 constexpr int kCumThreads = 1024;
 __global__ void __launch_bounds__(kCumThreads) cum_tiles_kernel(const Params p, int* __restrict__ cum) {
@@ -821,7 +1435,7 @@ __global__ void __launch_bounds__(256) join_kernel(const Params p, int n_rows, i
     before = __reduce_add_sync(0xffffffffu, lane < b ? n : 0);
   }
   const int tiles = (kv_tokens(p, b, &ok) + kTile - 1) / kTile;
-  const long long per = unit_tiles(sum * lists, ctas);
+  const long long per = unit_tiles(sum * lists, ctas, p.rounds);
   const long long c0 = before * lists + static_cast<long long>(list) * tiles;
   const int u0 = static_cast<int>(c0 / per), u1 = static_cast<int>((c0 + tiles - 1) / per);
   if (u0 == u1) return;
@@ -929,23 +1543,48 @@ cudaError_t launch_few(const CUtensorMap& tk, const CUtensorMap& tv, const Param
 Kv8AttnPlan plan_attention_kv8(int B, int L, int Hq, int Hkv, int max_pages, int num_sms) {
   Kv8AttnPlan pl;
   const int G = Hq / Hkv;
-  pl.lsub = G * L <= 32 ? L : 32 / G;
+  // up to 256 rows a group; more of them read their keys once a group
+  pl.lsub = G * L <= 256 ? L : 256 / G;
   pl.row_groups = (L + pl.lsub - 1) / pl.lsub;
   pl.rows = G * pl.lsub;
-  pl.n_rows = pl.rows <= 16 ? 16 : 32;
-  const long long tiles = static_cast<long long>(B) * Hkv * pl.row_groups * ((max_pages + kTilePages - 1) / kTilePages);
-  pl.grid = static_cast<int>(tiles < 2ll * num_sms ? tiles : 2ll * num_sms);
-  const long long units = tiles < static_cast<long long>(kRounds) * pl.grid ? tiles : static_cast<long long>(kRounds) * pl.grid;
+  pl.n_rows = pl.rows <= 16 ? 16 : pl.rows <= 32 ? 32 : pl.rows <= 128 ? 128 : 256;
+  const bool many = pl.n_rows >= 128;
+  const long long lists = static_cast<long long>(B) * Hkv * pl.row_groups;
+  const long long tiles = lists * ((max_pages + kTilePages - 1) / kTilePages);
+  const long long ctas = many ? num_sms : 2ll * num_sms;
+  pl.grid = static_cast<int>(tiles < ctas ? tiles : ctas);
+  pl.rounds = many ? 1 : kRounds;
+  const long long most = static_cast<long long>(kRounds) * pl.grid;
   // (a tile a list at most: no list is cut)
-  pl.parts = max_pages <= kTilePages ? 0 : 2 * units;
+  pl.parts = max_pages <= kTilePages ? 0 : 2 * (tiles < most ? tiles : most);
   pl.part_bytes = static_cast<size_t>(pl.parts) * pl.n_rows * kPartRow * sizeof(float);
-  pl.cum_offset = (pl.part_bytes + 255) / 256 * 256;
-  pl.bytes = pl.cum_offset + (B > 32 ? (static_cast<size_t>(B) + 1) * sizeof(int) : 0);
+  auto place = [](size_t& end, size_t bytes) {
+    const size_t at = (end + 255) / 256 * 256;
+    end = at + bytes;
+    return at;
+  };
+  pl.bytes = pl.part_bytes;
+  pl.cum_offset = place(pl.bytes, B > 32 ? (static_cast<size_t>(B) + 1) * sizeof(int) : 0);
+  pl.q_offset = place(pl.bytes, many ? static_cast<size_t>(B) * L * Hq * 256 : 0);
+  pl.q_scale_offset = place(pl.bytes, many ? static_cast<size_t>(lists) * sizeof(float) : 0);
   return pl;
 }
 
-cudaError_t launch_attention_kv8(const Kv8AttnParams& a, const Kv8AttnPlan& pl, const CUtensorMap& tk, const CUtensorMap& tv,
-                                 void* data, int* work, cudaStream_t stream) {
+template <int SUB>
+cudaError_t launch_many(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv, const Params& p, int grid,
+                        cudaStream_t stream) {
+  constexpr size_t smem = Many<SUB>::kSmem;
+  static std::atomic<unsigned long long> attr_done{0};
+  const cudaError_t e = once_per_device(attr_done, [] {
+    return cudaFuncSetAttribute(many_rows_kernel<SUB>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  });
+  if (e != cudaSuccess) return e;
+  return launch_pdl(many_rows_kernel<SUB>, dim3(grid), dim3(Many<SUB>::kThreads), smem, stream, tq, tk, tv, p);
+}
+
+cudaError_t launch_attention_kv8(const Kv8AttnParams& a, const Kv8AttnPlan& pl, const CUtensorMap& tq, const CUtensorMap& tk,
+                                 const CUtensorMap& tv, void* data, int* work, cudaStream_t stream) {
+  char* at = static_cast<char*>(data);
   Params p;
   p.q = a.q;
   p.scales = reinterpret_cast<const float2*>(a.scales);
@@ -956,6 +1595,7 @@ cudaError_t launch_attention_kv8(const Kv8AttnParams& a, const Kv8AttnPlan& pl, 
   p.err = a.err;
   p.work = work;
   p.cum = nullptr;
+  p.q_scale = reinterpret_cast<const float*>(at + pl.q_scale_offset);
   p.B = a.B;
   p.L = a.L;
   p.Hq = a.Hq;
@@ -966,18 +1606,26 @@ cudaError_t launch_attention_kv8(const Kv8AttnParams& a, const Kv8AttnPlan& pl, 
   p.lsub = pl.lsub;
   p.row_groups = pl.row_groups;
   p.rows = pl.rows;
+  p.rounds = pl.rounds;
   p.scale_log2 = a.scale_log2;
+  const unsigned lists = static_cast<unsigned>(p.B) * p.Hkv * p.row_groups;
   cudaError_t e;
   if (a.B > 32) {
-    int* cum = reinterpret_cast<int*>(static_cast<char*>(data) + pl.cum_offset);
+    int* cum = reinterpret_cast<int*>(at + pl.cum_offset);
     e = launch_pdl(cum_tiles_kernel, dim3(1), dim3(kCumThreads), 0, stream, p, cum);
     if (e != cudaSuccess) return e;
     p.cum = cum;
   }
-  e = pl.n_rows == 16 ? launch_few<16, 6>(tk, tv, p, pl.grid, stream) : launch_few<32, 5>(tk, tv, p, pl.grid, stream);
+  if (pl.n_rows >= 128) {
+    e = launch_pdl(split_q_kernel, dim3(lists), dim3(256), 0, stream, p, reinterpret_cast<uint8_t*>(at + pl.q_offset),
+                   reinterpret_cast<float*>(at + pl.q_scale_offset));
+    if (e != cudaSuccess) return e;
+    e = pl.n_rows == 128 ? launch_many<1>(tq, tk, tv, p, pl.grid, stream) : launch_many<2>(tq, tk, tv, p, pl.grid, stream);
+  } else {
+    e = pl.n_rows == 16 ? launch_few<16, 6>(tk, tv, p, pl.grid, stream) : launch_few<32, 5>(tk, tv, p, pl.grid, stream);
+  }
   if (e != cudaSuccess || pl.parts == 0) return e;
-  const dim3 grid(static_cast<unsigned>(p.B) * p.Hkv * p.row_groups, (p.rows + 7) / 8);
-  return launch_pdl(join_kernel, grid, dim3(256), 0, stream, p, pl.n_rows, pl.grid);
+  return launch_pdl(join_kernel, dim3(lists, (p.rows + 7) / 8), dim3(256), 0, stream, p, pl.n_rows, pl.grid);
 }
 
 }  // namespace bdlm
