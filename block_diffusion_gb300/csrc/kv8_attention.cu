@@ -467,91 +467,97 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     }
   } else if (warp == 1) {
     // =================================================================== MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t kIdescS = idesc_e4m3_f32(128, N, false, false);
-      constexpr uint32_t kIdescO = idesc_e4m3_f32(128, N, true, false);
-      const uint32_t q_addr = smem_u32(sQ), kv_addr = smem_u32(sKV), p_addr = smem_u32(sP);
-      bool ok = true;
-      int st = 0, pcount = 0, ocount = 0, q_used = 0;
-      uint32_t ph = 0;
-      auto do_s = [&](const Chunk& c, int u) {
-        if (!(ok = mbar_wait(&bar_sfree[u & 1], ((u >> 1) & 1) ^ 1, &abort_flag))) return;
-        if (c.first) {
-          if (!(ok = mbar_wait(&bar_qfull, q_used & 1, &abort_flag))) return;
-          ++q_used;
-        }
-        for (int j = 0; j < c.n_tiles; ++j) {
-          if (!(ok = mbar_wait(&bar_full[st], ph, &abort_flag))) return;
-          tc_fence_after();
-          const uint32_t ka = kv_addr + st * kStage;
-          const uint32_t tS = tmem + static_cast<uint32_t>(((u & 1) * kChunk + j) * N);
+    constexpr uint32_t kIdescS = idesc_e4m3_f32(128, N, false, false);
+    constexpr uint32_t kIdescO = idesc_e4m3_f32(128, N, true, false);
+    const uint64_t q_desc = smem_desc(smem_u32(sQ), 16, 1024), p_desc = smem_desc(smem_u32(sP), 16, 1024);
+    const uint64_t k_desc = smem_desc(smem_u32(sKV), 16, 1024), v_desc = smem_desc(smem_u32(sKV), kStage, 1024);
+    bool ok = true;
+    int st = 0, pcount = 0, ocount = 0, q_used = 0;
+    uint32_t ph = 0;
+    auto do_s = [&](bool first, bool last, int n_tiles, int u) {
+      if (!(ok = mbar_wait_warp(&bar_sfree[u & 1], ((u >> 1) & 1) ^ 1, &abort_flag))) return;
+      if (first) {
+        if (!(ok = mbar_wait_warp(&bar_qfull, q_used & 1, &abort_flag))) return;
+        ++q_used;
+      }
+      for (int j = 0; j < n_tiles; ++j) {
+        if (!(ok = mbar_wait_warp(&bar_full[st], ph, &abort_flag))) return;
+        tc_fence_after();
+        const uint32_t tS = tmem + static_cast<uint32_t>(((u & 1) * kChunk + j) * N);
+        const uint64_t kd = k_desc + static_cast<uint32_t>(st * (kStage >> 4));
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)   // 32 head dims of either part of q
-            umma_e4m3(tS, smem_desc(ka + (kk & 3) * 32, 16, 1024),
-                      smem_desc(q_addr + (kk >> 2) * (N * 128) + (kk & 3) * 32, 16, 1024), kIdescS, kk > 0 ? 1u : 0u);
+            umma_e4m3(tS, kd + (kk & 3) * 2, q_desc + ((kk >> 2) * (N * 128) + (kk & 3) * 32) / 16, kIdescS, kk > 0 ? 1u : 0u);
           umma_commit(&bar_empty[st]);
-          if (++st == STAGES) {
-            st = 0;
-            ph ^= 1;
+          if (j == n_tiles - 1) {
+            umma_commit(&bar_sfull[u & 1]);
+            if (last) umma_commit(&bar_qempty);
           }
         }
-        umma_commit(&bar_sfull[u & 1]);
-        if (c.last) umma_commit(&bar_qempty);
-      };
-      auto do_pv = [&](const Chunk& c, int u) {
-        for (int j = 0; j < c.n_tiles; ++j) {
-          if (!(ok = mbar_wait(&bar_full[st], ph, &abort_flag))) return;
-          const int valid = min(kTile, c.t_end - (c.t0 + j * kTile));
-          uint8_t* stage = sKV + st * kStage;
-          if (valid % kPage != 0) {
-            // slots behind the last token may hold anything (NaN); absent pages were read as zeros
-            uint4* z = reinterpret_cast<uint4*>(stage + valid * 128);
-            for (int o = 0; o < (kPage - valid % kPage) * 8; ++o) z[o] = make_uint4(0, 0, 0, 0);
-            fence_proxy_async_smem();
-          }
-          const int pb = pcount & 1;
-          if (!(ok = mbar_wait(&bar_pfull[pb], (pcount >> 1) & 1, &abort_flag))) return;
-          if (!c.first && j == 0 && s_pflag[pb]) {   // the softmax brings O to new maxima first
-            if (!(ok = mbar_wait(&bar_oready, ocount & 1, &abort_flag))) return;
-            ++ocount;
-          }
-          tc_fence_after();
-          const uint32_t va = kv_addr + st * kStage, pa = p_addr + pb * (N * 256);
-          const int steps = (valid + 31) / 32;
-          for (int q = 0; q < steps; ++q)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              umma_e4m3(tO, smem_desc(va + q * 4096, kStage, 1024), smem_desc(pa + h * (N * 128) + q * 32, 16, 1024),
-                        kIdescO, c.first && j == 0 && q == 0 && h == 0 ? 0u : 1u);
-          umma_commit(&bar_pempty[pb]);
-          ++pcount;
-          umma_commit(&bar_empty[st]);
-          if (++st == STAGES) {
-            st = 0;
-            ph ^= 1;
-          }
-        }
-        umma_commit(&bar_ofull[u & 1]);
-      };
-      Chunk cur, nxt;
-      ok = mbar_wait(&bar_cfull[0], 0, &abort_flag);
-      cur = s_chunk[0];
-      if (ok && !cur.end) {
-        do_s(cur, 0);
-        for (int u = 0; ok; ++u) {
-          const int rs = (u + 1) % kRing;
-          if (!(ok = mbar_wait(&bar_cfull[rs], ((u + 1) / kRing) & 1, &abort_flag))) break;
-          nxt = s_chunk[rs];
-          if (!nxt.end) do_s(nxt, u + 1);   // ahead of PV(u), so that the softmax can go on meanwhile
-          if (ok) do_pv(cur, u);
-          if (!ok) break;
-          mbar_arrive(&bar_cempty[u % kRing]);
-          if (nxt.end) break;
-          cur = nxt;
+        __syncwarp();
+        if (++st == STAGES) {
+          st = 0;
+          ph ^= 1;
         }
       }
-      umma_commit(&bar_done);
+    };
+    auto do_pv = [&](bool first, int t0, int t_end, int n_tiles, int u) {
+      for (int j = 0; j < n_tiles; ++j) {
+        if (!(ok = mbar_wait_warp(&bar_full[st], ph, &abort_flag))) return;
+        const int valid = min(kTile, t_end - (t0 + j * kTile));
+        if (valid % kPage != 0) {
+          // slots behind the last token may hold anything (NaN); absent pages were read as zeros
+          uint4* z = reinterpret_cast<uint4*>(sKV + st * kStage + valid * 128);
+          for (int o = lane; o < (kPage - valid % kPage) * 8; o += 32) z[o] = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        const int pb = pcount & 1;
+        if (!(ok = mbar_wait_warp(&bar_pfull[pb], (pcount >> 1) & 1, &abort_flag))) return;
+        if (!first && j == 0 && s_pflag[pb]) {   // the softmax brings O to new maxima first
+          if (!(ok = mbar_wait_warp(&bar_oready, ocount & 1, &abort_flag))) return;
+          ++ocount;
+        }
+        tc_fence_after();
+        const uint64_t vd = v_desc + static_cast<uint32_t>(st * (kStage >> 4)), pd = p_desc + static_cast<uint32_t>(pb * (N * 16));
+        const int steps = (valid + 31) / 32;
+        if (elect_one()) {
+          for (int q = 0; q < steps; ++q) {
+            umma_e4m3(tO, vd + q * 256, pd + q * 2, kIdescO, first && j == 0 && q == 0 ? 0u : 1u);
+            umma_e4m3(tO, vd + q * 256, pd + N * 8 + q * 2, kIdescO, 1u);
+          }
+          umma_commit(&bar_pempty[pb]);
+          umma_commit(&bar_empty[st]);
+          if (j == n_tiles - 1) umma_commit(&bar_ofull[u & 1]);
+        }
+        __syncwarp();
+        ++pcount;
+        if (++st == STAGES) {
+          st = 0;
+          ph ^= 1;
+        }
+      }
+    };
+    Chunk cur, nxt;
+    ok = mbar_wait_warp(&bar_cfull[0], 0, &abort_flag);
+    cur = s_chunk[0];
+    if (ok && !cur.end) {
+      do_s(true, cur.last, cur.n_tiles, 0);
+      for (int u = 0; ok; ++u) {
+        const int rs = (u + 1) % kRing;
+        if (!(ok = mbar_wait_warp(&bar_cfull[rs], ((u + 1) / kRing) & 1, &abort_flag))) break;
+        nxt = s_chunk[rs];
+        if (!nxt.end) do_s(nxt.first, nxt.last, nxt.n_tiles, u + 1);   // ahead of PV(u): the softmax goes on meanwhile
+        if (ok) do_pv(cur.first, cur.t0, cur.t_end, cur.n_tiles, u);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(&bar_cempty[u % kRing]);
+        if (nxt.end) break;
+        cur = nxt;
+      }
     }
+    if (elect_one()) umma_commit(&bar_done);
+    __syncwarp();
   } else {
     // =================================================================== softmax, epilogue
     const int q4 = warp & 3;
@@ -769,13 +775,13 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 template <int SUB>
 struct Many {
   static constexpr int kRowsItem = 128 * SUB;
-  static constexpr int kStages = SUB == 2 ? 2 : 3;      // of K, and of V
+  static constexpr int kStagesK = SUB == 2 ? 3 : 4, kStagesV = SUB == 2 ? 2 : 3;
   static constexpr int kSoftmaxWarps = 8 * SUB;
   static constexpr int kConvWarps = SUB == 2 ? 2 : 4;
   static constexpr int kThreads = 64 + 32 * (kSoftmaxWarps + kConvWarps);
   static constexpr int kChunk = 8;                      // tiles of a descriptor
   static constexpr int kWide = 2 * kStage;              // a tile's V in float16
-  static constexpr size_t kSmem = 1024 + kRowsItem * 256 + 2 * kStages * kStage + 2 * kWide;
+  static constexpr size_t kSmem = 1024 + kRowsItem * 256 + (kStagesK + kStagesV) * kStage + 2 * kWide;
 };
 
 __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
@@ -787,14 +793,40 @@ __device__ __forceinline__ uint32_t widen2(uint32_t two_codes) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Largest of 16 scores (those at and past nvalid aside).
-__device__ __forceinline__ float max16(const uint32_t* r, int nvalid) {
+__device__ __forceinline__ float max16(const uint32_t* r) {
   float v[16];
 #pragma unroll
-  for (int k = 0; k < 16; ++k) v[k] = k < nvalid ? __uint_as_float(r[k]) : -CUDART_INF_F;
+  for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(r[k]);
   const float a = fmax3(v[0], v[1], v[2]), b = fmax3(v[3], v[4], v[5]), c = fmax3(v[6], v[7], v[8]);
   const float d = fmax3(v[9], v[10], v[11]), e = fmax3(v[12], v[13], v[14]);
-  return fmax3(fmax3(a, b, c), fmax3(d, e, v[15]), -CUDART_INF_F);
+  return fmax3(fmax3(a, b, c), fmaxf(d, e), v[15]);
+}
+
+// Scores at and past nvalid read as -inf.
+__device__ __forceinline__ void cut32(uint32_t (&r)[32], int nvalid) {
+#pragma unroll
+  for (int k = 0; k < 32; ++k)
+    if (k >= nvalid) r[k] = 0xFF800000u;
+}
+
+// store_rows_128b with a staging buffer of 512 bytes, 4 rows at a time: 128 bytes per lane (w) to dst, or nowhere.
+__device__ __forceinline__ void store_rows(const uint32_t (&w)[32], void* dst, uint8_t* stage, int lane) {
+  const unsigned long long dptr = reinterpret_cast<unsigned long long>(dst);
+#pragma unroll
+  for (int p4 = 0; p4 < 8; ++p4) {
+    if ((lane >> 2) == p4) {
+      const int r = lane & 3;
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        *reinterpret_cast<uint4*>(stage + r * 128 + ((c ^ r) << 4)) = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+    }
+    __syncwarp();
+    const int r = lane >> 3, c = lane & 7;
+    const unsigned long long d = __shfl_sync(0xffffffffu, dptr, p4 * 4 + r);
+    const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((c ^ r) << 4));
+    if (d) reinterpret_cast<uint4*>(d)[c] = v;
+    __syncwarp();
+  }
 }
 
 template <int SUB>
@@ -802,15 +834,15 @@ __global__ void __launch_bounds__(Many<SUB>::kThreads, 1)
 many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const Params p) {
   using F = Many<SUB>;
-  constexpr int STAGES = F::kStages, kRowsItem = F::kRowsItem, kChunk = F::kChunk;
+  constexpr int KS = F::kStagesK, VS = F::kStagesV, kRowsItem = F::kRowsItem, kChunk = F::kChunk;
   constexpr int kChunkPages = kChunk * kTilePages;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* sQ = base;                       // two parts x kRowsItem rows x 128 bytes
   uint8_t* sK = sQ + kRowsItem * 256;
-  uint8_t* sV = sK + STAGES * kStage;
-  uint8_t* sW = sV + STAGES * kStage;       // two buffers of V in float16: two halves of 64 dims x 128 tokens
-  __shared__ uint64_t bar_qfull, bar_qempty, bar_kfull[STAGES], bar_kempty[STAGES], bar_vfull[STAGES], bar_vempty[STAGES];
+  uint8_t* sV = sK + KS * kStage;
+  uint8_t* sW = sV + VS * kStage;       // two buffers of V in float16: two halves of 64 dims x 128 tokens
+  __shared__ uint64_t bar_qfull, bar_qempty, bar_kfull[KS], bar_kempty[KS], bar_vfull[VS], bar_vempty[VS];
   __shared__ uint64_t bar_wfull[2], bar_wempty[2], bar_sfull[2], bar_pfull[2], bar_ofull[2], bar_done;
   __shared__ uint64_t bar_cfull[kRing], bar_cempty[kRing], bar_pair[4 * SUB][2], bar_pair_end[4 * SUB];
   __shared__ Chunk s_chunk[kRing];
@@ -818,16 +850,18 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   __shared__ int s_page[3][kChunkPages];
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
-  __shared__ __align__(16) uint8_t s_stage[F::kSoftmaxWarps][1024];
-  __shared__ float s_hmax[2][SUB][2][128], s_hsum[2][SUB][2][128];
+  __shared__ __align__(16) uint8_t s_stage[F::kSoftmaxWarps][512];
+  __shared__ float s_hmax[2][SUB][2][128], s_hsum[SUB][2][128];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(&bar_qfull, 1);
     mbar_init(&bar_qempty, 1);
-    for (int s = 0; s < STAGES; ++s) {
+    for (int s = 0; s < KS; ++s) {
       mbar_init(&bar_kfull[s], 1);
       mbar_init(&bar_kempty[s], 1);
+    }
+    for (int s = 0; s < VS; ++s) {
       mbar_init(&bar_vfull[s], 1);
       mbar_init(&bar_vempty[s], F::kConvWarps);
     }
@@ -934,7 +968,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       ok = __shfl_sync(0xffffffffu, ok, 0);
       ++q_loads;
     };
-    auto copy = [&](const CUtensorMap* tm, uint8_t* ring, uint64_t* full, uint64_t* empty, int& st, uint32_t& ph, int page) {
+    auto copy = [&](const CUtensorMap* tm, uint8_t* ring, uint64_t* full, uint64_t* empty, int stages, int& st, uint32_t& ph, int page) {
       if (lane == 0) {
         ok = mbar_wait<true>(&empty[st], ph ^ 1, &abort_flag);
         if (ok) mbar_arrive_expect_tx(&full[st], kStage);
@@ -942,7 +976,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (!ok) return;
       if (lane < kTilePages) tma_load_3d_hint(ring + st * kStage + lane * 2048, tm, &full[st], 0, 0, page, policy);
-      if (++st == STAGES) {
+      if (++st == stages) {
         st = 0;
         ph ^= 1;
       }
@@ -952,19 +986,19 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     int cs = 0;
     if (have) {
       load_q(cur);
-      copy(&tm_k, sK, bar_kfull, bar_kempty, kst, kph, s_page[0][lane & 7]);
+      copy(&tm_k, sK, bar_kfull, bar_kempty, KS, kst, kph, s_page[0][lane & 7]);
       have_next = prepare(nxt);
     }
     while (have && ok) {
       for (int j = 0; j < cur.n_tiles && ok; ++j) {
         // K of the next tile, then V of this one
         if (j + 1 < cur.n_tiles) {
-          copy(&tm_k, sK, bar_kfull, bar_kempty, kst, kph, s_page[cs % 3][(j + 1) * kTilePages + (lane & 7)]);
+          copy(&tm_k, sK, bar_kfull, bar_kempty, KS, kst, kph, s_page[cs % 3][(j + 1) * kTilePages + (lane & 7)]);
         } else if (have_next) {
           if (nxt.first) load_q(nxt);
-          if (ok) copy(&tm_k, sK, bar_kfull, bar_kempty, kst, kph, s_page[(cs + 1) % 3][lane & 7]);
+          if (ok) copy(&tm_k, sK, bar_kfull, bar_kempty, KS, kst, kph, s_page[(cs + 1) % 3][lane & 7]);
         }
-        if (ok) copy(&tm_v, sV, bar_vfull, bar_vempty, vst, vph, s_page[cs % 3][j * kTilePages + (lane & 7)]);
+        if (ok) copy(&tm_v, sV, bar_vfull, bar_vempty, VS, vst, vph, s_page[cs % 3][j * kTilePages + (lane & 7)]);
       }
       cur = nxt;
       have = have_next;
@@ -981,63 +1015,74 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
       }
       if (!ok) {
-        for (int s = 0; s < STAGES; ++s) {
-          mbar_wait_drain(&bar_kfull[s], kph ^ (s < kst ? 0 : 1));
-          mbar_wait_drain(&bar_vfull[s], vph ^ (s < vst ? 0 : 1));
-        }
+        for (int s = 0; s < KS; ++s) mbar_wait_drain(&bar_kfull[s], kph ^ (s < kst ? 0 : 1));
+        for (int s = 0; s < VS; ++s) mbar_wait_drain(&bar_vfull[s], vph ^ (s < vst ? 0 : 1));
         if (q_loads > 0) mbar_wait_drain(&bar_qfull, (q_loads - 1) & 1);
       }
     }
   } else if (warp == 1) {
     // =================================================================== MMA issuer
-    if (lane == 0) {
+    {
       constexpr uint32_t kIdescS = idesc_e4m3_f32(128, 128, false, false);
       constexpr uint32_t kIdescO = idesc_f16_f32(128, 128, false, true);
-      const uint32_t q_addr = smem_u32(sQ), k_addr = smem_u32(sK), w_addr = smem_u32(sW);
+      const uint64_t q_desc = smem_desc(smem_u32(sQ), 16, 1024), k_desc = smem_desc(smem_u32(sK), 16, 1024);
+      const uint64_t w_desc = smem_desc(smem_u32(sW), kStage, 1024);
       bool ok = true;
       int kst = 0, q_used = 0;
       uint32_t kph = 0;
       // S of tile number u, of group x
       auto issue_s = [&](int u, int x) {
         const uint32_t tS = tmem + static_cast<uint32_t>((SUB == 2 ? x : u & 1) * 128);
-        const uint32_t ka = k_addr + kst * kStage, qa = q_addr + x * 128 * 128;
+        const uint64_t kd = k_desc + static_cast<uint32_t>(kst * (kStage >> 4)), qd = q_desc + static_cast<uint32_t>(x * 1024);
+        if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          umma_e4m3(tS, smem_desc(qa + (kk >> 2) * (kRowsItem * 128) + (kk & 3) * 32, 16, 1024),
-                    smem_desc(ka + (kk & 3) * 32, 16, 1024), kIdescS, kk > 0 ? 1u : 0u);
-        umma_commit(&bar_sfull[SUB == 2 ? x : u & 1]);
+          for (int kk = 0; kk < 8; ++kk)
+            umma_e4m3(tS, qd + ((kk >> 2) * (kRowsItem * 128) + (kk & 3) * 32) / 16, kd + (kk & 3) * 2, kIdescS, kk > 0 ? 1u : 0u);
+          umma_commit(&bar_sfull[SUB == 2 ? x : u & 1]);
+        }
+        __syncwarp();
       };
       auto wait_k = [&](bool first) {
         if (first) {
-          if (!(ok = mbar_wait<true>(&bar_qfull, q_used & 1, &abort_flag))) return;
+          if (!(ok = mbar_wait_warp<true>(&bar_qfull, q_used & 1, &abort_flag))) return;
           ++q_used;
         }
-        if (!(ok = mbar_wait<true>(&bar_kfull[kst], kph, &abort_flag))) return;
+        if (!(ok = mbar_wait_warp<true>(&bar_kfull[kst], kph, &abort_flag))) return;
         tc_fence_after();
       };
       auto free_k = [&](bool last) {
-        umma_commit(&bar_kempty[kst]);
-        if (last) umma_commit(&bar_qempty);
-        if (++kst == STAGES) {
+        if (elect_one()) {
+          umma_commit(&bar_kempty[kst]);
+          if (last) umma_commit(&bar_qempty);
+        }
+        __syncwarp();
+        if (++kst == KS) {
           kst = 0;
           kph ^= 1;
         }
       };
       auto issue_pv = [&](int u, int x, bool first, int valid) {
-        const uint32_t wa = w_addr + (u & 1) * F::kWide;
+        const uint64_t wd = w_desc + static_cast<uint32_t>((u & 1) * (F::kWide >> 4));
         const uint32_t tP = tmem + static_cast<uint32_t>((SUB == 2 ? x : u & 1) * 128);
         const int steps = (valid + 15) / 16;
-        for (int q = 0; q < steps; ++q)   // keys 64h .. 64h + 63 of w as columns 64h .. 64h + 31
-          umma_bf16_ts(tO + static_cast<uint32_t>(x * 128), tP + static_cast<uint32_t>((q >> 2) * 64 + (q & 3) * 8),
-                       smem_desc(wa + q * 2048, kStage, 1024), kIdescO, first && q == 0 ? 0u : 1u);
+        if (elect_one()) {
+          for (int q = 0; q < steps; ++q)   // keys 64h .. 64h + 63 of w as columns 64h .. 64h + 31
+            umma_bf16_ts(tO + static_cast<uint32_t>(x * 128), tP + static_cast<uint32_t>((q >> 2) * 64 + (q & 3) * 8),
+                         wd + q * 128, kIdescO, first && q == 0 ? 0u : 1u);
+          if (x == SUB - 1) {
+            umma_commit(&bar_wempty[u & 1]);
+            umma_commit(&bar_ofull[u & 1]);
+          }
+        }
+        __syncwarp();
       };
       auto wait_p = [&](int u, int x) {
-        ok = SUB == 2 ? mbar_wait<true>(&bar_pfull[x], u & 1, &abort_flag)
-                      : mbar_wait<true>(&bar_pfull[u & 1], (u >> 1) & 1, &abort_flag);
+        ok = SUB == 2 ? mbar_wait_warp<true>(&bar_pfull[x], u & 1, &abort_flag)
+                      : mbar_wait_warp<true>(&bar_pfull[u & 1], (u >> 1) & 1, &abort_flag);
         tc_fence_after();
       };
       Chunk cur, nxt;
-      ok = mbar_wait<true>(&bar_cfull[0], 0, &abort_flag);
+      ok = mbar_wait_warp<true>(&bar_cfull[0], 0, &abort_flag);
       cur = s_chunk[0];
       if (ok && !cur.end) {
         wait_k(true);
@@ -1053,7 +1098,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             next_last = cur.last && j + 2 == cur.n_tiles;
           } else {
             const int rs = (cs + 1) % kRing;
-            if (!(ok = mbar_wait<true>(&bar_cfull[rs], ((cs + 1) / kRing) & 1, &abort_flag))) break;
+            if (!(ok = mbar_wait_warp<true>(&bar_cfull[rs], ((cs + 1) / kRing) & 1, &abort_flag))) break;
             nxt = s_chunk[rs];
             has_next = !nxt.end;
             next_first = nxt.first;
@@ -1068,26 +1113,20 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
               issue_s(u + 1, 0);
               free_k(next_last);
             }
-            if (!(ok = mbar_wait<true>(&bar_wfull[u & 1], (u >> 1) & 1, &abort_flag))) break;
+            if (!(ok = mbar_wait_warp<true>(&bar_wfull[u & 1], (u >> 1) & 1, &abort_flag))) break;
             wait_p(u, 0);
             if (!ok) break;
             issue_pv(u, 0, first, valid);
-            umma_commit(&bar_wempty[u & 1]);
-            umma_commit(&bar_ofull[u & 1]);
           } else {
             // PV_0(u), S_0(u + 1), PV_1(u), S_1(u + 1): S_x(u + 1) overwrites the weights that PV_x(u) reads, and
             // the tensor pipe executes one thread's MMAs in order.  Where the next tile has other queries
             // both PVs come first.
-            if (!(ok = mbar_wait<true>(&bar_wfull[u & 1], (u >> 1) & 1, &abort_flag))) break;
+            if (!(ok = mbar_wait_warp<true>(&bar_wfull[u & 1], (u >> 1) & 1, &abort_flag))) break;
             const bool inter = has_next && !next_first;
             for (int x = 0; x < 2 && ok; ++x) {
               wait_p(u, x);
               if (!ok) break;
               issue_pv(u, x, first, valid);
-              if (x == 1) {
-                umma_commit(&bar_wempty[u & 1]);
-                umma_commit(&bar_ofull[u & 1]);
-              }
               if (!inter) continue;
               if (x == 0) wait_k(false);
               if (ok) issue_s(u + 1, x);
@@ -1102,7 +1141,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             if (has_next) free_k(next_last);
           }
           if (whole) {
-            mbar_arrive(&bar_cempty[cs % kRing]);
+            if (lane == 0) mbar_arrive(&bar_cempty[cs % kRing]);
             if (!has_next) break;
             cur = nxt;
             j = 0;
@@ -1112,7 +1151,8 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           }
         }
       }
-      umma_commit(&bar_done);
+      if (elect_one()) umma_commit(&bar_done);
+      __syncwarp();
     }
   } else if (warp >= 2 + F::kSoftmaxWarps) {
     // =================================================================== converters
@@ -1159,7 +1199,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           mbar_arrive(&bar_vempty[vst]);
           mbar_arrive(&bar_wfull[u & 1]);
         }
-        if (++vst == STAGES) {
+        if (++vst == VS) {
           vst = 0;
           vph ^= 1;
         }
@@ -1209,9 +1249,8 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           tmem_wait_ld();
           tmem_regs_ready(*reinterpret_cast<uint32_t(*)[16]>(r));
           tmem_regs_ready(*reinterpret_cast<uint32_t(*)[16]>(r + 16));
-          const float t0 = full ? max16(r, 16) : max16(r, nvalid - g2 * 32);
-          const float t1 = full ? max16(r + 16, 16) : max16(r + 16, nvalid - g2 * 32 - 16);
-          mx = fmax3(mx, fmaf(t0, s0.x * c.q_scale, s0.y), fmaf(t1, s1.x * c.q_scale, s1.y));
+          if (!full) cut32(r, nvalid - g2 * 32);
+          mx = fmax3(mx, fmaf(max16(r), s0.x * c.q_scale, s0.y), fmaf(max16(r + 16), s1.x * c.q_scale, s1.y));
         }
         s_hmax[u & 1][x][half][n] = mx;
         mbar_arrive(&bar_pair[pq][u & 1]);
@@ -1235,6 +1274,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           tmem_wait_ld();
           tmem_regs_ready(*reinterpret_cast<uint32_t(*)[16]>(r));
           tmem_regs_ready(*reinterpret_cast<uint32_t(*)[16]>(r + 16));
+          if (!full) cut32(r, nvalid - g2 * 32);
           uint32_t pk[16];
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
@@ -1245,11 +1285,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               const int at = g * 16 + 2 * k;
-              float2 y = __ffma2_rn(make_float2(__uint_as_float(r[at]), __uint_as_float(r[at + 1])), a2, b2);
-              if (!full) {
-                if (g2 * 32 + at >= nvalid) y.x = -CUDART_INF_F;
-                if (g2 * 32 + at + 1 >= nvalid) y.y = -CUDART_INF_F;
-              }
+              const float2 y = __ffma2_rn(make_float2(__uint_as_float(r[at]), __uint_as_float(r[at + 1])), a2, b2);
               e[k] = make_float2(ex2(y.x), ex2(y.y));
               pk[g * 8 + k] = half2_bits(e[k].x, e[k].y);
             }
@@ -1284,10 +1320,10 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         // ---- this half of the row of O, divided by the row's sum or as a part
         if (!(ok = mbar_wait_warp<true>(&bar_ofull[u & 1], (u >> 1) & 1, &abort_flag))) break;
         tc_fence_after();
-        s_hsum[pair_ends & 1][x][half][n] = l_run;
+        s_hsum[x][half][n] = l_run;
         mbar_arrive(&bar_pair_end[pq]);
         if (!(ok = mbar_wait_warp<true>(&bar_pair_end[pq], pair_ends & 1, &abort_flag))) break;
-        const float l_row = s_hsum[pair_ends & 1][x][0][n] + s_hsum[pair_ends & 1][x][1][n];
+        const float l_row = s_hsum[x][0][n] + s_hsum[x][1][n];
         ++pair_ends;
         const int i_row = c.rg * p.lsub + r_item / p.G;
         const bool live = r_item < p.rows && i_row < p.L;
@@ -1308,7 +1344,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             }
           }
           uint16_t* dst = p.out + ((static_cast<size_t>(c.b) * p.L + i_row) * p.Hq + static_cast<size_t>(c.kvh) * p.G + r_item % p.G) * 128 + col0;
-          store_rows_128b(w, live ? dst : nullptr, stage, lane);
+          store_rows(w, live ? dst : nullptr, stage, lane);
         } else {
           float* mine = p.part + static_cast<size_t>(c.slot) * kRowsItem * kPartRow;
 #pragma unroll
@@ -1319,7 +1355,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             tmem_wait_ld();
             tmem_regs_ready(*reinterpret_cast<uint32_t(*)[16]>(o));
             tmem_regs_ready(*reinterpret_cast<uint32_t(*)[16]>(o + 16));
-            store_rows_128b(o, live ? mine + r_item * 128 + col0 + g2 * 32 : nullptr, stage, lane);
+            store_rows(o, live ? mine + r_item * 128 + col0 + g2 * 32 : nullptr, stage, lane);
           }
           if (live && half == 0) {
             mine[kRowsItem * 128 + r_item] = m_run;

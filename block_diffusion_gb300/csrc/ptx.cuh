@@ -281,6 +281,18 @@ __device__ __forceinline__ void umma_e4m3_ts(uint32_t d_tmem, uint32_t a_tmem, u
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// One lane of a converged warp, the same one every time.  A warp that runs its loop whole and issues under
+// this keeps descriptors in uniform registers, where tcgen05.mma takes them: issued by a lane of its own branch,
+// each MMA cost its thread about 120 cycles of moves, two to three times what the tensor cores take for it.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(yes));
+  return yes != 0;
+}
 // Arrives (once) on `bar` when every previously issued tcgen05.mma of this thread is done.
 __device__ __forceinline__ void umma_commit(uint64_t* bar) {
   asm volatile(
