@@ -1113,7 +1113,7 @@ int bdlm_attention_kv8(const bdlm_attn_desc* desc, const bdlm_bf16* q, const bdl
   if ((rc = get_encoder())) return rc;
   const bdlm::Kv8AttnPlan plan =
       bdlm::plan_attention_kv8(d.B, d.L, d.Hq, d.Hkv, d.max_pages_per_seq, st->num_sms);
-  if ((rc = ensure(st, st->attn_cnt, 2 * sizeof(int), true, stream))) return rc;
+  if ((rc = ensure(st, st->attn_cnt, plan.work_bytes, true, stream))) return rc;
   if ((rc = ensure(st, st->data, plan.bytes, false, stream))) return rc;
   // a page and head are 16 rows of 128 bytes
   CUtensorMap tm_q = {}, tm_k, tm_v;

@@ -48,13 +48,14 @@ struct Params {
   uint16_t* out;
   float* part;       // unit u's parts: 2u (of a list that began before it), 2u + 1 (of one that begins in it)
   int* err;
-  int* work;         // [0] next unit, [1] CTAs finished
-  const int* cum;    // [B + 1] tiles of the sequences before each (null: up to 32 sequences)
+  int* work;         // [0] CTAs finished, [1 + u] parts written of the list that unit u's end cuts (join_here)
+  const int* cum;    // [B + 1] tiles of the sequences before each (null: up to kFewSequences sequences)
   const float* q_scale;   // many rows: 2^e of each row group's queries
   int B, L, Hq, Hkv, G, max_pages, num_pages, lsub, row_groups, rows;
-  int rounds;        // of units, where a CTA's share is long
+  int join_here;     // the CTA that writes a list's last part joins them
   float scale_log2;
 };
+constexpr int kFewSequences = 256;
 
 // Some tiles of a list, as the warps pass them on.
 struct Chunk {
@@ -63,6 +64,7 @@ struct Chunk {
   int n_tiles;
   int first, last;   // of the tiles that this CTA sums up together
   int slot;          // part to write at the last chunk, -1: the output
+  int u0, parts;     // the list's first unit and its parts (slot >= 0)
   int end;
   float q_scale;     // q = (hi + lo) * q_scale, times c
 };
@@ -75,15 +77,69 @@ __device__ __forceinline__ int kv_tokens(const Params& p, int b, bool* ok) {
   return static_cast<int>(n < max_tok ? n : max_tok);
 }
 
-// Tiles of a unit: all of the work in `ctas` even shares, or in four rounds of them where a share is long
-// enough that CTAs' different speeds count for more than a unit's start and end.
-constexpr int kRounds = 4;
-constexpr int kRoundTiles = 32;   // tiles of a share from which on there are kRounds rounds
-__device__ __forceinline__ long long unit_tiles(long long total, int ctas, int rounds) {
+// Tiles of a unit, a CTA's even share of all.  (Shares of a quarter, taken in turn, were no faster: what they gain
+// in evenness goes into four times the parts.)
+__device__ __forceinline__ long long unit_tiles(long long total, int ctas) {
   const long long share = (total + ctas - 1) / ctas;
-  if (share < kRoundTiles) return share < 1 ? 1 : share;
-  return (total + static_cast<long long>(rounds) * ctas - 1) / (static_cast<long long>(rounds) * ctas);
+  return share < 1 ? 1 : share;
 }
+
+// Tiles of the sequences before each: in the lanes of a warp, or in memory.
+struct Before {
+  int own[kFewSequences / 32];   // lane l: before sequence 32 i + l
+  int all;
+
+  __device__ __forceinline__ void init(const Params& p, int lane) {
+    if (p.cum != nullptr) {
+      all = __ldg(p.cum + p.B);
+      return;
+    }
+    bool ok;
+#pragma unroll
+    for (int i = 0; i < kFewSequences / 32; ++i) {
+      const int b = i * 32 + lane;
+      own[i] = b < p.B ? (kv_tokens(p, b, &ok) + kTile - 1) / kTile : 0;
+    }
+    all = 0;
+#pragma unroll
+    for (int i = 0; i < kFewSequences / 32; ++i) {
+      if (i * 32 >= p.B) break;
+      int incl = own[i];
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += v;
+      }
+      own[i] = all + incl - own[i];
+      all += __shfl_sync(0xffffffffu, incl, 31);
+    }
+  }
+  // The sequence that tile x lies in, and the tiles before it.
+  __device__ __forceinline__ int find(const Params& p, int lane, int x, int& before) const {
+    int b = 0;
+    if (p.cum == nullptr) {
+#pragma unroll
+      for (int i = 0; i < kFewSequences / 32; ++i) {
+        if (i * 32 >= p.B) break;
+        const int c = __popc(__ballot_sync(0xffffffffu, i * 32 + lane < p.B && own[i] <= x));
+        if (c > 0) {
+          b = i * 32 + c - 1;
+          before = __shfl_sync(0xffffffffu, own[i], c - 1);
+        }
+      }
+    } else {
+      int n = p.B;
+      while (n > 1) {
+        const int step = (n + 31) / 32;
+        const int c = __popc(__ballot_sync(0xffffffffu, lane * step < n && __ldg(p.cum + b + (lane * step < n ? lane * step : 0)) <= x)) - 1;
+        b += c * step;
+        n = min(step, n - c * step);
+      }
+      before = __ldg(p.cum + b);
+    }
+    return b;
+  }
+};
 
 __device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
   return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
@@ -122,41 +178,32 @@ __device__ __forceinline__ float2 page_scale(float2 s) {
   return make_float2(fminf(fmaxf(s.x, kLeast), kMost), __log2f(fminf(fmaxf(s.y, kLeast), kMost)));
 }
 
-// The walk over a CTA's units, list by list, in chunks of up to CHUNK tiles (whole warp, uniform).
+// The walk over a CTA's unit, list by list, in chunks of up to CHUNK tiles (whole warp, uniform).
 template <int CHUNK>
 struct Walk {
-  long long total, per, pos, end;   // in tiles; pos, end: what is left of the unit
-  int unit, units;
+  long long per, pos, end;          // in tiles; pos: of what comes after the list at hand
   int b, kv_len, tiles, lists;      // the sequence at pos
   long long base;                   // tiles before it
-  int kvh, rg, tile, seg_end, slot, seg_first;
-  bool len_ok;
-  bool counted;
+  int kvh, rg, tile, seg_end, slot, u0, parts;
+  bool len_ok, fresh;
 
-  __device__ __forceinline__ void init(const Params& p, int lane, int& my_cum) {
+  __device__ __forceinline__ void init(const Params& p, int lane) {
+    Before before;
+    before.init(p, lane);
     lists = p.Hkv * p.row_groups;
-    long long sum;
-    if (p.cum == nullptr) {
-      bool ok;
-      int n = lane < p.B ? (kv_tokens(p, lane, &ok) + kTile - 1) / kTile : 0;
-      int incl = n;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += v;
-      }
-      my_cum = incl - n;
-      sum = __shfl_sync(0xffffffffu, incl, 31);
-    } else {
-      sum = __ldg(p.cum + p.B);
-    }
-    total = sum * lists;
-    per = unit_tiles(total, gridDim.x, p.rounds);
-    units = static_cast<int>((total + per - 1) / per);
-    counted = units > static_cast<int>(gridDim.x);
-    unit = -1;
-    pos = end = 0;
+    const long long total = static_cast<long long>(before.all) * lists;
+    per = unit_tiles(total, gridDim.x);
+    pos = blockIdx.x * per;
+    end = pos + per < total ? pos + per : total;
     tile = seg_end = 0;
+    if (pos >= end) {
+      pos = end;
+      return;
+    }
+    int n;
+    b = before.find(p, lane, static_cast<int>(pos / lists), n);   // before[b] <= pos / lists < before[b + 1]
+    base = static_cast<long long>(n) * lists;
+    sequence(p);
   }
 
   __device__ __forceinline__ void sequence(const Params& p) {
@@ -164,45 +211,11 @@ struct Walk {
     tiles = (kv_len + kTile - 1) / kTile;
   }
 
-  // Goes to the next unit; false: there is none.
-  __device__ __forceinline__ bool take(const Params& p, int lane, int my_cum) {
-    if (unit < 0) {
-      unit = blockIdx.x;
-    } else {
-      if (!counted) return false;
-      int u = 0;
-      if (lane == 0) u = atomicAdd(p.work, 1);
-      unit = static_cast<int>(gridDim.x) + __shfl_sync(0xffffffffu, u, 0);
-    }
-    if (unit >= units) return false;
-    pos = unit * per;
-    end = pos + per < total ? pos + per : total;
-    const int x = static_cast<int>(pos / lists);   // cum[b] <= x < cum[b + 1]
-    int before;
-    if (p.cum == nullptr) {
-      b = __popc(__ballot_sync(0xffffffffu, lane < p.B && my_cum <= x)) - 1;
-      before = __shfl_sync(0xffffffffu, my_cum, b);
-    } else {
-      int lo = 0, n = p.B;
-      while (n > 1) {
-        const int step = (n + 31) / 32, at = lo + lane * step;
-        const int c = __popc(__ballot_sync(0xffffffffu, lane * step < n && __ldg(p.cum + at) <= x)) - 1;
-        lo += c * step;
-        n = min(step, n - c * step);
-      }
-      b = lo;
-      before = __ldg(p.cum + b);
-    }
-    base = static_cast<long long>(before) * lists;
-    sequence(p);
-    return true;
-  }
-
   // The next chunk; false: no work is left.
-  __device__ __forceinline__ bool next(const Params& p, int lane, int my_cum, Chunk& c) {
-    seg_first = 0;
-    if (tile == seg_end) {
-      if (pos == end && !take(p, lane, my_cum)) return false;
+  __device__ __forceinline__ bool next(const Params& p, int lane, Chunk& c) {
+    fresh = tile == seg_end;
+    if (fresh) {
+      if (pos == end) return false;
       long long r = pos - base;
       if (r >= static_cast<long long>(tiles) * lists) {
         base += static_cast<long long>(tiles) * lists;
@@ -215,10 +228,15 @@ struct Walk {
       kvh = list / p.row_groups;
       tile = static_cast<int>(r - static_cast<long long>(list) * tiles);
       const int n = static_cast<int>(min(static_cast<long long>(tiles - tile), end - pos));
+      slot = -1;
+      if (n < tiles) {
+        const long long c0 = pos - tile;   // the list's first tile
+        u0 = tile == 0 ? static_cast<int>(blockIdx.x) : static_cast<int>(c0 / per);
+        parts = static_cast<int>((c0 + tiles - 1) / per) - u0 + 1;
+        slot = 2 * static_cast<int>(blockIdx.x) + (tile == 0 ? 1 : 0);
+      }
       seg_end = tile + n;
       pos += n;
-      slot = tile == 0 && seg_end == tiles ? -1 : 2 * unit + (tile == 0 ? 1 : 0);
-      seg_first = 1;
       if (!len_ok && tile == 0 && list == 0 && lane == 0) atomicOr(p.err, BDLM_DEVERR_LENGTH);
     }
     c.b = b;
@@ -228,11 +246,48 @@ struct Walk {
     c.t_end = kv_len;
     c.n_tiles = min(CHUNK, seg_end - tile);
     tile += c.n_tiles;
-    c.first = seg_first;
+    c.first = fresh;
     c.last = tile == seg_end;
     c.slot = slot;
+    c.u0 = u0;
+    c.parts = parts;
     c.end = 0;
     return true;
+  }
+};
+
+// A chunk's pages (page * Hkv + head, or `absent`) and scales, asked for lane by lane.
+template <int PAGES>
+struct PageLoads {
+  static constexpr int kEach = (PAGES + 31) / 32;
+  int unit[kEach];
+  float2 scale[kEach];
+
+  __device__ __forceinline__ void ask(const Params& p, const Chunk& c, int lane) {
+    const int at = c.t0 / kPage, n = min(c.n_tiles * kTilePages, (c.t_end - c.t0 + kPage - 1) / kPage);
+    int bad = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int q = i * 32 + lane;
+      int id = q < n ? __ldg(p.page_table + static_cast<size_t>(c.b) * p.max_pages + at + q) : -1;
+      if (id < 0 || id >= p.num_pages) {
+        bad |= q < n;
+        id = -1;
+      }
+      unit[i] = id >= 0 ? id * p.Hkv + c.kvh : p.num_pages * p.Hkv;   // past the pool: a box there reads zeros
+      scale[i] = id >= 0 ? __ldg(p.scales + unit[i]) : make_float2(0.f, 0.f);
+    }
+    if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.err, BDLM_DEVERR_PAGE);
+  }
+  __device__ __forceinline__ void give(int* units, float2* scales, int lane) const {
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const int q = i * 32 + lane;
+      if (q < PAGES) {
+        units[q] = unit[i];
+        scales[q] = page_scale(scale[i]);
+      }
+    }
   }
 };
 
@@ -241,11 +296,14 @@ constexpr int kPartRow = 130;   // floats of a row's part: O, m, l
 // ------------------------------------------------------------------ up to 32 query rows per KV head
 //
 // Transposed: S^T = K Q^T with 128 tokens on M and the query rows on N, O^T += V^T W^T with the 128 head
-// dims on M, so a few rows fill the tensor cores' tiles.  Warp 0 streams K and V (TMA, a box of 2 KB a
-// page, into a ring of 16 KB stages) and turns the queries into their parts; one thread of warp 1 issues the
-// MMAs; warps 2-5, a token (of S^T) or head dim (of O^T) a thread, do the softmax.  A chunk of tiles whose
+// dims on M, so a few rows fill the tensor cores' tiles.  Warp 6 walks the work ahead of all others: it looks up
+// pages and scales, and turns the queries into their parts.  Warp 0 streams K and V (TMA, a box of 2 KB a
+// page, into a ring of 16 KB stages); warp 1 issues the MMAs; warps 2-5, a token (of S^T) or head dim (of
+// O^T) a thread, do the softmax.  A chunk of tiles whose
 // S^T fit tensor memory is taken at once: the maxima over all of it, then its weights tile by tile.  S^T
 // is double-buffered and K of chunk u + 1 streams ahead of V of chunk u.
+
+constexpr int kFewThreads = 96 + kSoftmaxThreads;
 
 template <int N, int STAGES>
 struct Few {
@@ -255,8 +313,51 @@ struct Few {
   static constexpr size_t kSmem = 1024 + N * 256 + static_cast<size_t>(STAGES) * kStage + 2 * N * 256;
 };
 
+// Joins the parts of chunk c's list, in their order whoever comes last:
+//     out = sum_s e_s O_s / sum_s e_s l_s,   e_s = 2^(m_s - M).
+// 128 threads, a head dim each.
+template <int N>
+__device__ __forceinline__ void join_parts(const Params& p, const Chunk& c, int x, float* s_m, float* s_l, float (*s_red)[N]) {
+  auto part = [&](int s) { return p.part + static_cast<size_t>(2 * (c.u0 + s) + (s == 0 ? 1 : 0)) * N * kPartRow; };
+  if (x < N) {
+    float M = -CUDART_INF_F, den = 0.f;
+#pragma unroll 4
+    for (int s = 0; s < c.parts; ++s) M = fmaxf(M, __ldcg(part(s) + N * 128 + x));
+#pragma unroll 4
+    for (int s = 0; s < c.parts; ++s) den = fmaf(ex2(__ldcg(part(s) + N * 128 + x) - M), __ldcg(part(s) + N * 129 + x), den);
+    s_m[x] = M;
+    s_l[x] = den;
+  }
+  named_barrier(1, kSoftmaxThreads);
+  float acc[N];
+#pragma unroll
+  for (int n = 0; n < N; ++n) acc[n] = 0.f;
+  for (int s0 = 0; s0 < c.parts; s0 += 4) {
+    if (x < 4 * N) {
+      const int s = s0 + x / N, n = x % N;
+      s_red[x / N][n] = s < c.parts ? ex2(__ldcg(part(s) + N * 128 + n) - s_m[n]) : 0.f;
+    }
+    named_barrier(1, kSoftmaxThreads);
+    const int cnt = min(4, c.parts - s0);
+    for (int i = 0; i < cnt; ++i) {
+      const float* o = part(s0 + i) + x;
+#pragma unroll
+      for (int n = 0; n < N; ++n)
+        if (n < p.rows) acc[n] = fmaf(s_red[i][n], __ldcg(o + n * 128), acc[n]);
+    }
+    named_barrier(1, kSoftmaxThreads);
+  }
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    const int i = c.rg * p.lsub + n / p.G;
+    if (n < p.rows && i < p.L)
+      p.out[((static_cast<size_t>(c.b) * p.L + i) * p.Hq + static_cast<size_t>(c.kvh) * p.G + n % p.G) * 128 + x] =
+          __bfloat16_as_ushort(__float2bfloat16_rn(acc[n] / s_l[n]));
+  }
+}
+
 template <int N, int STAGES>
-__global__ void __launch_bounds__(64 + kSoftmaxThreads, 2)
+__global__ void __launch_bounds__(kFewThreads, 2)
 few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Params p) {
   using F = Few<N, STAGES>;
   constexpr int kChunk = F::kChunk;
@@ -271,11 +372,11 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
   __shared__ uint64_t bar_cfull[kRing], bar_cempty[kRing];
   __shared__ Chunk s_chunk[kRing];
   __shared__ float2 s_scale[kRing][F::kChunkPages];   // sK, log2 sV
-  __shared__ int s_page[3][F::kChunkPages];           // page * Hkv + head
+  __shared__ int s_page[kRing][F::kChunkPages];       // page * Hkv + head
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
   __shared__ float s_m[N], s_alpha[N], s_l[N], s_red[4][N];
-  __shared__ int s_need[2], s_pflag[2];
+  __shared__ int s_need[2], s_pflag[2], s_join;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -296,7 +397,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     mbar_init(&bar_done, 1);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&bar_cfull[i], 1);
-      mbar_init(&bar_cempty[i], 2);   // the MMA warp and a softmax thread
+      mbar_init(&bar_cempty[i], 3);   // copies, MMA, softmax
     }
     abort_flag = 0;
     s_need[0] = s_need[1] = 0;
@@ -315,153 +416,42 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
   const uint32_t tO = tmem + static_cast<uint32_t>(2 * kChunk * N);
 
   if (warp == 0) {
-    // =================================================================== producer
-    if (lane == 0) {
-      tma_prefetch_desc(&tm_k);
-      tma_prefetch_desc(&tm_v);
-    }
+    // =================================================================== copies
     const uint64_t policy = l2_policy_evict_first();
-    const int absent = p.num_pages * p.Hkv;   // past the pool: a box there reads zeros
-    int st = 0, my_cum = 0;
+    int st = 0;
     uint32_t ph = 0;
     bool ok = true;
-    Walk<kChunk> walk;
-    walk.init(p, lane, my_cum);
-    uint4 qr[N / 2];    // the queries of the chunk prepared last, where it is a first one
-    int q_exp = 0, q_loads = 0;
-    int seq = -1;       // chunks published
-
-    // Publishes the next chunk with its scales, and its pages for the copies.
-    auto prepare = [&](Chunk& c) -> bool {
-      const bool have = walk.next(p, lane, my_cum, c);
-      ++seq;
-      const int rs = seq % kRing;
-      float2 sc[(F::kChunkPages + 31) / 32];
-      if (have) {
-        int* page = s_page[seq % 3];
-        const int at = c.t0 / kPage, n = min(c.n_tiles * kTilePages, (c.t_end - c.t0 + kPage - 1) / kPage);
-        int bad = 0;
-#pragma unroll
-        for (int i = 0; i < (F::kChunkPages + 31) / 32; ++i) {
-          const int q = i * 32 + lane;
-          int id = q < n ? __ldg(p.page_table + static_cast<size_t>(c.b) * p.max_pages + at + q) : -1;
-          if (id < 0 || id >= p.num_pages) {
-            bad |= q < n;
-            id = -1;
-          }
-          const int unit = id * p.Hkv + c.kvh;
-          sc[i] = id >= 0 ? __ldg(p.scales + unit) : make_float2(0.f, 0.f);
-          if (q < F::kChunkPages) page[q] = id >= 0 ? unit : absent;
-        }
-        if (c.first) {
-          float most = 0.f;
-#pragma unroll
-          for (int i = 0; i < N / 2; ++i) {
-            const int n = 2 * i + (lane >> 4);
-            const int pos = c.rg * p.lsub + n / p.G;
-            qr[i] = make_uint4(0, 0, 0, 0);
-            if (n < p.rows && pos < p.L)
-              qr[i] = __ldg(reinterpret_cast<const uint4*>(
-                  p.q + ((static_cast<size_t>(c.b) * p.L + pos) * p.Hq + c.kvh * p.G + n % p.G) * 128) + (lane & 15));
-          }
-#pragma unroll
-          for (int i = 0; i < N / 2; ++i) most = fmaxf(most, magnitude(qr[i]));
-          q_exp = q_exponent(warp_max(most));
-        }
-        c.q_scale = pow2(q_exp) * p.scale_log2;
-        if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.err, BDLM_DEVERR_PAGE);
-      }
-      if (ok) ok = mbar_wait_warp(&bar_cempty[rs], ((seq / kRing) & 1) ^ 1, &abort_flag);
-      if (have) {
-#pragma unroll
-        for (int i = 0; i < (F::kChunkPages + 31) / 32; ++i) {
-          const int q = i * 32 + lane;
-          if (q < F::kChunkPages) s_scale[rs][q] = page_scale(sc[i]);
-        }
-      }
-      __syncwarp();
-      if (lane == 0) {
-        if (have) {
-          s_chunk[rs] = c;
-        } else {
-          s_chunk[rs].end = 1;
-        }
-        mbar_arrive(&bar_cfull[rs]);
-      }
-      return have;
-    };
-    // The parts of the prepared queries into shared memory, once the MMAs on the last ones are done.
-    auto load_q = [&]() {
-      if (ok) ok = mbar_wait_warp(&bar_qempty, (q_loads & 1) ^ 1, &abort_flag);
-      if (!ok) return;
-      const float inv = pow2(-q_exp);
-#pragma unroll
-      for (int i = 0; i < N / 2; ++i) {
-        const int n = 2 * i + (lane >> 4);
-        const uint32_t u[4] = {qr[i].x, qr[i].y, qr[i].z, qr[i].w};
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) split_e4m3x2(bf16_lo(u[k]) * inv, bf16_hi(u[k]) * inv, hi[k], lo[k]);
-        const uint32_t at = n * 128 + ((((lane & 15) >> 1) ^ (n & 7)) << 4) + (lane & 1) * 8;
-        *reinterpret_cast<uint2*>(sQ + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-        *reinterpret_cast<uint2*>(sQ + N * 128 + at) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar_qfull);
-      ++q_loads;
-    };
-    // Streams the K or V tiles of chunk number s.
-    auto emit = [&](const Chunk& c, int s, const CUtensorMap* tm) {
-      for (int j = 0; j < c.n_tiles && ok; ++j) {
-        if (lane == 0) {
-          ok = mbar_wait(&bar_empty[st], ph ^ 1, &abort_flag);
-          if (ok) mbar_arrive_expect_tx(&bar_full[st], kStage);
-        }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) break;
+    auto emit = [&](int s, int n_tiles, const CUtensorMap* tm) {   // of chunk number s
+      for (int j = 0; j < n_tiles && ok; ++j) {
+        if (!(ok = mbar_wait_warp(&bar_empty[st], ph ^ 1, &abort_flag))) break;
+        if (lane == 0) mbar_arrive_expect_tx(&bar_full[st], kStage);
+        __syncwarp();
         if (lane < kTilePages)
-          tma_load_3d_hint(sKV + st * kStage + lane * 2048, tm, &bar_full[st], 0, 0, s_page[s % 3][j * kTilePages + lane], policy);
+          tma_load_3d_hint(sKV + st * kStage + lane * 2048, tm, &bar_full[st], 0, 0, s_page[s % kRing][j * kTilePages + lane], policy);
         if (++st == STAGES) {
           st = 0;
           ph ^= 1;
         }
       }
     };
-    // K of the next chunk, then V of this one; the one after is prepared in between, while the ring is full.
-    Chunk cur, nxt, after;
-    bool have = prepare(cur);
-    int cs = 0;   // number of cur
-    bool have_next = false;
-    if (have) {
-      load_q();
-      emit(cur, 0, &tm_k);
-      have_next = prepare(nxt);
-    }
-    while (have && ok) {
-      bool have_after = false;
-      if (have_next) {
-        if (nxt.first) load_q();
-        emit(nxt, cs + 1, &tm_k);
-        have_after = prepare(after);
+    // K of the next chunk, then V of this one
+    if ((ok = mbar_wait_warp(&bar_cfull[0], 0, &abort_flag)) && !s_chunk[0].end) {
+      int n_tiles = s_chunk[0].n_tiles;
+      emit(0, n_tiles, &tm_k);
+      for (int u = 0; ok; ++u) {
+        const int rs = (u + 1) % kRing;
+        if (!(ok = mbar_wait_warp(&bar_cfull[rs], ((u + 1) / kRing) & 1, &abort_flag))) break;
+        const int end = s_chunk[rs].end, next = s_chunk[rs].n_tiles;
+        if (!end) emit(u + 1, next, &tm_k);
+        emit(u, n_tiles, &tm_v);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar_cempty[u % kRing]);
+        if (end) break;
+        n_tiles = next;
       }
-      emit(cur, cs, &tm_v);
-      cur = nxt;
-      nxt = after;
-      have = have_next;
-      have_next = have_after;
-      ++cs;
     }
     if (lane == 0) {
       griddep_launch_dependents();
-      if (walk.counted) {
-        // the last CTA to finish taking work resets the counter for the next launch
-        __threadfence();
-        if (atomicAdd(p.work + 1, 1) == static_cast<int>(gridDim.x) - 1) {
-          p.work[0] = 0;
-          p.work[1] = 0;
-        }
-      }
       if (!ok)
         for (int s = 0; s < STAGES; ++s) mbar_wait_drain(&bar_full[s], ph ^ (s < st ? 0 : 1));
     }
@@ -558,6 +548,69 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     }
     if (elect_one()) umma_commit(&bar_done);
     __syncwarp();
+  } else if (warp == 6) {
+    // =================================================================== the walk, queries
+    bool ok = true;
+    Walk<kChunk> walk;
+    walk.init(p, lane);
+    uint4 qr[N / 2];
+    int q_exp = 0, q_loads = 0;
+    Chunk c;
+    for (int seq = 0; ok; ++seq) {
+      const int rs = seq % kRing;
+      const bool have = walk.next(p, lane, c);
+      PageLoads<F::kChunkPages> pages;
+      if (have) {
+        if (c.first) {
+#pragma unroll
+          for (int i = 0; i < N / 2; ++i) {
+            const int n = 2 * i + (lane >> 4);
+            const int pos = c.rg * p.lsub + n / p.G;
+            qr[i] = make_uint4(0, 0, 0, 0);
+            if (n < p.rows && pos < p.L)
+              qr[i] = __ldg(reinterpret_cast<const uint4*>(
+                  p.q + ((static_cast<size_t>(c.b) * p.L + pos) * p.Hq + c.kvh * p.G + n % p.G) * 128) + (lane & 15));
+          }
+        }
+        pages.ask(p, c, lane);
+        if (c.first) {
+          float most = 0.f;
+#pragma unroll
+          for (int i = 0; i < N / 2; ++i) most = fmaxf(most, magnitude(qr[i]));
+          q_exp = q_exponent(warp_max(most));
+        }
+        c.q_scale = pow2(q_exp) * p.scale_log2;
+      } else {
+        c.end = 1;
+      }
+      if (!(ok = mbar_wait_warp(&bar_cempty[rs], ((seq / kRing) & 1) ^ 1, &abort_flag))) break;
+      if (have) pages.give(s_page[rs], s_scale[rs], lane);
+      __syncwarp();
+      if (lane == 0) {
+        s_chunk[rs] = c;
+        mbar_arrive(&bar_cfull[rs]);
+      }
+      if (!have) break;
+      if (!c.first) continue;
+      // the queries' parts into shared memory, once the MMAs on the last ones are done
+      if (!(ok = mbar_wait_warp(&bar_qempty, (q_loads & 1) ^ 1, &abort_flag))) break;
+      const float inv = pow2(-q_exp);
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        const int n = 2 * i + (lane >> 4);
+        const uint32_t u[4] = {qr[i].x, qr[i].y, qr[i].z, qr[i].w};
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) split_e4m3x2(bf16_lo(u[k]) * inv, bf16_hi(u[k]) * inv, hi[k], lo[k]);
+        const uint32_t at = n * 128 + ((((lane & 15) >> 1) ^ (n & 7)) << 4) + (lane & 1) * 8;
+        *reinterpret_cast<uint2*>(sQ + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+        *reinterpret_cast<uint2*>(sQ + N * 128 + at) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar_qfull);
+      ++q_loads;
+    }
   } else {
     // =================================================================== softmax, epilogue
     const int q4 = warp & 3;
@@ -643,26 +696,37 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       }
       // the weights, tile by tile, into shared memory
       {
-        float mr[N];
+        // (32 rows leave no registers for the maxima and a tile ahead)
+        constexpr bool kAhead = N <= 16;
+        float mr[kAhead ? N : 1];
+        if constexpr (kAhead) {
 #pragma unroll
-        for (int n = 0; n < N; ++n) mr[n] = s_m[n] - kWeightExp;
+          for (int n = 0; n < N; ++n) mr[n] = s_m[n] - kWeightExp;
+        }
         uint32_t r[N];
+        if constexpr (kAhead) {
 #pragma unroll
-        for (int cg = 0; cg < N / 16; ++cg) tmem_ld16(tS + cg * 16, *reinterpret_cast<uint32_t(*)[16]>(r + cg * 16));
+          for (int cg = 0; cg < N / 16; ++cg) tmem_ld16(tS + cg * 16, *reinterpret_cast<uint32_t(*)[16]>(r + cg * 16));
+        }
         for (int j = 0; j < c.n_tiles && ok; ++j) {
           const float2 sc = s_scale[rs][j * kTilePages + (x >> 4)];
           const float a = sc.x * c.q_scale, inv = ex2(-sc.y);
           const bool valid = c.t0 + j * kTile + x < c.t_end;
+          if constexpr (!kAhead) {
+#pragma unroll
+            for (int cg = 0; cg < N / 16; ++cg) tmem_ld16(tS + j * N + cg * 16, *reinterpret_cast<uint32_t(*)[16]>(r + cg * 16));
+          }
           tmem_wait_ld();
 #pragma unroll
           for (int cg = 0; cg < N / 16; ++cg) tmem_regs_ready(*reinterpret_cast<uint32_t(*)[16]>(r + cg * 16));
           float w[N];
 #pragma unroll
           for (int n = 0; n < N; ++n) {
-            w[n] = valid ? ex2(fmaf(__uint_as_float(r[n]), a, sc.y - mr[n])) : 0.f;
+            const float m = kAhead ? mr[kAhead ? n : 0] : s_m[n] - kWeightExp;
+            w[n] = valid ? ex2(fmaf(__uint_as_float(r[n]), a, sc.y - m)) : 0.f;
             l[n] = fmaf(w[n], inv, l[n]);
           }
-          if (j + 1 < c.n_tiles) {
+          if (kAhead && j + 1 < c.n_tiles) {
 #pragma unroll
             for (int cg = 0; cg < N / 16; ++cg)
               tmem_ld16(tS + (j + 1) * N + cg * 16, *reinterpret_cast<uint32_t(*)[16]>(r + cg * 16));
@@ -742,6 +806,16 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             st_global_hint(mine + N * 128 + x, s_m[x], keep);
             st_global_hint(mine + N * 129 + x, s_l[x], keep);
           }
+          if (p.join_here) {
+            __threadfence();
+            named_barrier(1, kSoftmaxThreads);
+            if (x == 0) s_join = atomicAdd(p.work + 1 + c.u0, 1) == c.parts - 1;
+            named_barrier(1, kSoftmaxThreads);
+            if (s_join) {
+              __threadfence();
+              join_parts<N>(p, c, x, s_m, s_l, s_red);
+            }
+          }
         }
         tc_fence_before();
       }
@@ -759,6 +833,16 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, F::kTmemCols);
+  }
+  if (p.join_here && warp == 0) {
+    // the last CTA to end leaves the counters as it found them
+    int last = 0;
+    if (lane == 0) {
+      __threadfence();
+      last = atomicAdd(p.work, 1) == static_cast<int>(gridDim.x) - 1;
+    }
+    if (__shfl_sync(0xffffffffu, last, 0))
+      for (int u = lane; u <= static_cast<int>(gridDim.x); u += 32) p.work[u] = 0;
   }
   if (threadIdx.x == 0 && abort_flag) atomicOr(p.err, BDLM_DEVERR_TIMEOUT);
 }
@@ -910,48 +994,27 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       tma_prefetch_desc(&tm_v);
     }
     const uint64_t policy = l2_policy_evict_first();
-    const int absent = p.num_pages * p.Hkv;
-    int my_cum = 0, kst = 0, vst = 0, q_loads = 0, seq = -1;
+    int kst = 0, vst = 0, q_loads = 0, seq = -1;
     uint32_t kph = 0, vph = 0;
     bool ok = true;
     Walk<kChunk> walk;
-    walk.init(p, lane, my_cum);
+    walk.init(p, lane);
     auto prepare = [&](Chunk& c) -> bool {
-      const bool have = walk.next(p, lane, my_cum, c);
+      const bool have = walk.next(p, lane, c);
       ++seq;
       const int rs = seq % kRing;
-      float2 sc[kChunkPages / 32];
+      PageLoads<kChunkPages> pages;
       if (have) {
-        int* page = s_page[seq % 3];
-        const int at = c.t0 / kPage, n = min(c.n_tiles * kTilePages, (c.t_end - c.t0 + kPage - 1) / kPage);
-        int bad = 0;
-#pragma unroll
-        for (int i = 0; i < kChunkPages / 32; ++i) {
-          const int q = i * 32 + lane;
-          int id = q < n ? __ldg(p.page_table + static_cast<size_t>(c.b) * p.max_pages + at + q) : -1;
-          if (id < 0 || id >= p.num_pages) {
-            bad |= q < n;
-            id = -1;
-          }
-          const int unit = id * p.Hkv + c.kvh;
-          sc[i] = id >= 0 ? __ldg(p.scales + unit) : make_float2(0.f, 0.f);
-          page[q] = id >= 0 ? unit : absent;
-        }
+        pages.ask(p, c, lane);
         c.q_scale = __ldg(p.q_scale + (static_cast<size_t>(c.b) * p.Hkv + c.kvh) * p.row_groups + c.rg) * p.scale_log2;
-        if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.err, BDLM_DEVERR_PAGE);
+      } else {
+        c.end = 1;
       }
       if (ok) ok = mbar_wait_warp<true>(&bar_cempty[rs], ((seq / kRing) & 1) ^ 1, &abort_flag);
-      if (have) {
-#pragma unroll
-        for (int i = 0; i < kChunkPages / 32; ++i) s_scale[rs][i * 32 + lane] = page_scale(sc[i]);
-      }
+      if (have) pages.give(s_page[seq % 3], s_scale[rs], lane);
       __syncwarp();
       if (lane == 0) {
-        if (have) {
-          s_chunk[rs] = c;
-        } else {
-          s_chunk[rs].end = 1;
-        }
+        s_chunk[rs] = c;
         mbar_arrive(&bar_cfull[rs]);
       }
       return have;
@@ -1007,13 +1070,6 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     }
     if (lane == 0) {
       griddep_launch_dependents();
-      if (walk.counted) {
-        __threadfence();
-        if (atomicAdd(p.work + 1, 1) == static_cast<int>(gridDim.x) - 1) {
-          p.work[0] = 0;
-          p.work[1] = 0;
-        }
-      }
       if (!ok) {
         for (int s = 0; s < KS; ++s) mbar_wait_drain(&bar_kfull[s], kph ^ (s < kst ? 0 : 1));
         for (int s = 0; s < VS; ++s) mbar_wait_drain(&bar_vfull[s], vph ^ (s < vst ? 0 : 1));
@@ -1415,7 +1471,7 @@ __global__ void __launch_bounds__(256) split_q_kernel(const Params p, uint8_t* _
   }
 }
 
-// Tiles of the sequences before each, for more than 32 sequences.  One CTA.
+// Tiles of the sequences before each, for more than kFewSequences.  One CTA.
 constexpr int kCumThreads = 1024;
 __global__ void __launch_bounds__(kCumThreads) cum_tiles_kernel(const Params p, int* __restrict__ cum) {
   __shared__ int s_warp[32];
@@ -1460,19 +1516,24 @@ __global__ void __launch_bounds__(256) join_kernel(const Params p, int n_rows, i
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int lists = p.Hkv * p.row_groups;
   const int b = blockIdx.x / lists, list = blockIdx.x - b * lists;
-  long long sum = 0, before = 0;
   bool ok;
+  int sum, before;
   if (p.cum != nullptr) {
     sum = __ldg(p.cum + p.B);
     before = __ldg(p.cum + b);
   } else {
-    const int n = lane < p.B ? (kv_tokens(p, lane, &ok) + kTile - 1) / kTile : 0;
-    sum = __reduce_add_sync(0xffffffffu, n);
-    before = __reduce_add_sync(0xffffffffu, lane < b ? n : 0);
+    sum = before = 0;
+    for (int i = lane; i < p.B; i += 32) {
+      const int n = (kv_tokens(p, i, &ok) + kTile - 1) / kTile;
+      sum += n;
+      if (i < b) before += n;
+    }
+    sum = __reduce_add_sync(0xffffffffu, sum);
+    before = __reduce_add_sync(0xffffffffu, before);
   }
   const int tiles = (kv_tokens(p, b, &ok) + kTile - 1) / kTile;
-  const long long per = unit_tiles(sum * lists, ctas, p.rounds);
-  const long long c0 = before * lists + static_cast<long long>(list) * tiles;
+  const long long per = unit_tiles(static_cast<long long>(sum) * lists, ctas);
+  const long long c0 = static_cast<long long>(before) * lists + static_cast<long long>(list) * tiles;
   const int u0 = static_cast<int>(c0 / per), u1 = static_cast<int>((c0 + tiles - 1) / per);
   if (u0 == u1) return;
   const int ns = u1 - u0 + 1;
@@ -1571,7 +1632,7 @@ cudaError_t launch_few(const CUtensorMap& tk, const CUtensorMap& tv, const Param
     return cudaFuncSetAttribute(few_rows_kernel<N, STAGES>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
   });
   if (e != cudaSuccess) return e;
-  return launch_pdl(few_rows_kernel<N, STAGES>, dim3(grid), dim3(64 + kSoftmaxThreads), smem, stream, tk, tv, p);
+  return launch_pdl(few_rows_kernel<N, STAGES>, dim3(grid), dim3(kFewThreads), smem, stream, tk, tv, p);
 }
 
 }  // namespace
@@ -1589,10 +1650,12 @@ Kv8AttnPlan plan_attention_kv8(int B, int L, int Hq, int Hkv, int max_pages, int
   const long long tiles = lists * ((max_pages + kTilePages - 1) / kTilePages);
   const long long ctas = many ? num_sms : 2ll * num_sms;
   pl.grid = static_cast<int>(tiles < ctas ? tiles : ctas);
-  pl.rounds = many ? 1 : kRounds;
-  const long long most = static_cast<long long>(kRounds) * pl.grid;
   // (a tile a list at most: no list is cut)
-  pl.parts = max_pages <= kTilePages ? 0 : 2 * (tiles < most ? tiles : most);
+  pl.parts = max_pages <= kTilePages ? 0 : 2 * pl.grid;
+  // Lists of few parts are joined by the CTA that writes the last (128 blocks of 4 over 512-4096 tokens: a kernel for it
+  // takes 10 us more); many parts of a list are read by more warps.
+  pl.join_here = pl.parts > 0 && !many && lists * kFewParts / 2 >= pl.grid;
+  pl.work_bytes = pl.join_here ? (static_cast<size_t>(pl.grid) + 1) * sizeof(int) : 0;
   pl.part_bytes = static_cast<size_t>(pl.parts) * pl.n_rows * kPartRow * sizeof(float);
   auto place = [](size_t& end, size_t bytes) {
     const size_t at = (end + 255) / 256 * 256;
@@ -1600,7 +1663,7 @@ Kv8AttnPlan plan_attention_kv8(int B, int L, int Hq, int Hkv, int max_pages, int
     return at;
   };
   pl.bytes = pl.part_bytes;
-  pl.cum_offset = place(pl.bytes, B > 32 ? (static_cast<size_t>(B) + 1) * sizeof(int) : 0);
+  pl.cum_offset = place(pl.bytes, B > kFewSequences ? (static_cast<size_t>(B) + 1) * sizeof(int) : 0);
   pl.q_offset = place(pl.bytes, many ? static_cast<size_t>(B) * L * Hq * 256 : 0);
   pl.q_scale_offset = place(pl.bytes, many ? static_cast<size_t>(lists) * sizeof(float) : 0);
   return pl;
@@ -1642,11 +1705,11 @@ cudaError_t launch_attention_kv8(const Kv8AttnParams& a, const Kv8AttnPlan& pl, 
   p.lsub = pl.lsub;
   p.row_groups = pl.row_groups;
   p.rows = pl.rows;
-  p.rounds = pl.rounds;
+  p.join_here = pl.join_here;
   p.scale_log2 = a.scale_log2;
   const unsigned lists = static_cast<unsigned>(p.B) * p.Hkv * p.row_groups;
   cudaError_t e;
-  if (a.B > 32) {
+  if (a.B > kFewSequences) {
     int* cum = reinterpret_cast<int*>(at + pl.cum_offset);
     e = launch_pdl(cum_tiles_kernel, dim3(1), dim3(kCumThreads), 0, stream, p, cum);
     if (e != cudaSuccess) return e;
@@ -1660,7 +1723,7 @@ cudaError_t launch_attention_kv8(const Kv8AttnParams& a, const Kv8AttnPlan& pl, 
   } else {
     e = pl.n_rows == 16 ? launch_few<16, 6>(tk, tv, p, pl.grid, stream) : launch_few<32, 5>(tk, tv, p, pl.grid, stream);
   }
-  if (e != cudaSuccess || pl.parts == 0) return e;
+  if (e != cudaSuccess || pl.parts == 0 || pl.join_here) return e;
   return launch_pdl(join_kernel, dim3(lists, (p.rows + 7) / 8), dim3(256), 0, stream, p, pl.n_rows, pl.grid);
 }
 

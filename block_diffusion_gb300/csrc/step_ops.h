@@ -65,14 +65,15 @@ struct Kv8AttnParams {
 struct Kv8AttnPlan {
   int lsub, row_groups, rows;   // block positions and query rows of a row group
   int n_rows;                   // rows padded
-  int grid, rounds;
+  int grid;
+  bool join_here;               // lists that are cut are joined by the attention kernel itself
   long long parts;
-  size_t part_bytes, cum_offset, q_offset, q_scale_offset, bytes;   // of the workspace
+  size_t part_bytes, cum_offset, q_offset, q_scale_offset, bytes, work_bytes;   // of the workspace
 };
 Kv8AttnPlan plan_attention_kv8(int B, int L, int Hq, int Hkv, int max_pages, int num_sms);
 // tm_k, tm_v: units of 16 x 128 bytes, boxes of one.  tm_q (n_rows >= 128): the parts of the queries at q_offset,
-// [B * L][Hq][256] bytes, boxes of 128 bytes x G heads x lsub positions.  data: plan.bytes; work: two ints, zero
-// between calls.
+// [B * L][Hq][256] bytes, boxes of 128 bytes x G heads x lsub positions.  data: plan.bytes; work: plan.work_bytes,
+// zero between calls.
 cudaError_t launch_attention_kv8(const Kv8AttnParams& p, const Kv8AttnPlan& plan, const CUtensorMap& tm_q,
                                  const CUtensorMap& tm_k, const CUtensorMap& tm_v, void* data, int* work,
                                  cudaStream_t stream);
