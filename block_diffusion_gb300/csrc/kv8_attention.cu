@@ -155,6 +155,11 @@ __device__ __forceinline__ void split_e4m3x2(float a, float b, uint32_t& hi, uin
   lo = e4m3x2(a - h.x, b - h.y);
 }
 
+__device__ __forceinline__ uint32_t half2_bits(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 // The largest of a few bf16 pairs' magnitudes as a float (NaN aside).
 __device__ __forceinline__ float magnitude(const uint4& w) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -263,15 +268,25 @@ struct PageLoads {
   int unit[kEach];
   float2 scale[kEach];
 
-  __device__ __forceinline__ void ask(const Params& p, const Chunk& c, int lane) {
-    const int at = c.t0 / kPage, n = min(c.n_tiles * kTilePages, (c.t_end - c.t0 + kPage - 1) / kPage);
-    int bad = 0;
+  static __device__ __forceinline__ int count(const Chunk& c) {
+    return min(c.n_tiles * kTilePages, (c.t_end - c.t0 + kPage - 1) / kPage);
+  }
+  __device__ __forceinline__ void ask_pages(const Params& p, const Chunk& c, int lane) {
+    const int at = c.t0 / kPage, n = count(c);
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
       const int q = i * 32 + lane;
-      int id = q < n ? __ldg(p.page_table + static_cast<size_t>(c.b) * p.max_pages + at + q) : -1;
+      unit[i] = q < n ? __ldg(p.page_table + static_cast<size_t>(c.b) * p.max_pages + at + q) : -1;
+    }
+  }
+  __device__ __forceinline__ void ask_scales(const Params& p, const Chunk& c, int lane) {
+    const int n = count(c);
+    int bad = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      int id = unit[i];
       if (id < 0 || id >= p.num_pages) {
-        bad |= q < n;
+        bad |= i * 32 + lane < n;
         id = -1;
       }
       unit[i] = id >= 0 ? id * p.Hkv + c.kvh : p.num_pages * p.Hkv;   // past the pool: a box there reads zeros
@@ -305,6 +320,7 @@ constexpr int kPartRow = 130;   // floats of a row's part: O, m, l
 
 constexpr int kFewThreads = 96 + kSoftmaxThreads;
 
+// N: rows of the MMAs, NC: rows that the softmax computes (the others' weights stay zero).
 template <int N, int STAGES>
 struct Few {
   static constexpr int kTmemCols = 256;   // two CTAs per SM
@@ -313,50 +329,68 @@ struct Few {
   static constexpr size_t kSmem = 1024 + N * 256 + static_cast<size_t>(STAGES) * kStage + 2 * N * 256;
 };
 
+// w's float16 pair in two e4m3 parts: each the low byte for the low one.
+__device__ __forceinline__ void split_half2(uint32_t w, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = *reinterpret_cast<const __half2*>(&w);
+  hi = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(h), __NV_SATFINITE, __NV_E4M3);
+  const __half2_raw back = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hi), __NV_E4M3);
+  lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(__hsub2(h, *reinterpret_cast<const __half2*>(&back))), __NV_SATFINITE,
+                                  __NV_E4M3);
+}
+
 // Joins the parts of chunk c's list, in their order whoever comes last:
-//     out = sum_s e_s O_s / sum_s e_s l_s,   e_s = 2^(m_s - M).
-// 128 threads, a head dim each.
-template <int N>
-__device__ __forceinline__ void join_parts(const Params& p, const Chunk& c, int x, float* s_m, float* s_l, float (*s_red)[N]) {
+//     out = sum_s e_s O_s / sum_s e_s l_s,   e_s = 2^(m_s - M),
+// two parts at a time, M and the sums brought along.  128 threads, a head dim each.
+template <int N, int NC>
+__device__ __forceinline__ void join_parts(const Params& p, const Chunk& c, int x, size_t row, int live, float* s_m, float* s_l,
+                                           float* s_alpha, float (*s_red)[N]) {
   auto part = [&](int s) { return p.part + static_cast<size_t>(2 * (c.u0 + s) + (s == 0 ? 1 : 0)) * N * kPartRow; };
-  if (x < N) {
-    float M = -CUDART_INF_F, den = 0.f;
-#pragma unroll 4
-    for (int s = 0; s < c.parts; ++s) M = fmaxf(M, __ldcg(part(s) + N * 128 + x));
-#pragma unroll 4
-    for (int s = 0; s < c.parts; ++s) den = fmaf(ex2(__ldcg(part(s) + N * 128 + x) - M), __ldcg(part(s) + N * 129 + x), den);
-    s_m[x] = M;
-    s_l[x] = den;
+  float acc[NC];
+#pragma unroll
+  for (int n = 0; n < NC; ++n) acc[n] = 0.f;
+  float M = -CUDART_INF_F, den = 0.f;   // threads x < NC: of row x
+#pragma unroll 1
+  for (int s0 = 0; s0 < c.parts; s0 += 2) {
+    const bool two = s0 + 1 < c.parts;
+    const float *a = part(s0), *b = part(two ? s0 + 1 : s0);
+    float o0[NC], o1[NC];
+#pragma unroll
+    for (int n = 0; n < NC; ++n) {
+      o0[n] = n < live ? __ldcg(a + n * 128 + x) : 0.f;
+      o1[n] = n < live ? __ldcg(b + n * 128 + x) : 0.f;
+    }
+    if (x < NC) {
+      const float m0 = __ldcg(a + N * 128 + x), l0 = __ldcg(a + N * 129 + x);
+      const float m1 = two ? __ldcg(b + N * 128 + x) : -CUDART_INF_F, l1 = __ldcg(b + N * 129 + x);
+      const float top = fmaxf(M, fmaxf(m0, m1));
+      const float was = ex2(M - top), e0 = ex2(m0 - top), e1 = ex2(m1 - top);
+      den = fmaf(den, was, fmaf(e0, l0, e1 * l1));
+      M = top;
+      s_alpha[x] = was;
+      s_red[0][x] = e0;
+      s_red[1][x] = e1;
+    }
+    named_barrier(1, kSoftmaxThreads);
+#pragma unroll
+    for (int n = 0; n < NC; ++n) acc[n] = fmaf(acc[n], s_alpha[n], fmaf(s_red[0][n], o0[n], s_red[1][n] * o1[n]));
+    named_barrier(1, kSoftmaxThreads);
   }
+  if (x < NC) s_l[x] = 1.f / den;
   named_barrier(1, kSoftmaxThreads);
-  float acc[N];
+  int g = 0;
 #pragma unroll
-  for (int n = 0; n < N; ++n) acc[n] = 0.f;
-  for (int s0 = 0; s0 < c.parts; s0 += 4) {
-    if (x < 4 * N) {
-      const int s = s0 + x / N, n = x % N;
-      s_red[x / N][n] = s < c.parts ? ex2(__ldcg(part(s) + N * 128 + n) - s_m[n]) : 0.f;
+  for (int n = 0; n < NC; ++n) {
+    if (n >= live) break;
+    p.out[row * 128 + x] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[n] * s_l[n]));
+    ++row;
+    if (++g == p.G) {
+      g = 0;
+      row += p.Hq - p.G;
     }
-    named_barrier(1, kSoftmaxThreads);
-    const int cnt = min(4, c.parts - s0);
-    for (int i = 0; i < cnt; ++i) {
-      const float* o = part(s0 + i) + x;
-#pragma unroll
-      for (int n = 0; n < N; ++n)
-        if (n < p.rows) acc[n] = fmaf(s_red[i][n], __ldcg(o + n * 128), acc[n]);
-    }
-    named_barrier(1, kSoftmaxThreads);
-  }
-#pragma unroll
-  for (int n = 0; n < N; ++n) {
-    const int i = c.rg * p.lsub + n / p.G;
-    if (n < p.rows && i < p.L)
-      p.out[((static_cast<size_t>(c.b) * p.L + i) * p.Hq + static_cast<size_t>(c.kvh) * p.G + n % p.G) * 128 + x] =
-          __bfloat16_as_ushort(__float2bfloat16_rn(acc[n] / s_l[n]));
   }
 }
 
-template <int N, int STAGES>
+template <int N, int NC, int STAGES>
 __global__ void __launch_bounds__(kFewThreads, 2)
 few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Params p) {
   using F = Few<N, STAGES>;
@@ -365,7 +399,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* sQ = base;                  // two parts x N rows x 128 bytes, 128-byte swizzle
   uint8_t* sKV = sQ + N * 256;
-  uint8_t* sP = sKV + STAGES * kStage;   // two buffers of two parts x N rows x 128 bytes
+  uint8_t* sP = sKV + STAGES * kStage;   // two buffers of two parts x N / 16 x 128 tokens x 16 bytes, a row each
   __shared__ uint64_t bar_qfull, bar_qempty, bar_full[STAGES], bar_empty[STAGES];
   __shared__ uint64_t bar_sfull[2], bar_sfree[2], bar_pfull[2], bar_pempty[2];
   __shared__ uint64_t bar_oready, bar_ofull[2], bar_done;
@@ -375,7 +409,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
   __shared__ int s_page[kRing][F::kChunkPages];       // page * Hkv + head
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
-  __shared__ float s_m[N], s_alpha[N], s_l[N], s_red[4][N];
+  __shared__ __align__(16) float s_m[N], s_alpha[N], s_l[N], s_red[4][N];
   __shared__ int s_need[2], s_pflag[2], s_join;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -407,6 +441,11 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
   if (warp == 1) {
     tmem_alloc(&tmem_base, F::kTmemCols);
     tmem_relinquish();
+  }
+  if constexpr (NC < N) {
+    for (int o = threadIdx.x * 16; o < 2 * N * 256; o += kFewThreads * 16)
+      *reinterpret_cast<uint4*>(sP + o) = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
   }
   tc_fence_before();
   __syncthreads();
@@ -458,8 +497,8 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
   } else if (warp == 1) {
     // =================================================================== MMA issuer
     constexpr uint32_t kIdescS = idesc_e4m3_f32(128, N, false, false);
-    constexpr uint32_t kIdescO = idesc_e4m3_f32(128, N, true, false);
-    const uint64_t q_desc = smem_desc(smem_u32(sQ), 16, 1024), p_desc = smem_desc(smem_u32(sP), 16, 1024);
+    constexpr uint32_t kIdescO = idesc_e4m3_f32(128, N, true, true);
+    const uint64_t q_desc = smem_desc(smem_u32(sQ), 16, 1024), p_desc = smem_desc_plain(smem_u32(sP), 128, kTile * 16);
     const uint64_t k_desc = smem_desc(smem_u32(sKV), 16, 1024), v_desc = smem_desc(smem_u32(sKV), kStage, 1024);
     bool ok = true;
     int st = 0, pcount = 0, ocount = 0, q_used = 0;
@@ -514,8 +553,8 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         const int steps = (valid + 31) / 32;
         if (elect_one()) {
           for (int q = 0; q < steps; ++q) {
-            umma_e4m3(tO, vd + q * 256, pd + q * 2, kIdescO, first && j == 0 && q == 0 ? 0u : 1u);
-            umma_e4m3(tO, vd + q * 256, pd + N * 8 + q * 2, kIdescO, 1u);
+            umma_e4m3(tO, vd + q * 256, pd + q * 32, kIdescO, first && j == 0 && q == 0 ? 0u : 1u);
+            umma_e4m3(tO, vd + q * 256, pd + N * 8 + q * 32, kIdescO, 1u);
           }
           umma_commit(&bar_pempty[pb]);
           umma_commit(&bar_empty[st]);
@@ -554,46 +593,38 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     Walk<kChunk> walk;
     walk.init(p, lane);
     uint4 qr[N / 2];
-    int q_exp = 0, q_loads = 0;
-    Chunk c;
-    for (int seq = 0; ok; ++seq) {
-      const int rs = seq % kRing;
-      const bool have = walk.next(p, lane, c);
-      PageLoads<F::kChunkPages> pages;
-      if (have) {
-        if (c.first) {
+    int q_exp = 0, q_loads = 0, seq = 0;
+    auto ask_q = [&](const Chunk& c) {
 #pragma unroll
-          for (int i = 0; i < N / 2; ++i) {
-            const int n = 2 * i + (lane >> 4);
-            const int pos = c.rg * p.lsub + n / p.G;
-            qr[i] = make_uint4(0, 0, 0, 0);
-            if (n < p.rows && pos < p.L)
-              qr[i] = __ldg(reinterpret_cast<const uint4*>(
-                  p.q + ((static_cast<size_t>(c.b) * p.L + pos) * p.Hq + c.kvh * p.G + n % p.G) * 128) + (lane & 15));
-          }
-        }
-        pages.ask(p, c, lane);
-        if (c.first) {
-          float most = 0.f;
-#pragma unroll
-          for (int i = 0; i < N / 2; ++i) most = fmaxf(most, magnitude(qr[i]));
-          q_exp = q_exponent(warp_max(most));
-        }
-        c.q_scale = pow2(q_exp) * p.scale_log2;
-      } else {
-        c.end = 1;
+      for (int i = 0; i < N / 2; ++i) {
+        const int n = 2 * i + (lane >> 4);
+        const int pos = c.rg * p.lsub + n / p.G;
+        qr[i] = make_uint4(0, 0, 0, 0);
+        if (n < p.rows && pos < p.L)
+          qr[i] = __ldg(reinterpret_cast<const uint4*>(
+              p.q + ((static_cast<size_t>(c.b) * p.L + pos) * p.Hq + c.kvh * p.G + n % p.G) * 128) + (lane & 15));
       }
-      if (!(ok = mbar_wait_warp(&bar_cempty[rs], ((seq / kRing) & 1) ^ 1, &abort_flag))) break;
-      if (have) pages.give(s_page[rs], s_scale[rs], lane);
+    };
+    // Publishes chunk number seq, and then the parts of its queries, once the MMAs on the last ones are done.
+    auto publish = [&](Chunk& c, const PageLoads<F::kChunkPages>& pages) {
+      if (c.first && !c.end) {
+        float most = 0.f;
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) most = fmaxf(most, magnitude(qr[i]));
+        q_exp = q_exponent(warp_max(most));
+      }
+      c.q_scale = pow2(q_exp) * p.scale_log2;
+      const int rs = seq % kRing;
+      if (!(ok = mbar_wait_warp(&bar_cempty[rs], ((seq / kRing) & 1) ^ 1, &abort_flag))) return;
+      if (!c.end) pages.give(s_page[rs], s_scale[rs], lane);
       __syncwarp();
       if (lane == 0) {
         s_chunk[rs] = c;
         mbar_arrive(&bar_cfull[rs]);
       }
-      if (!have) break;
-      if (!c.first) continue;
-      // the queries' parts into shared memory, once the MMAs on the last ones are done
-      if (!(ok = mbar_wait_warp(&bar_qempty, (q_loads & 1) ^ 1, &abort_flag))) break;
+      ++seq;
+      if (c.end || !c.first) return;
+      if (!(ok = mbar_wait_warp(&bar_qempty, (q_loads & 1) ^ 1, &abort_flag))) return;
       const float inv = pow2(-q_exp);
 #pragma unroll
       for (int i = 0; i < N / 2; ++i) {
@@ -610,13 +641,41 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar_qfull);
       ++q_loads;
+    };
+    // The first two chunks are asked for together: once the copies of the first are under way a look-up takes
+    // microseconds, and the copies would stand still for the second's.  From then on the walk is chunks ahead.
+    Chunk c, d;
+    PageLoads<F::kChunkPages> pages, ahead;
+    c.end = !walk.next(p, lane, c);
+    if (!c.end) {
+      ask_q(c);
+      pages.ask_pages(p, c, lane);
+      d.end = !walk.next(p, lane, d);
+      if (!d.end) ahead.ask_pages(p, d, lane);
+      pages.ask_scales(p, c, lane);
+      if (!d.end) ahead.ask_scales(p, d, lane);
+    }
+    publish(c, pages);
+    if (!c.end && ok) {
+      if (!d.end && d.first) ask_q(d);
+      publish(d, ahead);
+      while (!d.end && ok) {
+        d.end = !walk.next(p, lane, d);
+        if (!d.end) {
+          if (d.first) ask_q(d);
+          ahead.ask_pages(p, d, lane);
+          ahead.ask_scales(p, d, lane);
+        }
+        publish(d, ahead);
+      }
     }
   } else {
     // =================================================================== softmax, epilogue
     const int q4 = warp & 3;
     const int x = (q4 << 5) | lane;   // tensor-memory lane: token of a tile, or head dim
     const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
-    float l[N];
+    constexpr int CW = NC < 16 ? NC : 16;   // rows taken at once
+    float2 l[NC / 2];
     bool ok = true;
     int pcount = 0;
     for (int u = 0; ok; ++u) {
@@ -626,40 +685,58 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       if (c.end) break;
       if (c.first) {
 #pragma unroll
-        for (int n = 0; n < N; ++n) l[n] = 0.f;
-        if (x < N) s_m[x] = -CUDART_INF_F;
+        for (int n = 0; n < NC / 2; ++n) l[n] = make_float2(0.f, 0.f);
+        if (x < NC) s_m[x] = -CUDART_INF_F;
       }
       const uint32_t tS = tmem + lane_off + static_cast<uint32_t>((u & 1) * kChunk * N);
       if (!(ok = mbar_wait_warp(&bar_sfull[u & 1], (u >> 1) & 1, &abort_flag))) break;
       tc_fence_after();
-      // the exact maxima of x over the chunk
+      // the exact maxima of x over the chunk (behind the last token scores may be anything: -inf)
+      const int last_tile = (c.t_end - c.t0 - 1) / kTile;
+      const bool cut = c.t_end - c.t0 - last_tile * kTile <= x;   // this thread's token of it is past the end
+      auto load = [&](int j, int g, uint32_t (&r)[CW]) {
+        if constexpr (CW == 8)
+          tmem_ld8(tS + j * N, r);
+        else
+          tmem_ld16(tS + j * N + g * 16, r);
+      };
+      auto ready = [&](int j, uint32_t (&r)[CW]) {
+        tmem_wait_ld();
+        tmem_regs_ready(r);
+        if (j == last_tile && cut) {
 #pragma unroll
-      for (int cg = 0; cg < N / 16; ++cg) {
-        float mx[16];
+          for (int n = 0; n < CW; ++n) r[n] = 0xFF800000u;
+        }
+      };
 #pragma unroll
-        for (int k = 0; k < 16; ++k) mx[k] = -CUDART_INF_F;
+      for (int g = 0; g < NC / CW; ++g) {
+        float mx[CW];
+#pragma unroll
+        for (int n = 0; n < CW; ++n) mx[n] = -CUDART_INF_F;
         for (int j = 0; j < c.n_tiles; ++j) {
-          uint32_t r[16];
-          tmem_ld16(tS + j * N + cg * 16, r);
+          uint32_t r[CW];
+          load(j, g, r);
           const float2 sc = s_scale[rs][j * kTilePages + (x >> 4)];
           const float a = sc.x * c.q_scale;
-          tmem_wait_ld();
-          tmem_regs_ready(r);
-          if (c.t0 + j * kTile + x < c.t_end) {
+          ready(j, r);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) mx[k] = fmaxf(mx[k], fmaf(__uint_as_float(r[k]), a, sc.y));
+          for (int n = 0; n < CW; n += 2) {
+            const float2 y = __ffma2_rn(make_float2(__uint_as_float(r[n]), __uint_as_float(r[n + 1])), make_float2(a, a), make_float2(sc.y, sc.y));
+            mx[n] = fmaxf(mx[n], y.x);
+            mx[n + 1] = fmaxf(mx[n + 1], y.y);
           }
         }
 #pragma unroll
-        for (int k = 0; k < 16; ++k) mx[k] = warp_max(mx[k]);
+        for (int n = 0; n < CW; ++n) mx[n] = warp_max(mx[n]);
         if (lane == 0) {
 #pragma unroll
-          for (int k = 0; k < 16; ++k) s_red[q4][cg * 16 + k] = mx[k];
+          for (int n = 0; n < CW; n += 4)
+            *reinterpret_cast<float4*>(&s_red[q4][g * CW + n]) = make_float4(mx[n], mx[n + 1], mx[n + 2], mx[n + 3]);
         }
       }
       named_barrier(1, kSoftmaxThreads);
       if (x == 0) s_need[(u + 1) & 1] = 0;   // every reader of that slot is past this barrier
-      if (x < N) {
+      if (x < NC) {
         const float mc = fmaxf(fmaxf(s_red[0][x], s_red[1][x]), fmaxf(s_red[2][x], s_red[3][x]));
         const float mo = s_m[x];
         float alpha = 1.f;
@@ -685,124 +762,136 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
           tmem_wait_ld();
           tmem_regs_ready(r);
 #pragma unroll
-          for (int k = 0; k < 16; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * s_alpha[cg * 16 + k]);
+          for (int k = 0; k < 16; ++k)
+            if (cg * 16 + k < NC) r[k] = __float_as_uint(__uint_as_float(r[k]) * s_alpha[cg * 16 + k]);
           tmem_st16(tO + lane_off + cg * 16, r);
         }
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&bar_oready);
 #pragma unroll
-        for (int n = 0; n < N; ++n) l[n] *= s_alpha[n];
+        for (int n = 0; n < NC / 2; ++n) l[n] = __fmul2_rn(l[n], make_float2(s_alpha[2 * n], s_alpha[2 * n + 1]));
       }
-      // the weights, tile by tile, into shared memory
+      // The weights, tile by tile, into shared memory.  2^(c sK q . k - m + 7) is what l adds up; times sV it is w, whose
+      // float16 (finer than both parts, and exact to subtract from) is split.
       {
         // (32 rows leave no registers for the maxima and a tile ahead)
-        constexpr bool kAhead = N <= 16;
-        float mr[kAhead ? N : 1];
+        constexpr bool kAhead = NC <= 16;
+        float2 mr[CW / 2];
         if constexpr (kAhead) {
 #pragma unroll
-          for (int n = 0; n < N; ++n) mr[n] = s_m[n] - kWeightExp;
+          for (int n = 0; n < CW / 2; ++n) mr[n] = make_float2(kWeightExp - s_m[2 * n], kWeightExp - s_m[2 * n + 1]);
         }
-        uint32_t r[N];
-        if constexpr (kAhead) {
-#pragma unroll
-          for (int cg = 0; cg < N / 16; ++cg) tmem_ld16(tS + cg * 16, *reinterpret_cast<uint32_t(*)[16]>(r + cg * 16));
-        }
+        uint32_t r[CW];
+        load(0, 0, r);
         for (int j = 0; j < c.n_tiles && ok; ++j) {
           const float2 sc = s_scale[rs][j * kTilePages + (x >> 4)];
-          const float a = sc.x * c.q_scale, inv = ex2(-sc.y);
-          const bool valid = c.t0 + j * kTile + x < c.t_end;
-          if constexpr (!kAhead) {
-#pragma unroll
-            for (int cg = 0; cg < N / 16; ++cg) tmem_ld16(tS + j * N + cg * 16, *reinterpret_cast<uint32_t(*)[16]>(r + cg * 16));
-          }
-          tmem_wait_ld();
-#pragma unroll
-          for (int cg = 0; cg < N / 16; ++cg) tmem_regs_ready(*reinterpret_cast<uint32_t(*)[16]>(r + cg * 16));
-          float w[N];
-#pragma unroll
-          for (int n = 0; n < N; ++n) {
-            const float m = kAhead ? mr[kAhead ? n : 0] : s_m[n] - kWeightExp;
-            w[n] = valid ? ex2(fmaf(__uint_as_float(r[n]), a, sc.y - m)) : 0.f;
-            l[n] = fmaf(w[n], inv, l[n]);
-          }
-          if (kAhead && j + 1 < c.n_tiles) {
-#pragma unroll
-            for (int cg = 0; cg < N / 16; ++cg)
-              tmem_ld16(tS + (j + 1) * N + cg * 16, *reinterpret_cast<uint32_t(*)[16]>(r + cg * 16));
-          }
+          const float a = sc.x * c.q_scale, sv = ex2(sc.y);
           const int pb = pcount & 1;
-          if (!(ok = mbar_wait_warp(&bar_pempty[pb], ((pcount >> 1) & 1) ^ 1, &abort_flag))) break;
-          uint8_t* pbuf = sP + pb * (N * 256) + (x & 15);
+          uint8_t* to = sP + pb * (N * 256) + x * 16;
 #pragma unroll
-          for (int n = 0; n < N; n += 2) {
-            uint32_t hi, lo;
-            split_e4m3x2(w[n], w[n + 1], hi, lo);
-            const uint32_t a0 = n * 128 + (((x >> 4) ^ (n & 7)) << 4), a1 = (n + 1) * 128 + (((x >> 4) ^ ((n + 1) & 7)) << 4);
-            pbuf[a0] = static_cast<uint8_t>(hi);
-            pbuf[a1] = static_cast<uint8_t>(hi >> 8);
-            pbuf[N * 128 + a0] = static_cast<uint8_t>(lo);
-            pbuf[N * 128 + a1] = static_cast<uint8_t>(lo >> 8);
+          for (int g = 0; g < NC / CW; ++g) {
+            ready(j, r);
+            if constexpr (!kAhead) {
+#pragma unroll
+              for (int n = 0; n < CW / 2; ++n) mr[n] = make_float2(kWeightExp - s_m[g * CW + 2 * n], kWeightExp - s_m[g * CW + 2 * n + 1]);
+            }
+            uint32_t w[CW / 2];   // float16 pairs
+#pragma unroll
+            for (int n = 0; n < CW / 2; ++n) {
+              const float2 y = __ffma2_rn(make_float2(__uint_as_float(r[2 * n]), __uint_as_float(r[2 * n + 1])), make_float2(a, a), mr[n]);
+              const float2 e = make_float2(ex2(y.x), ex2(y.y));
+              l[g * CW / 2 + n] = __fadd2_rn(l[g * CW / 2 + n], e);
+              const float2 z = __fmul2_rn(e, make_float2(sv, sv));
+              w[n] = half2_bits(z.x, z.y);
+            }
+            if (g + 1 < NC / CW)
+              load(j, g + 1, r);
+            else if (j + 1 < c.n_tiles)
+              load(j + 1, 0, r);
+            uint32_t hi[CW / 4], lo[CW / 4];
+#pragma unroll
+            for (int n = 0; n < CW / 4; ++n) {
+              uint32_t h[2], o[2];
+#pragma unroll
+              for (int k = 0; k < 2; ++k) split_half2(w[2 * n + k], h[k], o[k]);
+              hi[n] = h[0] | h[1] << 16;
+              lo[n] = o[0] | o[1] << 16;
+            }
+            if (g == 0 && !(ok = mbar_wait_warp(&bar_pempty[pb], ((pcount >> 1) & 1) ^ 1, &abort_flag))) break;
+            if constexpr (NC == 8) {
+              *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
+              *reinterpret_cast<uint2*>(to + N * 128) = make_uint2(lo[0], lo[1]);
+            } else {
+              *reinterpret_cast<uint4*>(to + g * (kTile * 16)) = make_uint4(hi[0], hi[1], hi[CW / 4 - 2], hi[CW / 4 - 1]);
+              *reinterpret_cast<uint4*>(to + N * 128 + g * (kTile * 16)) = make_uint4(lo[0], lo[1], lo[CW / 4 - 2], lo[CW / 4 - 1]);
+            }
           }
+          if (!ok) break;
           if (x == 0) s_pflag[pb] = j == 0 && need;
           fence_proxy_async_smem();
           tc_fence_before();
           mbar_arrive(&bar_pfull[pb]);
           ++pcount;
         }
-        if (!ok) tmem_wait_ld();
+        if (!ok) tmem_wait_ld();   // (a load may be under way)
       }
       if (!ok) break;
       tc_fence_before();
       mbar_arrive(&bar_sfree[u & 1]);
       if (c.last) {
+        // The code from here on is met once a list, each time from memory: loops, not their bodies in a row.
         if (!(ok = mbar_wait_warp(&bar_ofull[u & 1], (u >> 1) & 1, &abort_flag))) break;
         tc_fence_after();
+        // the rows' sums, through the weights' buffers (no MMA reads them now)
+        float* sums = reinterpret_cast<float*>(sP);
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-          float v = l[n];
-#pragma unroll
-          for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-          if (lane == 0) s_red[q4][n] = v;
+        for (int n = 0; n < NC / 2; ++n) {
+          sums[(2 * n) * kTile + x] = l[n].x;
+          sums[(2 * n + 1) * kTile + x] = l[n].y;
         }
         named_barrier(1, kSoftmaxThreads);
-        if (x < N) s_l[x] = (s_red[0][x] + s_red[1][x]) + (s_red[2][x] + s_red[3][x]);
+        {
+          constexpr int kEach = kSoftmaxThreads / NC;   // threads of a row
+          float v = 0.f;
+#pragma unroll 4
+          for (int i = x % kEach; i < kTile; i += kEach) v += sums[(x / kEach) * kTile + i];
+#pragma unroll
+          for (int off = kEach / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+          if (x % kEach == 0) s_l[x / kEach] = c.slot < 0 ? 1.f / v : v;
+        }
         named_barrier(1, kSoftmaxThreads);
-        if (c.slot < 0) {
-          int i = c.rg * p.lsub, g = 0;
-          uint16_t* o = p.out + ((static_cast<size_t>(c.b) * p.L + i) * p.Hq + static_cast<size_t>(c.kvh) * p.G) * 128 + x;
-          const size_t next = static_cast<size_t>(p.Hq - p.G) * 128;   // past the other KV heads
+        if constexpr (NC < N) {   // the rows that nothing is computed for read as zeros again
+          for (int o = x * 16; o < 2 * N * 256; o += kSoftmaxThreads * 16) *reinterpret_cast<uint4*>(sP + o) = make_uint4(0, 0, 0, 0);
+        }
+        const size_t row0 = (static_cast<size_t>(c.b) * p.L + c.rg * p.lsub) * p.Hq + static_cast<size_t>(c.kvh) * p.G;
+        const int live = min(p.rows, (p.L - c.rg * p.lsub) * p.G);   // rows of the group that there are
+        float* mine = p.part + static_cast<size_t>(c.slot < 0 ? 0 : c.slot) * N * kPartRow;
+        const uint64_t keep = l2_policy_evict_last();   // read back soon
+        int g = 0;
+        size_t row = row0;
+#pragma unroll 1
+        for (int n0 = 0; n0 < live; n0 += 4) {
+          uint32_t r[4];
+          tmem_ld4(tO + lane_off + n0, r);
+          tmem_wait_ld();
+          tmem_regs_ready(r);
 #pragma unroll
-          for (int cg = 0; cg < N / 16; ++cg) {
-            uint32_t r[16];
-            tmem_ld16(tO + lane_off + cg * 16, r);
-            tmem_wait_ld();
-            tmem_regs_ready(r);
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const int n = cg * 16 + k;
-              if (n < p.rows && i < p.L) *o = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(r[k]) / s_l[n]));
-              o += 128;
-              if (++g == p.G) {
-                g = 0;
-                ++i;
-                o += next;
-              }
+          for (int k = 0; k < 4; ++k) {
+            if (n0 + k >= live) break;
+            if (c.slot < 0)
+              p.out[row * 128 + x] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(r[k]) * s_l[n0 + k]));
+            else
+              st_global_hint(mine + (n0 + k) * 128 + x, __uint_as_float(r[k]), keep);
+            ++row;
+            if (++g == p.G) {
+              g = 0;
+              row += p.Hq - p.G;
             }
           }
-        } else {
-          float* mine = p.part + static_cast<size_t>(c.slot) * N * kPartRow;
-          const uint64_t keep = l2_policy_evict_last();   // read back soon
-#pragma unroll
-          for (int cg = 0; cg < N / 16; ++cg) {
-            uint32_t r[16];
-            tmem_ld16(tO + lane_off + cg * 16, r);
-            tmem_wait_ld();
-            tmem_regs_ready(r);
-#pragma unroll
-            for (int k = 0; k < 16; ++k) st_global_hint(mine + (cg * 16 + k) * 128 + x, __uint_as_float(r[k]), keep);
-          }
-          if (x < N) {
+        }
+        if (c.slot >= 0) {
+          if (x < NC) {
             st_global_hint(mine + N * 128 + x, s_m[x], keep);
             st_global_hint(mine + N * 129 + x, s_l[x], keep);
           }
@@ -813,7 +902,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             named_barrier(1, kSoftmaxThreads);
             if (s_join) {
               __threadfence();
-              join_parts<N>(p, c, x, s_m, s_l, s_red);
+              join_parts<N, NC>(p, c, x, row0, live, s_m, s_l, s_alpha, s_red);
             }
           }
         }
@@ -868,10 +957,6 @@ struct Many {
   static constexpr size_t kSmem = 1024 + kRowsItem * 256 + (kStagesK + kStagesV) * kStage + 2 * kWide;
 };
 
-__device__ __forceinline__ uint32_t half2_bits(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 __device__ __forceinline__ uint32_t widen2(uint32_t two_codes) {
   const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two_codes), __NV_E4M3);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -1005,7 +1090,8 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       const int rs = seq % kRing;
       PageLoads<kChunkPages> pages;
       if (have) {
-        pages.ask(p, c, lane);
+        pages.ask_pages(p, c, lane);
+        pages.ask_scales(p, c, lane);
         c.q_scale = __ldg(p.q_scale + (static_cast<size_t>(c.b) * p.Hkv + c.kvh) * p.row_groups + c.rg) * p.scale_log2;
       } else {
         c.end = 1;
@@ -1622,17 +1708,17 @@ __global__ void __launch_bounds__(256) join_kernel(const Params p, int n_rows, i
   }
 }
 
-template <int N, int STAGES>
+template <int N, int NC, int STAGES>
 cudaError_t launch_few(const CUtensorMap& tk, const CUtensorMap& tv, const Params& p, int grid, cudaStream_t stream) {
   constexpr size_t smem = Few<N, STAGES>::kSmem;
   static std::atomic<unsigned long long> attr_done{0};
   const cudaError_t e = once_per_device(attr_done, [] {
-    const cudaError_t r = cudaFuncSetAttribute(few_rows_kernel<N, STAGES>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    const cudaError_t r = cudaFuncSetAttribute(few_rows_kernel<N, NC, STAGES>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (r != cudaSuccess) return r;
-    return cudaFuncSetAttribute(few_rows_kernel<N, STAGES>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    return cudaFuncSetAttribute(few_rows_kernel<N, NC, STAGES>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
   });
   if (e != cudaSuccess) return e;
-  return launch_pdl(few_rows_kernel<N, STAGES>, dim3(grid), dim3(kFewThreads), smem, stream, tk, tv, p);
+  return launch_pdl(few_rows_kernel<N, NC, STAGES>, dim3(grid), dim3(kFewThreads), smem, stream, tk, tv, p);
 }
 
 }  // namespace
@@ -1721,7 +1807,9 @@ cudaError_t launch_attention_kv8(const Kv8AttnParams& a, const Kv8AttnPlan& pl, 
     if (e != cudaSuccess) return e;
     e = pl.n_rows == 128 ? launch_many<1>(tq, tk, tv, p, pl.grid, stream) : launch_many<2>(tq, tk, tv, p, pl.grid, stream);
   } else {
-    e = pl.n_rows == 16 ? launch_few<16, 6>(tk, tv, p, pl.grid, stream) : launch_few<32, 5>(tk, tv, p, pl.grid, stream);
+    e = pl.n_rows == 32  ? launch_few<32, 32, 5>(tk, tv, p, pl.grid, stream)
+        : pl.rows <= 8 ? launch_few<16, 8, 6>(tk, tv, p, pl.grid, stream)
+                       : launch_few<16, 16, 6>(tk, tv, p, pl.grid, stream);
   }
   if (e != cudaSuccess || pl.parts == 0 || pl.join_here) return e;
   return launch_pdl(join_kernel, dim3(lists, (p.rows + 7) / 8), dim3(256), 0, stream, p, pl.n_rows, pl.grid);
