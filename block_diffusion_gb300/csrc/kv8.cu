@@ -43,7 +43,14 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-__global__ void __launch_bounds__(kWriteWarps * 32)
+// Largest magnitude of the warp's bf16 pairs (a NaN counts as nothing).
+__device__ __forceinline__ float most_of(uint32_t top) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(fmaxf(bf16_lo(top), bf16_hi(top))));
+  return y;
+}
+
+__global__ void __launch_bounds__(kWriteWarps * 32, 4)
 write_kv8_kernel(const WriteKv8Params p, int max_touched) {
   griddep_wait();
   griddep_launch_dependents();
@@ -52,12 +59,12 @@ write_kv8_kernel(const WriteKv8Params p, int max_touched) {
   const int b = blockIdx.x / max_touched, j = blockIdx.x - b * max_touched;
   if (hw >= 2 * p.Hkv) return;
   const int h = hw >> 1, which = hw & 1;
-  const int prefix = p.prefix_lens[b];
+  const int prefix = __ldg(p.prefix_lens + b);
   int n = p.n;
   long long row0 = static_cast<long long>(b) * p.n;
   if (p.first != nullptr) {
-    row0 = p.first[b];
-    const long long end = p.first[b + 1];
+    row0 = __ldg(p.first + b);
+    const long long end = __ldg(p.first + b + 1);
     if (row0 < 0 || end < row0 || end > p.n_rows || end - row0 > p.n) {
       if (lane == 0 && hw == 0 && j == 0) atomicOr(p.err, BDLM_DEVERR_ROW);
       return;
@@ -71,7 +78,20 @@ write_kv8_kernel(const WriteKv8Params p, int max_touched) {
   }
   const int col = prefix / kPage + j;
   if (col > (prefix + n - 1) / kPage) return;
-  const int page = p.page_table[static_cast<size_t>(b) * p.max_pages + col];
+  const int page = __ldg(p.page_table + static_cast<size_t>(b) * p.max_pages + col);
+  const int t0 = col * kPage;                         // the page's first token
+  const int held = max(0, prefix - t0);               // tokens before the new ones: slots 0 .. held - 1
+  const int live = min(kPage, prefix + n - t0);       // slots at and past live are left as they are
+  const uint16_t* x = p.x[which] + ((row0 + (t0 - prefix)) * p.Hkv + h) * 128;   // of slot 0, a new one or not
+  // lane l: 8 dims of slots 2i + l / 16
+  const int dim = (lane & 15) * 8, odd = lane >> 4;
+  uint4 w[8];   // asked for before the page is known to be there
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int slot = 2 * i + odd;
+    w[i] = make_uint4(0, 0, 0, 0);
+    if (slot >= held && slot < live) w[i] = __ldg(reinterpret_cast<const uint4*>(x + static_cast<long long>(slot) * p.Hkv * 128 + dim));
+  }
   if (page < 0 || page >= p.num_pages) {
     if (lane == 0 && hw == 0) atomicOr(p.err, BDLM_DEVERR_PAGE);
     return;
@@ -79,52 +99,60 @@ write_kv8_kernel(const WriteKv8Params p, int max_touched) {
   const size_t unit = static_cast<size_t>(page) * p.Hkv + h;
   uint8_t* codes = p.pages[which] + unit * (kPage * 128);
   float* scale = p.scales + unit * 2 + which;
-  const int t0 = col * kPage;                         // the page's first token
-  const int held = max(0, prefix - t0);               // tokens before the new ones: slots 0 .. held - 1
-  const int live = min(kPage, prefix + n - t0);       // slots at and past live are left as they are
-  const float was = held > 0 ? *scale : 0.f;
-  const uint16_t* x = p.x[which] + ((row0 + (t0 - prefix)) * p.Hkv + h) * 128;   // of slot 0, a new one or not
-  // lane l: 8 dims of slots 2i + l / 16
-  const int dim = (lane & 15) * 8, odd = lane >> 4;
-  float v[8][8];
-  float most = 0.f;
+  uint32_t top = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int slot = 2 * i + odd;
-    uint4 w = make_uint4(0, 0, 0, 0);
-    if (slot >= held && slot < live)
-      w = *reinterpret_cast<const uint4*>(x + static_cast<size_t>(slot) * p.Hkv * 128 + dim);
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+    const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      v[i][2 * k] = bf16_lo(u[k]);
-      v[i][2 * k + 1] = bf16_hi(u[k]);
+      const uint32_t mag = u[k] & 0x7FFF7FFFu;
+      const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&top), *reinterpret_cast<const __nv_bfloat162*>(&mag));
+      top = *reinterpret_cast<const uint32_t*>(&m);
     }
-    if (slot < held) {
-      const uint2 c = *reinterpret_cast<const uint2*>(codes + slot * 128 + dim);
-      const uint32_t cc[4] = {c.x & 0xFFFFu, c.x >> 16, c.y & 0xFFFFu, c.y >> 16};
+  }
+  float most = most_of(top), was = 0.f;
+  // Tokens that the page held before (one page of a sequence at most): their codes, 16 slots' at once
+  uint2 c[8];
+  if (held > 0) {
+    was = *scale;
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      c[i] = make_uint2(0, 0);
+      if (2 * i + odd < held) c[i] = *reinterpret_cast<const uint2*>(codes + (2 * i + odd) * 128 + dim);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t cc[4] = {c[i].x & 0xFFFFu, c[i].x >> 16, c[i].y & 0xFFFFu, c[i].y >> 16};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float2 f = from_e4m3x2(cc[k]);
-        v[i][2 * k] = f.x * was;
-        v[i][2 * k + 1] = f.y * was;
+        m = fmaxf(m, fmaxf(fabsf(f.x * was), fabsf(f.y * was)));
       }
     }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) most = fmaxf(most, fabsf(v[i][k]));   // (a NaN counts as nothing)
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(m));
+    most = fmaxf(most, m);
   }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
   const int e = scale_exponent(most);
   const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int slot = 2 * i + odd;
     if (slot >= live) continue;
-    uint32_t c[4];
+    uint32_t o[4];
+    if (slot >= held) {
+      const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) c[k] = e4m3x2(v[i][2 * k] * inv, v[i][2 * k + 1] * inv);
-    *reinterpret_cast<uint2*>(codes + slot * 128 + dim) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+      for (int k = 0; k < 4; ++k) o[k] = e4m3x2(bf16_lo(u[k]) * inv, bf16_hi(u[k]) * inv);
+    } else {
+      const uint32_t cc[4] = {c[i].x & 0xFFFFu, c[i].x >> 16, c[i].y & 0xFFFFu, c[i].y >> 16};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = from_e4m3x2(cc[k]);
+        o[k] = e4m3x2(f.x * was * inv, f.y * was * inv);   // (the value in float32 first)
+      }
+    }
+    *reinterpret_cast<uint2*>(codes + slot * 128 + dim) = make_uint2(o[0] | o[1] << 16, o[2] | o[3] << 16);
   }
   if (lane == 0) *scale = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
 }

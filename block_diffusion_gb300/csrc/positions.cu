@@ -22,8 +22,8 @@ constexpr int kScanThreads = 1024;
 
 // Running sums of two values over the CTA's threads, `a` and `b` becoming those up to and with the thread's
 // own; returns both totals.
-__device__ __forceinline__ void scan2(long long& a, long long& b, long long (&s)[2][33], long long& ta, long long& tb) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__device__ __forceinline__ void scan2(long long& a, long long& b, long long (&s)[2][32], long long& ta, long long& tb) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
     const long long x = __shfl_up_sync(0xffffffffu, a, off), y = __shfl_up_sync(0xffffffffu, b, off);
@@ -37,69 +37,65 @@ __device__ __forceinline__ void scan2(long long& a, long long& b, long long (&s)
     s[1][warp] = b;
   }
   __syncthreads();
-  if (warp == 0) {
-    long long x = s[0][lane], y = s[1][lane];
+  long long x = lane < warps ? s[0][lane] : 0, y = lane < warps ? s[1][lane] : 0;   // every warp for itself
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const long long u = __shfl_up_sync(0xffffffffu, x, off), v = __shfl_up_sync(0xffffffffu, y, off);
-      if (lane >= off) {
-        x += u;
-        y += v;
-      }
+  for (int off = 1; off < 32; off <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, x, off), v = __shfl_up_sync(0xffffffffu, y, off);
+    if (lane >= off) {
+      x += u;
+      y += v;
     }
-    s[0][lane] = x;
-    s[1][lane] = y;
   }
-  __syncthreads();
+  ta = __shfl_sync(0xffffffffu, x, 31);
+  tb = __shfl_sync(0xffffffffu, y, 31);
+  const long long pa = __shfl_sync(0xffffffffu, x, warp > 0 ? warp - 1 : 0), pb = __shfl_sync(0xffffffffu, y, warp > 0 ? warp - 1 : 0);
   if (warp > 0) {
-    a += s[0][warp - 1];
-    b += s[1][warp - 1];
+    a += pa;
+    b += pb;
   }
-  ta = s[0][31];
-  tb = s[1][31];
   __syncthreads();
 }
 
-// Row r of the packed tokens: its position and slot, and the table's entry where it opens a page.
-__device__ __forceinline__ void place_row(const TableParams& p, const int32_t* first, int r, int total) {
-  int at = -1, slot = -1;
-  if (r < total) {
-    int lo = 0, hi = p.B;   // first[lo] <= r < first[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (first[mid] <= r)
-        lo = mid;
-      else
-        hi = mid;
-    }
-    const int2 plan = p.plan[lo];
-    at = plan.x + (r - first[lo]);
-    const int col = at / kPage, held = (plan.x + kPage - 1) / kPage;
-    int32_t* entry = p.page_table + static_cast<size_t>(lo) * p.max_pages + col;
-    int id;
-    if (col < held) {
-      id = *entry;
-    } else {
-      id = __ldg(p.free_pages + plan.y + (col - held));
-      if (at % kPage == 0) *entry = id;
-    }
-    if (id < 0 || id >= p.num_pages)
-      atomicOr(p.err, BDLM_DEVERR_PAGE);
+// The sequence in [lo, hi) that packed row r lies in: first[lo] <= r < first[hi].
+__device__ __forceinline__ int sequence_of(const int32_t* first, int lo, int hi, int r) {
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (first[mid] <= r)
+      lo = mid;
     else
-      slot = id * kPage + at % kPage;
+      hi = mid;
   }
-  if (p.positions != nullptr) p.positions[r] = at;
-  if (p.slots != nullptr) p.slots[r] = slot;
+  return lo;
 }
 
-// WHOLE: the rows too (one launch for few of them).
+// Row r of the packed tokens, of sequence b: its position and slot, and the table's entry where it opens a page.
+__device__ __forceinline__ int2 place_row(const TableParams& p, int first, int2 plan, int b, int r) {
+  const int at = plan.x + (r - first);
+  const int col = at / kPage, held = (plan.x + kPage - 1) / kPage;
+  int32_t* entry = p.page_table + static_cast<size_t>(b) * p.max_pages + col;
+  int id;
+  if (col < held) {
+    id = *entry;
+  } else {
+    id = __ldg(p.free_pages + plan.y + (col - held));
+    if (at % kPage == 0) *entry = id;
+  }
+  const bool bad = id < 0 || id >= p.num_pages;
+  if (bad) atomicOr(p.err, BDLM_DEVERR_PAGE);
+  return make_int2(at, bad ? -1 : id * kPage + at % kPage);
+}
+
+// WHOLE: the rows too, in one launch, the sequences' first rows and plans at hand in shared memory.
+constexpr int kWholeSequences = 1024;
 template <bool WHOLE>
 __global__ void __launch_bounds__(kScanThreads) table_plan_kernel(const TableParams p) {
-  __shared__ long long s[2][33];
-  __shared__ long long s_rows, s_pages;
+  __shared__ long long s[2][32];
+  __shared__ unsigned long long s_rows, s_pages;
+  __shared__ int32_t s_first[WHOLE ? kWholeSequences + 1 : 1];
+  __shared__ int2 s_plan[WHOLE ? kWholeSequences : 1];
   griddep_wait();
   griddep_launch_dependents();
-  const int t = threadIdx.x;
+  const int t = threadIdx.x, threads = blockDim.x;
   if (t == 0) s_rows = s_pages = 0;
   int from = p.free_from != nullptr ? *p.free_from : 0;
   const bool from_ok = from >= 0 && from <= p.n_free;
@@ -109,7 +105,7 @@ __global__ void __launch_bounds__(kScanThreads) table_plan_kernel(const TablePar
   }
   const long long max_tok = static_cast<long long>(p.max_pages) * kPage;
   long long pages = 0, rows = 0;   // of the sequences before this round
-  for (int b0 = 0; b0 < p.B; b0 += kScanThreads) {
+  for (int b0 = 0; b0 < p.B; b0 += threads) {
     const int b = b0 + t;
     int was = 0, now = 0;
     if (b < p.B) {
@@ -120,50 +116,118 @@ __global__ void __launch_bounds__(kScanThreads) table_plan_kernel(const TablePar
         now = was;
       }
     }
+    // (where every page request is served, as it mostly is, one pass over both sums does)
     const long long need = now > was ? (now + kPage - 1) / kPage - (was + kPage - 1) / kPage : 0;
-    long long upto = need, unused = 0, tp, tr;
-    scan2(upto, unused, s, tp, tr);
+    long long upto = need, row = now > was ? now - was : 0, tp, tr;
+    scan2(upto, row, s, tp, tr);
     upto += pages;
-    pages += tp;
     bool served = need == 0 || upto <= p.n_free - from;
     const long long n = served && now > was ? now - was : 0;
-    long long row = n, most = need;
-    scan2(row, most, s, tr, tp);
+    if (pages + tp > p.n_free - from) {   // (the same for all threads)
+      long long unused = 0;
+      row = n;
+      scan2(row, unused, s, tr, unused);
+    }
+    pages += tp;
     row += rows;
     rows += tr;
     if (row > p.max_tokens && n > 0) served = false;
     if (b < p.B) {
-      p.lens_out[b] = served ? now : was;
-      p.plan[b] = make_int2(was, static_cast<int>(served ? from + upto - need : 0));
+      const int2 plan = make_int2(was, static_cast<int>(served ? from + upto - need : 0));
       // (a row past the last one served is cut to it below)
-      p.first[b + 1] = static_cast<int>(row > 0x7FFFFFFFll ? 0x7FFFFFFFll : row);
-      if (served && n > 0)
-        atomicMax(reinterpret_cast<unsigned long long*>(&s_rows), static_cast<unsigned long long>(row));
-      if (served && need > 0)
-        atomicMax(reinterpret_cast<unsigned long long*>(&s_pages), static_cast<unsigned long long>(upto));
+      const int next = static_cast<int>(row > 0x7FFFFFFFll ? 0x7FFFFFFFll : row);
+      p.lens_out[b] = served ? now : was;
+      if constexpr (WHOLE) {
+        s_plan[b] = plan;
+        s_first[b + 1] = next;
+      } else {
+        p.plan[b] = plan;
+        p.first[b + 1] = next;
+      }
+      if (served && n > 0) atomicMax(&s_rows, static_cast<unsigned long long>(row));
+      if (served && need > 0) atomicMax(&s_pages, static_cast<unsigned long long>(upto));
     }
   }
   __syncthreads();
   // rows grow along the sequences, so the last one served has the total
   const int total = static_cast<int>(s_rows);
-  for (int b = t; b < p.B; b += kScanThreads)
-    if (p.first[b + 1] > total) p.first[b + 1] = total;
+  for (int b = t; b < p.B; b += threads) {
+    if constexpr (WHOLE) {
+      if (s_first[b + 1] > total) s_first[b + 1] = total;
+      p.first[b + 1] = s_first[b + 1];
+    } else {
+      if (p.first[b + 1] > total) p.first[b + 1] = total;
+    }
+  }
   if (t == 0) {
     p.first[0] = 0;
-    if (p.free_next != nullptr) *p.free_next = static_cast<int>(from + s_pages);
+    if constexpr (WHOLE) s_first[0] = 0;
+    if (p.free_next != nullptr) *p.free_next = from + static_cast<int>(s_pages);
   }
   if constexpr (WHOLE) {
     __syncthreads();
-    for (int r = t; r < p.max_tokens; r += kScanThreads) place_row(p, p.first, r, total);
+    for (int r = t; r < p.max_tokens; r += threads) {
+      int2 at = make_int2(-1, -1);
+      if (r < total) {
+        const int b = sequence_of(s_first, 0, p.B, r);
+        at = place_row(p, s_first[b], s_plan[b], b, r);
+      }
+      if (p.positions != nullptr) p.positions[r] = at.x;
+      if (p.slots != nullptr) p.slots[r] = at.y;
+    }
   }
 }
 
-constexpr int kRowThreads = 256;
-__global__ void __launch_bounds__(kRowThreads) table_rows_kernel(const TableParams p) {
+// Many rows: a thread places four in a row.  A warp's 128 rows mostly are of one sequence or two, which the warp looks
+// for together, so that few threads search on their own.
+constexpr int kRowThreads = 256, kRowsEach = 4;
+__global__ void __launch_bounds__(kRowThreads) table_rows_kernel(const TableParams p, int wide) {
   griddep_wait();
   griddep_launch_dependents();
-  const int r = blockIdx.x * kRowThreads + threadIdx.x;
-  if (r < p.max_tokens) place_row(p, p.first, r, p.first[p.B]);
+  const int lane = threadIdx.x & 31;
+  const long long r0 = (static_cast<long long>(blockIdx.x) * kRowThreads + threadIdx.x) * kRowsEach;
+  const int total = p.first[p.B];
+  const long long warp0 = r0 - lane * kRowsEach;
+  int lo = 0;
+  if (warp0 < total) {
+    int n = p.B;   // first[lo] <= warp0 < first[lo + n]
+    while (n > 1) {
+      const int step = (n + 31) / 32;
+      const int c = __popc(__ballot_sync(0xffffffffu, lane * step < n && p.first[lo + (lane * step < n ? lane * step : 0)] <= warp0)) - 1;
+      lo += c * step;
+      n = min(step, n - c * step);
+    }
+  }
+  if (r0 >= p.max_tokens) return;
+  int pos[kRowsEach], slot[kRowsEach];
+  int begin = -1, end = -1;   // rows of sequence lo
+  int2 plan = make_int2(0, 0);
+#pragma unroll
+  for (int k = 0; k < kRowsEach; ++k) {
+    const long long r = r0 + k;
+    pos[k] = slot[k] = -1;
+    if (r >= total) continue;
+    if (r >= end) {
+      if (end >= 0 || r >= p.first[lo + 1]) lo = sequence_of(p.first, lo, p.B, static_cast<int>(r));
+      begin = p.first[lo];
+      end = p.first[lo + 1];
+      plan = p.plan[lo];
+    }
+    const int2 at = place_row(p, begin, plan, lo, static_cast<int>(r));
+    pos[k] = at.x;
+    slot[k] = at.y;
+  }
+  if (wide && r0 + kRowsEach <= p.max_tokens) {
+    if (p.positions != nullptr) *reinterpret_cast<int4*>(p.positions + r0) = make_int4(pos[0], pos[1], pos[2], pos[3]);
+    if (p.slots != nullptr) *reinterpret_cast<int4*>(p.slots + r0) = make_int4(slot[0], slot[1], slot[2], slot[3]);
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < kRowsEach; ++k) {
+    if (r0 + k >= p.max_tokens) break;
+    if (p.positions != nullptr) p.positions[r0 + k] = pos[k];
+    if (p.slots != nullptr) p.slots[r0 + k] = slot[k];
+  }
 }
 
 // ------------------------------------------------------------------ rotary positions
@@ -173,11 +237,51 @@ __global__ void __launch_bounds__(kRowThreads) table_rows_kernel(const TablePara
 // float32 loses it (position 500000 has steps of 0.03 radians there).  Its upper 32 bits then suffice for
 // sine and cosine in float32.
 constexpr int kRotaryThreads = 256;
-constexpr int kRotaryRows = 4;   // tokens of a CTA: a thread computes the angle of one pair
+constexpr int kRotaryRows = 4;    // tokens of a CTA: a thread computes the angle of one pair
+constexpr int kRotaryBatch = 3;
 
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Two 16-byte pieces of a head, turned or not: INTER: pieces c and c + 8, each of whole pairs.  Halves: piece c and the
+// one half of the turned part further on; behind them, two that stay as they are.
+template <bool INTER>
+__device__ __forceinline__ int2 pieces(int c, int rot) {
+  if constexpr (INTER) return make_int2(c, c + 8);
+  const int half = rot / 16;
+  return c < half ? make_int2(c, c + half) : make_int2(rot / 8 + 2 * (c - half), rot / 8 + 2 * (c - half) + 1);
+}
+
+template <bool INTER>
+__device__ __forceinline__ void turn(uint4& u, uint4& v, int c, int rot, const float2* cs) {
+  uint32_t a[4] = {u.x, u.y, u.z, u.w}, b[4] = {v.x, v.y, v.z, v.w};
+  if constexpr (INTER) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (c * 8 < rot) {
+        const float2 s = cs[c * 4 + k];
+        const float x = bf16_lo(a[k]), y = bf16_hi(a[k]);
+        a[k] = pack2(x * s.x - y * s.y, x * s.y + y * s.x);
+      }
+      if ((c + 8) * 8 < rot) {
+        const float2 s = cs[(c + 8) * 4 + k];
+        const float x = bf16_lo(b[k]), y = bf16_hi(b[k]);
+        b[k] = pack2(x * s.x - y * s.y, x * s.y + y * s.x);
+      }
+    }
+  } else if (c < rot / 16) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 lo = cs[c * 8 + 2 * k], hi = cs[c * 8 + 2 * k + 1];
+      const float a0 = bf16_lo(a[k]), a1 = bf16_hi(a[k]), b0 = bf16_lo(b[k]), b1 = bf16_hi(b[k]);
+      a[k] = pack2(a0 * lo.x - b0 * lo.y, a1 * hi.x - b1 * hi.y);
+      b[k] = pack2(a0 * lo.y + b0 * lo.x, a1 * hi.y + b1 * hi.x);
+    }
+  }
+  u = make_uint4(a[0], a[1], a[2], a[3]);
+  v = make_uint4(b[0], b[1], b[2], b[3]);
 }
 
 template <bool INTER>
@@ -197,9 +301,8 @@ rotary_kernel(const RotaryParams p, const __grid_constant__ bdlm_rotary_desc r) 
       if (p.positions != nullptr) {
         at = p.positions[row];
       } else {
-        const int b = static_cast<int>(row / p.n);
-        at = static_cast<long long>(p.start[b]) + (row - static_cast<long long>(b) * p.n);
-        if (p.start[b] < 0) at = -1;
+        const int b = static_cast<int>(row / p.n), start = p.start[b];
+        if (start >= 0) at = start + (row - static_cast<long long>(b) * p.n);
       }
     }
     if (i == 0) s_live[y] = at >= 0;
@@ -211,51 +314,43 @@ rotary_kernel(const RotaryParams p, const __grid_constant__ bdlm_rotary_desc r) 
     }
   }
   __syncthreads();
+  // Heads of the CTA's rows, end to end, eight threads a head; kRotaryBatch of them are under way in a thread at once.
   const int heads = p.Hq + p.Hkv, c = t & 7;
-  for (int y = 0; y < kRotaryRows; ++y) {
-    if (!s_live[y]) continue;
-    const long long row = row0 + y;
-    for (int h = t >> 3; h < heads; h += kRotaryThreads / 8) {
-      const bool is_q = h < p.Hq;
-      const int hh = is_q ? h : h - p.Hq;
-      const uint4* src = reinterpret_cast<const uint4*>((is_q ? p.q + row * p.q_stride : p.k + row * p.k_stride) + hh * 128);
-      uint4* dst = reinterpret_cast<uint4*>(is_q ? p.q_out + (row * p.Hq + hh) * 128 : p.k_out + (row * p.Hkv + hh) * 128);
-      if constexpr (INTER) {
-        // eight values are four pairs
-        uint4 v[2] = {src[c], src[c + 8]};
+  const int2 at = pieces<INTER>(c, rot);
+  int y = 0, h = t >> 3;
+  while (h >= heads && y < kRotaryRows) {
+    h -= heads;
+    ++y;
+  }
+  while (y < kRotaryRows) {
+    uint4 u[kRotaryBatch], v[kRotaryBatch];
+    uint4* dst[kRotaryBatch];
+    int row[kRotaryBatch];
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int d = (c + 8 * x) * 8;
-          uint32_t w[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
-          if (d < rot) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 cs = s_cs[y][d / 2 + k];
-              const float a = bf16_lo(w[k]), b = bf16_hi(w[k]);
-              w[k] = pack2(a * cs.x - b * cs.y, a * cs.y + b * cs.x);
-            }
-          }
-          dst[c + 8 * x] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-      } else {
-        // chunk c and the one half of the turned part further on; behind that, what stays as it is
-        const int half = rot / 16;
-        const bool turn = c < half;
-        const int c0 = turn ? c : rot / 8 + 2 * (c - half), c1 = turn ? c + half : c0 + 1;
-        const uint4 u = src[c0], v = src[c1];
-        uint32_t a[4] = {u.x, u.y, u.z, u.w}, b[4] = {v.x, v.y, v.z, v.w};
-        if (turn) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 lo = s_cs[y][c * 8 + 2 * k], hi = s_cs[y][c * 8 + 2 * k + 1];
-            const float a0 = bf16_lo(a[k]), a1 = bf16_hi(a[k]), b0 = bf16_lo(b[k]), b1 = bf16_hi(b[k]);
-            a[k] = pack2(a0 * lo.x - b0 * lo.y, a1 * hi.x - b1 * hi.y);
-            b[k] = pack2(a0 * lo.y + b0 * lo.x, a1 * hi.y + b1 * hi.x);
-          }
-        }
-        dst[c0] = make_uint4(a[0], a[1], a[2], a[3]);
-        dst[c1] = make_uint4(b[0], b[1], b[2], b[3]);
+    for (int k = 0; k < kRotaryBatch; ++k) {
+      dst[k] = nullptr;
+      row[k] = y;
+      if (y < kRotaryRows && s_live[y]) {
+        const bool is_q = h < p.Hq;
+        const int hh = is_q ? h : h - p.Hq;
+        const long long g = row0 + y;
+        const uint4* src = reinterpret_cast<const uint4*>((is_q ? p.q + g * p.q_stride : p.k + g * p.k_stride) + hh * 128);
+        dst[k] = reinterpret_cast<uint4*>(is_q ? p.q_out + (g * p.Hq + hh) * 128 : p.k_out + (g * p.Hkv + hh) * 128);
+        u[k] = src[at.x];
+        v[k] = src[at.y];
       }
+      h += kRotaryThreads / 8;
+      while (h >= heads && y < kRotaryRows) {
+        h -= heads;
+        ++y;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kRotaryBatch; ++k) {
+      if (dst[k] == nullptr) continue;
+      turn<INTER>(u[k], v[k], c, rot, s_cs[row[k]]);
+      dst[k][at.x] = u[k];
+      dst[k][at.y] = v[k];
     }
   }
 }
@@ -264,11 +359,15 @@ rotary_kernel(const RotaryParams p, const __grid_constant__ bdlm_rotary_desc r) 
 
 cudaError_t launch_build_tables(const TableParams& p, cudaStream_t stream) {
   // few rows: the CTA that plans them places them
-  if (p.max_tokens <= 4 * kScanThreads)
+  if (p.max_tokens <= 4 * kScanThreads && p.B <= kWholeSequences)
     return launch_pdl(table_plan_kernel<true>, dim3(1), dim3(kScanThreads), 0, stream, p);
-  const cudaError_t e = launch_pdl(table_plan_kernel<false>, dim3(1), dim3(kScanThreads), 0, stream, p);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(table_rows_kernel, dim3((p.max_tokens + kRowThreads - 1) / kRowThreads), dim3(kRowThreads), 0, stream, p);
+  const int threads = p.B >= kScanThreads ? kScanThreads : (p.B + 31) / 32 * 32;
+  const cudaError_t e = launch_pdl(table_plan_kernel<false>, dim3(1), dim3(threads), 0, stream, p);
+  if (e != cudaSuccess || p.max_tokens == 0) return e;
+  const int wide = ((reinterpret_cast<uintptr_t>(p.positions) | reinterpret_cast<uintptr_t>(p.slots)) & 15) == 0;
+  const long long each = static_cast<long long>(kRowThreads) * kRowsEach;
+  return launch_pdl(table_rows_kernel, dim3(static_cast<unsigned>((p.max_tokens + each - 1) / each)), dim3(kRowThreads), 0,
+                    stream, p, wide);
 }
 
 cudaError_t launch_rotary(const RotaryParams& p, const bdlm_rotary_desc& r, int num_sms, cudaStream_t stream) {
