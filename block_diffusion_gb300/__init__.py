@@ -216,10 +216,12 @@ def _rows(fn: str, t):
     dimensions (an address and None pass)."""
     if t is None or t.__class__ is int:
         return t
-    types = _types.get("b") or _element_types("b")
-    if t.dtype not in types[0] or t.get_device() != _current_device() or t.dim() < 2 or not (
-            t.stride(-1) == 1 and (t.stride(-2) == t.shape[-1] or t.shape[-2] == 1)):
+    if t.dtype not in (_types.get("b") or _element_types("b"))[0] or t.get_device() != _current_device():
         raise BdlmError(fn, BDLM_ERR_INVALID)
+    if not t.is_contiguous():
+        stride, shape = t.stride(), t.shape
+        if len(shape) < 2 or stride[-1] != 1 or (stride[-2] != shape[-1] and shape[-2] != 1):
+            raise BdlmError(fn, BDLM_ERR_INVALID)
     return t.data_ptr()
 
 
@@ -229,13 +231,11 @@ def _dense(fn: str, kinds: str, stream, *tensors) -> list:
     (b: bf16 or its 16 bits, i: int32, f: float32, w: 64-bit words, e: e4m3 or its 8 bits), not contiguous,
     or not on the current device.  Shapes are the caller's, as in C."""
     dev = _current_device()
-    out = []
     for types, t in zip(_types.get(kinds) or _element_types(kinds), tensors):
-        if t is not None and t.__class__ is not int:
-            if t.dtype not in types or t.get_device() != dev or not t.is_contiguous():
-                raise BdlmError(fn, BDLM_ERR_INVALID)
-            t = t.data_ptr()
-        out.append(t)
+        if t is not None and t.__class__ is not int and (
+                t.dtype not in types or t.get_device() != dev or not t.is_contiguous()):
+            raise BdlmError(fn, BDLM_ERR_INVALID)
+    out = [t if t is None or t.__class__ is int else t.data_ptr() for t in tensors]
     out.append(_raw_stream(dev) if stream is None else _stream(stream))
     return out
 

@@ -65,7 +65,8 @@ struct Chunk {
   int first, last;   // of the tiles that this CTA sums up together
   int slot;          // part to write at the last chunk, -1: the output
   int u0, parts;     // the list's first unit and its parts (slot >= 0)
-  int end;
+  int final;         // the CTA's last chunk
+  int end;           // no chunk: the CTA has no work
   float q_scale;     // q = (hi + lo) * q_scale, times c
 };
 
@@ -256,6 +257,7 @@ struct Walk {
     c.slot = slot;
     c.u0 = u0;
     c.parts = parts;
+    c.final = c.last && pos == end;
     c.end = 0;
     return true;
   }
@@ -307,6 +309,7 @@ struct PageLoads {
 };
 
 constexpr int kPartRow = 130;   // floats of a row's part: O, m, l
+constexpr int kFewParts = 8;    // parts a list, about
 
 // ------------------------------------------------------------------ up to 32 query rows per KV head
 //
@@ -456,6 +459,10 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 
   if (warp == 0) {
     // =================================================================== copies
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+    }
     const uint64_t policy = l2_policy_evict_first();
     int st = 0;
     uint32_t ph = 0;
@@ -475,18 +482,23 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     };
     // K of the next chunk, then V of this one
     if ((ok = mbar_wait_warp(&bar_cfull[0], 0, &abort_flag)) && !s_chunk[0].end) {
-      int n_tiles = s_chunk[0].n_tiles;
+      int n_tiles = s_chunk[0].n_tiles, final = s_chunk[0].final;
       emit(0, n_tiles, &tm_k);
       for (int u = 0; ok; ++u) {
-        const int rs = (u + 1) % kRing;
-        if (!(ok = mbar_wait_warp(&bar_cfull[rs], ((u + 1) / kRing) & 1, &abort_flag))) break;
-        const int end = s_chunk[rs].end, next = s_chunk[rs].n_tiles;
-        if (!end) emit(u + 1, next, &tm_k);
+        int next = 0, next_final = 0;
+        if (!final) {
+          const int rs = (u + 1) % kRing;
+          if (!(ok = mbar_wait_warp(&bar_cfull[rs], ((u + 1) / kRing) & 1, &abort_flag))) break;
+          next = s_chunk[rs].n_tiles;
+          next_final = s_chunk[rs].final;
+          emit(u + 1, next, &tm_k);
+        }
         emit(u, n_tiles, &tm_v);
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar_cempty[u % kRing]);
-        if (end) break;
+        if (final) break;
         n_tiles = next;
+        final = next_final;
       }
     }
     if (lane == 0) {
@@ -574,14 +586,16 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     if (ok && !cur.end) {
       do_s(true, cur.last, cur.n_tiles, 0);
       for (int u = 0; ok; ++u) {
-        const int rs = (u + 1) % kRing;
-        if (!(ok = mbar_wait_warp(&bar_cfull[rs], ((u + 1) / kRing) & 1, &abort_flag))) break;
-        nxt = s_chunk[rs];
-        if (!nxt.end) do_s(nxt.first, nxt.last, nxt.n_tiles, u + 1);   // ahead of PV(u): the softmax goes on meanwhile
+        if (!cur.final) {
+          const int rs = (u + 1) % kRing;
+          if (!(ok = mbar_wait_warp(&bar_cfull[rs], ((u + 1) / kRing) & 1, &abort_flag))) break;
+          nxt = s_chunk[rs];
+          do_s(nxt.first, nxt.last, nxt.n_tiles, u + 1);   // ahead of PV(u): the softmax goes on meanwhile
+        }
         if (ok) do_pv(cur.first, cur.t0, cur.t_end, cur.n_tiles, u);
         if (!ok) break;
         if (lane == 0) mbar_arrive(&bar_cempty[u % kRing]);
-        if (nxt.end) break;
+        if (cur.final) break;
         cur = nxt;
       }
     }
@@ -646,26 +660,27 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     // microseconds, and the copies would stand still for the second's.  From then on the walk is chunks ahead.
     Chunk c, d;
     PageLoads<F::kChunkPages> pages, ahead;
+    c.final = 1;
     c.end = !walk.next(p, lane, c);
     if (!c.end) {
       ask_q(c);
       pages.ask_pages(p, c, lane);
-      d.end = !walk.next(p, lane, d);
-      if (!d.end) ahead.ask_pages(p, d, lane);
+      if (!c.final) {
+        walk.next(p, lane, d);
+        ahead.ask_pages(p, d, lane);
+      }
       pages.ask_scales(p, c, lane);
-      if (!d.end) ahead.ask_scales(p, d, lane);
+      if (!c.final) ahead.ask_scales(p, d, lane);
     }
     publish(c, pages);
-    if (!c.end && ok) {
-      if (!d.end && d.first) ask_q(d);
+    if (!c.final && ok) {
+      if (d.first) ask_q(d);
       publish(d, ahead);
-      while (!d.end && ok) {
-        d.end = !walk.next(p, lane, d);
-        if (!d.end) {
-          if (d.first) ask_q(d);
-          ahead.ask_pages(p, d, lane);
-          ahead.ask_scales(p, d, lane);
-        }
+      while (!d.final && ok) {
+        walk.next(p, lane, d);
+        if (d.first) ask_q(d);
+        ahead.ask_pages(p, d, lane);
+        ahead.ask_scales(p, d, lane);
         publish(d, ahead);
       }
     }
@@ -911,6 +926,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       // the chunk's descriptor and scales (and O^T) are done with
       named_barrier(1, kSoftmaxThreads);
       if (x == 0) mbar_arrive(&bar_cempty[rs]);
+      if (c.final) break;
     }
   }
 
@@ -1593,119 +1609,135 @@ __global__ void __launch_bounds__(kCumThreads) cum_tiles_kernel(const Params p, 
 }
 
 // Joins the parts of the lists that units' borders cut:  out = sum_s e_s O_s / sum_s e_s l_s,  e_s = 2^(m_s - M).
-// CTA (list, eight rows): a warp a row where the parts are few, else eight warps a row, a part of the parts each.
-constexpr int kFewParts = 16;
-__global__ void __launch_bounds__(256) join_kernel(const Params p, int n_rows, int ctas) {
-  __shared__ float s_acc[8][128], s_den[8], s_top[8];
+// What a CTA of either kernel needs of its list; false: nothing was cut.
+struct JoinList {
+  int b, kvh, rg, u0, parts;
+
+  __device__ __forceinline__ bool find(const Params& p, int list, int ctas, int lane) {
+    const int lists = p.Hkv * p.row_groups;
+    b = list / lists;
+    list -= b * lists;
+    rg = list % p.row_groups;
+    kvh = list / p.row_groups;
+    bool ok;
+    int sum, before;
+    if (p.cum != nullptr) {
+      sum = __ldg(p.cum + p.B);
+      before = __ldg(p.cum + b);
+    } else {
+      sum = before = 0;
+      for (int i = lane; i < p.B; i += 32) {
+        const int n = (kv_tokens(p, i, &ok) + kTile - 1) / kTile;
+        sum += n;
+        if (i < b) before += n;
+      }
+      sum = __reduce_add_sync(0xffffffffu, sum);
+      before = __reduce_add_sync(0xffffffffu, before);
+    }
+    const int tiles = (kv_tokens(p, b, &ok) + kTile - 1) / kTile;
+    const long long per = unit_tiles(static_cast<long long>(sum) * lists, ctas);
+    const long long c0 = static_cast<long long>(before) * lists + static_cast<long long>(list) * tiles;
+    u0 = static_cast<int>(c0 / per);
+    parts = static_cast<int>((c0 + tiles - 1) / per) - u0 + 1;
+    return parts > 1;
+  }
+  // part s: the first in its unit's second slot, the others in their units' first
+  __device__ __forceinline__ const float* part(const Params& p, int s, int n_rows) const {
+    return p.part + static_cast<size_t>(2 * (u0 + s) + (s == 0 ? 1 : 0)) * n_rows * kPartRow;
+  }
+  __device__ __forceinline__ uint16_t* row(const Params& p, int n) const {
+    return p.out + ((static_cast<size_t>(b) * p.L + rg * p.lsub + n / p.G) * p.Hq + static_cast<size_t>(kvh) * p.G + n % p.G) * 128;
+  }
+};
+
+// Many lists of few parts: CTA (list, eight rows), a warp a row, four head dims a lane.
+__global__ void __launch_bounds__(256) join_few_kernel(const Params p, int n_rows, int ctas) {
   griddep_wait();
   griddep_launch_dependents();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int lists = p.Hkv * p.row_groups;
-  const int b = blockIdx.x / lists, list = blockIdx.x - b * lists;
-  bool ok;
-  int sum, before;
-  if (p.cum != nullptr) {
-    sum = __ldg(p.cum + p.B);
-    before = __ldg(p.cum + b);
-  } else {
-    sum = before = 0;
-    for (int i = lane; i < p.B; i += 32) {
-      const int n = (kv_tokens(p, i, &ok) + kTile - 1) / kTile;
-      sum += n;
-      if (i < b) before += n;
+  const int lane = threadIdx.x & 31, n = blockIdx.y * 8 + (threadIdx.x >> 5);
+  JoinList j;
+  if (!j.find(p, blockIdx.x, ctas, lane) || n >= p.rows || j.rg * p.lsub + n / p.G >= p.L) return;
+  float M = -CUDART_INF_F, den = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int at = 0; at < j.parts; at += 32) {
+    const int s = at + lane;
+    float m = -CUDART_INF_F, l = 0.f;
+    if (s < j.parts) {
+      m = __ldcg(j.part(p, s, n_rows) + n_rows * 128 + n);
+      l = __ldcg(j.part(p, s, n_rows) + n_rows * 129 + n);
     }
-    sum = __reduce_add_sync(0xffffffffu, sum);
-    before = __reduce_add_sync(0xffffffffu, before);
-  }
-  const int tiles = (kv_tokens(p, b, &ok) + kTile - 1) / kTile;
-  const long long per = unit_tiles(static_cast<long long>(sum) * lists, ctas);
-  const long long c0 = static_cast<long long>(before) * lists + static_cast<long long>(list) * tiles;
-  const int u0 = static_cast<int>(c0 / per), u1 = static_cast<int>((c0 + tiles - 1) / per);
-  if (u0 == u1) return;
-  const int ns = u1 - u0 + 1;
-  const int rg = list % p.row_groups, kvh = list / p.row_groups;
-  const size_t unit = static_cast<size_t>(n_rows) * kPartRow;
-  // part s of the list: the first in its unit's second slot, the others in their units' first
-  auto part = [&](int s) { return p.part + static_cast<size_t>(2 * (u0 + s) + (s == 0 ? 1 : 0)) * unit; };
-  auto write = [&](int n, const float4& acc) {
-    const int i = rg * p.lsub + n / p.G;
-    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y), hi = __floats2bfloat162_rn(acc.z, acc.w);
-    *reinterpret_cast<uint2*>(p.out + ((static_cast<size_t>(b) * p.L + i) * p.Hq + static_cast<size_t>(kvh) * p.G + n % p.G) * 128 +
-                              4 * lane) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-  };
-  // sums of parts s0, s0 + step, ... of row n, relative to their largest m
-  auto gather = [&](int n, int s0, int step, float& M, float& den, float4& acc) {
-    M = -CUDART_INF_F;
-    den = 0.f;
-    acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int at = s0; at < ns; at += 32 * step) {
-      const int s = at + lane * step;
-      float m = -CUDART_INF_F, l = 0.f;
-      if (s < ns) {
-        m = __ldcg(part(s) + n_rows * 128 + n);
-        l = __ldcg(part(s) + n_rows * 129 + n);
-      }
-      const float mn = fmaxf(M, warp_max(m));
-      const float e = s < ns ? ex2(m - mn) : 0.f, was = ex2(M - mn);
-      float d = e * l;
+    const float top = fmaxf(M, warp_max(m));
+    const float e = s < j.parts ? ex2(m - top) : 0.f, was = ex2(M - top);
+    float d = e * l;
 #pragma unroll
-      for (int off = 16; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
-      den = den * was + d;
-      acc = make_float4(acc.x * was, acc.y * was, acc.z * was, acc.w * was);
-      M = mn;
-      const int cnt = min(32, (ns - at + step - 1) / step);
+    for (int off = 16; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
+    den = den * was + d;
+    acc = make_float4(acc.x * was, acc.y * was, acc.z * was, acc.w * was);
+    M = top;
+    const int cnt = min(32, j.parts - at);
 #pragma unroll 4
-      for (int j = 0; j < cnt; ++j) {
-        const float w = __shfl_sync(0xffffffffu, e, j);
-        const float4 o = __ldcg(reinterpret_cast<const float4*>(part(at + j * step) + n * 128) + lane);
-        acc.x += w * o.x;
-        acc.y += w * o.y;
-        acc.z += w * o.z;
-        acc.w += w * o.w;
-      }
+    for (int i = 0; i < cnt; ++i) {
+      const float w = __shfl_sync(0xffffffffu, e, i);
+      const float4 o = __ldcg(reinterpret_cast<const float4*>(j.part(p, at + i, n_rows) + n * 128) + lane);
+      acc.x += w * o.x;
+      acc.y += w * o.y;
+      acc.z += w * o.z;
+      acc.w += w * o.w;
     }
-  };
-  const int n0 = blockIdx.y * 8;
-  float M, den;
-  float4 acc;
-  if (ns <= kFewParts) {
-    const int n = n0 + warp;
-    if (n >= p.rows || rg * p.lsub + n / p.G >= p.L) return;
-    gather(n, 0, 1, M, den, acc);
-    const float inv = 1.f / den;
-    write(n, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-    return;
   }
-  for (int r = 0; r < 8; ++r) {
-    const int n = n0 + r;
-    if (n >= p.rows || rg * p.lsub + n / p.G >= p.L) return;
-    gather(n, warp, 8, M, den, acc);
-    *reinterpret_cast<float4*>(&s_acc[warp][4 * lane]) = acc;
-    if (lane == 0) {
-      s_den[warp] = den;
-      s_top[warp] = M;
+  const float inv = 1.f / den;
+  const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+  reinterpret_cast<uint2*>(j.row(p, n))[lane] =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+}
+
+// Few lists of many parts: CTA (list, row), four groups of 128 threads, a head dim each, that take every fourth part.
+constexpr int kJoinThreads = 512;
+constexpr int kMaxCtas = 1024;   // parts of a list are at most the grid
+__global__ void __launch_bounds__(kJoinThreads) join_many_kernel(const Params p, int n_rows, int ctas) {
+  __shared__ float s_w[kMaxCtas], s_red[kJoinThreads / 32], s_acc[4][128];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int t = threadIdx.x, lane = t & 31, n = blockIdx.y;
+  JoinList j;
+  if (!j.find(p, blockIdx.x, ctas, lane) || j.rg * p.lsub + n / p.G >= p.L) return;
+  float m[kMaxCtas / kJoinThreads], l[kMaxCtas / kJoinThreads], M = -CUDART_INF_F;
+#pragma unroll
+  for (int i = 0; i < kMaxCtas / kJoinThreads; ++i) {
+    const int s = i * kJoinThreads + t;
+    m[i] = -CUDART_INF_F;
+    l[i] = 0.f;
+    if (s < j.parts) {
+      m[i] = __ldcg(j.part(p, s, n_rows) + n_rows * 128 + n);
+      l[i] = __ldcg(j.part(p, s, n_rows) + n_rows * 129 + n);
     }
-    __syncthreads();
-    if (warp == r) {
-      float top = s_top[0];
-      for (int w = 1; w < 8; ++w) top = fmaxf(top, s_top[w]);
-      float d = 0.f;
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int w = 0; w < 8; ++w) {
-        const float e = ex2(s_top[w] - top);
-        const float4 o = *reinterpret_cast<const float4*>(&s_acc[w][4 * lane]);
-        d += e * s_den[w];
-        a.x += e * o.x;
-        a.y += e * o.y;
-        a.z += e * o.z;
-        a.w += e * o.w;
-      }
-      const float inv = 1.f / d;
-      write(n, make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv));
-    }
-    __syncthreads();
+    M = fmaxf(M, m[i]);
   }
+  M = warp_max(M);
+  if (lane == 0) s_red[t >> 5] = M;
+  __syncthreads();
+  M = warp_max(s_red[lane % (kJoinThreads / 32)]);
+  float den = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMaxCtas / kJoinThreads; ++i) {
+    const float e = ex2(m[i] - M);
+    if (i * kJoinThreads + t < j.parts) s_w[i * kJoinThreads + t] = e;
+    den = fmaf(e, l[i], den);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) den += __shfl_xor_sync(0xffffffffu, den, off);
+  __syncthreads();
+  if (lane == 0) s_red[t >> 5] = den;
+  const int x = t & 127, g = t >> 7;
+  float acc = 0.f;
+#pragma unroll 8
+  for (int s = g; s < j.parts; s += 4) acc = fmaf(s_w[s], __ldcg(j.part(p, s, n_rows) + n * 128 + x), acc);
+  s_acc[g][x] = acc;
+  __syncthreads();
+  if (t >= 128) return;
+  den = 0.f;
+  for (int w = 0; w < kJoinThreads / 32; ++w) den += s_red[w];
+  j.row(p, n)[x] = __bfloat16_as_ushort(__float2bfloat16_rn(((s_acc[0][x] + s_acc[1][x]) + (s_acc[2][x] + s_acc[3][x])) / den));
 }
 
 template <int N, int NC, int STAGES>
@@ -1735,12 +1767,13 @@ Kv8AttnPlan plan_attention_kv8(int B, int L, int Hq, int Hkv, int max_pages, int
   const long long lists = static_cast<long long>(B) * Hkv * pl.row_groups;
   const long long tiles = lists * ((max_pages + kTilePages - 1) / kTilePages);
   const long long ctas = many ? num_sms : 2ll * num_sms;
-  pl.grid = static_cast<int>(tiles < ctas ? tiles : ctas);
+  pl.grid = static_cast<int>(tiles < ctas ? tiles : ctas < kMaxCtas ? ctas : kMaxCtas);
   // (a tile a list at most: no list is cut)
   pl.parts = max_pages <= kTilePages ? 0 : 2 * pl.grid;
-  // Lists of few parts are joined by the CTA that writes the last (128 blocks of 4 over 512-4096 tokens: a kernel for it
-  // takes 10 us more); many parts of a list are read by more warps.
-  pl.join_here = pl.parts > 0 && !many && lists * kFewParts / 2 >= pl.grid;
+  // Parts a list: about the CTAs over the lists.  Where they are few the CTA that writes the last joins them (few rows;
+  // 128 blocks of 4 over 512-4096 tokens: a kernel for it takes 10 us more), or a warp a row; many are read by a CTA a row.
+  pl.many_parts = lists * kFewParts < pl.grid;
+  pl.join_here = pl.parts > 0 && !many && !pl.many_parts;
   pl.work_bytes = pl.join_here ? (static_cast<size_t>(pl.grid) + 1) * sizeof(int) : 0;
   pl.part_bytes = static_cast<size_t>(pl.parts) * pl.n_rows * kPartRow * sizeof(float);
   auto place = [](size_t& end, size_t bytes) {
@@ -1812,7 +1845,8 @@ cudaError_t launch_attention_kv8(const Kv8AttnParams& a, const Kv8AttnPlan& pl, 
                        : launch_few<16, 16, 6>(tk, tv, p, pl.grid, stream);
   }
   if (e != cudaSuccess || pl.parts == 0 || pl.join_here) return e;
-  return launch_pdl(join_kernel, dim3(lists, (p.rows + 7) / 8), dim3(256), 0, stream, p, pl.n_rows, pl.grid);
+  if (pl.many_parts) return launch_pdl(join_many_kernel, dim3(lists, p.rows), dim3(kJoinThreads), 0, stream, p, pl.n_rows, pl.grid);
+  return launch_pdl(join_few_kernel, dim3(lists, (p.rows + 7) / 8), dim3(256), 0, stream, p, pl.n_rows, pl.grid);
 }
 
 }  // namespace bdlm

@@ -66,7 +66,7 @@ struct Kv8AttnPlan {
   int lsub, row_groups, rows;   // block positions and query rows of a row group
   int n_rows;                   // rows padded
   int grid;
-  bool join_here;               // lists that are cut are joined by the attention kernel itself
+  bool many_parts, join_here;   // join_here: by the attention kernel itself
   long long parts;
   size_t part_bytes, cum_offset, q_offset, q_scale_offset, bytes, work_bytes;   // of the workspace
 };
