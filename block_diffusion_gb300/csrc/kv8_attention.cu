@@ -967,7 +967,8 @@ struct Many {
   static constexpr int kStagesK = SUB == 2 ? 3 : 4, kStagesV = SUB == 2 ? 2 : 3;
   static constexpr int kSoftmaxWarps = 8 * SUB;
   static constexpr int kConvWarps = SUB == 2 ? 2 : 4;
-  static constexpr int kThreads = 64 + 32 * (kSoftmaxWarps + kConvWarps);
+  static constexpr int kSoftmax0 = 2 + kConvWarps;      // first softmax warp
+  static constexpr int kThreads = 32 * (kSoftmax0 + kSoftmaxWarps);
   static constexpr int kChunk = 8;                      // tiles of a descriptor
   static constexpr int kWide = 2 * kStage;              // a tile's V in float16
   static constexpr size_t kSmem = 1024 + kRowsItem * 256 + (kStagesK + kStagesV) * kStage + 2 * kWide;
@@ -1312,11 +1313,11 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       if (elect_one()) umma_commit(&bar_done);
       __syncwarp();
     }
-  } else if (warp >= 2 + F::kSoftmaxWarps) {
+  } else if (warp < 2 + F::kConvWarps) {
     // =================================================================== converters
     // Lane l takes 16 dims (chunk l % 8) of tokens l / 8 + 4k: 16 bytes in, twice 16 out.  Lanes of the two
     // halves write their two pieces in opposite order, so eight lanes' stores meet no bank twice.
-    const int w = warp - 2 - F::kSoftmaxWarps, c8 = lane & 7;
+    const int w = warp - 2, c8 = lane & 7;
     bool ok = true;
     int vst = 0, u = 0;
     uint32_t vph = 0;
@@ -1365,10 +1366,10 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar_cempty[rs]);
     }
-  } else {
+  } else if (warp >= F::kSoftmax0) {
     // =================================================================== softmax, epilogue
-    const int x = (warp - 2) >> 3;
-    const int half = ((warp - 2) >> 2) & 1;
+    const int x = (warp - F::kSoftmax0) >> 3;
+    const int half = ((warp - F::kSoftmax0) >> 2) & 1;
     const int q4 = warp & 3;
     const int n = (q4 << 5) | lane;
     const int pq = x * 4 + q4;   // the two halves' exchange barriers
@@ -1439,19 +1440,16 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             const float2 s = scales[2 * g2 + g];
             const float a = s.x * c.q_scale, b = s.y - m_run;
             const float2 a2 = make_float2(a, a), b2 = make_float2(b, b);
-            float2 e[8];
+            float2 t2 = make_float2(0.f, 0.f);   // (a tree's partial sums would be spilled)
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               const int at = g * 16 + 2 * k;
               const float2 y = __ffma2_rn(make_float2(__uint_as_float(r[at]), __uint_as_float(r[at + 1])), a2, b2);
-              e[k] = make_float2(ex2(y.x), ex2(y.y));
-              pk[g * 8 + k] = half2_bits(e[k].x, e[k].y);
+              const float2 e = make_float2(ex2(y.x), ex2(y.y));
+              pk[g * 8 + k] = half2_bits(e.x, e.y);
+              t2 = __fadd2_rn(t2, e);
             }
-#pragma unroll
-            for (int w = 4; w > 0; w >>= 1)
-#pragma unroll
-              for (int k = 0; k < w; ++k) e[k] = __fadd2_rn(e[k], e[k + w]);
-            sum = fmaf(e[0].x + e[0].y, ex2(-s.y), sum);
+            sum = fmaf(t2.x + t2.y, ex2(-s.y), sum);
           }
           tmem_st16(tSx + g2 * 16, pk);   // tokens 64h + 32 g2 .. + 31 as 16 columns
         }
@@ -1485,7 +1483,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         ++pair_ends;
         const int i_row = c.rg * p.lsub + r_item / p.G;
         const bool live = r_item < p.rows && i_row < p.L;
-        uint8_t* stage = s_stage[warp - 2];
+        uint8_t* stage = s_stage[warp - F::kSoftmax0];
         if (c.slot < 0) {
           const float inv = 1.f / l_row;
           uint32_t w[32];
@@ -1770,10 +1768,12 @@ Kv8AttnPlan plan_attention_kv8(int B, int L, int Hq, int Hkv, int max_pages, int
   pl.grid = static_cast<int>(tiles < ctas ? tiles : ctas < kMaxCtas ? ctas : kMaxCtas);
   // (a tile a list at most: no list is cut)
   pl.parts = max_pages <= kTilePages ? 0 : 2 * pl.grid;
-  // Parts a list: about the CTAs over the lists.  Where they are few the CTA that writes the last joins them (few rows;
-  // 128 blocks of 4 over 512-4096 tokens: a kernel for it takes 10 us more), or a warp a row; many are read by a CTA a row.
+  // Parts a list: about the CTAs over the lists.  With more lists than CTAs the CTA that writes a list's last part joins
+  // them, beside its copies (128 blocks of 4 over 512-4096 tokens: 113 us, 119 with a kernel for it); with fewer, whose
+  // parts are all written last, a kernel is as fast or faster (8 blocks of 4 over 500-1500: 17.4 us against 19.5).  Few
+  // lists of many parts take a CTA a row (one request of 6000 tokens: 16.7 us against 23 to 30).
   pl.many_parts = lists * kFewParts < pl.grid;
-  pl.join_here = pl.parts > 0 && !many && !pl.many_parts;
+  pl.join_here = pl.parts > 0 && !many && lists >= pl.grid;
   pl.work_bytes = pl.join_here ? (static_cast<size_t>(pl.grid) + 1) * sizeof(int) : 0;
   pl.part_bytes = static_cast<size_t>(pl.parts) * pl.n_rows * kPartRow * sizeof(float);
   auto place = [](size_t& end, size_t bytes) {
