@@ -48,7 +48,7 @@ struct Params {
   uint16_t* out;
   float* part;       // unit u's parts: 2u (of a list that began before it), 2u + 1 (of one that begins in it)
   int* err;
-  int* work;         // [0] CTAs finished, [1 + u] parts written of the list that unit u's end cuts (join_here)
+  int* work;         // [0] CTAs finished, then parts written of the list that each unit's end cuts (join_here)
   const int* cum;    // [B + 1] tiles of the sequences before each (null: up to kFewSequences sequences)
   const float* q_scale;   // many rows: 2^e of each row group's queries
   int B, L, Hq, Hkv, G, max_pages, num_pages, lsub, row_groups, rows;
@@ -314,18 +314,19 @@ constexpr int kFewParts = 8;    // parts a list, about
 // ------------------------------------------------------------------ up to 32 query rows per KV head
 //
 // Transposed: S^T = K Q^T with 128 tokens on M and the query rows on N, O^T += V^T W^T with the 128 head
-// dims on M, so a few rows fill the tensor cores' tiles.  Warp 6 walks the work ahead of all others: it looks up
-// pages and scales, and turns the queries into their parts.  Warp 0 streams K and V (TMA, a box of 2 KB a
-// page, into a ring of 16 KB stages); warp 1 issues the MMAs; warps 2-5, a token (of S^T) or head dim (of
-// O^T) a thread, do the softmax.  A chunk of tiles whose
+// dims on M, so a few rows fill the tensor cores' tiles.  The last warp walks the work ahead of all others: it looks
+// up pages and scales, and turns the queries into their parts.  Warp 0 streams K and V (TMA, a box of 2 KB a
+// page, into a ring of 16 KB stages); warp 1 issues the MMAs; four warps for every 16 rows, a token (of S^T) or head dim
+// (of O^T) a thread, do the softmax.  A chunk of tiles whose
 // S^T fit tensor memory is taken at once: the maxima over all of it, then its weights tile by tile.  S^T
 // is double-buffered and K of chunk u + 1 streams ahead of V of chunk u.
-
-constexpr int kFewThreads = 96 + kSoftmaxThreads;
 
 // N: rows of the MMAs, NC: rows that the softmax computes (the others' weights stay zero).
 template <int N, int STAGES>
 struct Few {
+  static constexpr int kSets = N / 16;          // of softmax warps: 16 rows each, of all tokens
+  static constexpr int kSoft = 128 * kSets;     // their threads
+  static constexpr int kThreads = 96 + kSoft;
   static constexpr int kTmemCols = 256;   // two CTAs per SM
   static constexpr int kChunk = (kTmemCols - N) / (2 * N);
   static constexpr int kChunkPages = kChunk * kTilePages;
@@ -344,45 +345,45 @@ __device__ __forceinline__ void split_half2(uint32_t w, uint32_t& hi, uint32_t& 
 // Joins the parts of chunk c's list, in their order whoever comes last:
 //     out = sum_s e_s O_s / sum_s e_s l_s,   e_s = 2^(m_s - M),
 // two parts at a time, M and the sums brought along.  128 threads, a head dim each.
-template <int N, int NC>
-__device__ __forceinline__ void join_parts(const Params& p, const Chunk& c, int x, size_t row, int live, float* s_m, float* s_l,
-                                           float* s_alpha, float (*s_red)[N]) {
+// Rows c0 .. c0 + CW - 1, of which `live` are there, from `row` of the output on; s_*: those rows'.
+template <int N, int CW>
+__device__ __forceinline__ void join_parts(const Params& p, const Chunk& c, int x, int c0, size_t row, int g, int live, float* s_l,
+                                           float* s_alpha, float* s_e0, float* s_e1, int barrier) {
   auto part = [&](int s) { return p.part + static_cast<size_t>(2 * (c.u0 + s) + (s == 0 ? 1 : 0)) * N * kPartRow; };
-  float acc[NC];
+  float acc[CW];
 #pragma unroll
-  for (int n = 0; n < NC; ++n) acc[n] = 0.f;
-  float M = -CUDART_INF_F, den = 0.f;   // threads x < NC: of row x
+  for (int n = 0; n < CW; ++n) acc[n] = 0.f;
+  float M = -CUDART_INF_F, den = 0.f;   // threads x < CW: of row c0 + x
 #pragma unroll 1
   for (int s0 = 0; s0 < c.parts; s0 += 2) {
     const bool two = s0 + 1 < c.parts;
     const float *a = part(s0), *b = part(two ? s0 + 1 : s0);
-    float o0[NC], o1[NC];
+    float o0[CW], o1[CW];
 #pragma unroll
-    for (int n = 0; n < NC; ++n) {
-      o0[n] = n < live ? __ldcg(a + n * 128 + x) : 0.f;
-      o1[n] = n < live ? __ldcg(b + n * 128 + x) : 0.f;
+    for (int n = 0; n < CW; ++n) {
+      o0[n] = n < live ? __ldcg(a + (c0 + n) * 128 + x) : 0.f;
+      o1[n] = n < live ? __ldcg(b + (c0 + n) * 128 + x) : 0.f;
     }
-    if (x < NC) {
-      const float m0 = __ldcg(a + N * 128 + x), l0 = __ldcg(a + N * 129 + x);
-      const float m1 = two ? __ldcg(b + N * 128 + x) : -CUDART_INF_F, l1 = __ldcg(b + N * 129 + x);
+    if (x < CW) {
+      const float m0 = __ldcg(a + N * 128 + c0 + x), l0 = __ldcg(a + N * 129 + c0 + x);
+      const float m1 = two ? __ldcg(b + N * 128 + c0 + x) : -CUDART_INF_F, l1 = __ldcg(b + N * 129 + c0 + x);
       const float top = fmaxf(M, fmaxf(m0, m1));
       const float was = ex2(M - top), e0 = ex2(m0 - top), e1 = ex2(m1 - top);
       den = fmaf(den, was, fmaf(e0, l0, e1 * l1));
       M = top;
       s_alpha[x] = was;
-      s_red[0][x] = e0;
-      s_red[1][x] = e1;
+      s_e0[x] = e0;
+      s_e1[x] = e1;
     }
-    named_barrier(1, kSoftmaxThreads);
+    named_barrier(barrier, 128);
 #pragma unroll
-    for (int n = 0; n < NC; ++n) acc[n] = fmaf(acc[n], s_alpha[n], fmaf(s_red[0][n], o0[n], s_red[1][n] * o1[n]));
-    named_barrier(1, kSoftmaxThreads);
+    for (int n = 0; n < CW; ++n) acc[n] = fmaf(acc[n], s_alpha[n], fmaf(s_e0[n], o0[n], s_e1[n] * o1[n]));
+    named_barrier(barrier, 128);
   }
-  if (x < NC) s_l[x] = 1.f / den;
-  named_barrier(1, kSoftmaxThreads);
-  int g = 0;
+  if (x < CW) s_l[x] = 1.f / den;
+  named_barrier(barrier, 128);
 #pragma unroll
-  for (int n = 0; n < NC; ++n) {
+  for (int n = 0; n < CW; ++n) {
     if (n >= live) break;
     p.out[row * 128 + x] = __bfloat16_as_ushort(__float2bfloat16_rn(acc[n] * s_l[n]));
     ++row;
@@ -394,7 +395,7 @@ __device__ __forceinline__ void join_parts(const Params& p, const Chunk& c, int 
 }
 
 template <int N, int NC, int STAGES>
-__global__ void __launch_bounds__(kFewThreads, 2)
+__global__ void __launch_bounds__(Few<N, STAGES>::kThreads, 2)
 few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Params p) {
   using F = Few<N, STAGES>;
   constexpr int kChunk = F::kChunk;
@@ -405,7 +406,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
   uint8_t* sP = sKV + STAGES * kStage;   // two buffers of two parts x N / 16 x 128 tokens x 16 bytes, a row each
   __shared__ uint64_t bar_qfull, bar_qempty, bar_full[STAGES], bar_empty[STAGES];
   __shared__ uint64_t bar_sfull[2], bar_sfree[2], bar_pfull[2], bar_pempty[2];
-  __shared__ uint64_t bar_oready, bar_ofull[2], bar_done;
+  __shared__ uint64_t bar_ofull[2], bar_done;
   __shared__ uint64_t bar_cfull[kRing], bar_cempty[kRing];
   __shared__ Chunk s_chunk[kRing];
   __shared__ float2 s_scale[kRing][F::kChunkPages];   // sK, log2 sV
@@ -413,7 +414,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
   __shared__ __align__(16) float s_m[N], s_alpha[N], s_l[N], s_red[4][N];
-  __shared__ int s_need[2], s_pflag[2], s_join;
+  __shared__ int s_need[F::kSets][2], s_join[F::kSets];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -425,20 +426,18 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar_sfull[i], 1);
-      mbar_init(&bar_sfree[i], kSoftmaxThreads);
-      mbar_init(&bar_pfull[i], kSoftmaxThreads);
+      mbar_init(&bar_sfree[i], F::kSoft);
+      mbar_init(&bar_pfull[i], F::kSoft);
       mbar_init(&bar_pempty[i], 1);
       mbar_init(&bar_ofull[i], 1);
     }
-    mbar_init(&bar_oready, kSoftmaxThreads);
     mbar_init(&bar_done, 1);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&bar_cfull[i], 1);
-      mbar_init(&bar_cempty[i], 3);   // copies, MMA, softmax
+      mbar_init(&bar_cempty[i], 2 + F::kSets);   // copies, MMA, softmax
     }
     abort_flag = 0;
-    s_need[0] = s_need[1] = 0;
-    s_pflag[0] = s_pflag[1] = 0;
+    for (int s = 0; s < F::kSets; ++s) s_need[s][0] = s_need[s][1] = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -446,7 +445,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     tmem_relinquish();
   }
   if constexpr (NC < N) {
-    for (int o = threadIdx.x * 16; o < 2 * N * 256; o += kFewThreads * 16)
+    for (int o = threadIdx.x * 16; o < 2 * N * 256; o += F::kThreads * 16)
       *reinterpret_cast<uint4*>(sP + o) = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
   }
@@ -513,7 +512,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     const uint64_t q_desc = smem_desc(smem_u32(sQ), 16, 1024), p_desc = smem_desc_plain(smem_u32(sP), 128, kTile * 16);
     const uint64_t k_desc = smem_desc(smem_u32(sKV), 16, 1024), v_desc = smem_desc(smem_u32(sKV), kStage, 1024);
     bool ok = true;
-    int st = 0, pcount = 0, ocount = 0, q_used = 0;
+    int st = 0, pcount = 0, q_used = 0;
     uint32_t ph = 0;
     auto do_s = [&](bool first, bool last, int n_tiles, int u) {
       if (!(ok = mbar_wait_warp(&bar_sfree[u & 1], ((u >> 1) & 1) ^ 1, &abort_flag))) return;
@@ -556,10 +555,6 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         }
         const int pb = pcount & 1;
         if (!(ok = mbar_wait_warp(&bar_pfull[pb], (pcount >> 1) & 1, &abort_flag))) return;
-        if (!first && j == 0 && s_pflag[pb]) {   // the softmax brings O to new maxima first
-          if (!(ok = mbar_wait_warp(&bar_oready, ocount & 1, &abort_flag))) return;
-          ++ocount;
-        }
         tc_fence_after();
         const uint64_t vd = v_desc + static_cast<uint32_t>(st * (kStage >> 4)), pd = p_desc + static_cast<uint32_t>(pb * (N * 16));
         const int steps = (valid + 31) / 32;
@@ -601,30 +596,39 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     }
     if (elect_one()) umma_commit(&bar_done);
     __syncwarp();
-  } else if (warp == 6) {
+  } else if (warp == 2 + F::kSoft / 32) {
     // =================================================================== the walk, queries
     bool ok = true;
     Walk<kChunk> walk;
     walk.init(p, lane);
-    uint4 qr[N / 2];
+    // rows 2i and 2i + 1 of the queries, eight values a lane; 32 rows are read twice rather than kept
+    constexpr bool kKeep = N <= 16;
+    uint4 qr[kKeep ? N / 2 : 1];
     int q_exp = 0, q_loads = 0, seq = 0;
+    auto query = [&](const Chunk& c, int i) {
+      const int n = 2 * i + (lane >> 4);
+      const int pos = c.rg * p.lsub + n / p.G;
+      if (n >= p.rows || pos >= p.L) return make_uint4(0, 0, 0, 0);
+      return __ldg(reinterpret_cast<const uint4*>(p.q + ((static_cast<size_t>(c.b) * p.L + pos) * p.Hq + c.kvh * p.G + n % p.G) * 128) +
+                   (lane & 15));
+    };
     auto ask_q = [&](const Chunk& c) {
+      if constexpr (kKeep) {
 #pragma unroll
-      for (int i = 0; i < N / 2; ++i) {
-        const int n = 2 * i + (lane >> 4);
-        const int pos = c.rg * p.lsub + n / p.G;
-        qr[i] = make_uint4(0, 0, 0, 0);
-        if (n < p.rows && pos < p.L)
-          qr[i] = __ldg(reinterpret_cast<const uint4*>(
-              p.q + ((static_cast<size_t>(c.b) * p.L + pos) * p.Hq + c.kvh * p.G + n % p.G) * 128) + (lane & 15));
+        for (int i = 0; i < N / 2; ++i) qr[i] = query(c, i);
       }
     };
     // Publishes chunk number seq, and then the parts of its queries, once the MMAs on the last ones are done.
     auto publish = [&](Chunk& c, const PageLoads<F::kChunkPages>& pages) {
       if (c.first && !c.end) {
         float most = 0.f;
+        if constexpr (kKeep) {
 #pragma unroll
-        for (int i = 0; i < N / 2; ++i) most = fmaxf(most, magnitude(qr[i]));
+          for (int i = 0; i < N / 2; ++i) most = fmaxf(most, magnitude(qr[i]));
+        } else {
+#pragma unroll 4
+          for (int i = 0; i < N / 2; ++i) most = fmaxf(most, magnitude(query(c, i)));
+        }
         q_exp = q_exponent(warp_max(most));
       }
       c.q_scale = pow2(q_exp) * p.scale_log2;
@@ -640,16 +644,22 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       if (c.end || !c.first) return;
       if (!(ok = mbar_wait_warp(&bar_qempty, (q_loads & 1) ^ 1, &abort_flag))) return;
       const float inv = pow2(-q_exp);
-#pragma unroll
-      for (int i = 0; i < N / 2; ++i) {
+      auto put = [&](int i, const uint4& v) {
         const int n = 2 * i + (lane >> 4);
-        const uint32_t u[4] = {qr[i].x, qr[i].y, qr[i].z, qr[i].w};
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) split_e4m3x2(bf16_lo(u[k]) * inv, bf16_hi(u[k]) * inv, hi[k], lo[k]);
         const uint32_t at = n * 128 + ((((lane & 15) >> 1) ^ (n & 7)) << 4) + (lane & 1) * 8;
         *reinterpret_cast<uint2*>(sQ + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
         *reinterpret_cast<uint2*>(sQ + N * 128 + at) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+      };
+      if constexpr (kKeep) {
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) put(i, qr[i]);
+      } else {
+#pragma unroll 4
+        for (int i = 0; i < N / 2; ++i) put(i, query(c, i));
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -686,11 +696,15 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     }
   } else {
     // =================================================================== softmax, epilogue
-    const int q4 = warp & 3;
+    // Set `set` of four warps computes rows c0 .. c0 + CW - 1 of every token; c0 and the sets' own barrier aside they
+    // do the same.
+    constexpr int CW = NC < 16 ? NC : 16;
+    static_assert(CW * F::kSets == NC, "a set for every 16 rows");
+    const int q4 = warp & 3, set = (warp - 2) >> 2, c0 = set * CW, own = 1 + set;
     const int x = (q4 << 5) | lane;   // tensor-memory lane: token of a tile, or head dim
     const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
-    constexpr int CW = NC < 16 ? NC : 16;   // rows taken at once
-    float2 l[NC / 2];
+    const uint32_t tOx = tO + lane_off + static_cast<uint32_t>(c0);
+    float2 l[CW / 2];
     bool ok = true;
     int pcount = 0;
     for (int u = 0; ok; ++u) {
@@ -700,20 +714,20 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       if (c.end) break;
       if (c.first) {
 #pragma unroll
-        for (int n = 0; n < NC / 2; ++n) l[n] = make_float2(0.f, 0.f);
-        if (x < NC) s_m[x] = -CUDART_INF_F;
+        for (int n = 0; n < CW / 2; ++n) l[n] = make_float2(0.f, 0.f);
+        if (x < CW) s_m[c0 + x] = -CUDART_INF_F;
       }
-      const uint32_t tS = tmem + lane_off + static_cast<uint32_t>((u & 1) * kChunk * N);
+      const uint32_t tS = tmem + lane_off + static_cast<uint32_t>((u & 1) * kChunk * N + c0);
       if (!(ok = mbar_wait_warp(&bar_sfull[u & 1], (u >> 1) & 1, &abort_flag))) break;
       tc_fence_after();
       // the exact maxima of x over the chunk (behind the last token scores may be anything: -inf)
       const int last_tile = (c.t_end - c.t0 - 1) / kTile;
       const bool cut = c.t_end - c.t0 - last_tile * kTile <= x;   // this thread's token of it is past the end
-      auto load = [&](int j, int g, uint32_t (&r)[CW]) {
+      auto load = [&](int j, uint32_t (&r)[CW]) {
         if constexpr (CW == 8)
           tmem_ld8(tS + j * N, r);
         else
-          tmem_ld16(tS + j * N + g * 16, r);
+          tmem_ld16(tS + j * N, r);
       };
       auto ready = [&](int j, uint32_t (&r)[CW]) {
         tmem_wait_ld();
@@ -723,14 +737,13 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
           for (int n = 0; n < CW; ++n) r[n] = 0xFF800000u;
         }
       };
-#pragma unroll
-      for (int g = 0; g < NC / CW; ++g) {
+      {
         float mx[CW];
 #pragma unroll
         for (int n = 0; n < CW; ++n) mx[n] = -CUDART_INF_F;
         for (int j = 0; j < c.n_tiles; ++j) {
           uint32_t r[CW];
-          load(j, g, r);
+          load(j, r);
           const float2 sc = s_scale[rs][j * kTilePages + (x >> 4)];
           const float a = sc.x * c.q_scale;
           ready(j, r);
@@ -746,104 +759,85 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         if (lane == 0) {
 #pragma unroll
           for (int n = 0; n < CW; n += 4)
-            *reinterpret_cast<float4*>(&s_red[q4][g * CW + n]) = make_float4(mx[n], mx[n + 1], mx[n + 2], mx[n + 3]);
+            *reinterpret_cast<float4*>(&s_red[q4][c0 + n]) = make_float4(mx[n], mx[n + 1], mx[n + 2], mx[n + 3]);
         }
       }
-      named_barrier(1, kSoftmaxThreads);
-      if (x == 0) s_need[(u + 1) & 1] = 0;   // every reader of that slot is past this barrier
-      if (x < NC) {
-        const float mc = fmaxf(fmaxf(s_red[0][x], s_red[1][x]), fmaxf(s_red[2][x], s_red[3][x]));
-        const float mo = s_m[x];
+      named_barrier(own, 128);
+      if (x == 0) s_need[set][(u + 1) & 1] = 0;   // every reader of that slot is past this barrier
+      if (x < CW) {
+        const int n = c0 + x;
+        const float mc = fmaxf(fmaxf(s_red[0][n], s_red[1][n]), fmaxf(s_red[2][n], s_red[3][n]));
+        const float mo = s_m[n];
         float alpha = 1.f;
         if (mo == -CUDART_INF_F) {
-          s_m[x] = mc;
+          s_m[n] = mc;
         } else if (mc - mo > kLazy) {
           alpha = ex2(mo - mc);
-          s_m[x] = mc;
-          s_need[u & 1] = 1;
+          s_m[n] = mc;
+          s_need[set][u & 1] = 1;
         }
-        s_alpha[x] = alpha;
+        s_alpha[n] = alpha;
       }
-      named_barrier(1, kSoftmaxThreads);
-      const bool need = s_need[u & 1] != 0;
+      named_barrier(own, 128);
+      const bool need = s_need[set][u & 1] != 0;
       if (!c.first && need) {
-        // O^T and l to the new maxima
+        // these rows of O^T and l to the new maxima
         if (!(ok = mbar_wait_warp(&bar_ofull[(u - 1) & 1], ((u - 1) >> 1) & 1, &abort_flag))) break;
         tc_fence_after();
+        uint32_t r[16];
+        tmem_ld16(tOx, r);
+        tmem_wait_ld();
+        tmem_regs_ready(r);
 #pragma unroll
-        for (int cg = 0; cg < N / 16; ++cg) {
-          uint32_t r[16];
-          tmem_ld16(tO + lane_off + cg * 16, r);
-          tmem_wait_ld();
-          tmem_regs_ready(r);
-#pragma unroll
-          for (int k = 0; k < 16; ++k)
-            if (cg * 16 + k < NC) r[k] = __float_as_uint(__uint_as_float(r[k]) * s_alpha[cg * 16 + k]);
-          tmem_st16(tO + lane_off + cg * 16, r);
-        }
+        for (int n = 0; n < CW; ++n) r[n] = __float_as_uint(__uint_as_float(r[n]) * s_alpha[c0 + n]);
+        tmem_st16(tOx, r);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(&bar_oready);
 #pragma unroll
-        for (int n = 0; n < NC / 2; ++n) l[n] = __fmul2_rn(l[n], make_float2(s_alpha[2 * n], s_alpha[2 * n + 1]));
+        for (int n = 0; n < CW / 2; ++n) l[n] = __fmul2_rn(l[n], make_float2(s_alpha[c0 + 2 * n], s_alpha[c0 + 2 * n + 1]));
       }
       // The weights, tile by tile, into shared memory.  2^(c sK q . k - m + 7) is what l adds up; times sV it is w, whose
-      // float16 (finer than both parts, and exact to subtract from) is split.
+      // float16 (finer than both parts, and exact to subtract from) is split.  (PV of the chunk's first tile waits for the
+      // weights, and so for O's new maxima.)
       {
-        // (32 rows leave no registers for the maxima and a tile ahead)
-        constexpr bool kAhead = NC <= 16;
         float2 mr[CW / 2];
-        if constexpr (kAhead) {
 #pragma unroll
-          for (int n = 0; n < CW / 2; ++n) mr[n] = make_float2(kWeightExp - s_m[2 * n], kWeightExp - s_m[2 * n + 1]);
-        }
+        for (int n = 0; n < CW / 2; ++n) mr[n] = make_float2(kWeightExp - s_m[c0 + 2 * n], kWeightExp - s_m[c0 + 2 * n + 1]);
         uint32_t r[CW];
-        load(0, 0, r);
+        load(0, r);
         for (int j = 0; j < c.n_tiles && ok; ++j) {
           const float2 sc = s_scale[rs][j * kTilePages + (x >> 4)];
           const float a = sc.x * c.q_scale, sv = ex2(sc.y);
-          const int pb = pcount & 1;
-          uint8_t* to = sP + pb * (N * 256) + x * 16;
+          ready(j, r);
+          uint32_t w[CW / 2];   // float16 pairs
 #pragma unroll
-          for (int g = 0; g < NC / CW; ++g) {
-            ready(j, r);
-            if constexpr (!kAhead) {
-#pragma unroll
-              for (int n = 0; n < CW / 2; ++n) mr[n] = make_float2(kWeightExp - s_m[g * CW + 2 * n], kWeightExp - s_m[g * CW + 2 * n + 1]);
-            }
-            uint32_t w[CW / 2];   // float16 pairs
-#pragma unroll
-            for (int n = 0; n < CW / 2; ++n) {
-              const float2 y = __ffma2_rn(make_float2(__uint_as_float(r[2 * n]), __uint_as_float(r[2 * n + 1])), make_float2(a, a), mr[n]);
-              const float2 e = make_float2(ex2(y.x), ex2(y.y));
-              l[g * CW / 2 + n] = __fadd2_rn(l[g * CW / 2 + n], e);
-              const float2 z = __fmul2_rn(e, make_float2(sv, sv));
-              w[n] = half2_bits(z.x, z.y);
-            }
-            if (g + 1 < NC / CW)
-              load(j, g + 1, r);
-            else if (j + 1 < c.n_tiles)
-              load(j + 1, 0, r);
-            uint32_t hi[CW / 4], lo[CW / 4];
-#pragma unroll
-            for (int n = 0; n < CW / 4; ++n) {
-              uint32_t h[2], o[2];
-#pragma unroll
-              for (int k = 0; k < 2; ++k) split_half2(w[2 * n + k], h[k], o[k]);
-              hi[n] = h[0] | h[1] << 16;
-              lo[n] = o[0] | o[1] << 16;
-            }
-            if (g == 0 && !(ok = mbar_wait_warp(&bar_pempty[pb], ((pcount >> 1) & 1) ^ 1, &abort_flag))) break;
-            if constexpr (NC == 8) {
-              *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
-              *reinterpret_cast<uint2*>(to + N * 128) = make_uint2(lo[0], lo[1]);
-            } else {
-              *reinterpret_cast<uint4*>(to + g * (kTile * 16)) = make_uint4(hi[0], hi[1], hi[CW / 4 - 2], hi[CW / 4 - 1]);
-              *reinterpret_cast<uint4*>(to + N * 128 + g * (kTile * 16)) = make_uint4(lo[0], lo[1], lo[CW / 4 - 2], lo[CW / 4 - 1]);
-            }
+          for (int n = 0; n < CW / 2; ++n) {
+            const float2 y = __ffma2_rn(make_float2(__uint_as_float(r[2 * n]), __uint_as_float(r[2 * n + 1])), make_float2(a, a), mr[n]);
+            const float2 e = make_float2(ex2(y.x), ex2(y.y));
+            l[n] = __fadd2_rn(l[n], e);
+            const float2 z = __fmul2_rn(e, make_float2(sv, sv));
+            w[n] = half2_bits(z.x, z.y);
           }
-          if (!ok) break;
-          if (x == 0) s_pflag[pb] = j == 0 && need;
+          if (j + 1 < c.n_tiles) load(j + 1, r);
+          uint32_t hi[CW / 4], lo[CW / 4];
+#pragma unroll
+          for (int n = 0; n < CW / 4; ++n) {
+            uint32_t h[2], o[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) split_half2(w[2 * n + k], h[k], o[k]);
+            hi[n] = h[0] | h[1] << 16;
+            lo[n] = o[0] | o[1] << 16;
+          }
+          const int pb = pcount & 1;
+          if (!(ok = mbar_wait_warp(&bar_pempty[pb], ((pcount >> 1) & 1) ^ 1, &abort_flag))) break;
+          uint8_t* to = sP + pb * (N * 256) + set * (kTile * 16) + x * 16;
+          if constexpr (CW == 8) {
+            *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(to + N * 128) = make_uint2(lo[0], lo[1]);
+          } else {
+            *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[CW / 4 - 2], hi[CW / 4 - 1]);
+            *reinterpret_cast<uint4*>(to + N * 128) = make_uint4(lo[0], lo[1], lo[CW / 4 - 2], lo[CW / 4 - 1]);
+          }
           fence_proxy_async_smem();
           tc_fence_before();
           mbar_arrive(&bar_pfull[pb]);
@@ -858,44 +852,48 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         // The code from here on is met once a list, each time from memory: loops, not their bodies in a row.
         if (!(ok = mbar_wait_warp(&bar_ofull[u & 1], (u >> 1) & 1, &abort_flag))) break;
         tc_fence_after();
-        // the rows' sums, through the weights' buffers (no MMA reads them now)
-        float* sums = reinterpret_cast<float*>(sP);
+        // the rows' sums, through the weights' buffers (no MMA reads them now; the sets have a half each)
+        float* sums = reinterpret_cast<float*>(sP) + c0 * kTile;
 #pragma unroll
-        for (int n = 0; n < NC / 2; ++n) {
+        for (int n = 0; n < CW / 2; ++n) {
           sums[(2 * n) * kTile + x] = l[n].x;
           sums[(2 * n + 1) * kTile + x] = l[n].y;
         }
-        named_barrier(1, kSoftmaxThreads);
+        named_barrier(own, 128);
         {
-          constexpr int kEach = kSoftmaxThreads / NC;   // threads of a row
+          constexpr int kEach = 128 / CW;   // threads of a row
           float v = 0.f;
 #pragma unroll 4
           for (int i = x % kEach; i < kTile; i += kEach) v += sums[(x / kEach) * kTile + i];
 #pragma unroll
           for (int off = kEach / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-          if (x % kEach == 0) s_l[x / kEach] = c.slot < 0 ? 1.f / v : v;
+          if (x % kEach == 0) s_l[c0 + x / kEach] = c.slot < 0 ? 1.f / v : v;
         }
-        named_barrier(1, kSoftmaxThreads);
+        if constexpr (F::kSets > 1)
+          named_barrier(3, F::kSoft);   // before either set's next weights
+        else
+          named_barrier(own, 128);
         if constexpr (NC < N) {   // the rows that nothing is computed for read as zeros again
-          for (int o = x * 16; o < 2 * N * 256; o += kSoftmaxThreads * 16) *reinterpret_cast<uint4*>(sP + o) = make_uint4(0, 0, 0, 0);
+          for (int o = x * 16; o < 2 * N * 256; o += 128 * 16) *reinterpret_cast<uint4*>(sP + o) = make_uint4(0, 0, 0, 0);
         }
-        const size_t row0 = (static_cast<size_t>(c.b) * p.L + c.rg * p.lsub) * p.Hq + static_cast<size_t>(c.kvh) * p.G;
-        const int live = min(p.rows, (p.L - c.rg * p.lsub) * p.G);   // rows of the group that there are
-        float* mine = p.part + static_cast<size_t>(c.slot < 0 ? 0 : c.slot) * N * kPartRow;
+        const int first = c.rg * p.lsub + c0 / p.G;   // block position and head of row c0
+        const int live = max(0, min(min(p.rows, (p.L - c.rg * p.lsub) * p.G) - c0, CW));   // rows of the set that there are
+        const size_t row0 = (static_cast<size_t>(c.b) * p.L + first) * p.Hq + static_cast<size_t>(c.kvh) * p.G + c0 % p.G;
+        float* mine = p.part + static_cast<size_t>(c.slot < 0 ? 0 : c.slot) * N * kPartRow + c0 * 128;
         const uint64_t keep = l2_policy_evict_last();   // read back soon
-        int g = 0;
+        int g = c0 % p.G;
         size_t row = row0;
 #pragma unroll 1
         for (int n0 = 0; n0 < live; n0 += 4) {
           uint32_t r[4];
-          tmem_ld4(tO + lane_off + n0, r);
+          tmem_ld4(tOx + n0, r);
           tmem_wait_ld();
           tmem_regs_ready(r);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             if (n0 + k >= live) break;
             if (c.slot < 0)
-              p.out[row * 128 + x] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(r[k]) * s_l[n0 + k]));
+              p.out[row * 128 + x] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(r[k]) * s_l[c0 + n0 + k]));
             else
               st_global_hint(mine + (n0 + k) * 128 + x, __uint_as_float(r[k]), keep);
             ++row;
@@ -906,25 +904,26 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
           }
         }
         if (c.slot >= 0) {
-          if (x < NC) {
-            st_global_hint(mine + N * 128 + x, s_m[x], keep);
-            st_global_hint(mine + N * 129 + x, s_l[x], keep);
+          float* ml = p.part + static_cast<size_t>(c.slot) * N * kPartRow + N * 128 + c0;
+          if (x < CW) {
+            st_global_hint(ml + x, s_m[c0 + x], keep);
+            st_global_hint(ml + N + x, s_l[c0 + x], keep);
           }
           if (p.join_here) {
             __threadfence();
-            named_barrier(1, kSoftmaxThreads);
-            if (x == 0) s_join = atomicAdd(p.work + 1 + c.u0, 1) == c.parts - 1;
-            named_barrier(1, kSoftmaxThreads);
-            if (s_join) {
+            named_barrier(own, 128);
+            if (x == 0) s_join[set] = atomicAdd(p.work + 1 + c.u0 * F::kSets + set, 1) == c.parts - 1;
+            named_barrier(own, 128);
+            if (s_join[set]) {
               __threadfence();
-              join_parts<N, NC>(p, c, x, row0, live, s_m, s_l, s_alpha, s_red);
+              join_parts<N, CW>(p, c, x, c0, row0, c0 % p.G, live, s_l + c0, s_alpha + c0, s_red[0] + c0, s_red[1] + c0, own);
             }
           }
         }
         tc_fence_before();
       }
       // the chunk's descriptor and scales (and O^T) are done with
-      named_barrier(1, kSoftmaxThreads);
+      named_barrier(own, 128);
       if (x == 0) mbar_arrive(&bar_cempty[rs]);
       if (c.final) break;
     }
@@ -947,7 +946,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       last = atomicAdd(p.work, 1) == static_cast<int>(gridDim.x) - 1;
     }
     if (__shfl_sync(0xffffffffu, last, 0))
-      for (int u = lane; u <= static_cast<int>(gridDim.x); u += 32) p.work[u] = 0;
+      for (int u = lane; u <= static_cast<int>(gridDim.x) * F::kSets; u += 32) p.work[u] = 0;
   }
   if (threadIdx.x == 0 && abort_flag) atomicOr(p.err, BDLM_DEVERR_TIMEOUT);
 }
@@ -1748,7 +1747,7 @@ cudaError_t launch_few(const CUtensorMap& tk, const CUtensorMap& tv, const Param
     return cudaFuncSetAttribute(few_rows_kernel<N, NC, STAGES>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
   });
   if (e != cudaSuccess) return e;
-  return launch_pdl(few_rows_kernel<N, NC, STAGES>, dim3(grid), dim3(kFewThreads), smem, stream, tk, tv, p);
+  return launch_pdl(few_rows_kernel<N, NC, STAGES>, dim3(grid), dim3(Few<N, STAGES>::kThreads), smem, stream, tk, tv, p);
 }
 
 }  // namespace
@@ -1774,7 +1773,7 @@ Kv8AttnPlan plan_attention_kv8(int B, int L, int Hq, int Hkv, int max_pages, int
   // lists of many parts take a CTA a row (one request of 6000 tokens: 16.7 us against 23 to 30).
   pl.many_parts = lists * kFewParts < pl.grid;
   pl.join_here = pl.parts > 0 && !many && lists >= pl.grid;
-  pl.work_bytes = pl.join_here ? (static_cast<size_t>(pl.grid) + 1) * sizeof(int) : 0;
+  pl.work_bytes = pl.join_here ? (static_cast<size_t>(pl.grid) * (pl.n_rows / 16) + 1) * sizeof(int) : 0;
   pl.part_bytes = static_cast<size_t>(pl.parts) * pl.n_rows * kPartRow * sizeof(float);
   auto place = [](size_t& end, size_t bytes) {
     const size_t at = (end + 255) / 256 * 256;
