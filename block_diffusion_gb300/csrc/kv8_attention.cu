@@ -327,7 +327,10 @@ struct Few {
   static constexpr int kSets = N / 16;          // of softmax warps: 16 rows each, of all tokens
   static constexpr int kSoft = 128 * kSets;     // their threads
   static constexpr int kThreads = 96 + kSoft;
-  static constexpr int kTmemCols = 256;   // two CTAs per SM
+  // Two CTAs per SM with 16 rows.  With 32 one, twice as wide: two left chunks of three tiles, whose ends took as long as
+  // they (128 blocks of 8 over 512-4096 tokens: KFIG).
+  static constexpr int kCtas = N == 16 ? 2 : 1;
+  static constexpr int kTmemCols = 512 / kCtas;
   static constexpr int kChunk = (kTmemCols - N) / (2 * N);
   static constexpr int kChunkPages = kChunk * kTilePages;
   static constexpr size_t kSmem = 1024 + N * 256 + static_cast<size_t>(STAGES) * kStage + 2 * N * 256;
@@ -395,7 +398,7 @@ __device__ __forceinline__ void join_parts(const Params& p, const Chunk& c, int 
 }
 
 template <int N, int NC, int STAGES>
-__global__ void __launch_bounds__(Few<N, STAGES>::kThreads, 2)
+__global__ void __launch_bounds__(Few<N, STAGES>::kThreads, Few<N, STAGES>::kCtas)
 few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Params p) {
   using F = Few<N, STAGES>;
   constexpr int kChunk = F::kChunk;
@@ -601,34 +604,25 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     bool ok = true;
     Walk<kChunk> walk;
     walk.init(p, lane);
-    // rows 2i and 2i + 1 of the queries, eight values a lane; 32 rows are read twice rather than kept
-    constexpr bool kKeep = N <= 16;
-    uint4 qr[kKeep ? N / 2 : 1];
+    uint4 qr[N / 2];    // rows 2i and 2i + 1 of the queries, eight values a lane
     int q_exp = 0, q_loads = 0, seq = 0;
-    auto query = [&](const Chunk& c, int i) {
-      const int n = 2 * i + (lane >> 4);
-      const int pos = c.rg * p.lsub + n / p.G;
-      if (n >= p.rows || pos >= p.L) return make_uint4(0, 0, 0, 0);
-      return __ldg(reinterpret_cast<const uint4*>(p.q + ((static_cast<size_t>(c.b) * p.L + pos) * p.Hq + c.kvh * p.G + n % p.G) * 128) +
-                   (lane & 15));
-    };
     auto ask_q = [&](const Chunk& c) {
-      if constexpr (kKeep) {
 #pragma unroll
-        for (int i = 0; i < N / 2; ++i) qr[i] = query(c, i);
+      for (int i = 0; i < N / 2; ++i) {
+        const int n = 2 * i + (lane >> 4);
+        const int pos = c.rg * p.lsub + n / p.G;
+        qr[i] = make_uint4(0, 0, 0, 0);
+        if (n < p.rows && pos < p.L)
+          qr[i] = __ldg(reinterpret_cast<const uint4*>(
+              p.q + ((static_cast<size_t>(c.b) * p.L + pos) * p.Hq + c.kvh * p.G + n % p.G) * 128) + (lane & 15));
       }
     };
     // Publishes chunk number seq, and then the parts of its queries, once the MMAs on the last ones are done.
     auto publish = [&](Chunk& c, const PageLoads<F::kChunkPages>& pages) {
       if (c.first && !c.end) {
         float most = 0.f;
-        if constexpr (kKeep) {
 #pragma unroll
-          for (int i = 0; i < N / 2; ++i) most = fmaxf(most, magnitude(qr[i]));
-        } else {
-#pragma unroll 4
-          for (int i = 0; i < N / 2; ++i) most = fmaxf(most, magnitude(query(c, i)));
-        }
+        for (int i = 0; i < N / 2; ++i) most = fmaxf(most, magnitude(qr[i]));
         q_exp = q_exponent(warp_max(most));
       }
       c.q_scale = pow2(q_exp) * p.scale_log2;
@@ -644,22 +638,16 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       if (c.end || !c.first) return;
       if (!(ok = mbar_wait_warp(&bar_qempty, (q_loads & 1) ^ 1, &abort_flag))) return;
       const float inv = pow2(-q_exp);
-      auto put = [&](int i, const uint4& v) {
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
         const int n = 2 * i + (lane >> 4);
-        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+        const uint32_t u[4] = {qr[i].x, qr[i].y, qr[i].z, qr[i].w};
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) split_e4m3x2(bf16_lo(u[k]) * inv, bf16_hi(u[k]) * inv, hi[k], lo[k]);
         const uint32_t at = n * 128 + ((((lane & 15) >> 1) ^ (n & 7)) << 4) + (lane & 1) * 8;
         *reinterpret_cast<uint2*>(sQ + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
         *reinterpret_cast<uint2*>(sQ + N * 128 + at) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-      };
-      if constexpr (kKeep) {
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) put(i, qr[i]);
-      } else {
-#pragma unroll 4
-        for (int i = 0; i < N / 2; ++i) put(i, query(c, i));
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -1763,7 +1751,7 @@ Kv8AttnPlan plan_attention_kv8(int B, int L, int Hq, int Hkv, int max_pages, int
   const bool many = pl.n_rows >= 128;
   const long long lists = static_cast<long long>(B) * Hkv * pl.row_groups;
   const long long tiles = lists * ((max_pages + kTilePages - 1) / kTilePages);
-  const long long ctas = many ? num_sms : 2ll * num_sms;
+  const long long ctas = pl.n_rows == 16 ? 2ll * num_sms : num_sms;
   pl.grid = static_cast<int>(tiles < ctas ? tiles : ctas < kMaxCtas ? ctas : kMaxCtas);
   // (a tile a list at most: no list is cut)
   pl.parts = max_pages <= kTilePages ? 0 : 2 * pl.grid;
@@ -1839,7 +1827,7 @@ cudaError_t launch_attention_kv8(const Kv8AttnParams& a, const Kv8AttnPlan& pl, 
     if (e != cudaSuccess) return e;
     e = pl.n_rows == 128 ? launch_many<1>(tq, tk, tv, p, pl.grid, stream) : launch_many<2>(tq, tk, tv, p, pl.grid, stream);
   } else {
-    e = pl.n_rows == 32  ? launch_few<32, 32, 5>(tk, tv, p, pl.grid, stream)
+    e = pl.n_rows == 32  ? launch_few<32, 32, 12>(tk, tv, p, pl.grid, stream)
         : pl.rows <= 8 ? launch_few<16, 8, 6>(tk, tv, p, pl.grid, stream)
                        : launch_few<16, 16, 6>(tk, tv, p, pl.grid, stream);
   }
