@@ -271,3 +271,53 @@ def test_pages_past_two_gigabytes(lib):
     R.check_attention(f(out), R.attention_kv8(q, wk, wv, ws, small, np.full(2, n - L), Hkv))
     got = host(k[torch.from_numpy(table.reshape(-1).astype(np.int64)).cuda()])
     assert R.same_codes(got, wk)
+
+
+@pytest.mark.parametrize("L,Hq,Hkv,B", [(1, 4, 1, 300), (2, 16, 1, 260), (12, 4, 1, 257), (64, 3, 1, 258)])
+def test_attention_of_many_sequences(lib, L, Hq, Hkv, B):
+    """More sequences than a warp keeps the tiles of."""
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, 200, B)
+    lens[rng.integers(0, B, 5)] = 400
+    c = Cache(rng, lens + L, Hkv)
+    q = W._normal_bf16(rng, (B, L, Hq, 128), 1.0)
+    out = attend(lib, c, q, L, Hq, Hkv)
+    R.check_attention(f(out), R.attention_kv8(q, c.k, c.v, c.scales, c.table, c.lens - L, Hkv))
+    assert lib.bdlm_device_error() == 0
+
+
+@pytest.mark.parametrize("L,Hq,Hkv,lens", [(1, 2, 1, [50000]), (16, 2, 1, [30001, 5]), (64, 2, 1, [20000]), (64, 4, 1, [20010]),
+                                           (3, 8, 2, [9000, 20000]), (1, 1, 1, [40000, 1, 700])])
+def test_attention_of_lists_in_many_parts(lib, L, Hq, Hkv, lens):
+    """Long lists that all CTAs share."""
+    rng = np.random.default_rng(L)
+    c = Cache(rng, np.array(lens) + L, Hkv)
+    q = W._normal_bf16(rng, (len(lens), L, Hq, 128), 1.0)
+    out = attend(lib, c, q, L, Hq, Hkv)
+    R.check_attention(f(out), R.attention_kv8(q, c.k, c.v, c.scales, c.table, c.lens - L, Hkv))
+    assert lib.bdlm_device_error() == 0
+
+
+@pytest.mark.parametrize("L,Hq,Hkv", [(1, 8, 8), (4, 32, 8), (4, 64, 8), (8, 128, 16)])
+def test_attention_repeats_bit_for_bit_beside_other_work(lib, L, Hq, Hkv):
+    """Lists that borders cut are joined in their order, whoever comes last: no run differs from another."""
+    import torch
+    rng = np.random.default_rng(12)
+    B = 40
+    c = Cache(rng, rng.integers(1, 1500, B) + L, Hkv)
+    q = W._normal_bf16(rng, (B, L, Hq, 128), 1.0)
+    first = attend(lib, c, q, L, Hq, Hkv)
+    R.check_attention(f(first), R.attention_kv8(q, c.k, c.v, c.scales, c.table, c.lens - L, Hkv))
+    d = lib.attn_desc(B, L, Hq, Hkv, 128, c.cols, c.pages)
+    (k, v, s, t), qd, n = c.dev(), bf16_tensor(q), dev(c.lens - L)
+    outs = [torch.zeros_like(first) for _ in range(20)]
+    busy = torch.randn(2048, 2048, device="cuda")
+    other = torch.cuda.Stream()
+    with torch.cuda.stream(other):
+        for _ in range(50):
+            busy @ busy
+    for o in outs:
+        lib.bdlm_attention_kv8(d, qd, k, v, s, t, n, o)
+    torch.cuda.synchronize()
+    for o in outs:
+        assert torch.equal(o.view(torch.int16), first.view(torch.int16))

@@ -69,6 +69,8 @@ def test_attention_descriptors(so):
                 dict(page_size=32), dict(sm_scale=float("inf")), dict(sm_scale=float("nan")), dict(B=2 ** 30, L=64), dict(cols=0)):
         assert attend(so, desc(**bad)) == -1, bad
     assert attend(so, desc(B=0)) == 0
+    assert attend(so, desc(B=0, num=2 ** 27)) == -3 and attend(so, desc(B=0, num=2 ** 27 - 1)) == 0      # 2^30 pages of a head
+    assert attend(so, desc(B=1, cols=2 ** 26 + 1)) == -3
 
 
 def test_write_sizes(so):
