@@ -78,10 +78,16 @@ __device__ __forceinline__ int kv_tokens(const Params& p, int b, bool* ok) {
   return static_cast<int>(n < max_tok ? n : max_tok);
 }
 
+// a / b of numbers of tiles, which 32 bits mostly hold (a division of 64 takes some 150 cycles).
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return static_cast<unsigned>(a) / static_cast<unsigned>(b);
+  return a / b;
+}
+
 // Tiles of a unit, a CTA's even share of all.  (Shares of a quarter, taken in turn, were no faster: what they gain
 // in evenness goes into four times the parts.)
 __device__ __forceinline__ long long unit_tiles(long long total, int ctas) {
-  const long long share = (total + ctas - 1) / ctas;
+  const long long share = quotient(total + ctas - 1, ctas);
   return share < 1 ? 1 : share;
 }
 
@@ -207,7 +213,7 @@ struct Walk {
       return;
     }
     int n;
-    b = before.find(p, lane, static_cast<int>(pos / lists), n);   // before[b] <= pos / lists < before[b + 1]
+    b = before.find(p, lane, static_cast<int>(quotient(pos, lists)), n);   // before[b] <= pos / lists < before[b + 1]
     base = static_cast<long long>(n) * lists;
     sequence(p);
   }
@@ -229,7 +235,7 @@ struct Walk {
         ++b;
         sequence(p);
       }
-      const int list = static_cast<int>(r / tiles);
+      const int list = static_cast<int>(quotient(r, tiles));
       rg = list % p.row_groups;
       kvh = list / p.row_groups;
       tile = static_cast<int>(r - static_cast<long long>(list) * tiles);
@@ -237,8 +243,8 @@ struct Walk {
       slot = -1;
       if (n < tiles) {
         const long long c0 = pos - tile;   // the list's first tile
-        u0 = tile == 0 ? static_cast<int>(blockIdx.x) : static_cast<int>(c0 / per);
-        parts = static_cast<int>((c0 + tiles - 1) / per) - u0 + 1;
+        u0 = tile == 0 ? static_cast<int>(blockIdx.x) : static_cast<int>(quotient(c0, per));
+        parts = static_cast<int>(quotient(c0 + tiles - 1, per)) - u0 + 1;
         slot = 2 * static_cast<int>(blockIdx.x) + (tile == 0 ? 1 : 0);
       }
       seg_end = tile + n;
@@ -452,6 +458,40 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       *reinterpret_cast<uint4*>(sP + o) = make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
   }
+  // The walk begins beside the set-up.  Its first two chunks are asked for together: once the copies of the first are
+  // under way a look-up takes microseconds, and the copies would stand still for the second's.  From then on the walk is
+  // chunks ahead.
+  Walk<kChunk> walk;
+  Chunk c, d;
+  PageLoads<F::kChunkPages> pages, ahead;
+  uint4 qr[N / 2];    // rows 2i and 2i + 1 of the queries, eight values a lane
+  auto ask_q = [&](const Chunk& c) {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const int n = 2 * i + (lane >> 4);
+      const int pos = c.rg * p.lsub + n / p.G;
+      qr[i] = make_uint4(0, 0, 0, 0);
+      if (n < p.rows && pos < p.L)
+        qr[i] = __ldg(reinterpret_cast<const uint4*>(
+            p.q + ((static_cast<size_t>(c.b) * p.L + pos) * p.Hq + c.kvh * p.G + n % p.G) * 128) + (lane & 15));
+    }
+  };
+  if (warp == 2 + F::kSoft / 32) {
+    griddep_wait();
+    walk.init(p, lane);
+    c.final = 1;
+    c.end = !walk.next(p, lane, c);
+    if (!c.end) {
+      ask_q(c);
+      pages.ask_pages(p, c, lane);
+      if (!c.final) {
+        walk.next(p, lane, d);
+        ahead.ask_pages(p, d, lane);
+      }
+      pages.ask_scales(p, c, lane);
+      if (!c.final) ahead.ask_scales(p, d, lane);
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -602,21 +642,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
   } else if (warp == 2 + F::kSoft / 32) {
     // =================================================================== the walk, queries
     bool ok = true;
-    Walk<kChunk> walk;
-    walk.init(p, lane);
-    uint4 qr[N / 2];    // rows 2i and 2i + 1 of the queries, eight values a lane
     int q_exp = 0, q_loads = 0, seq = 0;
-    auto ask_q = [&](const Chunk& c) {
-#pragma unroll
-      for (int i = 0; i < N / 2; ++i) {
-        const int n = 2 * i + (lane >> 4);
-        const int pos = c.rg * p.lsub + n / p.G;
-        qr[i] = make_uint4(0, 0, 0, 0);
-        if (n < p.rows && pos < p.L)
-          qr[i] = __ldg(reinterpret_cast<const uint4*>(
-              p.q + ((static_cast<size_t>(c.b) * p.L + pos) * p.Hq + c.kvh * p.G + n % p.G) * 128) + (lane & 15));
-      }
-    };
     // Publishes chunk number seq, and then the parts of its queries, once the MMAs on the last ones are done.
     auto publish = [&](Chunk& c, const PageLoads<F::kChunkPages>& pages) {
       if (c.first && !c.end) {
@@ -654,22 +680,6 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       if (lane == 0) mbar_arrive(&bar_qfull);
       ++q_loads;
     };
-    // The first two chunks are asked for together: once the copies of the first are under way a look-up takes
-    // microseconds, and the copies would stand still for the second's.  From then on the walk is chunks ahead.
-    Chunk c, d;
-    PageLoads<F::kChunkPages> pages, ahead;
-    c.final = 1;
-    c.end = !walk.next(p, lane, c);
-    if (!c.end) {
-      ask_q(c);
-      pages.ask_pages(p, c, lane);
-      if (!c.final) {
-        walk.next(p, lane, d);
-        ahead.ask_pages(p, d, lane);
-      }
-      pages.ask_scales(p, c, lane);
-      if (!c.final) ahead.ask_scales(p, d, lane);
-    }
     publish(c, pages);
     if (!c.final && ok) {
       if (d.first) ask_q(d);
@@ -1622,8 +1632,8 @@ struct JoinList {
     const int tiles = (kv_tokens(p, b, &ok) + kTile - 1) / kTile;
     const long long per = unit_tiles(static_cast<long long>(sum) * lists, ctas);
     const long long c0 = static_cast<long long>(before) * lists + static_cast<long long>(list) * tiles;
-    u0 = static_cast<int>(c0 / per);
-    parts = static_cast<int>((c0 + tiles - 1) / per) - u0 + 1;
+    u0 = static_cast<int>(quotient(c0, per));
+    parts = static_cast<int>(quotient(c0 + tiles - 1, per)) - u0 + 1;
     return parts > 1;
   }
   // part s: the first in its unit's second slot, the others in their units' first
@@ -1637,11 +1647,14 @@ struct JoinList {
 
 // Many lists of few parts: CTA (list, eight rows), a warp a row, four head dims a lane.
 __global__ void __launch_bounds__(256) join_few_kernel(const Params p, int n_rows, int ctas) {
+  const int lane = threadIdx.x & 31, n = blockIdx.y * 8 + (threadIdx.x >> 5);
+  // The lengths can be read before the attention kernel is done: its CTAs let this one start after they waited for what
+  // wrote them.
+  JoinList j;
+  const bool cut = j.find(p, blockIdx.x, ctas, lane);
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31, n = blockIdx.y * 8 + (threadIdx.x >> 5);
-  JoinList j;
-  if (!j.find(p, blockIdx.x, ctas, lane) || n >= p.rows || j.rg * p.lsub + n / p.G >= p.L) return;
+  if (!cut || n >= p.rows || j.rg * p.lsub + n / p.G >= p.L) return;
   float M = -CUDART_INF_F, den = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int at = 0; at < j.parts; at += 32) {
@@ -1681,11 +1694,12 @@ constexpr int kJoinThreads = 512;
 constexpr int kMaxCtas = 1024;   // parts of a list are at most the grid
 __global__ void __launch_bounds__(kJoinThreads) join_many_kernel(const Params p, int n_rows, int ctas) {
   __shared__ float s_w[kMaxCtas], s_red[kJoinThreads / 32], s_acc[4][128];
-  griddep_wait();
-  griddep_launch_dependents();
   const int t = threadIdx.x, lane = t & 31, n = blockIdx.y;
   JoinList j;
-  if (!j.find(p, blockIdx.x, ctas, lane) || j.rg * p.lsub + n / p.G >= p.L) return;
+  const bool cut = j.find(p, blockIdx.x, ctas, lane);   // (before the wait, as above)
+  griddep_wait();
+  griddep_launch_dependents();
+  if (!cut || j.rg * p.lsub + n / p.G >= p.L) return;
   float m[kMaxCtas / kJoinThreads], l[kMaxCtas / kJoinThreads], M = -CUDART_INF_F;
 #pragma unroll
   for (int i = 0; i < kMaxCtas / kJoinThreads; ++i) {
