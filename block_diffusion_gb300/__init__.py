@@ -200,10 +200,13 @@ def _stream(stream) -> int | None:
 
 
 _types = {}   # by the `kinds` of a call: what element types each of its tensors may have
+_on = _is_dense = _address = None   # a tensor's get_device, is_contiguous and data_ptr, looked up once
 
 
 def _element_types(kinds: str) -> tuple:
+    global _on, _is_dense, _address
     import torch
+    _on, _is_dense, _address = torch.Tensor.get_device, torch.Tensor.is_contiguous, torch.Tensor.data_ptr
     each = {"b": (torch.bfloat16, torch.int16, torch.uint16), "i": (torch.int32, torch.uint32),
             "f": (torch.float32,), "w": (torch.int64, torch.uint64),
             "e": (torch.float8_e4m3fn, torch.uint8)}
@@ -216,13 +219,13 @@ def _rows(fn: str, t):
     dimensions (an address and None pass)."""
     if t is None or t.__class__ is int:
         return t
-    if t.dtype not in (_types.get("b") or _element_types("b"))[0] or t.get_device() != _current_device():
+    if t.dtype not in (_types.get("b") or _element_types("b"))[0] or _on(t) != _current_device():
         raise BdlmError(fn, BDLM_ERR_INVALID)
-    if not t.is_contiguous():
+    if not _is_dense(t):
         stride, shape = t.stride(), t.shape
         if len(shape) < 2 or stride[-1] != 1 or (stride[-2] != shape[-1] and shape[-2] != 1):
             raise BdlmError(fn, BDLM_ERR_INVALID)
-    return t.data_ptr()
+    return _address(t)
 
 
 def _dense(fn: str, kinds: str, stream, *tensors) -> list:
@@ -231,11 +234,13 @@ def _dense(fn: str, kinds: str, stream, *tensors) -> list:
     (b: bf16 or its 16 bits, i: int32, f: float32, w: 64-bit words, e: e4m3 or its 8 bits), not contiguous,
     or not on the current device.  Shapes are the caller's, as in C."""
     dev = _current_device()
+    out = []
     for types, t in zip(_types.get(kinds) or _element_types(kinds), tensors):
-        if t is not None and t.__class__ is not int and (
-                t.dtype not in types or t.get_device() != dev or not t.is_contiguous()):
-            raise BdlmError(fn, BDLM_ERR_INVALID)
-    out = [t if t is None or t.__class__ is int else t.data_ptr() for t in tensors]
+        if t is not None and t.__class__ is not int:
+            if t.dtype not in types or _on(t) != dev or not _is_dense(t):
+                raise BdlmError(fn, BDLM_ERR_INVALID)
+            t = _address(t)
+        out.append(t)
     out.append(_raw_stream(dev) if stream is None else _stream(stream))
     return out
 
@@ -418,7 +423,7 @@ def bdlm_build_tables(desc: AttnDesc, old_lens, new_lens, free_pages, n_free: in
     old, new, free, ff, t, lo, fi, pos, sl, fn, s = _dense(
         "bdlm_build_tables", "iiiiiiiiii", stream, old_lens, new_lens, free_pages, free_from,
         page_table, lens_out, first, positions, slots, free_next)
-    rc = load_library().bdlm_build_tables(ctypes.byref(desc), old, new, free, int(n_free), ff, t, lo,
+    rc = load_library().bdlm_build_tables(desc, old, new, free, int(n_free), ff, t, lo,
                                           fi, int(max_tokens), pos, sl, fn, s)
     _check("bdlm_build_tables", rc)
 
@@ -440,7 +445,7 @@ def bdlm_rotary(desc: AttnDesc, rotary: RotaryDesc, n_tokens: int, q, q_stride: 
     start or positions may be None, and q with q_out or k with k_out."""
     qp, kp = _rows("bdlm_rotary", q), _rows("bdlm_rotary", k)
     st, pos, qo, ko, s = _dense("bdlm_rotary", "iibb", stream, start, positions, q_out, k_out)
-    rc = load_library().bdlm_rotary(ctypes.byref(desc), ctypes.byref(rotary), int(n_tokens), qp,
+    rc = load_library().bdlm_rotary(desc, rotary, int(n_tokens), qp,
                                     int(q_stride), kp, int(k_stride), st, pos, int(bool(inverse)), qo, ko, s)
     _check("bdlm_rotary", rc)
 
@@ -450,7 +455,7 @@ def bdlm_write_kv8(desc: AttnDesc, n_tokens: int, first, n_rows: int, k_new, v_n
     """first may be None (n_rows is not used then)."""
     f, *ptrs, s = _dense("bdlm_write_kv8", "ibbeefii", stream, first, k_new, v_new, k_pages, v_pages,
                          scales, page_table, prefix_lens)
-    rc = load_library().bdlm_write_kv8(ctypes.byref(desc), int(n_tokens), f, int(n_rows), *ptrs, s)
+    rc = load_library().bdlm_write_kv8(desc, int(n_tokens), f, int(n_rows), *ptrs, s)
     _check("bdlm_write_kv8", rc)
 
 
@@ -458,7 +463,7 @@ def bdlm_attention_kv8(desc: AttnDesc, q, k_pages, v_pages, scales, page_table, 
                        stream=None) -> None:
     ptrs = _dense("bdlm_attention_kv8", "beefiib", stream, q, k_pages, v_pages, scales, page_table,
                   prefix_lens, out)
-    rc = load_library().bdlm_attention_kv8(ctypes.byref(desc), *ptrs)
+    rc = load_library().bdlm_attention_kv8(desc, *ptrs)
     _check("bdlm_attention_kv8", rc)
 
 

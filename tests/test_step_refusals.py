@@ -136,9 +136,57 @@ def test_codes_of_the_plain_form():
     assert R.exponent(448.0) == 0 and R.exponent(448.0001) == 1 and R.exponent(0.0) == -40 and R.exponent(1e30) == 40
 
 
-def test_bindings_refuse_other_types():
+def binding_calls(bd):
+    """Each operator's call of B = 0 sequences (nothing is launched), and its tensors' types by name."""
+    d, r = bd.attn_desc(0, 4, 8, 8, 128, 2, 8), bd.bdlm_rotary_init(64, False, 10000.0)
+    b, i, f, e = "bfloat16", "int32", "float32", "float8_e4m3fn"
+    return [
+        (dict(old_lens=i, new_lens=i, free_pages=i, free_from=i, page_table=i, lens_out=i, first=i, positions=i, slots=i, free_next=i),
+         lambda t: bd.bdlm_build_tables(d, **t, n_free=4, max_tokens=8, stream=0)),
+        (dict(q=b, k=b, start=i, positions=i, q_out=b, k_out=b),
+         lambda t: bd.bdlm_rotary(d, r, 4, **t, q_stride=0, k_stride=0, inverse=False, stream=0)),
+        (dict(first=i, k_new=b, v_new=b, k_pages=e, v_pages=e, scales=f, page_table=i, prefix_lens=i),
+         lambda t: bd.bdlm_write_kv8(d, 4, **t, n_rows=8, stream=0)),
+        (dict(q=b, k_pages=e, v_pages=e, scales=f, page_table=i, prefix_lens=i, out=b),
+         lambda t: bd.bdlm_attention_kv8(d, **t, stream=0)),
+    ]
+
+
+def test_bindings_refuse_other_element_types(so, monkeypatch):
     import torch
+
     import block_diffusion_gb300 as bd
-    assert {"bdlm_build_tables", "bdlm_rotary_init", "bdlm_rotary", "bdlm_write_kv8", "bdlm_attention_kv8"} <= set(bd.EXPORTS)
-    if not torch.cuda.is_available():
-        pytest.skip("element types are looked at beside the current device")
+    monkeypatch.setattr(bd, "_device", lambda: -1)         # the CPU's tensors stand for the device's
+    monkeypatch.setattr(bd, "_raw_stream", lambda dev: 0)
+    every = [torch.bfloat16, torch.float16, torch.float32, torch.float64, torch.int8, torch.int32, torch.int64, torch.float8_e4m3fn,
+             torch.float8_e5m2]
+    for types, call in binding_calls(bd):
+        good = {n: torch.zeros((8, 8), dtype=getattr(torch, t)) for n, t in types.items()}
+        call(good)
+        for name, t in types.items():
+            for other in every:
+                if other != getattr(torch, t):
+                    with pytest.raises(bd.BdlmError) as err:
+                        call(dict(good, **{name: torch.zeros((8, 8), dtype=other)}))
+                    assert err.value.status == bd.BDLM_ERR_INVALID, (name, other)
+            # the same bits under another name pass
+            if t in ("bfloat16", "float8_e4m3fn"):
+                call(dict(good, **{name: good[name].view(torch.int16 if t == "bfloat16" else torch.uint8)}))
+            # parts of a wider tensor do not
+            wide = torch.zeros((8, 16), dtype=getattr(torch, t))
+            for bad in (wide[:, ::2], wide[:, :8]):
+                with pytest.raises(bd.BdlmError):
+                    call(dict(good, **{name: bad}))
+    types, call = binding_calls(bd)[1]
+    good = {n: torch.zeros((8, 8), dtype=getattr(torch, t)) for n, t in types.items()}
+    rows = torch.zeros((4, 6, 128), dtype=torch.bfloat16)
+    call(dict(good, q=rows[:, :3], k=rows[:, 3:5]))
+    call(dict(good, q=rows[:, :1]))
+    for bad in (rows[:, ::2], rows[..., :64], rows[..., ::2], rows.transpose(1, 2), rows[0, 0, ::2]):
+        with pytest.raises(bd.BdlmError):
+            call(dict(good, q=bad))
+
+
+def test_empty_calls_succeed_without_a_device(so):
+    for call in (tables, rotary, write, attend):
+        assert call(so, desc(B=0)) == 0
