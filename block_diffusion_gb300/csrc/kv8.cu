@@ -160,7 +160,7 @@ write_kv8_kernel(const WriteKv8Params p, int max_touched) {
 }  // namespace
 
 cudaError_t launch_write_kv8(const WriteKv8Params& p, cudaStream_t stream) {
-  const int touched = (p.n + 2 * kPage - 2) / kPage;   // pages that n tokens lie in at most
+  const int touched = static_cast<int>((p.n + 2ll * kPage - 2) / kPage);   // pages that n tokens lie in at most
   const dim3 grid(static_cast<unsigned>(p.B) * touched, (2 * p.Hkv + kWriteWarps - 1) / kWriteWarps);
   return launch_pdl(write_kv8_kernel, grid, dim3(kWriteWarps * 32), 0, stream, p, touched);
 }

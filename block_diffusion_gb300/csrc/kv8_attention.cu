@@ -334,7 +334,7 @@ struct Few {
   static constexpr int kSoft = 128 * kSets;     // their threads
   static constexpr int kThreads = 96 + kSoft;
   // Two CTAs per SM with 16 rows.  With 32 one, twice as wide: two left chunks of three tiles, whose ends took as long as
-  // they (128 blocks of 8 over 512-4096 tokens: KFIG).
+  // they (128 blocks of 8 over 512-4096 tokens: 186 us against 170).
   static constexpr int kCtas = N == 16 ? 2 : 1;
   static constexpr int kTmemCols = 512 / kCtas;
   static constexpr int kChunk = (kTmemCols - N) / (2 * N);

@@ -321,3 +321,18 @@ def test_attention_repeats_bit_for_bit_beside_other_work(lib, L, Hq, Hkv):
     torch.cuda.synchronize()
     for o in outs:
         assert torch.equal(o.view(torch.int16), first.view(torch.int16))
+
+
+def test_write_of_a_far_larger_maximum(lib):
+    """n_tokens is only the most that a packed sequence may have: the largest there is does no harm."""
+    import torch
+    rng = np.random.default_rng(13)
+    c = Cache(rng, [40], 2)
+    new = W._normal_bf16(rng, (21, 2, 128), 1.0)
+    first = np.array([3, 20], np.int32)
+    want = R.write_kv8(21, first, new, new, c.k, c.v, c.scales, c.table, np.array([5], np.int32))
+    k, v, s, t = c.dev()
+    d = lib.attn_desc(1, 1, 2, 2, 128, c.cols, c.pages)
+    lib.bdlm_write_kv8(d, 2 ** 24 - 1, dev(first), 21, bf16_tensor(new), bf16_tensor(new), k, v, s, t, dev(np.array([5], np.int32)))
+    assert np.array_equal(host(s), want[2]) and R.same_codes(host(k), want[0]) and R.same_codes(host(v), want[1])
+    assert lib.bdlm_device_error() == 0

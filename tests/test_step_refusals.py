@@ -108,7 +108,7 @@ def test_rotary_init(so):
     nan, inf = float("nan"), float("inf")
     for bad in (dict(rot_dim=0), dict(rot_dim=8), dict(rot_dim=130), dict(rot_dim=144), dict(base=1.0), dict(base=nan), dict(base=inf),
                 dict(scaling=-1), dict(scaling=5), dict(factor=0.5), dict(factor=nan), dict(factor=inf), dict(original_len=0.0),
-                dict(few=0.0), dict(many=1.0), dict(many=nan), dict(amplitude=-1.0), dict(amplitude=inf), dict(amplitude=nan)):
+                dict(few=0.0), dict(many=1.0), dict(many=nan), dict(amplitude=-1.0), dict(amplitude=inf), dict(amplitude=nan), dict(amplitude=1e39)):
         with pytest.raises(bd.BdlmError):
             bd.bdlm_rotary_init(**{**good, **bad})
     assert so.bdlm_rotary_init(None, 64, 0, 10000.0, 0, 1.0, 1.0, 1.0, 2.0, 0.0) == -1
