@@ -28,6 +28,7 @@
 #include "attention_common.cuh"
 #include "kernels.h"
 #include "ptx.cuh"
+#include "ptx_kv8.cuh"
 #include "step_ops.h"
 
 namespace bdlm {
