@@ -58,6 +58,16 @@ __device__ __forceinline__ void tmem_regs_ready(uint32_t (&r)[4]) {
   asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]));
 }
 
+__device__ __forceinline__ void tmem_st1(uint32_t taddr, uint32_t r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(taddr), "r"(r) : "memory");
+}
+
+// A matrix descriptor (smem_desc) without swizzling: blocks of 8 x 16 bytes in one piece each.  MN-major operands use
+// LBO = distance between the 8-row K groups and SBO = distance between blocks of 16 bytes along MN.
+__device__ __forceinline__ uint64_t smem_desc_plain(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return smem_desc(saddr, lbo, sbo) & ~(static_cast<uint64_t>(7) << 61);
+}
+
 // Instruction descriptors as idesc_bf16_f32, with f16 A and B (format 0) ...
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool a_mn_major,
                                                      bool b_mn_major) {
