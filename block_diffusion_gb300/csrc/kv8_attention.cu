@@ -1075,12 +1075,13 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  griddep_wait();
   const uint32_t tmem = tmem_base;
   const uint32_t tO = tmem + 256;   // S: two buffers, or one of each group
 
   if (warp == 0) {
     // =================================================================== producer
+    // All but the queries' parts and their scale can be read before the kernel that makes them is done: its CTAs let this
+    // one start after they waited for what wrote the rest.  All else here waits for the first chunk.
     if (lane == 0) {
       tma_prefetch_desc(&tm_q);
       tma_prefetch_desc(&tm_k);
@@ -1092,14 +1093,19 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     bool ok = true;
     Walk<kChunk> walk;
     walk.init(p, lane);
-    auto prepare = [&](Chunk& c) -> bool {
+    PageLoads<kChunkPages> pages;
+    auto look_up = [&](Chunk& c) -> bool {
       const bool have = walk.next(p, lane, c);
-      ++seq;
-      const int rs = seq % kRing;
-      PageLoads<kChunkPages> pages;
       if (have) {
         pages.ask_pages(p, c, lane);
         pages.ask_scales(p, c, lane);
+      }
+      return have;
+    };
+    auto publish = [&](Chunk& c, bool have) {
+      ++seq;
+      const int rs = seq % kRing;
+      if (have) {
         c.q_scale = __ldg(p.q_scale + (static_cast<size_t>(c.b) * p.Hkv + c.kvh) * p.row_groups + c.rg) * p.scale_log2;
       } else {
         c.end = 1;
@@ -1111,6 +1117,10 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         s_chunk[rs] = c;
         mbar_arrive(&bar_cfull[rs]);
       }
+    };
+    auto prepare = [&](Chunk& c) -> bool {
+      const bool have = look_up(c);
+      publish(c, have);
       return have;
     };
     auto load_q = [&](const Chunk& c) {
@@ -1139,11 +1149,13 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       }
     };
     Chunk cur, nxt;
-    bool have = prepare(cur), have_next = false;
+    bool have = look_up(cur), have_next = false;
     int cs = 0;
+    if (have) copy(&tm_k, sK, bar_kfull, bar_kempty, KS, kst, kph, pages.unit[0]);   // (lane l: page l)
+    griddep_wait();
+    publish(cur, have);
     if (have) {
       load_q(cur);
-      copy(&tm_k, sK, bar_kfull, bar_kempty, KS, kst, kph, s_page[0][lane & 7]);
       have_next = prepare(nxt);
     }
     while (have && ok) {
@@ -1532,9 +1544,11 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 }
 
 // The queries of each (sequence, KV head, row group) as two e4m3 parts of 128 bytes side by side, with the power of
-// two that they share.  A CTA a group.
-__global__ void __launch_bounds__(256) split_q_kernel(const Params p, uint8_t* __restrict__ q8, float* __restrict__ q_scale) {
-  __shared__ float s_most[8];
+// two that they share.  A CTA a group, its queries in registers between the two steps.
+constexpr int kSplitThreads = 512;
+__global__ void __launch_bounds__(kSplitThreads) split_q_kernel(const Params p, uint8_t* __restrict__ q8, float* __restrict__ q_scale) {
+  constexpr int kEach = 256 * 16 / kSplitThreads;   // pieces of eight values of a thread
+  __shared__ float s_most[kSplitThreads / 32];
   griddep_wait();
   griddep_launch_dependents();
   const int t = threadIdx.x, lane = t & 31;
@@ -1545,19 +1559,29 @@ __global__ void __launch_bounds__(256) split_q_kernel(const Params p, uint8_t* _
   auto at = [&](int n) {   // of row n, in rows of 128 values
     return (static_cast<size_t>(b) * p.L + l0 + n / p.G) * p.Hq + static_cast<size_t>(kvh) * p.G + n % p.G;
   };
+  uint4 v[kEach];
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int o = i * kSplitThreads + t;
+    v[i] = make_uint4(0, 0, 0, 0);
+    if (o < rows * 16) v[i] = __ldg(reinterpret_cast<const uint4*>(p.q + at(o >> 4) * 128) + (o & 15));
+  }
   float most = 0.f;
-  for (int o = t; o < rows * 16; o += 256) most = fmaxf(most, magnitude(__ldg(reinterpret_cast<const uint4*>(p.q + at(o >> 4) * 128) + (o & 15))));
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) most = fmaxf(most, magnitude(v[i]));
   most = warp_max(most);
   if (lane == 0) s_most[t >> 5] = most;
   __syncthreads();
-  for (int w = 0; w < 8; ++w) most = fmaxf(most, s_most[w]);
+  most = warp_max(s_most[lane % (kSplitThreads / 32)]);
   const int e = q_exponent(most);
   const float inv = pow2(-e);
   if (t == 0) q_scale[blockIdx.x] = pow2(e);
-  for (int o = t; o < rows * 16; o += 256) {
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int o = i * kSplitThreads + t;
+    if (o >= rows * 16) break;
     const size_t row = at(o >> 4);
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p.q + row * 128) + (o & 15));
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+    const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) split_e4m3x2(bf16_lo(u[k]) * inv, bf16_hi(u[k]) * inv, hi[k], lo[k]);
@@ -1643,48 +1667,75 @@ struct JoinList {
   }
 };
 
-// Many lists of few parts: CTA (list, eight rows), a warp a row, four head dims a lane.
+// Many lists of few parts: CTA (list, 8 R rows), R rows a warp, whose loads are under way together, four head dims a
+// lane.
+template <int R>
 __global__ void __launch_bounds__(256) join_few_kernel(const Params p, int n_rows, int ctas) {
-  const int lane = threadIdx.x & 31, n = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, n0 = (blockIdx.y * 8 + (threadIdx.x >> 5)) * R;
   // The lengths can be read before the attention kernel is done: its CTAs let this one start after they waited for what
   // wrote them.
   JoinList j;
   const bool cut = j.find(p, blockIdx.x, ctas, lane);
   griddep_wait();
   griddep_launch_dependents();
-  if (!cut || n >= p.rows || j.rg * p.lsub + n / p.G >= p.L) return;
-  float M = -CUDART_INF_F, den = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (!cut) return;
+  const int live = min(R, min(p.rows, (p.L - j.rg * p.lsub) * p.G) - n0);   // of the warp's rows
+  if (live <= 0) return;
+  float M[R], den[R];
+  float4 acc[R];
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    M[k] = -CUDART_INF_F;
+    den[k] = 0.f;
+    acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
   for (int at = 0; at < j.parts; at += 32) {
     const int s = at + lane;
-    float m = -CUDART_INF_F, l = 0.f;
-    if (s < j.parts) {
-      m = __ldcg(j.part(p, s, n_rows) + n_rows * 128 + n);
-      l = __ldcg(j.part(p, s, n_rows) + n_rows * 129 + n);
-    }
-    const float top = fmaxf(M, warp_max(m));
-    const float e = s < j.parts ? ex2(m - top) : 0.f, was = ex2(M - top);
-    float d = e * l;
+    float e[R], l[R];
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
-    den = den * was + d;
-    acc = make_float4(acc.x * was, acc.y * was, acc.z * was, acc.w * was);
-    M = top;
+    for (int k = 0; k < R; ++k) {
+      e[k] = -CUDART_INF_F;
+      l[k] = 0.f;
+      if (s < j.parts && k < live) {
+        e[k] = __ldcg(j.part(p, s, n_rows) + n_rows * 128 + n0 + k);
+        l[k] = __ldcg(j.part(p, s, n_rows) + n_rows * 129 + n0 + k);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      if (k >= live) break;
+      const float top = fmaxf(M[k], warp_max(e[k])), was = ex2(M[k] - top);
+      e[k] = s < j.parts ? ex2(e[k] - top) : 0.f;
+      float d = e[k] * l[k];
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
+      den[k] = den[k] * was + d;
+      acc[k] = make_float4(acc[k].x * was, acc[k].y * was, acc[k].z * was, acc[k].w * was);
+      M[k] = top;
+    }
     const int cnt = min(32, j.parts - at);
-#pragma unroll 4
+#pragma unroll(R == 1 ? 4 : 2)
     for (int i = 0; i < cnt; ++i) {
-      const float w = __shfl_sync(0xffffffffu, e, i);
-      const float4 o = __ldcg(reinterpret_cast<const float4*>(j.part(p, at + i, n_rows) + n * 128) + lane);
-      acc.x += w * o.x;
-      acc.y += w * o.y;
-      acc.z += w * o.z;
-      acc.w += w * o.w;
+      const float4* from = reinterpret_cast<const float4*>(j.part(p, at + i, n_rows) + n0 * 128) + lane;
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        const float w = __shfl_sync(0xffffffffu, e[k], i);
+        const float4 o = k < live ? __ldcg(from + k * 32) : make_float4(0.f, 0.f, 0.f, 0.f);
+        acc[k].x += w * o.x;
+        acc[k].y += w * o.y;
+        acc[k].z += w * o.z;
+        acc[k].w += w * o.w;
+      }
     }
   }
-  const float inv = 1.f / den;
-  const __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), hi = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-  reinterpret_cast<uint2*>(j.row(p, n))[lane] =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    if (k >= live) break;
+    const float inv = 1.f / den[k];
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[k].x * inv, acc[k].y * inv), hi = __floats2bfloat162_rn(acc[k].z * inv, acc[k].w * inv);
+    reinterpret_cast<uint2*>(j.row(p, n0 + k))[lane] =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  }
 }
 
 // Few lists of many parts: CTA (list, row), four groups of 128 threads, a head dim each, that take every fourth part.
@@ -1834,7 +1885,7 @@ cudaError_t launch_attention_kv8(const Kv8AttnParams& a, const Kv8AttnPlan& pl, 
     p.cum = cum;
   }
   if (pl.n_rows >= 128) {
-    e = launch_pdl(split_q_kernel, dim3(lists), dim3(256), 0, stream, p, reinterpret_cast<uint8_t*>(at + pl.q_offset),
+    e = launch_pdl(split_q_kernel, dim3(lists), dim3(kSplitThreads), 0, stream, p, reinterpret_cast<uint8_t*>(at + pl.q_offset),
                    reinterpret_cast<float*>(at + pl.q_scale_offset));
     if (e != cudaSuccess) return e;
     e = pl.n_rows == 128 ? launch_many<1>(tq, tk, tv, p, pl.grid, stream) : launch_many<2>(tq, tk, tv, p, pl.grid, stream);
@@ -1845,7 +1896,8 @@ cudaError_t launch_attention_kv8(const Kv8AttnParams& a, const Kv8AttnPlan& pl, 
   }
   if (e != cudaSuccess || pl.parts == 0 || pl.join_here) return e;
   if (pl.many_parts) return launch_pdl(join_many_kernel, dim3(lists, p.rows), dim3(kJoinThreads), 0, stream, p, pl.n_rows, pl.grid);
-  return launch_pdl(join_few_kernel, dim3(lists, (p.rows + 7) / 8), dim3(256), 0, stream, p, pl.n_rows, pl.grid);
+  if (pl.n_rows >= 128) return launch_pdl(join_few_kernel<4>, dim3(lists, (p.rows + 31) / 32), dim3(256), 0, stream, p, pl.n_rows, pl.grid);
+  return launch_pdl(join_few_kernel<1>, dim3(lists, (p.rows + 7) / 8), dim3(256), 0, stream, p, pl.n_rows, pl.grid);
 }
 
 }  // namespace bdlm
