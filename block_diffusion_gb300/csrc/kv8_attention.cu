@@ -37,6 +37,7 @@ namespace {
 constexpr int kTilePages = kTile / kPage;
 constexpr int kStage = kTile * 128;    // bytes of a tile's K or V
 constexpr int kRing = 4;               // chunk descriptors in flight
+constexpr int kAllTiles = 0x7FFFFFFF;  // a chunk as long as its list
 constexpr float kWeightExp = 7.0f;     // a query's largest weight is 2^7 ...
 constexpr float kLazy = 1.5f;          // ... to 2^8.5: a running maximum moves only when it rises by more (e4m3 ends at 448)
 constexpr float kLazyMany = 8.0f;      // the same where weights are float16: 1 to 2^8
@@ -68,7 +69,7 @@ struct Chunk {
   int u0, parts;     // the list's first unit and its parts (slot >= 0)
   int final;         // the CTA's last chunk
   int end;           // no chunk: the CTA has no work
-  float q_scale;     // q = (hi + lo) * q_scale, times c
+  float q_scale;     // q = (hi + lo) * q_scale, times c (many rows)
 };
 
 __device__ __forceinline__ int kv_tokens(const Params& p, int b, bool* ok) {
@@ -328,19 +329,23 @@ constexpr int kFewParts = 8;    // parts a list, about
 // S^T fit tensor memory is taken at once: the maxima over all of it, then its weights tile by tile.  S^T
 // is double-buffered and K of chunk u + 1 streams ahead of V of chunk u.
 
-// N: rows of the MMAs, NC: rows that the softmax computes (the others' weights stay zero).
-template <int N, int STAGES>
+// N: rows of the first MMAs, NC: rows that the softmax computes.
+template <int N, int NC, int STAGES>
 struct Few {
-  static constexpr int kSets = N / 16;          // of softmax warps: 16 rows each, of all tokens
+  static constexpr int CW = NC < 16 ? NC : 16;
+  static constexpr int kSets = NC / CW;         // of softmax warps: 16 rows each (8), of all tokens
   static constexpr int kSoft = 128 * kSets;     // their threads
-  static constexpr int kThreads = 96 + kSoft;
+  static constexpr int kThreads = 128 + kSoft;
+  static constexpr int kWalkWarp = 2 + kSoft / 32, kQueryWarp = kWalkWarp + 1;
   // Two CTAs per SM with 16 rows.  With 32 one, twice as wide: two left chunks of three tiles, whose ends took as long as
   // they (128 blocks of 8 over 512-4096 tokens: 186 us against 170).
   static constexpr int kCtas = N == 16 ? 2 : 1;
   static constexpr int kTmemCols = 512 / kCtas;
-  static constexpr int kChunk = (kTmemCols - N) / (2 * N);
+  static constexpr int kWeights = 2 * NC;       // rows of the second MMAs: both parts of the weights
+  static constexpr int kWeightBuf = kWeights * kTile;
+  static constexpr int kChunk = (kTmemCols - kWeights) / (2 * N);
   static constexpr int kChunkPages = kChunk * kTilePages;
-  static constexpr size_t kSmem = 1024 + N * 256 + static_cast<size_t>(STAGES) * kStage + 2 * N * 256;
+  static constexpr size_t kSmem = 1024 + N * 256 + static_cast<size_t>(STAGES) * kStage + 2 * kWeightBuf;
 };
 
 // w's float16 pair in two e4m3 parts: each the low byte for the low one.
@@ -405,15 +410,16 @@ __device__ __forceinline__ void join_parts(const Params& p, const Chunk& c, int 
 }
 
 template <int N, int NC, int STAGES>
-__global__ void __launch_bounds__(Few<N, STAGES>::kThreads, Few<N, STAGES>::kCtas)
+__global__ void __launch_bounds__(Few<N, NC, STAGES>::kThreads, Few<N, NC, STAGES>::kCtas)
 few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Params p) {
-  using F = Few<N, STAGES>;
+  using F = Few<N, NC, STAGES>;
+  constexpr int CW = F::CW;
   constexpr int kChunk = F::kChunk;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* sQ = base;                  // two parts x N rows x 128 bytes, 128-byte swizzle
   uint8_t* sKV = sQ + N * 256;
-  uint8_t* sP = sKV + STAGES * kStage;   // two buffers of two parts x N / 16 x 128 tokens x 16 bytes, a row each
+  uint8_t* sP = sKV + STAGES * kStage;   // two buffers of kWeights / 16 x 128 tokens x 16 bytes: a byte of each row
   __shared__ uint64_t bar_qfull, bar_qempty, bar_full[STAGES], bar_empty[STAGES];
   __shared__ uint64_t bar_sfull[2], bar_sfree[2], bar_pfull[2], bar_pempty[2];
   __shared__ uint64_t bar_ofull[2], bar_done;
@@ -425,6 +431,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
   __shared__ int abort_flag;
   __shared__ __align__(16) float s_m[N], s_alpha[N], s_l[N], s_red[4][N];
   __shared__ int s_need[F::kSets][2], s_join[F::kSets];
+  __shared__ float s_qscale[4];        // of a list's queries, times c: lists in turn (the softmax is two behind at most)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -454,15 +461,11 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     tmem_alloc(&tmem_base, F::kTmemCols);
     tmem_relinquish();
   }
-  if constexpr (NC < N) {
-    for (int o = threadIdx.x * 16; o < 2 * N * 256; o += F::kThreads * 16)
-      *reinterpret_cast<uint4*>(sP + o) = make_uint4(0, 0, 0, 0);
-    fence_proxy_async_smem();
-  }
   // The walk begins beside the set-up.  Its first two chunks are asked for together: once the copies of the first are
   // under way a look-up takes microseconds, and the copies would stand still for the second's.  From then on the walk is
-  // chunks ahead.
+  // chunks ahead.  The queries' warp walks from list to list.
   Walk<kChunk> walk;
+  Walk<kAllTiles> lists;
   Chunk c, d;
   PageLoads<F::kChunkPages> pages, ahead;
   uint4 qr[N / 2];    // rows 2i and 2i + 1 of the queries, eight values a lane
@@ -477,13 +480,12 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             p.q + ((static_cast<size_t>(c.b) * p.L + pos) * p.Hq + c.kvh * p.G + n % p.G) * 128) + (lane & 15));
     }
   };
-  if (warp == 2 + F::kSoft / 32) {
+  if (warp == F::kWalkWarp) {
     griddep_wait();
     walk.init(p, lane);
     c.final = 1;
     c.end = !walk.next(p, lane, c);
     if (!c.end) {
-      ask_q(c);
       pages.ask_pages(p, c, lane);
       if (!c.final) {
         walk.next(p, lane, d);
@@ -492,6 +494,11 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       pages.ask_scales(p, c, lane);
       if (!c.final) ahead.ask_scales(p, d, lane);
     }
+  } else if (warp == F::kQueryWarp) {
+    griddep_wait();
+    lists.init(p, lane);
+    c.end = !lists.next(p, lane, c);
+    if (!c.end) ask_q(c);
   }
   tc_fence_before();
   __syncthreads();
@@ -552,7 +559,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
   } else if (warp == 1) {
     // =================================================================== MMA issuer
     constexpr uint32_t kIdescS = idesc_e4m3_f32(128, N, false, false);
-    constexpr uint32_t kIdescO = idesc_e4m3_f32(128, N, true, true);
+    constexpr uint32_t kIdescO = idesc_e4m3_f32(128, F::kWeights, true, true);
     const uint64_t q_desc = smem_desc(smem_u32(sQ), 16, 1024), p_desc = smem_desc_plain(smem_u32(sP), 128, kTile * 16);
     const uint64_t k_desc = smem_desc(smem_u32(sKV), 16, 1024), v_desc = smem_desc(smem_u32(sKV), kStage, 1024);
     bool ok = true;
@@ -600,13 +607,14 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         const int pb = pcount & 1;
         if (!(ok = mbar_wait_warp(&bar_pfull[pb], (pcount >> 1) & 1, &abort_flag))) return;
         tc_fence_after();
-        const uint64_t vd = v_desc + static_cast<uint32_t>(st * (kStage >> 4)), pd = p_desc + static_cast<uint32_t>(pb * (N * 16));
+        const uint64_t vd = v_desc + static_cast<uint32_t>(st * (kStage >> 4)), pd = p_desc + static_cast<uint32_t>(pb * (F::kWeightBuf >> 4));
         const int steps = (valid + 31) / 32;
         if (elect_one()) {
-          for (int q = 0; q < steps; ++q) {
-            umma_e4m3(tO, vd + q * 256, pd + q * 32, kIdescO, first && j == 0 && q == 0 ? 0u : 1u);
-            umma_e4m3(tO, vd + q * 256, pd + N * 8 + q * 32, kIdescO, 1u);
-          }
+          // 32 tokens of both parts of w, each part into sums of its own: an MMA for either into the same sums, in a loop
+          // of `steps`, took 450 cycles a tile where this takes 170 to 190
+#pragma unroll
+          for (int q = 0; q < kTile / 32; ++q)
+            if (q < steps) umma_e4m3(tO, vd + q * 256, pd + q * 32, kIdescO, q == 0 && first && j == 0 ? 0u : 1u);
           umma_commit(&bar_pempty[pb]);
           umma_commit(&bar_empty[st]);
           if (j == n_tiles - 1) umma_commit(&bar_ofull[u & 1]);
@@ -640,19 +648,11 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     }
     if (elect_one()) umma_commit(&bar_done);
     __syncwarp();
-  } else if (warp == 2 + F::kSoft / 32) {
-    // =================================================================== the walk, queries
+  } else if (warp == F::kWalkWarp) {
+    // =================================================================== the walk
     bool ok = true;
-    int q_exp = 0, q_loads = 0, seq = 0;
-    // Publishes chunk number seq, and then the parts of its queries, once the MMAs on the last ones are done.
-    auto publish = [&](Chunk& c, const PageLoads<F::kChunkPages>& pages) {
-      if (c.first && !c.end) {
-        float most = 0.f;
-#pragma unroll
-        for (int i = 0; i < N / 2; ++i) most = fmaxf(most, magnitude(qr[i]));
-        q_exp = q_exponent(warp_max(most));
-      }
-      c.q_scale = pow2(q_exp) * p.scale_log2;
+    int seq = 0;
+    auto publish = [&](Chunk& c, const PageLoads<F::kChunkPages>& pages) {   // chunk number seq
       const int rs = seq % kRing;
       if (!(ok = mbar_wait_warp(&bar_cempty[rs], ((seq / kRing) & 1) ^ 1, &abort_flag))) return;
       if (!c.end) pages.give(s_page[rs], s_scale[rs], lane);
@@ -662,56 +662,72 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         mbar_arrive(&bar_cfull[rs]);
       }
       ++seq;
-      if (c.end || !c.first) return;
-      if (!(ok = mbar_wait_warp(&bar_qempty, (q_loads & 1) ^ 1, &abort_flag))) return;
-      const float inv = pow2(-q_exp);
+    };
+    publish(c, pages);
+    if (!c.final && ok) {
+      while (!d.final) {   // the next chunk's pages are asked for ahead of the wait for a place, its scales behind it
+        walk.next(p, lane, c);
+        pages.ask_pages(p, c, lane);
+        publish(d, ahead);
+        if (!ok) break;
+        pages.ask_scales(p, c, lane);
+        d = c;
+        ahead = pages;
+      }
+      if (ok) publish(d, ahead);
+    }
+  } else if (warp == F::kQueryWarp) {
+    // =================================================================== queries
+    // A list's queries in their two parts, kept in registers until the MMAs on the last list's are done.
+    bool ok = true;
+    for (int n_list = 0; !c.end; ++n_list) {
+      float most = 0.f;
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) most = fmaxf(most, magnitude(qr[i]));
+      const int e = q_exponent(warp_max(most));
+      const float inv = pow2(-e);
 #pragma unroll
       for (int i = 0; i < N / 2; ++i) {
-        const int n = 2 * i + (lane >> 4);
         const uint32_t u[4] = {qr[i].x, qr[i].y, qr[i].z, qr[i].w};
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) split_e4m3x2(bf16_lo(u[k]) * inv, bf16_hi(u[k]) * inv, hi[k], lo[k]);
-        const uint32_t at = n * 128 + ((((lane & 15) >> 1) ^ (n & 7)) << 4) + (lane & 1) * 8;
-        *reinterpret_cast<uint2*>(sQ + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-        *reinterpret_cast<uint2*>(sQ + N * 128 + at) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+        qr[i] = make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
       }
+      if (!(ok = mbar_wait_warp(&bar_qempty, (n_list & 1) ^ 1, &abort_flag))) break;
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) {
+        const int n = 2 * i + (lane >> 4);
+        const uint32_t at = n * 128 + ((((lane & 15) >> 1) ^ (n & 7)) << 4) + (lane & 1) * 8;
+        *reinterpret_cast<uint2*>(sQ + at) = make_uint2(qr[i].x, qr[i].y);
+        *reinterpret_cast<uint2*>(sQ + N * 128 + at) = make_uint2(qr[i].z, qr[i].w);
+      }
+      if (lane == 0) s_qscale[n_list & 3] = pow2(e) * p.scale_log2;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bar_qfull);
-      ++q_loads;
-    };
-    publish(c, pages);
-    if (!c.final && ok) {
-      if (d.first) ask_q(d);
-      publish(d, ahead);
-      while (!d.final && ok) {
-        walk.next(p, lane, d);
-        if (d.first) ask_q(d);
-        ahead.ask_pages(p, d, lane);
-        ahead.ask_scales(p, d, lane);
-        publish(d, ahead);
-      }
+      c.end = !lists.next(p, lane, c);
+      if (!c.end) ask_q(c);
     }
   } else {
     // =================================================================== softmax, epilogue
     // Set `set` of four warps computes rows c0 .. c0 + CW - 1 of every token; c0 and the sets' own barrier aside they
     // do the same.
-    constexpr int CW = NC < 16 ? NC : 16;
-    static_assert(CW * F::kSets == NC, "a set for every 16 rows");
+    static_assert(CW * F::kSets == NC && (CW == 8 || CW == 16), "whole sets");
     const int q4 = warp & 3, set = (warp - 2) >> 2, c0 = set * CW, own = 1 + set;
     const int x = (q4 << 5) | lane;   // tensor-memory lane: token of a tile, or head dim
     const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
     const uint32_t tOx = tO + lane_off + static_cast<uint32_t>(c0);
     float2 l[CW / 2];
     bool ok = true;
-    int pcount = 0;
+    int pcount = 0, n_list = -1;
     for (int u = 0; ok; ++u) {
       const int rs = u % kRing;
       if (!(ok = mbar_wait_warp(&bar_cfull[rs], (u / kRing) & 1, &abort_flag))) break;
       const Chunk c = s_chunk[rs];
       if (c.end) break;
       if (c.first) {
+        ++n_list;
 #pragma unroll
         for (int n = 0; n < CW / 2; ++n) l[n] = make_float2(0.f, 0.f);
         if (x < CW) s_m[c0 + x] = -CUDART_INF_F;
@@ -719,6 +735,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       const uint32_t tS = tmem + lane_off + static_cast<uint32_t>((u & 1) * kChunk * N + c0);
       if (!(ok = mbar_wait_warp(&bar_sfull[u & 1], (u >> 1) & 1, &abort_flag))) break;
       tc_fence_after();
+      const float q_scale = s_qscale[n_list & 3];
       // the exact maxima of x over the chunk (behind the last token scores may be anything: -inf)
       const int last_tile = (c.t_end - c.t0 - 1) / kTile;
       const bool cut = c.t_end - c.t0 - last_tile * kTile <= x;   // this thread's token of it is past the end
@@ -744,7 +761,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
           uint32_t r[CW];
           load(j, r);
           const float2 sc = s_scale[rs][j * kTilePages + (x >> 4)];
-          const float a = sc.x * c.q_scale;
+          const float a = sc.x * q_scale;
           ready(j, r);
 #pragma unroll
           for (int n = 0; n < CW; n += 2) {
@@ -783,13 +800,16 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         // these rows of O^T and l to the new maxima
         if (!(ok = mbar_wait_warp(&bar_ofull[(u - 1) & 1], ((u - 1) >> 1) & 1, &abort_flag))) break;
         tc_fence_after();
-        uint32_t r[16];
-        tmem_ld16(tOx, r);
-        tmem_wait_ld();
-        tmem_regs_ready(r);
+#pragma unroll 1
+        for (uint32_t col = 0; col < F::kWeights; col += NC < 16 ? 16 : N) {   // (eight rows: both parts at once)
+          uint32_t r[16];
+          tmem_ld16(tOx + col, r);
+          tmem_wait_ld();
+          tmem_regs_ready(r);
 #pragma unroll
-        for (int n = 0; n < CW; ++n) r[n] = __float_as_uint(__uint_as_float(r[n]) * s_alpha[c0 + n]);
-        tmem_st16(tOx, r);
+          for (int n = 0; n < 16; ++n) r[n] = __float_as_uint(__uint_as_float(r[n]) * s_alpha[c0 + n % CW]);
+          tmem_st16(tOx + col, r);
+        }
         tmem_wait_st();
         tc_fence_before();
 #pragma unroll
@@ -806,7 +826,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         load(0, r);
         for (int j = 0; j < c.n_tiles && ok; ++j) {
           const float2 sc = s_scale[rs][j * kTilePages + (x >> 4)];
-          const float a = sc.x * c.q_scale, sv = ex2(sc.y);
+          const float a = sc.x * q_scale, sv = ex2(sc.y);
           ready(j, r);
           uint32_t w[CW / 2];   // float16 pairs
 #pragma unroll
@@ -829,13 +849,12 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
           }
           const int pb = pcount & 1;
           if (!(ok = mbar_wait_warp(&bar_pempty[pb], ((pcount >> 1) & 1) ^ 1, &abort_flag))) break;
-          uint8_t* to = sP + pb * (N * 256) + set * (kTile * 16) + x * 16;
+          uint8_t* to = sP + pb * F::kWeightBuf + set * (kTile * 16) + x * 16;
           if constexpr (CW == 8) {
-            *reinterpret_cast<uint2*>(to) = make_uint2(hi[0], hi[1]);
-            *reinterpret_cast<uint2*>(to + N * 128) = make_uint2(lo[0], lo[1]);
+            *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], lo[0], lo[1]);
           } else {
             *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[CW / 4 - 2], hi[CW / 4 - 1]);
-            *reinterpret_cast<uint4*>(to + N * 128) = make_uint4(lo[0], lo[1], lo[CW / 4 - 2], lo[CW / 4 - 1]);
+            *reinterpret_cast<uint4*>(to + N * kTile) = make_uint4(lo[0], lo[1], lo[CW / 4 - 2], lo[CW / 4 - 1]);
           }
           fence_proxy_async_smem();
           tc_fence_before();
@@ -851,7 +870,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         // The code from here on is met once a list, each time from memory: loops, not their bodies in a row.
         if (!(ok = mbar_wait_warp(&bar_ofull[u & 1], (u >> 1) & 1, &abort_flag))) break;
         tc_fence_after();
-        // the rows' sums, through the weights' buffers (no MMA reads them now; the sets have a half each)
+        // the rows' sums, through the weights' buffers (no MMA reads them now; a piece a set)
         float* sums = reinterpret_cast<float*>(sP) + c0 * kTile;
 #pragma unroll
         for (int n = 0; n < CW / 2; ++n) {
@@ -869,12 +888,9 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
           if (x % kEach == 0) s_l[c0 + x / kEach] = c.slot < 0 ? 1.f / v : v;
         }
         if constexpr (F::kSets > 1)
-          named_barrier(3, F::kSoft);   // before either set's next weights
+          named_barrier(1 + F::kSets, F::kSoft);   // before any set's next weights
         else
           named_barrier(own, 128);
-        if constexpr (NC < N) {   // the rows that nothing is computed for read as zeros again
-          for (int o = x * 16; o < 2 * N * 256; o += 128 * 16) *reinterpret_cast<uint4*>(sP + o) = make_uint4(0, 0, 0, 0);
-        }
         const int first = c.rg * p.lsub + c0 / p.G;   // block position and head of row c0
         const int live = max(0, min(min(p.rows, (p.L - c.rg * p.lsub) * p.G) - c0, CW));   // rows of the set that there are
         const size_t row0 = (static_cast<size_t>(c.b) * p.L + first) * p.Hq + static_cast<size_t>(c.kvh) * p.G + c0 % p.G;
@@ -884,17 +900,20 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         size_t row = row0;
 #pragma unroll 1
         for (int n0 = 0; n0 < live; n0 += 4) {
-          uint32_t r[4];
+          uint32_t r[4], r2[4];
           tmem_ld4(tOx + n0, r);
+          tmem_ld4(tOx + NC + n0, r2);   // the lower part's
           tmem_wait_ld();
           tmem_regs_ready(r);
+          tmem_regs_ready(r2);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             if (n0 + k >= live) break;
+            const float o = __uint_as_float(r[k]) + __uint_as_float(r2[k]);
             if (c.slot < 0)
-              p.out[row * 128 + x] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(r[k]) * s_l[c0 + n0 + k]));
+              p.out[row * 128 + x] = __bfloat16_as_ushort(__float2bfloat16_rn(o * s_l[c0 + n0 + k]));
             else
-              st_global_hint(mine + (n0 + k) * 128 + x, __uint_as_float(r[k]), keep);
+              st_global_hint(mine + (n0 + k) * 128 + x, o, keep);
             ++row;
             if (++g == p.G) {
               g = 0;
@@ -1790,7 +1809,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_many_kernel(const Params p,
 
 template <int N, int NC, int STAGES>
 cudaError_t launch_few(const CUtensorMap& tk, const CUtensorMap& tv, const Params& p, int grid, cudaStream_t stream) {
-  constexpr size_t smem = Few<N, STAGES>::kSmem;
+  using F = Few<N, NC, STAGES>;
+  constexpr size_t smem = F::kSmem;
   static std::atomic<unsigned long long> attr_done{0};
   const cudaError_t e = once_per_device(attr_done, [] {
     const cudaError_t r = cudaFuncSetAttribute(few_rows_kernel<N, NC, STAGES>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
@@ -1798,7 +1818,7 @@ cudaError_t launch_few(const CUtensorMap& tk, const CUtensorMap& tv, const Param
     return cudaFuncSetAttribute(few_rows_kernel<N, NC, STAGES>, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
   });
   if (e != cudaSuccess) return e;
-  return launch_pdl(few_rows_kernel<N, NC, STAGES>, dim3(grid), dim3(Few<N, STAGES>::kThreads), smem, stream, tk, tv, p);
+  return launch_pdl(few_rows_kernel<N, NC, STAGES>, dim3(grid), dim3(F::kThreads), smem, stream, tk, tv, p);
 }
 
 }  // namespace
