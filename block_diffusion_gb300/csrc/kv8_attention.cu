@@ -757,6 +757,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         float mx[CW];
 #pragma unroll
         for (int n = 0; n < CW; ++n) mx[n] = -CUDART_INF_F;
+#pragma unroll 1
         for (int j = 0; j < c.n_tiles; ++j) {
           uint32_t r[CW];
           load(j, r);
@@ -1129,7 +1130,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       } else {
         c.end = 1;
       }
-      if (ok) ok = mbar_wait_warp<true>(&bar_cempty[rs], ((seq / kRing) & 1) ^ 1, &abort_flag);
+      if (ok) ok = mbar_wait_warp(&bar_cempty[rs], ((seq / kRing) & 1) ^ 1, &abort_flag);
       if (have) pages.give(s_page[seq % 3], s_scale[rs], lane);
       __syncwarp();
       if (lane == 0) {
@@ -1144,7 +1145,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     };
     auto load_q = [&](const Chunk& c) {
       if (lane == 0) {
-        if (ok) ok = mbar_wait<true>(&bar_qempty, (q_loads & 1) ^ 1, &abort_flag);
+        if (ok) ok = mbar_wait(&bar_qempty, (q_loads & 1) ^ 1, &abort_flag);
         if (ok) {
           mbar_arrive_expect_tx(&bar_qfull, 256u * static_cast<uint32_t>(p.rows));
           for (int h = 0; h < 2; ++h)
@@ -1156,7 +1157,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     };
     auto copy = [&](const CUtensorMap* tm, uint8_t* ring, uint64_t* full, uint64_t* empty, int stages, int& st, uint32_t& ph, int page) {
       if (lane == 0) {
-        ok = mbar_wait<true>(&empty[st], ph ^ 1, &abort_flag);
+        ok = mbar_wait(&empty[st], ph ^ 1, &abort_flag);
         if (ok) mbar_arrive_expect_tx(&full[st], kStage);
       }
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -1225,10 +1226,10 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       };
       auto wait_k = [&](bool first) {
         if (first) {
-          if (!(ok = mbar_wait_warp<true>(&bar_qfull, q_used & 1, &abort_flag))) return;
+          if (!(ok = mbar_wait_warp(&bar_qfull, q_used & 1, &abort_flag))) return;
           ++q_used;
         }
-        if (!(ok = mbar_wait_warp<true>(&bar_kfull[kst], kph, &abort_flag))) return;
+        if (!(ok = mbar_wait_warp(&bar_kfull[kst], kph, &abort_flag))) return;
         tc_fence_after();
       };
       auto free_k = [&](bool last) {
@@ -1247,9 +1248,11 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const uint32_t tP = tmem + static_cast<uint32_t>((SUB == 2 ? x : u & 1) * 128);
         const int steps = (valid + 15) / 16;
         if (elect_one()) {
-          for (int q = 0; q < steps; ++q)   // keys 64h .. 64h + 63 of w as columns 64h .. 64h + 31
-            umma_bf16_ts(tO + static_cast<uint32_t>(x * 128), tP + static_cast<uint32_t>((q >> 2) * 64 + (q & 3) * 8),
-                         wd + q * 128, kIdescO, first && q == 0 ? 0u : 1u);
+#pragma unroll
+          for (int q = 0; q < kTile / 16; ++q)   // keys 64h .. 64h + 63 of w as columns 64h .. 64h + 31
+            if (q < steps)
+              umma_bf16_ts(tO + static_cast<uint32_t>(x * 128), tP + static_cast<uint32_t>((q >> 2) * 64 + (q & 3) * 8),
+                           wd + q * 128, kIdescO, first && q == 0 ? 0u : 1u);
           if (x == SUB - 1) {
             umma_commit(&bar_wempty[u & 1]);
             umma_commit(&bar_ofull[u & 1]);
@@ -1258,12 +1261,12 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         __syncwarp();
       };
       auto wait_p = [&](int u, int x) {
-        ok = SUB == 2 ? mbar_wait_warp<true>(&bar_pfull[x], u & 1, &abort_flag)
-                      : mbar_wait_warp<true>(&bar_pfull[u & 1], (u >> 1) & 1, &abort_flag);
+        ok = SUB == 2 ? mbar_wait_warp(&bar_pfull[x], u & 1, &abort_flag)
+                      : mbar_wait_warp(&bar_pfull[u & 1], (u >> 1) & 1, &abort_flag);
         tc_fence_after();
       };
       Chunk cur, nxt;
-      ok = mbar_wait_warp<true>(&bar_cfull[0], 0, &abort_flag);
+      ok = mbar_wait_warp(&bar_cfull[0], 0, &abort_flag);
       cur = s_chunk[0];
       if (ok && !cur.end) {
         wait_k(true);
@@ -1279,7 +1282,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             next_last = cur.last && j + 2 == cur.n_tiles;
           } else {
             const int rs = (cs + 1) % kRing;
-            if (!(ok = mbar_wait_warp<true>(&bar_cfull[rs], ((cs + 1) / kRing) & 1, &abort_flag))) break;
+            if (!(ok = mbar_wait_warp(&bar_cfull[rs], ((cs + 1) / kRing) & 1, &abort_flag))) break;
             nxt = s_chunk[rs];
             has_next = !nxt.end;
             next_first = nxt.first;
@@ -1294,7 +1297,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
               issue_s(u + 1, 0);
               free_k(next_last);
             }
-            if (!(ok = mbar_wait_warp<true>(&bar_wfull[u & 1], (u >> 1) & 1, &abort_flag))) break;
+            if (!(ok = mbar_wait_warp(&bar_wfull[u & 1], (u >> 1) & 1, &abort_flag))) break;
             wait_p(u, 0);
             if (!ok) break;
             issue_pv(u, 0, first, valid);
@@ -1302,7 +1305,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             // PV_0(u), S_0(u + 1), PV_1(u), S_1(u + 1): S_x(u + 1) overwrites the weights that PV_x(u) reads, and
             // the tensor pipe executes one thread's MMAs in order.  Where the next tile has other queries
             // both PVs come first.
-            if (!(ok = mbar_wait_warp<true>(&bar_wfull[u & 1], (u >> 1) & 1, &abort_flag))) break;
+            if (!(ok = mbar_wait_warp(&bar_wfull[u & 1], (u >> 1) & 1, &abort_flag))) break;
             const bool inter = has_next && !next_first;
             for (int x = 0; x < 2 && ok; ++x) {
               wait_p(u, x);
@@ -1345,17 +1348,17 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     uint32_t vph = 0;
     for (int cs = 0; ok; ++cs) {
       const int rs = cs % kRing;
-      if (!(ok = mbar_wait_warp<true>(&bar_cfull[rs], (cs / kRing) & 1, &abort_flag))) break;
+      if (!(ok = mbar_wait_warp(&bar_cfull[rs], (cs / kRing) & 1, &abort_flag))) break;
       const Chunk c = s_chunk[rs];
       if (c.end) break;
       for (int j = 0; j < c.n_tiles; ++j, ++u) {
         const int valid = min(kTile, c.t_end - (c.t0 + j * kTile));
-        if (!(ok = mbar_wait_warp<true>(&bar_wempty[u & 1], ((u >> 1) & 1) ^ 1, &abort_flag))) break;
-        if (!(ok = mbar_wait_warp<true>(&bar_vfull[vst], vph, &abort_flag))) break;
+        if (!(ok = mbar_wait_warp(&bar_wempty[u & 1], ((u >> 1) & 1) ^ 1, &abort_flag))) break;
+        if (!(ok = mbar_wait_warp(&bar_vfull[vst], vph, &abort_flag))) break;
         const uint8_t* src = sV + vst * kStage;
         uint8_t* dst = sW + (u & 1) * F::kWide + (c8 >> 2) * kStage;
         constexpr int kEach = kTile / 4 / F::kConvWarps;   // tokens of a lane
-#pragma unroll 1
+#pragma unroll(SUB == 1 ? 2 : 1)
         for (int k0 = 0; k0 < kEach; k0 += 4) {
           uint4 v[4];
 #pragma unroll
@@ -1404,7 +1407,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     float m_run = -CUDART_INF_F, l_run = 0.f;   // l_run: this half's sum
     for (int cs = 0; ok; ++cs) {
       const int rs = cs % kRing;
-      if (!(ok = mbar_wait_warp<true>(&bar_cfull[rs], (cs / kRing) & 1, &abort_flag))) break;
+      if (!(ok = mbar_wait_warp(&bar_cfull[rs], (cs / kRing) & 1, &abort_flag))) break;
       const Chunk c = s_chunk[rs];
       if (c.end) break;
       if (c.first) {
@@ -1413,8 +1416,8 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       }
       for (int j = 0; j < c.n_tiles; ++j, ++u) {
         const uint32_t tSx = tmem + lane_off + static_cast<uint32_t>((SUB == 2 ? x : u & 1) * 128) + col0;
-        ok = SUB == 2 ? mbar_wait_warp<true>(&bar_sfull[x], u & 1, &abort_flag)
-                      : mbar_wait_warp<true>(&bar_sfull[u & 1], (u >> 1) & 1, &abort_flag);
+        ok = SUB == 2 ? mbar_wait_warp(&bar_sfull[x], u & 1, &abort_flag)
+                      : mbar_wait_warp(&bar_sfull[u & 1], (u >> 1) & 1, &abort_flag);
         if (!ok) break;
         tc_fence_after();
         const int nvalid = min(kTile, c.t_end - (c.t0 + j * kTile)) - half * 64;   // of this half's columns
@@ -1424,10 +1427,11 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           for (int col = max(nvalid, 0); col < 64; ++col) tmem_st1(tSx + col, 0xFF800000u);
           tmem_wait_st();
         }
-        // (Rolled loops, here and in what follows: unrolled, the warps waited for instructions twice as long as they
-        // issued them; 16 blocks of 64 over 8192-16384 tokens 251 us against 223.)
+        // (Code that runs once a list, or seldom, is in rolled loops here, and so are the converters' of 256 rows: with all
+        // of it unrolled the warps waited for instructions twice as long as they issued them.  Unrolling these two halves
+        // of a tile, which every tile meets, was worth 210 -> 203 us for 16 blocks of 64 over 8192-16384 tokens.)
         float mx = -CUDART_INF_F;
-#pragma unroll 1
+#pragma unroll
         for (int g2 = 0; g2 < 2; ++g2) {
           uint32_t r[32];
           tmem_ld16(tSx + g2 * 32, *reinterpret_cast<uint32_t(*)[16]>(r));
@@ -1440,7 +1444,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
         s_hmax[u & 1][x][half][n] = mx;
         mbar_arrive(&bar_pair[pq][u & 1]);
-        if (!(ok = mbar_wait_warp<true>(&bar_pair[pq][u & 1], (u >> 1) & 1, &abort_flag))) break;
+        if (!(ok = mbar_wait_warp(&bar_pair[pq][u & 1], (u >> 1) & 1, &abort_flag))) break;
         mx = fmaxf(s_hmax[u & 1][x][0][n], s_hmax[u & 1][x][1][n]);
         float alpha = 1.f;
         bool resc = false;
@@ -1452,7 +1456,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           resc = true;
         }
         float sum = 0.f;
-#pragma unroll 1
+#pragma unroll
         for (int g2 = 0; g2 < 2; ++g2) {
           uint32_t r[32];
           tmem_ld16(tSx + g2 * 32, *reinterpret_cast<uint32_t(*)[16]>(r));
@@ -1482,7 +1486,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         l_run = fmaf(l_run, alpha, sum);
         if (__any_sync(0xffffffffu, resc)) {
           // this warp's half of its rows of O to the new maxima once the last tile's PV is done
-          if (!(ok = mbar_wait_warp<true>(&bar_ofull[(u - 1) & 1], ((u - 1) >> 1) & 1, &abort_flag))) break;
+          if (!(ok = mbar_wait_warp(&bar_ofull[(u - 1) & 1], ((u - 1) >> 1) & 1, &abort_flag))) break;
           tc_fence_after();
 #pragma unroll 1
           for (int g = 0; g < 4; ++g) {
@@ -1500,11 +1504,11 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         mbar_arrive(&bar_pfull[SUB == 2 ? x : u & 1]);
         if (!c.last || j != c.n_tiles - 1) continue;
         // ---- this half of the row of O, divided by the row's sum or as a part
-        if (!(ok = mbar_wait_warp<true>(&bar_ofull[u & 1], (u >> 1) & 1, &abort_flag))) break;
+        if (!(ok = mbar_wait_warp(&bar_ofull[u & 1], (u >> 1) & 1, &abort_flag))) break;
         tc_fence_after();
         s_hsum[x][half][n] = l_run;
         mbar_arrive(&bar_pair_end[pq]);
-        if (!(ok = mbar_wait_warp<true>(&bar_pair_end[pq], pair_ends & 1, &abort_flag))) break;
+        if (!(ok = mbar_wait_warp(&bar_pair_end[pq], pair_ends & 1, &abort_flag))) break;
         const float l_row = s_hsum[x][0][n] + s_hsum[x][1][n];
         ++pair_ends;
         const int i_row = c.rg * p.lsub + r_item / p.G;
