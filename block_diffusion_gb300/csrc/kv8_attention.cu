@@ -336,7 +336,7 @@ struct Few {
   static constexpr int kSets = NC / CW;         // of softmax warps: 16 rows each (8), of all tokens
   static constexpr int kSoft = 128 * kSets;     // their threads
   static constexpr int kThreads = 128 + kSoft;
-  static constexpr int kWalkWarp = 2 + kSoft / 32, kQueryWarp = kWalkWarp + 1;
+  static constexpr int kWalkWarp = 2 + kSoft / 32, kSecondWarp = kWalkWarp + 1;
   // Two CTAs per SM with 16 rows.  With 32 one, twice as wide: two left chunks of three tiles, whose ends took as long as
   // they (128 blocks of 8 over 512-4096 tokens: 186 us against 170).
   static constexpr int kCtas = N == 16 ? 2 : 1;
@@ -420,7 +420,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
   uint8_t* sQ = base;                  // two parts x N rows x 128 bytes, 128-byte swizzle
   uint8_t* sKV = sQ + N * 256;
   uint8_t* sP = sKV + STAGES * kStage;   // two buffers of kWeights / 16 x 128 tokens x 16 bytes: a byte of each row
-  __shared__ uint64_t bar_qfull, bar_qempty, bar_full[STAGES], bar_empty[STAGES];
+  __shared__ uint64_t bar_qempty, bar_kfull[STAGES], bar_vfull[STAGES], bar_empty[STAGES];
   __shared__ uint64_t bar_sfull[2], bar_sfree[2], bar_pfull[2], bar_pempty[2];
   __shared__ uint64_t bar_ofull[2], bar_done;
   __shared__ uint64_t bar_cfull[kRing], bar_cempty[kRing];
@@ -435,23 +435,23 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    mbar_init(&bar_qfull, 1);
     mbar_init(&bar_qempty, 1);
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&bar_full[s], 1);
+      mbar_init(&bar_kfull[s], 1);   // (apart: a warp that skips the other's tiles would meet a parity of two fills ago)
+      mbar_init(&bar_vfull[s], 1);
       mbar_init(&bar_empty[s], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bar_sfull[i], 1);
+      mbar_init(&bar_sfull[i], 2);   // the MMAs, and the queries' scale
       mbar_init(&bar_sfree[i], F::kSoft);
       mbar_init(&bar_pfull[i], F::kSoft);
       mbar_init(&bar_pempty[i], 1);
       mbar_init(&bar_ofull[i], 1);
     }
-    mbar_init(&bar_done, 1);
+    mbar_init(&bar_done, 2);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&bar_cfull[i], 1);
-      mbar_init(&bar_cempty[i], 2 + F::kSets);   // copies, MMA, softmax
+      mbar_init(&bar_cempty[i], 2 + F::kSets);   // copies, second MMAs, softmax
     }
     abort_flag = 0;
     for (int s = 0; s < F::kSets; ++s) s_need[s][0] = s_need[s][1] = 0;
@@ -463,15 +463,16 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
   }
   // The walk begins beside the set-up.  Its first two chunks are asked for together: once the copies of the first are
   // under way a look-up takes microseconds, and the copies would stand still for the second's.  From then on the walk is
-  // chunks ahead.  The queries' warp walks from list to list.
+  // chunks ahead.  The first MMAs' warp walks from list to list, for
+  // the queries.
   Walk<kChunk> walk;
   Walk<kAllTiles> lists;
   Chunk c, d;
   PageLoads<F::kChunkPages> pages, ahead;
-  uint4 qr[N / 2];    // rows 2i and 2i + 1 of the queries, eight values a lane
+  uint4 qr[NC / 2];   // rows 2i and 2i + 1 of the queries, eight values a lane
   auto ask_q = [&](const Chunk& c) {
 #pragma unroll
-    for (int i = 0; i < N / 2; ++i) {
+    for (int i = 0; i < NC / 2; ++i) {
       const int n = 2 * i + (lane >> 4);
       const int pos = c.rg * p.lsub + n / p.G;
       qr[i] = make_uint4(0, 0, 0, 0);
@@ -494,11 +495,14 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       pages.ask_scales(p, c, lane);
       if (!c.final) ahead.ask_scales(p, d, lane);
     }
-  } else if (warp == F::kQueryWarp) {
+  } else if (warp == 1) {
     griddep_wait();
     lists.init(p, lane);
     c.end = !lists.next(p, lane, c);
     if (!c.end) ask_q(c);
+    for (int n = NC; n < N; ++n)   // rows that no query fills
+      *reinterpret_cast<uint2*>(sQ + (lane >> 4) * (N * 128) + n * 128 + (lane & 15) * 8) = make_uint2(0, 0);
+    if (!c.end) c.end = !lists.next(p, lane, c);
   }
   tc_fence_before();
   __syncthreads();
@@ -515,15 +519,16 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     }
     const uint64_t policy = l2_policy_evict_first();
     int st = 0;
-    uint32_t ph = 0;
+    uint32_t ph = 0, kbits = 0, vbits = 0;   // parities of the stages' next fills with K, with V
     bool ok = true;
-    auto emit = [&](int s, int n_tiles, const CUtensorMap* tm) {   // of chunk number s
+    auto emit = [&](int s, int n_tiles, const CUtensorMap* tm, uint64_t* full, uint32_t& bits) {   // of chunk number s
       for (int j = 0; j < n_tiles && ok; ++j) {
         if (!(ok = mbar_wait_warp(&bar_empty[st], ph ^ 1, &abort_flag))) break;
-        if (lane == 0) mbar_arrive_expect_tx(&bar_full[st], kStage);
+        if (lane == 0) mbar_arrive_expect_tx(&full[st], kStage);
+        bits ^= 1u << st;
         __syncwarp();
         if (lane < kTilePages)
-          tma_load_3d_hint(sKV + st * kStage + lane * 2048, tm, &bar_full[st], 0, 0, s_page[s % kRing][j * kTilePages + lane], policy);
+          tma_load_3d_hint(sKV + st * kStage + lane * 2048, tm, &full[st], 0, 0, s_page[s % kRing][j * kTilePages + lane], policy);
         if (++st == STAGES) {
           st = 0;
           ph ^= 1;
@@ -533,7 +538,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     // K of the next chunk, then V of this one
     if ((ok = mbar_wait_warp(&bar_cfull[0], 0, &abort_flag)) && !s_chunk[0].end) {
       int n_tiles = s_chunk[0].n_tiles, final = s_chunk[0].final;
-      emit(0, n_tiles, &tm_k);
+      emit(0, n_tiles, &tm_k, bar_kfull, kbits);
       for (int u = 0; ok; ++u) {
         int next = 0, next_final = 0;
         if (!final) {
@@ -541,9 +546,9 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
           if (!(ok = mbar_wait_warp(&bar_cfull[rs], ((u + 1) / kRing) & 1, &abort_flag))) break;
           next = s_chunk[rs].n_tiles;
           next_final = s_chunk[rs].final;
-          emit(u + 1, next, &tm_k);
+          emit(u + 1, next, &tm_k, bar_kfull, kbits);
         }
-        emit(u, n_tiles, &tm_v);
+        emit(u, n_tiles, &tm_v, bar_vfull, vbits);
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar_cempty[u % kRing]);
         if (final) break;
@@ -554,25 +559,62 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     if (lane == 0) {
       griddep_launch_dependents();
       if (!ok)
-        for (int s = 0; s < STAGES; ++s) mbar_wait_drain(&bar_full[s], ph ^ (s < st ? 0 : 1));
+        for (int s = 0; s < STAGES; ++s) {
+          mbar_wait_drain(&bar_kfull[s], ((kbits >> s) & 1) ^ 1);
+          mbar_wait_drain(&bar_vfull[s], ((vbits >> s) & 1) ^ 1);
+        }
     }
   } else if (warp == 1) {
-    // =================================================================== MMA issuer
+    // =================================================================== queries, first MMAs
+    // One warp each for the first and the second MMAs: a warp that issued both was busy with it for most of the time (128
+    // blocks of 8 over 512-4096 tokens: FIG), and stood still for one's operands where it could have issued the
+    // other's.
     constexpr uint32_t kIdescS = idesc_e4m3_f32(128, N, false, false);
-    constexpr uint32_t kIdescO = idesc_e4m3_f32(128, F::kWeights, true, true);
-    const uint64_t q_desc = smem_desc(smem_u32(sQ), 16, 1024), p_desc = smem_desc_plain(smem_u32(sP), 128, kTile * 16);
-    const uint64_t k_desc = smem_desc(smem_u32(sKV), 16, 1024), v_desc = smem_desc(smem_u32(sKV), kStage, 1024);
+    const uint64_t q_desc = smem_desc(smem_u32(sQ), 16, 1024), k_desc = smem_desc(smem_u32(sKV), 16, 1024);
     bool ok = true;
-    int st = 0, pcount = 0, q_used = 0;
-    uint32_t ph = 0;
-    auto do_s = [&](bool first, bool last, int n_tiles, int u) {
-      if (!(ok = mbar_wait_warp(&bar_sfree[u & 1], ((u >> 1) & 1) ^ 1, &abort_flag))) return;
-      if (first) {
-        if (!(ok = mbar_wait_warp(&bar_qfull, q_used & 1, &abort_flag))) return;
-        ++q_used;
+    int st = 0, n_list = 0;
+    uint32_t bits = 0;   // parities of the stages' next fills with K
+    // The list's queries in their two parts, once the MMAs on the last one's are done; the next one's are asked for, the
+    // walk a list ahead of that.
+    auto next_q = [&]() {
+      float most = 0.f;
+#pragma unroll
+      for (int i = 0; i < NC / 2; ++i) most = fmaxf(most, magnitude(qr[i]));
+      const int e = q_exponent(warp_max(most));
+      const float inv = pow2(-e);
+      if (!(ok = mbar_wait_warp(&bar_qempty, (n_list & 1) ^ 1, &abort_flag))) return;
+#pragma unroll
+      for (int i = 0; i < NC / 2; ++i) {
+        const int n = 2 * i + (lane >> 4);
+        const uint32_t u[4] = {qr[i].x, qr[i].y, qr[i].z, qr[i].w};
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) split_e4m3x2(bf16_lo(u[k]) * inv, bf16_hi(u[k]) * inv, hi[k], lo[k]);
+        const uint32_t at = n * 128 + ((((lane & 15) >> 1) ^ (n & 7)) << 4) + (lane & 1) * 8;
+        *reinterpret_cast<uint2*>(sQ + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+        *reinterpret_cast<uint2*>(sQ + N * 128 + at) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
       }
+      if (lane == 0) s_qscale[n_list & 3] = pow2(e) * p.scale_log2;
+      fence_proxy_async_smem();
+      __syncwarp();
+      ++n_list;
+      if (!c.end) {
+        ask_q(c);
+        c.end = !lists.next(p, lane, c);
+      }
+    };
+    int skip = 0;   // V's tiles of the chunk before the last, between the copies of K
+    for (int u = 0; ok; ++u) {
+      const int rs = u % kRing;
+      if (!(ok = mbar_wait_warp(&bar_cfull[rs], (u / kRing) & 1, &abort_flag))) break;
+      const int n_tiles = s_chunk[rs].n_tiles, first = s_chunk[rs].first, last = s_chunk[rs].last, final = s_chunk[rs].final;
+      if (s_chunk[rs].end) break;
+      if (first) next_q();
+      if (!ok || !(ok = mbar_wait_warp(&bar_sfree[u & 1], ((u >> 1) & 1) ^ 1, &abort_flag))) break;
+      if (lane == 0) mbar_arrive(&bar_sfull[u & 1]);
       for (int j = 0; j < n_tiles; ++j) {
-        if (!(ok = mbar_wait_warp(&bar_full[st], ph, &abort_flag))) return;
+        if (!(ok = mbar_wait_warp(&bar_kfull[st], (bits >> st) & 1, &abort_flag))) break;
+        bits ^= 1u << st;
         tc_fence_after();
         const uint32_t tS = tmem + static_cast<uint32_t>(((u & 1) * kChunk + j) * N);
         const uint64_t kd = k_desc + static_cast<uint32_t>(st * (kStage >> 4));
@@ -587,59 +629,63 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
           }
         }
         __syncwarp();
-        if (++st == STAGES) {
-          st = 0;
-          ph ^= 1;
-        }
+        if (++st == STAGES) st = 0;
       }
-    };
-    auto do_pv = [&](bool first, int t0, int t_end, int n_tiles, int u) {
-      for (int j = 0; j < n_tiles; ++j) {
-        if (!(ok = mbar_wait_warp(&bar_full[st], ph, &abort_flag))) return;
-        const int valid = min(kTile, t_end - (t0 + j * kTile));
-        if (valid % kPage != 0) {
-          // slots behind the last token may hold anything (NaN); absent pages were read as zeros
-          uint4* z = reinterpret_cast<uint4*>(sKV + st * kStage + valid * 128);
-          for (int o = lane; o < (kPage - valid % kPage) * 8; o += 32) z[o] = make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-        const int pb = pcount & 1;
-        if (!(ok = mbar_wait_warp(&bar_pfull[pb], (pcount >> 1) & 1, &abort_flag))) return;
-        tc_fence_after();
-        const uint64_t vd = v_desc + static_cast<uint32_t>(st * (kStage >> 4)), pd = p_desc + static_cast<uint32_t>(pb * (F::kWeightBuf >> 4));
-        const int steps = (valid + 31) / 32;
-        if (elect_one()) {
-          // 32 tokens of both parts of w, each part into sums of its own: an MMA for either into the same sums, in a loop
-          // of `steps`, took 450 cycles a tile where this takes 170 to 190
-#pragma unroll
-          for (int q = 0; q < kTile / 32; ++q)
-            if (q < steps) umma_e4m3(tO, vd + q * 256, pd + q * 32, kIdescO, q == 0 && first && j == 0 ? 0u : 1u);
-          umma_commit(&bar_pempty[pb]);
-          umma_commit(&bar_empty[st]);
-          if (j == n_tiles - 1) umma_commit(&bar_ofull[u & 1]);
-        }
-        __syncwarp();
-        ++pcount;
-        if (++st == STAGES) {
-          st = 0;
-          ph ^= 1;
-        }
-      }
-    };
+      if (!ok || final) break;
+      st = (st + skip) % STAGES;
+      skip = n_tiles;
+    }
+    if (elect_one()) umma_commit(&bar_done);
+    __syncwarp();
+  } else if (warp == F::kSecondWarp) {
+    // =================================================================== second MMAs
+    constexpr uint32_t kIdescO = idesc_e4m3_f32(128, F::kWeights, true, true);
+    const uint64_t v_desc = smem_desc(smem_u32(sKV), kStage, 1024), p_desc = smem_desc_plain(smem_u32(sP), 128, kTile * 16);
+    bool ok = mbar_wait_warp(&bar_cfull[0], 0, &abort_flag);
+    int st = 0, pcount = 0;
+    uint32_t bits = 0;   // parities of the stages' next fills with V
     Chunk cur, nxt;
-    ok = mbar_wait_warp(&bar_cfull[0], 0, &abort_flag);
-    cur = s_chunk[0];
+    if (ok) cur = s_chunk[0];
     if (ok && !cur.end) {
-      do_s(true, cur.last, cur.n_tiles, 0);
+      st = cur.n_tiles % STAGES;   // behind K's tiles
       for (int u = 0; ok; ++u) {
         if (!cur.final) {
           const int rs = (u + 1) % kRing;
           if (!(ok = mbar_wait_warp(&bar_cfull[rs], ((u + 1) / kRing) & 1, &abort_flag))) break;
           nxt = s_chunk[rs];
-          do_s(nxt.first, nxt.last, nxt.n_tiles, u + 1);   // ahead of PV(u): the softmax goes on meanwhile
+          st = (st + nxt.n_tiles) % STAGES;
         }
-        if (ok) do_pv(cur.first, cur.t0, cur.t_end, cur.n_tiles, u);
+        for (int j = 0; j < cur.n_tiles; ++j) {
+          if (!(ok = mbar_wait_warp(&bar_vfull[st], (bits >> st) & 1, &abort_flag))) break;
+          bits ^= 1u << st;
+          const int valid = min(kTile, cur.t_end - (cur.t0 + j * kTile));
+          if (valid % kPage != 0) {
+            // slots behind the last token may hold anything (NaN); absent pages were read as zeros
+            uint4* z = reinterpret_cast<uint4*>(sKV + st * kStage + valid * 128);
+            for (int o = lane; o < (kPage - valid % kPage) * 8; o += 32) z[o] = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          const int pb = pcount & 1;
+          if (!(ok = mbar_wait_warp(&bar_pfull[pb], (pcount >> 1) & 1, &abort_flag))) break;
+          tc_fence_after();
+          const uint64_t vd = v_desc + static_cast<uint32_t>(st * (kStage >> 4));
+          const uint64_t pd = p_desc + static_cast<uint32_t>(pb * (F::kWeightBuf >> 4));
+          const int steps = (valid + 31) / 32;
+          if (elect_one()) {
+            // 32 tokens of both parts of w, each part into sums of its own: an MMA for either into the same sums, in a
+            // loop of `steps`, took 450 cycles a tile where this takes 170 to 190
+#pragma unroll
+            for (int q = 0; q < kTile / 32; ++q)
+              if (q < steps) umma_e4m3(tO, vd + q * 256, pd + q * 32, kIdescO, q == 0 && cur.first && j == 0 ? 0u : 1u);
+            umma_commit(&bar_pempty[pb]);
+            umma_commit(&bar_empty[st]);
+            if (j == cur.n_tiles - 1) umma_commit(&bar_ofull[u & 1]);
+          }
+          __syncwarp();
+          ++pcount;
+          if (++st == STAGES) st = 0;
+        }
         if (!ok) break;
         if (lane == 0) mbar_arrive(&bar_cempty[u % kRing]);
         if (cur.final) break;
@@ -675,39 +721,6 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         ahead = pages;
       }
       if (ok) publish(d, ahead);
-    }
-  } else if (warp == F::kQueryWarp) {
-    // =================================================================== queries
-    // A list's queries in their two parts, kept in registers until the MMAs on the last list's are done.
-    bool ok = true;
-    for (int n_list = 0; !c.end; ++n_list) {
-      float most = 0.f;
-#pragma unroll
-      for (int i = 0; i < N / 2; ++i) most = fmaxf(most, magnitude(qr[i]));
-      const int e = q_exponent(warp_max(most));
-      const float inv = pow2(-e);
-#pragma unroll
-      for (int i = 0; i < N / 2; ++i) {
-        const uint32_t u[4] = {qr[i].x, qr[i].y, qr[i].z, qr[i].w};
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) split_e4m3x2(bf16_lo(u[k]) * inv, bf16_hi(u[k]) * inv, hi[k], lo[k]);
-        qr[i] = make_uint4(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16, lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-      }
-      if (!(ok = mbar_wait_warp(&bar_qempty, (n_list & 1) ^ 1, &abort_flag))) break;
-#pragma unroll
-      for (int i = 0; i < N / 2; ++i) {
-        const int n = 2 * i + (lane >> 4);
-        const uint32_t at = n * 128 + ((((lane & 15) >> 1) ^ (n & 7)) << 4) + (lane & 1) * 8;
-        *reinterpret_cast<uint2*>(sQ + at) = make_uint2(qr[i].x, qr[i].y);
-        *reinterpret_cast<uint2*>(sQ + N * 128 + at) = make_uint2(qr[i].z, qr[i].w);
-      }
-      if (lane == 0) s_qscale[n_list & 3] = pow2(e) * p.scale_log2;
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar_qfull);
-      c.end = !lists.next(p, lane, c);
-      if (!c.end) ask_q(c);
     }
   } else {
     // =================================================================== softmax, epilogue
