@@ -25,6 +25,10 @@ constexpr int kPage = 16;
 // is exact, so a value is rounded once, to e4m3's four bits, whatever the scale, and tokens that the page
 // held before move to another scale without rounding anew (but for those that fall below its smallest
 // step).  A finer scale would gain up to one bit of range below, not of precision.
+//
+// Bound: HBM, 512 bytes read and 256 written a token and head: 32 prompts of up to 4096 tokens, 8 heads, in 70 us, 5.9
+// TB/s (87 % of the copy rate).  The whole page is in the warp's registers between its maximum and its codes, as bf16
+// pairs: as 64 floats a lane fewer pages were under way (100 us).  A block's write (128 pages) is latency, 5.3 us.
 constexpr int kWriteWarps = 8;
 constexpr int kScaleExp = 40;
 

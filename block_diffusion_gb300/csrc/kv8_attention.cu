@@ -16,9 +16,18 @@
 //    sum w_t / sV_t is the divisor.  So w's parts keep their precision where it counts, whatever the
 //    scales are from page to page.
 //  * Work: the tiles of 128 tokens of all (sequence, KV head, row group) lists, end to end, are cut
-//    into units of equal numbers of tiles, which CTAs take in turn.  A list that a unit's border cuts is
-//    written in parts (O, m, l) that a second kernel joins in order.  So the work is even whatever the
-//    lengths, and there are at most two parts a unit.
+//    into units of equal numbers of tiles, one a CTA.  A list that a unit's border cuts is written in parts
+//    (O, m, l), at most two a unit, that are joined in order: by the CTA that writes the last of them, or by a
+//    kernel behind (plan_attention_kv8).  So the work is even whatever the lengths.
+//
+// Bound: the codes, 256 bytes a token and KV head, come once from HBM.  Measured (a graph of calls):
+//     64 blocks of 2 over 2000-8000 tokens, 4 rows a KV head .... 106 us, 6.2 TB/s (91 % of the copy rate)
+//     128 blocks of 4 over 512-4096 tokens, 16 rows a KV head ... 107.5 us, 5.7 TB/s (84 %)
+//     32 single tokens over 16384-32768 tokens, 8 rows .......... 127 us, 6.3 TB/s (93 %)
+//     128 blocks of 8 over 512-4096 tokens, 32 rows ............. 154 us, 4.0 TB/s (60 %): lists' ends
+//     16 blocks of 32 over 8192-16384 tokens, 128 rows .......... 126 us, 3.3 TB/s: the softmax's latency
+//     16 blocks of 64 over 8192-16384 tokens, 256 rows .......... 198 us, 1.05 PFLOP/s (55 %): MMAs and softmax in turn
+//     one block of 4 over 2000 tokens, 8 rows .................... 10.3 us, latency
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -322,12 +331,15 @@ constexpr int kFewParts = 8;    // parts a list, about
 // ------------------------------------------------------------------ up to 32 query rows per KV head
 //
 // Transposed: S^T = K Q^T with 128 tokens on M and the query rows on N, O^T += V^T W^T with the 128 head
-// dims on M, so a few rows fill the tensor cores' tiles.  The last warp walks the work ahead of all others: it looks
-// up pages and scales, and turns the queries into their parts.  Warp 0 streams K and V (TMA, a box of 2 KB a
-// page, into a ring of 16 KB stages); warp 1 issues the MMAs; four warps for every 16 rows, a token (of S^T) or head dim
-// (of O^T) a thread, do the softmax.  A chunk of tiles whose
-// S^T fit tensor memory is taken at once: the maxima over all of it, then its weights tile by tile.  S^T
-// is double-buffered and K of chunk u + 1 streams ahead of V of chunk u.
+// dims on M, so a few rows fill the tensor cores' tiles.  One warp walks the work ahead of all others and looks up
+// pages and scales.  Warp 0 streams K and V (TMA, a box of 2 KB a page, into a ring of 16 KB stages); warp 1 turns the
+// queries into their parts and issues the first MMAs, the last warp the second; four warps for every 16 rows, a
+// token (of S^T) or head dim (of O^T) a thread, do the softmax.  A chunk of tiles whose S^T fit tensor memory is
+// taken at once: the maxima over all of it, then its weights tile by tile.  S^T is double-buffered and K of chunk
+// u + 1 streams ahead of V of chunk u.
+//
+// Bound: HBM with up to 16 rows.  With 32, each list's end (the last weights, O^T out, the next queries) holds the one CTA
+// of an SM up for about a tile's time: 32 blocks of 8 over 2000-16000 tokens run at 4.9 TB/s, 128 over 512-4096 at 4.0.
 
 // N: rows of the first MMAs, NC: rows that the softmax computes.
 template <int N, int NC, int STAGES>
@@ -338,7 +350,7 @@ struct Few {
   static constexpr int kThreads = 128 + kSoft;
   static constexpr int kWalkWarp = 2 + kSoft / 32, kSecondWarp = kWalkWarp + 1;
   // Two CTAs per SM with 16 rows.  With 32 one, twice as wide: two left chunks of three tiles, whose ends took as long as
-  // they (128 blocks of 8 over 512-4096 tokens: 186 us against 170).
+  // they (128 blocks of 8 over 512-4096 tokens: 186 us against 170, before the MMAs had a warp each).
   static constexpr int kCtas = N == 16 ? 2 : 1;
   static constexpr int kTmemCols = 512 / kCtas;
   static constexpr int kWeights = 2 * NC;       // rows of the second MMAs: both parts of the weights
@@ -567,8 +579,8 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
   } else if (warp == 1) {
     // =================================================================== queries, first MMAs
     // One warp each for the first and the second MMAs: a warp that issued both was busy with it for most of the time (128
-    // blocks of 8 over 512-4096 tokens: FIG), and stood still for one's operands where it could have issued the
-    // other's.
+    // blocks of 8 over 512-4096 tokens: 158 us against 153), and stood still for one's operands where it could have issued
+    // the other's.
     constexpr uint32_t kIdescS = idesc_e4m3_f32(128, N, false, false);
     const uint64_t q_desc = smem_desc(smem_u32(sQ), 16, 1024), k_desc = smem_desc(smem_u32(sKV), 16, 1024);
     bool ok = true;
@@ -992,6 +1004,11 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 // memory) and the second product is kind::f16.  The first takes K's codes as they are and Q's two parts,
 // which a small kernel makes beforehand.  Softmax: two threads a row, 64 tokens each; a page's scales are
 // the same for 16 of them, so the maximum is taken of raw scores page by page.
+//
+// Bound, with 256 rows: a group's softmax (about 2000 cycles a tile) and its MMAs (1000 alone, 1400 beside the
+// converters' and copies' use of shared memory) follow one another, and the two groups' overlap only in part; without the
+// exponentials it takes as long.  198 us for 16 blocks of 64 over 8192-16384 tokens, of which the joins take about 10 and
+// the queries' parts 5; bf16's block attention takes 237 for twice the bytes.
 template <int SUB>
 struct Many {
   static constexpr int kRowsItem = 128 * SUB;

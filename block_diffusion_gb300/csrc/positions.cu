@@ -18,6 +18,10 @@ constexpr int kPage = 16;
 // the list of free pages in sequence order: running sums over the sequences say where each one's pages and
 // tokens begin.  A sequence is served where the pages up to and with its own, and the tokens, suffice;
 // behind the first that is not served only those that need nothing are.
+//
+// Bound: latency.  A table costs a dozen bytes a sequence and row, but sums over all sequences come before the first
+// row.  One launch of one CTA while its threads have no more than four rows each (a step of 128 sequences: 5.6 us); above
+// that a CTA plans and a second kernel places the rows (256 prompts, 2^20 rows: 10.2 us; the rows alone 8.4 MB).
 constexpr int kScanThreads = 1024;
 
 // Running sums of two values over the CTA's threads, `a` and `b` becoming those up to and with the thread's
@@ -236,6 +240,10 @@ __global__ void __launch_bounds__(kRowThreads) table_rows_kernel(const TablePara
 // product with the position, modulo 2^64, is the angle modulo a turn exactly, however far the position:
 // float32 loses it (position 500000 has steps of 0.03 radians there).  Its upper 32 bits then suffice for
 // sine and cosine in float32.
+//
+// Bound: HBM, 256 bytes read and as many written a token and head: 8 prompts of 4096 tokens, 40 heads, in 94 us, 6.7
+// TB/s (99 % of the copy rate); 105 us with one head under way a thread instead of three.  A block's queries and keys
+// (128 x 4 tokens) are latency, 4.4 us.
 constexpr int kRotaryThreads = 256;
 constexpr int kRotaryRows = 4;    // tokens of a CTA: a thread computes the angle of one pair
 constexpr int kRotaryBatch = 3;
