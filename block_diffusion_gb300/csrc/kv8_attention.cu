@@ -95,6 +95,18 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
   return a / b;
 }
 
+// mbar_wait_warp; FAR: with all that follows a first failed try out of line.  Its loops in every place that waits made the
+// warps wait for instructions: 128 blocks of 8 over 512-4096 tokens 153 us against 145, 1024 sequences of 100-1000 tokens
+// 221 against 206, 16 blocks of 32 over 8192-16384 124.5 against 122.  With 256 rows, whose softmax has no registers to
+// spare for a call, in line: 16 blocks of 64 197 us against 200.
+__device__ __noinline__ bool wait_on(uint64_t* bar, uint32_t parity, int* abort) { return mbar_wait_warp(bar, parity, abort); }
+template <bool FAR>
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, int* abort) {
+  if constexpr (!FAR) return mbar_wait_warp(bar, parity, abort);
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return wait_on(bar, parity, abort);
+}
+
 // Tiles of a unit, a CTA's even share of all.  (Shares of a quarter, taken in turn, were no faster: what they gain
 // in evenness goes into four times the parts.)
 __device__ __forceinline__ long long unit_tiles(long long total, int ctas) {
@@ -535,7 +547,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     bool ok = true;
     auto emit = [&](int s, int n_tiles, const CUtensorMap* tm, uint64_t* full, uint32_t& bits) {   // of chunk number s
       for (int j = 0; j < n_tiles && ok; ++j) {
-        if (!(ok = mbar_wait_warp(&bar_empty[st], ph ^ 1, &abort_flag))) break;
+        if (!(ok = wait_warp<true>(&bar_empty[st], ph ^ 1, &abort_flag))) break;
         if (lane == 0) mbar_arrive_expect_tx(&full[st], kStage);
         bits ^= 1u << st;
         __syncwarp();
@@ -548,14 +560,14 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       }
     };
     // K of the next chunk, then V of this one
-    if ((ok = mbar_wait_warp(&bar_cfull[0], 0, &abort_flag)) && !s_chunk[0].end) {
+    if ((ok = wait_warp<true>(&bar_cfull[0], 0, &abort_flag)) && !s_chunk[0].end) {
       int n_tiles = s_chunk[0].n_tiles, final = s_chunk[0].final;
       emit(0, n_tiles, &tm_k, bar_kfull, kbits);
       for (int u = 0; ok; ++u) {
         int next = 0, next_final = 0;
         if (!final) {
           const int rs = (u + 1) % kRing;
-          if (!(ok = mbar_wait_warp(&bar_cfull[rs], ((u + 1) / kRing) & 1, &abort_flag))) break;
+          if (!(ok = wait_warp<true>(&bar_cfull[rs], ((u + 1) / kRing) & 1, &abort_flag))) break;
           next = s_chunk[rs].n_tiles;
           next_final = s_chunk[rs].final;
           emit(u + 1, next, &tm_k, bar_kfull, kbits);
@@ -594,7 +606,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       for (int i = 0; i < NC / 2; ++i) most = fmaxf(most, magnitude(qr[i]));
       const int e = q_exponent(warp_max(most));
       const float inv = pow2(-e);
-      if (!(ok = mbar_wait_warp(&bar_qempty, (n_list & 1) ^ 1, &abort_flag))) return;
+      if (!(ok = wait_warp<true>(&bar_qempty, (n_list & 1) ^ 1, &abort_flag))) return;
 #pragma unroll
       for (int i = 0; i < NC / 2; ++i) {
         const int n = 2 * i + (lane >> 4);
@@ -618,14 +630,14 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     int skip = 0;   // V's tiles of the chunk before the last, between the copies of K
     for (int u = 0; ok; ++u) {
       const int rs = u % kRing;
-      if (!(ok = mbar_wait_warp(&bar_cfull[rs], (u / kRing) & 1, &abort_flag))) break;
+      if (!(ok = wait_warp<true>(&bar_cfull[rs], (u / kRing) & 1, &abort_flag))) break;
       const int n_tiles = s_chunk[rs].n_tiles, first = s_chunk[rs].first, last = s_chunk[rs].last, final = s_chunk[rs].final;
       if (s_chunk[rs].end) break;
       if (first) next_q();
-      if (!ok || !(ok = mbar_wait_warp(&bar_sfree[u & 1], ((u >> 1) & 1) ^ 1, &abort_flag))) break;
+      if (!ok || !(ok = wait_warp<true>(&bar_sfree[u & 1], ((u >> 1) & 1) ^ 1, &abort_flag))) break;
       if (lane == 0) mbar_arrive(&bar_sfull[u & 1]);
       for (int j = 0; j < n_tiles; ++j) {
-        if (!(ok = mbar_wait_warp(&bar_kfull[st], (bits >> st) & 1, &abort_flag))) break;
+        if (!(ok = wait_warp<true>(&bar_kfull[st], (bits >> st) & 1, &abort_flag))) break;
         bits ^= 1u << st;
         tc_fence_after();
         const uint32_t tS = tmem + static_cast<uint32_t>(((u & 1) * kChunk + j) * N);
@@ -653,7 +665,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     // =================================================================== second MMAs
     constexpr uint32_t kIdescO = idesc_e4m3_f32(128, F::kWeights, true, true);
     const uint64_t v_desc = smem_desc(smem_u32(sKV), kStage, 1024), p_desc = smem_desc_plain(smem_u32(sP), 128, kTile * 16);
-    bool ok = mbar_wait_warp(&bar_cfull[0], 0, &abort_flag);
+    bool ok = wait_warp<true>(&bar_cfull[0], 0, &abort_flag);
     int st = 0, pcount = 0;
     uint32_t bits = 0;   // parities of the stages' next fills with V
     Chunk cur, nxt;
@@ -663,12 +675,12 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       for (int u = 0; ok; ++u) {
         if (!cur.final) {
           const int rs = (u + 1) % kRing;
-          if (!(ok = mbar_wait_warp(&bar_cfull[rs], ((u + 1) / kRing) & 1, &abort_flag))) break;
+          if (!(ok = wait_warp<true>(&bar_cfull[rs], ((u + 1) / kRing) & 1, &abort_flag))) break;
           nxt = s_chunk[rs];
           st = (st + nxt.n_tiles) % STAGES;
         }
         for (int j = 0; j < cur.n_tiles; ++j) {
-          if (!(ok = mbar_wait_warp(&bar_vfull[st], (bits >> st) & 1, &abort_flag))) break;
+          if (!(ok = wait_warp<true>(&bar_vfull[st], (bits >> st) & 1, &abort_flag))) break;
           bits ^= 1u << st;
           const int valid = min(kTile, cur.t_end - (cur.t0 + j * kTile));
           if (valid % kPage != 0) {
@@ -679,7 +691,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             __syncwarp();
           }
           const int pb = pcount & 1;
-          if (!(ok = mbar_wait_warp(&bar_pfull[pb], (pcount >> 1) & 1, &abort_flag))) break;
+          if (!(ok = wait_warp<true>(&bar_pfull[pb], (pcount >> 1) & 1, &abort_flag))) break;
           tc_fence_after();
           const uint64_t vd = v_desc + static_cast<uint32_t>(st * (kStage >> 4));
           const uint64_t pd = p_desc + static_cast<uint32_t>(pb * (F::kWeightBuf >> 4));
@@ -712,7 +724,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     int seq = 0;
     auto publish = [&](Chunk& c, const PageLoads<F::kChunkPages>& pages) {   // chunk number seq
       const int rs = seq % kRing;
-      if (!(ok = mbar_wait_warp(&bar_cempty[rs], ((seq / kRing) & 1) ^ 1, &abort_flag))) return;
+      if (!(ok = wait_warp<true>(&bar_cempty[rs], ((seq / kRing) & 1) ^ 1, &abort_flag))) return;
       if (!c.end) pages.give(s_page[rs], s_scale[rs], lane);
       __syncwarp();
       if (lane == 0) {
@@ -748,7 +760,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     int pcount = 0, n_list = -1;
     for (int u = 0; ok; ++u) {
       const int rs = u % kRing;
-      if (!(ok = mbar_wait_warp(&bar_cfull[rs], (u / kRing) & 1, &abort_flag))) break;
+      if (!(ok = wait_warp<true>(&bar_cfull[rs], (u / kRing) & 1, &abort_flag))) break;
       const Chunk c = s_chunk[rs];
       if (c.end) break;
       if (c.first) {
@@ -758,7 +770,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         if (x < CW) s_m[c0 + x] = -CUDART_INF_F;
       }
       const uint32_t tS = tmem + lane_off + static_cast<uint32_t>((u & 1) * kChunk * N + c0);
-      if (!(ok = mbar_wait_warp(&bar_sfull[u & 1], (u >> 1) & 1, &abort_flag))) break;
+      if (!(ok = wait_warp<true>(&bar_sfull[u & 1], (u >> 1) & 1, &abort_flag))) break;
       tc_fence_after();
       const float q_scale = s_qscale[n_list & 3];
       // the exact maxima of x over the chunk (behind the last token scores may be anything: -inf)
@@ -824,7 +836,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       const bool need = s_need[set][u & 1] != 0;
       if (!c.first && need) {
         // these rows of O^T and l to the new maxima
-        if (!(ok = mbar_wait_warp(&bar_ofull[(u - 1) & 1], ((u - 1) >> 1) & 1, &abort_flag))) break;
+        if (!(ok = wait_warp<true>(&bar_ofull[(u - 1) & 1], ((u - 1) >> 1) & 1, &abort_flag))) break;
         tc_fence_after();
 #pragma unroll 1
         for (uint32_t col = 0; col < F::kWeights; col += NC < 16 ? 16 : N) {   // (eight rows: both parts at once)
@@ -874,7 +886,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             lo[n] = o[0] | o[1] << 16;
           }
           const int pb = pcount & 1;
-          if (!(ok = mbar_wait_warp(&bar_pempty[pb], ((pcount >> 1) & 1) ^ 1, &abort_flag))) break;
+          if (!(ok = wait_warp<true>(&bar_pempty[pb], ((pcount >> 1) & 1) ^ 1, &abort_flag))) break;
           uint8_t* to = sP + pb * F::kWeightBuf + set * (kTile * 16) + x * 16;
           if constexpr (CW == 8) {
             *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], lo[0], lo[1]);
@@ -894,7 +906,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       mbar_arrive(&bar_sfree[u & 1]);
       if (c.last) {
         // The code from here on is met once a list, each time from memory: loops, not their bodies in a row.
-        if (!(ok = mbar_wait_warp(&bar_ofull[u & 1], (u >> 1) & 1, &abort_flag))) break;
+        if (!(ok = wait_warp<true>(&bar_ofull[u & 1], (u >> 1) & 1, &abort_flag))) break;
         tc_fence_after();
         // the rows' sums, through the weights' buffers (no MMA reads them now; a piece a set)
         float* sums = reinterpret_cast<float*>(sP) + c0 * kTile;
@@ -1160,7 +1172,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       } else {
         c.end = 1;
       }
-      if (ok) ok = mbar_wait_warp(&bar_cempty[rs], ((seq / kRing) & 1) ^ 1, &abort_flag);
+      if (ok) ok = wait_warp<SUB == 1>(&bar_cempty[rs], ((seq / kRing) & 1) ^ 1, &abort_flag);
       if (have) pages.give(s_page[seq % 3], s_scale[rs], lane);
       __syncwarp();
       if (lane == 0) {
@@ -1256,10 +1268,10 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       };
       auto wait_k = [&](bool first) {
         if (first) {
-          if (!(ok = mbar_wait_warp(&bar_qfull, q_used & 1, &abort_flag))) return;
+          if (!(ok = wait_warp<SUB == 1>(&bar_qfull, q_used & 1, &abort_flag))) return;
           ++q_used;
         }
-        if (!(ok = mbar_wait_warp(&bar_kfull[kst], kph, &abort_flag))) return;
+        if (!(ok = wait_warp<SUB == 1>(&bar_kfull[kst], kph, &abort_flag))) return;
         tc_fence_after();
       };
       auto free_k = [&](bool last) {
@@ -1291,12 +1303,12 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         __syncwarp();
       };
       auto wait_p = [&](int u, int x) {
-        ok = SUB == 2 ? mbar_wait_warp(&bar_pfull[x], u & 1, &abort_flag)
-                      : mbar_wait_warp(&bar_pfull[u & 1], (u >> 1) & 1, &abort_flag);
+        ok = SUB == 2 ? wait_warp<SUB == 1>(&bar_pfull[x], u & 1, &abort_flag)
+                      : wait_warp<SUB == 1>(&bar_pfull[u & 1], (u >> 1) & 1, &abort_flag);
         tc_fence_after();
       };
       Chunk cur, nxt;
-      ok = mbar_wait_warp(&bar_cfull[0], 0, &abort_flag);
+      ok = wait_warp<SUB == 1>(&bar_cfull[0], 0, &abort_flag);
       cur = s_chunk[0];
       if (ok && !cur.end) {
         wait_k(true);
@@ -1312,7 +1324,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             next_last = cur.last && j + 2 == cur.n_tiles;
           } else {
             const int rs = (cs + 1) % kRing;
-            if (!(ok = mbar_wait_warp(&bar_cfull[rs], ((cs + 1) / kRing) & 1, &abort_flag))) break;
+            if (!(ok = wait_warp<SUB == 1>(&bar_cfull[rs], ((cs + 1) / kRing) & 1, &abort_flag))) break;
             nxt = s_chunk[rs];
             has_next = !nxt.end;
             next_first = nxt.first;
@@ -1327,7 +1339,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
               issue_s(u + 1, 0);
               free_k(next_last);
             }
-            if (!(ok = mbar_wait_warp(&bar_wfull[u & 1], (u >> 1) & 1, &abort_flag))) break;
+            if (!(ok = wait_warp<SUB == 1>(&bar_wfull[u & 1], (u >> 1) & 1, &abort_flag))) break;
             wait_p(u, 0);
             if (!ok) break;
             issue_pv(u, 0, first, valid);
@@ -1335,7 +1347,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             // PV_0(u), S_0(u + 1), PV_1(u), S_1(u + 1): S_x(u + 1) overwrites the weights that PV_x(u) reads, and
             // the tensor pipe executes one thread's MMAs in order.  Where the next tile has other queries
             // both PVs come first.
-            if (!(ok = mbar_wait_warp(&bar_wfull[u & 1], (u >> 1) & 1, &abort_flag))) break;
+            if (!(ok = wait_warp<SUB == 1>(&bar_wfull[u & 1], (u >> 1) & 1, &abort_flag))) break;
             const bool inter = has_next && !next_first;
             for (int x = 0; x < 2 && ok; ++x) {
               wait_p(u, x);
@@ -1378,13 +1390,13 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     uint32_t vph = 0;
     for (int cs = 0; ok; ++cs) {
       const int rs = cs % kRing;
-      if (!(ok = mbar_wait_warp(&bar_cfull[rs], (cs / kRing) & 1, &abort_flag))) break;
+      if (!(ok = wait_warp<SUB == 1>(&bar_cfull[rs], (cs / kRing) & 1, &abort_flag))) break;
       const Chunk c = s_chunk[rs];
       if (c.end) break;
       for (int j = 0; j < c.n_tiles; ++j, ++u) {
         const int valid = min(kTile, c.t_end - (c.t0 + j * kTile));
-        if (!(ok = mbar_wait_warp(&bar_wempty[u & 1], ((u >> 1) & 1) ^ 1, &abort_flag))) break;
-        if (!(ok = mbar_wait_warp(&bar_vfull[vst], vph, &abort_flag))) break;
+        if (!(ok = wait_warp<SUB == 1>(&bar_wempty[u & 1], ((u >> 1) & 1) ^ 1, &abort_flag))) break;
+        if (!(ok = wait_warp<SUB == 1>(&bar_vfull[vst], vph, &abort_flag))) break;
         const uint8_t* src = sV + vst * kStage;
         uint8_t* dst = sW + (u & 1) * F::kWide + (c8 >> 2) * kStage;
         constexpr int kEach = kTile / 4 / F::kConvWarps;   // tokens of a lane
@@ -1437,7 +1449,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     float m_run = -CUDART_INF_F, l_run = 0.f;   // l_run: this half's sum
     for (int cs = 0; ok; ++cs) {
       const int rs = cs % kRing;
-      if (!(ok = mbar_wait_warp(&bar_cfull[rs], (cs / kRing) & 1, &abort_flag))) break;
+      if (!(ok = wait_warp<SUB == 1>(&bar_cfull[rs], (cs / kRing) & 1, &abort_flag))) break;
       const Chunk c = s_chunk[rs];
       if (c.end) break;
       if (c.first) {
@@ -1446,8 +1458,8 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       }
       for (int j = 0; j < c.n_tiles; ++j, ++u) {
         const uint32_t tSx = tmem + lane_off + static_cast<uint32_t>((SUB == 2 ? x : u & 1) * 128) + col0;
-        ok = SUB == 2 ? mbar_wait_warp(&bar_sfull[x], u & 1, &abort_flag)
-                      : mbar_wait_warp(&bar_sfull[u & 1], (u >> 1) & 1, &abort_flag);
+        ok = SUB == 2 ? wait_warp<SUB == 1>(&bar_sfull[x], u & 1, &abort_flag)
+                      : wait_warp<SUB == 1>(&bar_sfull[u & 1], (u >> 1) & 1, &abort_flag);
         if (!ok) break;
         tc_fence_after();
         const int nvalid = min(kTile, c.t_end - (c.t0 + j * kTile)) - half * 64;   // of this half's columns
@@ -1474,7 +1486,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
         s_hmax[u & 1][x][half][n] = mx;
         mbar_arrive(&bar_pair[pq][u & 1]);
-        if (!(ok = mbar_wait_warp(&bar_pair[pq][u & 1], (u >> 1) & 1, &abort_flag))) break;
+        if (!(ok = wait_warp<SUB == 1>(&bar_pair[pq][u & 1], (u >> 1) & 1, &abort_flag))) break;
         mx = fmaxf(s_hmax[u & 1][x][0][n], s_hmax[u & 1][x][1][n]);
         float alpha = 1.f;
         bool resc = false;
@@ -1516,7 +1528,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         l_run = fmaf(l_run, alpha, sum);
         if (__any_sync(0xffffffffu, resc)) {
           // this warp's half of its rows of O to the new maxima once the last tile's PV is done
-          if (!(ok = mbar_wait_warp(&bar_ofull[(u - 1) & 1], ((u - 1) >> 1) & 1, &abort_flag))) break;
+          if (!(ok = wait_warp<SUB == 1>(&bar_ofull[(u - 1) & 1], ((u - 1) >> 1) & 1, &abort_flag))) break;
           tc_fence_after();
 #pragma unroll 1
           for (int g = 0; g < 4; ++g) {
@@ -1534,11 +1546,11 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         mbar_arrive(&bar_pfull[SUB == 2 ? x : u & 1]);
         if (!c.last || j != c.n_tiles - 1) continue;
         // ---- this half of the row of O, divided by the row's sum or as a part
-        if (!(ok = mbar_wait_warp(&bar_ofull[u & 1], (u >> 1) & 1, &abort_flag))) break;
+        if (!(ok = wait_warp<SUB == 1>(&bar_ofull[u & 1], (u >> 1) & 1, &abort_flag))) break;
         tc_fence_after();
         s_hsum[x][half][n] = l_run;
         mbar_arrive(&bar_pair_end[pq]);
-        if (!(ok = mbar_wait_warp(&bar_pair_end[pq], pair_ends & 1, &abort_flag))) break;
+        if (!(ok = wait_warp<SUB == 1>(&bar_pair_end[pq], pair_ends & 1, &abort_flag))) break;
         const float l_row = s_hsum[x][0][n] + s_hsum[x][1][n];
         ++pair_ends;
         const int i_row = c.rg * p.lsub + r_item / p.G;
@@ -1767,7 +1779,7 @@ __global__ void __launch_bounds__(256) join_few_kernel(const Params p, int n_row
       M[k] = top;
     }
     const int cnt = min(32, j.parts - at);
-#pragma unroll(R == 1 ? 4 : 2)
+#pragma unroll(R == 1 ? 4 : 1)
     for (int i = 0; i < cnt; ++i) {
       const float4* from = reinterpret_cast<const float4*>(j.part(p, at + i, n_rows) + n0 * 128) + lane;
 #pragma unroll
