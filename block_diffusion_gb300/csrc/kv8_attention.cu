@@ -22,12 +22,13 @@
 //
 // Bound: the codes, 256 bytes a token and KV head, come once from HBM.  Measured (a graph of calls):
 //     64 blocks of 2 over 2000-8000 tokens, 4 rows a KV head .... 106 us, 6.2 TB/s (91 % of the copy rate)
-//     128 blocks of 4 over 512-4096 tokens, 16 rows a KV head ... 107.5 us, 5.7 TB/s (84 %)
+//     128 blocks of 4 over 512-4096 tokens, 16 rows a KV head ... 106-108 us, 5.7-5.8 TB/s (85 %)
 //     32 single tokens over 16384-32768 tokens, 8 rows .......... 127 us, 6.3 TB/s (93 %)
-//     128 blocks of 8 over 512-4096 tokens, 32 rows ............. 154 us, 4.0 TB/s (60 %): lists' ends
-//     16 blocks of 32 over 8192-16384 tokens, 128 rows .......... 126 us, 3.3 TB/s: the softmax's latency
+//     128 blocks of 8 over 512-4096 tokens, 32 rows ............. 145 us, 4.3 TB/s (63 %): lists' ends
+//     16 blocks of 32 over 8192-16384 tokens, 128 rows .......... 122 us, 3.4 TB/s: the softmax's latency
 //     16 blocks of 64 over 8192-16384 tokens, 256 rows .......... 198 us, 1.05 PFLOP/s (55 %): MMAs and softmax in turn
-//     one block of 4 over 2000 tokens, 8 rows .................... 10.3 us, latency
+//     1024 single tokens over 100-1000 tokens, 4 rows ........... 195 us, 6.0 TB/s (89 %)
+//     one block of 4 over 2000 tokens, 8 rows .................... 10.2 us, latency
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -351,7 +352,7 @@ constexpr int kFewParts = 8;    // parts a list, about
 // u + 1 streams ahead of V of chunk u.
 //
 // Bound: HBM with up to 16 rows.  With 32, each list's end (the last weights, O^T out, the next queries) holds the one CTA
-// of an SM up for about a tile's time: 32 blocks of 8 over 2000-16000 tokens run at 4.9 TB/s, 128 over 512-4096 at 4.0.
+// of an SM up for about a tile's time: 32 blocks of 8 over 2000-16000 tokens run at 4.9 TB/s, 128 over 512-4096 at 4.3.
 
 // N: rows of the first MMAs, NC: rows that the softmax computes.
 template <int N, int NC, int STAGES>
@@ -1876,6 +1877,8 @@ Kv8AttnPlan plan_attention_kv8(int B, int L, int Hq, int Hkv, int max_pages, int
   pl.lsub = G * L <= 256 ? L : 256 / G;
   pl.row_groups = (L + pl.lsub - 1) / pl.lsub;
   pl.rows = G * pl.lsub;
+  // Rows that the MMAs take, the fewest that hold them: 16 rows (128 blocks of 4) in 107 us against 140 as 32, 32 (blocks of
+  // 8) in 145 against 219 as 128.
   pl.n_rows = pl.rows <= 16 ? 16 : pl.rows <= 32 ? 32 : pl.rows <= 128 ? 128 : 256;
   const bool many = pl.n_rows >= 128;
   const long long lists = static_cast<long long>(B) * Hkv * pl.row_groups;
@@ -1885,9 +1888,10 @@ Kv8AttnPlan plan_attention_kv8(int B, int L, int Hq, int Hkv, int max_pages, int
   // (a tile a list at most: no list is cut)
   pl.parts = max_pages <= kTilePages ? 0 : 2 * pl.grid;
   // Parts a list: about the CTAs over the lists.  With more lists than CTAs the CTA that writes a list's last part joins
-  // them, beside its copies (128 blocks of 4 over 512-4096 tokens: 113 us, 119 with a kernel for it); with fewer, whose
-  // parts are all written last, a kernel is as fast or faster (8 blocks of 4 over 500-1500: 17.4 us against 19.5).  Few
-  // lists of many parts take a CTA a row (one request of 6000 tokens: 16.7 us against 23 to 30).
+  // them, beside its copies (128 blocks of 4 over 512-4096 tokens: 107 us, 110 with a kernel for it; 1024 single tokens over
+  // 100-1000: 195 against 206); with fewer, whose parts are all written last, a kernel is faster (8 blocks of 4 over
+  // 500-1500: 13.8 us against 16.7; one request of 6000: 14.1 against 19.4).  Few lists of many parts take a CTA a row (that
+  // request: 16.7 us against 23 to 30 with few parts' kernel, before the rest was faster).
   pl.many_parts = lists * kFewParts < pl.grid;
   pl.join_here = pl.parts > 0 && !many && lists >= pl.grid;
   pl.work_bytes = pl.join_here ? (static_cast<size_t>(pl.grid) * (pl.n_rows / 16) + 1) * sizeof(int) : 0;
@@ -1957,6 +1961,7 @@ cudaError_t launch_attention_kv8(const Kv8AttnParams& a, const Kv8AttnPlan& pl, 
     e = pl.n_rows == 128 ? launch_many<1>(tq, tk, tv, p, pl.grid, stream) : launch_many<2>(tq, tk, tv, p, pl.grid, stream);
   } else {
     e = pl.n_rows == 32  ? launch_few<32, 32, 12>(tk, tv, p, pl.grid, stream)
+        // (eight rows: half the softmax; 1024 single tokens over 100-1000 tokens 195 us against 269, one block 10.2 against 11.2)
         : pl.rows <= 8 ? launch_few<16, 8, 6>(tk, tv, p, pl.grid, stream)
                        : launch_few<16, 16, 6>(tk, tv, p, pl.grid, stream);
   }
