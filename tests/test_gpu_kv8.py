@@ -336,3 +336,57 @@ def test_write_of_a_far_larger_maximum(lib):
     lib.bdlm_write_kv8(d, 2 ** 24 - 1, dev(first), 21, bf16_tensor(new), bf16_tensor(new), k, v, s, t, dev(np.array([5], np.int32)))
     assert np.array_equal(host(s), want[2]) and R.same_codes(host(k), want[0]) and R.same_codes(host(v), want[1])
     assert lib.bdlm_device_error() == 0
+
+
+@pytest.mark.parametrize("L,Hq,Hkv,B", [(2, 8, 2, 9), (8, 8, 2, 5), (16, 8, 2, 6), (64, 8, 2, 3), (40, 2, 1, 300), (3, 2, 1, 300)])
+@pytest.mark.parametrize("captured", [False, True])
+def test_attention_right_behind_what_wrote_its_inputs(lib, L, Hq, Hkv, B, captured):
+    """Lengths, tables, pages and queries that change from call to call, with nothing between their writers and the call
+    that reads them: the same as with the GPU idle before each call."""
+    import torch
+    rng = np.random.default_rng(L)
+    sets = []
+    for i in range(2):
+        c = Cache(rng, rng.integers(0, 60 + 500 * i, B) + L, Hkv)
+        new = [bf16_tensor(W._normal_bf16(rng, (B * L, Hkv, 128), 2.0 ** (3 * i))) for _ in range(2)]
+        sets.append((c, new, bf16_tensor(W._normal_bf16(rng, (B, L, Hq, 128), 1.0))))
+    cols, pages = max(c.cols for c, _, _ in sets), max(c.pages for c, _, _ in sets)
+    src = []
+    for c, new, q in sets:
+        t = np.full((B, cols), -1, np.int32)
+        t[:, :c.cols] = c.table
+        pad = lambda x: dev(np.concatenate([x, np.full((pages - c.pages,) + x.shape[1:], 127, x.dtype)]))
+        src.append([pad(c.k), pad(c.v), pad(c.scales), dev(t), dev(c.lens - L), *new, q])
+    d = lib.attn_desc(B, L, Hq, Hkv, 128, cols, pages)
+    at = [torch.empty_like(x) for x in src[0]]
+    steps = 8
+    outs = [torch.zeros((B, L, Hq, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2 * steps)]
+
+    def step(i, out, idle, stream=None):
+        k, v, s, t, n, nk, nv, q = at
+        for x, y in zip(at, src[i % 2]):
+            x.copy_(y)
+        if idle:
+            torch.cuda.synchronize()
+        lib.bdlm_write_kv8(d, L, None, 0, nk, nv, k, v, s, t, n, stream=stream)
+        if idle:
+            torch.cuda.synchronize()
+        lib.bdlm_attention_kv8(d, q, k, v, s, t, n, out, stream=stream)
+
+    for i in range(steps):
+        step(i, outs[i], True)
+    torch.cuda.synchronize()
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for i in range(steps):
+                step(i, outs[steps + i], False, torch.cuda.current_stream())
+        graph.replay()
+    else:
+        for i in range(steps):
+            step(i, outs[steps + i], False)
+    torch.cuda.synchronize()
+    for i in range(steps):
+        assert torch.equal(outs[i].view(torch.int16), outs[steps + i].view(torch.int16)), i
+    assert not torch.equal(outs[0].view(torch.int16), outs[1].view(torch.int16))
+    assert lib.bdlm_device_error() == 0
