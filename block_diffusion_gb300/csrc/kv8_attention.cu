@@ -757,13 +757,17 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
     const uint32_t tOx = tO + lane_off + static_cast<uint32_t>(c0);
     float2 l[CW / 2];
-    bool ok = true;
     int pcount = 0, n_list = -1;
-    for (int u = 0; ok; ++u) {
+    // The set meets at named barriers, which have no limit of their own.  So no warp leaves alone: one whose wait gives up
+    // goes on with what there is (the call fails, its results are void), and all leave where one has no chunk.
+    for (int u = 0;; ++u) {
       const int rs = u % kRing;
-      if (!(ok = wait_warp<true>(&bar_cfull[rs], (u / kRing) & 1, &abort_flag))) break;
-      const Chunk c = s_chunk[rs];
-      if (c.end) break;
+      const bool got = wait_warp<true>(&bar_cfull[rs], (u / kRing) & 1, &abort_flag);
+      Chunk c = s_chunk[rs];
+      if (!got || c.end) {
+        c.n_tiles = c.first = 0;
+        s_need[set][u & 1] = 2;
+      }
       if (c.first) {
         ++n_list;
 #pragma unroll
@@ -771,7 +775,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         if (x < CW) s_m[c0 + x] = -CUDART_INF_F;
       }
       const uint32_t tS = tmem + lane_off + static_cast<uint32_t>((u & 1) * kChunk * N + c0);
-      if (!(ok = wait_warp<true>(&bar_sfull[u & 1], (u >> 1) & 1, &abort_flag))) break;
+      if (c.n_tiles > 0) wait_warp<true>(&bar_sfull[u & 1], (u >> 1) & 1, &abort_flag);
       tc_fence_after();
       const float q_scale = s_qscale[n_list & 3];
       // the exact maxima of x over the chunk (behind the last token scores may be anything: -inf)
@@ -829,15 +833,16 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         } else if (mc - mo > kLazy) {
           alpha = ex2(mo - mc);
           s_m[n] = mc;
-          s_need[set][u & 1] = 1;
+          s_need[set][u & 1] |= 1;
         }
         s_alpha[n] = alpha;
       }
       named_barrier(own, 128);
-      const bool need = s_need[set][u & 1] != 0;
+      const int need = s_need[set][u & 1];
+      if (need > 1) break;
       if (!c.first && need) {
         // these rows of O^T and l to the new maxima
-        if (!(ok = wait_warp<true>(&bar_ofull[(u - 1) & 1], ((u - 1) >> 1) & 1, &abort_flag))) break;
+        wait_warp<true>(&bar_ofull[(u - 1) & 1], ((u - 1) >> 1) & 1, &abort_flag);
         tc_fence_after();
 #pragma unroll 1
         for (uint32_t col = 0; col < F::kWeights; col += NC < 16 ? 16 : N) {   // (eight rows: both parts at once)
@@ -863,7 +868,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         for (int n = 0; n < CW / 2; ++n) mr[n] = make_float2(kWeightExp - s_m[c0 + 2 * n], kWeightExp - s_m[c0 + 2 * n + 1]);
         uint32_t r[CW];
         load(0, r);
-        for (int j = 0; j < c.n_tiles && ok; ++j) {
+        for (int j = 0; j < c.n_tiles; ++j) {
           const float2 sc = s_scale[rs][j * kTilePages + (x >> 4)];
           const float a = sc.x * q_scale, sv = ex2(sc.y);
           ready(j, r);
@@ -887,7 +892,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
             lo[n] = o[0] | o[1] << 16;
           }
           const int pb = pcount & 1;
-          if (!(ok = wait_warp<true>(&bar_pempty[pb], ((pcount >> 1) & 1) ^ 1, &abort_flag))) break;
+          wait_warp<true>(&bar_pempty[pb], ((pcount >> 1) & 1) ^ 1, &abort_flag);
           uint8_t* to = sP + pb * F::kWeightBuf + set * (kTile * 16) + x * 16;
           if constexpr (CW == 8) {
             *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], lo[0], lo[1]);
@@ -900,36 +905,31 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
           mbar_arrive(&bar_pfull[pb]);
           ++pcount;
         }
-        if (!ok) tmem_wait_ld();   // (a load may be under way)
       }
-      if (!ok) break;
       tc_fence_before();
       mbar_arrive(&bar_sfree[u & 1]);
       if (c.last) {
         // The code from here on is met once a list, each time from memory: loops, not their bodies in a row.
-        if (!(ok = wait_warp<true>(&bar_ofull[u & 1], (u >> 1) & 1, &abort_flag))) break;
+        wait_warp<true>(&bar_ofull[u & 1], (u >> 1) & 1, &abort_flag);
         tc_fence_after();
-        // the rows' sums, through the weights' buffers (no MMA reads them now; a piece a set)
-        float* sums = reinterpret_cast<float*>(sP) + c0 * kTile;
+        // the rows' sums, through the set's own pieces of the weights' buffers (no MMA reads them now): four rows a piece
+        auto sums = [&](int n) { return reinterpret_cast<float*>(sP) + ((n >> 2) * F::kSets + set) * (4 * kTile) + (n & 3) * kTile; };
 #pragma unroll
         for (int n = 0; n < CW / 2; ++n) {
-          sums[(2 * n) * kTile + x] = l[n].x;
-          sums[(2 * n + 1) * kTile + x] = l[n].y;
+          sums(2 * n)[x] = l[n].x;
+          sums(2 * n + 1)[x] = l[n].y;
         }
         named_barrier(own, 128);
         {
           constexpr int kEach = 128 / CW;   // threads of a row
           float v = 0.f;
 #pragma unroll 4
-          for (int i = x % kEach; i < kTile; i += kEach) v += sums[(x / kEach) * kTile + i];
+          for (int i = x % kEach; i < kTile; i += kEach) v += sums(x / kEach)[i];
 #pragma unroll
           for (int off = kEach / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
           if (x % kEach == 0) s_l[c0 + x / kEach] = c.slot < 0 ? 1.f / v : v;
         }
-        if constexpr (F::kSets > 1)
-          named_barrier(1 + F::kSets, F::kSoft);   // before any set's next weights
-        else
-          named_barrier(own, 128);
+        named_barrier(own, 128);   // before the set's next weights
         const int first = c.rg * p.lsub + c0 / p.G;   // block position and head of row c0
         const int live = max(0, min(min(p.rows, (p.L - c.rg * p.lsub) * p.G) - c0, CW));   // rows of the set that there are
         const size_t row0 = (static_cast<size_t>(c.b) * p.L + first) * p.Hq + static_cast<size_t>(c.kvh) * p.G + c0 % p.G;
