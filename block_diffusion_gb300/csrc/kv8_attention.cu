@@ -21,13 +21,13 @@
 //    kernel behind (plan_attention_kv8).  So the work is even whatever the lengths.
 //
 // Bound: the codes, 256 bytes a token and KV head, come once from HBM.  Measured (a graph of calls):
-//     64 blocks of 2 over 2000-8000 tokens, 4 rows a KV head .... 106 us, 6.2 TB/s (91 % of the copy rate)
-//     128 blocks of 4 over 512-4096 tokens, 16 rows a KV head ... 106-108 us, 5.7-5.8 TB/s (85 %)
-//     32 single tokens over 16384-32768 tokens, 8 rows .......... 127 us, 6.3 TB/s (93 %)
+//     64 blocks of 2 over 2000-8000 tokens, 4 rows a KV head .... 103 us, 6.4 TB/s (94 % of the copy rate)
+//     128 blocks of 4 over 512-4096 tokens, 16 rows a KV head ... 107.5 us, 5.7 TB/s (84 %)
+//     32 single tokens over 16384-32768 tokens, 8 rows .......... 123 us, 6.6 TB/s (97 %)
 //     128 blocks of 8 over 512-4096 tokens, 32 rows ............. 145 us, 4.3 TB/s (63 %): lists' ends
 //     16 blocks of 32 over 8192-16384 tokens, 128 rows .......... 122 us, 3.4 TB/s: the softmax's latency
-//     16 blocks of 64 over 8192-16384 tokens, 256 rows .......... 198 us, 1.05 PFLOP/s (55 %): MMAs and softmax in turn
-//     1024 single tokens over 100-1000 tokens, 4 rows ........... 195 us, 6.0 TB/s (89 %)
+//     16 blocks of 64 over 8192-16384 tokens, 256 rows .......... 197 us, 1.05 PFLOP/s (55 %): MMAs and softmax in turn
+//     1024 single tokens over 100-1000 tokens, 4 rows ........... 198 us, 5.9 TB/s (88 %)
 //     one block of 4 over 2000 tokens, 8 rows .................... 10.2 us, latency
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -1960,10 +1960,14 @@ cudaError_t launch_attention_kv8(const Kv8AttnParams& a, const Kv8AttnPlan& pl, 
     if (e != cudaSuccess) return e;
     e = pl.n_rows == 128 ? launch_many<1>(tq, tk, tv, p, pl.grid, stream) : launch_many<2>(tq, tk, tv, p, pl.grid, stream);
   } else {
+    // Stages of 16 KB: two CTAs of four keep 128 KB an SM under way.  Six, all that fit, are slower where lists are long (32
+    // single tokens over 16384-32768 tokens 128.5 us against 122.7, 32 blocks of 4 over 2000-16000 99.7 against 95.8) and the
+    // same where they are short; three cost 2 to 4 %.  The one CTA of 32 rows takes twelve: 145 us for 128 blocks of 8
+    // over 512-4096, 147.6 with eight, the same on long lists.
     e = pl.n_rows == 32  ? launch_few<32, 32, 12>(tk, tv, p, pl.grid, stream)
         // (eight rows: half the softmax; 1024 single tokens over 100-1000 tokens 195 us against 269, one block 10.2 against 11.2)
-        : pl.rows <= 8 ? launch_few<16, 8, 6>(tk, tv, p, pl.grid, stream)
-                       : launch_few<16, 16, 6>(tk, tv, p, pl.grid, stream);
+        : pl.rows <= 8 ? launch_few<16, 8, 4>(tk, tv, p, pl.grid, stream)
+                       : launch_few<16, 16, 4>(tk, tv, p, pl.grid, stream);
   }
   if (e != cudaSuccess || pl.parts == 0 || pl.join_here) return e;
   if (pl.many_parts) return launch_pdl(join_many_kernel, dim3(lists, p.rows), dim3(kJoinThreads), 0, stream, p, pl.n_rows, pl.grid);
