@@ -207,6 +207,10 @@ __device__ __forceinline__ int q_exponent(float most) {
   return min(max(e, -110), 119);
 }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+// What scores of queries over 2^e are multiplied by, beside a page's sK: 2^e c, or 2^-86 where that is less.  Times the
+// least sK, 2^-40, it is a normal number then: a score of -inf (behind the last token) stays one, where 0 would make it
+// NaN.  Scores below it are 0 to within 2^25 2^40 2^-86 = 2^-21 either way.
+__device__ __forceinline__ float q_factor(float pow2_e, float scale_log2) { return fmaxf(pow2_e * scale_log2, 1.2924697071141057e-26f); }
 
 // A page's sK and log2 sV, as the softmax takes them (NaN counts as the smallest).
 __device__ __forceinline__ float2 page_scale(float2 s) {
@@ -619,7 +623,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         *reinterpret_cast<uint2*>(sQ + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
         *reinterpret_cast<uint2*>(sQ + N * 128 + at) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
       }
-      if (lane == 0) s_qscale[n_list & 3] = pow2(e) * p.scale_log2;
+      if (lane == 0) s_qscale[n_list & 3] = q_factor(pow2(e), p.scale_log2);
       fence_proxy_async_smem();
       __syncwarp();
       ++n_list;
@@ -1169,7 +1173,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       ++seq;
       const int rs = seq % kRing;
       if (have) {
-        c.q_scale = __ldg(p.q_scale + (static_cast<size_t>(c.b) * p.Hkv + c.kvh) * p.row_groups + c.rg) * p.scale_log2;
+        c.q_scale = q_factor(__ldg(p.q_scale + (static_cast<size_t>(c.b) * p.Hkv + c.kvh) * p.row_groups + c.rg), p.scale_log2);
       } else {
         c.end = 1;
       }

@@ -1,0 +1,42 @@
+"""Attention over the 8-bit cache for queries of zeros, of tiny values and of very different sizes."""
+import numpy as np
+import pytest
+
+import step_ref as R
+import workloads as W
+from test_gpu_kv8 import Cache, attend, f
+
+pytestmark = pytest.mark.gpu
+
+# query rows per KV head: 1, 8, 16, 32, 128, 255, 256
+ROWS = [(1, 2, 2), (4, 4, 2), (4, 8, 2), (8, 8, 2), (32, 8, 2), (64, 24, 6), (64, 8, 2)]
+
+
+@pytest.mark.parametrize("L,Hq,Hkv", ROWS)
+@pytest.mark.parametrize("size", [0.0, 2.0 ** -120])
+def test_queries_of_zeros(lib, L, Hq, Hkv, size):
+    """All queries of a sequence and KV head zero, or next to it: every token weighs the same, whatever pages the last
+    tile of 128 tokens lacks.  (Factors of 2^-110 and of a missing page's 2^-40 met as 0, and 0 times -inf.)"""
+    lens = [n for n in (65, 128, 129, 144, 240, 241, 16, 1000) if n >= L]
+    rng = np.random.default_rng(L + Hq)
+    c = Cache(rng, np.array(lens), Hkv)
+    c.scales[c.table[0, 0]] = 2.0 ** -40                  # a page of zeros, as the write makes it
+    c.k[c.table[0, 0]] = c.v[c.table[0, 0]] = 0
+    q = W._normal_bf16(rng, (len(lens), L, Hq, 128), 1.0)
+    q[:, :, :Hq // Hkv] = W.f32_to_bf16_bits(np.full(128, size, np.float32))
+    q[1] = q[0, 0, 0]
+    out = attend(lib, c, q, L, Hq, Hkv)
+    R.check_attention(f(out), R.attention_kv8(q, c.k, c.v, c.scales, c.table, c.lens - L, Hkv))
+    assert lib.bdlm_device_error() == 0
+
+
+@pytest.mark.parametrize("L,Hq,Hkv", ROWS)
+def test_a_tiny_softmax_scale(lib, L, Hq, Hkv):
+    """A scale next to zero does the same to any queries, over bad pages too."""
+    rng = np.random.default_rng(L + Hq + 1)
+    c = Cache(rng, np.array([70, 333, 1200]) + L, Hkv)
+    q = W._normal_bf16(rng, (3, L, Hq, 128), 1.0)
+    c.table[1, 2], c.table[2, 7] = -1, c.pages
+    out = attend(lib, c, q, L, Hq, Hkv, scale=1e-36)
+    R.check_attention(f(out), R.attention_kv8(q, c.k, c.v, c.scales, c.table, c.lens - L, Hkv, scale=1e-36))
+    assert lib.bdlm_device_error() == lib.BDLM_DEVERR_PAGE
