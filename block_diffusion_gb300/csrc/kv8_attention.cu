@@ -7,12 +7,15 @@
 //    float32), so nothing is widened on the way and a token costs 256 bytes of shared memory.  The
 //    other operand has 8 bits as well: q and p are held as two e4m3 parts each, the value rounded to four
 //    bits and what that leaves, rounded to four bits again.  A pair is off by 2^-8 of the value, as bf16
-//    is, and by no less than half its smallest step, 2^-18 of the largest value of what shares its power of
-//    two (a KV head's queries; a query's weights).  Both parts of an operand multiply the same codes into
-//    the same sums: twice the products of one part, at twice bf16's rate.
+//    is, and by no less than half its smallest step: of q 2^-18 of the largest value that shares its power of
+//    two (a KV head's queries), both parts into the same sums; of a weight 2^-23 of the query's largest in its
+//    chunk of tokens.  The weights' second part is 2^5 times itself, with sums apart, and every chunk's weights
+//    are taken to its own maximum: with one dominant token the others' are small, many, and all needed (held next to
+//    the list's maximum, without the 2^5, 32768 tokens beside one of 90 % came out two fifths too small).
+//    Twice the products of one part, at twice bf16's rate.
 //  * A page's scale of K is a factor of its scores.  Its scale of V goes into the weight: with
 //        x_t = c sK_t q . k_t + log2 sV_t    and its maximum m,
-//    w_t = 2^(x_t - m + 7) is what the second product takes (no sum ever meets a scale) and
+//    w_t = 2^(x_t - m + 8) is what the second product takes (no sum ever meets a scale) and
 //    sum w_t / sV_t is the divisor.  So w's parts keep their precision where it counts, whatever the
 //    scales are from page to page.
 //  * Work: the tiles of 128 tokens of all (sequence, KV head, row group) lists, end to end, are cut
@@ -48,9 +51,11 @@ constexpr int kTilePages = kTile / kPage;
 constexpr int kStage = kTile * 128;    // bytes of a tile's K or V
 constexpr int kRing = 4;               // chunk descriptors in flight
 constexpr int kAllTiles = 0x7FFFFFFF;  // a chunk as long as its list
-constexpr float kWeightExp = 7.0f;     // a query's largest weight is 2^7 ...
-constexpr float kLazy = 1.5f;          // ... to 2^8.5: a running maximum moves only when it rises by more (e4m3 ends at 448)
-constexpr float kLazyMany = 8.0f;      // the same where weights are float16: 1 to 2^8
+constexpr float kWeightExp = 8.0f;     // a query's largest weight of a chunk is 2^8 (e4m3 ends at 448) ...
+constexpr float kReach = 24.0f;        // ... or less: sums in a far lower power of two than the list's largest would overflow
+constexpr float kLowPart = 32.0f;      // the second part: of weights up to 2^8 the first leaves 2^3 at most
+constexpr float kWeightExpMany = 7.0f; // the same where weights are float16: 2^7 ...
+constexpr float kLazyMany = 8.0f;      // ... to 2^15: a running maximum moves only when it rises by more
 
 struct Params {
   const uint16_t* q;
@@ -377,13 +382,14 @@ struct Few {
   static constexpr size_t kSmem = 1024 + N * 256 + static_cast<size_t>(STAGES) * kStage + 2 * kWeightBuf;
 };
 
-// w's float16 pair in two e4m3 parts: each the low byte for the low one.
+// w's float16 pair in two e4m3 parts, the second kLowPart times itself (exact in float16): each the low byte for the low
+// one.
 __device__ __forceinline__ void split_half2(uint32_t w, uint32_t& hi, uint32_t& lo) {
   const __half2 h = *reinterpret_cast<const __half2*>(&w);
   hi = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(h), __NV_SATFINITE, __NV_E4M3);
   const __half2_raw back = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(hi), __NV_E4M3);
-  lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(__hsub2(h, *reinterpret_cast<const __half2*>(&back))), __NV_SATFINITE,
-                                  __NV_E4M3);
+  const __half2 rest = __hmul2(__hsub2(h, *reinterpret_cast<const __half2*>(&back)), __float2half2_rn(kLowPart));
+  lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(rest), __NV_SATFINITE, __NV_E4M3);
 }
 
 // Joins the parts of chunk c's list, in their order whoever comes last:
@@ -458,8 +464,8 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
   __shared__ int s_page[kRing][F::kChunkPages];       // page * Hkv + head
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
-  __shared__ __align__(16) float s_m[N], s_alpha[N], s_l[N], s_red[4][N];
-  __shared__ int s_need[F::kSets][2], s_join[F::kSets];
+  __shared__ __align__(16) float s_m[N], s_top[N], s_alpha[N], s_l[N], s_red[4][N];
+  __shared__ int s_leave[F::kSets][2], s_join[F::kSets];
   __shared__ float s_qscale[4];        // of a list's queries, times c: lists in turn (the softmax is two behind at most)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -483,7 +489,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       mbar_init(&bar_cempty[i], 2 + F::kSets);   // copies, second MMAs, softmax
     }
     abort_flag = 0;
-    for (int s = 0; s < F::kSets; ++s) s_need[s][0] = s_need[s][1] = 0;
+    for (int s = 0; s < F::kSets; ++s) s_leave[s][0] = s_leave[s][1] = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -770,13 +776,12 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       Chunk c = s_chunk[rs];
       if (!got || c.end) {
         c.n_tiles = c.first = 0;
-        s_need[set][u & 1] = 2;
+        s_leave[set][u & 1] = 1;
       }
       if (c.first) {
         ++n_list;
 #pragma unroll
         for (int n = 0; n < CW / 2; ++n) l[n] = make_float2(0.f, 0.f);
-        if (x < CW) s_m[c0 + x] = -CUDART_INF_F;
       }
       const uint32_t tS = tmem + lane_off + static_cast<uint32_t>((u & 1) * kChunk * N + c0);
       if (c.n_tiles > 0) wait_warp<true>(&bar_sfull[u & 1], (u >> 1) & 1, &abort_flag);
@@ -826,26 +831,19 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         }
       }
       named_barrier(own, 128);
-      if (x == 0) s_need[set][(u + 1) & 1] = 0;   // every reader of that slot is past this barrier
+      if (x == 0) s_leave[set][(u + 1) & 1] = 0;   // every reader of that slot is past this barrier
       if (x < CW) {
         const int n = c0 + x;
         const float mc = fmaxf(fmaxf(s_red[0][n], s_red[1][n]), fmaxf(s_red[2][n], s_red[3][n]));
-        const float mo = s_m[n];
-        float alpha = 1.f;
-        if (mo == -CUDART_INF_F) {
-          s_m[n] = mc;
-        } else if (mc - mo > kLazy) {
-          alpha = ex2(mo - mc);
-          s_m[n] = mc;
-          s_need[set][u & 1] |= 1;
-        }
-        s_alpha[n] = alpha;
+        const float top = c.first ? mc : fmaxf(mc, s_top[n]), m = fmaxf(mc, top - kReach);   // top: of the list so far
+        s_alpha[n] = ex2(s_m[n] - m);   // (not used of a first chunk)
+        s_top[n] = top;
+        s_m[n] = m;
       }
       named_barrier(own, 128);
-      const int need = s_need[set][u & 1];
-      if (need > 1) break;
-      if (!c.first && need) {
-        // these rows of O^T and l to the new maxima
+      if (s_leave[set][u & 1]) break;
+      if (!c.first) {
+        // these rows of O^T and l from the last chunk's power of two to this one's
         wait_warp<true>(&bar_ofull[(u - 1) & 1], ((u - 1) >> 1) & 1, &abort_flag);
         tc_fence_after();
 #pragma unroll 1
@@ -863,7 +861,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 #pragma unroll
         for (int n = 0; n < CW / 2; ++n) l[n] = __fmul2_rn(l[n], make_float2(s_alpha[c0 + 2 * n], s_alpha[c0 + 2 * n + 1]));
       }
-      // The weights, tile by tile, into shared memory.  2^(c sK q . k - m + 7) is what l adds up; times sV it is w, whose
+      // The weights, tile by tile, into shared memory.  2^(c sK q . k - m + 8) is what l adds up; times sV it is w, whose
       // float16 (finer than both parts, and exact to subtract from) is split.  (PV of the chunk's first tile waits for the
       // weights, and so for O's new maxima.)
       {
@@ -952,7 +950,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             if (n0 + k >= live) break;
-            const float o = __uint_as_float(r[k]) + __uint_as_float(r2[k]);
+            const float o = fmaf(__uint_as_float(r2[k]), 1.f / kLowPart, __uint_as_float(r[k]));
             if (c.slot < 0)
               p.out[row * 128 + x] = __bfloat16_as_ushort(__float2bfloat16_rn(o * s_l[c0 + n0 + k]));
             else
@@ -1451,7 +1449,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const uint32_t tOx = tO + lane_off + static_cast<uint32_t>(x * 128) + col0;
     bool ok = true;
     int u = 0, pair_ends = 0;
-    float m_run = -CUDART_INF_F, l_run = 0.f;   // l_run: this half's sum
+    float m_run = -CUDART_INF_F, l_run = 0.f;   // kWeightExpMany below a running maximum; this half's sum
     for (int cs = 0; ok; ++cs) {
       const int rs = cs % kRing;
       if (!(ok = wait_warp<SUB == 1>(&bar_cfull[rs], (cs / kRing) & 1, &abort_flag))) break;
@@ -1495,6 +1493,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         mx = fmaxf(s_hmax[u & 1][x][0][n], s_hmax[u & 1][x][1][n]);
         float alpha = 1.f;
         bool resc = false;
+        mx -= kWeightExpMany;
         if (m_run == -CUDART_INF_F) {
           m_run = mx;
         } else if (mx - m_run > kLazyMany) {
