@@ -7,8 +7,8 @@
 //    float32), so nothing is widened on the way and a token costs 256 bytes of shared memory.  The
 //    other operand has 8 bits as well: q and p are held as two e4m3 parts each, the value rounded to four
 //    bits and what that leaves, rounded to four bits again.  A pair is off by 2^-8 of the value, as bf16
-//    is, and by no less than half its smallest step: of q 2^-18 of the largest value that shares its power of
-//    two (a KV head's queries), both parts into the same sums; of a weight 2^-23 of the query's largest in its
+//    is, and by no less than half its smallest step: of q 2^-18 of the row's largest value (a row has a power of two
+//    of its own, so none depends on another), both parts into the same sums; of a weight 2^-23 of the query's largest in its
 //    chunk of tokens.  The weights' second part is 2^5 times itself, with sums apart, and every chunk's weights
 //    are taken to its own maximum: with one dominant token the others' are small, many, and all needed (held next to
 //    the list's maximum, without the 2^5, 32768 tokens beside one of 90 % came out two fifths too small).
@@ -67,7 +67,7 @@ struct Params {
   int* err;
   int* work;         // [0] CTAs finished, then parts written of the list that each unit's end cuts (join_here)
   const int* cum;    // [B + 1] tiles of the sequences before each (null: up to kFewSequences sequences)
-  const float* q_scale;   // many rows: 2^e of each row group's queries
+  const float* q_scale;   // many rows: 2^e of each query
   int B, L, Hq, Hkv, G, max_pages, num_pages, lsub, row_groups, rows;
   int join_here;     // the CTA that writes a list's last part joins them
   float scale_log2;
@@ -84,7 +84,6 @@ struct Chunk {
   int u0, parts;     // the list's first unit and its parts (slot >= 0)
   int final;         // the CTA's last chunk
   int end;           // no chunk: the CTA has no work
-  float q_scale;     // q = (hi + lo) * q_scale, times c (many rows)
 };
 
 __device__ __forceinline__ int kv_tokens(const Params& p, int b, bool* ok) {
@@ -196,13 +195,38 @@ __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// The largest of a few bf16 pairs' magnitudes as a float (NaN aside).
-__device__ __forceinline__ float magnitude(const uint4& w) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-  float m = 0.f;
+// The larger of two bf16 pairs, half by half (a NaN counts as nothing beside a number) ...
+__device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&m);
+}
+// ... and the magnitudes of eight values, as far as that goes.
+__device__ __forceinline__ uint32_t magnitude(const uint4& w) {
+  constexpr uint32_t kNoSign = 0x7FFF7FFFu;
+  return max_pair(max_pair(w.x & kNoSign, w.y & kNoSign), max_pair(w.z & kNoSign, w.w & kNoSign));
+}
+
+// The largest magnitude of R queries, 16 lanes a query: lane l has query l R / 16's.  (A shuffle for each two lanes and query
+// that are still apart, 15 for 16 queries instead of 64.)
+template <int R>
+__device__ __forceinline__ float rows_max(uint32_t (&m)[R], int lane) {
+  int left = R;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) m = fmaxf(m, fmaxf(fabsf(bf16_lo(u[k])), fabsf(bf16_hi(u[k]))));
-  return m;
+  for (int off = 8; off > 0; off >>= 1) {
+    const bool up = lane & off;
+    if (left > 1) {
+      left /= 2;
+#pragma unroll
+      for (int i = 0; i < R / 2; ++i) {
+        if (i >= left) break;
+        const uint32_t give = up ? m[i] : m[i + left], keep = up ? m[i + left] : m[i];
+        m[i] = max_pair(keep, __shfl_xor_sync(0xffffffffu, give, off));
+      }
+    } else {
+      m[0] = max_pair(m[0], __shfl_xor_sync(0xffffffffu, m[0], off));
+    }
+  }
+  return fmaxf(bf16_lo(m[0]), bf16_hi(m[0]));
 }
 
 // The power of two 2^e that takes a largest magnitude to 448 or less (and above 224 where it can).
@@ -466,7 +490,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
   __shared__ int abort_flag;
   __shared__ __align__(16) float s_m[N], s_top[N], s_alpha[N], s_l[N], s_red[4][N];
   __shared__ int s_leave[F::kSets][2], s_join[F::kSets];
-  __shared__ float s_qscale[4];        // of a list's queries, times c: lists in turn (the softmax is two behind at most)
+  __shared__ __align__(16) float s_qscale[4][N];   // of a list's rows, times c: lists in turn (the softmax is two behind at most)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -612,15 +636,16 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     // The list's queries in their two parts, once the MMAs on the last one's are done; the next one's are asked for, the
     // walk a list ahead of that.
     auto next_q = [&]() {
-      float most = 0.f;
+      constexpr int R = NC / 2;   // rows of each half of the warp
+      uint32_t most[R];
 #pragma unroll
-      for (int i = 0; i < NC / 2; ++i) most = fmaxf(most, magnitude(qr[i]));
-      const int e = q_exponent(warp_max(most));
-      const float inv = pow2(-e);
+      for (int i = 0; i < R; ++i) most[i] = magnitude(qr[i]);
+      const int e = q_exponent(rows_max(most, lane));
       if (!(ok = wait_warp<true>(&bar_qempty, (n_list & 1) ^ 1, &abort_flag))) return;
 #pragma unroll
       for (int i = 0; i < NC / 2; ++i) {
         const int n = 2 * i + (lane >> 4);
+        const float inv = __shfl_sync(0xffffffffu, pow2(-e), (lane & 16) | i * (16 / R));
         const uint32_t u[4] = {qr[i].x, qr[i].y, qr[i].z, qr[i].w};
         uint32_t hi[4], lo[4];
 #pragma unroll
@@ -629,7 +654,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         *reinterpret_cast<uint2*>(sQ + at) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
         *reinterpret_cast<uint2*>(sQ + N * 128 + at) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
       }
-      if (lane == 0) s_qscale[n_list & 3] = q_factor(pow2(e), p.scale_log2);
+      if (lane % (16 / R) == 0) s_qscale[n_list & 3][(lane & 15) / (16 / R) * 2 + (lane >> 4)] = q_factor(pow2(e), p.scale_log2);
       fence_proxy_async_smem();
       __syncwarp();
       ++n_list;
@@ -786,7 +811,9 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
       const uint32_t tS = tmem + lane_off + static_cast<uint32_t>((u & 1) * kChunk * N + c0);
       if (c.n_tiles > 0) wait_warp<true>(&bar_sfull[u & 1], (u >> 1) & 1, &abort_flag);
       tc_fence_after();
-      const float q_scale = s_qscale[n_list & 3];
+      float2 q_scale[CW / 2];   // of two rows each
+#pragma unroll
+      for (int n = 0; n < CW / 2; ++n) q_scale[n] = reinterpret_cast<const float2*>(s_qscale[n_list & 3] + c0)[n];
       // the exact maxima of x over the chunk (behind the last token scores may be anything: -inf)
       const int last_tile = (c.t_end - c.t0 - 1) / kTile;
       const bool cut = c.t_end - c.t0 - last_tile * kTile <= x;   // this thread's token of it is past the end
@@ -813,11 +840,11 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
           uint32_t r[CW];
           load(j, r);
           const float2 sc = s_scale[rs][j * kTilePages + (x >> 4)];
-          const float a = sc.x * q_scale;
           ready(j, r);
 #pragma unroll
           for (int n = 0; n < CW; n += 2) {
-            const float2 y = __ffma2_rn(make_float2(__uint_as_float(r[n]), __uint_as_float(r[n + 1])), make_float2(a, a), make_float2(sc.y, sc.y));
+            const float2 a = __fmul2_rn(q_scale[n / 2], make_float2(sc.x, sc.x));
+            const float2 y = __ffma2_rn(make_float2(__uint_as_float(r[n]), __uint_as_float(r[n + 1])), a, make_float2(sc.y, sc.y));
             mx[n] = fmaxf(mx[n], y.x);
             mx[n + 1] = fmaxf(mx[n + 1], y.y);
           }
@@ -872,12 +899,13 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
         load(0, r);
         for (int j = 0; j < c.n_tiles; ++j) {
           const float2 sc = s_scale[rs][j * kTilePages + (x >> 4)];
-          const float a = sc.x * q_scale, sv = ex2(sc.y);
+          const float sv = ex2(sc.y);
           ready(j, r);
           uint32_t w[CW / 2];   // float16 pairs
 #pragma unroll
           for (int n = 0; n < CW / 2; ++n) {
-            const float2 y = __ffma2_rn(make_float2(__uint_as_float(r[2 * n]), __uint_as_float(r[2 * n + 1])), make_float2(a, a), mr[n]);
+            const float2 a = __fmul2_rn(q_scale[n], make_float2(sc.x, sc.x));
+            const float2 y = __ffma2_rn(make_float2(__uint_as_float(r[2 * n]), __uint_as_float(r[2 * n + 1])), a, mr[n]);
             const float2 e = make_float2(ex2(y.x), ex2(y.y));
             l[n] = __fadd2_rn(l[n], e);
             const float2 z = __fmul2_rn(e, make_float2(sv, sv));
@@ -1170,11 +1198,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     auto publish = [&](Chunk& c, bool have) {
       ++seq;
       const int rs = seq % kRing;
-      if (have) {
-        c.q_scale = q_factor(__ldg(p.q_scale + (static_cast<size_t>(c.b) * p.Hkv + c.kvh) * p.row_groups + c.rg), p.scale_log2);
-      } else {
-        c.end = 1;
-      }
+      if (!have) c.end = 1;
       if (ok) ok = wait_warp<SUB == 1>(&bar_cempty[rs], ((seq / kRing) & 1) ^ 1, &abort_flag);
       if (have) pages.give(s_page[seq % 3], s_scale[rs], lane);
       __syncwarp();
@@ -1444,6 +1468,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const int n = (q4 << 5) | lane;
     const int pq = x * 4 + q4;   // the two halves' exchange barriers
     const int r_item = x * 128 + n;
+    const int r_off = r_item / p.G * p.Hq + r_item % p.G;   // from the group's first row of q and the output
     const uint32_t lane_off = static_cast<uint32_t>(q4 * 32) << 16;
     const uint32_t col0 = static_cast<uint32_t>(half * 64);
     const uint32_t tOx = tO + lane_off + static_cast<uint32_t>(x * 128) + col0;
@@ -1453,19 +1478,23 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     for (int cs = 0; ok; ++cs) {
       const int rs = cs % kRing;
       if (!(ok = wait_warp<SUB == 1>(&bar_cfull[rs], (cs / kRing) & 1, &abort_flag))) break;
-      const Chunk c = s_chunk[rs];
-      if (c.end) break;
-      if (c.first) {
+      const Chunk& at = s_chunk[rs];   // (what every tile needs is read once; a copy of all would take registers)
+      const int n_tiles = at.n_tiles, t0 = at.t0, t_end = at.t_end;
+      if (at.end) break;
+      if (at.first) {
         m_run = -CUDART_INF_F;
         l_run = 0.f;
       }
-      for (int j = 0; j < c.n_tiles; ++j, ++u) {
+      const size_t row0 = (static_cast<size_t>(at.b) * p.L + at.rg * p.lsub) * p.Hq + static_cast<size_t>(at.kvh) * p.G;
+      const bool live = r_item < min(p.rows, (p.L - at.rg * p.lsub) * p.G);
+      const float q_scale = q_factor(__ldcg(p.q_scale + row0 + (live ? r_off : 0)), p.scale_log2);   // q = (hi + lo) * q_scale, times c
+      for (int j = 0; j < n_tiles; ++j, ++u) {
         const uint32_t tSx = tmem + lane_off + static_cast<uint32_t>((SUB == 2 ? x : u & 1) * 128) + col0;
         ok = SUB == 2 ? wait_warp<SUB == 1>(&bar_sfull[x], u & 1, &abort_flag)
                       : wait_warp<SUB == 1>(&bar_sfull[u & 1], (u >> 1) & 1, &abort_flag);
         if (!ok) break;
         tc_fence_after();
-        const int nvalid = min(kTile, c.t_end - (c.t0 + j * kTile)) - half * 64;   // of this half's columns
+        const int nvalid = min(kTile, t_end - (t0 + j * kTile)) - half * 64;   // of this half's columns
         const float2* scales = &s_scale[rs][j * kTilePages + half * 4];
         if (nvalid < 64) {   // scores behind the last token may be anything: -inf
 #pragma unroll 1
@@ -1485,7 +1514,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
           tmem_wait_ld();
           tmem_regs_ready(*reinterpret_cast<uint32_t(*)[16]>(r));
           tmem_regs_ready(*reinterpret_cast<uint32_t(*)[16]>(r + 16));
-          mx = fmax3(mx, fmaf(max16(r), s0.x * c.q_scale, s0.y), fmaf(max16(r + 16), s1.x * c.q_scale, s1.y));
+          mx = fmax3(mx, fmaf(max16(r), s0.x * q_scale, s0.y), fmaf(max16(r + 16), s1.x * q_scale, s1.y));
         }
         s_hmax[u & 1][x][half][n] = mx;
         mbar_arrive(&bar_pair[pq][u & 1]);
@@ -1514,7 +1543,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             const float2 s = scales[2 * g2 + g];
-            const float a = s.x * c.q_scale, b = s.y - m_run;
+            const float a = s.x * q_scale, b = s.y - m_run;
             const float2 a2 = make_float2(a, a), b2 = make_float2(b, b);
             float2 t2 = make_float2(0.f, 0.f);   // (a tree's partial sums would be spilled)
 #pragma unroll
@@ -1548,7 +1577,7 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&bar_pfull[SUB == 2 ? x : u & 1]);
-        if (!c.last || j != c.n_tiles - 1) continue;
+        if (!at.last || j != n_tiles - 1) continue;
         // ---- this half of the row of O, divided by the row's sum or as a part
         if (!(ok = wait_warp<SUB == 1>(&bar_ofull[u & 1], (u >> 1) & 1, &abort_flag))) break;
         tc_fence_after();
@@ -1557,10 +1586,8 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         if (!(ok = wait_warp<SUB == 1>(&bar_pair_end[pq], pair_ends & 1, &abort_flag))) break;
         const float l_row = s_hsum[x][0][n] + s_hsum[x][1][n];
         ++pair_ends;
-        const int i_row = c.rg * p.lsub + r_item / p.G;
-        const bool live = r_item < p.rows && i_row < p.L;
         uint8_t* stage = s_stage[warp - F::kSoftmax0];
-        if (c.slot < 0) {
+        if (at.slot < 0) {
           const float inv = 1.f / l_row;
           uint32_t w[32];
 #pragma unroll
@@ -1575,10 +1602,10 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
               w[8 * g + k] = *reinterpret_cast<const uint32_t*>(&h2);
             }
           }
-          uint16_t* dst = p.out + ((static_cast<size_t>(c.b) * p.L + i_row) * p.Hq + static_cast<size_t>(c.kvh) * p.G + r_item % p.G) * 128 + col0;
+          uint16_t* dst = p.out + (row0 + r_off) * 128 + col0;
           store_rows(w, live ? dst : nullptr, stage, lane);
         } else {
-          float* mine = p.part + static_cast<size_t>(c.slot) * kRowsItem * kPartRow;
+          float* mine = p.part + static_cast<size_t>(at.slot) * kRowsItem * kPartRow;
 #pragma unroll
           for (int g2 = 0; g2 < 2; ++g2) {
             uint32_t o[32];
@@ -1612,50 +1639,36 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   if (threadIdx.x == 0 && abort_flag) atomicOr(p.err, BDLM_DEVERR_TIMEOUT);
 }
 
-// The queries of each (sequence, KV head, row group) as two e4m3 parts of 128 bytes side by side, with the power of
-// two that they share.  A CTA a group, its queries in registers between the two steps.
-constexpr int kSplitThreads = 512;
+// The queries as two e4m3 parts of 128 bytes side by side, with each one's power of two: 16 lanes a query, kSplitEach of
+// them under way a thread.
+constexpr int kSplitThreads = 256, kSplitEach = 4;
 __global__ void __launch_bounds__(kSplitThreads) split_q_kernel(const Params p, uint8_t* __restrict__ q8, float* __restrict__ q_scale) {
-  constexpr int kEach = 256 * 16 / kSplitThreads;   // pieces of eight values of a thread
-  __shared__ float s_most[kSplitThreads / 32];
   griddep_wait();
   griddep_launch_dependents();
-  const int t = threadIdx.x, lane = t & 31;
-  const int lists = p.Hkv * p.row_groups;
-  const int b = blockIdx.x / lists, list = blockIdx.x - b * lists;
-  const int rg = list % p.row_groups, kvh = list / p.row_groups;
-  const int l0 = rg * p.lsub, rows = min(p.lsub, p.L - l0) * p.G;
-  auto at = [&](int n) {   // of row n, in rows of 128 values
-    return (static_cast<size_t>(b) * p.L + l0 + n / p.G) * p.Hq + static_cast<size_t>(kvh) * p.G + n % p.G;
-  };
-  uint4 v[kEach];
+  const int t = threadIdx.x;
+  const long long rows = static_cast<long long>(p.B) * p.L * p.Hq;
+  const long long row0 = static_cast<long long>(blockIdx.x) * (kSplitThreads / 16 * kSplitEach) + (t >> 4);
+  uint4 v[kSplitEach];
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int o = i * kSplitThreads + t;
+  for (int i = 0; i < kSplitEach; ++i) {
+    const long long row = row0 + i * (kSplitThreads / 16);
     v[i] = make_uint4(0, 0, 0, 0);
-    if (o < rows * 16) v[i] = __ldg(reinterpret_cast<const uint4*>(p.q + at(o >> 4) * 128) + (o & 15));
+    if (row < rows) v[i] = __ldg(reinterpret_cast<const uint4*>(p.q + row * 128) + (t & 15));
   }
-  float most = 0.f;
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) most = fmaxf(most, magnitude(v[i]));
-  most = warp_max(most);
-  if (lane == 0) s_most[t >> 5] = most;
-  __syncthreads();
-  most = warp_max(s_most[lane % (kSplitThreads / 32)]);
-  const int e = q_exponent(most);
-  const float inv = pow2(-e);
-  if (t == 0) q_scale[blockIdx.x] = pow2(e);
-#pragma unroll
-  for (int i = 0; i < kEach; ++i) {
-    const int o = i * kSplitThreads + t;
-    if (o >= rows * 16) break;
-    const size_t row = at(o >> 4);
+  for (int i = 0; i < kSplitEach; ++i) {
+    const long long row = row0 + i * (kSplitThreads / 16);
+    uint32_t most[1] = {magnitude(v[i])};
+    const int e = q_exponent(rows_max(most, t & 31));
+    if (row >= rows) continue;
+    const float inv = pow2(-e);
+    if ((t & 15) == 0) q_scale[row] = pow2(e);
     const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) split_e4m3x2(bf16_lo(u[k]) * inv, bf16_hi(u[k]) * inv, hi[k], lo[k]);
-    *reinterpret_cast<uint2*>(q8 + row * 256 + (o & 15) * 8) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-    *reinterpret_cast<uint2*>(q8 + row * 256 + 128 + (o & 15) * 8) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+    *reinterpret_cast<uint2*>(q8 + row * 256 + (t & 15) * 8) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+    *reinterpret_cast<uint2*>(q8 + row * 256 + 128 + (t & 15) * 8) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
   }
 }
 
@@ -1907,7 +1920,7 @@ Kv8AttnPlan plan_attention_kv8(int B, int L, int Hq, int Hkv, int max_pages, int
   pl.bytes = pl.part_bytes;
   pl.cum_offset = place(pl.bytes, B > kFewSequences ? (static_cast<size_t>(B) + 1) * sizeof(int) : 0);
   pl.q_offset = place(pl.bytes, many ? static_cast<size_t>(B) * L * Hq * 256 : 0);
-  pl.q_scale_offset = place(pl.bytes, many ? static_cast<size_t>(lists) * sizeof(float) : 0);
+  pl.q_scale_offset = place(pl.bytes, many ? static_cast<size_t>(B) * L * Hq * sizeof(float) : 0);
   return pl;
 }
 
@@ -1958,7 +1971,9 @@ cudaError_t launch_attention_kv8(const Kv8AttnParams& a, const Kv8AttnPlan& pl, 
     p.cum = cum;
   }
   if (pl.n_rows >= 128) {
-    e = launch_pdl(split_q_kernel, dim3(lists), dim3(kSplitThreads), 0, stream, p, reinterpret_cast<uint8_t*>(at + pl.q_offset),
+    constexpr long long kRows = kSplitThreads / 16 * kSplitEach;
+    const unsigned ctas = static_cast<unsigned>((static_cast<long long>(p.B) * p.L * p.Hq + kRows - 1) / kRows);
+    e = launch_pdl(split_q_kernel, dim3(ctas), dim3(kSplitThreads), 0, stream, p, reinterpret_cast<uint8_t*>(at + pl.q_offset),
                    reinterpret_cast<float*>(at + pl.q_scale_offset));
     if (e != cudaSuccess) return e;
     e = pl.n_rows == 128 ? launch_many<1>(tq, tk, tv, p, pl.grid, stream) : launch_many<2>(tq, tk, tv, p, pl.grid, stream);

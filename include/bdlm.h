@@ -586,11 +586,13 @@ int bdlm_write_kv8(const bdlm_attn_desc* desc, int n_tokens, const int32_t* firs
 /*
  * Block attention over the 8-bit cache: bdlm_block_attention with K and V as bdlm_write_kv8 holds
  * them.  L = 1 is single-token decoding.  Scales outside [2^-40, 2^40] count as the nearest of the two, NaN
- * as 2^-40; any others are taken as they are, powers of two or not.  A page with a bad id reads as zeros.  A
- * softmax weight times its page's scale of V is held within 2^-7.8 of itself or, where that is more, 2^-23 of the
- * row's largest such number among the 896 tokens that it is taken with (over 32 query rows per KV head: 2^-11, or
- * 2^-32 of the row's largest); sums, maxima and the divisor are float32.  q, out
- * [B, L, Hq, D] bf16 (16-byte aligned), q finite, and all else as bdlm_block_attention.  num_pages * Hkv >=
+ * as 2^-40; any others are taken as they are, powers of two or not.  A page with a bad id reads as zeros.
+ * What is held in fewer than float32's bits: an element of q within 2^-8 of itself or, where that is more, 2^-18 of the
+ * largest of its query; a softmax weight times its page's scale of V within 2^-7.8 of itself or 2^-23 of the
+ * query's largest such number among the up to 896 tokens that it is taken with, or 2^-47 of its largest of all (over 32
+ * query rows per KV head: 2^-11 of itself, or 2^-32 of the query's largest).  Queries do not depend on one another: one
+ * that is not finite has no defined output, and changes no other's.
+ * q, out [B, L, Hq, D] bf16 (16-byte aligned), and all else as bdlm_block_attention.  num_pages * Hkv >=
  * 2^30 or max_pages_per_seq > 2^26 returns BDLM_ERR_UNSUPPORTED.
  */
 int bdlm_attention_kv8(const bdlm_attn_desc* desc, const bdlm_bf16* q, const bdlm_e4m3* k_pages,

@@ -5,6 +5,7 @@ import pytest
 import step_ref as R
 import workloads as W
 from test_gpu_kv8 import Cache, attend, f
+from test_gpu_kv8_tails import SCALE, tolerance
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +41,37 @@ def test_a_tiny_softmax_scale(lib, L, Hq, Hkv):
     out = attend(lib, c, q, L, Hq, Hkv, scale=1e-36)
     R.check_attention(f(out), R.attention_kv8(q, c.k, c.v, c.scales, c.table, c.lens - L, Hkv, scale=1e-36))
     assert lib.bdlm_device_error() == lib.BDLM_DEVERR_PAGE
+
+
+@pytest.mark.parametrize("L,Hq,Hkv", [(2, 8, 2), (4, 8, 2), (8, 8, 2), (32, 8, 2), (33, 24, 6), (64, 16, 4), (40, 32, 2)])
+@pytest.mark.parametrize("huge", [3000.0, 1e30, np.inf, np.nan])
+def test_a_row_keeps_out_of_the_others(lib, L, Hq, Hkv, huge):
+    """Rows that share a KV head, one or all heads of a position with values far from the others' (a padded slot's, say),
+    others far smaller: each row comes out as if it were alone."""
+    rng = np.random.default_rng(L * Hq)
+    G, lens = Hq // Hkv, np.array([50, 777, 2100])
+    c = Cache(rng, lens + L, Hkv)
+    x = rng.normal(size=(3, L, Hq, 128)).astype(np.float32)
+    x[:, :, 1] *= 2.0 ** -6
+    x[:, -1] *= huge
+    x[0, 0, 0, 3] = huge
+    q = W.f32_to_bf16_bits(x)
+    x = R.f64(q)
+    apart = (~np.isfinite(x) | (np.abs(x) > 100)).any(-1)
+    assert apart.any() and not apart.all()
+    got = f(attend(lib, c, q, L, Hq, Hkv))
+    for b, n in enumerate(c.lens):
+        ids = c.table[b, :(n + 15) // 16]
+        for g in range(Hkv):
+            rows = ~apart[b, :, g * G:(g + 1) * G].reshape(-1)
+            if not rows.any():
+                continue
+            kk, codes = (R.E4M3[t[ids, g]].reshape(-1, 128)[:n] for t in (c.k, c.v))
+            sk, sv = (np.repeat(c.scales[ids, g, i].astype(np.float64), 16)[:n] for i in range(2))
+            kk = kk * sk[:, None]
+            qq = x[b, :, g * G:(g + 1) * G].reshape(-1, 128)[rows]
+            p = np.exp(qq @ kk.T * SCALE)
+            p /= p.sum(1, keepdims=True)
+            out = (p * sv) @ codes
+            excess = np.abs(got[b, :, g * G:(g + 1) * G].reshape(-1, 128)[rows] - out) - tolerance(qq, kk, codes, sv, p, out, L * G <= 32)
+            assert excess.max() <= 0, (b, g, excess.max())
