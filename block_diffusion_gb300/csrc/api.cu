@@ -995,14 +995,15 @@ int bdlm_rotary_init(bdlm_rotary_desc* rotary, int rot_dim, int interleaved, dou
     return BDLM_ERR_INVALID;
   const double pi = 3.14159265358979323846;
   if (scaling == BDLM_ROTARY_BASE) base *= pow(factor, rot_dim / (rot_dim - 2.0));
-  // YARN: the pairs where a turn count would be `many` and `few`, rounded outwards
+  // YARN: the pairs where a turn count would be `many` and `few`, rounded outwards, within 0 .. rot_dim - 1.  (The upper
+  // one may lie past the last pair, rot_dim / 2 - 1: where that still makes more than `few` turns it keeps its part.)
   const auto pair_of = [&](double turns) {
     return rot_dim * log(original_len / (turns * 2.0 * pi)) / (2.0 * log(base));
   };
   double low = 0.0, high = 0.0;
   if (scaling == BDLM_ROTARY_YARN) {
     low = fmax(floor(pair_of(many)), 0.0);
-    high = fmin(ceil(pair_of(few)), rot_dim / 2 - 1.0);
+    high = fmin(ceil(pair_of(few)), rot_dim - 1.0);
   }
   *rotary = bdlm_rotary_desc{};
   rotary->rot_dim = rot_dim;

@@ -507,8 +507,10 @@ enum {
                               last one's frequency divided by factor */
   BDLM_ROTARY_BANDS = 3,   /* by the turns t_i = original_len * f_i / 2 pi of a pair: f_i for t_i >=
                               many, f_i / factor for t_i <= few, between them linear in t_i */
-  BDLM_ROTARY_YARN = 4     /* the same, but linear in i between the pairs, rounded outwards, where t_i
-                              would be many and few; amplitude 0.1 ln(factor) + 1 */
+  BDLM_ROTARY_YARN = 4     /* the same, but linear in i between the pairs, rounded outwards and kept within
+                              0 .. rot_dim - 1, where t_i would be many and few (the last pair is
+                              rot_dim / 2 - 1: over a long original_len it keeps a part of its frequency);
+                              amplitude 0.1 ln(factor) + 1 */
 };
 
 /* Frequencies of rotary positions, in host memory (filled by bdlm_rotary_init). */
