@@ -986,7 +986,7 @@ int bdlm_rotary_init(bdlm_rotary_desc* rotary, int rot_dim, int interleaved, dou
                      double amplitude) {
   if (!rotary || rot_dim < 16 || rot_dim > 128 || rot_dim % 16 != 0 || !(base > 1.0) || !isfinite(base) ||
       scaling < BDLM_ROTARY_NONE || scaling > BDLM_ROTARY_YARN || !(amplitude >= 0.0) ||
-      amplitude > 3e38)   // (it is kept as a float)
+      amplitude > 3e38 || (amplitude > 0.0 && amplitude < 1.2e-38))   // (it is kept as a float)
     return BDLM_ERR_INVALID;
   if (scaling != BDLM_ROTARY_NONE && (!(factor >= 1.0) || !isfinite(factor))) return BDLM_ERR_INVALID;
   const bool by_turns = scaling == BDLM_ROTARY_BANDS || scaling == BDLM_ROTARY_YARN;

@@ -524,7 +524,7 @@ typedef struct {
  * Fills *rotary (host memory; no GPU is touched) with f_i = base^(-2 i / rot_dim), i < rot_dim / 2,
  * scaled as `scaling` says.  rot_dim: a multiple of 16, 16 .. 128; base > 1; factor >= 1 and
  * original_len > 0 where `scaling` uses them; 0 < few < many for BANDS and YARN.  amplitude: a number
- * > 0 (at most 3e38), or 0 for the one that belongs to the scaling (1, or YARN's).
+ * from 1.2e-38 to 3e38, or 0 for the one that belongs to the scaling (1, or YARN's).
  */
 int bdlm_rotary_init(bdlm_rotary_desc* rotary, int rot_dim, int interleaved, double base,
                      int scaling, double factor, double original_len, double few, double many,

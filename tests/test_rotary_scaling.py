@@ -60,3 +60,13 @@ def test_bands(bd, length):
     keep = np.interp(length * own / (2 * math.pi), [1.0, 4.0], [0.0, 1.0])
     want = own * (keep + (1 - keep) / 8)
     assert np.all(np.abs(frequencies(r) - want) <= 1e-12 * want + 1e-18)
+
+
+@pytest.mark.parametrize("amplitude", [1e-300, 1e-50, 1e-46, 1e-39])
+def test_an_amplitude_that_no_float_holds_is_refused(bd, amplitude):
+    """It would be 0, and so would all results, or have few bits left."""
+    with pytest.raises(bd.BdlmError) as e:
+        bd.bdlm_rotary_init(64, False, 10000.0, amplitude=amplitude)
+    assert e.value.status == bd.BDLM_ERR_INVALID
+    for good in (1.2e-38, 0.5, 3e38):
+        assert bd.bdlm_rotary_init(64, False, 10000.0, amplitude=good).amplitude == np.float32(good)
