@@ -574,6 +574,10 @@ typedef uint8_t bdlm_e4m3;   /* raw e4m3 bits (no infinities; 0x7F and 0xFF are 
  * at most +-448.  Tokens before prefix_lens[b] in the first such page are held anew in its new scale
  * (exactly, where the old one was a power of two and no value falls below the smallest step); slots behind
  * the last new token are left as they were.  A page that gets new tokens belongs to one sequence.
+ * So drafts of a block that are written over one another can cost the committed tokens of its first page bits: each of
+ * their values is off by 2^-10 of the largest scale that the page has had at most (2^-17.8 of the largest draft value,
+ * or less), and stays so when the scale comes down again.  Where drafts may hold outliers far above 2^10 times
+ * what has to last, write them when they are committed, or the page's committed tokens again from bf16.
  *   k_new, v_new  [B * n_tokens, or n_rows, Hkv, D] bf16 (16-byte aligned)
  *   first         [B + 1] int32, or NULL (n_rows is not used then)
  * A bad page id or a length that does not fit the page table skips what it concerns and sets a device
