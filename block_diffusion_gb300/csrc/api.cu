@@ -1065,7 +1065,7 @@ int bdlm_rotary(const bdlm_attn_desc* desc, const bdlm_rotary_desc* rotary, int 
   p.Hkv = k ? d.Hkv : 0;
   p.rows = static_cast<long long>(d.B) * n_tokens;
   p.inverse = inverse != 0;
-  return bdlm::launch_rotary(p, *rotary, st->num_sms, static_cast<cudaStream_t>(stream)) == cudaSuccess
+  return bdlm::launch_rotary(p, *rotary, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? BDLM_OK
              : BDLM_ERR_CUDA;
 }

@@ -4,13 +4,12 @@
 // head that shares a scale is 2 KB in one piece.  scales [num_pages, Hkv, 2] holds K's and V's: a value is
 // its code times its scale.
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
 #include <stdint.h>
 
 #include "kernels.h"
-#include "ptx.cuh"
+#include "ptx_kv8.cuh"
 #include "step_ops.h"
 
 namespace bdlm {
@@ -31,21 +30,6 @@ constexpr int kPage = 16;
 // pairs: as 64 floats a lane fewer pages were under way (100 us).  A block's write (128 pages) is latency, 5.3 us.
 constexpr int kWriteWarps = 8;
 constexpr int kScaleExp = 40;
-
-// The scale's exponent for a largest magnitude (0 and up, not NaN).
-__device__ __forceinline__ int scale_exponent(float most) {
-  const uint32_t bits = __float_as_uint(most);
-  const int e = static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);   // 448 = 1.75 * 2^8
-  return min(max(e, -kScaleExp), kScaleExp);
-}
-
-__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-}
-__device__ __forceinline__ float2 from_e4m3x2(uint32_t w) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w), __NV_E4M3);
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
-}
 
 // Largest magnitude of the warp's bf16 pairs (a NaN counts as nothing).
 __device__ __forceinline__ float most_of(uint32_t top) {
@@ -137,7 +121,7 @@ write_kv8_kernel(const WriteKv8Params p, int max_touched) {
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(m));
     most = fmaxf(most, m);
   }
-  const int e = scale_exponent(most);
+  const int e = min(max(e4m3_exponent(most), -kScaleExp), kScaleExp);
   const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {

@@ -33,7 +33,6 @@
 //     1024 single tokens over 100-1000 tokens, 4 rows ........... 198 us, 5.9 TB/s (88 %)
 //     one block of 4 over 2000 tokens, 8 rows .................... 10.2 us, latency
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
 #include <stdint.h>
@@ -176,13 +175,6 @@ struct Before {
   }
 };
 
-__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-}
-__device__ __forceinline__ float2 from_e4m3x2(uint32_t w) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w), __NV_E4M3);
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
-}
 // a and b in two e4m3 parts: each the low half for a, the high one for b.
 __device__ __forceinline__ void split_e4m3x2(float a, float b, uint32_t& hi, uint32_t& lo) {
   hi = e4m3x2(a, b);
@@ -230,11 +222,7 @@ __device__ __forceinline__ float rows_max(uint32_t (&m)[R], int lane) {
 }
 
 // The power of two 2^e that takes a largest magnitude to 448 or less (and above 224 where it can).
-__device__ __forceinline__ int q_exponent(float most) {
-  const uint32_t bits = __float_as_uint(most);
-  const int e = static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-  return min(max(e, -110), 119);
-}
+__device__ __forceinline__ int q_exponent(float most) { return min(max(e4m3_exponent(most), -110), 119); }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 // What scores of queries over 2^e are multiplied by, beside a page's sK: 2^e c, or 2^-86 where that is less.  Times the
 // least sK, 2^-40, it is a normal number then: a score of -inf (behind the last token) stays one, where 0 would make it
@@ -628,7 +616,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     // One warp each for the first and the second MMAs: a warp that issued both was busy with it for most of the time (128
     // blocks of 8 over 512-4096 tokens: 158 us against 153), and stood still for one's operands where it could have issued
     // the other's.
-    constexpr uint32_t kIdescS = idesc_e4m3_f32(128, N, false, false);
+    constexpr uint32_t kIdescS = idesc_format0_f32(128, N, false, false);
     const uint64_t q_desc = smem_desc(smem_u32(sQ), 16, 1024), k_desc = smem_desc(smem_u32(sKV), 16, 1024);
     bool ok = true;
     int st = 0, n_list = 0;
@@ -699,7 +687,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
     __syncwarp();
   } else if (warp == F::kSecondWarp) {
     // =================================================================== second MMAs
-    constexpr uint32_t kIdescO = idesc_e4m3_f32(128, F::kWeights, true, true);
+    constexpr uint32_t kIdescO = idesc_format0_f32(128, F::kWeights, true, true);
     const uint64_t v_desc = smem_desc(smem_u32(sKV), kStage, 1024), p_desc = smem_desc_plain(smem_u32(sP), 128, kTile * 16);
     bool ok = wait_warp<true>(&bar_cfull[0], 0, &abort_flag);
     int st = 0, pcount = 0;
@@ -1274,8 +1262,8 @@ many_rows_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   } else if (warp == 1) {
     // =================================================================== MMA issuer
     {
-      constexpr uint32_t kIdescS = idesc_e4m3_f32(128, 128, false, false);
-      constexpr uint32_t kIdescO = idesc_f16_f32(128, 128, false, true);
+      constexpr uint32_t kIdescS = idesc_format0_f32(128, 128, false, false);
+      constexpr uint32_t kIdescO = idesc_format0_f32(128, 128, false, true);
       const uint64_t q_desc = smem_desc(smem_u32(sQ), 16, 1024), k_desc = smem_desc(smem_u32(sK), 16, 1024);
       const uint64_t w_desc = smem_desc(smem_u32(sW), kStage, 1024);
       bool ok = true;
@@ -1692,7 +1680,7 @@ __global__ void __launch_bounds__(kCumThreads) cum_tiles_kernel(const Params p, 
     }
     if (lane == 31) s_warp[warp] = incl;
     __syncthreads();
-    int w = lane < 32 ? s_warp[lane] : 0;
+    int w = s_warp[lane];
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
       const int v = __shfl_up_sync(0xffffffffu, w, off);

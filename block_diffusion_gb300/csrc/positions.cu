@@ -378,7 +378,7 @@ cudaError_t launch_build_tables(const TableParams& p, cudaStream_t stream) {
                     stream, p, wide);
 }
 
-cudaError_t launch_rotary(const RotaryParams& p, const bdlm_rotary_desc& r, int num_sms, cudaStream_t stream) {
+cudaError_t launch_rotary(const RotaryParams& p, const bdlm_rotary_desc& r, cudaStream_t stream) {
   const unsigned grid = static_cast<unsigned>((p.rows + kRotaryRows - 1) / kRotaryRows);
   return launch_pdl(r.interleaved ? rotary_kernel<true> : rotary_kernel<false>, dim3(grid), dim3(kRotaryThreads), 0,
                     stream, p, r);

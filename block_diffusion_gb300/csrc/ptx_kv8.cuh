@@ -1,10 +1,28 @@
-// PTX wrappers of the operators over the 8-bit cache: MMAs of e4m3 and float16 operands, narrow accesses to
-// tensor memory, a page fetched by one 3-dimensional copy.
+// What the operators over the 8-bit cache share: conversions of e4m3, MMAs of e4m3 and float16 operands, narrow
+// accesses to tensor memory, a page fetched by one 3-dimensional copy.
 #pragma once
+
+#include <cuda_fp8.h>
 
 #include "ptx.cuh"
 
 namespace bdlm {
+
+// Two values as e4m3 codes, rounded to nearest even, at most +-448; the first in the low byte.
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t w) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w), __NV_E4M3);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// The least e with most <= 448 * 2^e (448 = 1.75 * 2^8, the largest e4m3) of a normal number; -134 or less of zero and
+// what is below those, 120 or more of infinity.
+__device__ __forceinline__ int e4m3_exponent(float most) {
+  const uint32_t bits = __float_as_uint(most);
+  return static_cast<int>(bits >> 23) - 127 - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+}
 
 __device__ __forceinline__ void tma_load_3d_hint(void* dst, const CUtensorMap* map, uint64_t* bar,
                                                  int c0, int c1, int c2, uint64_t policy) {
@@ -68,16 +86,9 @@ __device__ __forceinline__ uint64_t smem_desc_plain(uint32_t saddr, uint32_t lbo
   return smem_desc(saddr, lbo, sbo) & ~(static_cast<uint64_t>(7) << 61);
 }
 
-// Instruction descriptors as idesc_bf16_f32, with f16 A and B (format 0) ...
-__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool a_mn_major,
-                                                     bool b_mn_major) {
-  return (1u << 4) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
-         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
-}
-
-// ... and of kind::f8f6f4 with e4m3 A and B (format 0).
-__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, bool a_mn_major,
-                                                      bool b_mn_major) {
+// Instruction descriptors as idesc_bf16_f32, with A and B of format 0: float16 in kind::f16, e4m3 in kind::f8f6f4.
+__host__ __device__ constexpr uint32_t idesc_format0_f32(int M, int N, bool a_mn_major,
+                                                         bool b_mn_major) {
   return (1u << 4) | ((a_mn_major ? 1u : 0u) << 15) | ((b_mn_major ? 1u : 0u) << 16) |
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }

@@ -36,7 +36,7 @@ struct RotaryParams {
   long long rows;
   int inverse;
 };
-cudaError_t launch_rotary(const RotaryParams& p, const bdlm_rotary_desc& r, int num_sms, cudaStream_t stream);
+cudaError_t launch_rotary(const RotaryParams& p, const bdlm_rotary_desc& r, cudaStream_t stream);
 
 // ------------------------------------------------------------------ kv8.cu
 struct WriteKv8Params {
