@@ -7,9 +7,9 @@
 //    float32), so nothing is widened on the way and a token costs 256 bytes of shared memory.  The
 //    other operand has 8 bits as well: q and p are held as two e4m3 parts each, the value rounded to four
 //    bits and what that leaves, rounded to four bits again.  A pair is off by 2^-8 of the value, as bf16
-//    is, and by no less than half its smallest step: of q 2^-18 of the row's largest value (a row has a power of two
-//    of its own, so none depends on another), both parts into the same sums; of a weight 2^-23 of the query's largest in its
-//    chunk of tokens.  The weights' second part is 2^5 times itself, with sums apart, and every chunk's weights
+//    is, and by no less than half its smallest step: of q 2^-17.8 of the row's largest value (a row has a power of
+//    two of its own, so none depends on another; 128 blocks of 8 took 143.5 us with one a list, 148.4 so), both parts into the
+//    same sums; of a weight 2^-23 of the query's largest in its chunk of tokens.  The weights' second part is 2^5 times itself, with sums apart, and every chunk's weights
 //    are taken to its own maximum: with one dominant token the others' are small, many, and all needed (held next to
 //    the list's maximum, without the 2^5, 32768 tokens beside one of 90 % came out two fifths too small).
 //    Twice the products of one part, at twice bf16's rate.
@@ -24,14 +24,14 @@
 //    kernel behind (plan_attention_kv8).  So the work is even whatever the lengths.
 //
 // Bound: the codes, 256 bytes a token and KV head, come once from HBM.  Measured (a graph of calls):
-//     64 blocks of 2 over 2000-8000 tokens, 4 rows a KV head .... 103 us, 6.4 TB/s (94 % of the copy rate)
-//     128 blocks of 4 over 512-4096 tokens, 16 rows a KV head ... 107.5 us, 5.7 TB/s (84 %)
+//     64 blocks of 2 over 2000-8000 tokens, 4 rows a KV head .... 104 us, 6.3 TB/s (93 % of the copy rate)
+//     128 blocks of 4 over 512-4096 tokens, 16 rows a KV head ... 108.5 us, 5.7 TB/s (83 %)
 //     32 single tokens over 16384-32768 tokens, 8 rows .......... 123 us, 6.6 TB/s (97 %)
-//     128 blocks of 8 over 512-4096 tokens, 32 rows ............. 145 us, 4.3 TB/s (63 %): lists' ends
-//     16 blocks of 32 over 8192-16384 tokens, 128 rows .......... 122 us, 3.4 TB/s: the softmax's latency
+//     128 blocks of 8 over 512-4096 tokens, 32 rows ............. 148 us, 4.2 TB/s (61 %): lists' ends
+//     16 blocks of 32 over 8192-16384 tokens, 128 rows .......... 123 us, 3.4 TB/s: the softmax's latency
 //     16 blocks of 64 over 8192-16384 tokens, 256 rows .......... 197 us, 1.05 PFLOP/s (55 %): MMAs and softmax in turn
-//     1024 single tokens over 100-1000 tokens, 4 rows ........... 198 us, 5.9 TB/s (88 %)
-//     one block of 4 over 2000 tokens, 8 rows .................... 10.2 us, latency
+//     1024 single tokens over 100-1000 tokens, 4 rows ........... 197 us, 5.9 TB/s (88 %)
+//     one block of 4 over 2000 tokens, 8 rows .................... 10.6 us, latency
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -373,7 +373,7 @@ constexpr int kFewParts = 8;    // parts a list, about
 // u + 1 streams ahead of V of chunk u.
 //
 // Bound: HBM with up to 16 rows.  With 32, each list's end (the last weights, O^T out, the next queries) holds the one CTA
-// of an SM up for about a tile's time: 32 blocks of 8 over 2000-16000 tokens run at 4.9 TB/s, 128 over 512-4096 at 4.3.
+// of an SM up for about a tile's time: 32 blocks of 8 over 2000-16000 tokens run at 4.7 TB/s, 128 over 512-4096 at 4.2.
 
 // N: rows of the first MMAs, NC: rows that the softmax computes.
 template <int N, int NC, int STAGES>
@@ -1038,7 +1038,7 @@ few_rows_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant_
 //
 // Bound, with 256 rows: a group's softmax (about 2000 cycles a tile) and its MMAs (1000 alone, 1400 beside the
 // converters' and copies' use of shared memory) follow one another, and the two groups' overlap only in part; without the
-// exponentials it takes as long.  198 us for 16 blocks of 64 over 8192-16384 tokens, of which the joins take about 10 and
+// exponentials it takes as long.  197 us for 16 blocks of 64 over 8192-16384 tokens, of which the joins take about 10 and
 // the queries' parts 5; bf16's block attention takes 237 for twice the bytes.
 template <int SUB>
 struct Many {
@@ -1882,7 +1882,7 @@ Kv8AttnPlan plan_attention_kv8(int B, int L, int Hq, int Hkv, int max_pages, int
   pl.row_groups = (L + pl.lsub - 1) / pl.lsub;
   pl.rows = G * pl.lsub;
   // Rows that the MMAs take, the fewest that hold them: 16 rows (128 blocks of 4) in 107 us against 140 as 32, 32 (blocks of
-  // 8) in 145 against 219 as 128.
+  // 8) in 148 against 207 as 128.
   pl.n_rows = pl.rows <= 16 ? 16 : pl.rows <= 32 ? 32 : pl.rows <= 128 ? 128 : 256;
   const bool many = pl.n_rows >= 128;
   const long long lists = static_cast<long long>(B) * Hkv * pl.row_groups;
@@ -1968,8 +1968,8 @@ cudaError_t launch_attention_kv8(const Kv8AttnParams& a, const Kv8AttnPlan& pl, 
   } else {
     // Stages of 16 KB: two CTAs of four keep 128 KB an SM under way.  Six, all that fit, are slower where lists are long (32
     // single tokens over 16384-32768 tokens 128.5 us against 122.7, 32 blocks of 4 over 2000-16000 99.7 against 95.8) and the
-    // same where they are short; three cost 2 to 4 %.  The one CTA of 32 rows takes twelve: 145 us for 128 blocks of 8
-    // over 512-4096, 147.6 with eight, the same on long lists.
+    // same where they are short; three cost 2 to 4 %.  The one CTA of 32 rows takes twelve: 148.5 us for 128 blocks of 8
+    // over 512-4096, 153.7 with eight, 126.4 against 127.4 on long lists.
     e = pl.n_rows == 32  ? launch_few<32, 32, 12>(tk, tv, p, pl.grid, stream)
         // (eight rows: half the softmax; 1024 single tokens over 100-1000 tokens 195 us against 269, one block 10.2 against 11.2)
         : pl.rows <= 8 ? launch_few<16, 8, 4>(tk, tv, p, pl.grid, stream)

@@ -538,8 +538,9 @@ int bdlm_rotary_init(bdlm_rotary_desc* rotary, int rot_dim, int interleaved, dou
  * In each head, pair j < rot_dim / 2 is elements (j, j + rot_dim/2), or (2j, 2j + 1) with `interleaved`:
  *     (x, y) -> amplitude * (x cos a - y sin a, x sin a + y cos a),   a = p * f_j;
  * elements rot_dim .. 127 are copied.  `inverse` turns by -a instead, which is the gradient's way back
- * through the call (and, with an amplitude of 1, undoes it).  Angles are exact to 2^-32 of a turn at any
- * position, products are float32, results are rounded once to bf16.
+ * through the call (and, with an amplitude of 1, undoes it).  Angles are within 2^-26 of a turn, plus what the
+ * frequencies' 53 bits make of the position (2^-24 of a turn at 2^31); products are float32, results are rounded once
+ * to bf16.
  *   q, k           [B, n_tokens, Hq / Hkv, D] bf16, 16-byte aligned; a token's heads side by side, the next
  *                  token q_stride / k_stride elements on (multiples of 8; 0: Hq * D / Hkv * D)
  *   positions      [B, n_tokens] int32, or NULL;  start [B] int32, read where positions is NULL
@@ -593,7 +594,7 @@ int bdlm_write_kv8(const bdlm_attn_desc* desc, int n_tokens, const int32_t* firs
  * Block attention over the 8-bit cache: bdlm_block_attention with K and V as bdlm_write_kv8 holds
  * them.  L = 1 is single-token decoding.  Scales outside [2^-40, 2^40] count as the nearest of the two, NaN
  * as 2^-40; any others are taken as they are, powers of two or not.  A page with a bad id reads as zeros.
- * What is held in fewer than float32's bits: an element of q within 2^-8 of itself or, where that is more, 2^-18 of the
+ * What is held in fewer than float32's bits: an element of q within 2^-8 of itself or, where that is more, 2^-17.8 of the
  * largest of its query; a softmax weight times its page's scale of V within 2^-7.8 of itself or 2^-23 of the
  * query's largest such number among the up to 896 tokens that it is taken with, or 2^-47 of its largest of all (over 32
  * query rows per KV head: 2^-11 of itself, or 2^-32 of the query's largest).  Queries do not depend on one another: one
