@@ -216,7 +216,8 @@ def _element_types(kinds: str) -> tuple:
 
 def _lies_as(t, tokens: int, row: int, stride: int) -> bool:
     """Whether a tensor holds `tokens` tokens of `row` elements, `stride` elements from one to the next.  Where it is not
-    dense its last two dimensions are a token's heads, and those before them the tokens."""
+    dense, as many of its last dimensions as make up a row, two at least, have to be packed; those before them are the
+    tokens."""
     shape = tuple(t.shape)
     if _is_dense(t):
         if tokens > 1 and stride != row:
@@ -233,12 +234,21 @@ def _lies_as(t, tokens: int, row: int, stride: int) -> bool:
         return False
     if tokens == 0:
         return True
-    n = 1
-    for size, step in zip(shape[-3::-1], steps[-3::-1]):
-        if size != 1 and step != n * stride:
+    n, at = shape[-2] * shape[-1], len(shape) - 2
+    while n < row and at > 0:
+        at -= 1
+        if shape[at] != 1 and steps[at] != n:
             return False
-        n *= size
-    return n >= tokens and shape[-2] * shape[-1] >= row
+        n *= shape[at]
+    if n < row:
+        return False
+    n = 1
+    while at > 0:
+        at -= 1
+        if shape[at] != 1 and steps[at] != n * stride:
+            return False
+        n *= shape[at]
+    return n >= tokens
 
 
 def _rows(fn: str, t, B: int, n: int, heads: int, stride: int):

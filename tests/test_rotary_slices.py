@@ -87,3 +87,14 @@ def test_dense_tensors_of_any_shape(call):
         call(3, 5, wide.view(shape), 1024)
     call(1, 1, tensor(4, 128), 4096)                       # one token: no stride
     call(3, 5, x.data_ptr(), 4096)                         # an address is the caller's
+
+
+def test_heads_in_two_dimensions(call):
+    """A token's heads as [Hkv, G]: packed in the wider tensor, or with others between them."""
+    x = tensor(3, 5, 3, 2, 128)
+    call(3, 5, x[:, :, :2], 768)
+    call.refused(3, 5, x[:, :, :2], 0)
+    call.refused(3, 5, x[:, :, :, :1], 768, Hq=3)
+    call.refused(3, 5, x[:, :, :1], 768)
+    call(15, 1, x.view(15, 3, 2, 128)[:, 1:], 768)
+    call(3, 5, tensor(3, 5, 4, 1, 128)[:, :, 1:, :], 512, Hq=3)
