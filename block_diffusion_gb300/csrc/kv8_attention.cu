@@ -222,7 +222,7 @@ __device__ __forceinline__ float rows_max(uint32_t (&m)[R], int lane) {
 }
 
 // The power of two 2^e that takes a largest magnitude to 448 or less (and above 224 where it can).
-__device__ __forceinline__ int q_exponent(float most) { return min(max(e4m3_exponent(most), -110), 119); }
+__device__ __forceinline__ int q_exponent(float most) { return min(max(e4m3_exponent(most), -110), 120); }
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 // What scores of queries over 2^e are multiplied by, beside a page's sK: 2^e c, or 2^-86 where that is less.  Times the
 // least sK, 2^-40, it is a normal number then: a score of -inf (behind the last token) stays one, where 0 would make it

@@ -75,3 +75,30 @@ def test_a_row_keeps_out_of_the_others(lib, L, Hq, Hkv, huge):
             out = (p * sv) @ codes
             excess = np.abs(got[b, :, g * G:(g + 1) * G].reshape(-1, 128)[rows] - out) - tolerance(qq, kk, codes, sv, p, out, L * G <= 32)
             assert excess.max() <= 0, (b, g, excess.max())
+
+
+@pytest.mark.parametrize("L,Hq,Hkv", ROWS)
+def test_the_largest_queries(lib, L, Hq, Hkv):
+    """Elements up to the largest bf16, brought back by a small softmax scale."""
+    rng = np.random.default_rng(L + Hq + 2)
+    c = Cache(rng, np.array([300, 1000]) + L, Hkv)
+    x = rng.uniform(-1, 1, (2, L, Hq, 128)) * 3.3895e38
+    x[..., 5] = 3.3895e38
+    q = W.f32_to_bf16_bits(x.astype(np.float32))
+    assert np.isfinite(R.f64(q)).all() and R.f64(q).max() > 1.99 * 2.0 ** 127
+    out = f(attend(lib, c, q, L, Hq, Hkv, scale=1e-39))
+    small = W.f32_to_bf16_bits((R.f64(q) * 2.0 ** -128).astype(np.float32))
+    scale = float(np.float32(1e-39)) * 2.0 ** 128
+    for b, n in enumerate(c.lens):
+        ids = c.table[b, :(n + 15) // 16]
+        for g in range(Hkv):
+            kk, codes = (R.E4M3[t[ids, g]].reshape(-1, 128)[:n] for t in (c.k, c.v))
+            sk, sv = (np.repeat(c.scales[ids, g, i].astype(np.float64), 16)[:n] for i in range(2))
+            kk = kk * sk[:, None] * (scale / SCALE)
+            G = Hq // Hkv
+            qq = R.f64(small[b, :, g * G:(g + 1) * G]).reshape(-1, 128)
+            p = np.exp(qq @ kk.T * SCALE)
+            p /= p.sum(1, keepdims=True)
+            want = (p * sv) @ codes
+            excess = np.abs(out[b, :, g * G:(g + 1) * G].reshape(-1, 128) - want) - tolerance(qq, kk, codes, sv, p, want, L * G <= 32)
+            assert excess.max() <= 0, (b, g, excess.max())
