@@ -7,12 +7,12 @@
 //    float32), so nothing is widened on the way and a token costs 256 bytes of shared memory.  The
 //    other operand has 8 bits as well: q and p are held as two e4m3 parts each, the value rounded to four
 //    bits and what that leaves, rounded to four bits again.  A pair is off by 2^-8 of the value, as bf16
-//    is, and by no less than half its smallest step: of q 2^-17.8 of the row's largest value (a row has a power of
-//    two of its own, so none depends on another; 128 blocks of 8 took 143.5 us with one a list, 148.4 so), both parts into the
-//    same sums; of a weight 2^-23 of the query's largest in its chunk of tokens.  The weights' second part is 2^5 times itself, with sums apart, and every chunk's weights
-//    are taken to its own maximum: with one dominant token the others' are small, many, and all needed (held next to
-//    the list's maximum, without the 2^5, 32768 tokens beside one of 90 % came out two fifths too small).
-//    Twice the products of one part, at twice bf16's rate.
+//    is, and by no less than half its smallest step: of q 2^-17.8 of the row's largest value, of a weight 2^-23 of
+//    the query's largest in its chunk of tokens.  A row of q has a power of two of its own, so none depends on another
+//    (128 blocks of 8 took 143.5 us with one a list, 148.4 so).  The weights' second part is 2^5 times itself, with
+//    sums apart, and every chunk's weights are taken to its own maximum: with one dominant token the others' are small,
+//    many, and all needed (held next to the list's maximum, without the 2^5, 32768 tokens beside one of 90 % came out
+//    two fifths too small).  Twice the products of one part, at twice bf16's rate.
 //  * A page's scale of K is a factor of its scores.  Its scale of V goes into the weight: with
 //        x_t = c sK_t q . k_t + log2 sV_t    and its maximum m,
 //    w_t = 2^(x_t - m + 8) is what the second product takes (no sum ever meets a scale) and
